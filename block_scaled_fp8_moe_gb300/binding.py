@@ -27,7 +27,8 @@ EXPORTED = [
     "moe_route_topk_noalloc", "moe_selftest_timeout", "moe_route_topk_anchored", "moe_forward_anchored",
     "moe_packed_shared_w13_bytes", "moe_packed_shared_w2_bytes", "moe_pack_shared_w13", "moe_pack_shared_w2",
     "moe_shared_workspace_bytes", "moe_forward_shared", "moe_dead_from_survival", "moe_w2_grouped", "moe_combine",
-    "moe_probe_mma_rate", "moe_quant_mxfp8_plan", "moe_experts_grouped",
+    "moe_probe_mma_rate", "moe_quant_mxfp8_plan", "moe_experts_grouped", "moe_add_rmsnorm_mxfp8", "moe_kv_append",
+    "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_prefill_attention",
 ]
 
 MOE_FLAG_SWIGLU_DEBUG = 1
@@ -48,6 +49,17 @@ class MoeSharedExpert(ctypes.Structure):
 class MoeIntermediates(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "topk_w", "expert_counts", "expert_offsets", "xq", "xs", "hq", "hs", "swiglu")]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("format", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_s", ctypes.c_void_p), ("v_s", ctypes.c_void_p)]
+
+
+class MoeAttention(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _P = ctypes.c_void_p
@@ -92,9 +104,19 @@ lib.moe_shared_workspace_bytes.restype = _SZ
 lib.moe_shared_workspace_bytes.argtypes = [_SHP, _I32]
 lib.moe_forward_shared.argtypes = ([_SHP] + [_P] * 9 + [ctypes.POINTER(MoeSharedExpert), _P,
                                    ctypes.POINTER(MoeIntermediates), _P, _SZ, _P, _P])
+_I64 = ctypes.c_int64
+_ATT = ctypes.POINTER(MoeAttention)
+_KVC = ctypes.POINTER(MoeKvCache)
+lib.moe_add_rmsnorm_mxfp8.argtypes = [_I32, _I32, _P, _P, _P, ctypes.c_float] + [_P] * 5
+lib.moe_kv_append.argtypes = [_KVC, _I32, _P, _I64, _P, _I64, _P, _P, _SZ, _P]
+lib.moe_paged_attention_workspace_bytes.restype = _SZ
+lib.moe_paged_attention_workspace_bytes.argtypes = [_ATT, _I32, _I32]
+lib.moe_paged_attention.argtypes = [_ATT, _KVC, _I32, _I32, _P, _I64, _P, _I32, _P, _P, _P, _SZ, _P]
+lib.moe_prefill_attention.argtypes = [_ATT, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]
 for _n in EXPORTED:
     if _n not in ("moe_status_string", "moe_workspace_bytes", "moe_packed_w13_bytes", "moe_packed_w2_bytes",
-                  "moe_packed_shared_w13_bytes", "moe_packed_shared_w2_bytes", "moe_shared_workspace_bytes"):
+                  "moe_packed_shared_w13_bytes", "moe_packed_shared_w2_bytes", "moe_shared_workspace_bytes",
+                  "moe_paged_attention_workspace_bytes"):
         getattr(lib, _n).restype = ctypes.c_int
 
 
@@ -402,6 +424,231 @@ def moe_forward(shp: MoeShape, x, w_router, bias, dead, w13p, w13sp, w2p, w2sp, 
             _ptr(w2p, torch.uint8), _ptr(w2sp, torch.uint8), _ptr(out, torch.bfloat16, shp.T * shp.H, "out"),
             ctypes.byref(im) if im is not None else None, _ptr(ws), ws.numel(), _stream(stream)),
             "moe_forward_anchored")
+    return out
+
+
+# --------------------------------------------------------------------------------------------------
+# Residual norm, key/value cache, attention
+# --------------------------------------------------------------------------------------------------
+MOE_KV_BF16 = 0
+MOE_KV_MXFP8 = 1
+
+
+def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of this type on device `dev`."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[int, int]:
+    """The address and the row stride of bf16 rows [rows, heads, D] (rows may lie apart)."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    n, h, d = t.shape
+    if h != heads or d != D:
+        raise ValueError(f"{name} must be [rows, {heads}, {D}], is {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != D and h > 1):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.data_ptr(), row if n > 1 else max(row, h * d)
+
+
+def _current(t: torch.Tensor, name: str) -> int:
+    """t's device, which has to be the current one (launches go there)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
+
+
+def _new(shape_, dtype, like: torch.Tensor, stream):
+    """An output, allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape_, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape_, dtype=dtype, device=like.device)
+
+
+_scratch: dict[tuple[int, int], torch.Tensor] = {}
+_outgrown: list[torch.Tensor] = []      # kept: a captured CUDA graph may still write to them
+
+
+def _workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """This stream's workspace of the attention and cache calls, grown as needed (at least twofold); its status word
+    starts at zero."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    key = (like.get_device(), s.cuda_stream)
+    ws = _scratch.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(s):
+            old, ws = ws, torch.empty(max(nbytes, 4096, 2 * ws.numel() if ws is not None else 0), dtype=torch.uint8,
+                                      device=like.device)
+            ws[:256].zero_() if old is None else ws[:256].copy_(old[:256])
+        if old is not None:
+            _outgrown.append(old)
+        _scratch[key] = ws
+    return ws
+
+
+def attention_status(device=None, stream=None) -> None:
+    """Synchronises `stream` and raises what the attention and cache calls without a workspace of their own found
+    invalid on the device there (a page, slot or length out of range), then clears it."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    ws = _scratch.get((s.device_index, s.cuda_stream))
+    if ws is not None:
+        moe_check_device_status(ws, s)
+
+
+def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=None, y=None, q=None, s=None,
+                          quant: bool = True, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight and y's MXFP8 codes and scales, for bf16 rows [..., cols].
+
+    Returns (y, sum, q, s): bf16(y), bf16(h), u8 codes and u8 scales [..., cols / 32]. sum_out and y may be x or residual
+    themselves. With quant=False, q and s are None."""
+    dev = _current(x, "x")
+    cols = x.shape[-1]
+    n = x.numel()
+    rows = n // cols if cols else 0
+    px, pw = _on(x, "x", torch.bfloat16, dev), _on(weight, "weight", torch.bfloat16, dev)
+    if weight.numel() != cols:
+        raise ValueError(f"weight needs {cols} elements, has {weight.numel()}")
+    pr = None
+    if residual is not None:
+        pr = _on(residual, "residual", torch.bfloat16, dev)
+        if residual.numel() != n:
+            raise ValueError(f"residual needs {n} elements, has {residual.numel()}")
+    sum_out = _new(x.shape, torch.bfloat16, x, stream) if sum_out is None else sum_out
+    y = _new(x.shape, torch.bfloat16, x, stream) if y is None else y
+    if quant:
+        q = _new(x.shape, torch.uint8, x, stream) if q is None else q
+        s = _new((*x.shape[:-1], cols // 32), torch.uint8, x, stream) if s is None else s
+    for t, need, name in ((sum_out, n, "sum_out"), (y, n, "y"), (q, n, "q"),
+                          (s, rows * (cols // 32), "s")):
+        if t is not None and t.numel() != need:
+            raise ValueError(f"{name} needs {need} elements, has {t.numel()}")
+    _check(lib.moe_add_rmsnorm_mxfp8(
+        rows, cols, px, pr, pw, eps, _on(sum_out, "sum_out", torch.bfloat16, dev), _on(y, "y", torch.bfloat16, dev),
+        None if q is None else _on(q, "q", torch.uint8, dev), None if s is None else _on(s, "s", torch.uint8, dev),
+        _stream(stream)), "moe_add_rmsnorm_mxfp8")
+    return y, sum_out, q, s
+
+
+class KvCache:
+    """A paged key/value cache: k and v [pages, Hkv, page_size, D] in bf16, or u8 E4M3 codes with u8 UE8M0 scales
+    k_s and v_s [pages, Hkv, page_size, D/32] (see include/moe.h). Holds the tensors it is given."""
+
+    def __init__(self, k, v, k_s=None, v_s=None):
+        dev = _current(k, "k")
+        mx = k_s is not None
+        if k.dim() != 4 or v.shape != k.shape or (mx != (v_s is not None)):
+            raise ValueError("k and v must be [pages, Hkv, page_size, D], with both scale tensors or none")
+        pages, Hkv, page_size, D = k.shape
+        dtype = torch.uint8 if mx else torch.bfloat16
+        ptrs = [_on(k, "k", dtype, dev), _on(v, "v", dtype, dev), None, None]
+        if mx:
+            for i, (t, name) in enumerate(((k_s, "k_s"), (v_s, "v_s"))):
+                if tuple(t.shape) != (pages, Hkv, page_size, D // 32):
+                    raise ValueError(f"{name} must be [pages, Hkv, page_size, D/32], is {tuple(t.shape)}")
+                ptrs[2 + i] = _on(t, name, torch.uint8, dev)
+        self.k, self.v, self.k_s, self.v_s = k, v, k_s, v_s
+        self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
+        self.desc = MoeKvCache(pages, page_size, Hkv, D, MOE_KV_MXFP8 if mx else MOE_KV_BF16, *ptrs)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, Hkv: int, D: int, mxfp8: bool = False, device="cuda"):
+        shp = (pages, Hkv, page_size, D)
+        if not mxfp8:
+            return cls(*(torch.zeros(shp, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        k, v = (torch.zeros(shp, dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, *(torch.zeros(*shp[:3], D // 32, dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
+    """Stores the bf16 rows k and v [T, Hkv, D] (rows may lie apart) at slots i32 [T] (page * page_size + place;
+    -1 = not stored)."""
+    dev = _current(k, "k")
+    pk, sk = _rows_on(k, "k", cache.Hkv, cache.D, dev)
+    pv, sv = _rows_on(v, "v", cache.Hkv, cache.D, dev)
+    T = slots.numel()
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"k and v need {T} rows, have {k.shape[0]} and {v.shape[0]}")
+    ps = _on(slots, "slots", torch.int32, dev)
+    ws = _workspace(256, k, stream) if ws is None else ws
+    _check(lib.moe_kv_append(ctypes.byref(cache.desc), T, pk, sk, pv, sv, ps, _on(ws, "ws", torch.uint8, dev),
+                             ws.numel(), _stream(stream)), "moe_kv_append")
+
+
+def moe_paged_attention_workspace_bytes(B: int, rows: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    a = MoeAttention(B, Hq, Hkv, D, 0, 0, 1.0)
+    return int(lib.moe_paged_attention_workspace_bytes(ctypes.byref(a), rows, max_len))
+
+
+def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, scale: float | None = None,
+                        window: int = 0, sinks: int = 0, out=None, ws=None, stream=None):
+    """Attention of q bf16 [B, rows, Hq, D] (each sequence's newest rows) over the paged cache. block_table i32
+    [B, width], seq_lens i32 [B] (the new rows counted), max_len >= every seq_len. Returns bf16 [B, rows, Hq, D]."""
+    dev = _current(q, "q")
+    B, rows, Hq, D = q.shape
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError(f"block_table must be [{B}, width] and seq_lens [{B}]")
+    if q.is_contiguous():
+        pq, sq = _on(q, "q", torch.bfloat16, dev), Hq * D
+    else:
+        if rows > 1 and B > 1 and q.stride(0) != rows * q.stride(1):
+            raise ValueError("q: rows must be evenly spaced")
+        pq, sq = _rows_on(q[:, 0] if rows == 1 else q[0], "q", Hq, D, dev)
+        if rows > 1 and B > 1:
+            sq = q.stride(1)
+    a = MoeAttention(B, Hq, cache.Hkv, D, window, sinks, D ** -0.5 if scale is None else scale)
+    if out is None:
+        out = _new((B, rows, Hq, D), torch.bfloat16, q, stream)
+    elif out.numel() != q.numel():
+        raise ValueError(f"out needs {q.numel()} elements, has {out.numel()}")
+    if ws is None:
+        ws = _workspace(lib.moe_paged_attention_workspace_bytes(ctypes.byref(a), rows, max_len), q, stream)
+    _check(lib.moe_paged_attention(
+        ctypes.byref(a), ctypes.byref(cache.desc), rows, max_len, pq, sq,
+        _on(block_table, "block_table", torch.int32, dev), block_table.shape[1],
+        _on(seq_lens, "seq_lens", torch.int32, dev), _on(out, "out", torch.bfloat16, dev),
+        _on(ws, "ws", torch.uint8, dev), ws.numel(), _stream(stream)), "moe_paged_attention")
+    return out
+
+
+def moe_prefill_attention(q, k, v, cu_q, cu_k=None, scale: float | None = None, window: int = 0, sinks: int = 0,
+                          out=None, ws=None, stream=None):
+    """Attention of packed prompts: q bf16 [Tq, Hq, D], k and v bf16 [Tk, Hkv, D] (rows may lie apart), cu_q and cu_k
+    i32 [B + 1] the sequences' bounds (cu_k None: the same). Returns bf16 [Tq, Hq, D]; rows outside every sequence are
+    left as they are in `out`."""
+    dev = _current(q, "q")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    pq, sq = _rows_on(q, "q", Hq, D, dev)
+    pk, sk = _rows_on(k, "k", Hkv, D, dev)
+    pv, sv = _rows_on(v, "v", Hkv, D, dev)
+    if v.shape[0] != Tk:
+        raise ValueError(f"v needs {Tk} rows, has {v.shape[0]}")
+    B = cu_q.numel() - 1
+    if B < 0 or (cu_k is not None and cu_k.numel() != B + 1):
+        raise ValueError("cu_q and cu_k need one entry more than there are sequences")
+    if cu_k is None and Tq != Tk:
+        raise ValueError("without cu_k, k and v need as many rows as q")
+    if out is None:
+        out = _new((Tq, Hq, D), torch.bfloat16, q, stream)
+    elif out.numel() != q.numel():
+        raise ValueError(f"out needs {q.numel()} elements, has {out.numel()}")
+    a = MoeAttention(B, Hq, Hkv, D, window, sinks, D ** -0.5 if scale is None else scale)
+    ws = _workspace(256, q, stream) if ws is None else ws
+    _check(lib.moe_prefill_attention(
+        ctypes.byref(a), Tq, Tk, pq, sq, pk, sk, pv, sv, _on(cu_q, "cu_q", torch.int32, dev),
+        None if cu_k is None else _on(cu_k, "cu_k", torch.int32, dev), _on(out, "out", torch.bfloat16, dev),
+        _on(ws, "ws", torch.uint8, dev), ws.numel(), _stream(stream)), "moe_prefill_attention")
     return out
 
 

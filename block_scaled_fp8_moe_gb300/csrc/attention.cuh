@@ -1,0 +1,116 @@
+// What the attention kernels share: which keys a row sees, the cache's addresses, and the attention of
+// one row by one warp straight from its definition (fp32, no tensor cores).
+#pragma once
+#include <cmath>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+inline bool attention_ok(const moe_attention* a) {
+  return a && a->B >= 0 && a->Hq > 0 && a->Hkv > 0 && a->Hq % a->Hkv == 0 && (a->D == 64 || a->D == 128) &&
+         a->Hq <= 65535 && a->B <= (1 << 24) && a->window >= 0 && a->sinks >= 0 && std::isfinite(a->scale);
+}
+
+inline bool kv_cache_ok(const moe_kv_cache* c) {
+  return c && c->pages > 0 && c->Hkv > 0 && (c->D == 64 || c->D == 128) && c->page_size >= 8 && c->page_size <= 256 &&
+         (c->page_size & (c->page_size - 1)) == 0 && (c->format == MOE_KV_BF16 || c->format == MOE_KV_MXFP8) &&
+         (int64_t)c->pages * c->Hkv < ((int64_t)1 << 31) / c->page_size;
+}
+
+inline bool kv_cache_pointers_ok(const moe_kv_cache* c) {
+  const bool mx = c->format == MOE_KV_MXFP8;
+  if (!c->k || !c->v || (mx && (!c->k_s || !c->v_s))) return false;
+  uintptr_t any = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v);
+  if (mx) any |= reinterpret_cast<uintptr_t>(c->k_s) | reinterpret_cast<uintptr_t>(c->v_s);
+  return (any & 127) == 0;
+}
+
+inline bool status_ws_ok(void* ws, size_t ws_bytes) {
+  return ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && ws_bytes >= 256;
+}
+
+// The keys that the row at position p sees are [0, low) and [first, p + 1), low <= first; none for p < 0.
+struct Visible {
+  int low, first, end;
+  __device__ __forceinline__ Visible(int p, int window, int sinks) {
+    end = p + 1;
+    first = (window && p >= window) ? p + 1 - window : 0;
+    low = min(sinks, first);
+  }
+  __device__ __forceinline__ int count() const { return end <= 0 ? 0 : low + end - first; }
+  __device__ __forceinline__ int key(int i) const { return i < low ? i : first + (i - low); }
+  __device__ __forceinline__ bool sees(int j) const { return j < end && (j >= first || j < low); }
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Two bf16, `lo` in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 2^(b - 127) of a UE8M0 byte in fp32 (b = 0 is the subnormal 2^-127, b = 255 is NaN).
+__device__ __forceinline__ float ue8m0(uint32_t b) {
+  return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+}
+
+// One E4M3 code in fp32, the format's NaN codes aside.
+__device__ __forceinline__ float e4m3(uint32_t c) {
+  // sign, exponent and fraction moved into fp32's places give the value times 2^(7 - 127), subnormals too
+  return __uint_as_float(((c & 0x80u) << 24) | ((c & 0x7Fu) << 20)) * __uint_as_float((127u + 120u) << 23);
+}
+
+// A lane's part of a row of D values: the values lane * D/32 ... in fp32.
+template <int D>
+struct LaneRow {
+  static constexpr int N = D / 32;
+  float f[N];
+  __device__ __forceinline__ void load_bf16(const uint16_t* row, int lane) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + lane * N + 2 * i);
+      f[2 * i] = bf16_lo(w);
+      f[2 * i + 1] = bf16_hi(w);
+    }
+  }
+  __device__ __forceinline__ void load_mxfp8(const uint8_t* row, const uint8_t* scales, int lane) {
+    const float sc = ue8m0(scales[lane * N / 32]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = e4m3(row[lane * N + i]) * sc;
+  }
+};
+
+// One row's attention by one warp, its lanes spread over D, every `step`-th visible key from `i0` on.
+// `load(j, k, v)` fetches a key's and its value's parts and returns whether the key is there. m, l, o
+// hold the running maximum of the scores (times log2 e), the sum and the weighted values (of the lane).
+template <int D, class Load>
+__device__ __forceinline__ void attend_row(const LaneRow<D>& q, const Visible& see, int i0, int step, float scale_log2,
+                                           float& m, float& l, float (&o)[D / 32], const Load& load) {
+  constexpr int N = D / 32;
+  const int n = see.count();
+  for (int i = i0; i < n; i += step) {
+    LaneRow<D> k, v;
+    if (!load(see.key(i), k, v)) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int d = 0; d < N; ++d) s = fmaf(q.f[d], k.f[d], s);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    s *= scale_log2;
+    const float mn = fmaxf(m, s);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float keep = exp2f(m - base), p = exp2f(s - base);
+    m = mn;
+    l = l * keep + p;
+#pragma unroll
+    for (int d = 0; d < N; ++d) o[d] = o[d] * keep + p * v.f[d];
+  }
+}
+
+}  // namespace moe

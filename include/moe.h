@@ -339,6 +339,100 @@ MOE_API int moe_route_topk_noalloc(const moe_shape* shape, const uint16_t* x, co
                                    int32_t* expert_counts, int32_t* expert_offsets, int32_t* slot_of_row,
                                    int32_t* row_of_slot, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Around the experts: residual norm, key/value cache, attention (one decoder block's other parts)
+ *
+ * These calls take their sizes themselves (no moe_shape). Conventions as above: device pointers,
+ * caller-owned buffers, asynchronous on `stream`, checks before any launch.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Residual addition, RMS norm and MXFP8 quantisation of rows in one pass:
+ *   h = x + residual (fp32; residual NULL: h = x),  sum = bf16_rne(h)
+ *   y = bf16_rne(h * (1 / sqrt(mean(h^2) + eps)) * weight)   statistics in fp32 from the unrounded h
+ *   q / s = moe_quant_mxfp8(y), bit for bit: the row the router and the experts read.
+ * x, residual, sum, y bf16 [rows, cols]; weight bf16 [cols]; q u8 [rows, cols]; s u8 [rows, cols/32].
+ * sum, y and (q, s) are each optional (NULL = not written; q and s both or neither). sum or y may be
+ * the same buffer as x or residual. cols % 32 == 0, cols <= 16384, rows >= 0 (0 is a no-op), eps >= 0
+ * and finite. x, residual, weight, sum, y 16-byte aligned, q 8-byte aligned. */
+MOE_API int moe_add_rmsnorm_mxfp8(int32_t rows, int32_t cols, const uint16_t* x, const uint16_t* residual,
+                                  const uint16_t* weight, float eps, uint16_t* sum, uint16_t* y, uint8_t* q,
+                                  uint8_t* s, void* stream);
+
+/* A paged key/value cache. Token j of a sequence lives in page block_table[j / page_size] at place
+ * j % page_size. Layout of k and v: [pages, Hkv, page_size, D], so that one head's part of a page is
+ * one contiguous block.
+ *   MOE_KV_BF16   k, v bf16; k_s, v_s unused
+ *   MOE_KV_MXFP8  k, v u8 E4M3 codes, k_s, v_s u8 [pages, Hkv, page_size, D/32] UE8M0 scales, the rule
+ *                 of moe_quant_mxfp8 per 32 values of a row. A block with a value that is not finite is
+ *                 stored with scale byte 255 (NaN) and reads back as NaN; the codes of the format's own
+ *                 NaN (0x7F, 0xFF) are never written and must not be in the cache.
+ * D is 64 or 128, page_size a power of two from 8 to 256, pages * Hkv * page_size < 2^31. k, v, k_s,
+ * v_s 128-byte aligned. */
+#define MOE_KV_BF16 0
+#define MOE_KV_MXFP8 1
+typedef struct moe_kv_cache {
+  int32_t pages, page_size, Hkv, D;
+  int32_t format; /* MOE_KV_* */
+  void* k;
+  void* v;
+  uint8_t* k_s;
+  uint8_t* v_s;
+} moe_kv_cache;
+
+/* Stores T new tokens: k and v bf16, token t's heads at k + t * k_stride (elements; [Hkv, D] contiguous
+ * there, strides multiples of 8 and at least Hkv * D), go to page slots[t] / page_size, place
+ * slots[t] % page_size. slots i32 [T]; -1 = not stored (a dead row); two equal slots in one call leave
+ * one of the two tokens' values, which one is not defined, head by head. Any other slot outside
+ * [0, pages * page_size) is not stored and recorded in the status word (MOE_ERR_DEVICE_INPUT). ws: at least 256
+ * bytes, 256-byte aligned, its first 4 bytes the status word. k, v 16-byte aligned. */
+MOE_API int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_t* k, int64_t k_stride,
+                          const uint16_t* v, int64_t v_stride, const int32_t* slots, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Attention: out = softmax(scale * q k^T) v over the keys that a row sees, in fp32, one rounding to bf16
+ * at the end (the softmax weights are rounded to bf16 for the tensor cores' second product). Query
+ * head h reads key head h / (Hq / Hkv). The row at position p of its sequence sees key j when
+ *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks):
+ * a sliding window and the sequence's first `sinks` tokens, which stay visible. A row that sees nothing
+ * gets +0. Keys and values that a row does not see, and what lies in a page behind its sequence's last
+ * token, do not reach its result whatever they hold, NaN and infinities included. */
+typedef struct moe_attention {
+  int32_t B;             /* sequences                                       */
+  int32_t Hq, Hkv, D;    /* heads of q, heads of k and v (Hq % Hkv == 0), head size: 64 or 128 */
+  int32_t window, sinks; /* window 0: no window (sinks has no effect then)  */
+  float scale;           /* finite; usually 1 / sqrt(D)                      */
+} moe_attention;
+
+/* Attention of `rows` new tokens of every sequence over a paged cache that already holds them (a decode
+ * step, rows = 1, or the verification rows of speculative decoding). seq_lens i32 [B] counts a
+ * sequence's cached tokens, the new ones included: row r is at position seq_lens[b] - rows + r, and rows
+ * at negative positions see nothing. q bf16: row (b, r) at q + (b * rows + r) * q_stride (elements), [Hq, D]
+ * contiguous there; out bf16 [B, rows, Hq, D]. block_table i32 [B, table_width]; entries that no visible key
+ * needs are not read. max_len bounds seq_lens (max_len <= table_width * page_size): it sizes the grid and
+ * the workspace, not the work. A sequence outside [0, max_len] gets zeros, keys in a page outside [0, pages)
+ * are left out, and both are recorded in the status word (MOE_ERR_DEVICE_INPUT).
+ * A sequence is cut into pieces by its own length alone and the pieces are joined in order, so a row's
+ * result does not depend on its batch. 1 <= rows <= 64; q, out 16-byte aligned, q_stride % 8 == 0.
+ * ws: moe_paged_attention_workspace_bytes (0 for unsupported sizes). */
+MOE_API size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len);
+MOE_API int moe_paged_attention(const moe_attention* a, const moe_kv_cache* cache, int32_t rows, int32_t max_len,
+                                const uint16_t* q, int64_t q_stride, const int32_t* block_table,
+                                int32_t table_width, const int32_t* seq_lens, uint16_t* out, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Attention of whole prompts, packed one behind the other: sequence b's query rows are
+ * [cu_q[b], cu_q[b+1]) of the Tq rows of q, its keys [cu_k[b], cu_k[b+1]) of the Tk rows of k and v
+ * (cu_q, cu_k i32 [B + 1], starting at 0, not falling, ending at most at Tq and Tk; cu_k NULL: cu_q). The
+ * last query row is at its last key's position, so a prompt whose earlier part is already in k and v
+ * continues. Row t's heads at q + t * q_stride ([Hq, D]), k + t * k_stride and v + t * v_stride ([Hkv, D]);
+ * out bf16 [Tq, Hq, D]. Rows outside every sequence are not written. A cu entry that breaks the rule is recorded
+ * (MOE_ERR_DEVICE_INPUT) and its sequence left out. q, k, v, out 16-byte aligned, strides multiples of
+ * 8 elements. ws: at least 256 bytes, 256-byte aligned, its first 4 bytes the status word. */
+MOE_API int moe_prefill_attention(const moe_attention* a, int32_t Tq, int32_t Tk, const uint16_t* q, int64_t q_stride,
+                                  const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                  const int32_t* cu_q, const int32_t* cu_k, uint16_t* out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* Test/debug helper: synchronises `stream`, reads and clears the device status word at the start
  * of `ws`, and returns MOE_OK, MOE_ERR_TIMEOUT (an expired device-side wait) or
  * MOE_ERR_DEVICE_INPUT (an input the device found invalid); MOE_ERR_CUDA if the stream itself

@@ -1,0 +1,302 @@
+"""GPU parity: attention of a few new rows per sequence over the paged cache, against the float64 oracle on the values
+that the cache holds. The tolerance is the oracle's own (oracle.attention.attention_tolerance)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(torch.bfloat16).cuda()
+
+
+class Paged:
+    """A cache that holds sequences of the given lengths in pages of a random order. What lies behind a sequence's end
+    and in the pages that nobody has is poison: NaN, infinities, NaN scales."""
+
+    def __init__(self, lens, rows, Hq, Hkv, D, page, mx, seed=0, q_scale=1.0, width=None, spread=0.0):
+        from block_scaled_fp8_moe_gb300 import binding as B
+        rng = np.random.default_rng(seed)
+        self.B, self.lens, self.rows = B, lens, rows
+        used = [-(-n // page) for n in lens]
+        pages = sum(used) + 2
+        width = max(max(used, default=0), 1) if width is None else width
+        order = rng.permutation(pages)
+        table = np.full((len(lens), width), -7, dtype=np.int32)
+        k = np.full((pages, Hkv, page, D), np.nan, dtype=np.float32)
+        k[:, :, ::2] = np.inf
+        v = -k
+        self.kv = []
+        at = 0
+        for b, n in enumerate(lens):
+            mine = order[at:at + used[b]]
+            at += used[b]
+            table[b, :used[b]] = mine
+            kb = rng.standard_normal((n, Hkv, D)) * np.exp(spread * rng.standard_normal((n, 1, 1)))
+            vb = rng.standard_normal((n, Hkv, D)) * np.exp(spread * rng.standard_normal((n, Hkv, 1)))
+            for j in range(n):
+                k[mine[j // page], :, j % page] = kb[j]
+                v[mine[j // page], :, j % page] = vb[j]
+        k, v = _bf16(k), _bf16(v)
+        if mx:
+            parts = []
+            for t in (k, v):
+                q, s = A.quant_block_mxfp8(t.float().cpu().numpy())
+                parts.append((q, s, F.dequant_blocks(F.decode_e4m3(q), s)))
+            self.cache = B.KvCache(*(torch.from_numpy(p[0]).cuda() for p in parts),
+                                   *(torch.from_numpy(p[1]).cuda() for p in parts))
+            self.values = [p[2] for p in parts]
+        else:
+            self.cache = B.KvCache(k, v)
+            self.values = [t.float().cpu().numpy().astype(np.float64) for t in (k, v)]
+        self.table = torch.from_numpy(table).cuda()
+        self.q = _bf16(rng.standard_normal((len(lens), rows, Hq, D)) * q_scale)
+        self.page, self.used = page, used
+
+    def seq_lens(self):
+        return torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+
+    def oracle(self, window=0, sinks=0, scale=None, only=None):
+        q = self.q.float().cpu().numpy()
+        out, mag = np.zeros(q.shape), np.zeros(q.shape)
+        for b, n in enumerate(self.lens):
+            if only is not None and b not in only:
+                continue
+            mine = self.table[b, :self.used[b]].cpu().numpy()
+            k, v = (t[mine].transpose(0, 2, 1, 3).reshape(-1, *t.shape[1::2])[:n] for t in self.values)
+            out[b], mag[b] = A.attend_heads(q[b], k, v, n - self.rows, q.shape[-1] ** -0.5 if scale is None else scale,
+                                            window, sinks)
+        return out, mag
+
+    def run(self, window=0, sinks=0, max_len=None, **kw):
+        max_len = max(self.lens) if max_len is None else max_len
+        return self.B.moe_paged_attention(self.q, self.cache, self.table, self.seq_lens(), max_len, window=window,
+                                          sinks=sinks, **kw)
+
+    def check(self, window=0, sinks=0, **kw):
+        got = self.run(window, sinks, **kw).float().cpu().numpy()
+        want, mag = self.oracle(window, sinks, kw.get("scale"))
+        bad = np.abs(got - want) > A.attention_tolerance(want, mag)
+        assert not bad.any() and np.isfinite(got).all(), (int(bad.sum()), float(np.nanmax(np.abs(got - want))))
+        self.B.attention_status()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq,Hkv,page", [(1, 8, 1, 16), (1, 4, 4, 8), (6, 16, 2, 16), (2, 5, 1, 64),
+                                              (7, 14, 2, 32), (3, 24, 3, 128), (1, 70, 1, 256), (16, 8, 1, 64)])
+def test_lengths_heads_and_pages(rows, Hq, Hkv, page, D, mx):
+    lens = [1, rows, 17, 0, 63, 64, 65, 129, 300, 2]
+    Paged(lens, rows, Hq, Hkv, D, page, mx, seed=rows * 100 + Hq).check()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 4), (16, 0), (64, 4), (100, 70), (128, 300), (1000, 3),
+                                          (257, 129)])
+def test_windows_and_first_tokens(window, sinks, mx):
+    Paged([700, 5, 64, 129, 1, 333, 1100], 3, 8, 2, 64, 16, mx, seed=window).check(window, sinks)
+
+
+@pytest.mark.parametrize("mx,D", [(False, 128), (True, 128), (False, 64), (True, 64)])
+def test_long_sequences_in_many_pieces(mx, D):
+    Paged([5000, 4097, 1, 2049, 9001], 2, 4, 1, D, 32, mx, seed=4).check()
+    Paged([9001, 4097], 1, 4, 2, D, 64, mx, seed=5).check(4100, 33)
+
+
+def test_one_large_score_takes_all():
+    """Scores far apart, and growing along the sequence, so that the running maximum moves again and again."""
+    for mx in (False, True):
+        p = Paged([900, 33], 2, 4, 2, 128, 16, mx, seed=8, q_scale=6.0, spread=0.7)
+        p.check()
+        p.check(scale=-0.5)
+        p.check(scale=0.0)
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    for mx in (False, True):
+        p = Paged([3000, 40, 777, 1025], 4, 8, 2, 64, 16, mx, seed=3)
+        whole = p.run()
+        for b, n in enumerate(p.lens):
+            for max_len in (n, n + 1, 3000):
+                one = p.B.moe_paged_attention(p.q[b:b + 1].contiguous(), p.cache, p.table[b:b + 1].contiguous(),
+                                              p.seq_lens()[b:b + 1], max_len)
+                assert torch.equal(one[0], whole[b])
+
+
+def test_later_rows_values_do_not_reach_earlier_rows():
+    """Verification rows: what a draft token's key and value hold does not matter to the rows before it."""
+    for bad in (float("nan"), float("inf"), 3e38):
+        p = Paged([130, 64, 70], 6, 8, 2, 64, 16, False, seed=6)
+        for b, n in enumerate(p.lens):
+            for j in (n - 1, n - 2):
+                page = int(p.table[b, j // p.page])
+                p.cache.k[page, :, j % p.page] = bad
+                p.cache.v[page, :, j % p.page, ::3] = bad
+        p.values = [t.float().cpu().numpy().astype(np.float64) for t in (p.cache.k, p.cache.v)]
+        got = p.run().float().cpu().numpy()
+        with np.errstate(all="ignore"):
+            want, mag = p.oracle()
+        assert np.all(np.abs(got - want)[:, :4] <= A.attention_tolerance(want, mag)[:, :4])
+        if bad != 3e38:
+            assert not np.isfinite(got[:, 4:]).any(axis=(0, 1, 2)).all()
+
+
+def test_values_that_are_not_finite_and_unseen_are_left_out():
+    """Outside the window, between the first tokens and the window, inside the same pages."""
+    p = Paged([400], 2, 4, 2, 128, 64, False, seed=7)
+    for j in (3, 30, 250, 298):
+        page = int(p.table[0, j // p.page])
+        p.cache.k[page, :, j % p.page] = float("nan")
+        p.cache.v[page, :, j % p.page] = float("-inf")
+    p.values = [t.float().cpu().numpy().astype(np.float64) for t in (p.cache.k, p.cache.v)]
+    p.check(100, 3)
+    got = p.run(100, 4)                       # the fourth first token is one of them
+    assert got.isnan().all()
+
+
+def test_a_nan_scale_reads_as_nan():
+    p = Paged([40], 1, 2, 1, 64, 16, True, seed=2)
+    page = int(p.table[0, 1])
+    p.cache.v_s[page, 0, 5, 1] = 255
+    got = p.run()
+    assert got[..., 32:].isnan().all() and got[..., :32].isfinite().all()
+    p.cache.k_s[page, 0, 5, 0] = 255
+    assert p.run().isnan().all()
+
+
+def test_mxfp8_scales_over_their_range():
+    """Blocks from 2^-120 to 2^100 in one cache; the largest decide the scores."""
+    p = Paged([90], 1, 2, 1, 64, 16, True, seed=12)
+    rng = np.random.default_rng(0)
+    for t, x, span in ((p.cache.k, p.cache.k_s, (0, 120)), (p.cache.v, p.cache.v_s, (7, 227))):
+        x.copy_(torch.from_numpy(rng.integers(*span, tuple(x.shape), dtype=np.uint8)).cuda())
+        t &= 0xBF                             # finite codes, of at most 15/8
+    p.values = [F.dequant_blocks(F.decode_e4m3(t.cpu().numpy()), s.cpu().numpy())
+                for t, s in ((p.cache.k, p.cache.k_s), (p.cache.v, p.cache.v_s))]
+    p.check()
+
+
+def test_strided_queries_other_outputs_and_streams():
+    p = Paged([90, 41], 3, 8, 2, 128, 16, False, seed=9)
+    want = p.run()
+    wide = torch.zeros(2, 3, 12, 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, :8] = p.q
+    plain, p.q = p.q, wide[:, :, :8]
+    assert torch.equal(p.run(), want)
+    p.q = plain
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    out = torch.empty_like(want)
+    assert p.run(stream=side, out=out) is out
+    side.synchronize()
+    assert torch.equal(out, want)
+    need = p.B.moe_paged_attention_workspace_bytes(2, 3, 8, 2, 128, 90)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    p.run(ws=ws)
+    lens, graph = p.seq_lens(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.B.moe_paged_attention(p.q, p.cache, p.table, lens, 90, out=out, ws=ws)
+    for n in ([90, 41], [3, 17], [0, 90]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        p.table[1, 3:] = p.table[0, 3:]       # the second sequence may be longer than it was made
+        out.fill_(7)
+        graph.replay()
+        fresh = p.B.moe_paged_attention(p.q, p.cache, p.table, lens, 90)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), fresh.view(torch.int16))
+
+
+def test_many_calls_in_turn_give_the_same_bits():
+    p, small = Paged([4000, 30, 2500], 2, 8, 2, 128, 16, False, seed=1), Paged([50], 1, 8, 2, 128, 16, False, seed=2)
+    want, want_small = p.run(), small.run()
+    for _ in range(50):
+        a, b = p.run(), small.run()
+        assert torch.equal(a, want) and torch.equal(b, want_small)
+
+
+def test_lengths_and_pages_out_of_range_are_reported():
+    p = Paged([90, 41, 60], 1, 4, 2, 64, 16, False, seed=9)
+    want = p.run()
+    for bad in (-1, 91, 2 ** 31 - 1):
+        got = p.B.moe_paged_attention(p.q, p.cache, p.table, torch.tensor([90, bad, 60], dtype=torch.int32,
+                                                                          device="cuda"), 90)
+        assert not got[1].any() and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+        with pytest.raises(p.B.MoeError) as e:
+            p.B.attention_status()
+        assert e.value.code == p.B.MOE_ERR_DEVICE_INPUT
+    for mx in (False, True):
+        p = Paged([90, 41, 60], 1, 4, 2, 64, 16, mx, seed=9)
+        want = p.run()
+        for bad in (-1, p.cache.pages, 2 ** 31 - 1):
+            table = p.table.clone()
+            table[0, 2] = bad                 # the keys 32 to 47 are left out
+            got = p.B.moe_paged_attention(p.q, p.cache, table, p.seq_lens(), 90)
+            with pytest.raises(p.B.MoeError):
+                p.B.attention_status()
+            assert torch.equal(got[1:], want[1:]) and got[0].isfinite().all() and not torch.equal(got[0], want[0])
+            # a table without that page
+            mine = [int(i) for i in p.table[0, :6] if int(i) != int(p.table[0, 2])]
+            cut = torch.tensor([mine], dtype=torch.int32, device="cuda")
+            short = p.B.moe_paged_attention(p.q[:1], p.cache, cut, torch.tensor([74], dtype=torch.int32, device="cuda"),
+                                            74)
+            tol = 2.0 ** -6                   # both are within the oracle's bound, of values below 4
+            assert (got[0].float() - short[0].float()).abs().max() < tol
+    p.B.attention_status()
+
+
+def test_offsets_past_32_bits():
+    """Pages whose values lie more than 2^31 elements, and 2^32 bytes, into the cache."""
+    from block_scaled_fp8_moe_gb300 import binding as B
+    Hkv, page, D = 8, 64, 128
+    for mx in (False, True):
+        pages = 2 ** 31 // (Hkv * page * D) + 40
+        c = B.KvCache.empty(pages, page, Hkv, D, mxfp8=mx)
+        k, v = (_bf16(np.random.default_rng(i).standard_normal((100, Hkv, D))) for i in (0, 1))
+        slots = torch.arange(100, dtype=torch.int32, device="cuda") + (pages - 2) * page
+        B.moe_kv_append(c, k, v, slots)
+        q = _bf16(np.random.default_rng(2).standard_normal((1, 1, 16, D)))
+        table = torch.tensor([[pages - 2, pages - 1]], dtype=torch.int32, device="cuda")
+        got = B.moe_paged_attention(q, c, table, torch.tensor([100], dtype=torch.int32, device="cuda"), 100)
+        vals = []
+        for t in (k, v):
+            a = t.float().cpu().numpy()
+            if mx:
+                cq, cs = A.quant_block_mxfp8(a)
+                a = F.dequant_blocks(F.decode_e4m3(cq), cs)
+            vals.append(a)
+        want, mag = A.attend_heads(q[0].float().cpu().numpy(), *vals, 99, D ** -0.5)
+        assert np.all(np.abs(got[0].float().cpu().numpy() - want) <= A.attention_tolerance(want, mag))
+        B.attention_status()
+        del c
+    torch.cuda.empty_cache()
+
+
+def test_refusals():
+    p = Paged([90, 41], 2, 4, 2, 64, 16, False, seed=9)
+    B, t, n = p.B, p.table, p.seq_lens()
+    f = B.moe_paged_attention
+    for call in (lambda: f(p.q.float(), p.cache, t, n, 90), lambda: f(p.q, p.cache, t.long(), n, 90),
+                 lambda: f(p.q, p.cache, t[:1], n, 90), lambda: f(p.q, p.cache, t, n[:1], 90),
+                 lambda: f(p.q, p.cache, t, n, 90, out=torch.empty_like(p.q[:1])),
+                 lambda: f(p.q.cpu(), p.cache, t, n, 90), lambda: f(p.q.transpose(2, 3), p.cache, t, n, 90)):
+        with pytest.raises(ValueError):
+            call()
+    small = torch.zeros(128, dtype=torch.uint8, device="cuda")
+    for code, call in ((B.MOE_ERR_INVALID_ARG, lambda: f(p.q, p.cache, t, n, 16 * t.shape[1] + 1)),
+                       (B.MOE_ERR_INVALID_ARG, lambda: f(p.q, p.cache, t, n, -1)),
+                       (B.MOE_ERR_UNSUPPORTED_SHAPE, lambda: f(p.q[:, :, :3].contiguous(), p.cache, t, n, 90)),
+                       (B.MOE_ERR_UNSUPPORTED_SHAPE, lambda: f(p.q, p.cache, t, n, 90, window=-1)),
+                       (B.MOE_ERR_UNSUPPORTED_SHAPE, lambda: f(p.q, p.cache, t, n, 90, sinks=-1)),
+                       (B.MOE_ERR_UNSUPPORTED_SHAPE, lambda: f(p.q, p.cache, t, n, 90, scale=float("nan"))),
+                       (B.MOE_ERR_WORKSPACE, lambda: f(p.q, p.cache, t, n, 90, ws=small)),
+                       (B.MOE_ERR_UNSUPPORTED_SHAPE,
+                        lambda: f(torch.zeros(2, 65, 4, 64, dtype=torch.bfloat16, device="cuda"), p.cache, t, n, 90))):
+        with pytest.raises(B.MoeError) as e:
+            call()
+        assert e.value.code == code
+    assert f(p.q[:0], p.cache, t[:0], n[:0], 0).shape == (0, 2, 4, 64)
