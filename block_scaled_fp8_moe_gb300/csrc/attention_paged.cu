@@ -1,75 +1,642 @@
-// Attention of a few new rows of every sequence over the paged cache.
+// Attention of a few new rows of every sequence over the paged cache (a decode step, or the verification rows of
+// speculative decoding), cut into pieces along the cache and joined.
+//
+// Bound: HBM. Every visible key and value is read once for all rows and all heads of a group; per key and kv head that
+// is 4 D bytes (bf16) or 2.06 D (MXFP8) against 4 D R flops, R = rows * Hq / Hkv: far above what CUDA cores do at full
+// bandwidth (R = 8 would need 54 of their ~75 TFLOP/s), so both products run on the tensor cores, as m16n8k16 with the
+// rows as M. (A tcgen05 product has at least 64 rows; most of them would be padding here.)
+//
+// A block takes one piece of one (sequence, kv head): a producer warp streams pages by TMA through a ring of 64-token
+// stages, WM x WT warps consume it, WM along the rows (16 each), WT along the tokens. Every warp keeps its own running
+// maximum, sum and output, so that nothing but the ring's barriers is shared until the end.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "gemm.cuh"
 #include "ptx.cuh"
 
 namespace moe {
 
-constexpr int kRowWarps = 8;
+constexpr int kTileTok = 64;          // tokens of a stage
+constexpr int kBlockRows = 64;        // rows (row, head of the group) a block takes at most
+constexpr int kPieceTiles = 8;        // a piece has at least this many tiles (512 tokens) ...
+constexpr int kMaxPieces = 64;        // ... and a sequence at most this many pieces
+constexpr uint64_t kPagedWaitNs = 1000000000ull;
 
 struct PagedArgs {
   moe_attention a;
-  moe_kv_cache c;
+  int pages, page_size, page_log2;
+  const uint8_t* k_s;
+  const uint8_t* v_s;
   int rows, max_len, table_width;
+  int mblocks, max_pieces;
   const uint16_t* q;
   long long q_stride;
   const int32_t* table;
   const int32_t* lens;
   uint16_t* out;
   uint32_t* status;
+  float* part_o;    // [B, Hkv, max_pieces, R, D]: sums of weighted values
+  float* part_ml;   // [B, Hkv, max_pieces, R, 2]: running maximum (times log2 e) and sum
 };
 
-// One block per (head, row, sequence), its warps over the keys.
-template <int D, bool MX>
-__global__ void __launch_bounds__(kRowWarps * 32) paged_rows_kernel(const PagedArgs p) {
-  constexpr int N = D / 32;
-  __shared__ float sm[kRowWarps], sl[kRowWarps], so[kRowWarps][D];
+// What the rows [r_lo, r_hi] of a sequence see, as tiles of 64 tokens, and its pieces. The pieces follow from the
+// sequence's own length alone: a row's result is the same in every batch.
+struct Pieces {
+  int pmin, pmax;        // positions of the first and the last row
+  int first_any, first_all;
+  int sink_tiles, win_tile, tiles;
+  int per, count;
+  __device__ __forceinline__ Pieces(int len, int rows, int r_lo, int r_hi, int window, int sinks) {
+    pmin = len - rows + r_lo;
+    pmax = len == 0 ? -1 : len - rows + r_hi;
+    first_any = (window && pmin >= window) ? pmin + 1 - window : 0;
+    first_all = (window && pmax >= window) ? pmax + 1 - window : 0;
+    sink_tiles = (min(sinks, first_all) + kTileTok - 1) / kTileTok;
+    win_tile = max(first_any / kTileTok, sink_tiles);
+    tiles = pmax < 0 ? 0 : sink_tiles + (pmax + kTileTok) / kTileTok - win_tile;
+    per = max(kPieceTiles, (tiles + kMaxPieces - 1) / kMaxPieces);
+    count = max(1, (tiles + per - 1) / per);
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : win_tile + (i - sink_tiles); }
+};
+
+__device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool report) {
+  const int len = p.lens[b];
+  if (len >= 0 && len <= p.max_len) return len;
+  if (report) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+  return 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Two E4M3 codes as bf16 with their values times 2^-120: sign, exponent and fraction in bf16's places (subnormal codes
+// become subnormals). `sel` takes [code of the high half, sign of the low one's (replicated), the low one's, any].
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return (uint32_t)((int32_t)r >> 4) & 0x87F087F0u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A scale byte's factor for e4m3_pair's values, 2^(120 + byte - 127), as bf16 bits: bytes up to 134 fit. What lies
+// above (values past 57,344) takes a second factor; byte 255 is NaN.
+constexpr uint32_t kScaleFits = 134;
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return (min(byte, kScaleFits) + 120u) << 7; }
+__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
+  return byte == 255u ? 0x7FC0u : byte > kScaleFits ? (byte - kScaleFits + 127u) << 7 : 0x3F80u;
+}
+
+template <int D_, bool MX_, int WM_, int WT_>
+struct PagedCfg {
+  static constexpr int D = D_, WM = WM_, WT = WT_;
+  static constexpr bool MX = MX_;
+  static constexpr int WARPS = WM * WT, ST = kTileTok / WT;
+  static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
+  static constexpr int ROWB = MX ? D : 128;                        // bytes of a row in a column block
+  static constexpr int KV = kTileTok * D * (MX ? 1 : 2);           // bytes of a stage's keys, or values
+  static constexpr int SC = MX ? kTileTok * D / 32 : 0;
+  static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
+  static constexpr int STAGES = 98304 / STAGE;
+  static constexpr int PITCH = D + 4;                              // floats of a row in the join buffer
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static_assert(WARPS * 16 * (PITCH + 2) * 4 <= STAGES * STAGE, "the join buffer lies over the ring");
+  static_assert(2 * SC <= 1024, "scales");
+};
+
+// Shared address of 16-byte chunk `chunk` (of the row's D values) of token `tok`.
+template <class C>
+__device__ __forceinline__ uint32_t kv_addr(uint32_t base, int tok, int chunk) {
+  if (C::ROWB == 128) return base + (chunk >> 3) * (kTileTok * 128) + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
+  return base + tok * 64 + ((chunk ^ ((tok >> 1) & 3)) << 4);
+}
+
+template <class C>
+__device__ __forceinline__ float value_at(const uint8_t* stage_v, const uint8_t* scales, int tok, int d) {
+  if (C::MX) {
+    const uint32_t at = kv_addr<C>(0, tok, d >> 4) + (d & 15);
+    return e4m3(stage_v[at]) * ue8m0(scales[tok * (C::D / 32) + (d >> 5)]);
+  }
+  const uint32_t at = kv_addr<C>(0, tok, d >> 3) + (d & 7) * 2;
+  return bf16_lo(*reinterpret_cast<const uint16_t*>(stage_v + at));
+}
+
+template <class C>
+__global__ void __launch_bounds__((C::WARPS + 1) * 32, 2)
+paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const PagedArgs p) {
+  constexpr int D = C::D, ST = C::ST, NT = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ uint32_t page_mask[C::STAGES];
+  __shared__ volatile uint32_t abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int h = blockIdx.x, r = blockIdx.y % p.rows, hk = h / (p.a.Hq / p.a.Hkv);
-  const long long b = blockIdx.y / p.rows;
-  int len = p.lens[b];
-  if (len < 0 || len > p.max_len) {
-    if (threadIdx.x == 0) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-    len = 0;
-  }
-  const Visible see(len == 0 ? -1 : len - p.rows + r, p.a.window, p.a.sinks);
-  LaneRow<D> q;
-  q.load_bf16(p.q + (b * p.rows + r) * p.q_stride + (long long)h * D, lane);
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  attend_row<D>(q, see, warp, kRowWarps, p.a.scale * 1.4426950408889634f, m, l, o,
-                [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
-                  const int page = p.table[b * p.table_width + j / p.c.page_size];
-                  if (page < 0 || page >= p.c.pages) {
-                    if (lane == 0) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-                    return false;
-                  }
-                  const long long row = ((long long)page * p.c.Hkv + hk) * p.c.page_size + j % p.c.page_size;
-                  if (MX) {
-                    k.load_mxfp8(static_cast<const uint8_t*>(p.c.k) + row * D, p.c.k_s + row * N, lane);
-                    v.load_mxfp8(static_cast<const uint8_t*>(p.c.v) + row * D, p.c.v_s + row * N, lane);
-                  } else {
-                    k.load_bf16(static_cast<const uint16_t*>(p.c.k) + row * D, lane);
-                    v.load_bf16(static_cast<const uint16_t*>(p.c.v) + row * D, lane);
-                  }
-                  return true;
-                });
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < N; ++i) so[warp][lane * N + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float top = -INFINITY, tl = 0.f, to = 0.f;
-    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < kRowWarps; ++w) {
-      const float f = exp2f(sm[w] - (top == -INFINITY ? 0.f : top));
-      tl += sl[w] * f;
-      to += so[w][threadIdx.x] * f;
+  long long u = blockIdx.x;
+  const int piece = (int)(u % p.max_pieces);
+  u /= p.max_pieces;
+  const int hk = (int)(u % p.a.Hkv);
+  u /= p.a.Hkv;
+  const int mb = (int)(u % p.mblocks);
+  const long long b = u / p.mblocks;
+  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
+
+  pdl_trigger();
+  pdl_wait();
+  const int len = checked_len(p, b, threadIdx.x == 0);
+  const int rho_end = min(R, (mb + 1) * kBlockRows);
+  const Pieces pc(len, p.rows, mb * kBlockRows / G, (rho_end - 1) / G, p.a.window, p.a.sinks);
+  if (piece >= pc.count) return;
+  const int i0 = piece * pc.per, i1 = min(pc.tiles, i0 + pc.per);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], C::WARPS);
     }
-    reinterpret_cast<__nv_bfloat16*>(p.out)[((b * p.rows + r) * p.a.Hq + h) * D + threadIdx.x] =
-        __float2bfloat16_rn(tl == 0.f ? 0.f : to / tl);
+    abort_flag = 0;
+    mbar_fence_init();
   }
+  __syncthreads();
+
+  if (warp == C::WARPS) {
+    // ---------------- producer ----------------
+    const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;   // pages of a tile
+    const int rows_of = min(p.page_size, kTileTok);
+    const int32_t* table = p.table + b * p.table_width;
+    const int last_page = pc.pmax >> p.page_log2;
+    int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
+    int issued = 0;
+    for (int i = i0; i < i1; ++i, ++issued) {
+      const int s = issued % C::STAGES;
+      const int tok0 = pc.tile(i) * kTileTok, page0 = tok0 >> p.page_log2;
+      if (page0 < base || page0 + in_tile > base + 32) {
+        // in_tile divides 32, and so tiles do not straddle groups of 32 entries
+        const int nb = page0 & ~31;
+        ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+        base = nb;
+        next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+      // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+      const int t0 = tok0 + lane * rows_of;
+      const bool want = lane < in_tile && t0 <= pc.pmax &&
+                        (t0 + rows_of > pc.first_any || t0 < min(p.a.sinks, pc.first_all));
+      const bool good = want && id >= 0 && id < p.pages;
+      if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+      const uint32_t mask = __ballot_sync(0xffffffffu, good);
+      if (issued >= C::STAGES &&
+          !mbar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag, p.status, DEV_TIMEOUT_EMPTY))
+        break;
+      if (lane == 0) {
+        page_mask[s] = mask;
+        mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
+      }
+      __syncwarp();
+      if (good) {
+        const int row = (int)(((long long)id * p.a.Hkv + hk) << p.page_log2) + (t0 & (p.page_size - 1));
+        uint8_t* st = smem + s * C::STAGE;
+#pragma unroll
+        for (int h = 0; h < C::HALVES; ++h) {
+          const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
+          tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
+          tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
+        }
+        if (C::MX) {
+          const uint32_t bytes = rows_of * (D / 32);
+          uint8_t* sc = st + 2 * C::KV + lane * bytes;
+          bulk_load(sc, p.k_s + (long long)row * (D / 32), bytes, &full[s]);
+          bulk_load(sc + C::SC, p.v_s + (long long)row * (D / 32), bytes, &full[s]);
+        }
+      }
+    }
+    // a piece that gives up still waits for its copies in flight
+    __syncwarp();
+    if (abort_flag && lane == 0)
+      for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+        mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  const int wm = warp % C::WM, wt = warp / C::WM;
+  const int g = lane >> 2, c = lane & 3;
+  int pos[2], first[2];
+  uint32_t qf[D / 16][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int rho = mb * kBlockRows + wm * 16 + g + 8 * h;
+    const bool live = rho < R;
+    const int r = rho / G;
+    pos[h] = live ? len - p.rows + r : -1;
+    first[h] = (p.a.window && pos[h] >= p.a.window) ? pos[h] + 1 - p.a.window : 0;
+    const uint16_t* row = p.q + (b * p.rows + r) * p.q_stride + (long long)(hk * G + rho % G) * D;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      // MX: the k of a step are the codes that one thread has at hand (8 in a row, 4 for each of two steps)
+      const int d0 = C::MX ? (ks / 2) * 32 + 8 * c + 4 * (ks & 1) : ks * 16 + 2 * c;
+      const int d1 = C::MX ? d0 + 2 : d0 + 8;
+      qf[ks][h] = live ? *reinterpret_cast<const uint32_t*>(row + d0) : 0;
+      qf[ks][2 + h] = live ? *reinterpret_cast<const uint32_t*>(row + d1) : 0;
+    }
+  }
+  float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  const float scale = p.a.scale * 1.4426950408889634f;
+
+  for (int i = i0; i < i1; ++i) {
+    const int n = i - i0, s = n % C::STAGES;
+    if (!mbar_wait(&full[s], (n / C::STAGES) & 1, kPagedWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL)) break;
+    const int loc0 = wt * ST, tok0 = pc.tile(i) * kTileTok + loc0;
+    const uint8_t* st = smem + s * C::STAGE;
+    const uint32_t kb = smem_u32(st), vb = kb + C::KV;
+    const uint32_t mask = page_mask[s];
+    const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;
+    // every row of the block sees every token of this warp
+    const bool whole = tok0 + ST - 1 <= pc.pmin && (tok0 >= pc.first_all || tok0 + ST <= p.a.sinks) &&
+                       mask == (in_tile == 32 ? 0xffffffffu : (1u << in_tile) - 1u);
+    if (tok0 <= pc.pmax) {
+      float sc[ST / 8][4];
+#pragma unroll
+      for (int j = 0; j < ST / 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+      if (!C::MX) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int jp = 0; jp < ST / 16; ++jp) {
+            uint32_t r[4];
+            ldsm4(kv_addr<C>(kb, loc0 + jp * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), r);
+            mma_16816(sc[2 * jp], qf[ks], r[0], r[1]);
+            mma_16816(sc[2 * jp + 1], qf[ks], r[2], r[3]);
+          }
+      } else {
+        const uint8_t* scales = st + 2 * C::KV;
+#pragma unroll
+        for (int j = 0; j < ST / 8; ++j) {
+          const int t = loc0 + j * 8 + g;
+          const uint32_t sw = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
+                                       : *reinterpret_cast<const uint16_t*>(scales + t * 2);
+          const bool large = __any_sync(0xffffffffu, __vcmpgtu4(sw, kScaleFits * 0x01010101u) != 0);
+#pragma unroll
+          for (int bl = 0; bl < D / 32; ++bl) {
+            uint32_t w0, w1;
+            const uint32_t at = kv_addr<C>(kb, t, 2 * bl + (c >> 1)) + 8 * (c & 1);
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+            const uint32_t by = (sw >> (8 * bl)) & 255u, f = scale_bits(by) * 0x10001u;
+            uint32_t x[4] = {mul_bf16x2(e4m3_pair(w0, w0, 0x1800), f), mul_bf16x2(e4m3_pair(w0, w0, 0x3A22), f),
+                             mul_bf16x2(e4m3_pair(w1, w1, 0x1800), f), mul_bf16x2(e4m3_pair(w1, w1, 0x3A22), f)};
+            if (large) {
+              const uint32_t f2 = scale_rest(by) * 0x10001u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = mul_bf16x2(x[e], f2);
+            }
+            mma_16816(sc[j], qf[2 * bl], x[0], x[1]);
+            mma_16816(sc[j], qf[2 * bl + 1], x[2], x[3]);
+          }
+        }
+      }
+
+      // ---- what the rows do not see ----
+      unsigned long long drop = 0, alone = 0;      // of this warp's tokens: left out of the product; added one by one
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < ST / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[j][e] *= scale;
+      } else {
+#pragma unroll
+        for (int j = 0; j < ST / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int loc = j * 8 + 2 * c + (e & 1), t = tok0 + loc;
+            const bool there = (mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u;
+            const bool see = there && t <= pos[e >> 1] && (t >= first[e >> 1] || t < p.a.sinks);
+            sc[j][e] = see ? sc[j][e] * scale : -INFINITY;
+          }
+        // A weight of zero does not hide a value that is not finite: the product leaves out what no row sees, and
+        // what only some rows see where it is not finite.
+#pragma unroll
+        for (int w = 0; w < (ST + 31) / 32; ++w) {
+          const int loc = w * 32 + lane, t = tok0 + loc;
+          const bool there = loc < ST && ((mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u);
+          const bool any = there && t <= pc.pmax && (t >= pc.first_any || t < p.a.sinks);
+          const bool all = any && t <= pc.pmin && (t >= pc.first_all || t < p.a.sinks);
+          drop |= (unsigned long long)__ballot_sync(0xffffffffu, loc < ST && !any) << (32 * w);
+          alone |= (unsigned long long)__ballot_sync(0xffffffffu, any && !all) << (32 * w);
+        }
+        for (unsigned long long some = alone; some; some &= some - 1) {
+          const int loc = __ffsll(some) - 1;
+          bool fine = true;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e)
+            fine = fine && isfinite(value_at<C>(st + C::KV, st + 2 * C::KV + C::SC, loc0 + loc, lane + 32 * e));
+          if (__all_sync(0xffffffffu, fine)) alone &= ~(1ull << loc);
+        }
+        drop |= alone;
+      }
+
+      // ---- softmax ----
+      float mx[2] = {-INFINITY, -INFINITY}, base[2];
+#pragma unroll
+      for (int j = 0; j < ST / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], sc[j][e]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        mx[h] = fmaxf(mx[h], m[h]);
+        base[h] = mx[h] == -INFINITY ? 0.f : mx[h];
+      }
+      if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+        const float k0 = ex2(m[0] - base[0]), k1 = ex2(m[1] - base[1]);
+        l[0] *= k0;
+        l[1] *= k1;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][0] *= k0;
+          o[j][1] *= k0;
+          o[j][2] *= k1;
+          o[j][3] *= k1;
+        }
+        m[0] = mx[0];
+        m[1] = mx[1];
+      }
+      uint32_t pf[ST / 16][4];
+#pragma unroll
+      for (int j = 0; j < ST / 8; ++j) {
+        // the weights are rounded to bf16 for the second product; the sum takes the rounded ones, so that a single
+        // large weight divides out exactly
+        const uint32_t w0 = bf16x2(ex2(sc[j][0] - base[0]), ex2(sc[j][1] - base[0]));
+        const uint32_t w1 = bf16x2(ex2(sc[j][2] - base[1]), ex2(sc[j][3] - base[1]));
+        l[0] += bf16_lo(w0) + bf16_hi(w0);
+        l[1] += bf16_lo(w1) + bf16_hi(w1);
+        pf[j / 2][(j & 1) * 2] = w0;
+        pf[j / 2][(j & 1) * 2 + 1] = w1;
+      }
+
+      // ---- weighted values ----
+#pragma unroll
+      for (int t = 0; t < ST / 16; ++t) {
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (drop) {
+          const uint32_t d16 = (uint32_t)(drop >> (16 * t));
+          keep0 = ((d16 >> (2 * c)) & 1u ? 0u : 0xffffu) | ((d16 >> (2 * c + 1)) & 1u ? 0u : 0xffff0000u);
+          keep1 = ((d16 >> (2 * c + 8)) & 1u ? 0u : 0xffffu) | ((d16 >> (2 * c + 9)) & 1u ? 0u : 0xffff0000u);
+        }
+        if (!C::MX) {
+#pragma unroll
+          for (int np = 0; np < D / 16; ++np) {
+            uint32_t r[4];
+            ldsm4t(kv_addr<C>(vb, loc0 + t * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * np + (lane >> 4)), r);
+            if (drop) r[0] &= keep0, r[1] &= keep1, r[2] &= keep0, r[3] &= keep1;
+            mma_16816(o[2 * np], pf[t], r[0], r[1]);
+            mma_16816(o[2 * np + 1], pf[t], r[2], r[3]);
+          }
+        } else {
+          // thread (g, c) holds the D/8 values from g D/8 on of its four tokens; product j takes the j-th of each
+          const uint8_t* scales = st + 2 * C::KV + C::SC;
+          uint32_t w[4][D / 32], by[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = loc0 + t * 16 + 2 * c + (e & 1) + 8 * (e >> 1);
+            if constexpr (D == 128) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                           : "r"(kv_addr<C>(vb, tk, g)) : "memory");
+            } else {
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
+                           : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
+            }
+            by[e] = scales[tk * (D / 32) + g / (256 / D)];
+          }
+          const uint32_t f0 = scale_bits(by[0]) | scale_bits(by[1]) << 16, f1 = scale_bits(by[2]) | scale_bits(by[3]) << 16;
+          const bool large = __any_sync(0xffffffffu, max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            constexpr uint32_t kSel[4] = {0x4800, 0x5911, 0x6A22, 0x7B33};
+            uint32_t x0 = mul_bf16x2(e4m3_pair(w[0][j / 4], w[1][j / 4], kSel[j & 3]), f0);
+            uint32_t x1 = mul_bf16x2(e4m3_pair(w[2][j / 4], w[3][j / 4], kSel[j & 3]), f1);
+            if (large) {
+              x0 = mul_bf16x2(x0, scale_rest(by[0]) | scale_rest(by[1]) << 16);
+              x1 = mul_bf16x2(x1, scale_rest(by[2]) | scale_rest(by[3]) << 16);
+            }
+            if (drop) x0 &= keep0, x1 &= keep1;
+            mma_16816(o[j], pf[t], x0, x1);
+          }
+        }
+      }
+      for (; alone; alone &= alone - 1) {
+        const int loc = __ffsll(alone) - 1, t = tok0 + loc;
+        uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+        for (int j = 0; j < ST / 8; ++j)
+          if (j == loc >> 3) w0 = pf[j / 2][(j & 1) * 2], w1 = pf[j / 2][(j & 1) * 2 + 1];
+        w0 = __shfl_sync(0xffffffffu, w0, (lane & 28) | ((loc & 7) >> 1));
+        w1 = __shfl_sync(0xffffffffu, w1, (lane & 28) | ((loc & 7) >> 1));
+        const float p0 = loc & 1 ? bf16_hi(w0) : bf16_lo(w0), p1 = loc & 1 ? bf16_hi(w1) : bf16_lo(w1);
+        const bool see0 = t <= pos[0] && (t >= first[0] || t < p.a.sinks);
+        const bool see1 = t <= pos[1] && (t >= first[1] || t < p.a.sinks);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float v = value_at<C>(st + C::KV, st + 2 * C::KV + C::SC, loc0 + loc,
+                                        C::MX ? (2 * c + e) * (D / 8) + j : j * 8 + 2 * c + e);
+            if (see0) o[j][e] = fmaf(p0, v, o[j][e]);
+            if (see1) o[j][2 + e] = fmaf(p1, v, o[j][2 + e]);
+          }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+  }
+
+  // ---------------- the warps' parts joined, in the order of their tokens ----------------
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+  }
+  named_bar_sync(1, C::WARPS * 32);        // the ring is read out
+  float* jo = reinterpret_cast<float*>(smem);
+  float* jml = jo + C::WARPS * 16 * C::PITCH;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = (wt * C::WM + wm) * 16 + g + 8 * h;
+    if (c == 0) jml[2 * row] = m[h], jml[2 * row + 1] = l[h];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        jo[row * C::PITCH + (C::MX ? (2 * c + e) * (D / 8) + j : j * 8 + 2 * c + e)] = o[j][2 * h + e];
+  }
+  named_bar_sync(1, C::WARPS * 32);
+  if (abort_flag) return;
+  for (int x = threadIdx.x; x < C::WM * 16 * (D / 4); x += C::WARPS * 32) {
+    const int row = x / (D / 4), d = x % (D / 4) * 4, rho = mb * kBlockRows + row;
+    if (rho >= R) break;
+    float top = -INFINITY, tl = 0.f;
+    float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < C::WT; ++w) top = fmaxf(top, jml[2 * (w * C::WM * 16 + row)]);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < C::WT; ++w) {
+      const int rr = w * C::WM * 16 + row;
+      const float f = ex2(jml[2 * rr] - base);
+      const float4 v = *reinterpret_cast<const float4*>(jo + rr * C::PITCH + d);
+      tl += f * jml[2 * rr + 1];
+      to.x += f * v.x;
+      to.y += f * v.y;
+      to.z += f * v.z;
+      to.w += f * v.w;
+    }
+    if (pc.count == 1) {
+      const float inv = 1.f / tl;
+      const bool none = tl == 0.f;
+      const long long at = ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d;
+      *reinterpret_cast<uint2*>(p.out + at) =
+          none ? make_uint2(0, 0) : make_uint2(bf16x2(to.x * inv, to.y * inv), bf16x2(to.z * inv, to.w * inv));
+    } else {
+      const long long at = ((b * p.a.Hkv + hk) * p.max_pieces + piece) * R + rho;
+      *reinterpret_cast<float4*>(p.part_o + at * D + d) = to;
+      if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, tl);
+    }
+  }
+}
+
+// One warp per row: the pieces' parts joined in order. Rows of one piece are already written.
+template <int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs p) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x % 32;
+  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
+  const long long x = (long long)blockIdx.x * 4 + threadIdx.x / 32;
+  pdl_wait();
+  if (x >= (long long)p.a.B * p.a.Hkv * R) return;
+  const int rho = (int)(x % R), hk = (int)(x / R % p.a.Hkv);
+  const long long b = x / R / p.a.Hkv;
+  const int mb = rho / kBlockRows;
+  const Pieces pc(checked_len(p, b, false), p.rows, mb * kBlockRows / G, (min(R, (mb + 1) * kBlockRows) - 1) / G,
+                  p.a.window, p.a.sinks);
+  if (pc.count == 1) return;
+  const long long at = (b * p.a.Hkv + hk) * p.max_pieces * R + rho;
+  static_assert(kMaxPieces == 64, "two pieces a lane");
+  float w[2], ls[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    const float2 v = i < pc.count ? *reinterpret_cast<const float2*>(p.part_ml + (at + (long long)i * R) * 2)
+                                  : make_float2(-INFINITY, 0.f);
+    w[h] = v.x;
+    ls[h] = v.y;
+  }
+  float top = fmaxf(w[0], w[1]);
+#pragma unroll
+  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  const float base = top == -INFINITY ? 0.f : top;
+  w[0] = ex2(w[0] - base);
+  w[1] = ex2(w[1] - base);
+  float tl = w[0] * ls[0] + w[1] * ls[1];
+#pragma unroll
+  for (int s = 16; s; s >>= 1) tl += __shfl_xor_sync(0xffffffffu, tl, s);
+  float o[N] = {};
+#pragma unroll 4
+  for (int i = 0; i < pc.count; ++i) {
+    const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
+    const float* v = p.part_o + (at + (long long)i * R) * D + lane * N;
+    if constexpr (N == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(v);
+      o[0] = fmaf(f, t.x, o[0]), o[1] = fmaf(f, t.y, o[1]), o[2] = fmaf(f, t.z, o[2]), o[3] = fmaf(f, t.w, o[3]);
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(v);
+      o[0] = fmaf(f, t.x, o[0]), o[1] = fmaf(f, t.y, o[1]);
+    }
+  }
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + lane * N);
+  const float inv = 1.f / tl;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) out[i] = tl == 0.f ? 0u : bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+}
+
+// The most pieces a sequence of up to max_len tokens can have.
+static int max_pieces_of(const moe_attention* a, int rows, int max_len) {
+  long long tiles = ((long long)max_len + kTileTok - 1) / kTileTok;
+  if (a->window) {
+    const long long sinks = ((long long)a->sinks + kTileTok - 1) / kTileTok;
+    tiles = std::min(tiles, sinks + ((long long)a->window + rows) / kTileTok + 2);
+  }
+  return (int)std::max(1ll, std::min((long long)kMaxPieces, (tiles + kPieceTiles - 1) / kPieceTiles));
+}
+
+static size_t part_rows(const moe_attention* a, int rows, int max_len) {
+  const int pieces = max_pieces_of(a, rows, max_len);
+  return pieces == 1 ? 0 : (size_t)a->B * a->Hq * rows * pieces;
+}
+
+static int page_map(CUtensorMap* m, void* base, const moe_kv_cache* c) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return MOE_ERR_CUDA;
+  const bool mx = c->format == MOE_KV_MXFP8;
+  const cuuint64_t dims[2] = {(cuuint64_t)c->D, (cuuint64_t)c->pages * c->Hkv * c->page_size};
+  const cuuint64_t stride[1] = {(cuuint64_t)c->D * (mx ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(mx ? c->D : 64), (cuuint32_t)std::min(c->page_size, kTileTok)};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, stride,
+                         box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         mx && c->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <class C>
+static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  CUtensorMap km, vm;
+  int rc = page_map(&km, cache->k, cache);
+  if (rc || (rc = page_map(&vm, cache->v, cache))) return rc;
+  auto kern = paged_attention_kernel<C>;
+  if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM))) return rc;
+  const long long grid = (long long)p.a.B * p.mblocks * p.a.Hkv * p.max_pieces;
+  rc = launch_pdl(kern, dim3((unsigned)grid), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
+  if (rc || p.max_pieces == 1) return rc;
+  const long long out_rows = (long long)p.a.B * p.a.Hq * p.rows;
+  return launch_pdl(paged_join_kernel<C::D>, dim3((unsigned)((out_rows + 3) / 4)), dim3(128), 0, st, p);
+}
+
+template <int D, bool MX>
+static int launch_rows(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  // warps along the rows as far as there are rows, the others along the tokens
+  const int r = std::min(kBlockRows, p.rows * (p.a.Hq / p.a.Hkv));
+  if (r <= 16) return launch_paged<PagedCfg<D, MX, 1, 4>>(p, cache, st);
+  if (r <= 32) return launch_paged<PagedCfg<D, MX, 2, 2>>(p, cache, st);
+  return launch_paged<PagedCfg<D, MX, 4, 1>>(p, cache, st);
 }
 
 }  // namespace moe
@@ -78,7 +645,8 @@ using namespace moe;
 
 extern "C" size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len) {
   if (!attention_ok(a) || rows < 1 || rows > 64 || max_len < 0) return 0;
-  return 256;
+  const size_t n = part_rows(a, rows, max_len);
+  return 256 + align_up(n * a->D * 4, 256) + align_up(n * 8, 256);
 }
 
 extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* cache, int32_t rows, int32_t max_len,
@@ -96,12 +664,30 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   if (q_stride < (int64_t)a->Hq * a->D || q_stride % 8) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens)) & 3) return MOE_ERR_INVALID_ARG;
-  if ((int64_t)a->B * rows > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
-  const PagedArgs p{*a, *cache, rows, max_len, table_width, q, q_stride, block_table, seq_lens, out,
-                    static_cast<uint32_t*>(ws)};
+  PagedArgs p{};
+  p.a = *a;
+  p.pages = cache->pages;
+  p.page_size = cache->page_size;
+  while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
+  p.k_s = cache->k_s;
+  p.v_s = cache->v_s;
+  p.rows = rows;
+  p.max_len = max_len;
+  p.table_width = table_width;
+  p.mblocks = ceil_div(rows * (a->Hq / a->Hkv), kBlockRows);
+  p.max_pieces = max_pieces_of(a, rows, max_len);
+  if ((int64_t)a->B * p.mblocks * a->Hkv * p.max_pieces >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.out = out;
+  p.status = static_cast<uint32_t*>(ws);
+  const size_t n = part_rows(a, rows, max_len);
+  p.part_o = ws_ptr<float>(ws, 256);
+  p.part_ml = ws_ptr<float>(ws, 256 + align_up(n * a->D * 4, 256));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool mx = cache->format == MOE_KV_MXFP8;
-  auto kern = a->D == 64 ? (mx ? paged_rows_kernel<64, true> : paged_rows_kernel<64, false>)
-                         : (mx ? paged_rows_kernel<128, true> : paged_rows_kernel<128, false>);
-  kern<<<dim3(a->Hq, a->B * rows), kRowWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return launch_status();
+  if (a->D == 64) return mx ? launch_rows<64, true>(p, cache, st) : launch_rows<64, false>(p, cache, st);
+  return mx ? launch_rows<128, true>(p, cache, st) : launch_rows<128, false>(p, cache, st);
 }
