@@ -1,11 +1,29 @@
 // Attention of whole prompts, packed one behind the other.
+//
+// Bound: the tensor cores. Per visible (row, key) pair and head 4 D flops; keys come from L2 (a block reads its keys
+// once for 256 rows). Both products run on tcgen05 with accumulators in Tensor Memory: S = Q K^T (128 x 128 keys), the
+// softmax weights P as bf16 over S's own columns, O += P V with P read from Tensor Memory.
+//
+// A block has two tiles of 128 rows that share their keys: two heads of a group, or where a group has an odd number of
+// heads, 256 rows of one. While one tile's weights are computed (one warpgroup each, a thread per row), the tensor
+// cores work on the other's products:  PV0(i) QK0(i+1) | PV1(i) QK1(i+1).
+// The output is rescaled only when a row's maximum has grown by more than 2^8 since the last time (weights of up to 256
+// are as exact in bf16 as those up to 1), so that the softmax warps seldom touch it.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "gemm.cuh"
 #include "ptx.cuh"
 
 namespace moe {
+
+constexpr int kTileM = 128;             // query rows of a tile
+constexpr int kTileN = 128;             // keys of a step
+constexpr uint64_t kPrefillWaitNs = 1000000000ull;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kBadKeys = 64;            // keys with values that are not finite that a block lists
 
 struct PrefillArgs {
   moe_attention a;
@@ -20,6 +38,7 @@ struct PrefillArgs {
   const int32_t* cu_k;
   uint16_t* out;
   uint32_t* status;
+  int pair;                             // 1: the two tiles are two heads, 0: two blocks of rows
 };
 
 struct Span {
@@ -41,32 +60,540 @@ __device__ __forceinline__ Span span_of(const PrefillArgs& p, int b) {
   return s;
 }
 
-// One warp per (row, head): the row's sequence by a walk over cu_q.
+// D (+)= A B with A from Tensor Memory (bf16, two a column).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+#define MOE_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                     "=r"(r[i + 6]), "=r"(r[i + 7])
+#define MOE_RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                      "+r"(r[i + 6]), "+r"(r[i + 7])
+#define MOE_RI8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                      "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 lanes x 32 columns from r[i] on / back.
+template <int N>
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[N], int i) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : MOE_R8(r, i), MOE_R8(r, i + 8), MOE_R8(r, i + 16), MOE_R8(r, i + 24) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::MOE_RI8(r, 0), MOE_RI8(r, 8), "r"(taddr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[N], int i) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::MOE_RI8(r, i), MOE_RI8(r, i + 8), MOE_RI8(r, i + 16), MOE_RI8(r, i + 24), "r"(taddr) : "memory");
+}
+// No use of r[i..i+31] is scheduled before this point.
+template <int N>
+__device__ __forceinline__ void reg_fence32(uint32_t (&r)[N], int i) {
+  asm volatile("" : MOE_RW8(r, i), MOE_RW8(r, i + 8), MOE_RW8(r, i + 16), MOE_RW8(r, i + 24));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) prefill_rows_kernel(const PrefillArgs p) {
+struct PrefillCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE = kTileN * D * 2;                      // bytes of a tile of rows, keys or values
+  static constexpr int STAGES = D == 128 ? 5 : 8;
+  static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024;
+  // two softmax warpgroups and one whose first two warps load and issue; of the registers that the block is launched with
+  // (168 a thread) the third warpgroup gives up what the others take: 2 x 232 + 40 = 3 x 168
+  static constexpr int THREADS = 384;
+  // Tensor Memory columns
+  static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;
+};
+
+// One row's attention straight from its definition, by a warp: for rows that see a key or value that is not finite.
+template <int D>
+__device__ __noinline__ void redo_row(const PrefillArgs& p, const Span& s, int row, int h) {
   constexpr int N = D / 32;
-  const int lane = threadIdx.x % 32, h = blockIdx.y, hk = h / (p.a.Hq / p.a.Hkv);
-  const int t = blockIdx.x * 8 + threadIdx.x / 32;
-  Span s{0, 0, 0, 0};
-  for (int b = 0; b < p.a.B; ++b) {
-    s = span_of(p, b);
-    if (t >= s.q0 && t < s.q0 + s.qn) break;
-    s.qn = 0;
-  }
-  if (s.qn == 0) return;
-  const Visible see(s.kn - s.qn + t - s.q0, p.a.window, p.a.sinks);
+  const int lane = threadIdx.x % 32, hk = h / (p.a.Hq / p.a.Hkv);
+  const long long t = s.q0 + row;
+  const Visible see(s.kn - s.qn + row, p.a.window, p.a.sinks);
   LaneRow<D> q;
-  q.load_bf16(p.q + (long long)t * p.q_stride + (long long)h * D, lane);
+  q.load_bf16(p.q + t * p.q_stride + (long long)h * D, lane);
   float m = -INFINITY, l = 0.f, o[N] = {};
   attend_row<D>(q, see, 0, 1, p.a.scale * 1.4426950408889634f, m, l, o, [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
     k.load_bf16(p.k + (long long)(s.k0 + j) * p.k_stride + (long long)hk * D, lane);
     v.load_bf16(p.v + (long long)(s.k0 + j) * p.v_stride + (long long)hk * D, lane);
     return true;
   });
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((long long)t * p.a.Hq + h) * D + lane * N);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (t * p.a.Hq + h) * D + lane * N);
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) out[i] = bf16x2(l == 0.f ? 0.f : o[2 * i] * inv, l == 0.f ? 0.f : o[2 * i + 1] * inv);
+  for (int i = 0; i < N / 2; ++i)
+    out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PrefillCfg<D>::THREADS, 1)
+prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const PrefillArgs p) {
+  using C = PrefillCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t q_full, s_full[2], p_full[2], o_full[2], kv_full[C::STAGES], kv_empty[C::STAGES], drain;
+  __shared__ uint64_t v_clean[C::STAGES];
+  __shared__ int bad_count, bad_keys[kBadKeys];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag;
+  __shared__ int work[2];                       // sequence (-1: nothing to do) and first row
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + 2 * C::TILE;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per_block = p.pair ? kTileM : 2 * kTileM;
+  const int head_blocks = p.pair ? p.a.Hq / 2 : p.a.Hq;
+  const int h0 = (blockIdx.x % head_blocks) * (p.pair ? 2 : 1);
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+      mbar_init(&v_clean[i], 64);
+    }
+    abort_flag = 0;
+    bad_count = 0;
+    mbar_fence_init();
+  }
+  pdl_wait();
+  if (warp == 8) {
+    // The block's sequence and rows: blocks are numbered from the last rows of the last sequence on, so that long rows
+    // are begun first.
+    int total = 0;
+    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
+      const int n = b0 + lane < p.a.B ? span_of(p, b0 + lane).qn : 0;
+      total += __reduce_add_sync(0xffffffffu, (n + per_block - 1) / per_block);
+    }
+    int want = total - 1 - (int)(blockIdx.x / head_blocks), b = -1, r0 = 0;
+    for (int b0 = 0; want >= 0 && b0 < p.a.B; b0 += 32) {
+      const int n = b0 + lane < p.a.B ? span_of(p, b0 + lane).qn : 0;
+      const int mine = (n + per_block - 1) / per_block;
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, want < upto);
+      if (here) {
+        const int who = __ffs(here) - 1;
+        b = b0 + who;
+        r0 = (want - __shfl_sync(0xffffffffu, upto - mine, who)) * per_block;
+        break;
+      }
+      want -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) {
+      work[0] = b;
+      work[1] = r0;
+    }
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int b = work[0], r0 = work[1];
+  const Span span = b < 0 ? Span{0, 0, 0, 0} : span_of(p, b);
+
+  // The keys that any of the block's rows sees, as tiles: the first tokens', then the window's.
+  const int off = span.kn - span.qn;            // position of row 0
+  const int r_end = min(span.qn, r0 + per_block);
+  const int p_lo = off + r0, p_hi = b < 0 ? -1 : off + r_end - 1;
+  const int first_any = (p.a.window && p_lo >= p.a.window) ? p_lo + 1 - p.a.window : 0;
+  const int first_hi = (p.a.window && p_hi >= p.a.window) ? p_hi + 1 - p.a.window : 0;
+  const int sink_tiles = (min(p.a.sinks, first_hi) + kTileN - 1) / kTileN;
+  const int win_tile = max(first_any / kTileN, sink_tiles);
+  const int tiles = p_hi < 0 ? 0 : sink_tiles + (p_hi + kTileN) / kTileN - win_tile;
+  auto key_of = [&](int i) { return (i < sink_tiles ? i : win_tile + (i - sink_tiles)) * kTileN; };
+  const int hk = h0 / (p.a.Hq / p.a.Hkv);
+  // Whether some row of tile x does not see some key of step i. There the weights of tile x go to the product in two
+  // parts, rounded and rest, because rows that see few keys have them in such steps; elsewhere the roundings of many
+  // keys even out.
+  auto edge_of = [&](int x, int i) {
+    const int t0 = r0 + (p.pair ? 0 : x * kTileM), j0 = key_of(i), last = off + t0 + kTileM - 1;
+    const int first_last = (p.a.window && last >= p.a.window) ? last + 1 - p.a.window : 0;
+    return t0 + kTileM > r_end || j0 + kTileN - 1 > off + t0 || (j0 < first_last && j0 + kTileN > p.a.sinks);
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    // ---------------- loads ----------------
+    if (warp == 8 && lane == 0 && tiles > 0) {
+      mbar_arrive_expect_tx(&q_full, 2 * C::TILE);
+      for (int x = 0; x < 2; ++x)
+        for (int d = 0; d < C::HALVES; ++d)
+          tma_load_3d(smem + x * C::TILE + d * kTileM * 128, &qmap, d * 64, p.pair ? h0 + x : h0,
+                      span.q0 + r0 + (p.pair ? 0 : x * kTileM), &q_full);
+      int n = 0;
+      for (; n < 2 * tiles; ++n) {              // K of a step, V of a step, in turn
+        const int s = n % C::STAGES;
+        if (n >= C::STAGES && !mbar_wait(&kv_empty[s], (n / C::STAGES - 1) & 1, kPrefillWaitNs, &abort_flag, p.status,
+                                         DEV_TIMEOUT_EMPTY))
+          break;
+        mbar_arrive_expect_tx(&kv_full[s], C::TILE);
+        for (int d = 0; d < C::HALVES; ++d)
+          tma_load_3d(ring + s * C::TILE + d * kTileN * 128, n & 1 ? &vmap : &kmap, d * 64, hk, span.k0 + key_of(n / 2),
+                      &kv_full[s]);
+      }
+      if (abort_flag) {                         // copies in flight end before the block does
+        mbar_wait(&q_full, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+        for (int j = max(0, n - C::STAGES); j < n; ++j)
+          mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      }
+    }
+    // ---------------- products ----------------
+    if (warp == 9 && lane == 0 && tiles > 0) {
+      const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN);
+      const uint32_t idesc_pv = idesc_bf16_f32(kTileM, D) | (1u << 16);      // V: its D values contiguous, keys apart
+      const uint32_t qa = smem_u32(smem), ra = smem_u32(ring);
+      auto qk = [&](int x, int s) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t at = (ks / 4) * kTileN * 128 + (ks % 4) * 32;
+          mma_bf16(tmem + (x ? C::S1 : C::S0), smem_desc(qa + x * C::TILE + at, 16, 1024, 2),
+                   smem_desc(ra + s * C::TILE + at, 16, 1024, 2), idesc_qk, ks > 0);
+        }
+        tc_commit(&s_full[x]);
+      };
+      auto pv = [&](int x, int s, bool more, bool edge, bool release) {
+#pragma unroll
+        for (int ks = 0; ks < kTileN / 16; ++ks)
+          mma_bf16_ts(tmem + (x ? C::O1 : C::O0), tmem + (x ? C::S1 : C::S0) + ks * 8,
+                      smem_desc(ra + s * C::TILE + ks * 2048, kTileN * 128, 1024, 2), idesc_pv, more || ks > 0);
+        if (edge)
+#pragma unroll
+          for (int ks = 0; ks < kTileN / 16; ++ks)
+            mma_bf16_ts(tmem + (x ? C::O1 : C::O0), tmem + (x ? C::S1 : C::S0) + kTileN / 2 + ks * 8,
+                        smem_desc(ra + s * C::TILE + ks * 2048, kTileN * 128, 1024, 2), idesc_pv, 1);
+        if (release) tc_commit(&kv_empty[s]);
+        tc_commit(&o_full[x]);
+      };
+      auto have = [&](int n) {
+        return mbar_wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, kPrefillWaitNs, &abort_flag, p.status,
+                         DEV_TIMEOUT_FULL);
+      };
+      bool ok = mbar_wait(&q_full, 0, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL) && have(0);
+      if (ok) {
+        qk(0, 0);
+        qk(1, 0);
+        tc_commit(&kv_empty[0]);
+      }
+      uint32_t cleaned = 0;                     // parity of v_clean's next phase, a bit a stage
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int vs = (2 * i + 1) % C::STAGES, ks = (2 * i + 2) % C::STAGES;
+        const bool edge[2] = {edge_of(0, i), edge_of(1, i)};
+        if (edge[0] || edge[1]) {
+          ok = mbar_wait(&v_clean[vs], (cleaned >> vs) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL);
+          cleaned ^= 1u << vs;
+        } else {
+          ok = have(2 * i + 1);
+        }
+        for (int x = 0; ok && x < 2; ++x) {
+          ok = mbar_wait(&p_full[x], i & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
+          if (!ok) break;
+          tc_fence_after();
+          pv(x, vs, i > 0, edge[x], x == 1 && i + 1 < tiles);
+          if (i + 1 < tiles) {
+            // S of the next step over P of this one: products are executed in the order of their issue
+            if (x == 0 && !(ok = have(2 * i + 2))) break;
+            qk(x, ks);
+            if (x == 1) tc_commit(&kv_empty[ks]);
+          }
+        }
+      }
+      if (!ok) {
+        tc_commit(&drain);
+        mbar_wait(&drain, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      }
+    }
+    // ---------------- values that are not finite ----------------
+    // A weight of zero does not hide such a value in the product. Where a row of the block does not see every key of a
+    // step, they are set to zero, and the rows that do see them are listed to be computed again.
+    if (warp >= 10) {
+      const int tid = threadIdx.x - 320;
+      for (int i = 0; i < tiles; ++i) {
+        if (!edge_of(0, i) && !edge_of(1, i)) continue;
+        const int n = 2 * i + 1, st = n % C::STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[st], (n / C::STAGES) & 1, kPrefillWaitNs, &abort_flag, p.status,
+                                               DEV_TIMEOUT_FULL)))
+          break;
+        uint4* v = reinterpret_cast<uint4*>(ring + st * C::TILE);
+        bool wrote = false;
+#pragma unroll 4
+        for (int e = tid; e < C::TILE / 16; e += 64) {
+          const uint4 a = v[e];
+          // an exponent field of all ones carries into the bit above it when its lowest bit is added
+          const uint32_t any = (((a.x & 0x7F807F80u) + 0x00800080u) | ((a.y & 0x7F807F80u) + 0x00800080u) |
+                                ((a.z & 0x7F807F80u) + 0x00800080u) | ((a.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+          if (any) {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            uint32_t z[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const uint32_t hit = ((w[f] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              z[f] = w[f] & ~((hit >> 15) * 0xFFFFu);
+            }
+            v[e] = make_uint4(z[0], z[1], z[2], z[3]);
+            wrote = true;
+          }
+          // 8 neighbouring lanes hold one key's 64 values: one of them lists it
+          const unsigned hits = __ballot_sync(0xffffffffu, any != 0) & (0xFFu << (tid & 24));
+          if (any && __ffs(hits) - 1 == (tid & 31)) {
+            const int at = atomicAdd(&bad_count, 1);
+            if (at < kBadKeys) bad_keys[at] = key_of(i) + e / 8 % kTileN;
+          }
+        }
+        if (wrote) fence_async_smem();
+        mbar_arrive(&v_clean[st]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    // ---------------- softmax ----------------
+    const int x = warp / 4, tid = threadIdx.x % 128;
+    const int h = p.pair ? h0 + x : h0;
+    const int row = r0 + (p.pair ? 0 : x * kTileM) + tid;                      // of the sequence
+    const bool live = row < r_end;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + (x ? C::S1 : C::S0) + lanes, to = tmem + (x ? C::O1 : C::O0) + lanes;
+    const int pos = live ? off + row : -1;
+    const int first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
+    // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
+    const float sgn = p.a.scale < 0.f ? -1.f : 1.f;
+    const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
+    const uint64_t c2 = pack2(c, c);
+    float m = -INFINITY;                        // the maximum that the weights so far refer to
+    uint64_t l2 = pack2(0.f, 0.f);
+    bool ok = true;
+    for (int i = 0; ok && i < tiles; ++i) {
+      ok = mbar_wait(&s_full[x], i & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
+      if (sgn < 0.f) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e) s[e] ^= 0x80000000u;
+      }
+      const int j0 = key_of(i);
+      const bool edge = edge_of(x, i);
+      if (edge) {
+        const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (!(e <= hi && (e >= lo || e < low))) s[e] = 0xff800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 128; e += 4)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) mx[f] = fmaxf(mx[f], __uint_as_float(s[e + f]));
+      const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      if (__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) {      // (-inf) - (-inf): no
+        if (i > 0) {
+          ok = mbar_wait(&o_full[x], (i - 1) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = m == -INFINITY ? 0.f : ex2f((m - mn) * c);
+          const uint64_t f2 = pack2(f, f);
+          l2 = mul2(l2, f2);
+#pragma unroll
+          for (int e = 0; e < D; e += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + e, o, 0);
+            tmem_ld_wait();
+            reg_fence32(o, 0);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+            tmem_st32(to + e, o, 0);
+          }
+        }
+        m = mn;
+      }
+      const float base = m == -INFINITY ? 0.f : -m * c;
+      const uint64_t b2 = pack2(base, base);
+      uint64_t la = pack2(0.f, 0.f), lb = la;
+#pragma unroll
+      for (int e = 0; e < 128; e += 4) {
+        float w0, w1, w2, w3;
+        unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), w0, w1);
+        unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), w2, w3);
+        w0 = ex2f(w0), w1 = ex2f(w1), w2 = ex2f(w2), w3 = ex2f(w3);
+        la = add2(la, pack2(w0, w1));
+        lb = add2(lb, pack2(w2, w3));
+        if (!edge) {
+          s[e / 2] = bf16x2(w0, w1);            // s[e / 2] has been read
+          s[e / 2 + 1] = bf16x2(w2, w3);
+        } else {
+          s[e] = __float_as_uint(w0), s[e + 1] = __float_as_uint(w1);
+          s[e + 2] = __float_as_uint(w2), s[e + 3] = __float_as_uint(w3);
+        }
+      }
+      l2 = add2(l2, add2(la, lb));
+      if (!edge) {
+        tmem_st32(ts, s, 0);
+        tmem_st32(ts + 32, s, 32);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) {
+          uint32_t top[16], rest[16];
+#pragma unroll
+          for (int d = 0; d < 16; ++d) {
+            const float w0 = __uint_as_float(s[e + 2 * d]), w1 = __uint_as_float(s[e + 2 * d + 1]);
+            top[d] = bf16x2(w0, w1);
+            rest[d] = bf16x2(w0 - bf16_lo(top[d]), w1 - bf16_hi(top[d]));
+          }
+          tmem_st16(ts + e / 2, top);
+          tmem_st16(ts + kTileN / 2 + e / 2, rest);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[x]);
+    }
+    if (ok && tiles > 0) {
+      ok = mbar_wait(&o_full[x], (tiles - 1) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok && b >= 0) {
+      float la, lb;
+      unpack2(l2, la, lb);
+      const float l = la + lb, inv = 1.f / l;
+      // every value that is not finite was listed before the last product that met it
+      const int listed = *reinterpret_cast<volatile int*>(&bad_count);
+      bool fine = listed <= kBadKeys;
+      const Visible see(pos, p.a.window, p.a.sinks);
+      for (int i = 0; i < min(listed, kBadKeys); ++i) fine = fine && !see.sees(bad_keys[i]);
+      uint16_t* out = p.out + ((long long)(span.q0 + row) * p.a.Hq + h) * D;
+#pragma unroll
+      for (int e = 0; e < D; e += 32) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld32(to + e, o, 0);
+          tmem_ld_wait();
+          reg_fence32(o, 0);
+        }
+#pragma unroll
+        for (int d = 0; d < 32; d += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const float u = l == 0.f ? 0.f : __uint_as_float(o[d + 2 * f]) * inv;
+            const float v = l == 0.f ? 0.f : __uint_as_float(o[d + 2 * f + 1]) * inv;
+            fine = fine && isfinite(u) && isfinite(v);
+            w[f] = bf16x2(u, v);
+          }
+          if (live) *reinterpret_cast<uint4*>(out + e + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      for (unsigned again = __ballot_sync(0xffffffffu, live && !fine); again; again &= again - 1)
+        redo_row<D>(p, span, row - lane + __ffs(again) - 1, h);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+static int rows_map(CUtensorMap* m, const void* base, int D, int heads, int rows, long long stride) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return MOE_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTileN};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int D>
+static int launch_prefill(const PrefillArgs& p, cudaStream_t st) {
+  CUtensorMap qm, km, vm;
+  int rc = rows_map(&qm, p.q, D, p.a.Hq, p.Tq, p.q_stride);
+  // without keys no tile is loaded; the maps have to describe something all the same
+  if (!rc) rc = p.Tk ? rows_map(&km, p.k, D, p.a.Hkv, p.Tk, p.k_stride) : rows_map(&km, p.q, D, p.a.Hq, p.Tq, p.q_stride);
+  if (!rc) rc = p.Tk ? rows_map(&vm, p.v, D, p.a.Hkv, p.Tk, p.v_stride) : rows_map(&vm, p.q, D, p.a.Hq, p.Tq, p.q_stride);
+  if (rc) return rc;
+  auto kern = prefill_attention_kernel<D>;
+  if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), PrefillCfg<D>::SMEM))) return rc;
+  const int per_block = p.pair ? kTileM : 2 * kTileM;
+  const long long blocks = ((long long)p.Tq / per_block + p.a.B) * (p.pair ? p.a.Hq / 2 : p.a.Hq);
+  if (blocks >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PrefillCfg<D>::THREADS), PrefillCfg<D>::SMEM, st, qm, km, vm, p);
 }
 
 }  // namespace moe
@@ -89,8 +616,7 @@ extern "C" int moe_prefill_attention(const moe_attention* a, int32_t Tq, int32_t
     return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3) return MOE_ERR_INVALID_ARG;
   const PrefillArgs p{*a, Tq, Tk, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k ? cu_k : cu_q, out,
-                      static_cast<uint32_t*>(ws)};
-  auto kern = a->D == 64 ? prefill_rows_kernel<64> : prefill_rows_kernel<128>;
-  kern<<<dim3((Tq + 7) / 8, a->Hq), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return launch_status();
+                      static_cast<uint32_t*>(ws), (a->Hq / a->Hkv) % 2 == 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->D == 64 ? launch_prefill<64>(p, st) : launch_prefill<128>(p, st);
 }
