@@ -149,7 +149,7 @@ struct PrefillCfg {
   static constexpr int STAGES = D == 128 ? 5 : 8;
   static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024;
   // two softmax warpgroups and one whose first two warps load and issue; of the registers that the block is launched with
-  // (168 a thread) the third warpgroup gives up what the others take: 2 x 232 + 40 = 3 x 168
+  // (168 a thread) the third warpgroup gives up what the others take: 2 x 208 + 88 = 3 x 168
   static constexpr int THREADS = 384;
   // Tensor Memory columns
   static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;
@@ -279,7 +279,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ---------------- loads ----------------
     if (warp == 8 && lane == 0 && tiles > 0) {
       mbar_arrive_expect_tx(&q_full, 2 * C::TILE);
@@ -411,7 +411,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax ----------------
     const int x = warp / 4, tid = threadIdx.x % 128;
     const int h = p.pair ? h0 + x : h0;
@@ -482,24 +482,21 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       const float base = m == -INFINITY ? 0.f : -m * c;
       const uint64_t b2 = pack2(base, base);
       uint64_t la = pack2(0.f, 0.f), lb = la;
-#pragma unroll
-      for (int e = 0; e < 128; e += 4) {
-        float w0, w1, w2, w3;
+      auto weights = [&](int e, float& w0, float& w1, float& w2, float& w3) {
         unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), w0, w1);
         unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), w2, w3);
         w0 = ex2f(w0), w1 = ex2f(w1), w2 = ex2f(w2), w3 = ex2f(w3);
         la = add2(la, pack2(w0, w1));
         lb = add2(lb, pack2(w2, w3));
-        if (!edge) {
+      };
+      if (!edge) {
+#pragma unroll
+        for (int e = 0; e < 128; e += 4) {
+          float w0, w1, w2, w3;
+          weights(e, w0, w1, w2, w3);
           s[e / 2] = bf16x2(w0, w1);            // s[e / 2] has been read
           s[e / 2 + 1] = bf16x2(w2, w3);
-        } else {
-          s[e] = __float_as_uint(w0), s[e + 1] = __float_as_uint(w1);
-          s[e + 2] = __float_as_uint(w2), s[e + 3] = __float_as_uint(w3);
         }
-      }
-      l2 = add2(l2, add2(la, lb));
-      if (!edge) {
         tmem_st32(ts, s, 0);
         tmem_st32(ts + 32, s, 32);
       } else {
@@ -507,15 +504,20 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         for (int e = 0; e < 128; e += 32) {
           uint32_t top[16], rest[16];
 #pragma unroll
-          for (int d = 0; d < 16; ++d) {
-            const float w0 = __uint_as_float(s[e + 2 * d]), w1 = __uint_as_float(s[e + 2 * d + 1]);
-            top[d] = bf16x2(w0, w1);
-            rest[d] = bf16x2(w0 - bf16_lo(top[d]), w1 - bf16_hi(top[d]));
+          for (int d = 0; d < 16; d += 2) {
+            float w[4];
+            weights(e + 2 * d, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              top[d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
+              rest[d + f] = bf16x2(w[2 * f] - bf16_lo(top[d + f]), w[2 * f + 1] - bf16_hi(top[d + f]));
+            }
           }
           tmem_st16(ts + e / 2, top);
           tmem_st16(ts + kTileN / 2 + e / 2, rest);
         }
       }
+      l2 = add2(l2, add2(la, lb));
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[x]);
