@@ -93,11 +93,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[N], int 
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : MOE_R8(r, i), MOE_R8(r, i + 8), MOE_R8(r, i + 16), MOE_R8(r, i + 24) : "r"(taddr) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::MOE_RI8(r, 0), MOE_RI8(r, 8), "r"(taddr) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[N], int i) {
   asm volatile(
@@ -191,7 +186,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + 2 * C::TILE;
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int per_block = p.pair ? kTileM : 2 * kTileM;
   const int head_blocks = p.pair ? p.a.Hq / 2 : p.a.Hq;
   const int h0 = (blockIdx.x % head_blocks) * (p.pair ? 2 : 1);
@@ -271,11 +266,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   const int hk = h0 / (p.a.Hq / p.a.Hkv);
   // Whether some row of tile x does not see some key of step i. There the weights of tile x go to the product in two
   // parts, rounded and rest, because rows that see few keys have them in such steps; elsewhere the roundings of many
-  // keys even out.
+  // keys even out. (Scales below zero, which nobody uses, take this way throughout.)
   auto edge_of = [&](int x, int i) {
     const int t0 = r0 + (p.pair ? 0 : x * kTileM), j0 = key_of(i), last = off + t0 + kTileM - 1;
     const int first_last = (p.a.window && last >= p.a.window) ? last + 1 - p.a.window : 0;
-    return t0 + kTileM > r_end || j0 + kTileN - 1 > off + t0 || (j0 < first_last && j0 + kTileN > p.a.sinks);
+    return t0 + kTileM > r_end || j0 + kTileN - 1 > off + t0 || (j0 < first_last && j0 + kTileN > p.a.sinks) ||
+           p.a.scale < 0.f;
   };
 
   if (warp >= 8) {
@@ -305,66 +301,83 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       }
     }
     // ---------------- products ----------------
-    if (warp == 9 && lane == 0 && tiles > 0) {
+    // The whole warp goes along and one lane issues: addresses stay uniform, and so in uniform registers. (With one
+    // lane alone in the branch each product took 80 to 160 cycles to issue, of the 32 that it runs.)
+    if (warp == 9 && tiles > 0) {
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const bool leader = elect_one();
       const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN);
       const uint32_t idesc_pv = idesc_bf16_f32(kTileM, D) | (1u << 16);      // V: its D values contiguous, keys apart
-      const uint32_t qa = smem_u32(smem), ra = smem_u32(ring);
-      auto qk = [&](int x, int s) {
+      const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);
+      const uint64_t vdesc = smem_desc(smem_u32(ring), kTileN * 128, 1024, 2);
+      auto qk = [&](int x, int s, bool release) {
+        if (leader) {
+          const uint64_t qx = qdesc + x * (C::TILE >> 4), kx = kdesc + s * (C::TILE >> 4);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = (ks / 4) * kTileN * 128 + (ks % 4) * 32;
-          mma_bf16(tmem + (x ? C::S1 : C::S0), smem_desc(qa + x * C::TILE + at, 16, 1024, 2),
-                   smem_desc(ra + s * C::TILE + at, 16, 1024, 2), idesc_qk, ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int at = ((ks / 4) * kTileN * 128 + (ks % 4) * 32) >> 4;
+            mma_bf16(tm + x * (C::S1 - C::S0) + C::S0, qx + at, kx + at, idesc_qk, ks > 0);
+          }
+          tc_commit(&s_full[x]);
+          if (release) tc_commit(&kv_empty[s]);
         }
-        tc_commit(&s_full[x]);
+        __syncwarp();
       };
       auto pv = [&](int x, int s, bool more, bool edge, bool release) {
+        if (leader) {
+          const uint32_t d = tm + x * (C::O1 - C::O0) + C::O0, a = tm + x * (C::S1 - C::S0) + C::S0;
+          const uint64_t vx = vdesc + s * (C::TILE >> 4);
+          if (!edge) {
 #pragma unroll
-        for (int ks = 0; ks < kTileN / 16; ++ks)
-          mma_bf16_ts(tmem + (x ? C::O1 : C::O0), tmem + (x ? C::S1 : C::S0) + ks * 8,
-                      smem_desc(ra + s * C::TILE + ks * 2048, kTileN * 128, 1024, 2), idesc_pv, more || ks > 0);
-        if (edge)
+            for (int ks = 0; ks < kTileN / 16; ++ks)
+              mma_bf16_ts(d, a + ks * 8, vx + ks * (2048 >> 4), idesc_pv, more || ks > 0);
+          } else {
+            // of every 32 columns 16 hold the rounded weights of 32 keys, 16 the rests
 #pragma unroll
-          for (int ks = 0; ks < kTileN / 16; ++ks)
-            mma_bf16_ts(tmem + (x ? C::O1 : C::O0), tmem + (x ? C::S1 : C::S0) + kTileN / 2 + ks * 8,
-                        smem_desc(ra + s * C::TILE + ks * 2048, kTileN * 128, 1024, 2), idesc_pv, 1);
-        if (release) tc_commit(&kv_empty[s]);
-        tc_commit(&o_full[x]);
+            for (int ks = 0; ks < kTileN / 16; ++ks) {
+              mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8, vx + ks * (2048 >> 4), idesc_pv, more || ks > 0);
+              mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8 + 16, vx + ks * (2048 >> 4), idesc_pv, 1);
+            }
+          }
+          if (release) tc_commit(&kv_empty[s]);
+          tc_commit(&o_full[x]);
+        }
+        __syncwarp();
       };
-      auto have = [&](int n) {
-        return mbar_wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, kPrefillWaitNs, &abort_flag, p.status,
-                         DEV_TIMEOUT_FULL);
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPrefillWaitNs, &abort_flag, p.status, code)) != 0;
       };
-      bool ok = mbar_wait(&q_full, 0, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL) && have(0);
+      auto have = [&](int n) { return wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, DEV_TIMEOUT_FULL); };
+      bool ok = wait(&q_full, 0, DEV_TIMEOUT_FULL) && have(0);
       if (ok) {
-        qk(0, 0);
-        qk(1, 0);
-        tc_commit(&kv_empty[0]);
+        qk(0, 0, false);
+        qk(1, 0, true);
       }
       uint32_t cleaned = 0;                     // parity of v_clean's next phase, a bit a stage
       for (int i = 0; ok && i < tiles; ++i) {
         const int vs = (2 * i + 1) % C::STAGES, ks = (2 * i + 2) % C::STAGES;
         const bool edge[2] = {edge_of(0, i), edge_of(1, i)};
         if (edge[0] || edge[1]) {
-          ok = mbar_wait(&v_clean[vs], (cleaned >> vs) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL);
+          ok = wait(&v_clean[vs], (cleaned >> vs) & 1, DEV_TIMEOUT_FULL);
           cleaned ^= 1u << vs;
         } else {
           ok = have(2 * i + 1);
         }
-        for (int x = 0; ok && x < 2; ++x) {
-          ok = mbar_wait(&p_full[x], i & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ok = ok && wait(&p_full[x], i & 1, DEV_TIMEOUT_ACCUM);
           if (!ok) break;
           tc_fence_after();
           pv(x, vs, i > 0, edge[x], x == 1 && i + 1 < tiles);
           if (i + 1 < tiles) {
             // S of the next step over P of this one: products are executed in the order of their issue
             if (x == 0 && !(ok = have(2 * i + 2))) break;
-            qk(x, ks);
-            if (x == 1) tc_commit(&kv_empty[ks]);
+            qk(x, ks, x == 1);
           }
         }
       }
-      if (!ok) {
+      if (!ok && leader) {
         tc_commit(&drain);
         mbar_wait(&drain, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
       }
@@ -422,7 +435,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     const int pos = live ? off + row : -1;
     const int first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
     // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
-    const float sgn = p.a.scale < 0.f ? -1.f : 1.f;
+    const uint32_t turn = p.a.scale < 0.f ? 0x80000000u : 0u;
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
     const uint64_t c2 = pack2(c, c);
     float m = -INFINITY;                        // the maximum that the weights so far refer to
@@ -433,40 +446,20 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
-      tmem_ld_wait();
-#pragma unroll
-      for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
-      if (sgn < 0.f) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e) s[e] ^= 0x80000000u;
-      }
       const int j0 = key_of(i);
-      const bool edge = edge_of(x, i);
-      if (edge) {
-        const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (!(e <= hi && (e >= lo || e < low))) s[e] = 0xff800000u;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 128; e += 4)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) mx[f] = fmaxf(mx[f], __uint_as_float(s[e + f]));
-      const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-      if (__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) {      // (-inf) - (-inf): no
+      float mx = -INFINITY;
+      // The maximum that the weights refer to moves only when one has outgrown it; then what has been summed is rescaled.
+      auto move_base = [&]() {
+        const float mn = fmaxf(m, mx);
+        if (!__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) return true;      // (-inf) - (-inf): no
         if (i > 0) {
-          ok = mbar_wait(&o_full[x], (i - 1) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], (i - 1) & 1, kPrefillWaitNs, &abort_flag, p.status,
+                                                 DEV_TIMEOUT_ACCUM)))
+            return false;
           tc_fence_after();
           const float f = m == -INFINITY ? 0.f : ex2f((m - mn) * c);
-          const uint64_t f2 = pack2(f, f);
-          l2 = mul2(l2, f2);
-#pragma unroll
+          l2 = mul2(l2, pack2(f, f));
+#pragma unroll 1
           for (int e = 0; e < D; e += 32) {
             uint32_t o[32];
             tmem_ld32(to + e, o, 0);
@@ -478,43 +471,83 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           }
         }
         m = mn;
-      }
-      const float base = m == -INFINITY ? 0.f : -m * c;
-      const uint64_t b2 = pack2(base, base);
-      uint64_t la = pack2(0.f, 0.f), lb = la;
-      auto weights = [&](int e, float& w0, float& w1, float& w2, float& w3) {
-        unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), w0, w1);
-        unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), w2, w3);
-        w0 = ex2f(w0), w1 = ex2f(w1), w2 = ex2f(w2), w3 = ex2f(w3);
-        la = add2(la, pack2(w0, w1));
-        lb = add2(lb, pack2(w2, w3));
+        return true;
       };
-      if (!edge) {
+      uint64_t la = pack2(0.f, 0.f), lb = la, b2 = la;
+      auto weights = [&](const uint32_t* s, float (&w)[4]) {
+        unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, b2), w[0], w[1]);
+        unpack2(fma2(pack2(__uint_as_float(s[2]), __uint_as_float(s[3])), c2, b2), w[2], w[3]);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) w[f] = ex2f(w[f]);
+        la = add2(la, pack2(w[0], w[1]));
+        lb = add2(lb, pack2(w[2], w[3]));
+      };
+      if (!edge_of(x, i)) {
+        uint32_t s[128];
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 4)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) m4[f] = fmaxf(m4[f], __uint_as_float(s[e + f]));
+        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (!(ok = move_base())) break;
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        b2 = pack2(base, base);
 #pragma unroll
         for (int e = 0; e < 128; e += 4) {
-          float w0, w1, w2, w3;
-          weights(e, w0, w1, w2, w3);
-          s[e / 2] = bf16x2(w0, w1);            // s[e / 2] has been read
-          s[e / 2 + 1] = bf16x2(w2, w3);
+          float w[4];
+          weights(s + e, w);
+          s[e / 2] = bf16x2(w[0], w[1]);        // s[e / 2] has been read
+          s[e / 2 + 1] = bf16x2(w[2], w[3]);
         }
         tmem_st32(ts, s, 0);
         tmem_st32(ts + 32, s, 32);
       } else {
+        // Twice over the scores, 32 at a time, in little code: these steps are few.
+        const int hi = min(pos - j0, 127), lo = max(first - j0, 0), low = min(p.a.sinks - j0, hi + 1);
+        auto load = [&](int e, uint32_t (&s)[32]) {
+          tmem_ld32(ts + e, s, 0);
+          // bit d: the row sees key e + d, that is lo <= e + d <= hi or e + d < low
+          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+          const uint32_t see = (below(hi + 1 - e) & ~below(lo - e)) | below(low - e);
+          tmem_ld_wait();
+          reg_fence32(s, 0);
 #pragma unroll
+          for (int d = 0; d < 32; ++d) s[d] = (see >> d) & 1u ? s[d] ^ turn : 0xff800000u;
+        };
+#pragma unroll 1
         for (int e = 0; e < 128; e += 32) {
-          uint32_t top[16], rest[16];
+          uint32_t s[32];
+          load(e, s);
+#pragma unroll
+          for (int d = 0; d < 32; ++d) mx = fmaxf(mx, __uint_as_float(s[d]));
+        }
+        if (!(ok = move_base())) break;
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        b2 = pack2(base, base);
+#pragma unroll 1
+        for (int e = 0; e < 128; e += 32) {
+          uint32_t s[32];
+          load(e, s);
+          uint32_t rest[16];
 #pragma unroll
           for (int d = 0; d < 16; d += 2) {
             float w[4];
-            weights(e + 2 * d, w[0], w[1], w[2], w[3]);
+            weights(s + 2 * d, w);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              top[d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
-              rest[d + f] = bf16x2(w[2 * f] - bf16_lo(top[d + f]), w[2 * f + 1] - bf16_hi(top[d + f]));
+              s[d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
+              rest[d + f] = bf16x2(w[2 * f] - bf16_lo(s[d + f]), w[2 * f + 1] - bf16_hi(s[d + f]));
             }
           }
-          tmem_st16(ts + e / 2, top);
-          tmem_st16(ts + kTileN / 2 + e / 2, rest);
+#pragma unroll
+          for (int d = 0; d < 16; ++d) s[16 + d] = rest[d];
+          tmem_st32(ts + e, s, 0);
         }
       }
       l2 = add2(l2, add2(la, lb));
@@ -537,7 +570,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       const Visible see(pos, p.a.window, p.a.sinks);
       for (int i = 0; i < min(listed, kBadKeys); ++i) fine = fine && !see.sees(bad_keys[i]);
       uint16_t* out = p.out + ((long long)(span.q0 + row) * p.a.Hq + h) * D;
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < D; e += 32) {
         uint32_t o[32];
         if (tiles > 0) {
