@@ -7,7 +7,8 @@
 // A block has two tiles of 128 rows that share their keys: two heads of a group, or where a group has an odd number of
 // heads, 256 rows of one. While one tile's weights are computed (one warpgroup each, a thread per row), the tensor
 // cores work on the other's products:  PV0(i) QK0(i+1) | PV1(i) QK1(i+1).
-// The output is rescaled only when a row's maximum has grown by more than 2^8 since the last time (weights of up to 256
+// Blocks stay (one an SM) and take one item after the other, so that the next item's loads and first products run under
+// the last one's end. The output is rescaled only when a row's maximum has grown by more than 2^8 since the last time (weights of up to 256
 // are as exact in bf16 as those up to 1), so that the softmax warps seldom touch it.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,6 +24,7 @@ constexpr int kTileM = 128;             // query rows of a tile
 constexpr int kTileN = 128;             // keys of a step
 constexpr uint64_t kPrefillWaitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kFewKeys = 512;           // rows that see fewer keep their weights in two parts
 constexpr int kBadKeys = 64;            // keys with values that are not finite that a block lists
 
 struct PrefillArgs {
@@ -93,6 +95,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[N], int 
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : MOE_R8(r, i), MOE_R8(r, i + 8), MOE_R8(r, i + 16), MOE_R8(r, i + 24) : "r"(taddr) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::MOE_RI8(r, 0), MOE_RI8(r, 8), "r"(taddr) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[N], int i) {
   asm volatile(
@@ -137,12 +144,20 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int D>
 struct PrefillCfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = kTileN * D * 2;                      // bytes of a tile of rows, keys or values
-  static constexpr int STAGES = D == 128 ? 5 : 8;
-  static constexpr int SMEM = 2 * TILE + STAGES * TILE + 1024;
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static_assert(STAGES % 2 == 0, "keys in the even stages, values in the odd ones");
+  static constexpr int OUT = 8 * 4096;                             // the output's way to global memory, 4 KB a warp
+  static constexpr int SMEM = 2 * TILE + STAGES * TILE + OUT + 1024;
   // two softmax warpgroups and one whose first two warps load and issue; of the registers that the block is launched with
   // (168 a thread) the third warpgroup gives up what the others take: 2 x 208 + 88 = 3 x 168
   static constexpr int THREADS = 384;
@@ -171,33 +186,75 @@ __device__ __noinline__ void redo_row(const PrefillArgs& p, const Span& s, int r
     out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
 }
 
+// Which steps of a tile are edges: some row of it does not see some key of the step that begins at j0. (Scales below
+// zero, which nobody uses, take the way of such steps throughout.)
+struct Edges {
+  int hi, lo, low;
+  __device__ __forceinline__ bool at(int j0) const { return j0 > hi || (j0 < lo && j0 > low); }
+};
+
+// A block's item: up to 2 x 128 rows of a sequence and the keys that any of them sees, as steps of 128: the first tokens'
+// steps, then the window's.
+struct Item {
+  Span s;
+  int r0, h0;                           // first row (of the sequence), first head
+  int off, r_end, sink_tiles, win_shift, tiles;
+  __device__ __forceinline__ Item(const PrefillArgs& p, const int (&slot)[8])
+      : s{slot[0], slot[1], slot[2], slot[3]}, r0(slot[4]), h0(slot[5]) {
+    off = s.kn - s.qn;                  // position of row 0
+    r_end = min(s.qn, r0 + (p.pair ? kTileM : 2 * kTileM));
+    const int p_hi = off + r_end - 1;
+    const int first_hi = first_of(p, p_hi);
+    sink_tiles = (min(p.a.sinks, first_hi) + kTileN - 1) / kTileN;
+    const int win_tile = max(first_of(p, off + r0) / kTileN, sink_tiles);
+    win_shift = win_tile - sink_tiles;
+    tiles = p_hi < 0 ? 0 : (p_hi + kTileN) / kTileN - win_shift;
+  }
+  static __device__ __forceinline__ int first_of(const PrefillArgs& p, int pos) {
+    return p.a.window && pos >= p.a.window ? pos + 1 - p.a.window : 0;
+  }
+  __device__ __forceinline__ int key_of(int i) const { return (i < sink_tiles ? i : i + win_shift) * kTileN; }
+  __device__ __forceinline__ int row_of(const PrefillArgs& p, int x) const { return r0 + (p.pair ? 0 : x * kTileM); }
+  __device__ __forceinline__ Edges edges(const PrefillArgs& p, int x) const {
+    const int t0 = row_of(p, x);
+    if (t0 + kTileM > r_end || p.a.scale < 0.f) return Edges{-1, 0, 0};
+    return Edges{off + t0 + 1 - kTileN, first_of(p, off + t0 + kTileM - 1), p.a.sinks - kTileN};
+  }
+  // Tiles whose first row sees few keys give their weights to the product in two parts in edge steps, rounded and rest;
+  // over many keys the roundings even out.
+  __device__ __forceinline__ bool split(const PrefillArgs& p, int x) const {
+    return off + row_of(p, x) < kFewKeys || (p.a.window && p.a.window < kFewKeys);
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const PrefillArgs p) {
   using C = PrefillCfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t q_full, s_full[2], p_full[2], o_full[2], kv_full[C::STAGES], kv_empty[C::STAGES], drain;
-  __shared__ uint64_t v_clean[C::STAGES];
-  __shared__ int bad_count, bad_keys[kBadKeys];
+  __shared__ uint64_t w_full[2], w_empty[2], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
+  __shared__ uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], v_clean[C::STAGES];
+  __shared__ int slots[2][8];                   // items: span, first row, first head, whether there is one
+  __shared__ int bad_count[2], bad_keys[2][kBadKeys];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
-  __shared__ int work[2];                       // sequence (-1: nothing to do) and first row
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + 2 * C::TILE;
+  uint8_t* staging = ring + C::STAGES * C::TILE;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  const int per_block = p.pair ? kTileM : 2 * kTileM;
-  const int head_blocks = p.pair ? p.a.Hq / 2 : p.a.Hq;
-  const int h0 = (blockIdx.x % head_blocks) * (p.pair ? 2 : 1);
-
   pdl_trigger();
   if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
     mbar_init(&drain, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 11);               // the warps of the products, of the cleaning and of the softmax
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i][0], 128);
+      mbar_init(&p_full[i][1], 128);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < C::STAGES; ++i) {
@@ -206,41 +263,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       mbar_init(&v_clean[i], 64);
     }
     abort_flag = 0;
-    bad_count = 0;
     mbar_fence_init();
-  }
-  pdl_wait();
-  if (warp == 8) {
-    // The block's sequence and rows: blocks are numbered from the last rows of the last sequence on, so that long rows
-    // are begun first.
-    int total = 0;
-    for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-      const int n = b0 + lane < p.a.B ? span_of(p, b0 + lane).qn : 0;
-      total += __reduce_add_sync(0xffffffffu, (n + per_block - 1) / per_block);
-    }
-    int want = total - 1 - (int)(blockIdx.x / head_blocks), b = -1, r0 = 0;
-    for (int b0 = 0; want >= 0 && b0 < p.a.B; b0 += 32) {
-      const int n = b0 + lane < p.a.B ? span_of(p, b0 + lane).qn : 0;
-      const int mine = (n + per_block - 1) / per_block;
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += x;
-      }
-      const unsigned here = __ballot_sync(0xffffffffu, want < upto);
-      if (here) {
-        const int who = __ffs(here) - 1;
-        b = b0 + who;
-        r0 = (want - __shfl_sync(0xffffffffu, upto - mine, who)) * per_block;
-        break;
-      }
-      want -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) {
-      work[0] = b;
-      work[1] = r0;
-    }
   }
   if (warp == 9) {
     tmem_alloc(&tmem_slot, 512);
@@ -250,60 +273,98 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int b = work[0], r0 = work[1];
-  const Span span = b < 0 ? Span{0, 0, 0, 0} : span_of(p, b);
+  pdl_wait();
 
-  // The keys that any of the block's rows sees, as tiles: the first tokens', then the window's.
-  const int off = span.kn - span.qn;            // position of row 0
-  const int r_end = min(span.qn, r0 + per_block);
-  const int p_lo = off + r0, p_hi = b < 0 ? -1 : off + r_end - 1;
-  const int first_any = (p.a.window && p_lo >= p.a.window) ? p_lo + 1 - p.a.window : 0;
-  const int first_hi = (p.a.window && p_hi >= p.a.window) ? p_hi + 1 - p.a.window : 0;
-  const int sink_tiles = (min(p.a.sinks, first_hi) + kTileN - 1) / kTileN;
-  const int win_tile = max(first_any / kTileN, sink_tiles);
-  const int tiles = p_hi < 0 ? 0 : sink_tiles + (p_hi + kTileN) / kTileN - win_tile;
-  auto key_of = [&](int i) { return (i < sink_tiles ? i : win_tile + (i - sink_tiles)) * kTileN; };
-  const int hk = h0 / (p.a.Hq / p.a.Hkv);
-  // Whether some row of tile x does not see some key of step i. There the weights of tile x go to the product in two
-  // parts, rounded and rest, because rows that see few keys have them in such steps; elsewhere the roundings of many
-  // keys even out. (Scales below zero, which nobody uses, take this way throughout.)
-  auto edge_of = [&](int x, int i) {
-    const int t0 = r0 + (p.pair ? 0 : x * kTileM), j0 = key_of(i), last = off + t0 + kTileM - 1;
-    const int first_last = (p.a.window && last >= p.a.window) ? last + 1 - p.a.window : 0;
-    return t0 + kTileM > r_end || j0 + kTileN - 1 > off + t0 || (j0 < first_last && j0 + kTileN > p.a.sinks) ||
-           p.a.scale < 0.f;
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPrefillWaitNs, &abort_flag, p.status, code)) != 0;
+  };
+  auto item_there = [&](int n) {
+    return wait(&w_full[n & 1], (n >> 1) & 1, DEV_TIMEOUT_FULL) && slots[n & 1][6] != 0;
+  };
+  auto item_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    // ---------------- loads ----------------
-    if (warp == 8 && lane == 0 && tiles > 0) {
-      mbar_arrive_expect_tx(&q_full, 2 * C::TILE);
-      for (int x = 0; x < 2; ++x)
-        for (int d = 0; d < C::HALVES; ++d)
-          tma_load_3d(smem + x * C::TILE + d * kTileM * 128, &qmap, d * 64, p.pair ? h0 + x : h0,
-                      span.q0 + r0 + (p.pair ? 0 : x * kTileM), &q_full);
-      int n = 0;
-      for (; n < 2 * tiles; ++n) {              // K of a step, V of a step, in turn
-        const int s = n % C::STAGES;
-        if (n >= C::STAGES && !mbar_wait(&kv_empty[s], (n / C::STAGES - 1) & 1, kPrefillWaitNs, &abort_flag, p.status,
-                                         DEV_TIMEOUT_EMPTY))
-          break;
-        mbar_arrive_expect_tx(&kv_full[s], C::TILE);
-        for (int d = 0; d < C::HALVES; ++d)
-          tma_load_3d(ring + s * C::TILE + d * kTileN * 128, n & 1 ? &vmap : &kmap, d * 64, hk, span.k0 + key_of(n / 2),
-                      &kv_full[s]);
+    // ---------------- items and loads ----------------
+    if (warp == 8) {
+      const int per_item = p.pair ? kTileM : 2 * kTileM;
+      const int head_items = p.pair ? p.a.Hq / 2 : p.a.Hq;
+      int kv = 0, qs = 0;                       // tiles of keys or values, and pairs of tiles of queries, loaded so far
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        // Items are numbered from the last rows of the last sequence on, so that long rows are begun first; the heads of
+        // the same rows are neighbours and share their keys in L2.
+        const unsigned idx = (unsigned)n * gridDim.x + blockIdx.x;      // at most a grid past the last
+        int want = (int)(idx / (unsigned)head_items), found = 0;
+        Span sp{0, 0, 0, 0};
+        for (int b0 = (p.a.B - 1) / 32 * 32; b0 >= 0 && !found; b0 -= 32) {
+          const int b = b0 + 31 - lane;         // lane 0 has the last sequence
+          const Span mine = b < p.a.B ? span_of(p, b) : Span{0, 0, 0, 0};
+          const int cnt = (mine.qn + per_item - 1) / per_item;
+          int upto = cnt;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+          }
+          const unsigned here = __ballot_sync(0xffffffffu, want < upto);
+          if (here) {
+            const int who = __ffs(here) - 1;
+            found = 1;
+            want = __shfl_sync(0xffffffffu, upto, who) - 1 - want;      // of the sequence's items, from its first on
+            sp.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
+            sp.qn = __shfl_sync(0xffffffffu, mine.qn, who);
+            sp.k0 = __shfl_sync(0xffffffffu, mine.k0, who);
+            sp.kn = __shfl_sync(0xffffffffu, mine.kn, who);
+          } else {
+            want -= __shfl_sync(0xffffffffu, upto, 31);
+          }
+        }
+        if (n >= 2 && !wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
+        const int slot[8] = {sp.q0, sp.qn, sp.k0, sp.kn, want * per_item, (int)(idx % (unsigned)head_items) * (p.pair ? 2 : 1), found, 0};
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 7; ++i) slots[n & 1][i] = slot[i];
+          mbar_arrive(&w_full[n & 1]);
+        }
+        if (!found) break;
+        const Item it(p, slot);
+        if (it.tiles == 0) continue;
+        if (qs > 0 && !wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full, 2 * C::TILE);
+          for (int x = 0; x < 2; ++x)
+            for (int d = 0; d < C::HALVES; ++d)
+              tma_load_3d(smem + x * C::TILE + d * kTileM * 128, &qmap, d * 64, p.pair ? it.h0 + x : it.h0,
+                          it.s.q0 + it.row_of(p, x), &q_full);
+        }
+        ++qs;
+        const int hk = it.h0 / (p.a.Hq / p.a.Hkv);
+        for (int i = 0; ok && i < 2 * it.tiles; ++i) {      // K of a step, V of a step, in turn
+          const int s = kv % C::STAGES;
+          if (kv >= C::STAGES && !(ok = wait(&kv_empty[s], (kv / C::STAGES - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&kv_full[s], C::TILE);
+            for (int d = 0; d < C::HALVES; ++d)
+              tma_load_3d(ring + s * C::TILE + d * kTileN * 128, i & 1 ? &vmap : &kmap, d * 64, hk,
+                          it.s.k0 + it.key_of(i / 2), &kv_full[s]);
+          }
+          ++kv;
+        }
       }
       if (abort_flag) {                         // copies in flight end before the block does
-        mbar_wait(&q_full, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
-        for (int j = max(0, n - C::STAGES); j < n; ++j)
+        if (qs) mbar_wait(&q_full, (qs - 1) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+        for (int j = max(0, kv - C::STAGES); j < kv; ++j)
           mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
       }
     }
     // ---------------- products ----------------
     // The whole warp goes along and one lane issues: addresses stay uniform, and so in uniform registers. (With one
-    // lane alone in the branch each product took 80 to 160 cycles to issue, of the 32 that it runs.)
-    if (warp == 9 && tiles > 0) {
+    // lane alone in the branch each product took 80 to 160 cycles to issue, of the 64 that it runs.)
+    if (warp == 9) {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const bool leader = elect_one();
       const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN);
@@ -311,7 +372,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);
       const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);
       const uint64_t vdesc = smem_desc(smem_u32(ring), kTileN * 128, 1024, 2);
-      auto qk = [&](int x, int s, bool release) {
+      auto qk = [&](int x, int s) {
         if (leader) {
           const uint64_t qx = qdesc + x * (C::TILE >> 4), kx = kdesc + s * (C::TILE >> 4);
 #pragma unroll
@@ -320,64 +381,80 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             mma_bf16(tm + x * (C::S1 - C::S0) + C::S0, qx + at, kx + at, idesc_qk, ks > 0);
           }
           tc_commit(&s_full[x]);
-          if (release) tc_commit(&kv_empty[s]);
         }
         __syncwarp();
       };
-      auto pv = [&](int x, int s, bool more, bool edge, bool release) {
+      // Half h of the keys of a step; its weights are there.
+      auto pv = [&](int x, int h, int s, bool more, bool split) {
         if (leader) {
           const uint32_t d = tm + x * (C::O1 - C::O0) + C::O0, a = tm + x * (C::S1 - C::S0) + C::S0;
           const uint64_t vx = vdesc + s * (C::TILE >> 4);
-          if (!edge) {
+          if (!split) {
 #pragma unroll
-            for (int ks = 0; ks < kTileN / 16; ++ks)
-              mma_bf16_ts(d, a + ks * 8, vx + ks * (2048 >> 4), idesc_pv, more || ks > 0);
+            for (int k4 = 0; k4 < kTileN / 32; ++k4) {
+              const int ks = h * kTileN / 32 + k4;
+              mma_bf16_ts(d, a + ks * 8, vx + ks * (2048 >> 4), idesc_pv, more || k4 > 0);
+            }
           } else {
             // of every 32 columns 16 hold the rounded weights of 32 keys, 16 the rests
 #pragma unroll
-            for (int ks = 0; ks < kTileN / 16; ++ks) {
-              mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8, vx + ks * (2048 >> 4), idesc_pv, more || ks > 0);
+            for (int k4 = 0; k4 < kTileN / 32; ++k4) {
+              const int ks = h * kTileN / 32 + k4;
+              mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8, vx + ks * (2048 >> 4), idesc_pv, more || k4 > 0);
               mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8 + 16, vx + ks * (2048 >> 4), idesc_pv, 1);
             }
           }
-          if (release) tc_commit(&kv_empty[s]);
-          tc_commit(&o_full[x]);
         }
         __syncwarp();
       };
-      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPrefillWaitNs, &abort_flag, p.status, code)) != 0;
+      auto release = [&](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
       };
+      int kv = 0, step = 0, qs = 0;             // tiles of keys or values, steps and pairs of query tiles so far
       auto have = [&](int n) { return wait(&kv_full[n % C::STAGES], (n / C::STAGES) & 1, DEV_TIMEOUT_FULL); };
-      bool ok = wait(&q_full, 0, DEV_TIMEOUT_FULL) && have(0);
-      if (ok) {
-        qk(0, 0, false);
-        qk(1, 0, true);
-      }
-      uint32_t cleaned = 0;                     // parity of v_clean's next phase, a bit a stage
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int vs = (2 * i + 1) % C::STAGES, ks = (2 * i + 2) % C::STAGES;
-        const bool edge[2] = {edge_of(0, i), edge_of(1, i)};
-        if (edge[0] || edge[1]) {
-          ok = wait(&v_clean[vs], (cleaned >> vs) & 1, DEV_TIMEOUT_FULL);
-          cleaned ^= 1u << vs;
-        } else {
-          ok = have(2 * i + 1);
-        }
+      bool ok = true;
+      for (int n = 0; ok && item_there(n); ++n) {
+        const Item it(p, slots[n & 1]);
+        item_done(n);
+        if (it.tiles == 0) continue;
+        ok = wait(&q_full, qs & 1, DEV_TIMEOUT_FULL) && have(kv);
+        if (!ok) break;
+        ++qs;
+        // S lies over the last item's weights: products are executed in the order of their issue
+        qk(0, kv % C::STAGES);
+        qk(1, kv % C::STAGES);
+        release(&kv_empty[kv % C::STAGES]);
+        if (it.tiles == 1) release(&q_empty);
+        const Edges e0 = it.edges(p, 0), e1 = it.edges(p, 1);
+        const bool split[2] = {it.split(p, 0), it.split(p, 1)};
+        for (int i = 0; ok && i < it.tiles; ++i, ++step) {
+          const int vs = (kv + 1) % C::STAGES, ks = (kv + 2) % C::STAGES;
+          const bool edge[2] = {e0.at(it.key_of(i)), e1.at(it.key_of(i))};
+          ok = wait(&v_clean[vs], ((kv + 1) / C::STAGES) & 1, DEV_TIMEOUT_FULL);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          ok = ok && wait(&p_full[x], i & 1, DEV_TIMEOUT_ACCUM);
-          if (!ok) break;
-          tc_fence_after();
-          pv(x, vs, i > 0, edge[x], x == 1 && i + 1 < tiles);
-          if (i + 1 < tiles) {
-            // S of the next step over P of this one: products are executed in the order of their issue
-            if (x == 0 && !(ok = have(2 * i + 2))) break;
-            qk(x, ks, x == 1);
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || !(ok = wait(&p_full[x][0], step & 1, DEV_TIMEOUT_ACCUM))) break;
+            tc_fence_after();
+            pv(x, 0, vs, i > 0, edge[x] && split[x]);
+            if (!(ok = wait(&p_full[x][1], step & 1, DEV_TIMEOUT_ACCUM))) break;
+            tc_fence_after();
+            pv(x, 1, vs, true, edge[x] && split[x]);
+            if (x == 1) release(&kv_empty[vs]);
+            release(&o_full[x]);
+            if (i + 1 < it.tiles) {
+              if (x == 0 && !(ok = have(kv + 2))) break;
+              qk(x, ks);
+            }
           }
+          if (i + 1 < it.tiles) {
+            release(&kv_empty[ks]);
+            if (i + 2 == it.tiles) release(&q_empty);
+          }
+          kv += 2;
         }
       }
-      if (!ok && leader) {
+      if (leader && abort_flag) {
         tc_commit(&drain);
         mbar_wait(&drain, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
       }
@@ -387,199 +464,226 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     // step, they are set to zero, and the rows that do see them are listed to be computed again.
     if (warp >= 10) {
       const int tid = threadIdx.x - 320;
-      for (int i = 0; i < tiles; ++i) {
-        if (!edge_of(0, i) && !edge_of(1, i)) continue;
-        const int n = 2 * i + 1, st = n % C::STAGES;
-        if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[st], (n / C::STAGES) & 1, kPrefillWaitNs, &abort_flag, p.status,
-                                               DEV_TIMEOUT_FULL)))
-          break;
-        uint4* v = reinterpret_cast<uint4*>(ring + st * C::TILE);
-        bool wrote = false;
+      int kv = 0;
+      bool ok = true;
+      for (int n = 0; ok && item_there(n); ++n) {
+        const Item it(p, slots[n & 1]);
+        if (tid == 0) bad_count[n & 1] = 0;     // the last item but one, whose list this was, is done
+        named_bar_sync(2, 64);
+        const Edges e0 = it.edges(p, 0), e1 = it.edges(p, 1);
+        for (int i = 0; i < it.tiles; ++i, kv += 2) {
+          // every step's values pass here, edge or not: a barrier's parity tells its next phase from the last one only
+          // to a waiter that has seen them all
+          const int j0 = it.key_of(i), st = (kv + 1) % C::STAGES;
+          if (!(ok = wait(&kv_full[st], ((kv + 1) / C::STAGES) & 1, DEV_TIMEOUT_FULL))) break;
+          if (!e0.at(j0) && !e1.at(j0)) {
+            mbar_arrive(&v_clean[st]);
+            continue;
+          }
+          uint4* v = reinterpret_cast<uint4*>(ring + st * C::TILE);
+          bool wrote = false;
 #pragma unroll 4
-        for (int e = tid; e < C::TILE / 16; e += 64) {
-          const uint4 a = v[e];
-          // an exponent field of all ones carries into the bit above it when its lowest bit is added
-          const uint32_t any = (((a.x & 0x7F807F80u) + 0x00800080u) | ((a.y & 0x7F807F80u) + 0x00800080u) |
-                                ((a.z & 0x7F807F80u) + 0x00800080u) | ((a.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
-          if (any) {
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-            uint32_t z[4];
+          for (int e = tid; e < C::TILE / 16; e += 64) {
+            const uint4 a = v[e];
+            // an exponent field of all ones carries into the bit above it when its lowest bit is added
+            const uint32_t any = (((a.x & 0x7F807F80u) + 0x00800080u) | ((a.y & 0x7F807F80u) + 0x00800080u) |
+                                  ((a.z & 0x7F807F80u) + 0x00800080u) | ((a.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+            // 8 neighbouring lanes hold one key's 64 values: one of them lists it
+            const unsigned hits = __ballot_sync(0xffffffffu, any != 0);
+            if (any) {
+              const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+              uint32_t z[4];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const uint32_t hit = ((w[f] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              z[f] = w[f] & ~((hit >> 15) * 0xFFFFu);
+              for (int f = 0; f < 4; ++f) {
+                const uint32_t hit = ((w[f] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                z[f] = w[f] & ~((hit >> 15) * 0xFFFFu);
+              }
+              v[e] = make_uint4(z[0], z[1], z[2], z[3]);
+              wrote = true;
+              if (__ffs(hits & (0xFFu << (tid & 24))) - 1 == (tid & 31)) {
+                const int at = atomicAdd(&bad_count[n & 1], 1);
+                if (at < kBadKeys) bad_keys[n & 1][at] = j0 + e / 8 % kTileN;
+              }
             }
-            v[e] = make_uint4(z[0], z[1], z[2], z[3]);
-            wrote = true;
           }
-          // 8 neighbouring lanes hold one key's 64 values: one of them lists it
-          const unsigned hits = __ballot_sync(0xffffffffu, any != 0) & (0xFFu << (tid & 24));
-          if (any && __ffs(hits) - 1 == (tid & 31)) {
-            const int at = atomicAdd(&bad_count, 1);
-            if (at < kBadKeys) bad_keys[at] = key_of(i) + e / 8 % kTileN;
-          }
+          if (wrote) fence_async_smem();
+          mbar_arrive(&v_clean[st]);
         }
-        if (wrote) fence_async_smem();
-        mbar_arrive(&v_clean[st]);
+        item_done(n);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax ----------------
     const int x = warp / 4, tid = threadIdx.x % 128;
-    const int h = p.pair ? h0 + x : h0;
-    const int row = r0 + (p.pair ? 0 : x * kTileM) + tid;                      // of the sequence
-    const bool live = row < r_end;
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t ts = tmem + (x ? C::S1 : C::S0) + lanes, to = tmem + (x ? C::O1 : C::O0) + lanes;
-    const int pos = live ? off + row : -1;
-    const int first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
     // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
     const uint32_t turn = p.a.scale < 0.f ? 0x80000000u : 0u;
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
     const uint64_t c2 = pack2(c, c);
-    float m = -INFINITY;                        // the maximum that the weights so far refer to
-    uint64_t l2 = pack2(0.f, 0.f);
+    int step = 0;                               // steps so far
     bool ok = true;
-    for (int i = 0; ok && i < tiles; ++i) {
-      ok = mbar_wait(&s_full[x], i & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const int j0 = key_of(i);
-      float mx = -INFINITY;
-      // The maximum that the weights refer to moves only when one has outgrown it; then what has been summed is rescaled.
-      auto move_base = [&]() {
-        const float mn = fmaxf(m, mx);
-        if (!__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) return true;      // (-inf) - (-inf): no
-        if (i > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], (i - 1) & 1, kPrefillWaitNs, &abort_flag, p.status,
-                                                 DEV_TIMEOUT_ACCUM)))
-            return false;
-          tc_fence_after();
-          const float f = m == -INFINITY ? 0.f : ex2f((m - mn) * c);
-          l2 = mul2(l2, pack2(f, f));
+    for (int n = 0; ok && item_there(n); ++n) {
+      int tiles, sink_tiles, win_shift, pos, first;
+      bool split;
+      Edges edges;
+      {
+        const Item it(p, slots[n & 1]);
+        const int row = it.row_of(p, x) + tid;  // of the sequence
+        pos = row < it.r_end ? it.off + row : -1;
+        first = Item::first_of(p, pos);
+        split = it.split(p, x);
+        edges = it.edges(p, x);
+        tiles = it.tiles, sink_tiles = it.sink_tiles, win_shift = it.win_shift;
+      }
+      float m = -INFINITY;                      // the maximum that the weights so far refer to
+      uint64_t l2 = pack2(0.f, 0.f);
+      for (int i = 0; i < tiles; ++i, ++step) {
+        if (!(ok = wait(&s_full[x], step & 1, DEV_TIMEOUT_ACCUM))) break;
+        tc_fence_after();
+        const int j0 = (i < sink_tiles ? i : i + win_shift) * kTileN;
+        float mx = -INFINITY;
+        // The maximum that the weights refer to moves only when one has outgrown it; then what has been summed is
+        // rescaled.
+        auto move_base = [&]() {
+          const float mn = fmaxf(m, mx);
+          if (!__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) return true;    // (-inf) - (-inf): no
+          if (i > 0) {
+            if (!wait(&o_full[x], (step - 1) & 1, DEV_TIMEOUT_ACCUM)) return false;
+            tc_fence_after();
+            const float f = m == -INFINITY ? 0.f : ex2f((m - mn) * c);
+            l2 = mul2(l2, pack2(f, f));
 #pragma unroll 1
-          for (int e = 0; e < D; e += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + e, o, 0);
-            tmem_ld_wait();
-            reg_fence32(o, 0);
+            for (int e = 0; e < D; e += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + e, o);
+              tmem_ld_wait();
+              reg_fence16(o);
 #pragma unroll
-            for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
-            tmem_st32(to + e, o, 0);
+              for (int d = 0; d < 16; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+              tmem_st16(to + e, o);
+            }
           }
-        }
-        m = mn;
-        return true;
-      };
-      uint64_t la = pack2(0.f, 0.f), lb = la, b2 = la;
-      auto weights = [&](const uint32_t* s, float (&w)[4]) {
-        unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, b2), w[0], w[1]);
-        unpack2(fma2(pack2(__uint_as_float(s[2]), __uint_as_float(s[3])), c2, b2), w[2], w[3]);
+          m = mn;
+          return true;
+        };
+        uint64_t la = pack2(0.f, 0.f), lb = la, b2 = la;
+        auto weights = [&](const uint32_t* s, float (&w)[4]) {
+          unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, b2), w[0], w[1]);
+          unpack2(fma2(pack2(__uint_as_float(s[2]), __uint_as_float(s[3])), c2, b2), w[2], w[3]);
 #pragma unroll
-        for (int f = 0; f < 4; ++f) w[f] = ex2f(w[f]);
-        la = add2(la, pack2(w[0], w[1]));
-        lb = add2(lb, pack2(w[2], w[3]));
-      };
-      if (!edge_of(x, i)) {
+          for (int f = 0; f < 4; ++f) w[f] = ex2f(w[f]);
+          la = add2(la, pack2(w[0], w[1]));
+          lb = add2(lb, pack2(w[2], w[3]));
+        };
+        // the weights of half h are in Tensor Memory
+        auto hand_over = [&](int h) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[x][h]);
+        };
+        const bool edge = edges.at(j0);
         uint32_t s[128];
 #pragma unroll
         for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
+        if (edge) {
+          const int hi = min(pos - j0, 127), lo = max(first - j0, 0), low = min(p.a.sinks - j0, hi + 1);
+          auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
+#pragma unroll
+          for (int e = 0; e < 128; e += 32) {
+            // bit d: the row sees key e + d, that is lo <= e + d <= hi or e + d < low
+            const uint32_t see = (below(hi + 1 - e) & ~below(lo - e)) | below(low - e);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) s[e + d] = (see >> d) & 1u ? s[e + d] ^ turn : 0xff800000u;
+          }
+        }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; e += 4)
+        for (int e = 0; e < 128; e += 8)
 #pragma unroll
-          for (int f = 0; f < 4; ++f) m4[f] = fmaxf(m4[f], __uint_as_float(s[e + f]));
-        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int f = 0; f < 4; ++f)
+            m4[f] = max3(m4[f], __uint_as_float(s[e + 2 * f]), __uint_as_float(s[e + 2 * f + 1]));
+        mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
         if (!(ok = move_base())) break;
         const float base = m == -INFINITY ? 0.f : -m * c;
         b2 = pack2(base, base);
+        if (!edge || !split) {
 #pragma unroll
-        for (int e = 0; e < 128; e += 4) {
-          float w[4];
-          weights(s + e, w);
-          s[e / 2] = bf16x2(w[0], w[1]);        // s[e / 2] has been read
-          s[e / 2 + 1] = bf16x2(w[2], w[3]);
-        }
-        tmem_st32(ts, s, 0);
-        tmem_st32(ts + 32, s, 32);
-      } else {
-        // Twice over the scores, 32 at a time, in little code: these steps are few.
-        const int hi = min(pos - j0, 127), lo = max(first - j0, 0), low = min(p.a.sinks - j0, hi + 1);
-        auto load = [&](int e, uint32_t (&s)[32]) {
-          tmem_ld32(ts + e, s, 0);
-          // bit d: the row sees key e + d, that is lo <= e + d <= hi or e + d < low
-          auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
-          const uint32_t see = (below(hi + 1 - e) & ~below(lo - e)) | below(low - e);
-          tmem_ld_wait();
-          reg_fence32(s, 0);
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int d = 0; d < 32; ++d) s[d] = (see >> d) & 1u ? s[d] ^ turn : 0xff800000u;
-        };
-#pragma unroll 1
-        for (int e = 0; e < 128; e += 32) {
-          uint32_t s[32];
-          load(e, s);
-#pragma unroll
-          for (int d = 0; d < 32; ++d) mx = fmaxf(mx, __uint_as_float(s[d]));
-        }
-        if (!(ok = move_base())) break;
-        const float base = m == -INFINITY ? 0.f : -m * c;
-        b2 = pack2(base, base);
-#pragma unroll 1
-        for (int e = 0; e < 128; e += 32) {
-          uint32_t s[32];
-          load(e, s);
-          uint32_t rest[16];
-#pragma unroll
-          for (int d = 0; d < 16; d += 2) {
-            float w[4];
-            weights(s + 2 * d, w);
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              s[d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
-              rest[d + f] = bf16x2(w[2 * f] - bf16_lo(s[d + f]), w[2 * f + 1] - bf16_hi(s[d + f]));
+            for (int e = 64 * h; e < 64 * h + 64; e += 4) {
+              float w[4];
+              weights(s + e, w);
+              s[e / 2] = bf16x2(w[0], w[1]);    // s[e / 2] has been read
+              s[e / 2 + 1] = bf16x2(w[2], w[3]);
             }
+            tmem_st32(ts + 32 * h, s, 32 * h);
+            hand_over(h);
           }
+        } else {
 #pragma unroll
-          for (int d = 0; d < 16; ++d) s[16 + d] = rest[d];
-          tmem_st32(ts + e, s, 0);
+          for (int e = 0; e < 128; e += 32) {
+            uint32_t rest[16];
+#pragma unroll
+            for (int d = 0; d < 16; d += 2) {
+              float w[4];
+              weights(s + e + 2 * d, w);
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                s[e + d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
+                rest[d + f] = bf16x2(w[2 * f] - bf16_lo(s[e + d + f]), w[2 * f + 1] - bf16_hi(s[e + d + f]));
+              }
+            }
+#pragma unroll
+            for (int d = 0; d < 16; ++d) s[e + 16 + d] = rest[d];
+            tmem_st32(ts + e, s, e);
+            if (e & 32) hand_over(e / 64);
+          }
         }
+        l2 = add2(l2, add2(la, lb));
       }
-      l2 = add2(l2, add2(la, lb));
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_full[x]);
-    }
-    if (ok && tiles > 0) {
-      ok = mbar_wait(&o_full[x], (tiles - 1) & 1, kPrefillWaitNs, &abort_flag, p.status, DEV_TIMEOUT_ACCUM);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok && b >= 0) {
+      if (ok && tiles > 0) {
+        ok = wait(&o_full[x], (step - 1) & 1, DEV_TIMEOUT_ACCUM);
+        tc_fence_after();
+      }
+      if (!ok) break;
+
+      // what the end of an item needs is worked out here, not kept in registers over the steps
+      int ln = lane;
+      asm volatile("" : "+r"(ln));
+      const Item it(p, slots[n & 1]);
+      const int h = p.pair ? it.h0 + x : it.h0, row = it.row_of(p, x) + warp % 4 * 32 + ln;
+      const bool live = row < it.r_end;
       float la, lb;
       unpack2(l2, la, lb);
       const float l = la + lb, inv = 1.f / l;
-      // every value that is not finite was listed before the last product that met it
-      const int listed = *reinterpret_cast<volatile int*>(&bad_count);
-      bool fine = listed <= kBadKeys;
-      const Visible see(pos, p.a.window, p.a.sinks);
-      for (int i = 0; i < min(listed, kBadKeys); ++i) fine = fine && !see.sees(bad_keys[i]);
-      uint16_t* out = p.out + ((long long)(span.q0 + row) * p.a.Hq + h) * D;
+      bool fine = true;
+      if (it.tiles > 0) {
+        // every value that is not finite was listed before the last product that met it
+        const int listed = *reinterpret_cast<volatile int*>(&bad_count[n & 1]);
+        fine = listed <= kBadKeys;
+        const Visible see(live ? it.off + row : -1, p.a.window, p.a.sinks);
+        for (int i = 0; i < min(listed, kBadKeys); ++i) fine = fine && !see.sees(bad_keys[n & 1][i]);
+      }
+      // Through shared memory, so that a warp writes 128-byte pieces of rows: 64 columns of its 32 rows at a time, in
+      // chunks of 16 bytes whose order is turned by the row.
+      uint4* mine = reinterpret_cast<uint4*>(staging + warp * 4096);
+      const unsigned rows_live = __ballot_sync(0xffffffffu, live);
+      uint16_t* out = p.out + ((long long)(it.s.q0 + row - ln) * p.a.Hq + h) * D;
 #pragma unroll 1
-      for (int e = 0; e < D; e += 32) {
-        uint32_t o[32];
-        if (tiles > 0) {
-          tmem_ld32(to + e, o, 0);
-          tmem_ld_wait();
-          reg_fence32(o, 0);
-        }
+      for (int half = 0; half < D / 64; ++half) {
+        uint32_t o[64];
+        tmem_ld32(to + half * 64, o, 0);        // without keys: whatever is there, and not used
+        tmem_ld32(to + half * 64 + 32, o, 32);
+        tmem_ld_wait();
+        reg_fence32(o, 0);
+        reg_fence32(o, 32);
 #pragma unroll
-        for (int d = 0; d < 32; d += 8) {
+        for (int d = 0; d < 64; d += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
@@ -588,11 +692,20 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             fine = fine && isfinite(u) && isfinite(v);
             w[f] = bf16x2(u, v);
           }
-          if (live) *reinterpret_cast<uint4*>(out + e + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          mine[ln * 8 + ((d / 8) ^ (ln & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = e * 4 + ln / 8, ch = ln % 8;
+          if ((rows_live >> r) & 1u)
+            *reinterpret_cast<uint4*>(out + (long long)r * p.a.Hq * D + half * 64 + ch * 8) = mine[r * 8 + (ch ^ (r & 7))];
+        }
+        __syncwarp();
       }
       for (unsigned again = __ballot_sync(0xffffffffu, live && !fine); again; again &= again - 1)
-        redo_row<D>(p, span, row - lane + __ffs(again) - 1, h);
+        redo_row<D>(p, it.s, row - ln + __ffs(again) - 1, h);
+      item_done(n);
     }
   }
   __syncwarp();
@@ -626,9 +739,9 @@ static int launch_prefill(const PrefillArgs& p, cudaStream_t st) {
   auto kern = prefill_attention_kernel<D>;
   if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), PrefillCfg<D>::SMEM))) return rc;
   const int per_block = p.pair ? kTileM : 2 * kTileM;
-  const long long blocks = ((long long)p.Tq / per_block + p.a.B) * (p.pair ? p.a.Hq / 2 : p.a.Hq);
-  if (blocks >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  return launch_pdl(kern, dim3((unsigned)blocks), dim3(PrefillCfg<D>::THREADS), PrefillCfg<D>::SMEM, st, qm, km, vm, p);
+  const long long items = ((long long)p.Tq / per_block + p.a.B) * (p.pair ? p.a.Hq / 2 : p.a.Hq);     // at most
+  if (items >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return launch_pdl(kern, dim3((unsigned)std::min(items, (long long)num_sms())), dim3(PrefillCfg<D>::THREADS), PrefillCfg<D>::SMEM, st, qm, km, vm, p);
 }
 
 }  // namespace moe

@@ -132,6 +132,33 @@ def test_a_value_that_is_not_finite_reaches_its_column_alone():
     assert np.isposinf(got[10:, :, 7]).all() and np.isfinite(got[:10]).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 64, 8), (128, 32, 4), (128, 33, 11)])
+def test_more_work_than_the_gpu_has_room_for(D, Hq, Hkv):
+    """Several times as many blocks of rows as multiprocessors, with values that are not finite here and there: sampled
+    rows against the oracle, and call after call the same bits."""
+    lens = [1500, 3, 2300, 700, 1]
+    p = Prompts(lens, Hq, Hkv, D, seed=11)
+    bad = {2: 1000, 0: 1490}                       # sequence: a key whose value is not finite
+    begin = np.concatenate([[0], np.cumsum(lens)])
+    for b, j in bad.items():
+        p.v[int(begin[b]) + j, :, 3] = float("nan")
+    for window, sinks in ((0, 0), (300, 5)):
+        first = p.run(window, sinks)
+        p.B.attention_status()
+        for _ in range(5):
+            assert torch.equal(p.run(window, sinks).view(torch.int16), first.view(torch.int16))
+        q, k, v, got = _np(p.q), _np(p.k), _np(p.v), _np(first)
+        for b, n in enumerate(lens):
+            rows = slice(int(begin[b]), int(begin[b]) + n)
+            for r in sorted({0, n // 3, n // 2, n - 1, min(n - 1, 1001), min(n - 1, 1489)}):
+                with np.errstate(all="ignore"):
+                    want, mag = A.attend_heads(q[rows][r:r + 1], k[rows], v[rows], r, D ** -0.5, window, sinks)
+                mine = got[rows][r:r + 1]
+                cols = [d for d in range(D) if d != 3]
+                assert np.all(np.abs(mine - want)[..., cols] <= A.attention_tolerance(want, mag)[..., cols])
+                assert np.array_equal(np.isnan(mine[..., 3]), np.isnan(want[..., 3]))
+
+
 def test_other_outputs_streams_and_graphs():
     p = Prompts([129, 300], 4, 2, 128, seed=9)
     want = p.run(64, 4)
