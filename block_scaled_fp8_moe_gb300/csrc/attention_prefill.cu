@@ -165,7 +165,8 @@ struct PrefillCfg {
   static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;
 };
 
-// One row's attention straight from its definition, by a warp: for rows that see a key or value that is not finite.
+// One row's attention straight from its definition, by a warp: for rows that see a value that is not finite in a step
+// where others do not.
 template <int D>
 __device__ __noinline__ void redo_row(const PrefillArgs& p, const Span& s, int row, int h) {
   constexpr int N = D / 32;
@@ -296,8 +297,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       bool ok = true;
       for (int n = 0; ok; ++n) {
         // Items are numbered from the last rows of the last sequence on, so that long rows are begun first; the heads of
-        // the same rows are neighbours and share their keys in L2.
-        const unsigned idx = (unsigned)n * gridDim.x + blockIdx.x;      // at most a grid past the last
+        // the same rows are neighbours and share their keys in L2. Every other round is dealt out backwards: who had the
+        // longest item of one round has the shortest of the next.
+        const unsigned idx = (unsigned)n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         int want = (int)(idx / (unsigned)head_items), found = 0;
         Span sp{0, 0, 0, 0};
         for (int b0 = (p.a.B - 1) / 32 * 32; b0 >= 0 && !found; b0 -= 32) {
@@ -330,7 +332,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           for (int i = 0; i < 7; ++i) slots[n & 1][i] = slot[i];
           mbar_arrive(&w_full[n & 1]);
         }
-        if (!found) break;
+        if (!found) break;                      // the later rounds have none either
         const Item it(p, slot);
         if (it.tiles == 0) continue;
         if (qs > 0 && !wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
@@ -591,14 +593,24 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
 #pragma unroll
         for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
         if (edge) {
-          const int hi = min(pos - j0, 127), lo = max(first - j0, 0), low = min(p.a.sinks - j0, hi + 1);
-          auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
+          // the row sees key j0 + e when e <= hi and (e >= lo or e < low); mostly only one of the three matters
+          const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
+          if (turn) {
 #pragma unroll
-          for (int e = 0; e < 128; e += 32) {
-            // bit d: the row sees key e + d, that is lo <= e + d <= hi or e + d < low
-            const uint32_t see = (below(hi + 1 - e) & ~below(lo - e)) | below(low - e);
+            for (int e = 0; e < 128; ++e) s[e] ^= turn;
+          }
+          if (__any_sync(0xffffffffu, hi < kTileN - 1)) {
 #pragma unroll
-            for (int d = 0; d < 32; ++d) s[e + d] = (see >> d) & 1u ? s[e + d] ^ turn : 0xff800000u;
+            for (int e = 0; e < 128; ++e) s[e] = e <= hi ? s[e] : 0xff800000u;
+          }
+          if (__any_sync(0xffffffffu, lo > 0)) {
+            if (low <= 0) {
+#pragma unroll
+              for (int e = 0; e < 128; ++e) s[e] = e >= lo ? s[e] : 0xff800000u;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 128; ++e) s[e] = e >= lo || e < low ? s[e] : 0xff800000u;
+            }
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -660,14 +672,17 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       const bool live = row < it.r_end;
       float la, lb;
       unpack2(l2, la, lb);
-      const float l = la + lb, inv = 1.f / l;
-      bool fine = true;
+      const float l = la + lb;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // Rows that see a listed key are computed again. (Every value that is not finite was listed before the last product
+      // that met it. A score that is NaN makes the sum NaN, and with it the row: that is its result.)
+      bool again = false;
       if (it.tiles > 0) {
-        // every value that is not finite was listed before the last product that met it
         const int listed = *reinterpret_cast<volatile int*>(&bad_count[n & 1]);
-        fine = listed <= kBadKeys;
+        again = listed > kBadKeys;
         const Visible see(live ? it.off + row : -1, p.a.window, p.a.sinks);
-        for (int i = 0; i < min(listed, kBadKeys); ++i) fine = fine && !see.sees(bad_keys[n & 1][i]);
+        for (int i = 0; i < min(listed, kBadKeys); ++i) again = again || see.sees(bad_keys[n & 1][i]);
+        again = again && live && l == l;
       }
       // Through shared memory, so that a warp writes 128-byte pieces of rows: 64 columns of its 32 rows at a time, in
       // chunks of 16 bytes whose order is turned by the row.
@@ -682,14 +697,18 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         tmem_ld_wait();
         reg_fence32(o, 0);
         reg_fence32(o, 32);
+        const uint64_t inv2 = pack2(inv, inv);
+        if (it.tiles == 0) {
+#pragma unroll
+          for (int d = 0; d < 64; ++d) o[d] = 0;
+        }
 #pragma unroll
         for (int d = 0; d < 64; d += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const float u = l == 0.f ? 0.f : __uint_as_float(o[d + 2 * f]) * inv;
-            const float v = l == 0.f ? 0.f : __uint_as_float(o[d + 2 * f + 1]) * inv;
-            fine = fine && isfinite(u) && isfinite(v);
+            float u, v;
+            unpack2(mul2(pack2(__uint_as_float(o[d + 2 * f]), __uint_as_float(o[d + 2 * f + 1])), inv2), u, v);
             w[f] = bf16x2(u, v);
           }
           mine[ln * 8 + ((d / 8) ^ (ln & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -703,8 +722,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         }
         __syncwarp();
       }
-      for (unsigned again = __ballot_sync(0xffffffffu, live && !fine); again; again &= again - 1)
-        redo_row<D>(p, it.s, row - ln + __ffs(again) - 1, h);
+      for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
+        redo_row<D>(p, it.s, row - ln + __ffs(rows) - 1, h);
       item_done(n);
     }
   }
