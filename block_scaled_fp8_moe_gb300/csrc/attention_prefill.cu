@@ -24,6 +24,7 @@ constexpr int kTileM = 128;             // query rows of a tile
 constexpr int kTileN = 128;             // keys of a step
 constexpr uint64_t kPrefillWaitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kShort = 32;              // keys of a step that has few first tokens alone
 constexpr int kFewKeys = 512;           // rows that see fewer keep their weights in two parts
 constexpr int kBadKeys = 64;            // keys with values that are not finite that a block lists
 
@@ -95,7 +96,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[N], int 
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : MOE_R8(r, i), MOE_R8(r, i + 8), MOE_R8(r, i + 16), MOE_R8(r, i + 24) : "r"(taddr) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+template <int N>
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[N]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
       ::MOE_RI8(r, 0), MOE_RI8(r, 8), "r"(taddr) : "memory");
@@ -141,6 +143,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// a b + c of two bf16 each.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
@@ -200,6 +209,7 @@ struct Item {
   Span s;
   int r0, h0;                           // first row (of the sequence), first head
   int off, r_end, sink_tiles, win_shift, tiles;
+  bool short_sinks;                     // step 0 has the first tokens alone, and no more than 32
   __device__ __forceinline__ Item(const PrefillArgs& p, const int (&slot)[8])
       : s{slot[0], slot[1], slot[2], slot[3]}, r0(slot[4]), h0(slot[5]) {
     off = s.kn - s.qn;                  // position of row 0
@@ -209,6 +219,7 @@ struct Item {
     sink_tiles = (min(p.a.sinks, first_hi) + kTileN - 1) / kTileN;
     const int win_tile = max(first_of(p, off + r0) / kTileN, sink_tiles);
     win_shift = win_tile - sink_tiles;
+    short_sinks = sink_tiles == 1 && p.a.sinks <= kShort && first_of(p, off + r0) >= kTileN;
     tiles = p_hi < 0 ? 0 : (p_hi + kTileN) / kTileN - win_shift;
   }
   static __device__ __forceinline__ int first_of(const PrefillArgs& p, int pos) {
@@ -369,25 +380,25 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     if (warp == 9) {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const bool leader = elect_one();
-      const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN);
+      const uint32_t idesc_qk = idesc_bf16_f32(kTileM, kTileN), idesc_short = idesc_bf16_f32(kTileM, kShort);
       const uint32_t idesc_pv = idesc_bf16_f32(kTileM, D) | (1u << 16);      // V: its D values contiguous, keys apart
       const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);
       const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);
       const uint64_t vdesc = smem_desc(smem_u32(ring), kTileN * 128, 1024, 2);
-      auto qk = [&](int x, int s) {
+      auto qk = [&](int x, int s, bool brief) {
         if (leader) {
           const uint64_t qx = qdesc + x * (C::TILE >> 4), kx = kdesc + s * (C::TILE >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const int at = ((ks / 4) * kTileN * 128 + (ks % 4) * 32) >> 4;
-            mma_bf16(tm + x * (C::S1 - C::S0) + C::S0, qx + at, kx + at, idesc_qk, ks > 0);
+            mma_bf16(tm + x * (C::S1 - C::S0) + C::S0, qx + at, kx + at, brief ? idesc_short : idesc_qk, ks > 0);
           }
           tc_commit(&s_full[x]);
         }
         __syncwarp();
       };
       // Half h of the keys of a step; its weights are there.
-      auto pv = [&](int x, int h, int s, bool more, bool split) {
+      auto pv = [&](int x, int h, int s, bool more, bool split, bool brief) {
         if (leader) {
           const uint32_t d = tm + x * (C::O1 - C::O0) + C::O0, a = tm + x * (C::S1 - C::S0) + C::S0;
           const uint64_t vx = vdesc + s * (C::TILE >> 4);
@@ -395,6 +406,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
 #pragma unroll
             for (int k4 = 0; k4 < kTileN / 32; ++k4) {
               const int ks = h * kTileN / 32 + k4;
+              if (brief && ks >= kShort / 16) break;
               mma_bf16_ts(d, a + ks * 8, vx + ks * (2048 >> 4), idesc_pv, more || k4 > 0);
             }
           } else {
@@ -402,6 +414,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
 #pragma unroll
             for (int k4 = 0; k4 < kTileN / 32; ++k4) {
               const int ks = h * kTileN / 32 + k4;
+              if (brief && ks >= kShort / 16) break;
               mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8, vx + ks * (2048 >> 4), idesc_pv, more || k4 > 0);
               mma_bf16_ts(d, a + ks / 2 * 32 + ks % 2 * 8 + 16, vx + ks * (2048 >> 4), idesc_pv, 1);
             }
@@ -424,29 +437,30 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         if (!ok) break;
         ++qs;
         // S lies over the last item's weights: products are executed in the order of their issue
-        qk(0, kv % C::STAGES);
-        qk(1, kv % C::STAGES);
+        qk(0, kv % C::STAGES, it.short_sinks);
+        qk(1, kv % C::STAGES, it.short_sinks);
         release(&kv_empty[kv % C::STAGES]);
         if (it.tiles == 1) release(&q_empty);
         const Edges e0 = it.edges(p, 0), e1 = it.edges(p, 1);
         const bool split[2] = {it.split(p, 0), it.split(p, 1)};
         for (int i = 0; ok && i < it.tiles; ++i, ++step) {
           const int vs = (kv + 1) % C::STAGES, ks = (kv + 2) % C::STAGES;
+          const bool brief = it.short_sinks && i == 0;
           const bool edge[2] = {e0.at(it.key_of(i)), e1.at(it.key_of(i))};
           ok = wait(&v_clean[vs], ((kv + 1) / C::STAGES) & 1, DEV_TIMEOUT_FULL);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || !(ok = wait(&p_full[x][0], step & 1, DEV_TIMEOUT_ACCUM))) break;
             tc_fence_after();
-            pv(x, 0, vs, i > 0, edge[x] && split[x]);
+            pv(x, 0, vs, i > 0, edge[x] && split[x], brief);
             if (!(ok = wait(&p_full[x][1], step & 1, DEV_TIMEOUT_ACCUM))) break;
             tc_fence_after();
-            pv(x, 1, vs, true, edge[x] && split[x]);
+            if (!brief) pv(x, 1, vs, true, edge[x] && split[x], false);
             if (x == 1) release(&kv_empty[vs]);
             release(&o_full[x]);
             if (i + 1 < it.tiles) {
               if (x == 0 && !(ok = have(kv + 2))) break;
-              qk(x, ks);
+              qk(x, ks, false);
             }
           }
           if (i + 1 < it.tiles) {
@@ -483,8 +497,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             continue;
           }
           uint4* v = reinterpret_cast<uint4*>(ring + st * C::TILE);
+          // zero times a value that is not finite is NaN, and stays in the sum
+          uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 8
+          for (int e = tid; e < C::TILE / 16; e += 64) {
+            const uint4 a = v[e];
+            sum[0] = fma_bf16x2(a.x, 0, sum[0]);
+            sum[1] = fma_bf16x2(a.y, 0, sum[1]);
+            sum[2] = fma_bf16x2(a.z, 0, sum[2]);
+            sum[3] = fma_bf16x2(a.w, 0, sum[3]);
+          }
+          if (!__any_sync(0xffffffffu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)) {
+            mbar_arrive(&v_clean[st]);
+            continue;
+          }
           bool wrote = false;
-#pragma unroll 4
+#pragma unroll 1
           for (int e = tid; e < C::TILE / 16; e += 64) {
             const uint4 a = v[e];
             // an exponent field of all ones carries into the bit above it when its lowest bit is added
@@ -593,7 +621,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
 #pragma unroll
         for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
         if (edge) {
-          // the row sees key j0 + e when e <= hi and (e >= lo or e < low); mostly only one of the three matters
+          // The row sees key j0 + e when e <= hi and (e >= lo or e < low); mostly only one of the three matters. (Scores
+          // that a short step has not computed are hidden with the rest behind the first tokens.)
           const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
           if (turn) {
 #pragma unroll
@@ -689,36 +718,43 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       uint4* mine = reinterpret_cast<uint4*>(staging + warp * 4096);
       const unsigned rows_live = __ballot_sync(0xffffffffu, live);
       uint16_t* out = p.out + ((long long)(it.s.q0 + row - ln) * p.a.Hq + h) * D;
-#pragma unroll 1
-      for (int half = 0; half < D / 64; ++half) {
-        uint32_t o[64];
-        tmem_ld32(to + half * 64, o, 0);        // without keys: whatever is there, and not used
-        tmem_ld32(to + half * 64 + 32, o, 32);
-        tmem_ld_wait();
-        reg_fence32(o, 0);
-        reg_fence32(o, 32);
-        const uint64_t inv2 = pack2(inv, inv);
-        if (it.tiles == 0) {
+      uint32_t o[D];
 #pragma unroll
-          for (int d = 0; d < 64; ++d) o[d] = 0;
-        }
+      for (int e = 0; e < D; e += 32) tmem_ld32(to + e, o, e);        // without keys: whatever is there, and not used
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < D; e += 32) reg_fence32(o, e);
+      if (it.tiles == 0) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] = 0;
+      }
+      const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
 #pragma unroll
         for (int d = 0; d < 64; d += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
+            const int e = half * 64 + d + 2 * f;
             float u, v;
-            unpack2(mul2(pack2(__uint_as_float(o[d + 2 * f]), __uint_as_float(o[d + 2 * f + 1])), inv2), u, v);
+            unpack2(mul2(pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), inv2), u, v);
             w[f] = bf16x2(u, v);
           }
           mine[ln * 8 + ((d / 8) ^ (ln & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
+        uint4 t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = e * 4 + ln / 8, ch = ln % 8;
+          t[e] = mine[r * 8 + (ch ^ (r & 7))];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int r = e * 4 + ln / 8, ch = ln % 8;
           if ((rows_live >> r) & 1u)
-            *reinterpret_cast<uint4*>(out + (long long)r * p.a.Hq * D + half * 64 + ch * 8) = mine[r * 8 + (ch ^ (r & 7))];
+            *reinterpret_cast<uint4*>(out + (long long)r * p.a.Hq * D + half * 64 + ch * 8) = t[e];
         }
         __syncwarp();
       }
