@@ -6,7 +6,9 @@ is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -434,9 +436,15 @@ MOE_KV_BF16 = 0
 MOE_KV_MXFP8 = 1
 
 
+# These calls run once or more per layer and step, where the host's time counts as much as the kernel's: addresses
+# go to ctypes as plain integers, and descriptors and sizes are kept by their values.
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
     """The address of a contiguous tensor of this type on device `dev`."""
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -447,7 +455,7 @@ def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
 
 def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[int, int]:
     """The address and the row stride of bf16 rows [rows, heads, D] (rows may lie apart)."""
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
@@ -468,42 +476,56 @@ def _current(t: torch.Tensor, name: str) -> int:
     return dev
 
 
-def _new(shape_, dtype, like: torch.Tensor, stream):
-    """An output, allocated on the stream that will write it."""
-    if stream is None:
-        return torch.empty(shape_, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape_, dtype=dtype, device=like.device)
+_as_is = contextlib.nullcontext()
 
 
-_scratch: dict[tuple[int, int], torch.Tensor] = {}
+def _allocating(stream):
+    """Where outputs are allocated: on the stream that will write them."""
+    return _as_is if stream is None else torch.cuda.stream(stream)
+
+
+def _sized(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> int:
+    if t.numel() != numel:
+        raise ValueError(f"{name} needs {numel} elements, has {t.numel()}")
+    return _on(t, name, dtype, dev)
+
+
+_scratch: dict[tuple[int, int], tuple[torch.Tensor, int, int]] = {}
 _outgrown: list[torch.Tensor] = []      # kept: a captured CUDA graph may still write to them
 
 
-def _workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
-    """This stream's workspace of the attention and cache calls, grown as needed (at least twofold); its status word
-    starts at zero."""
-    s = torch.cuda.current_stream() if stream is None else stream
-    key = (like.get_device(), s.cuda_stream)
-    ws = _scratch.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(s):
-            old, ws = ws, torch.empty(max(nbytes, 4096, 2 * ws.numel() if ws is not None else 0), dtype=torch.uint8,
-                                      device=like.device)
-            ws[:256].zero_() if old is None else ws[:256].copy_(old[:256])
-        if old is not None:
-            _outgrown.append(old)
-        _scratch[key] = ws
-    return ws
+def _workspace(nbytes: int, like: torch.Tensor, stream, dev: int, raw: int) -> tuple[int, int]:
+    """Address and size of this stream's workspace of the attention and cache calls, grown as needed (at least
+    twofold); its status word starts at zero."""
+    have = _scratch.get((dev, raw))
+    if have is None or have[2] < nbytes:
+        size = max(nbytes, 4096, 0 if have is None else 2 * have[2])
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+            ws[:256].zero_() if have is None else ws[:256].copy_(have[0][:256])
+        if have is not None:
+            _outgrown.append(have[0])
+        have = _scratch[dev, raw] = (ws, ws.data_ptr(), size)
+    return have[1], have[2]
 
 
 def attention_status(device=None, stream=None) -> None:
     """Synchronises `stream` and raises what the attention and cache calls without a workspace of their own found
     invalid on the device there (a page, slot or length out of range), then clears it."""
     s = torch.cuda.current_stream(device) if stream is None else stream
-    ws = _scratch.get((s.device_index, s.cuda_stream))
-    if ws is not None:
-        moe_check_device_status(ws, s)
+    have = _scratch.get((s.device_index, s.cuda_stream))
+    if have is not None:
+        moe_check_device_status(have[0], s)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention(B: int, Hq: int, Hkv: int, D: int, window: int, sinks: int, scale: float | None):
+    return ctypes.byref(MoeAttention(B, Hq, Hkv, D, window, sinks, D ** -0.5 if scale is None else scale))
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_bytes(a, rows: int, max_len: int) -> int:
+    return int(lib.moe_paged_attention_workspace_bytes(a, rows, max_len))
 
 
 def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=None, y=None, q=None, s=None,
@@ -513,30 +535,46 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
     Returns (y, sum, q, s): bf16(y), bf16(h), u8 codes and u8 scales [..., cols / 32]. sum_out and y may be x or residual
     themselves. With quant=False, q and s are None."""
     dev = _current(x, "x")
-    cols = x.shape[-1]
+    bf16, u8 = torch.bfloat16, torch.uint8
+    shape_ = x.shape
+    cols = shape_[-1]
     n = x.numel()
     rows = n // cols if cols else 0
-    px, pw = _on(x, "x", torch.bfloat16, dev), _on(weight, "weight", torch.bfloat16, dev)
+    px, pw = _on(x, "x", bf16, dev), _on(weight, "weight", bf16, dev)
     if weight.numel() != cols:
         raise ValueError(f"weight needs {cols} elements, has {weight.numel()}")
     pr = None
     if residual is not None:
-        pr = _on(residual, "residual", torch.bfloat16, dev)
+        pr = _on(residual, "residual", bf16, dev)
         if residual.numel() != n:
             raise ValueError(f"residual needs {n} elements, has {residual.numel()}")
-    sum_out = _new(x.shape, torch.bfloat16, x, stream) if sum_out is None else sum_out
-    y = _new(x.shape, torch.bfloat16, x, stream) if y is None else y
-    if quant:
-        q = _new(x.shape, torch.uint8, x, stream) if q is None else q
-        s = _new((*x.shape[:-1], cols // 32), torch.uint8, x, stream) if s is None else s
-    for t, need, name in ((sum_out, n, "sum_out"), (y, n, "y"), (q, n, "q"),
-                          (s, rows * (cols // 32), "s")):
-        if t is not None and t.numel() != need:
-            raise ValueError(f"{name} needs {need} elements, has {t.numel()}")
-    _check(lib.moe_add_rmsnorm_mxfp8(
-        rows, cols, px, pr, pw, eps, _on(sum_out, "sum_out", torch.bfloat16, dev), _on(y, "y", torch.bfloat16, dev),
-        None if q is None else _on(q, "q", torch.uint8, dev), None if s is None else _on(s, "s", torch.uint8, dev),
-        _stream(stream)), "moe_add_rmsnorm_mxfp8")
+
+    with _allocating(stream):
+        if sum_out is None:
+            sum_out = torch.empty_like(x)
+            psum = sum_out.data_ptr()
+        else:
+            psum = _sized(sum_out, "sum_out", bf16, n, dev)
+        if y is None:
+            y = torch.empty_like(x)
+            py = y.data_ptr()
+        else:
+            py = _sized(y, "y", bf16, n, dev)
+        pq = ps = None
+        if quant:
+            if q is None:
+                q = torch.empty_like(x, dtype=u8)
+                pq = q.data_ptr()
+            else:
+                pq = _sized(q, "q", u8, n, dev)
+            if s is None:
+                s = torch.empty(shape_[:-1] + (cols // 32,), dtype=u8, device=x.device)
+                ps = s.data_ptr()
+            else:
+                ps = _sized(s, "s", u8, rows * (cols // 32), dev)
+    rc = lib.moe_add_rmsnorm_mxfp8(rows, cols, px, pr, pw, eps, psum, py, pq, ps, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_add_rmsnorm_mxfp8")
     return y, sum_out, q, s
 
 
@@ -560,6 +598,7 @@ class KvCache:
         self.k, self.v, self.k_s, self.v_s = k, v, k_s, v_s
         self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
         self.desc = MoeKvCache(pages, page_size, Hkv, D, MOE_KV_MXFP8 if mx else MOE_KV_BF16, *ptrs)
+        self.ref = ctypes.byref(self.desc)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, Hkv: int, D: int, mxfp8: bool = False, device="cuda"):
@@ -580,14 +619,15 @@ def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"k and v need {T} rows, have {k.shape[0]} and {v.shape[0]}")
     ps = _on(slots, "slots", torch.int32, dev)
-    ws = _workspace(256, k, stream) if ws is None else ws
-    _check(lib.moe_kv_append(ctypes.byref(cache.desc), T, pk, sk, pv, sv, ps, _on(ws, "ws", torch.uint8, dev),
-                             ws.numel(), _stream(stream)), "moe_kv_append")
+    raw = _raw_stream(stream, dev)
+    pws, nws = _workspace(256, k, stream, dev, raw) if ws is None else (_on(ws, "ws", torch.uint8, dev), ws.numel())
+    rc = lib.moe_kv_append(cache.ref, T, pk, sk, pv, sv, ps, pws, nws, raw)
+    if rc:
+        _check(rc, "moe_kv_append")
 
 
 def moe_paged_attention_workspace_bytes(B: int, rows: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
-    a = MoeAttention(B, Hq, Hkv, D, 0, 0, 1.0)
-    return int(lib.moe_paged_attention_workspace_bytes(ctypes.byref(a), rows, max_len))
+    return _paged_bytes(_attention(B, Hq, Hkv, D, 0, 0, 1.0), rows, max_len)
 
 
 def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, scale: float | None = None,
@@ -596,6 +636,7 @@ def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, 
     [B, width], seq_lens i32 [B] (the new rows counted), max_len >= every seq_len. Returns bf16 [B, rows, Hq, D]."""
     dev = _current(q, "q")
     B, rows, Hq, D = q.shape
+    width = block_table.shape[-1]
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError(f"block_table must be [{B}, width] and seq_lens [{B}]")
     if q.is_contiguous():
@@ -606,18 +647,21 @@ def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, 
         pq, sq = _rows_on(q[:, 0] if rows == 1 else q[0], "q", Hq, D, dev)
         if rows > 1 and B > 1:
             sq = q.stride(1)
-    a = MoeAttention(B, Hq, cache.Hkv, D, window, sinks, D ** -0.5 if scale is None else scale)
+    a = _attention(B, Hq, cache.Hkv, D, window, sinks, scale)
     if out is None:
-        out = _new((B, rows, Hq, D), torch.bfloat16, q, stream)
-    elif out.numel() != q.numel():
-        raise ValueError(f"out needs {q.numel()} elements, has {out.numel()}")
+        with _allocating(stream):
+            out = torch.empty((B, rows, Hq, D), dtype=torch.bfloat16, device=q.device)
+    pout = _sized(out, "out", torch.bfloat16, q.numel(), dev)
+    raw = _raw_stream(stream, dev)
     if ws is None:
-        ws = _workspace(lib.moe_paged_attention_workspace_bytes(ctypes.byref(a), rows, max_len), q, stream)
-    _check(lib.moe_paged_attention(
-        ctypes.byref(a), ctypes.byref(cache.desc), rows, max_len, pq, sq,
-        _on(block_table, "block_table", torch.int32, dev), block_table.shape[1],
-        _on(seq_lens, "seq_lens", torch.int32, dev), _on(out, "out", torch.bfloat16, dev),
-        _on(ws, "ws", torch.uint8, dev), ws.numel(), _stream(stream)), "moe_paged_attention")
+        pws, nws = _workspace(_paged_bytes(a, rows, max_len), q, stream, dev, raw)
+    else:
+        pws, nws = _on(ws, "ws", torch.uint8, dev), ws.numel()
+    rc = lib.moe_paged_attention(a, cache.ref, rows, max_len, pq, sq, _on(block_table, "block_table", torch.int32, dev),
+                                 width, _on(seq_lens, "seq_lens", torch.int32, dev),
+                                 pout, pws, nws, raw)
+    if rc:
+        _check(rc, "moe_paged_attention")
     return out
 
 
@@ -640,15 +684,17 @@ def moe_prefill_attention(q, k, v, cu_q, cu_k=None, scale: float | None = None, 
     if cu_k is None and Tq != Tk:
         raise ValueError("without cu_k, k and v need as many rows as q")
     if out is None:
-        out = _new((Tq, Hq, D), torch.bfloat16, q, stream)
-    elif out.numel() != q.numel():
-        raise ValueError(f"out needs {q.numel()} elements, has {out.numel()}")
-    a = MoeAttention(B, Hq, Hkv, D, window, sinks, D ** -0.5 if scale is None else scale)
-    ws = _workspace(256, q, stream) if ws is None else ws
-    _check(lib.moe_prefill_attention(
-        ctypes.byref(a), Tq, Tk, pq, sq, pk, sk, pv, sv, _on(cu_q, "cu_q", torch.int32, dev),
-        None if cu_k is None else _on(cu_k, "cu_k", torch.int32, dev), _on(out, "out", torch.bfloat16, dev),
-        _on(ws, "ws", torch.uint8, dev), ws.numel(), _stream(stream)), "moe_prefill_attention")
+        with _allocating(stream):
+            out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+    pout = _sized(out, "out", torch.bfloat16, q.numel(), dev)
+    raw = _raw_stream(stream, dev)
+    pws, nws = _workspace(256, q, stream, dev, raw) if ws is None else (_on(ws, "ws", torch.uint8, dev), ws.numel())
+    rc = lib.moe_prefill_attention(
+        _attention(B, Hq, Hkv, D, window, sinks, scale), Tq, Tk, pq, sq, pk, sk, pv, sv,
+        _on(cu_q, "cu_q", torch.int32, dev), None if cu_k is None else _on(cu_k, "cu_k", torch.int32, dev),
+        pout, pws, nws, raw)
+    if rc:
+        _check(rc, "moe_prefill_attention")
     return out
 
 
