@@ -11,7 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["quant.cu", "route.cu", "router_screen.cu", "gemm.cu", "gemm2sm.cu", "gemm_ws.cu", "api.cu", "peak.cu",
-           "norm.cu", "kv_append.cu", "attention_paged.cu", "attention_prefill.cu"]
+           "norm.cu", "kv_append.cu", "attention_paged.cu", "attention_paged_tc.cu",
+           "attention_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fvisibility=hidden"]

@@ -42,10 +42,14 @@ struct Visible {
     first = (window && p >= window) ? p + 1 - window : 0;
     low = min(sinks, first);
   }
-  __device__ __forceinline__ int count() const { return end <= 0 ? 0 : low + end - first; }
-  __device__ __forceinline__ int key(int i) const { return i < low ? i : first + (i - low); }
   __device__ __forceinline__ bool sees(int j) const { return j < end && (j >= first || j < low); }
 };
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -86,17 +90,21 @@ struct LaneRow {
   }
 };
 
-// One row's attention by one warp, its lanes spread over D, every `step`-th visible key from `i0` on.
-// `load(j, k, v)` fetches a key's and its value's parts and returns whether the key is there. m, l, o
-// hold the running maximum of the scores (times log2 e), the sum and the weighted values (of the lane).
+// One row's attention by one warp straight from the definition, its lanes spread over D, over the visible keys from j0 to
+// j1. `load(j, k, v)` fetches a key's and its value's parts and returns whether the key is there. m, l, o hold the running
+// maximum of the scores (times log2 e), the sum and the weighted values (of the lane).
 template <int D, class Load>
-__device__ __forceinline__ void attend_row(const LaneRow<D>& q, const Visible& see, int i0, int step, float scale_log2,
-                                           float& m, float& l, float (&o)[D / 32], const Load& load) {
+__device__ __forceinline__ void attend_keys(const LaneRow<D>& q, const Visible& see, int j0, int j1, float scale_log2,
+                                            float& m, float& l, float (&o)[D / 32], const Load& load) {
   constexpr int N = D / 32;
-  const int n = see.count();
-  for (int i = i0; i < n; i += step) {
+  j1 = min(j1, see.end);
+  for (int j = j0; j < j1; ++j) {
+    if (!see.sees(j)) {
+      if (j < see.first) j = min(see.first, j1) - 1;
+      continue;
+    }
     LaneRow<D> k, v;
-    if (!load(see.key(i), k, v)) continue;
+    if (!load(j, k, v)) continue;
     float s = 0.f;
 #pragma unroll
     for (int d = 0; d < N; ++d) s = fmaf(q.f[d], k.f[d], s);

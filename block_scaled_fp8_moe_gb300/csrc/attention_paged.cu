@@ -3,78 +3,25 @@
 //
 // Bound: HBM. Every visible key and value is read once for all rows and all heads of a group; per key and kv head that
 // is 4 D bytes (bf16) or 2.06 D (MXFP8) against 4 D R flops, R = rows * Hq / Hkv: far above what CUDA cores do at full
-// bandwidth (R = 8 would need 54 of their ~75 TFLOP/s), so both products run on the tensor cores, as m16n8k16 with the
-// rows as M. (A tcgen05 product has at least 64 rows; most of them would be padding here.)
+// bandwidth (R = 8 would need 54 of their ~75 TFLOP/s), so both products run on the tensor cores. This file's kernel takes
+// up to 16 rows, as m16n8k16 with the rows as M (a tcgen05 product has at least 64); more rows go to
+// attention_paged_tc.cu. Pieces of both are joined here.
 //
 // A block takes one piece of one (sequence, kv head): a producer warp streams pages by TMA through a ring of 64-token
-// stages, WM x WT warps consume it, WM along the rows (16 each), WT along the tokens. Every warp keeps its own running
-// maximum, sum and output, so that nothing but the ring's barriers is shared until the end.
+// stages, four warps consume it, 16 tokens of a stage each. Every warp keeps its own running maximum, sum and output, so
+// that nothing but the ring's barriers is shared until the end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
+#include "attention_paged.cuh"
 #include "common.cuh"
-#include "gemm.cuh"
 #include "ptx.cuh"
 
 namespace moe {
 
 constexpr int kTileTok = 64;          // tokens of a stage
-constexpr int kBlockRows = 64;        // rows (row, head of the group) a block takes at most
-constexpr int kPieceTiles = 8;        // a piece has at least this many tiles (512 tokens) ...
-constexpr int kMaxPieces = 64;        // ... and a sequence at most this many pieces
-constexpr uint64_t kPagedWaitNs = 1000000000ull;
-
-struct PagedArgs {
-  moe_attention a;
-  int pages, page_size, page_log2;
-  const uint8_t* k_s;
-  const uint8_t* v_s;
-  int rows, max_len, table_width;
-  int mblocks, max_pieces;
-  const uint16_t* q;
-  long long q_stride;
-  const int32_t* table;
-  const int32_t* lens;
-  uint16_t* out;
-  uint32_t* status;
-  float* part_o;    // [B, Hkv, max_pieces, R, D]: sums of weighted values
-  float* part_ml;   // [B, Hkv, max_pieces, R, 2]: running maximum (times log2 e) and sum
-};
-
-// What the rows [r_lo, r_hi] of a sequence see, as tiles of 64 tokens, and its pieces. The pieces follow from the
-// sequence's own length alone: a row's result is the same in every batch.
-struct Pieces {
-  int pmin, pmax;        // positions of the first and the last row
-  int first_any, first_all;
-  int sink_tiles, win_tile, tiles;
-  int per, count;
-  __device__ __forceinline__ Pieces(int len, int rows, int r_lo, int r_hi, int window, int sinks) {
-    pmin = len - rows + r_lo;
-    pmax = len == 0 ? -1 : len - rows + r_hi;
-    first_any = (window && pmin >= window) ? pmin + 1 - window : 0;
-    first_all = (window && pmax >= window) ? pmax + 1 - window : 0;
-    sink_tiles = (min(sinks, first_all) + kTileTok - 1) / kTileTok;
-    win_tile = max(first_any / kTileTok, sink_tiles);
-    tiles = pmax < 0 ? 0 : sink_tiles + (pmax + kTileTok) / kTileTok - win_tile;
-    per = max(kPieceTiles, (tiles + kMaxPieces - 1) / kMaxPieces);
-    count = max(1, (tiles + per - 1) / per);
-  }
-  __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : win_tile + (i - sink_tiles); }
-};
-
-__device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool report) {
-  const int len = p.lens[b];
-  if (len >= 0 && len <= p.max_len) return len;
-  if (report) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-  return 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
+constexpr int kFewRows = 16;          // rows that this kernel takes
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -91,31 +38,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// Two E4M3 codes as bf16 with their values times 2^-120: sign, exponent and fraction in bf16's places (subnormal codes
-// become subnormals). `sel` takes [code of the high half, sign of the low one's (replicated), the low one's, any].
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return (uint32_t)((int32_t)r >> 4) & 0x87F087F0u;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// A scale byte's factor for e4m3_pair's values, 2^(120 + byte - 127), as bf16 bits: bytes up to 134 fit. What lies
-// above (values past 57,344) takes a second factor; byte 255 is NaN.
-constexpr uint32_t kScaleFits = 134;
-__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return (min(byte, kScaleFits) + 120u) << 7; }
-__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
-  return byte == 255u ? 0x7FC0u : byte > kScaleFits ? (byte - kScaleFits + 127u) << 7 : 0x3F80u;
-}
-
-template <int D_, bool MX_, int WM_, int WT_>
+template <int D_, bool MX_>
 struct PagedCfg {
-  static constexpr int D = D_, WM = WM_, WT = WT_;
+  static constexpr int D = D_;
   static constexpr bool MX = MX_;
-  static constexpr int WARPS = WM * WT, ST = kTileTok / WT;
+  static constexpr int WARPS = 4, ST = kTileTok / WARPS;           // tokens of a stage that a warp takes
   static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
   static constexpr int ROWB = MX ? D : 128;                        // bytes of a row in a column block
   static constexpr int KV = kTileTok * D * (MX ? 1 : 2);           // bytes of a stage's keys, or values
@@ -161,16 +88,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   const int piece = (int)(u % p.max_pieces);
   u /= p.max_pieces;
   const int hk = (int)(u % p.a.Hkv);
-  u /= p.a.Hkv;
-  const int mb = (int)(u % p.mblocks);
-  const long long b = u / p.mblocks;
+  const long long b = u / p.a.Hkv;
   const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
 
   pdl_trigger();
   pdl_wait();
   const int len = checked_len(p, b, threadIdx.x == 0);
-  const int rho_end = min(R, (mb + 1) * kBlockRows);
-  const Pieces pc(len, p.rows, mb * kBlockRows / G, (rho_end - 1) / G, p.a.window, p.a.sinks);
+  const Pieces pc(p, len, 0);
   if (piece >= pc.count) return;
   const int i0 = piece * pc.per, i1 = min(pc.tiles, i0 + pc.per);
 
@@ -244,13 +168,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   }
 
   // ---------------- consumers ----------------
-  const int wm = warp % C::WM, wt = warp / C::WM;
-  const int g = lane >> 2, c = lane & 3;
+    const int g = lane >> 2, c = lane & 3;
   int pos[2], first[2];
   uint32_t qf[D / 16][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int rho = mb * kBlockRows + wm * 16 + g + 8 * h;
+    const int rho = g + 8 * h;
     const bool live = rho < R;
     const int r = rho / G;
     pos[h] = live ? len - p.rows + r : -1;
@@ -273,7 +196,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   for (int i = i0; i < i1; ++i) {
     const int n = i - i0, s = n % C::STAGES;
     if (!mbar_wait(&full[s], (n / C::STAGES) & 1, kPagedWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL)) break;
-    const int loc0 = wt * ST, tok0 = pc.tile(i) * kTileTok + loc0;
+    const int loc0 = warp * ST, tok0 = pc.tile(i) * kTileTok + loc0;
     const uint8_t* st = smem + s * C::STAGE;
     const uint32_t kb = smem_u32(st), vb = kb + C::KV;
     const uint32_t mask = page_mask[s];
@@ -489,7 +412,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   float* jml = jo + C::WARPS * 16 * C::PITCH;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int row = (wt * C::WM + wm) * 16 + g + 8 * h;
+    const int row = warp * 16 + g + 8 * h;
     if (c == 0) jml[2 * row] = m[h], jml[2 * row + 1] = l[h];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -499,17 +422,17 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   }
   named_bar_sync(1, C::WARPS * 32);
   if (abort_flag) return;
-  for (int x = threadIdx.x; x < C::WM * 16 * (D / 4); x += C::WARPS * 32) {
-    const int row = x / (D / 4), d = x % (D / 4) * 4, rho = mb * kBlockRows + row;
+  for (int x = threadIdx.x; x < kFewRows * (D / 4); x += C::WARPS * 32) {
+    const int rho = x / (D / 4), d = x % (D / 4) * 4;
     if (rho >= R) break;
     float top = -INFINITY, tl = 0.f;
     float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < C::WT; ++w) top = fmaxf(top, jml[2 * (w * C::WM * 16 + row)]);
+    for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, jml[2 * (w * 16 + rho)]);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int w = 0; w < C::WT; ++w) {
-      const int rr = w * C::WM * 16 + row;
+    for (int w = 0; w < C::WARPS; ++w) {
+      const int rr = w * 16 + rho;
       const float f = ex2(jml[2 * rr] - base);
       const float4 v = *reinterpret_cast<const float4*>(jo + rr * C::PITCH + d);
       tl += f * jml[2 * rr + 1];
@@ -543,9 +466,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs p) {
   if (x >= (long long)p.a.B * p.a.Hkv * R) return;
   const int rho = (int)(x % R), hk = (int)(x / R % p.a.Hkv);
   const long long b = x / R / p.a.Hkv;
-  const int mb = rho / kBlockRows;
-  const Pieces pc(checked_len(p, b, false), p.rows, mb * kBlockRows / G, (min(R, (mb + 1) * kBlockRows) - 1) / G,
-                  p.a.window, p.a.sinks);
+  const Pieces pc(p, checked_len(p, b, false), rho / p.block_rows);
   if (pc.count == 1) return;
   const long long at = (b * p.a.Hkv + hk) * p.max_pieces * R + rho;
   static_assert(kMaxPieces == 64, "two pieces a lane");
@@ -586,14 +507,26 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs p) {
   for (int i = 0; i < N / 2; ++i) out[i] = tl == 0.f ? 0u : bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
 }
 
+// Blocks of up to 16 rows take steps of 64 tokens, more rows steps of 128.
+static int tile_of(const moe_attention* a, int rows) {
+  return rows * (a->Hq / a->Hkv) <= kFewRows ? kTileTok : 2 * kTileTok;
+}
+
 // The most pieces a sequence of up to max_len tokens can have.
 static int max_pieces_of(const moe_attention* a, int rows, int max_len) {
-  long long tiles = ((long long)max_len + kTileTok - 1) / kTileTok;
+  const int tile = tile_of(a, rows);
+  long long tiles = ((long long)max_len + tile - 1) / tile;
   if (a->window) {
-    const long long sinks = ((long long)a->sinks + kTileTok - 1) / kTileTok;
-    tiles = std::min(tiles, sinks + ((long long)a->window + rows) / kTileTok + 2);
+    const long long sinks = ((long long)a->sinks + tile - 1) / tile;
+    tiles = std::min(tiles, sinks + ((long long)a->window + rows) / tile + 2);
   }
-  return (int)std::max(1ll, std::min((long long)kMaxPieces, (tiles + kPieceTiles - 1) / kPieceTiles));
+  // a shorter sequence can have more, where a piece's steps change
+  long long most = 1;
+  for (long long t : {tiles, std::min(tiles, 63ll), std::min(tiles, tile == kTileTok ? 512ll : 256ll)}) {
+    const int per = piece_steps(tile, (int)t);
+    most = std::max(most, (t + per - 1) / per);
+  }
+  return (int)most;
 }
 
 static size_t part_rows(const moe_attention* a, int rows, int max_len) {
@@ -601,42 +534,30 @@ static size_t part_rows(const moe_attention* a, int rows, int max_len) {
   return pieces == 1 ? 0 : (size_t)a->B * a->Hq * rows * pieces;
 }
 
-static int page_map(CUtensorMap* m, void* base, const moe_kv_cache* c) {
-  EncodeTiledFn enc = get_encode();
-  if (!enc) return MOE_ERR_CUDA;
-  const bool mx = c->format == MOE_KV_MXFP8;
-  const cuuint64_t dims[2] = {(cuuint64_t)c->D, (cuuint64_t)c->pages * c->Hkv * c->page_size};
-  const cuuint64_t stride[1] = {(cuuint64_t)c->D * (mx ? 1 : 2)};
-  const cuuint32_t box[2] = {(cuuint32_t)(mx ? c->D : 64), (cuuint32_t)std::min(c->page_size, kTileTok)};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, stride,
-                         box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         mx && c->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
-}
-
-template <class C>
-static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+template <int D, bool MX>
+static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  using C = PagedCfg<D, MX>;
   CUtensorMap km, vm;
-  int rc = page_map(&km, cache->k, cache);
-  if (rc || (rc = page_map(&vm, cache->v, cache))) return rc;
+  const int box = std::min(cache->page_size, kTileTok);
+  const CUtensorMapSwizzle swizzle = C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  int rc = page_map(&km, cache->k, cache, box, swizzle);
+  if (rc || (rc = page_map(&vm, cache->v, cache, box, swizzle))) return rc;
   auto kern = paged_attention_kernel<C>;
   if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM))) return rc;
-  const long long grid = (long long)p.a.B * p.mblocks * p.a.Hkv * p.max_pieces;
-  rc = launch_pdl(kern, dim3((unsigned)grid), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
-  if (rc || p.max_pieces == 1) return rc;
-  const long long out_rows = (long long)p.a.B * p.a.Hq * p.rows;
-  return launch_pdl(paged_join_kernel<C::D>, dim3((unsigned)((out_rows + 3) / 4)), dim3(128), 0, st, p);
+  const long long grid = (long long)p.a.B * p.a.Hkv * p.max_pieces;
+  return launch_pdl(kern, dim3((unsigned)grid), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
 }
 
-template <int D, bool MX>
-static int launch_rows(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  // warps along the rows as far as there are rows, the others along the tokens
-  const int r = std::min(kBlockRows, p.rows * (p.a.Hq / p.a.Hkv));
-  if (r <= 16) return launch_paged<PagedCfg<D, MX, 1, 4>>(p, cache, st);
-  if (r <= 32) return launch_paged<PagedCfg<D, MX, 2, 2>>(p, cache, st);
-  return launch_paged<PagedCfg<D, MX, 4, 1>>(p, cache, st);
+static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  const bool mx = cache->format == MOE_KV_MXFP8, d64 = p.a.D == 64;
+  int rc;
+  if (p.tile != kTileTok) rc = launch_paged_tc(p, cache, st);
+  else if (d64) rc = mx ? launch_few<64, true>(p, cache, st) : launch_few<64, false>(p, cache, st);
+  else rc = mx ? launch_few<128, true>(p, cache, st) : launch_few<128, false>(p, cache, st);
+  if (rc || p.max_pieces == 1) return rc;
+  const long long out_rows = (long long)p.a.B * p.a.Hq * p.rows;
+  return launch_pdl(d64 ? paged_join_kernel<64> : paged_join_kernel<128>, dim3((unsigned)((out_rows + 3) / 4)), dim3(128),
+                    0, st, p);
 }
 
 }  // namespace moe
@@ -669,12 +590,16 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.pages = cache->pages;
   p.page_size = cache->page_size;
   while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
+  p.k = static_cast<const uint8_t*>(cache->k);
+  p.v = static_cast<const uint8_t*>(cache->v);
   p.k_s = cache->k_s;
   p.v_s = cache->v_s;
   p.rows = rows;
   p.max_len = max_len;
   p.table_width = table_width;
-  p.mblocks = ceil_div(rows * (a->Hq / a->Hkv), kBlockRows);
+  p.tile = tile_of(a, rows);
+  p.block_rows = p.tile == kTileTok ? kFewRows : 128;
+  p.mblocks = ceil_div(rows * (a->Hq / a->Hkv), p.block_rows);
   p.max_pieces = max_pieces_of(a, rows, max_len);
   if ((int64_t)a->B * p.mblocks * a->Hkv * p.max_pieces >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
   p.q = q;
@@ -686,8 +611,5 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   const size_t n = part_rows(a, rows, max_len);
   p.part_o = ws_ptr<float>(ws, 256);
   p.part_ml = ws_ptr<float>(ws, 256 + align_up(n * a->D * 4, 256));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool mx = cache->format == MOE_KV_MXFP8;
-  if (a->D == 64) return mx ? launch_rows<64, true>(p, cache, st) : launch_rows<64, false>(p, cache, st);
-  return mx ? launch_rows<128, true>(p, cache, st) : launch_rows<128, false>(p, cache, st);
+  return launch_paged(p, cache, static_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,110 @@
+// What the two kernels of the paged attention share: their arguments, a sequence's pieces, and MXFP8 in bf16.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attention.cuh"
+#include "gemm.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kMaxPieces = 64;
+constexpr uint64_t kPagedWaitNs = 1000000000ull;
+
+struct PagedArgs {
+  moe_attention a;
+  int pages, page_size, page_log2;
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* k_s;
+  const uint8_t* v_s;
+  int rows, max_len, table_width;
+  int tile, block_rows;      // tokens of a step; rows (row, head of the group) of a block
+  int mblocks, max_pieces;
+  const uint16_t* q;
+  long long q_stride;
+  const int32_t* table;
+  const int32_t* lens;
+  uint16_t* out;
+  uint32_t* status;
+  float* part_o;    // [B, Hkv, max_pieces, R, D]: sums of weighted values
+  float* part_ml;   // [B, Hkv, max_pieces, R, 2]: running maximum (times log2 e) and sum
+};
+
+// Steps of a piece. Steps of 64 tokens (few rows, several small blocks a multiprocessor): at least 8 of them, and at most
+// 64 pieces. Steps of 128 (one block a multiprocessor): at least 4, 8 from 8192 tokens on, and at most 32 pieces; shorter
+// pieces cost more in partial results than they gain in balance.
+__host__ __device__ inline int piece_steps(int tile, int tiles) {
+  if (tile == 64) return tiles > 8 * 64 ? (tiles + 63) / 64 : 8;
+  return tiles < 64 ? 4 : tiles > 8 * 32 ? (tiles + 31) / 32 : 8;
+}
+
+// What the rows of block mb of a sequence see, as steps, and its pieces. The pieces follow from the sequence's own length
+// alone: a row's result is the same in every batch.
+struct Pieces {
+  int pmin, pmax;        // positions of the first and the last row
+  int first_any, first_all;
+  int sink_tiles, win_tile, tiles;
+  int per, count;
+  __device__ __forceinline__ Pieces(const PagedArgs& p, int len, int mb) {
+    const int G = p.a.Hq / p.a.Hkv, r_hi = (min(p.rows * G, (mb + 1) * p.block_rows) - 1) / G;
+    pmin = len - p.rows + mb * p.block_rows / G;
+    pmax = len == 0 ? -1 : len - p.rows + r_hi;
+    first_any = (p.a.window && pmin >= p.a.window) ? pmin + 1 - p.a.window : 0;
+    first_all = (p.a.window && pmax >= p.a.window) ? pmax + 1 - p.a.window : 0;
+    sink_tiles = (min(p.a.sinks, first_all) + p.tile - 1) / p.tile;
+    win_tile = max(first_any / p.tile, sink_tiles);
+    tiles = pmax < 0 ? 0 : sink_tiles + (pmax + p.tile) / p.tile - win_tile;
+    per = piece_steps(p.tile, tiles);
+    count = max(1, (tiles + per - 1) / per);
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : win_tile + (i - sink_tiles); }
+};
+
+__device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool report) {
+  const int len = p.lens[b];
+  if (len >= 0 && len <= p.max_len) return len;
+  if (report) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+  return 0;
+}
+
+// Two E4M3 codes as bf16 with their values times 2^-120: sign, exponent and fraction in bf16's places (subnormal codes
+// become subnormals). `sel` takes [code of the high half, sign of the low one's (replicated), the low one's, any].
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return (uint32_t)((int32_t)r >> 4) & 0x87F087F0u;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A scale byte's factor for e4m3_pair's values, 2^(120 + byte - 127), as bf16 bits: bytes up to 134 fit. What lies
+// above (values past 57,344) takes a second factor; byte 255 is NaN.
+constexpr uint32_t kScaleFits = 134;
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return (min(byte, kScaleFits) + 120u) << 7; }
+__device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
+  return byte == 255u ? 0x7FC0u : byte > kScaleFits ? (byte - kScaleFits + 127u) << 7 : 0x3F80u;
+}
+
+// Tensor map of the cache's rows [pages * Hkv * page_size, D], loaded `rows` at a time.
+inline int page_map(CUtensorMap* m, const void* base, const moe_kv_cache* c, int rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return MOE_ERR_CUDA;
+  const bool mx = c->format == MOE_KV_MXFP8;
+  const cuuint64_t dims[2] = {(cuuint64_t)c->D, (cuuint64_t)c->pages * c->Hkv * c->page_size};
+  const cuuint64_t stride[1] = {(cuuint64_t)c->D * (mx ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(mx ? c->D : 64), (cuuint32_t)rows};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                         const_cast<void*>(base), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// The kernel for many rows a block (attention_paged_tc.cu).
+int launch_paged_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,707 @@
+// Attention of many rows over the paged cache: blocks of more than 16 rows (row, head of the group), as the verification
+// rows of speculative decoding make them (6 rows and 8 heads to a group are 48).
+//
+// Bound: HBM, as for few rows, but here the products decide whether it is reached: 4 D R flops a key are more than
+// mma.sync does at that rate once R passes 16 or so, and an MXFP8 cache would have to be converted by every warp again.
+// So both products run on tcgen05 with the rows as M = 128 (the rows beyond R cost nothing but tensor time, of which
+// there is enough: 1024 cycles a step of 128 tokens, against 2800 that its bytes take in bf16 and 1440 in MXFP8).
+//
+// Resident blocks take item after item: one piece of one (sequence, kv head). Its steps go in turn to two chains, each with
+// scores, weights and output of its own in Tensor Memory and a warpgroup of its own (a thread per row), so that one
+// chain's products run under the other's softmax:  PV0(0) QK0(2) | PV1(1) QK1(3) | PV0(2) QK0(4) ...  The chains' outputs
+// are joined at the item's end.
+// Pages come by TMA, bf16 straight into the ring that the products read, MXFP8 into a ring of raw codes from where a
+// warpgroup converts them once for all rows (exactly: four significant bits and a power of two fit bf16).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attention.cuh"
+#include "attention_paged.cuh"
+#include "attention_tc.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kRowsM = 128;             // rows of a block
+constexpr int kStepTok = 128;           // tokens of a step
+constexpr int kInfos = 16;              // steps whose tokens are remembered
+constexpr int kListed = 64;             // keys with values that are not finite that an item lists
+constexpr float kGrow = 8.f;            // the maximum that weights refer to moves when outgrown by 2^8
+
+template <int D_, bool MX_>
+struct TcCfg {
+  static constexpr int D = D_;
+  static constexpr bool MX = MX_;
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE = kStepTok * D * 2;                    // a step's keys, or values, in bf16; the queries
+  static constexpr int RAW = MX ? (kStepTok * D + kStepTok * (D / 32) + 1023) / 1024 * 1024 : 0;
+  static constexpr int RAWS = !MX ? 1 : D == 128 ? 5 : 10;         // stages of raw codes
+  static constexpr int ENTRIES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 12);
+  static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + 1024;
+  static constexpr int THREADS = MX ? 512 : 384;
+  // registers: the block is launched with 128 (168) a thread; the two softmax warpgroups take what the others give up
+  static constexpr int MORE = MX ? 184 : 208, LESS = MX ? 72 : 88;
+  static constexpr int FEEDERS = MX ? 4 : 1;                       // warps that hand tiles to the products
+  static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;   // Tensor Memory columns
+  static_assert(SMEM + 4096 <= 227 * 1024, "shared memory");
+};
+
+// Item `n` of a block, as it lies in shared memory.
+struct PagedItem {
+  int b, hk, mb, piece, len, there;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs p) {
+  constexpr int D = C::D;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t w_full[2], w_empty[2], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
+  __shared__ uint64_t chain1_there, chain1_read;
+  __shared__ uint64_t landed[C::MX ? C::RAWS : C::ENTRIES], raw_empty[C::RAWS], ready[C::ENTRIES], ent_empty[C::ENTRIES];
+  __shared__ PagedItem items[2];
+  __shared__ int4 infos[kInfos];                // of a step: first token, pages there, whether some row does not see a key
+  __shared__ int listed_n[2], listed[2][kListed];
+  __shared__ float2 chain1_ml[kRowsM];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = smem + C::TILE;
+  uint8_t* raws = ring + C::ENTRIES * C::TILE;
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&drain, 1);
+    mbar_init(&chain1_there, 128);
+    mbar_init(&chain1_read, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 10 + C::FEEDERS);  // the warps of the products, of the queries, of the feeding, of the softmax
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i][0], 128);
+      mbar_init(&p_full[i][1], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < (C::MX ? C::RAWS : C::ENTRIES); ++i) mbar_init(&landed[i], 1);
+    for (int i = 0; i < C::RAWS; ++i) mbar_init(&raw_empty[i], C::FEEDERS);
+    for (int i = 0; i < C::ENTRIES; ++i) {
+      mbar_init(&ready[i], C::FEEDERS);
+      mbar_init(&ent_empty[i], 1);
+    }
+    abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPagedWaitNs, &abort_flag, p.status, code)) != 0;
+  };
+  auto item_there = [&](int n) {
+    return wait(&w_full[n & 1], (n >> 1) & 1, DEV_TIMEOUT_FULL) && items[n & 1].there != 0;
+  };
+  auto item_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+  };
+  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
+  // An item's tiles pass in this order: K0 K1 V0 K2 V1 K3 V2 ..., one counter for all.
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LESS));
+    if (warp == 8) {
+      // ---------------- items and loads ----------------
+      const int units = p.a.B * p.mblocks * p.a.Hkv;
+      const int total = units * p.max_pieces;
+      const int in_tile = p.page_size >= kStepTok ? 1 : kStepTok >> p.page_log2;   // pages of a step
+      const int rows_of = min(p.page_size, kStepTok);
+      int n = 0, tile = 0, steps = 0;
+      bool ok = true;
+      // 32 candidates at a time; pieces that a sequence does not have are passed over. The first pieces of all come first,
+      // so that the ones that are there spread evenly over the blocks.
+      for (long long c0 = blockIdx.x; ok && c0 < total; c0 += 32ll * gridDim.x) {
+        const long long idx = c0 + (long long)lane * gridDim.x;
+        PagedItem mine{0, 0, 0, 0, 0, 0};
+        if (idx < total) {
+          int u = (int)(idx % units);
+          mine.piece = (int)(idx / units);
+          mine.hk = u % p.a.Hkv;
+          u /= p.a.Hkv;
+          mine.mb = u % p.mblocks;
+          mine.b = u / p.mblocks;
+          mine.len = checked_len(p, mine.b, true);
+          mine.there = mine.piece < Pieces(p, mine.len, mine.mb).count;
+        }
+        for (unsigned some = __ballot_sync(0xffffffffu, mine.there != 0); ok && some; some &= some - 1) {
+          const int who = __ffs(some) - 1;
+          PagedItem it;
+          it.b = __shfl_sync(0xffffffffu, mine.b, who);
+          it.hk = __shfl_sync(0xffffffffu, mine.hk, who);
+          it.mb = __shfl_sync(0xffffffffu, mine.mb, who);
+          it.piece = __shfl_sync(0xffffffffu, mine.piece, who);
+          it.len = __shfl_sync(0xffffffffu, mine.len, who);
+          it.there = 1;
+          if (n >= 2 && !(ok = wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
+          if (lane == 0) {
+            items[n & 1] = it;
+            listed_n[n & 1] = 0;                // the last item but one, whose list this was, is done
+            mbar_arrive(&w_full[n & 1]);
+          }
+          ++n;
+          const Pieces pc(p, it.len, it.mb);
+          const int i0 = it.piece * pc.per, cnt = min(pc.tiles - i0, pc.per);
+          const int32_t* table = p.table + (long long)it.b * p.table_width;
+          const int last_page = pc.pmax >> p.page_log2;
+          int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
+          int held[2] = {-1, -1};                    // page of this lane in the last two steps
+          auto load = [&](int i, bool is_v, int id) {
+            const int tok0 = pc.tile(i0 + i) * kStepTok, t0 = tok0 + lane * rows_of;
+            const int st = tile % (C::MX ? C::RAWS : C::ENTRIES), use = tile / (C::MX ? C::RAWS : C::ENTRIES);
+            const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
+            if (use > 0 && !(ok = wait(C::MX ? &raw_empty[st] : &ent_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
+            if (lane == 0) {
+              if (!is_v) {
+                const bool whole = tok0 + kStepTok - 1 <= pc.pmin && (tok0 >= pc.first_all || tok0 + kStepTok <= p.a.sinks) &&
+                                   mask == (1u << in_tile) - 1u;
+                infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
+              }
+              mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D));
+            }
+            __syncwarp();
+            if (id >= 0) {
+              const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
+              const CUtensorMap* map = is_v ? &vmap : &kmap;
+              if (C::MX) {
+                uint8_t* dst = raws + st * C::RAW;
+                tma_load_2d(dst + lane * rows_of * D, map, 0, row, &landed[st]);
+                bulk_load(dst + kStepTok * D + lane * rows_of * (D / 32), (is_v ? p.v_s : p.k_s) + (long long)row * (D / 32),
+                          rows_of * (D / 32), &landed[st]);
+              } else {
+                uint8_t* dst = ring + st * C::TILE;
+                for (int h = 0; h < C::HALVES; ++h)
+                  tma_load_2d(dst + h * kStepTok * 128 + lane * rows_of * 128, map, h * 64, row, &landed[st]);
+              }
+            }
+            ++tile;
+          };
+          auto load_k = [&](int i) {
+            const int tok0 = pc.tile(i0 + i) * kStepTok, page0 = tok0 >> p.page_log2;
+            if (page0 < base || page0 + in_tile > base + 32) {
+              const int nb = page0 & ~31;            // in_tile divides 32: a step's pages lie in one group of 32 entries
+              ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+              base = nb;
+              next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+            // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+            const int t0 = tok0 + lane * rows_of;
+            const bool want = lane < in_tile && t0 <= pc.pmax &&
+                              (t0 + rows_of > pc.first_any || t0 < min(p.a.sinks, pc.first_all));
+            const bool good = want && id >= 0 && id < p.pages;
+            if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+            const int got = good ? id : -1;
+            if (i & 1) held[1] = got; else held[0] = got;
+            load(i, false, got);
+          };
+          if (cnt > 0) load_k(0);
+          if (ok && cnt > 1) load_k(1);
+          for (int i = 0; ok && i < cnt; ++i) {
+            load(i, true, i & 1 ? held[1] : held[0]);
+            if (ok && i + 2 < cnt) load_k(i + 2);
+          }
+          steps += max(cnt, 0);
+        }
+      }
+      // no more items
+      if (ok && (n < 2 || wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) && lane == 0) {
+        items[n & 1].there = 0;
+        mbar_arrive(&w_full[n & 1]);
+      }
+      if (abort_flag)                           // copies in flight end before the block does
+        for (int j = max(0, tile - (C::MX ? C::RAWS : C::ENTRIES)); j < tile; ++j)
+          mbar_wait(&landed[j % (C::MX ? C::RAWS : C::ENTRIES)], (j / (C::MX ? C::RAWS : C::ENTRIES)) & 1, kPagedWaitNs,
+                    nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+    } else if (warp == 9) {
+      // ---------------- products ----------------
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const bool leader = elect_one();
+      const uint32_t idesc_qk = idesc_bf16_f32(kRowsM, kStepTok);
+      const uint32_t idesc_pv = idesc_bf16_f32(kRowsM, D) | (1u << 16);
+      const uint64_t qdesc = smem_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t kdesc = smem_desc(smem_u32(ring), 16, 1024, 2);
+      const uint64_t vdesc = smem_desc(smem_u32(ring), kStepTok * 128, 1024, 2);
+      int tile = 0, qs = 0, done[2] = {0, 0};   // tiles, queries and steps of the chains so far
+      auto have = [&]() { return wait(&ready[tile % C::ENTRIES], (tile / C::ENTRIES) & 1, DEV_TIMEOUT_FULL); };
+      auto qk = [&](int x) {
+        if (leader) {
+          const uint64_t kx = kdesc + (tile % C::ENTRIES) * (C::TILE >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int at = ((ks / 4) * kStepTok * 128 + (ks % 4) * 32) >> 4;
+            mma_bf16(tm + (x ? C::S1 : C::S0), qdesc + at, kx + at, idesc_qk, ks > 0);
+          }
+          tc_commit(&s_full[x]);
+          tc_commit(&ent_empty[tile % C::ENTRIES]);
+        }
+        __syncwarp();
+        ++tile;
+      };
+      auto pv = [&](int x, int h, bool more) {
+        if (leader) {
+          const uint32_t d = tm + (x ? C::O1 : C::O0), a = tm + (x ? C::S1 : C::S0);
+          const uint64_t vx = vdesc + (tile % C::ENTRIES) * (C::TILE >> 4);
+#pragma unroll
+          for (int k4 = 0; k4 < kStepTok / 32; ++k4) {
+            const int ks = h * kStepTok / 32 + k4;
+            mma_bf16_ts(d, a + ks * 8, vx + ks * (2048 >> 4), idesc_pv, more || k4 > 0);
+          }
+        }
+        __syncwarp();
+      };
+      bool ok = true;
+      for (int n = 0; ok && item_there(n); ++n) {
+        const PagedItem it = items[n & 1];
+        item_done(n);
+        const Pieces pc(p, it.len, it.mb);
+        const int cnt = min(pc.tiles - it.piece * pc.per, pc.per);
+        if (cnt <= 0) continue;
+        if (!(ok = wait(&q_full, qs & 1, DEV_TIMEOUT_FULL))) break;
+        ++qs;
+        tc_fence_after();
+        for (int x = 0; ok && x < min(cnt, 2); ++x) {
+          if (!(ok = have())) break;
+          tc_fence_after();
+          qk(x);
+        }
+        if (cnt <= 2 && leader) tc_commit(&q_empty);
+        for (int i = 0; ok && i < cnt; ++i) {
+          const int x = i & 1, k = x ? done[1] : done[0];
+          if (!(ok = have() && wait(&p_full[x][0], k & 1, DEV_TIMEOUT_ACCUM))) break;
+          tc_fence_after();
+          pv(x, 0, i > 1);
+          if (!(ok = wait(&p_full[x][1], k & 1, DEV_TIMEOUT_ACCUM))) break;
+          tc_fence_after();
+          pv(x, 1, true);
+          if (leader) {
+            tc_commit(&ent_empty[tile % C::ENTRIES]);
+            tc_commit(&o_full[x]);
+          }
+          __syncwarp();
+          ++tile;
+          if (x) ++done[1]; else ++done[0];
+          if (i + 2 < cnt) {
+            if (!(ok = have())) break;
+            tc_fence_after();
+            qk(x);
+            if (i + 3 == cnt && leader) tc_commit(&q_empty);
+          }
+        }
+      }
+      if (leader && abort_flag) {
+        tc_commit(&drain);
+        mbar_wait(&drain, 0, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      }
+    } else if (warp == 10) {
+      // ---------------- queries ----------------
+      // Into the layout of a swizzled TMA tile. Rows beyond R keep what was there: a row of the products depends on its own
+      // query alone.
+      int qs = 0;
+      bool ok = true;
+      for (int n = 0; ok && item_there(n); ++n) {
+        const PagedItem it = items[n & 1];
+        const Pieces pc(p, it.len, it.mb);
+        if (min(pc.tiles - it.piece * pc.per, pc.per) > 0) {
+          if (qs > 0 && !(ok = wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
+          ++qs;
+          const int live = min(R - it.mb * kRowsM, kRowsM);
+#pragma unroll 4
+          for (int e = lane; e < live * (D / 8); e += 32) {
+            const int row = e / (D / 8), ch = e % (D / 8), rho = it.mb * kRowsM + row;
+            const uint4 v = *reinterpret_cast<const uint4*>(p.q + ((long long)it.b * p.rows + rho / G) * p.q_stride +
+                                                            (long long)(it.hk * G + rho % G) * D + ch * 8);
+            *reinterpret_cast<uint4*>(smem + (ch >> 3) * kRowsM * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full);
+        }
+        item_done(n);
+      }
+    } else if (C::MX ? warp >= 12 : warp == 11) {
+      // ---------------- feeding ----------------
+      // Hands every tile to the products, MXFP8 converted. In steps where some row does not see a key, values that are not
+      // finite become zero (a weight of zero would not hide them), and those that some row sees are listed: rows that see
+      // them are computed again.
+      const int tid = C::MX ? threadIdx.x - 384 : lane;
+      int tile = 0, steps = 0;
+      bool ok = true;
+      for (int n = 0; ok && item_there(n); ++n) {
+        const PagedItem it = items[n & 1];
+        const Pieces pc(p, it.len, it.mb);
+        const int cnt = min(pc.tiles - it.piece * pc.per, pc.per);
+        auto list = [&](int tok) {
+          if (tok > pc.pmax || (tok < pc.first_any && tok >= p.a.sinks)) return;
+          const int at = atomicAdd(&listed_n[n & 1], 1);
+          if (at < kListed) listed[n & 1][at] = tok;
+        };
+        auto feed = [&](int i, bool is_v) {
+          const int e = tile % C::ENTRIES, st = C::MX ? tile % C::RAWS : e;
+          if (!(ok = wait(&landed[st], (tile / (C::MX ? C::RAWS : C::ENTRIES)) & 1, DEV_TIMEOUT_FULL))) return;
+          const int4 info = infos[(steps + i) % kInfos];
+          const bool edge = is_v && info.z != 0;
+          uint8_t* dst = ring + e * C::TILE;
+          if (C::MX) {
+            if (tile >= C::ENTRIES && !(ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
+            const uint8_t* src = raws + st * C::RAW;
+            constexpr int CH = D / 16;          // 16 codes at a time
+#pragma unroll 4
+            for (int j = 0; j < kStepTok * CH / 128; ++j) {
+              const int at = tid + 128 * j, row = at / CH, ch = at % CH;
+              const uint4 w = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
+              const uint32_t by = src[kStepTok * D + row * (D / 32) + ch / 2], f = scale_bits(by) * 0x10001u;
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                o[2 * b] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x1800), f);
+                o[2 * b + 1] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x3A22), f);
+              }
+              if (by > kScaleFits) {
+                const uint32_t f2 = scale_rest(by) * 0x10001u;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) o[b] = mul_bf16x2(o[b], f2);
+              }
+              if (edge) {
+                bool bad = false;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                  const uint32_t hit = ((o[b] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  bad = bad || hit;
+                  o[b] &= ~((hit >> 15) * 0xFFFFu);
+                }
+                if (bad) list(info.x + row);
+              }
+              uint8_t* to = dst + (ch >> 2) * kStepTok * 128 + row * 128;
+              const int c0 = (2 * ch) & 7;
+              *reinterpret_cast<uint4*>(to + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[st]);
+          } else if (edge) {
+            uint4* v = reinterpret_cast<uint4*>(dst);
+            // zero times a value that is not finite is NaN, and stays in the sum
+            uint32_t sum = 0;
+#pragma unroll 8
+            for (int a = lane; a < C::TILE / 16; a += 32) {
+              const uint4 w = v[a];
+              sum = fma_bf16x2(w.x, 0, sum);
+              sum = fma_bf16x2(w.y, 0, sum);
+              sum = fma_bf16x2(w.z, 0, sum);
+              sum = fma_bf16x2(w.w, 0, sum);
+            }
+            if (__any_sync(0xffffffffu, (sum & 0x7FFF7FFFu) != 0)) {
+#pragma unroll 1
+              for (int a = lane; a < C::TILE / 16; a += 32) {
+                const uint4 w = v[a];
+                uint32_t z[4] = {w.x, w.y, w.z, w.w};
+                bool bad = false;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const uint32_t hit = ((z[b] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  bad = bad || hit;
+                  z[b] &= ~((hit >> 15) * 0xFFFFu);
+                }
+                // 8 neighbouring lanes hold one key's 64 values: one of them lists it
+                const unsigned hits = __ballot_sync(0xffffffffu, bad) & (0xFFu << (lane & 24));
+                if (bad) {
+                  v[a] = make_uint4(z[0], z[1], z[2], z[3]);
+                  if (__ffs(hits) - 1 == lane) list(info.x + a / 8 % kStepTok);
+                }
+              }
+              fence_async_smem();
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&ready[e]);
+          ++tile;
+        };
+        if (cnt > 0) feed(0, false);
+        if (ok && cnt > 1) feed(1, false);
+        for (int i = 0; ok && i < cnt; ++i) {
+          feed(i, true);
+          if (ok && i + 2 < cnt) feed(i + 2, false);
+        }
+        steps += max(cnt, 0);
+        item_done(n);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE));
+    // ---------------- softmax ----------------
+    const int x = warp / 4, row = threadIdx.x % 128;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + (x ? C::S1 : C::S0) + lanes, to = tmem + (x ? C::O1 : C::O0) + lanes;
+    // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
+    const uint32_t turn = p.a.scale < 0.f ? 0x80000000u : 0u;
+    const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
+    const uint64_t c2 = pack2(c, c);
+    int done = 0, steps = 0;                    // steps of this chain, and of all, so far
+    bool ok = true;
+    for (int n = 0; ok && item_there(n); ++n) {
+      int cnt, pos, first;
+      bool warp_live;
+      {
+        const PagedItem it = items[n & 1];
+        const Pieces pc(p, it.len, it.mb);
+        cnt = max(0, min(pc.tiles - it.piece * pc.per, pc.per));
+        const int rho = it.mb * kRowsM + row;
+        pos = rho < R ? it.len - p.rows + rho / G : -1;
+        first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
+        warp_live = __any_sync(0xffffffffu, rho < R);
+      }
+      float m = -INFINITY;                      // the maximum that the weights so far refer to
+      uint64_t l2 = pack2(0.f, 0.f);
+      bool any = false;                         // a step of this chain
+      for (int i = x; i < cnt; i += 2, ++done) {
+        if (!(ok = wait(&s_full[x], done & 1, DEV_TIMEOUT_ACCUM))) break;
+        tc_fence_after();
+        if (!warp_live) {                       // rows that nobody has: their weights may be anything
+          mbar_arrive(&p_full[x][0]);
+          mbar_arrive(&p_full[x][1]);
+          any = true;
+          continue;
+        }
+        const int4 info = infos[(steps + i) % kInfos];
+        uint32_t s[128];
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
+        if (turn) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] ^= turn;
+        }
+        if (info.z) {
+          const int hi = pos - info.x, lo = first - info.x, low = p.a.sinks - info.x;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = e <= hi && (e >= lo || e < low) ? s[e] : 0xff800000u;
+          const int in_tile = p.page_size >= kStepTok ? 1 : kStepTok >> p.page_log2;
+          if ((unsigned)info.y != (1u << in_tile) - 1u) {
+#pragma unroll
+            for (int e = 0; e < 128; e += 8)    // a page has at least 8 tokens
+              if (!(((unsigned)info.y >> (e >> min(p.page_log2, 7))) & 1u)) {
+#pragma unroll
+                for (int d = 0; d < 8; ++d) s[e + d] = 0xff800000u;
+              }
+          }
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 8)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            m4[f] = max3(m4[f], __uint_as_float(s[e + 2 * f]), __uint_as_float(s[e + 2 * f + 1]));
+        const float mn = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), m);
+        if (__any_sync(0xffffffffu, (mn - m) * c > kGrow)) {             // (-inf) - (-inf): no
+          if (any) {
+            if (!(ok = wait(&o_full[x], (done - 1) & 1, DEV_TIMEOUT_ACCUM))) break;
+            tc_fence_after();
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+            l2 = mul2(l2, pack2(f, f));
+#pragma unroll 1
+            for (int e = 0; e < D; e += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + e, o);
+              tmem_ld_wait();
+              reg_fence16(o);
+#pragma unroll
+              for (int d = 0; d < 16; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+              tmem_st16(to + e, o);
+            }
+          }
+          m = mn;
+        }
+        any = true;
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t b2 = pack2(base, base);
+        uint64_t la = pack2(0.f, 0.f), lb = la;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 64 * h; e < 64 * h + 64; e += 4) {
+            float w[4];
+            unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, b2), w[0], w[1]);
+            unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), w[2], w[3]);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) w[f] = ex2(w[f]);
+            const uint32_t u = bf16x2(w[0], w[1]), v = bf16x2(w[2], w[3]);
+            // the sum takes the weights as the product does, rounded, so that a single large one divides out exactly
+            la = add2(la, pack2(bf16_lo(u), bf16_hi(u)));
+            lb = add2(lb, pack2(bf16_lo(v), bf16_hi(v)));
+            s[e / 2] = u;                       // s[e / 2] has been read
+            s[e / 2 + 1] = v;
+          }
+          tmem_st32(ts + 32 * h, s, 32 * h);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[x][h]);
+        }
+        l2 = add2(l2, add2(la, lb));
+      }
+      if (ok && any) {
+        ok = wait(&o_full[x], (done - 1) & 1, DEV_TIMEOUT_ACCUM);
+        tc_fence_after();
+      }
+      steps += cnt;
+      float la, lb;
+      unpack2(l2, la, lb);
+      const float l = la + lb, top = m == -INFINITY ? -INFINITY : m * c;
+
+      // ---- the chains joined, by the first one's warps: both have the same rows in the same lanes ----
+      if (x == 1) chain1_ml[row] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
+      tc_fence_before();
+      if (x == 1) mbar_arrive(&chain1_there);
+      if (x == 0) {
+        ok = wait(&chain1_there, n & 1, DEV_TIMEOUT_ACCUM) && ok;
+        tc_fence_after();
+        const PagedItem it = items[n & 1];
+        const Pieces pc(p, it.len, it.mb);
+        const int rho = it.mb * kRowsM + row;
+        const bool live = rho < R;
+        const float2 other = chain1_ml[row];
+        const float both = fmaxf(top, other.x), base = both == -INFINITY ? 0.f : both;
+        const float f0 = ex2(top - base), f1 = ex2(other.x - base), tl = f0 * l + f1 * other.y;
+        const float inv = pc.count > 1 ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
+        const float g0 = f0 * inv, g1 = f1 * inv;
+        const long long out_at = (((long long)it.b * p.rows + rho / G) * p.a.Hq + it.hk * G + rho % G) * D;
+        const long long part_at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + rho;
+        if (ok && warp_live) {
+#pragma unroll 1
+          for (int e = 0; e < D; e += 32) {
+            uint32_t a[32], b[32];
+            tmem_ld32(to + e, a, 0);
+            tmem_ld32(to + C::O1 - C::O0 + e, b, 0);
+            tmem_ld_wait();
+            reg_fence32(a, 0);
+            reg_fence32(b, 0);
+            float v[32];
+#pragma unroll
+            for (int d = 0; d < 32; ++d) {
+              // a chain without steps has no output: what is there is nobody's
+              v[d] = cnt > 0 ? __uint_as_float(a[d]) * g0 : 0.f;
+              if (cnt > 1) v[d] = fmaf(__uint_as_float(b[d]), g1, v[d]);
+            }
+            if (live) {
+              if (pc.count == 1) {
+#pragma unroll
+                for (int d = 0; d < 32; d += 8)
+                  *reinterpret_cast<uint4*>(p.out + out_at + e + d) =
+                      make_uint4(bf16x2(v[d], v[d + 1]), bf16x2(v[d + 2], v[d + 3]), bf16x2(v[d + 4], v[d + 5]),
+                                 bf16x2(v[d + 6], v[d + 7]));
+              } else {
+#pragma unroll
+                for (int d = 0; d < 32; d += 4)
+                  *reinterpret_cast<float4*>(p.part_o + part_at * D + e + d) = make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]);
+              }
+            }
+          }
+          if (live && pc.count > 1) *reinterpret_cast<float2*>(p.part_ml + part_at * 2) = make_float2(both, tl);
+        }
+        tc_fence_before();
+        mbar_arrive(&chain1_read);              // the second chain may go on
+
+        // ---- rows that see a listed key, from the definition ----
+        if (ok && cnt > 0) {
+          const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
+          bool again = some > kListed;
+          const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
+          for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
+          again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
+          for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1) {
+            constexpr int N = D / 32;
+            const int r2 = __shfl_sync(0xffffffffu, rho, __ffs(rows) - 1);
+            const Visible see2(it.len - p.rows + r2 / G, p.a.window, p.a.sinks);
+            LaneRow<D> q;
+            q.load_bf16(p.q + ((long long)it.b * p.rows + r2 / G) * p.q_stride + (long long)(it.hk * G + r2 % G) * D, lane);
+            float m2 = -INFINITY, s2 = 0.f, o[N] = {};
+            const int t0 = it.piece * pc.per;
+            for (int i = 0; i < cnt; ++i) {
+              const int tok0 = pc.tile(t0 + i) * kStepTok;
+              attend_keys<D>(q, see2, tok0, tok0 + kStepTok, p.a.scale * 1.4426950408889634f, m2, s2, o,
+                             [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
+                               const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
+                               if (page < 0 || page >= p.pages) return false;
+                               const long long at = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) +
+                                                    (j & (p.page_size - 1));
+                               if (C::MX) {
+                                 k.load_mxfp8(p.k + at * D, p.k_s + at * N, lane);
+                                 v.load_mxfp8(p.v + at * D, p.v_s + at * N, lane);
+                               } else {
+                                 k.load_bf16(reinterpret_cast<const uint16_t*>(p.k) + at * D, lane);
+                                 v.load_bf16(reinterpret_cast<const uint16_t*>(p.v) + at * D, lane);
+                               }
+                               return true;
+                             });
+            }
+            if (pc.count == 1) {
+              uint32_t* out = reinterpret_cast<uint32_t*>(
+                  p.out + (((long long)it.b * p.rows + r2 / G) * p.a.Hq + it.hk * G + r2 % G) * D + lane * N);
+#pragma unroll
+              for (int i = 0; i < N / 2; ++i) out[i] = s2 == 0.f ? 0u : bf16x2(o[2 * i] / s2, o[2 * i + 1] / s2);
+            } else {
+              const long long at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + r2;
+#pragma unroll
+              for (int i = 0; i < N; ++i) p.part_o[at * D + lane * N + i] = o[i];
+              if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m2, s2);
+            }
+          }
+        }
+      } else {
+        ok = wait(&chain1_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;
+        tc_fence_after();
+      }
+      item_done(n);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool MX>
+static int launch_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  using C = TcCfg<D, MX>;
+  CUtensorMap km, vm;
+  const int box = std::min(cache->page_size, kStepTok);
+  const CUtensorMapSwizzle swizzle = MX ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  int rc = page_map(&km, cache->k, cache, box, swizzle);
+  if (rc || (rc = page_map(&vm, cache->v, cache, box, swizzle))) return rc;
+  auto kern = paged_tc_kernel<C>;
+  if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM))) return rc;
+  const long long items = (long long)p.a.B * p.mblocks * p.a.Hkv * p.max_pieces;
+  return launch_pdl(kern, dim3((unsigned)std::min(items, (long long)num_sms())), dim3(C::THREADS), C::SMEM, st, km, vm, p);
+}
+
+int launch_paged_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  const bool mx = cache->format == MOE_KV_MXFP8;
+  if (p.a.D == 64) return mx ? launch_tc<64, true>(p, cache, st) : launch_tc<64, false>(p, cache, st);
+  return mx ? launch_tc<128, true>(p, cache, st) : launch_tc<128, false>(p, cache, st);
+}
+
+}  // namespace moe

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 #include "ptx.cuh"
@@ -63,102 +64,6 @@ __device__ __forceinline__ Span span_of(const PrefillArgs& p, int b) {
   return s;
 }
 
-// D (+)= A B with A from Tensor Memory (bf16, two a column).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-#define MOE_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
-                     "=r"(r[i + 6]), "=r"(r[i + 7])
-#define MOE_RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
-                      "+r"(r[i + 6]), "+r"(r[i + 7])
-#define MOE_RI8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
-                      "r"(r[i + 6]), "r"(r[i + 7])
-
-// 32 lanes x 32 columns from r[i] on / back.
-template <int N>
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[N], int i) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : MOE_R8(r, i), MOE_R8(r, i + 8), MOE_R8(r, i + 16), MOE_R8(r, i + 24) : "r"(taddr) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[N]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::MOE_RI8(r, 0), MOE_RI8(r, 8), "r"(taddr) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[N], int i) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::MOE_RI8(r, i), MOE_RI8(r, i + 8), MOE_RI8(r, i + 16), MOE_RI8(r, i + 24), "r"(taddr) : "memory");
-}
-// No use of r[i..i+31] is scheduled before this point.
-template <int N>
-__device__ __forceinline__ void reg_fence32(uint32_t (&r)[N], int i) {
-  asm volatile("" : MOE_RW8(r, i), MOE_RW8(r, i + 8), MOE_RW8(r, i + 16), MOE_RW8(r, i + 24));
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2f(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// a b + c of two bf16 each.
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 template <int D>
 struct PrefillCfg {
   static constexpr int HALVES = D / 64;
@@ -185,7 +90,7 @@ __device__ __noinline__ void redo_row(const PrefillArgs& p, const Span& s, int r
   LaneRow<D> q;
   q.load_bf16(p.q + t * p.q_stride + (long long)h * D, lane);
   float m = -INFINITY, l = 0.f, o[N] = {};
-  attend_row<D>(q, see, 0, 1, p.a.scale * 1.4426950408889634f, m, l, o, [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
+  attend_keys<D>(q, see, 0, s.kn, p.a.scale * 1.4426950408889634f, m, l, o, [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
     k.load_bf16(p.k + (long long)(s.k0 + j) * p.k_stride + (long long)hk * D, lane);
     v.load_bf16(p.v + (long long)(s.k0 + j) * p.v_stride + (long long)hk * D, lane);
     return true;
@@ -341,6 +246,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         if (lane == 0) {
 #pragma unroll
           for (int i = 0; i < 7; ++i) slots[n & 1][i] = slot[i];
+          bad_count[n & 1] = 0;                 // the last item but one, whose list this was, is done
           mbar_arrive(&w_full[n & 1]);
         }
         if (!found) break;                      // the later rounds have none either
@@ -484,8 +390,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
         const Item it(p, slots[n & 1]);
-        if (tid == 0) bad_count[n & 1] = 0;     // the last item but one, whose list this was, is done
-        named_bar_sync(2, 64);
         const Edges e0 = it.edges(p, 0), e1 = it.edges(p, 1);
         for (int i = 0; i < it.tiles; ++i, kv += 2) {
           // every step's values pass here, edge or not: a barrier's parity tells its next phase from the last one only
@@ -582,7 +486,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           if (i > 0) {
             if (!wait(&o_full[x], (step - 1) & 1, DEV_TIMEOUT_ACCUM)) return false;
             tc_fence_after();
-            const float f = m == -INFINITY ? 0.f : ex2f((m - mn) * c);
+            const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
             l2 = mul2(l2, pack2(f, f));
 #pragma unroll 1
             for (int e = 0; e < D; e += 16) {
@@ -603,7 +507,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, b2), w[0], w[1]);
           unpack2(fma2(pack2(__uint_as_float(s[2]), __uint_as_float(s[3])), c2, b2), w[2], w[3]);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) w[f] = ex2f(w[f]);
+          for (int f = 0; f < 4; ++f) w[f] = ex2(w[f]);
           la = add2(la, pack2(w[0], w[1]));
           lb = add2(lb, pack2(w[2], w[3]));
         };

@@ -249,6 +249,101 @@ def test_lengths_and_pages_out_of_range_are_reported():
     p.B.attention_status()
 
 
+# Blocks of many rows go another way than blocks of up to 16: the same checks there.
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq,Hkv,page", [(17, 1, 1, 8), (6, 64, 2, 16), (64, 4, 1, 64), (5, 40, 1, 128),
+                                              (3, 12, 2, 256)])
+def test_many_rows(rows, Hq, Hkv, page, D, mx):
+    lens = [1, rows, 17, 0, 127, 128, 129, 257, 700, 1400, 2]
+    Paged(lens, rows, Hq, Hkv, D, page, mx, seed=rows * 100 + Hq).check()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 4), (16, 0), (64, 4), (100, 70), (128, 300), (1000, 3),
+                                          (257, 129)])
+def test_many_rows_windows_and_first_tokens(window, sinks, mx):
+    Paged([700, 5, 64, 129, 1, 333, 1100], 5, 16, 2, 64, 16, mx, seed=window).check(window, sinks)
+    Paged([1100, 2300], 4, 16, 2, 128, 64, mx, seed=window).check(window, sinks)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_many_rows_long_and_growing(mx):
+    Paged([9001, 4097, 1, 2049, 12000], 6, 16, 2, 64, 32, mx, seed=4).check()
+    p = Paged([900, 33, 5000], 6, 8, 1, 128, 16, mx, seed=8, q_scale=6.0, spread=0.7)
+    p.check()
+    p.check(scale=-0.5)
+    p.check(scale=0.0)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_many_rows_do_not_depend_on_their_batch(mx):
+    p = Paged([3000, 40, 777, 1025, 9000], 6, 16, 2, 64, 16, mx, seed=3)
+    whole = p.run()
+    for b, n in enumerate(p.lens):
+        for max_len in (n, n + 1, 9000):
+            one = p.B.moe_paged_attention(p.q[b:b + 1].contiguous(), p.cache, p.table[b:b + 1].contiguous(),
+                                          p.seq_lens()[b:b + 1], min(max_len, 16 * p.table.shape[1]))
+            assert torch.equal(one[0], whole[b])
+    for _ in range(30):
+        assert torch.equal(p.run(), whole)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_many_rows_values_that_are_not_finite(mx):
+    """Unseen ones are left out; one that later rows see reaches those and their columns alone."""
+    p = Paged([700, 300], 6, 8, 1, 128, 64, mx, seed=7)
+    clean = p.run(100, 3)
+
+    def put(b, j, key, value):
+        page, at = int(p.table[b, j // 64]), j % 64
+        if mx:
+            if key:
+                p.cache.k_s[page, :, at] = 255
+            p.cache.v_s[page, :, at, value] = 255
+        else:
+            if key:
+                p.cache.k[page, :, at] = float("nan")
+            p.cache.v[page, :, at, 32 * value] = float("-inf")
+    for j in (3, 30, 250, 593):                # the window of the first row begins at 595
+        put(0, j, True, 0)
+    assert torch.equal(p.run(100, 3), clean)
+    put(1, 297, False, 2)                       # seen by the last three of six rows, at 297 to 299
+    got = p.run(100, 3)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1, :3], clean[1, :3])
+    hit = got[1, 3:].float()
+    assert not hit[..., 64].isfinite().any()
+    keep = [d for d in range(128) if not 64 <= d < 96]
+    assert (hit[..., keep] - clean[1, 3:].float()[..., keep]).abs().max() < 2.0 ** -6   # both within the oracle's bound
+    put(1, 296, True, 0)                        # and a key: the rows from the third on are lost
+    got = p.run(100, 3)
+    assert torch.equal(got[1, :2], clean[1, :2]) and got[1, 2:].isnan().all()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_many_rows_pages_out_of_range(mx):
+    p = Paged([500, 41], 6, 8, 2, 64, 16, mx, seed=9)
+    want = p.run()
+    for bad in (-1, p.cache.pages, 2 ** 31 - 1):
+        table = p.table.clone()
+        table[0, 2] = bad
+        got = p.B.moe_paged_attention(p.q, p.cache, table, p.seq_lens(), 500)
+        with pytest.raises(p.B.MoeError):
+            p.B.attention_status()
+        assert torch.equal(got[1], want[1]) and got[0].isfinite().all() and not torch.equal(got[0], want[0])
+        lens = torch.tensor([501, 41], dtype=torch.int32, device="cuda")
+        got = p.B.moe_paged_attention(p.q, p.cache, p.table, lens, 500)
+        with pytest.raises(p.B.MoeError):
+            p.B.attention_status()
+        assert not got[0].any() and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_more_pieces_than_the_gpu_has_room_for(mx):
+    lens = [int(n) for n in np.random.default_rng(1).integers(1, 1500, 60)] + [0, 3, 1500]
+    Paged(lens, 3, 24, 4, 64, 16, mx, seed=5).check()
+
+
 def test_offsets_past_32_bits():
     """Pages whose values lie more than 2^31 elements, and 2^32 bytes, into the cache."""
     from block_scaled_fp8_moe_gb300 import binding as B
