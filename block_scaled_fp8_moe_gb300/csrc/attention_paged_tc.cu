@@ -36,9 +36,10 @@ struct TcCfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = kStepTok * D * 2;                    // a step's keys, or values, in bf16; the queries
   static constexpr int RAW = MX ? (kStepTok * D + kStepTok * (D / 32) + 1023) / 1024 * 1024 : 0;
-  static constexpr int RAWS = !MX ? 1 : D == 128 ? 5 : 10;         // stages of raw codes
-  static constexpr int ENTRIES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 12);
-  static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + 1024;
+  static constexpr int RAWS = !MX ? 1 : D == 128 ? 4 : 9;          // stages of raw codes
+  static constexpr int ENTRIES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  static constexpr int OUT = 4 * 4096;                             // the output's way to global memory, 4 KB a warp
+  static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + OUT + 1024;
   static constexpr int THREADS = MX ? 512 : 384;
   // registers: the block is launched with 128 (168) a thread; the two softmax warpgroups take what the others give up
   static constexpr int MORE = MX ? 184 : 208, LESS = MX ? 72 : 88;
@@ -69,6 +70,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + C::TILE;
   uint8_t* raws = ring + C::ENTRIES * C::TILE;
+  uint8_t* staging = raws + (C::MX ? C::RAWS * C::RAW : 0);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   pdl_trigger();
@@ -364,38 +366,48 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           if (C::MX) {
             if (tile >= C::ENTRIES && !(ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
             const uint8_t* src = raws + st * C::RAW;
-            constexpr int CH = D / 16;          // 16 codes at a time
-#pragma unroll 4
-            for (int j = 0; j < kStepTok * CH / 128; ++j) {
-              const int at = tid + 128 * j, row = at / CH, ch = at % CH;
-              const uint4 w = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
-              const uint32_t by = src[kStepTok * D + row * (D / 32) + ch / 2], f = scale_bits(by) * 0x10001u;
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-              uint32_t o[8];
+            constexpr int CH = D / 16;          // 16 codes at a time, four such a thread
+            const int ch = tid % CH, c0 = (2 * ch) & 7;
+            uint8_t* to = dst + (ch >> 2) * kStepTok * 128;
+#pragma unroll 1
+            for (int r0 = tid / CH; r0 < kStepTok; r0 += 4 * 128 / CH) {
+              uint4 w[4];
+              uint32_t by[4];
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                o[2 * b] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x1800), f);
-                o[2 * b + 1] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x3A22), f);
+              for (int j = 0; j < 4; ++j) {
+                const int row = r0 + j * (128 / CH);
+                w[j] = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
+                by[j] = src[kStepTok * D + row * (D / 32) + ch / 2];
               }
-              if (by > kScaleFits) {
-                const uint32_t f2 = scale_rest(by) * 0x10001u;
+              const bool large = __any_sync(0xffffffffu, max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits);
 #pragma unroll
-                for (int b = 0; b < 8; ++b) o[b] = mul_bf16x2(o[b], f2);
-              }
-              if (edge) {
-                bool bad = false;
+              for (int j = 0; j < 4; ++j) {
+                const int row = r0 + j * (128 / CH);
+                const uint32_t f = scale_bits(by[j]) * 0x10001u, ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                uint32_t o[8];
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                  const uint32_t hit = ((o[b] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                  bad = bad || hit;
-                  o[b] &= ~((hit >> 15) * 0xFFFFu);
+                for (int b = 0; b < 4; ++b) {
+                  o[2 * b] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x1800), f);
+                  o[2 * b + 1] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x3A22), f);
                 }
-                if (bad) list(info.x + row);
+                if (large) {
+                  const uint32_t f2 = scale_rest(by[j]) * 0x10001u;
+#pragma unroll
+                  for (int b = 0; b < 8; ++b) o[b] = mul_bf16x2(o[b], f2);
+                  if (edge) {                   // a value is not finite only where its scale is large
+                    bool bad = false;
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                      const uint32_t hit = ((o[b] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                      bad = bad || hit;
+                      o[b] &= ~((hit >> 15) * 0xFFFFu);
+                    }
+                    if (bad) list(info.x + row);
+                  }
+                }
+                *reinterpret_cast<uint4*>(to + row * 128 + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(to + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
               }
-              uint8_t* to = dst + (ch >> 2) * kStepTok * 128 + row * 128;
-              const int c0 = (2 * ch) & 7;
-              *reinterpret_cast<uint4*>(to + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             fence_async_smem();
             __syncwarp();
@@ -587,9 +599,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         const float f0 = ex2(top - base), f1 = ex2(other.x - base), tl = f0 * l + f1 * other.y;
         const float inv = pc.count > 1 ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
         const float g0 = f0 * inv, g1 = f1 * inv;
-        const long long out_at = (((long long)it.b * p.rows + rho / G) * p.a.Hq + it.hk * G + rho % G) * D;
         const long long part_at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + rho;
         if (ok && warp_live) {
+          // Through shared memory, 32 columns of the warp's rows at a time in chunks of 16 bytes whose order is turned by the
+          // row, so that rows are written in pieces of 128 (64) bytes.
+          uint4* mine = reinterpret_cast<uint4*>(staging + warp * 4096);
+          const unsigned rows_live = __ballot_sync(0xffffffffu, live);
+          const int rho0 = rho - lane;
 #pragma unroll 1
           for (int e = 0; e < D; e += 32) {
             uint32_t a[32], b[32];
@@ -605,19 +621,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
               v[d] = cnt > 0 ? __uint_as_float(a[d]) * g0 : 0.f;
               if (cnt > 1) v[d] = fmaf(__uint_as_float(b[d]), g1, v[d]);
             }
-            if (live) {
-              if (pc.count == 1) {
+            if (pc.count == 1) {
 #pragma unroll
-                for (int d = 0; d < 32; d += 8)
-                  *reinterpret_cast<uint4*>(p.out + out_at + e + d) =
-                      make_uint4(bf16x2(v[d], v[d + 1]), bf16x2(v[d + 2], v[d + 3]), bf16x2(v[d + 4], v[d + 5]),
-                                 bf16x2(v[d + 6], v[d + 7]));
-              } else {
+              for (int d = 0; d < 4; ++d)
+                mine[lane * 8 + (d ^ (lane & 7))] = make_uint4(bf16x2(v[8 * d], v[8 * d + 1]), bf16x2(v[8 * d + 2], v[8 * d + 3]),
+                                                               bf16x2(v[8 * d + 4], v[8 * d + 5]), bf16x2(v[8 * d + 6], v[8 * d + 7]));
+              __syncwarp();
 #pragma unroll
-                for (int d = 0; d < 32; d += 4)
-                  *reinterpret_cast<float4*>(p.part_o + part_at * D + e + d) = make_float4(v[d], v[d + 1], v[d + 2], v[d + 3]);
+              for (int j = 0; j < 4; ++j) {
+                const int r = j * 8 + lane / 4, ch = lane % 4, rr = rho0 + r;
+                if ((rows_live >> r) & 1u)
+                  *reinterpret_cast<uint4*>(p.out + (((long long)it.b * p.rows + rr / G) * p.a.Hq + it.hk * G + rr % G) * D +
+                                            e + ch * 8) = mine[r * 8 + (ch ^ (r & 7))];
+              }
+            } else {
+#pragma unroll
+              for (int d = 0; d < 8; ++d)
+                mine[lane * 8 + (d ^ (lane & 7))] = make_uint4(__float_as_uint(v[4 * d]), __float_as_uint(v[4 * d + 1]),
+                                                               __float_as_uint(v[4 * d + 2]), __float_as_uint(v[4 * d + 3]));
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int r = j * 4 + lane / 8, ch = lane % 8;
+                if ((rows_live >> r) & 1u)
+                  *reinterpret_cast<uint4*>(p.part_o + (part_at - lane + r) * D + e + ch * 4) = mine[r * 8 + (ch ^ (r & 7))];
               }
             }
+            __syncwarp();
           }
           if (live && pc.count > 1) *reinterpret_cast<float2*>(p.part_ml + part_at * 2) = make_float2(both, tl);
         }
