@@ -366,47 +366,59 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           if (C::MX) {
             if (tile >= C::ENTRIES && !(ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
             const uint8_t* src = raws + st * C::RAW;
-            constexpr int CH = D / 16;          // 16 codes at a time, four such a thread
-            const int ch = tid % CH, c0 = (2 * ch) & 7;
-            uint8_t* to = dst + (ch >> 2) * kStepTok * 128;
+            constexpr int CH = D / 16, RPT = 128 / CH;          // 16 codes at a time; rows of the tile a pass covers
+            const int ch = tid % CH, row0 = tid / CH;
+            // a thread's rows are RPT apart, a multiple of 8: their chunks are turned alike
+            const uint32_t from = smem_u32(src) + row0 * D + ch * 16, sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
+            const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 + ((((2 * ch) & 7) ^ (row0 & 7)) << 4);
+            static_assert(RPT % 8 == 0, "turned alike");
+            uint32_t top = 0;
 #pragma unroll 1
-            for (int r0 = tid / CH; r0 < kStepTok; r0 += 4 * 128 / CH) {
-              uint4 w[4];
-              uint32_t by[4];
+            for (int r = 0; r < kStepTok; r += 4 * RPT) {
+              uint32_t w[4][4], by[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int row = r0 + j * (128 / CH);
-                w[j] = *reinterpret_cast<const uint4*>(src + row * D + ch * 16);
-                by[j] = src[kStepTok * D + row * (D / 32) + ch / 2];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[j][0]), "=r"(w[j][1]), "=r"(w[j][2]), "=r"(w[j][3]) : "r"(from + (r + j * RPT) * D));
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(by[j]) : "r"(sc + (r + j * RPT) * (D / 32)));
               }
-              const bool large = __any_sync(0xffffffffu, max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int row = r0 + j * (128 / CH);
-                const uint32_t f = scale_bits(by[j]) * 0x10001u, ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                top = max(top, by[j]);
+                const uint32_t f = ((by[j] + 120u) << 7) * 0x10001u;
                 uint32_t o[8];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                  o[2 * b] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x1800), f);
-                  o[2 * b + 1] = mul_bf16x2(e4m3_pair(ws[b], ws[b], 0x3A22), f);
+                  o[2 * b] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], 0x1800), f);
+                  o[2 * b + 1] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], 0x3A22), f);
                 }
-                if (large) {
-                  const uint32_t f2 = scale_rest(by[j]) * 0x10001u;
-#pragma unroll
-                  for (int b = 0; b < 8; ++b) o[b] = mul_bf16x2(o[b], f2);
-                  if (edge) {                   // a value is not finite only where its scale is large
-                    bool bad = false;
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                      const uint32_t hit = ((o[b] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                      bad = bad || hit;
-                      o[b] &= ~((hit >> 15) * 0xFFFFu);
-                    }
-                    if (bad) list(info.x + row);
+                const uint32_t at = to + (r + j * RPT) * 128;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+              }
+            }
+            // Scales past what one factor holds (values from 57,344 on, and NaN): those chunks once more, in two factors. A
+            // value is not finite only there.
+            if (__any_sync(0xffffffffu, top > kScaleFits)) {
+#pragma unroll 1
+              for (int r = 0; r < kStepTok; r += RPT) {
+                const int row = row0 + r;
+                const uint32_t by = src[kStepTok * D + row * (D / 32) + ch / 2];
+                if (by <= kScaleFits) continue;
+                const uint32_t f = scale_bits(by) * 0x10001u, f2 = scale_rest(by) * 0x10001u;
+                bool bad = false;
+#pragma unroll 1
+                for (int b = 0; b < 8; ++b) {
+                  const uint32_t w = *reinterpret_cast<const uint32_t*>(src + row * D + ch * 16 + (b / 2) * 4);
+                  uint32_t o = mul_bf16x2(mul_bf16x2(e4m3_pair(w, w, b & 1 ? 0x3A22 : 0x1800), f), f2);
+                  const uint32_t hit = ((o & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  if (edge) {
+                    bad = bad || hit;
+                    o &= ~((hit >> 15) * 0xFFFFu);
                   }
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(((to + r * 128) ^ (b / 4 * 16)) + b % 4 * 4), "r"(o) : "memory");
                 }
-                *reinterpret_cast<uint4*>(to + row * 128 + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(to + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                if (bad) list(info.x + row);
               }
             }
             fence_async_smem();
