@@ -36,22 +36,69 @@ struct TcCfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = kStepTok * D * 2;                    // a step's keys, or values, in bf16; the queries
   static constexpr int RAW = MX ? (kStepTok * D + kStepTok * (D / 32) + 1023) / 1024 * 1024 : 0;
-  static constexpr int RAWS = !MX ? 1 : D == 128 ? 4 : 9;          // stages of raw codes
+  static constexpr int RAWS = !MX ? 1 : D == 128 ? 4 : 10;          // stages of raw codes
   static constexpr int ENTRIES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-  static constexpr int OUT = 4 * 4096;                             // the output's way to global memory, 4 KB a warp
-  static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + OUT + 1024;
-  static constexpr int THREADS = MX ? 512 : 384;
-  // registers: the block is launched with 128 (168) a thread; the two softmax warpgroups take what the others give up
-  static constexpr int MORE = MX ? 184 : 208, LESS = MX ? 72 : 88;
-  static constexpr int FEEDERS = MX ? 4 : 1;                       // warps that hand tiles to the products
+  static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + 1024;
+  static constexpr int THREADS = MX ? 640 : 384;
+  // registers: the block is launched with 96 (168) a thread; the two softmax warpgroups take what the others give up
+  static constexpr int MORE = MX ? 168 : 208, LESS = MX ? 48 : 88;
+  static constexpr int FEEDERS = MX ? 4 : 1;                       // warps that hand a tile to the products
+  static constexpr int GROUPS = MX ? 2 : 1;                        // of them, which take tiles in turn
   static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;   // Tensor Memory columns
+  static_assert(RAWS % GROUPS == 0, "a group of feeders sees every phase of its stages");
   static_assert(SMEM + 4096 <= 227 * 1024, "shared memory");
 };
 
-// Item `n` of a block, as it lies in shared memory.
+// Item `n` of a block, as it lies in shared memory: what the warps need of it, worked out once.
 struct PagedItem {
-  int b, hk, mb, piece, len, there;
+  int there, b, hk, rho0, live;                 // first row of the block, rows there are
+  int pos0;                                     // position of row 0 of the sequence's new rows
+  int pmax, first_any, sink_tiles, win_tile;
+  int i0, cnt, piece, pieces;                   // first step, steps; piece of how many
+  __device__ __forceinline__ int tok(int i) const {
+    const int t = i0 + i;
+    return (t < sink_tiles ? t : win_tile + (t - sink_tiles)) * kStepTok;
+  }
 };
+
+// One row's part of an item straight from the definition, by a warp: for rows that see a value that is not finite in a step
+// where others do not.
+template <int D, bool MX>
+__device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, int rho) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x % 32, G = p.a.Hq / p.a.Hkv, r = rho / G;
+  const Visible see(it.pos0 + r, p.a.window, p.a.sinks);
+  const long long row = ((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho % G;
+  LaneRow<D> q;
+  q.load_bf16(p.q + ((long long)it.b * p.rows + r) * p.q_stride + (long long)(it.hk * G + rho % G) * D, lane);
+  float m = -INFINITY, l = 0.f, o[N] = {};
+  for (int i = 0; i < it.cnt; ++i)
+    attend_keys<D>(q, see, it.tok(i), it.tok(i) + kStepTok, p.a.scale * 1.4426950408889634f, m, l, o,
+                   [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
+                     const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
+                     if (page < 0 || page >= p.pages) return false;
+                     const long long at = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) + (j & (p.page_size - 1));
+                     if (MX) {
+                       k.load_mxfp8(p.k + at * D, p.k_s + at * N, lane);
+                       v.load_mxfp8(p.v + at * D, p.v_s + at * N, lane);
+                     } else {
+                       k.load_bf16(reinterpret_cast<const uint16_t*>(p.k) + at * D, lane);
+                       v.load_bf16(reinterpret_cast<const uint16_t*>(p.v) + at * D, lane);
+                     }
+                     return true;
+                   });
+  if (it.pieces == 1) {
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * N);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
+  } else {
+    const int R = p.rows * G;
+    const long long at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + rho;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.part_o[at * D + lane * N + i] = o[i];
+    if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+  }
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -59,18 +106,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   constexpr int D = C::D;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t w_full[2], w_empty[2], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
-  __shared__ uint64_t chain1_there, chain1_read;
+  __shared__ uint64_t sums_there, outs_read;
   __shared__ uint64_t landed[C::MX ? C::RAWS : C::ENTRIES], raw_empty[C::RAWS], ready[C::ENTRIES], ent_empty[C::ENTRIES];
   __shared__ PagedItem items[2];
   __shared__ int4 infos[kInfos];                // of a step: first token, pages there, whether some row does not see a key
   __shared__ int listed_n[2], listed[2][kListed];
-  __shared__ float2 chain1_ml[kRowsM];
+  __shared__ float2 sums[2][kRowsM];            // the chains' maximum (times log2 e) and sum of a row
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = smem + C::TILE;
   uint8_t* raws = ring + C::ENTRIES * C::TILE;
-  uint8_t* staging = raws + (C::MX ? C::RAWS * C::RAW : 0);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   pdl_trigger();
@@ -78,11 +124,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
     mbar_init(&drain, 1);
-    mbar_init(&chain1_there, 128);
-    mbar_init(&chain1_read, 128);
+    mbar_init(&sums_there, 256);
+    mbar_init(&outs_read, 256);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 10 + C::FEEDERS);  // the warps of the products, of the queries, of the feeding, of the softmax
+      mbar_init(&w_empty[i], 10 + C::FEEDERS * C::GROUPS);  // the warps of the products, of the queries, of the feeding, of the softmax
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i][0], 128);
       mbar_init(&p_full[i][1], 128);
@@ -108,7 +154,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   pdl_wait();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPagedWaitNs, &abort_flag, p.status, code)) != 0;
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, kPagedWaitNs, &abort_flag, code)) != 0;
   };
   auto item_there = [&](int n) {
     return wait(&w_full[n & 1], (n >> 1) & 1, DEV_TIMEOUT_FULL) && items[n & 1].there != 0;
@@ -117,7 +163,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     __syncwarp();
     if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   };
-  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
   // An item's tiles pass in this order: K0 K1 V0 K2 V1 K3 V2 ..., one counter for all.
 
   if (warp >= 8) {
@@ -134,47 +179,75 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       // so that the ones that are there spread evenly over the blocks.
       for (long long c0 = blockIdx.x; ok && c0 < total; c0 += 32ll * gridDim.x) {
         const long long idx = c0 + (long long)lane * gridDim.x;
-        PagedItem mine{0, 0, 0, 0, 0, 0};
+        PagedItem mine{};
+        int first_all = 0, pmin = 0;
         if (idx < total) {
           int u = (int)(idx % units);
           mine.piece = (int)(idx / units);
           mine.hk = u % p.a.Hkv;
           u /= p.a.Hkv;
-          mine.mb = u % p.mblocks;
+          const int mb = u % p.mblocks;
           mine.b = u / p.mblocks;
-          mine.len = checked_len(p, mine.b, true);
-          mine.there = mine.piece < Pieces(p, mine.len, mine.mb).count;
+          const int len = checked_len(p, mine.b, true);
+          const Pieces pc(p, len, mb);
+          mine.there = mine.piece < pc.count;
+          mine.rho0 = mb * kRowsM;
+          mine.live = min(p.rows * (p.a.Hq / p.a.Hkv) - mine.rho0, kRowsM);
+          mine.pos0 = len - p.rows;
+          mine.pmax = pc.pmax, mine.first_any = pc.first_any;
+          mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
+          mine.i0 = mine.piece * pc.per;
+          mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+          mine.pieces = pc.count;
+          first_all = pc.first_all, pmin = pc.pmin;
         }
         for (unsigned some = __ballot_sync(0xffffffffu, mine.there != 0); ok && some; some &= some - 1) {
           const int who = __ffs(some) - 1;
-          PagedItem it;
-          it.b = __shfl_sync(0xffffffffu, mine.b, who);
-          it.hk = __shfl_sync(0xffffffffu, mine.hk, who);
-          it.mb = __shfl_sync(0xffffffffu, mine.mb, who);
-          it.piece = __shfl_sync(0xffffffffu, mine.piece, who);
-          it.len = __shfl_sync(0xffffffffu, mine.len, who);
-          it.there = 1;
           if (n >= 2 && !(ok = wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
-          if (lane == 0) {
-            items[n & 1] = it;
+          if (lane == who) {
+            items[n & 1] = mine;
             listed_n[n & 1] = 0;                // the last item but one, whose list this was, is done
-            mbar_arrive(&w_full[n & 1]);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&w_full[n & 1]);
+          const PagedItem it = items[n & 1];
+          const int all_from = __shfl_sync(0xffffffffu, first_all, who), all_to = __shfl_sync(0xffffffffu, pmin, who);
           ++n;
-          const Pieces pc(p, it.len, it.mb);
-          const int i0 = it.piece * pc.per, cnt = min(pc.tiles - i0, pc.per);
+          const int cnt = it.cnt;
           const int32_t* table = p.table + (long long)it.b * p.table_width;
-          const int last_page = pc.pmax >> p.page_log2;
+          const int last_page = it.pmax >> p.page_log2;
           int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
           int held[2] = {-1, -1};                    // page of this lane in the last two steps
-          auto load = [&](int i, bool is_v, int id) {
-            const int tok0 = pc.tile(i0 + i) * kStepTok, t0 = tok0 + lane * rows_of;
-            const int st = tile % (C::MX ? C::RAWS : C::ENTRIES), use = tile / (C::MX ? C::RAWS : C::ENTRIES);
+          for (int t = 0; t < 2 * cnt + 2; ++t) {    // the turns: K0 K1 V0 K2 V1 ...
+            const bool is_v = t >= 2 && !(t & 1);
+            const int i = t < 2 ? t : is_v ? (t - 2) / 2 : (t + 1) / 2;
+            if (i >= cnt) continue;
+            const int tok0 = it.tok(i), t0 = tok0 + lane * rows_of;
+            int id = i & 1 ? held[1] : held[0];
+            if (!is_v) {
+              const int page0 = tok0 >> p.page_log2;
+              if (page0 < base || page0 + in_tile > base + 32) {
+                const int nb = page0 & ~31;          // in_tile divides 32: a step's pages lie in one group of 32 entries
+                ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+                base = nb;
+                next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+              }
+              id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+              // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+              const bool want = lane < in_tile && t0 <= it.pmax &&
+                                (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, all_from));
+              const bool good = want && id >= 0 && id < p.pages;
+              if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+              id = good ? id : -1;
+              if (i & 1) held[1] = id; else held[0] = id;
+            }
+            constexpr int N = C::MX ? C::RAWS : C::ENTRIES;
+            const int st = tile % N, use = tile / N;
             const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
-            if (use > 0 && !(ok = wait(C::MX ? &raw_empty[st] : &ent_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
+            if (use > 0 && !(ok = wait(C::MX ? &raw_empty[st] : &ent_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
             if (lane == 0) {
               if (!is_v) {
-                const bool whole = tok0 + kStepTok - 1 <= pc.pmin && (tok0 >= pc.first_all || tok0 + kStepTok <= p.a.sinks) &&
+                const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks) &&
                                    mask == (1u << in_tile) - 1u;
                 infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
               }
@@ -196,33 +269,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
               }
             }
             ++tile;
-          };
-          auto load_k = [&](int i) {
-            const int tok0 = pc.tile(i0 + i) * kStepTok, page0 = tok0 >> p.page_log2;
-            if (page0 < base || page0 + in_tile > base + 32) {
-              const int nb = page0 & ~31;            // in_tile divides 32: a step's pages lie in one group of 32 entries
-              ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
-              base = nb;
-              next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
-            }
-            const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
-            // pages that no row sees are not loaded: past the end, or between the first tokens and the window
-            const int t0 = tok0 + lane * rows_of;
-            const bool want = lane < in_tile && t0 <= pc.pmax &&
-                              (t0 + rows_of > pc.first_any || t0 < min(p.a.sinks, pc.first_all));
-            const bool good = want && id >= 0 && id < p.pages;
-            if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-            const int got = good ? id : -1;
-            if (i & 1) held[1] = got; else held[0] = got;
-            load(i, false, got);
-          };
-          if (cnt > 0) load_k(0);
-          if (ok && cnt > 1) load_k(1);
-          for (int i = 0; ok && i < cnt; ++i) {
-            load(i, true, i & 1 ? held[1] : held[0]);
-            if (ok && i + 2 < cnt) load_k(i + 2);
           }
-          steps += max(cnt, 0);
+          steps += cnt;
         }
       }
       // no more items
@@ -273,11 +321,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       };
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
-        const PagedItem it = items[n & 1];
+        const int cnt = items[n & 1].cnt;
         item_done(n);
-        const Pieces pc(p, it.len, it.mb);
-        const int cnt = min(pc.tiles - it.piece * pc.per, pc.per);
-        if (cnt <= 0) continue;
+        if (cnt == 0) continue;
         if (!(ok = wait(&q_full, qs & 1, DEV_TIMEOUT_FULL))) break;
         ++qs;
         tc_fence_after();
@@ -321,18 +367,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       int qs = 0;
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
-        const PagedItem it = items[n & 1];
-        const Pieces pc(p, it.len, it.mb);
-        if (min(pc.tiles - it.piece * pc.per, pc.per) > 0) {
+        const PagedItem& it = items[n & 1];
+        if (it.cnt > 0) {
           if (qs > 0 && !(ok = wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
           ++qs;
-          const int live = min(R - it.mb * kRowsM, kRowsM);
-#pragma unroll 4
-          for (int e = lane; e < live * (D / 8); e += 32) {
-            const int row = e / (D / 8), ch = e % (D / 8), rho = it.mb * kRowsM + row;
-            const uint4 v = *reinterpret_cast<const uint4*>(p.q + ((long long)it.b * p.rows + rho / G) * p.q_stride +
-                                                            (long long)(it.hk * G + rho % G) * D + ch * 8);
-            *reinterpret_cast<uint4*>(smem + (ch >> 3) * kRowsM * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+          const int G = p.a.Hq / p.a.Hkv;
+          // a scale below zero turns the queries' sign instead
+          const uint32_t turn = p.a.scale < 0.f ? 0x80008000u : 0u;
+          const uint16_t* q = p.q + (long long)it.b * p.rows * p.q_stride + (long long)it.hk * G * D;
+          constexpr int CH = D / 8, RPW = 32 / CH;  // chunks of 16 bytes of a row, rows at a time
+          const int ch = lane % CH, live = it.live;
+          int row = lane / CH, r = (it.rho0 + row) / G, h = it.rho0 + row - r * G;
+          for (int base = 0; base < live; base += 8 * RPW) {
+            uint4 v[8];
+            int at = row;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              v[j] = row < live ? *reinterpret_cast<const uint4*>(q + r * p.q_stride + h * D + ch * 8) : make_uint4(0, 0, 0, 0);
+              row += RPW;
+              h += RPW;
+              while (h >= G) h -= G, ++r;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j, at += RPW)
+              if (at < live) {
+                v[j].x ^= turn, v[j].y ^= turn, v[j].z ^= turn, v[j].w ^= turn;
+                *reinterpret_cast<uint4*>(smem + (ch >> 3) * kRowsM * 128 + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = v[j];
+              }
           }
           fence_async_smem();
           __syncwarp();
@@ -345,20 +406,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       // Hands every tile to the products, MXFP8 converted. In steps where some row does not see a key, values that are not
       // finite become zero (a weight of zero would not hide them), and those that some row sees are listed: rows that see
       // them are computed again.
-      const int tid = C::MX ? threadIdx.x - 384 : lane;
+      const int tid = C::MX ? threadIdx.x % 128 : lane, group = C::MX ? warp / 4 - 3 : 0;
       int tile = 0, steps = 0;
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
-        const PagedItem it = items[n & 1];
-        const Pieces pc(p, it.len, it.mb);
-        const int cnt = min(pc.tiles - it.piece * pc.per, pc.per);
+        const int cnt = items[n & 1].cnt, pmax = items[n & 1].pmax, first_any = items[n & 1].first_any;
         auto list = [&](int tok) {
-          if (tok > pc.pmax || (tok < pc.first_any && tok >= p.a.sinks)) return;
+          if (tok > pmax || (tok < first_any && tok >= p.a.sinks)) return;
           const int at = atomicAdd(&listed_n[n & 1], 1);
           if (at < kListed) listed[n & 1][at] = tok;
         };
         auto feed = [&](int i, bool is_v) {
           const int e = tile % C::ENTRIES, st = C::MX ? tile % C::RAWS : e;
+          if (tile % C::GROUPS != group) {      // the other group's; its entry's phase passes here too
+            if (tile >= C::ENTRIES) ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY);
+            ++tile;
+            return;
+          }
           if (!(ok = wait(&landed[st], (tile / (C::MX ? C::RAWS : C::ENTRIES)) & 1, DEV_TIMEOUT_FULL))) return;
           const int4 info = infos[(steps + i) % kInfos];
           const bool edge = is_v && info.z != 0;
@@ -462,13 +526,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           if (lane == 0) mbar_arrive(&ready[e]);
           ++tile;
         };
-        if (cnt > 0) feed(0, false);
-        if (ok && cnt > 1) feed(1, false);
-        for (int i = 0; ok && i < cnt; ++i) {
-          feed(i, true);
-          if (ok && i + 2 < cnt) feed(i + 2, false);
+        // one call for all: K0 K1 V0 K2 V1 ... are the turns 0 1 2 3 4 ...; the last but one turn has no K
+        for (int t = 0; ok && t < 2 * cnt + 2; ++t) {
+          const bool is_v = t >= 2 && !(t & 1);
+          const int i = t < 2 ? t : is_v ? (t - 2) / 2 : (t + 1) / 2;
+          if (i < cnt) feed(i, is_v);
         }
-        steps += max(cnt, 0);
+        steps += cnt;
         item_done(n);
       }
     }
@@ -478,24 +542,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     const int x = warp / 4, row = threadIdx.x % 128;
     const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
     const uint32_t ts = tmem + (x ? C::S1 : C::S0) + lanes, to = tmem + (x ? C::O1 : C::O0) + lanes;
-    // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
-    const uint32_t turn = p.a.scale < 0.f ? 0x80000000u : 0u;
+    // scores in units of log2 e / scale; a scale of zero becomes one that tells none apart
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
     const uint64_t c2 = pack2(c, c);
     int done = 0, steps = 0;                    // steps of this chain, and of all, so far
     bool ok = true;
     for (int n = 0; ok && item_there(n); ++n) {
-      int cnt, pos, first;
-      bool warp_live;
-      {
-        const PagedItem it = items[n & 1];
-        const Pieces pc(p, it.len, it.mb);
-        cnt = max(0, min(pc.tiles - it.piece * pc.per, pc.per));
-        const int rho = it.mb * kRowsM + row;
-        pos = rho < R ? it.len - p.rows + rho / G : -1;
-        first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
-        warp_live = __any_sync(0xffffffffu, rho < R);
-      }
+      const int cnt = items[n & 1].cnt;
+      const bool live = row < items[n & 1].live, warp_live = __any_sync(0xffffffffu, live);
+      const int pos = live ? items[n & 1].pos0 + (items[n & 1].rho0 + row) / (p.a.Hq / p.a.Hkv) : -1;
+      const int first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
       float m = -INFINITY;                      // the maximum that the weights so far refer to
       uint64_t l2 = pack2(0.f, 0.f);
       bool any = false;                         // a step of this chain
@@ -509,30 +565,34 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           continue;
         }
         const int4 info = infos[(steps + i) % kInfos];
+        if (info.z) {
+          // Hidden in Tensor Memory, 32 scores at a time: little code, and groups that all of the warp's rows see are left.
+          // The row sees token info.x + e when e <= hi and (e >= lo or e < low), and its page is there.
+          const int hi = pos - info.x, lo = first - info.x, low = p.a.sinks - info.x;
+          const uint32_t pages = (uint32_t)info.y;
+          auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
+#pragma unroll 1
+          for (int e = 0; e < kStepTok; e += 32) {
+            uint32_t see = below(hi + 1 - e) & (~below(lo - e) | below(low - e));
+            for (int d = 0; d < 32; d += 8)     // a page has at least 8 tokens
+              if (!((pages >> ((e + d) >> min(p.page_log2, 7))) & 1u)) see &= ~(0xFFu << d);
+            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+            uint32_t s[32];
+            tmem_ld32(ts + e, s, 0);
+            tmem_ld_wait();
+            reg_fence32(s, 0);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) s[d] = (see >> d) & 1u ? s[d] : 0xff800000u;
+            tmem_st32(ts + e, s, 0);
+          }
+          tmem_st_wait();
+        }
         uint32_t s[128];
 #pragma unroll
         for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
-        if (turn) {
-#pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] ^= turn;
-        }
-        if (info.z) {
-          const int hi = pos - info.x, lo = first - info.x, low = p.a.sinks - info.x;
-#pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] = e <= hi && (e >= lo || e < low) ? s[e] : 0xff800000u;
-          const int in_tile = p.page_size >= kStepTok ? 1 : kStepTok >> p.page_log2;
-          if ((unsigned)info.y != (1u << in_tile) - 1u) {
-#pragma unroll
-            for (int e = 0; e < 128; e += 8)    // a page has at least 8 tokens
-              if (!(((unsigned)info.y >> (e >> min(p.page_log2, 7))) & 1u)) {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) s[e + d] = 0xff800000u;
-              }
-          }
-        }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 128; e += 8)
@@ -595,126 +655,77 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       unpack2(l2, la, lb);
       const float l = la + lb, top = m == -INFINITY ? -INFINITY : m * c;
 
-      // ---- the chains joined, by the first one's warps: both have the same rows in the same lanes ----
-      if (x == 1) chain1_ml[row] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
+      // ---- the chains joined: both have the same rows in the same lanes, and each takes half of the columns ----
+      sums[x][row] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
       tc_fence_before();
-      if (x == 1) mbar_arrive(&chain1_there);
-      if (x == 0) {
-        ok = wait(&chain1_there, n & 1, DEV_TIMEOUT_ACCUM) && ok;
-        tc_fence_after();
-        const PagedItem it = items[n & 1];
-        const Pieces pc(p, it.len, it.mb);
-        const int rho = it.mb * kRowsM + row;
-        const bool live = rho < R;
-        const float2 other = chain1_ml[row];
-        const float both = fmaxf(top, other.x), base = both == -INFINITY ? 0.f : both;
-        const float f0 = ex2(top - base), f1 = ex2(other.x - base), tl = f0 * l + f1 * other.y;
-        const float inv = pc.count > 1 ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
+      mbar_arrive(&sums_there);
+      ok = wait(&sums_there, n & 1, DEV_TIMEOUT_ACCUM) && ok;
+      tc_fence_after();
+      const PagedItem& it = items[n & 1];
+      const int G = p.a.Hq / p.a.Hkv, rho = it.rho0 + row, r = rho / G;
+      const float2 s0 = sums[0][row], s1 = sums[1][row];
+      const float both = fmaxf(s0.x, s1.x), base = both == -INFINITY ? 0.f : both;
+      const float f0 = ex2(s0.x - base), f1 = ex2(s1.x - base), tl = f0 * s0.y + f1 * s1.y;
+      if (ok && warp_live) {
+        const bool one = it.pieces == 1;
+        const float inv = !one ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
         const float g0 = f0 * inv, g1 = f1 * inv;
-        const long long part_at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + rho;
-        if (ok && warp_live) {
-          // Through shared memory, 32 columns of the warp's rows at a time in chunks of 16 bytes whose order is turned by the
-          // row, so that rows are written in pieces of 128 (64) bytes.
-          uint4* mine = reinterpret_cast<uint4*>(staging + warp * 4096);
-          const unsigned rows_live = __ballot_sync(0xffffffffu, live);
-          const int rho0 = rho - lane;
+        const long long part_at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * p.rows * G + rho;
+        uint16_t* out = p.out + (((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho - r * G) * D;
+        const uint32_t o0 = tmem + C::O0 + lanes, o1 = tmem + C::O1 + lanes;
 #pragma unroll 1
-          for (int e = 0; e < D; e += 32) {
-            uint32_t a[32], b[32];
-            tmem_ld32(to + e, a, 0);
-            tmem_ld32(to + C::O1 - C::O0 + e, b, 0);
-            tmem_ld_wait();
-            reg_fence32(a, 0);
-            reg_fence32(b, 0);
-            float v[32];
+        for (int e = x * (D / 2); e < (x + 1) * (D / 2); e += 32) {
+          uint32_t a[32], b[32];
+          tmem_ld32(o0 + e, a, 0);
+          tmem_ld32(o1 + e, b, 0);
+          tmem_ld_wait();
+          reg_fence32(a, 0);
+          reg_fence32(b, 0);
+          // a chain without steps has no output: what is there is nobody's
+          if (cnt < 2) {
 #pragma unroll
-            for (int d = 0; d < 32; ++d) {
-              // a chain without steps has no output: what is there is nobody's
-              v[d] = cnt > 0 ? __uint_as_float(a[d]) * g0 : 0.f;
-              if (cnt > 1) v[d] = fmaf(__uint_as_float(b[d]), g1, v[d]);
-            }
-            if (pc.count == 1) {
+            for (int d = 0; d < 32; ++d) b[d] = 0;
+          }
+          if (cnt < 1) {
 #pragma unroll
-              for (int d = 0; d < 4; ++d)
-                mine[lane * 8 + (d ^ (lane & 7))] = make_uint4(bf16x2(v[8 * d], v[8 * d + 1]), bf16x2(v[8 * d + 2], v[8 * d + 3]),
-                                                               bf16x2(v[8 * d + 4], v[8 * d + 5]), bf16x2(v[8 * d + 6], v[8 * d + 7]));
-              __syncwarp();
+            for (int d = 0; d < 32; ++d) a[d] = 0;
+          }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int r = j * 8 + lane / 4, ch = lane % 4, rr = rho0 + r;
-                if ((rows_live >> r) & 1u)
-                  *reinterpret_cast<uint4*>(p.out + (((long long)it.b * p.rows + rr / G) * p.a.Hq + it.hk * G + rr % G) * D +
-                                            e + ch * 8) = mine[r * 8 + (ch ^ (r & 7))];
+          for (int d = 0; d < 32; ++d)
+            a[d] = __float_as_uint(fmaf(__uint_as_float(b[d]), g1, __uint_as_float(a[d]) * g0));
+          if (live) {
+            if (one) {
+#pragma unroll
+              for (int d = 0; d < 32; d += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                  w[f] = bf16x2(__uint_as_float(a[d + 2 * f]), __uint_as_float(a[d + 2 * f + 1]));
+                *reinterpret_cast<uint4*>(out + e + d) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             } else {
 #pragma unroll
-              for (int d = 0; d < 8; ++d)
-                mine[lane * 8 + (d ^ (lane & 7))] = make_uint4(__float_as_uint(v[4 * d]), __float_as_uint(v[4 * d + 1]),
-                                                               __float_as_uint(v[4 * d + 2]), __float_as_uint(v[4 * d + 3]));
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int r = j * 4 + lane / 8, ch = lane % 8;
-                if ((rows_live >> r) & 1u)
-                  *reinterpret_cast<uint4*>(p.part_o + (part_at - lane + r) * D + e + ch * 4) = mine[r * 8 + (ch ^ (r & 7))];
-              }
+              for (int d = 0; d < 32; d += 4)
+                *reinterpret_cast<uint4*>(p.part_o + part_at * D + e + d) = make_uint4(a[d], a[d + 1], a[d + 2], a[d + 3]);
             }
-            __syncwarp();
           }
-          if (live && pc.count > 1) *reinterpret_cast<float2*>(p.part_ml + part_at * 2) = make_float2(both, tl);
         }
-        tc_fence_before();
-        mbar_arrive(&chain1_read);              // the second chain may go on
+        if (x == 0 && live && !one) *reinterpret_cast<float2*>(p.part_ml + part_at * 2) = make_float2(both, tl);
+      }
+      tc_fence_before();
+      mbar_arrive(&outs_read);                  // the next item's products may write there
+      ok = wait(&outs_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;
+      tc_fence_after();
 
-        // ---- rows that see a listed key, from the definition ----
-        if (ok && cnt > 0) {
-          const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
-          bool again = some > kListed;
-          const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
-          for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
-          again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
-          for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1) {
-            constexpr int N = D / 32;
-            const int r2 = __shfl_sync(0xffffffffu, rho, __ffs(rows) - 1);
-            const Visible see2(it.len - p.rows + r2 / G, p.a.window, p.a.sinks);
-            LaneRow<D> q;
-            q.load_bf16(p.q + ((long long)it.b * p.rows + r2 / G) * p.q_stride + (long long)(it.hk * G + r2 % G) * D, lane);
-            float m2 = -INFINITY, s2 = 0.f, o[N] = {};
-            const int t0 = it.piece * pc.per;
-            for (int i = 0; i < cnt; ++i) {
-              const int tok0 = pc.tile(t0 + i) * kStepTok;
-              attend_keys<D>(q, see2, tok0, tok0 + kStepTok, p.a.scale * 1.4426950408889634f, m2, s2, o,
-                             [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
-                               const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
-                               if (page < 0 || page >= p.pages) return false;
-                               const long long at = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) +
-                                                    (j & (p.page_size - 1));
-                               if (C::MX) {
-                                 k.load_mxfp8(p.k + at * D, p.k_s + at * N, lane);
-                                 v.load_mxfp8(p.v + at * D, p.v_s + at * N, lane);
-                               } else {
-                                 k.load_bf16(reinterpret_cast<const uint16_t*>(p.k) + at * D, lane);
-                                 v.load_bf16(reinterpret_cast<const uint16_t*>(p.v) + at * D, lane);
-                               }
-                               return true;
-                             });
-            }
-            if (pc.count == 1) {
-              uint32_t* out = reinterpret_cast<uint32_t*>(
-                  p.out + (((long long)it.b * p.rows + r2 / G) * p.a.Hq + it.hk * G + r2 % G) * D + lane * N);
-#pragma unroll
-              for (int i = 0; i < N / 2; ++i) out[i] = s2 == 0.f ? 0u : bf16x2(o[2 * i] / s2, o[2 * i + 1] / s2);
-            } else {
-              const long long at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + r2;
-#pragma unroll
-              for (int i = 0; i < N; ++i) p.part_o[at * D + lane * N + i] = o[i];
-              if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m2, s2);
-            }
-          }
-        }
-      } else {
-        ok = wait(&chain1_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;
-        tc_fence_after();
+      // ---- rows that see a listed key, from the definition ----
+      if (x == 0 && ok && cnt > 0) {
+        const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
+        bool again = some > kListed;
+        const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
+        for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
+        again = again && live && tl == tl;      // a score that is NaN makes the sum NaN, and with it the row
+        for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
+          redo_part<D, C::MX>(p, it, rho - lane + __ffs(rows) - 1);
       }
       item_done(n);
     }
@@ -724,6 +735,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && abort_flag) atomicCAS(p.status, 0u, abort_flag);
 }
 
 template <int D, bool MX>
