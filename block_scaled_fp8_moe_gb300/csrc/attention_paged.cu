@@ -423,8 +423,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   named_bar_sync(1, C::WARPS * 32);
   if (abort_flag) return;
   for (int x = threadIdx.x; x < kFewRows * (D / 4); x += C::WARPS * 32) {
-    const int rho = x / (D / 4), d = x % (D / 4) * 4;
-    if (rho >= R) break;
+    const int rho = x % kFewRows, d = x / kFewRows * 4;
+    if (rho >= R) continue;
     float top = -INFINITY, tl = 0.f;
     float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -448,63 +448,48 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
       *reinterpret_cast<uint2*>(p.out + at) =
           none ? make_uint2(0, 0) : make_uint2(bf16x2(to.x * inv, to.y * inv), bf16x2(to.z * inv, to.w * inv));
     } else {
-      const long long at = ((b * p.a.Hkv + hk) * p.max_pieces + piece) * R + rho;
-      *reinterpret_cast<float4*>(p.part_o + at * D + d) = to;
-      if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top, tl);
+      const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
+      *reinterpret_cast<float4*>(part_of(p, at, D, rho, d / 4)) = to;
+      if (d == 0) *sums_of(p, at, rho) = make_float2(top, tl);
     }
   }
 }
 
-// One warp per row: the pieces' parts joined in order. Rows of one piece are already written.
+// The pieces' parts joined in order, a thread per four columns of a row, rows next to each other. Rows of one piece are
+// already written.
+constexpr int kJoinRows = 8;            // rows of a block ...
+constexpr int kJoinCols = 16;           // ... and groups of four columns
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs p) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const PagedArgs p) {
   const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
-  const long long x = (long long)blockIdx.x * 4 + threadIdx.x / 32;
+  const int row_blocks = (R + kJoinRows - 1) / kJoinRows;
+  const unsigned unit = blockIdx.x / row_blocks;
+  const int rho = (int)(blockIdx.x % row_blocks) * kJoinRows + threadIdx.x % kJoinRows;
+  const int d4 = blockIdx.y * kJoinCols + threadIdx.x / kJoinRows, hk = (int)(unit % p.a.Hkv);
+  const long long b = unit / p.a.Hkv;
   pdl_wait();
-  if (x >= (long long)p.a.B * p.a.Hkv * R) return;
-  const int rho = (int)(x % R), hk = (int)(x / R % p.a.Hkv);
-  const long long b = x / R / p.a.Hkv;
+  if (rho >= R) return;
   const Pieces pc(p, checked_len(p, b, false), rho / p.block_rows);
   if (pc.count == 1) return;
-  const long long at = (b * p.a.Hkv + hk) * p.max_pieces * R + rho;
-  static_assert(kMaxPieces == 64, "two pieces a lane");
-  float w[2], ls[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 32 * h;
-    const float2 v = i < pc.count ? *reinterpret_cast<const float2*>(p.part_ml + (at + (long long)i * R) * 2)
-                                  : make_float2(-INFINITY, 0.f);
-    w[h] = v.x;
-    ls[h] = v.y;
-  }
-  float top = fmaxf(w[0], w[1]);
-#pragma unroll
-  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  const long long at = (b * p.a.Hkv + hk) * p.max_pieces;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < pc.count; ++i) top = fmaxf(top, sums_of(p, at + i, rho)->x);
   const float base = top == -INFINITY ? 0.f : top;
-  w[0] = ex2(w[0] - base);
-  w[1] = ex2(w[1] - base);
-  float tl = w[0] * ls[0] + w[1] * ls[1];
-#pragma unroll
-  for (int s = 16; s; s >>= 1) tl += __shfl_xor_sync(0xffffffffu, tl, s);
-  float o[N] = {};
-#pragma unroll 4
+  float tl = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
   for (int i = 0; i < pc.count; ++i) {
-    const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
-    const float* v = p.part_o + (at + (long long)i * R) * D + lane * N;
-    if constexpr (N == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(v);
-      o[0] = fmaf(f, t.x, o[0]), o[1] = fmaf(f, t.y, o[1]), o[2] = fmaf(f, t.z, o[2]), o[3] = fmaf(f, t.w, o[3]);
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(v);
-      o[0] = fmaf(f, t.x, o[0]), o[1] = fmaf(f, t.y, o[1]);
-    }
+    const float2 s = *sums_of(p, at + i, rho);
+    const float4 v = *reinterpret_cast<const float4*>(part_of(p, at + i, D, rho, d4));
+    const float f = ex2(s.x - base);
+    tl = fmaf(f, s.y, tl);
+    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
   }
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + lane * N);
   const float inv = 1.f / tl;
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) out[i] = tl == 0.f ? 0u : bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  *reinterpret_cast<uint2*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d4 * 4) =
+      tl == 0.f ? make_uint2(0, 0) : make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
 }
 
 // Blocks of up to 16 rows take steps of 64 tokens, more rows steps of 128.
@@ -555,9 +540,10 @@ static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStrea
   else if (d64) rc = mx ? launch_few<64, true>(p, cache, st) : launch_few<64, false>(p, cache, st);
   else rc = mx ? launch_few<128, true>(p, cache, st) : launch_few<128, false>(p, cache, st);
   if (rc || p.max_pieces == 1) return rc;
-  const long long out_rows = (long long)p.a.B * p.a.Hq * p.rows;
-  return launch_pdl(d64 ? paged_join_kernel<64> : paged_join_kernel<128>, dim3((unsigned)((out_rows + 3) / 4)), dim3(128),
-                    0, st, p);
+  const int R = p.rows * (p.a.Hq / p.a.Hkv);
+  return launch_pdl(d64 ? paged_join_kernel<64> : paged_join_kernel<128>,
+                    dim3((unsigned)(ceil_div(R, kJoinRows) * p.a.B * p.a.Hkv), (unsigned)(p.a.D / 4 / kJoinCols)),
+                    dim3(kJoinRows * kJoinCols), 0, st, p);
 }
 
 }  // namespace moe
@@ -601,7 +587,10 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.block_rows = p.tile == kTileTok ? kFewRows : 128;
   p.mblocks = ceil_div(rows * (a->Hq / a->Hkv), p.block_rows);
   p.max_pieces = max_pieces_of(a, rows, max_len);
-  if ((int64_t)a->B * p.mblocks * a->Hkv * p.max_pieces >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // grids and the numbers of pieces stay below 2^31
+  if ((int64_t)a->B * a->Hkv * std::max((int64_t)p.mblocks * p.max_pieces, (int64_t)ceil_div(rows * (a->Hq / a->Hkv), kJoinRows)) >=
+      (int64_t)1 << 31)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   p.q = q;
   p.q_stride = q_stride;
   p.table = block_table;

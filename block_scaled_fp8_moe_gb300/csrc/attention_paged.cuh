@@ -28,9 +28,19 @@ struct PagedArgs {
   const int32_t* lens;
   uint16_t* out;
   uint32_t* status;
-  float* part_o;    // [B, Hkv, max_pieces, R, D]: sums of weighted values
+  // Partial results of pieces. Rows are next to each other, because threads of a warp have rows of their own where they are
+  // written and where they are joined.
+  float* part_o;    // [B, Hkv, max_pieces, D / 4, R, 4]: sums of weighted values
   float* part_ml;   // [B, Hkv, max_pieces, R, 2]: running maximum (times log2 e) and sum
 };
+
+// Four columns of row rho's sums, and its maximum and sum, in piece `at` (of all).
+__device__ __forceinline__ float* part_of(const PagedArgs& p, long long at, int D, int rho, int d4) {
+  return p.part_o + ((at * (D / 4) + d4) * (p.rows * (p.a.Hq / p.a.Hkv)) + rho) * 4;
+}
+__device__ __forceinline__ float2* sums_of(const PagedArgs& p, long long at, int rho) {
+  return reinterpret_cast<float2*>(p.part_ml) + at * (p.rows * (p.a.Hq / p.a.Hkv)) + rho;
+}
 
 // Steps of a piece. Steps of 64 tokens (few rows, several small blocks a multiprocessor): at least 8 of them, and at most
 // 64 pieces. Steps of 128 (one block a multiprocessor): at least 4, 8 from 8192 tokens on, and at most 32 pieces; shorter

@@ -61,10 +61,10 @@ struct PagedItem {
   }
 };
 
-// One row's part of an item straight from the definition, by a warp: for rows that see a value that is not finite in a step
-// where others do not.
+// One row's part of an item straight from the definition, by a warp, which writes one half of its columns: for rows that see a
+// value that is not finite in a step where others do not.
 template <int D, bool MX>
-__device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, int rho) {
+__device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, int rho, int half) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, G = p.a.Hq / p.a.Hkv, r = rho / G;
   const Visible see(it.pos0 + r, p.a.window, p.a.sinks);
@@ -87,16 +87,18 @@ __device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, 
                      }
                      return true;
                    });
+  const bool mine = lane / 16 == half;
   if (it.pieces == 1) {
     uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * N);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
+    for (int i = 0; i < N / 2; ++i)
+      if (mine) out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
   } else {
-    const int R = p.rows * G;
-    const long long at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * R + rho;
+    const long long at = ((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece;
 #pragma unroll
-    for (int i = 0; i < N; ++i) p.part_o[at * D + lane * N + i] = o[i];
-    if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+    for (int i = 0; i < N; ++i)
+      if (mine) part_of(p, at, D, rho, (lane * N + i) / 4)[(lane * N + i) % 4] = o[i];
+    if (half == 0 && lane == 0) *sums_of(p, at, rho) = make_float2(m, l);
   }
 }
 
@@ -377,23 +379,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           const uint16_t* q = p.q + (long long)it.b * p.rows * p.q_stride + (long long)it.hk * G * D;
           constexpr int CH = D / 8, RPW = 32 / CH;  // chunks of 16 bytes of a row, rows at a time
           const int ch = lane % CH, live = it.live;
-          int row = lane / CH, r = (it.rho0 + row) / G, h = it.rho0 + row - r * G;
-          for (int base = 0; base < live; base += 8 * RPW) {
-            uint4 v[8];
-            int at = row;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              v[j] = row < live ? *reinterpret_cast<const uint4*>(q + r * p.q_stride + h * D + ch * 8) : make_uint4(0, 0, 0, 0);
-              row += RPW;
-              h += RPW;
-              while (h >= G) h -= G, ++r;
+          int r = (it.rho0 + lane / CH) / G, h = it.rho0 + lane / CH - r * G;
+          uint8_t* dst = smem + (ch >> 3) * kRowsM * 128;
+#pragma unroll 2
+          for (int row = lane / CH; row < live; row += RPW) {
+            cp_async_16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q + r * p.q_stride + h * D + ch * 8, 16);
+            h += RPW;
+            while (h >= G) h -= G, ++r;
+          }
+          cp_async_wait_all();
+          if (turn) {
+            for (int row = lane / CH; row < live; row += RPW) {
+              uint4* v = reinterpret_cast<uint4*>(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+              *v = make_uint4(v->x ^ turn, v->y ^ turn, v->z ^ turn, v->w ^ turn);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j, at += RPW)
-              if (at < live) {
-                v[j].x ^= turn, v[j].y ^= turn, v[j].z ^= turn, v[j].w ^= turn;
-                *reinterpret_cast<uint4*>(smem + (ch >> 3) * kRowsM * 128 + at * 128 + (((ch & 7) ^ (at & 7)) << 4)) = v[j];
-              }
           }
           fence_async_smem();
           __syncwarp();
@@ -666,67 +665,70 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       const float2 s0 = sums[0][row], s1 = sums[1][row];
       const float both = fmaxf(s0.x, s1.x), base = both == -INFINITY ? 0.f : both;
       const float f0 = ex2(s0.x - base), f1 = ex2(s1.x - base), tl = f0 * s0.y + f1 * s1.y;
-      if (ok && warp_live) {
-        const bool one = it.pieces == 1;
-        const float inv = !one ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
-        const float g0 = f0 * inv, g1 = f1 * inv;
-        const long long part_at = (((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece) * p.rows * G + rho;
-        uint16_t* out = p.out + (((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho - r * G) * D;
-        const uint32_t o0 = tmem + C::O0 + lanes, o1 = tmem + C::O1 + lanes;
-#pragma unroll 1
-        for (int e = x * (D / 2); e < (x + 1) * (D / 2); e += 32) {
-          uint32_t a[32], b[32];
-          tmem_ld32(o0 + e, a, 0);
-          tmem_ld32(o1 + e, b, 0);
-          tmem_ld_wait();
-          reg_fence32(a, 0);
-          reg_fence32(b, 0);
-          // a chain without steps has no output: what is there is nobody's
-          if (cnt < 2) {
+      const int e0 = x * (D / 2);
+      uint32_t a[D / 2], b[D / 2];
 #pragma unroll
-            for (int d = 0; d < 32; ++d) b[d] = 0;
-          }
-          if (cnt < 1) {
+      for (int e = 0; e < D / 2; e += 32) {
+        tmem_ld32(tmem + C::O0 + lanes + e0 + e, a, e);
+        tmem_ld32(tmem + C::O1 + lanes + e0 + e, b, e);
+      }
+      tmem_ld_wait();
 #pragma unroll
-            for (int d = 0; d < 32; ++d) a[d] = 0;
-          }
-#pragma unroll
-          for (int d = 0; d < 32; ++d)
-            a[d] = __float_as_uint(fmaf(__uint_as_float(b[d]), g1, __uint_as_float(a[d]) * g0));
-          if (live) {
-            if (one) {
-#pragma unroll
-              for (int d = 0; d < 32; d += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                  w[f] = bf16x2(__uint_as_float(a[d + 2 * f]), __uint_as_float(a[d + 2 * f + 1]));
-                *reinterpret_cast<uint4*>(out + e + d) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-#pragma unroll
-              for (int d = 0; d < 32; d += 4)
-                *reinterpret_cast<uint4*>(p.part_o + part_at * D + e + d) = make_uint4(a[d], a[d + 1], a[d + 2], a[d + 3]);
-            }
-          }
-        }
-        if (x == 0 && live && !one) *reinterpret_cast<float2*>(p.part_ml + part_at * 2) = make_float2(both, tl);
+      for (int e = 0; e < D / 2; e += 32) {
+        reg_fence32(a, e);
+        reg_fence32(b, e);
       }
       tc_fence_before();
       mbar_arrive(&outs_read);                  // the next item's products may write there
+      if (ok && live) {
+        const bool one = it.pieces == 1;
+        const float inv = !one ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
+        const float g0 = f0 * inv, g1 = f1 * inv;
+        // a chain without steps has no output: what is there is nobody's
+        if (cnt < 2) {
+#pragma unroll
+          for (int d = 0; d < D / 2; ++d) b[d] = 0;
+        }
+        if (cnt < 1) {
+#pragma unroll
+          for (int d = 0; d < D / 2; ++d) a[d] = 0;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 2; ++d)
+          a[d] = __float_as_uint(fmaf(__uint_as_float(b[d]), g1, __uint_as_float(a[d]) * g0));
+        if (one) {
+          uint16_t* out = p.out + (((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho - r * G) * D + e0;
+#pragma unroll
+          for (int d = 0; d < D / 2; d += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) w[f] = bf16x2(__uint_as_float(a[d + 2 * f]), __uint_as_float(a[d + 2 * f + 1]));
+            *reinterpret_cast<uint4*>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          const long long at = ((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece;
+          float* part = part_of(p, at, D, rho, e0 / 4);
+          const long long next = (long long)p.rows * G * 4;
+#pragma unroll
+          for (int d = 0; d < D / 2; d += 4)
+            *reinterpret_cast<uint4*>(part + d / 4 * next) = make_uint4(a[d], a[d + 1], a[d + 2], a[d + 3]);
+          if (x == 0) *sums_of(p, at, rho) = make_float2(both, tl);
+        }
+      }
+      // ---- rows that see a listed key, from the definition: each chain's warps their half of the columns ----
+      if (ok && cnt > 0) {
+        const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
+        if (some) {
+          bool again = some > kListed;
+          const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
+          for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
+          again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
+          for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
+            redo_part<D, C::MX>(p, it, rho - lane + __ffs(rows) - 1, x);
+        }
+      }
       ok = wait(&outs_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;
       tc_fence_after();
-
-      // ---- rows that see a listed key, from the definition ----
-      if (x == 0 && ok && cnt > 0) {
-        const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
-        bool again = some > kListed;
-        const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
-        for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
-        again = again && live && tl == tl;      // a score that is NaN makes the sum NaN, and with it the row
-        for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-          redo_part<D, C::MX>(p, it, rho - lane + __ffs(rows) - 1);
-      }
       item_done(n);
     }
   }
