@@ -7,14 +7,16 @@
 // up to 16 rows, as m16n8k16 with the rows as M (a tcgen05 product has at least 64); more rows go to
 // attention_paged_tc.cu. Pieces of both are joined here.
 //
-// A block takes one piece of one (sequence, kv head): a producer warp streams pages by TMA through a ring of 64-token
-// stages, four warps consume it, 16 tokens of a stage each. Every warp keeps its own running maximum, sum and output, so
-// that nothing but the ring's barriers is shared until the end.
+// Resident blocks (two a multiprocessor) take item after item, one piece of one (sequence, kv head): a producer warp streams
+// pages by TMA through a ring of 64-token stages and runs ahead into the next item, four warps consume it, 16 tokens of a
+// stage each. Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
+// until an item's end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
 #include "attention_paged.cuh"
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -50,10 +52,19 @@ struct PagedCfg {
   static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
   static constexpr int STAGES = 98304 / STAGE;
   static constexpr int PITCH = D + 4;                              // floats of a row in the join buffer
-  static constexpr int SMEM = STAGES * STAGE + 1024;
-  static_assert(WARPS * 16 * (PITCH + 2) * 4 <= STAGES * STAGE, "the join buffer lies over the ring");
+  static constexpr int JOIN = 2 * 8 * PITCH * 4;                   // of two warps 8 rows at a time
+  static constexpr int SMEM = STAGES * STAGE + JOIN + 1024;
   static_assert(2 * SC <= 1024, "scales");
 };
+
+// A barrier of the consuming warps, and whether any thread says so.
+template <int WARPS>
+__device__ __forceinline__ bool consumers_any(bool said) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((uint32_t)said), "n"(WARPS * 32) : "memory");
+  return r != 0;
+}
 
 // Shared address of 16-byte chunk `chunk` (of the row's D values) of token `tok`.
 template <class C>
@@ -72,139 +83,210 @@ __device__ __forceinline__ float value_at(const uint8_t* stage_v, const uint8_t*
   return bf16_lo(*reinterpret_cast<const uint16_t*>(stage_v + at));
 }
 
+// Item `n` of a block, as it lies in shared memory: what the warps need of it, worked out once.
+struct FewItem {
+  int there, b, hk;
+  int pos0, pmin, pmax;                         // positions of the first of all rows, of the first and last that are there
+  int first_any, first_all, sink_tiles, win_tile;
+  int i0, cnt, piece, pieces;                   // first step, steps; piece of how many
+  __device__ __forceinline__ int tok(int i) const {
+    const int t = i0 + i;
+    return (t < sink_tiles ? t : win_tile + (t - sink_tiles)) * kTileTok;
+  }
+};
+
 template <class C>
 __global__ void __launch_bounds__((C::WARPS + 1) * 32, 2)
 paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const PagedArgs p) {
   constexpr int D = C::D, ST = C::ST, NT = D / 8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], w_full[2], w_empty[2];
   __shared__ uint32_t page_mask[C::STAGES];
+  __shared__ FewItem items[2];
+  __shared__ float2 sums[C::WARPS][16];         // the warps' maximum (times log2 e) and sum of a row
   __shared__ volatile uint32_t abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  long long u = blockIdx.x;
-  const int piece = (int)(u % p.max_pieces);
-  u /= p.max_pieces;
-  const int hk = (int)(u % p.a.Hkv);
-  const long long b = u / p.a.Hkv;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
 
   pdl_trigger();
-  pdl_wait();
-  const int len = checked_len(p, b, threadIdx.x == 0);
-  const Pieces pc(p, len, 0);
-  if (piece >= pc.count) return;
-  const int i0 = piece * pc.per, i1 = min(pc.tiles, i0 + pc.per);
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], C::WARPS);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_empty[s], C::WARPS);
+    }
     abort_flag = 0;
     mbar_fence_init();
   }
   __syncthreads();
+  pdl_wait();
+  const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;     // pages of a step
 
   if (warp == C::WARPS) {
-    // ---------------- producer ----------------
-    const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;   // pages of a tile
+    // ---------------- items and loads ----------------
     const int rows_of = min(p.page_size, kTileTok);
-    const int32_t* table = p.table + b * p.table_width;
-    const int last_page = pc.pmax >> p.page_log2;
-    int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
-    int issued = 0;
-    for (int i = i0; i < i1; ++i, ++issued) {
-      const int s = issued % C::STAGES;
-      const int tok0 = pc.tile(i) * kTileTok, page0 = tok0 >> p.page_log2;
-      if (page0 < base || page0 + in_tile > base + 32) {
-        // in_tile divides 32, and so tiles do not straddle groups of 32 entries
-        const int nb = page0 & ~31;
-        ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
-        base = nb;
-        next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+    const int units = p.a.B * p.a.Hkv, total = units * p.max_pieces;
+    int n = 0, issued = 0;
+    bool ok = true;
+    // 32 candidates at a time; pieces that a sequence does not have are passed over. The first pieces of all come first, so
+    // that the ones that are there spread evenly over the blocks.
+    for (long long c0 = blockIdx.x; ok && c0 < total; c0 += 32ll * gridDim.x) {
+      const long long idx = c0 + (long long)lane * gridDim.x;
+      FewItem mine{};
+      if (idx < total) {
+        const int u = (int)(idx % units);
+        mine.piece = (int)(idx / units);
+        mine.hk = u % p.a.Hkv;
+        mine.b = u / p.a.Hkv;
+        const int len = checked_len(p, mine.b, true);
+        const Pieces pc(p, len, 0);
+        mine.there = mine.piece < pc.count;
+        mine.pos0 = len - p.rows;
+        mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
+        mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
+        mine.i0 = mine.piece * pc.per;
+        mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+        mine.pieces = pc.count;
       }
-      const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
-      // pages that no row sees are not loaded: past the end, or between the first tokens and the window
-      const int t0 = tok0 + lane * rows_of;
-      const bool want = lane < in_tile && t0 <= pc.pmax &&
-                        (t0 + rows_of > pc.first_any || t0 < min(p.a.sinks, pc.first_all));
-      const bool good = want && id >= 0 && id < p.pages;
-      if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-      const uint32_t mask = __ballot_sync(0xffffffffu, good);
-      if (issued >= C::STAGES &&
-          !mbar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag, p.status, DEV_TIMEOUT_EMPTY))
-        break;
-      if (lane == 0) {
-        page_mask[s] = mask;
-        mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
-      }
-      __syncwarp();
-      if (good) {
-        const int row = (int)(((long long)id * p.a.Hkv + hk) << p.page_log2) + (t0 & (p.page_size - 1));
-        uint8_t* st = smem + s * C::STAGE;
+      for (unsigned some = __ballot_sync(0xffffffffu, mine.there != 0); ok && some; some &= some - 1) {
+        const int who = __ffs(some) - 1;
+        if (n >= 2)
+          ok = __all_sync(0xffffffffu, bar_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kPagedWaitNs, &abort_flag,
+                                                DEV_TIMEOUT_EMPTY));
+        if (!ok) break;
+        if (lane == who) items[n & 1] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_full[n & 1]);
+        const FewItem it = items[n & 1];
+        ++n;
+        const int32_t* table = p.table + (long long)it.b * p.table_width;
+        const int last_page = it.pmax >> p.page_log2;
+        int base = -1000, ids = 0, next = 0;   // 32 table entries from `base` on, and the 32 behind them
+        for (int i = 0; i < it.cnt; ++i, ++issued) {
+          const int s = issued % C::STAGES;
+          const int tok0 = it.tok(i), page0 = tok0 >> p.page_log2;
+          if (page0 < base || page0 + in_tile > base + 32) {
+            // in_tile divides 32: a step's pages lie in one group of 32 entries
+            const int nb = page0 & ~31;
+            ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+            base = nb;
+            next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+          }
+          const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+          // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+          const int t0 = tok0 + lane * rows_of;
+          const bool want = lane < in_tile && t0 <= it.pmax &&
+                            (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, it.first_all));
+          const bool good = want && id >= 0 && id < p.pages;
+          if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+          const uint32_t mask = __ballot_sync(0xffffffffu, good);
+          if (issued >= C::STAGES &&
+              !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
+                                                      DEV_TIMEOUT_EMPTY))))
+            break;
+          if (lane == 0) {
+            page_mask[s] = mask;
+            mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
+          }
+          __syncwarp();
+          if (good) {
+            const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
+            uint8_t* st = smem + s * C::STAGE;
 #pragma unroll
-        for (int h = 0; h < C::HALVES; ++h) {
-          const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
-          tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
-          tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
-        }
-        if (C::MX) {
-          const uint32_t bytes = rows_of * (D / 32);
-          uint8_t* sc = st + 2 * C::KV + lane * bytes;
-          bulk_load(sc, p.k_s + (long long)row * (D / 32), bytes, &full[s]);
-          bulk_load(sc + C::SC, p.v_s + (long long)row * (D / 32), bytes, &full[s]);
+            for (int h = 0; h < C::HALVES; ++h) {
+              const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
+              tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
+              tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
+            }
+            if (C::MX) {
+              const uint32_t bytes = rows_of * (D / 32);
+              uint8_t* sc = st + 2 * C::KV + lane * bytes;
+              bulk_load(sc, p.k_s + (long long)row * (D / 32), bytes, &full[s]);
+              bulk_load(sc + C::SC, p.v_s + (long long)row * (D / 32), bytes, &full[s]);
+            }
+          }
         }
       }
     }
-    // a piece that gives up still waits for its copies in flight
-    __syncwarp();
-    if (abort_flag && lane == 0)
+    // no more items
+    if (ok && n >= 2)
+      ok = __all_sync(0xffffffffu, bar_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_EMPTY));
+    if (ok && lane == 0) {
+      items[n & 1].there = 0;
+      mbar_arrive(&w_full[n & 1]);
+    }
+    // a block that gives up still waits for its copies in flight
+    if (abort_flag && lane == 0) {
+      atomicCAS(p.status, 0u, abort_flag);
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
         mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+    }
     return;
   }
 
   // ---------------- consumers ----------------
     const int g = lane >> 2, c = lane & 3;
-  int pos[2], first[2];
+  const float scale = p.a.scale * 1.4426950408889634f;
   uint32_t qf[D / 16][4];
+  // The queries of item n, once it is known; false: there is none.
+  auto load_q = [&](int n) {
+    if (!__all_sync(0xffffffffu, bar_wait(&w_full[n & 1], (n >> 1) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_FULL)) ||
+        !items[n & 1].there)
+      return false;
+    const long long b = items[n & 1].b;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rho = g + 8 * h;
+      const bool live = rho < R;
+      const int r = rho / G;
+      const uint16_t* row = p.q + (b * p.rows + r) * p.q_stride + (long long)(items[n & 1].hk * G + rho - r * G) * D;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        // MX: the k of a step are the codes that one thread has at hand (8 in a row, 4 for each of two steps)
+        const int d0 = C::MX ? (ks / 2) * 32 + 8 * c + 4 * (ks & 1) : ks * 16 + 2 * c;
+        const int d1 = C::MX ? d0 + 2 : d0 + 8;
+        qf[ks][h] = live ? *reinterpret_cast<const uint32_t*>(row + d0) : 0;
+        qf[ks][2 + h] = live ? *reinterpret_cast<const uint32_t*>(row + d1) : 0;
+      }
+    }
+    return true;
+  };
+  int tiles = 0;                                // steps so far
+  // the warps go on together or not at all, also when one of them has given up
+  bool stop = consumers_any<C::WARPS>(!load_q(0));
+  for (int n = 0; !stop; ++n) {
+  const FewItem& it = items[n & 1];
+  const int cnt = it.cnt;
+  int pos[2], first[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int rho = g + 8 * h;
-    const bool live = rho < R;
-    const int r = rho / G;
-    pos[h] = live ? len - p.rows + r : -1;
+    pos[h] = rho < R ? it.pos0 + rho / G : -1;
     first[h] = (p.a.window && pos[h] >= p.a.window) ? pos[h] + 1 - p.a.window : 0;
-    const uint16_t* row = p.q + (b * p.rows + r) * p.q_stride + (long long)(hk * G + rho % G) * D;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      // MX: the k of a step are the codes that one thread has at hand (8 in a row, 4 for each of two steps)
-      const int d0 = C::MX ? (ks / 2) * 32 + 8 * c + 4 * (ks & 1) : ks * 16 + 2 * c;
-      const int d1 = C::MX ? d0 + 2 : d0 + 8;
-      qf[ks][h] = live ? *reinterpret_cast<const uint32_t*>(row + d0) : 0;
-      qf[ks][2 + h] = live ? *reinterpret_cast<const uint32_t*>(row + d1) : 0;
-    }
   }
   float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  const float scale = p.a.scale * 1.4426950408889634f;
 
-  for (int i = i0; i < i1; ++i) {
-    const int n = i - i0, s = n % C::STAGES;
-    if (!mbar_wait(&full[s], (n / C::STAGES) & 1, kPagedWaitNs, &abort_flag, p.status, DEV_TIMEOUT_FULL)) break;
-    const int loc0 = warp * ST, tok0 = pc.tile(i) * kTileTok + loc0;
+  for (int i = 0; i < cnt; ++i, ++tiles) {
+    const int s = tiles % C::STAGES;
+    if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_FULL)) break;
+    __syncwarp();
+    const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
     const uint8_t* st = smem + s * C::STAGE;
     const uint32_t kb = smem_u32(st), vb = kb + C::KV;
     const uint32_t mask = page_mask[s];
-    const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;
     // every row of the block sees every token of this warp
-    const bool whole = tok0 + ST - 1 <= pc.pmin && (tok0 >= pc.first_all || tok0 + ST <= p.a.sinks) &&
+    const bool whole = tok0 + ST - 1 <= it.pmin && (tok0 >= it.first_all || tok0 + ST <= p.a.sinks) &&
                        mask == (in_tile == 32 ? 0xffffffffu : (1u << in_tile) - 1u);
-    if (tok0 <= pc.pmax) {
+    if (tok0 <= it.pmax) {
       float sc[ST / 8][4];
 #pragma unroll
       for (int j = 0; j < ST / 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
@@ -268,8 +350,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         for (int w = 0; w < (ST + 31) / 32; ++w) {
           const int loc = w * 32 + lane, t = tok0 + loc;
           const bool there = loc < ST && ((mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u);
-          const bool any = there && t <= pc.pmax && (t >= pc.first_any || t < p.a.sinks);
-          const bool all = any && t <= pc.pmin && (t >= pc.first_all || t < p.a.sinks);
+          const bool any = there && t <= it.pmax && (t >= it.first_any || t < p.a.sinks);
+          const bool all = any && t <= it.pmin && (t >= it.first_all || t < p.a.sinks);
           drop |= (unsigned long long)__ballot_sync(0xffffffffu, loc < ST && !any) << (32 * w);
           alone |= (unsigned long long)__ballot_sync(0xffffffffu, any && !all) << (32 * w);
         }
@@ -406,52 +488,76 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if (c == 0) sums[warp][g + 8 * h] = make_float2(m[h], l[h]);
   }
-  named_bar_sync(1, C::WARPS * 32);        // the ring is read out
-  float* jo = reinterpret_cast<float*>(smem);
-  float* jml = jo + C::WARPS * 16 * C::PITCH;
+  const int piece = it.piece, pieces = it.pieces, hk = it.hk;
+  const long long b = it.b;
+  const bool more = load_q(n + 1);              // on their way while this item ends
+  stop = consumers_any<C::WARPS>(!more || abort_flag);
+  float top[2], tl[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int row = warp * 16 + g + 8 * h;
-    if (c == 0) jml[2 * row] = m[h], jml[2 * row + 1] = l[h];
+    top[h] = -INFINITY, tl[h] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int w = 0; w < C::WARPS; ++w) top[h] = fmaxf(top[h], sums[w][g + 8 * h].x);
+    const float base = top[h] == -INFINITY ? 0.f : top[h];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        jo[row * C::PITCH + (C::MX ? (2 * c + e) * (D / 8) + j : j * 8 + 2 * c + e)] = o[j][2 * h + e];
+    for (int w = 0; w < C::WARPS; ++w) tl[h] += ex2(sums[w][g + 8 * h].x - base) * sums[w][g + 8 * h].y;
+    const float f = ex2(m[h] - base);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][2 * h] *= f, o[j][2 * h + 1] *= f;
   }
-  named_bar_sync(1, C::WARPS * 32);
-  if (abort_flag) return;
-  for (int x = threadIdx.x; x < kFewRows * (D / 4); x += C::WARPS * 32) {
-    const int rho = x % kFewRows, d = x / kFewRows * 4;
-    if (rho >= R) continue;
-    float top = -INFINITY, tl = 0.f;
-    float4 to = make_float4(0.f, 0.f, 0.f, 0.f);
+  // ((0 + 2) + (1 + 3)): the upper two warps hand theirs to the lower two, those one to the other, 8 rows at a time
 #pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, jml[2 * (w * 16 + rho)]);
-    const float base = top == -INFINITY ? 0.f : top;
+  for (int h = 0; h < 2; ++h) {
+    if (h == 1 && R <= 8) break;
 #pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) {
-      const int rr = w * 16 + rho;
-      const float f = ex2(jml[2 * rr] - base);
-      const float4 v = *reinterpret_cast<const float4*>(jo + rr * C::PITCH + d);
-      tl += f * jml[2 * rr + 1];
-      to.x += f * v.x;
-      to.y += f * v.y;
-      to.z += f * v.z;
-      to.w += f * v.w;
+    for (int far = 2; far; far >>= 1) {
+      float* mine = join + ((warp & (far - 1)) * 8 + g) * C::PITCH;
+      if (warp >= far && warp < 2 * far) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(mine + j * 8 + 2 * c) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+      }
+      named_bar_sync(1, C::WARPS * 32);
+      if (warp < far) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float2 v = *reinterpret_cast<const float2*>(mine + j * 8 + 2 * c);
+          o[j][2 * h] += v.x, o[j][2 * h + 1] += v.y;
+        }
+      }
+      named_bar_sync(1, C::WARPS * 32);
     }
-    if (pc.count == 1) {
-      const float inv = 1.f / tl;
-      const bool none = tl == 0.f;
-      const long long at = ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d;
-      *reinterpret_cast<uint2*>(p.out + at) =
-          none ? make_uint2(0, 0) : make_uint2(bf16x2(to.x * inv, to.y * inv), bf16x2(to.z * inv, to.w * inv));
-    } else {
+    const int rho = g + 8 * h;
+    if (warp == 0 && rho < R && !abort_flag) {
+      const bool one = pieces == 1;
+      const float inv = !one ? 1.f : tl[h] == 0.f ? 0.f : 1.f / tl[h];
+      const int r = rho / G;
       const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
-      *reinterpret_cast<float4*>(part_of(p, at, D, rho, d / 4)) = to;
-      if (d == 0) *sums_of(p, at, rho) = make_float2(top, tl);
+      uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        // thread (g, c) has of product j the columns 2c and 2c + 1; MX: the j-th of what two threads' values are
+        const float v0 = o[j][2 * h] * inv, v1 = o[j][2 * h + 1] * inv;
+        if (!C::MX) {
+          const int d = j * 8 + 2 * c;
+          if (one) *reinterpret_cast<uint32_t*>(out + d) = bf16x2(v0, v1);
+          else *reinterpret_cast<float2*>(part_of(p, at, D, rho, d / 4) + d % 4) = make_float2(v0, v1);
+        } else {
+          const int d = 2 * c * (D / 8) + j;
+          if (one) {
+            out[d] = (uint16_t)bf16x2(v0, 0.f);
+            out[d + D / 8] = (uint16_t)bf16x2(v1, 0.f);
+          } else {
+            part_of(p, at, D, rho, d / 4)[d % 4] = v0;
+            part_of(p, at, D, rho, (d + D / 8) / 4)[d % 4] = v1;
+          }
+        }
+      }
+      if (!one && c == 0) *sums_of(p, at, rho) = make_float2(top[h], tl[h]);
     }
+  }
+  if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   }
 }
 
@@ -473,19 +579,26 @@ __global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const
   const Pieces pc(p, checked_len(p, b, false), rho / p.block_rows);
   if (pc.count == 1) return;
   const long long at = (b * p.a.Hkv + hk) * p.max_pieces;
-  float top = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < pc.count; ++i) top = fmaxf(top, sums_of(p, at + i, rho)->x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float tl = 0.f;
+  float m = -INFINITY, tl = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < pc.count; ++i) {
-    const float2 s = *sums_of(p, at + i, rho);
-    const float4 v = *reinterpret_cast<const float4*>(part_of(p, at + i, D, rho, d4));
-    const float f = ex2(s.x - base);
-    tl = fmaf(f, s.y, tl);
-    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+  for (int i = 0; i < pc.count; i += 8) {
+    float2 s[8];
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s[k] = i + k < pc.count ? *sums_of(p, at + i + k, rho) : make_float2(-INFINITY, 0.f);
+      v[k] = i + k < pc.count ? *reinterpret_cast<const float4*>(part_of(p, at + i + k, D, rho, d4))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float mn = fmaxf(m, s[k].x), base = mn == -INFINITY ? 0.f : mn;
+      const float keep = ex2(m - base), f = ex2(s[k].x - base);
+      m = mn;
+      tl = fmaf(f, s[k].y, tl * keep);
+      o.x = fmaf(f, v[k].x, o.x * keep), o.y = fmaf(f, v[k].y, o.y * keep);
+      o.z = fmaf(f, v[k].z, o.z * keep), o.w = fmaf(f, v[k].w, o.w * keep);
+    }
   }
   const float inv = 1.f / tl;
   *reinterpret_cast<uint2*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d4 * 4) =
@@ -529,8 +642,8 @@ static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_
   if (rc || (rc = page_map(&vm, cache->v, cache, box, swizzle))) return rc;
   auto kern = paged_attention_kernel<C>;
   if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM))) return rc;
-  const long long grid = (long long)p.a.B * p.a.Hkv * p.max_pieces;
-  return launch_pdl(kern, dim3((unsigned)grid), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
+  const long long items = (long long)p.a.B * p.a.Hkv * p.max_pieces;
+  return launch_pdl(kern, dim3((unsigned)std::min(items, 2ll * num_sms())), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
 }
 
 static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
