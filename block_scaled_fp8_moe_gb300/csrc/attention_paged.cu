@@ -259,6 +259,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
     return true;
   };
   int tiles = 0;                                // steps so far
+  const uint32_t k16 = C::MX ? sixteen() : 0;
   // the warps go on together or not at all, also when one of them has given up
   bool stop = consumers_any<C::WARPS>(!load_q(0));
   for (int n = 0; !stop; ++n) {
@@ -314,8 +315,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
             const uint32_t at = kv_addr<C>(kb, t, 2 * bl + (c >> 1)) + 8 * (c & 1);
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
             const uint32_t by = (sw >> (8 * bl)) & 255u, f = scale_bits(by) * 0x10001u;
-            uint32_t x[4] = {mul_bf16x2(e4m3_pair(w0, w0, 0x1800), f), mul_bf16x2(e4m3_pair(w0, w0, 0x3A22), f),
-                             mul_bf16x2(e4m3_pair(w1, w1, 0x1800), f), mul_bf16x2(e4m3_pair(w1, w1, 0x3A22), f)};
+            uint32_t x[4] = {mul_bf16x2(e4m3_pair(w0, w0, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w0, w0, kCodes23, k16), f),
+                             mul_bf16x2(e4m3_pair(w1, w1, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w1, w1, kCodes23, k16), f)};
             if (large) {
               const uint32_t f2 = scale_rest(by) * 0x10001u;
 #pragma unroll
@@ -445,9 +446,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
           const bool large = __any_sync(0xffffffffu, max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            constexpr uint32_t kSel[4] = {0x4800, 0x5911, 0x6A22, 0x7B33};
-            uint32_t x0 = mul_bf16x2(e4m3_pair(w[0][j / 4], w[1][j / 4], kSel[j & 3]), f0);
-            uint32_t x1 = mul_bf16x2(e4m3_pair(w[2][j / 4], w[3][j / 4], kSel[j & 3]), f1);
+            constexpr uint32_t kSel[4] = {0xC480, 0xD591, 0xE6A2, 0xF7B3};      // the j-th code of either word
+            uint32_t x0 = mul_bf16x2(e4m3_pair(w[0][j / 4], w[1][j / 4], kSel[j & 3], k16), f0);
+            uint32_t x1 = mul_bf16x2(e4m3_pair(w[2][j / 4], w[3][j / 4], kSel[j & 3], k16), f1);
             if (large) {
               x0 = mul_bf16x2(x0, scale_rest(by[0]) | scale_rest(by[1]) << 16);
               x1 = mul_bf16x2(x1, scale_rest(by[2]) | scale_rest(by[3]) << 16);

@@ -80,12 +80,20 @@ __device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool
 }
 
 // Two E4M3 codes as bf16 with their values times 2^-120: sign, exponent and fraction in bf16's places (subnormal codes
-// become subnormals). `sel` takes [code of the high half, sign of the low one's (replicated), the low one's, any].
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b, uint32_t sel) {
+// become subnormals). `sel` takes, from the lowest byte on, a code, its sign (replicated), another code, its sign; four bits
+// further up sign and code lie where bf16 has them. The shift is a product with a 16 that the compiler does not know
+// (`sixteen()`): the pipe of the other instructions is the one that conversions are short of.
+__device__ __forceinline__ uint32_t sixteen() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, 16;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b, uint32_t sel, uint32_t k16) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return (uint32_t)((int32_t)r >> 4) & 0x87F087F0u;
+  return (r * k16) & 0x87F087F0u;
 }
+constexpr uint32_t kCodes01 = 0x9180, kCodes23 = 0xB3A2;   // codes 0 and 1 (2 and 3) of one word
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

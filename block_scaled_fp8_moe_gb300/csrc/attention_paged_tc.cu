@@ -406,6 +406,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       // finite become zero (a weight of zero would not hide them), and those that some row sees are listed: rows that see
       // them are computed again.
       const int tid = C::MX ? threadIdx.x % 128 : lane, group = C::MX ? warp / 4 - 3 : 0;
+      const uint32_t k16 = sixteen();
       int tile = 0, steps = 0;
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
@@ -452,8 +453,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 uint32_t o[8];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                  o[2 * b] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], 0x1800), f);
-                  o[2 * b + 1] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], 0x3A22), f);
+                  o[2 * b] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], kCodes01, k16), f);
+                  o[2 * b + 1] = mul_bf16x2(e4m3_pair(w[j][b], w[j][b], kCodes23, k16), f);
                 }
                 const uint32_t at = to + (r + j * RPT) * 128;
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
@@ -473,7 +474,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
 #pragma unroll 1
                 for (int b = 0; b < 8; ++b) {
                   const uint32_t w = *reinterpret_cast<const uint32_t*>(src + row * D + ch * 16 + (b / 2) * 4);
-                  uint32_t o = mul_bf16x2(mul_bf16x2(e4m3_pair(w, w, b & 1 ? 0x3A22 : 0x1800), f), f2);
+                  uint32_t o = mul_bf16x2(mul_bf16x2(e4m3_pair(w, w, b & 1 ? kCodes23 : kCodes01, k16), f), f2);
                   const uint32_t hit = ((o & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                   if (edge) {
                     bad = bad || hit;
@@ -631,17 +632,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, b2), w[2], w[3]);
 #pragma unroll
             for (int f = 0; f < 4; ++f) w[f] = ex2(w[f]);
-            const uint32_t u = bf16x2(w[0], w[1]), v = bf16x2(w[2], w[3]);
-            // the sum takes the weights as the product does, rounded, so that a single large one divides out exactly
-            la = add2(la, pack2(bf16_lo(u), bf16_hi(u)));
-            lb = add2(lb, pack2(bf16_lo(v), bf16_hi(v)));
-            s[e / 2] = u;                       // s[e / 2] has been read
-            s[e / 2 + 1] = v;
+            la = add2(la, pack2(w[0], w[1]));
+            lb = add2(lb, pack2(w[2], w[3]));
+            s[e / 2] = bf16x2(w[0], w[1]);      // s[e / 2] has been read
+            s[e / 2 + 1] = bf16x2(w[2], w[3]);
           }
           tmem_st32(ts + 32 * h, s, 32 * h);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[x][h]);
+        }
+        if (info.z) {
+          // A row that sees few keys has them in such steps: there the sum takes the weights as the product does, rounded,
+          // so that a single large one divides out exactly. Over many keys the roundings even out.
+          la = lb = pack2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            la = add2(la, pack2(bf16_lo(s[e]), bf16_hi(s[e])));
+            lb = add2(lb, pack2(bf16_lo(s[e + 1]), bf16_hi(s[e + 1])));
+          }
         }
         l2 = add2(l2, add2(la, lb));
       }
