@@ -193,7 +193,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   pdl_wait();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, kPrefillWaitNs, &abort_flag, p.status, code)) != 0;
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, kPrefillWaitNs, &abort_flag, code)) != 0;
   };
   auto item_there = [&](int n) {
     return wait(&w_full[n & 1], (n >> 1) & 1, DEV_TIMEOUT_FULL) && slots[n & 1][6] != 0;
@@ -518,34 +518,32 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           mbar_arrive(&p_full[x][h]);
         };
         const bool edge = edges.at(j0);
+        if (edge) {
+          // Hidden in Tensor Memory, 32 scores at a time: little code, and groups that all of the warp's rows see are left.
+          // The row sees key j0 + e when e <= hi and (e >= lo or e < low). (Scores that a short step has not computed are
+          // hidden with the rest behind the first tokens.)
+          const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
+          auto below = [](int k) { return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u; };
+#pragma unroll 1
+          for (int e = 0; e < kTileN; e += 32) {
+            const uint32_t see = below(hi + 1 - e) & (~below(lo - e) | below(low - e));
+            if (!turn && __all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+            uint32_t s[32];
+            tmem_ld32(ts + e, s, 0);
+            tmem_ld_wait();
+            reg_fence32(s, 0);
+#pragma unroll
+            for (int d = 0; d < 32; ++d) s[d] = (see >> d) & 1u ? s[d] ^ turn : 0xff800000u;
+            tmem_st32(ts + e, s, 0);
+          }
+          tmem_st_wait();
+        }
         uint32_t s[128];
 #pragma unroll
         for (int e = 0; e < 128; e += 32) tmem_ld32(ts + e, s, e);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 128; e += 32) reg_fence32(s, e);
-        if (edge) {
-          // The row sees key j0 + e when e <= hi and (e >= lo or e < low); mostly only one of the three matters. (Scores
-          // that a short step has not computed are hidden with the rest behind the first tokens.)
-          const int hi = pos - j0, lo = first - j0, low = p.a.sinks - j0;
-          if (turn) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) s[e] ^= turn;
-          }
-          if (__any_sync(0xffffffffu, hi < kTileN - 1)) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e) s[e] = e <= hi ? s[e] : 0xff800000u;
-          }
-          if (__any_sync(0xffffffffu, lo > 0)) {
-            if (low <= 0) {
-#pragma unroll
-              for (int e = 0; e < 128; ++e) s[e] = e >= lo ? s[e] : 0xff800000u;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 128; ++e) s[e] = e >= lo || e < low ? s[e] : 0xff800000u;
-            }
-          }
-        }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int e = 0; e < 128; e += 8)
@@ -570,22 +568,23 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             hand_over(h);
           }
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < 128; e += 32) {
-            uint32_t rest[16];
+            uint32_t s[32], u[32];              // of u, 16 of the rounded weights and 16 of the rests
+            tmem_ld32(ts + e, s, 0);
+            tmem_ld_wait();
+            reg_fence32(s, 0);
 #pragma unroll
             for (int d = 0; d < 16; d += 2) {
               float w[4];
-              weights(s + e + 2 * d, w);
+              weights(s + 2 * d, w);
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
-                s[e + d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
-                rest[d + f] = bf16x2(w[2 * f] - bf16_lo(s[e + d + f]), w[2 * f + 1] - bf16_hi(s[e + d + f]));
+                u[d + f] = bf16x2(w[2 * f], w[2 * f + 1]);
+                u[16 + d + f] = bf16x2(w[2 * f] - bf16_lo(u[d + f]), w[2 * f + 1] - bf16_hi(u[d + f]));
               }
             }
-#pragma unroll
-            for (int d = 0; d < 16; ++d) s[e + 16 + d] = rest[d];
-            tmem_st32(ts + e, s, e);
+            tmem_st32(ts + e, u, 0);
             if (e & 32) hand_over(e / 64);
           }
         }
@@ -672,6 +671,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && abort_flag) atomicCAS(p.status, 0u, abort_flag);
 }
 
 static int rows_map(CUtensorMap* m, const void* base, int D, int heads, int rows, long long stride) {

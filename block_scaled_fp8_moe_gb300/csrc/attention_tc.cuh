@@ -9,35 +9,21 @@
 
 namespace moe {
 
-// Bounded wait in few instructions (these kernels run five kinds of warps side by side, and their code has to share the
-// instruction cache): the thread sleeps until the phase completes, and gives up after limit_ns, or once another thread of
-// the block has given up. The one that gives up leaves `code` in *abort, which the kernel records at its end.
+// Bounded wait: the thread sleeps until the phase completes, and gives up after limit_ns, or once another thread of the block
+// has given up. The one that gives up leaves `code` in *abort, which the kernel records at its end (these kernels run five
+// kinds of warps side by side, and their code has to share the instruction cache).
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort,
                                          uint32_t code) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 a;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra DONE;\n\t"
-      "mov.u64 t0, %globaltimer;\n\t"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "@p bra DONE;\n\t"
-      "ld.volatile.shared.b32 a, [%4];\n\t"
-      "setp.ne.b32 q, a, 0;\n\t"
-      "@q bra DONE;\n\t"
-      "mov.u64 t1, %globaltimer;\n\t"
-      "sub.u64 t1, t1, t0;\n\t"
-      "setp.lt.u64 q, t1, %5;\n\t"
-      "@q bra AGAIN;\n\t"
-      "st.volatile.shared.b32 [%4], %6;\n\t"
-      "DONE:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"((uint32_t)MOE_WAIT_HINT_NS), "r"(smem_u32((const void*)abort)), "l"(limit_ns),
-        "r"(code)
-      : "memory");
-  return ok != 0;
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort = code;
+      return false;
+    }
+  }
 }
 
 // D (+)= A B with A from Tensor Memory (bf16, two a column).
