@@ -8,55 +8,70 @@
 
 namespace moe {
 
-// One thread per 8 values (16 bytes in); 4 neighbouring lanes hold one block of 32.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;
+
+// A thread has 8 values (16 bytes) of `kAppendUnroll` tokens at a time, all loaded before any is written; 4 neighbouring lanes
+// have one block of 32. `group` threads (a power of two, up to a block) share a token, its keys first, then its values.
+// Bound: HBM, 4 bytes a value in bf16 and 3.03 in MXFP8.
 template <bool MX>
-__global__ void __launch_bounds__(256)
-kv_append_kernel(moe_kv_cache c, int T, const uint16_t* __restrict__ k, long long k_stride,
-                 const uint16_t* __restrict__ v, long long v_stride, const int32_t* __restrict__ slots,
-                 uint32_t* status) {
+__global__ void __launch_bounds__(kAppendThreads, 6)
+kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, long long k_stride,
+                 const uint16_t* __restrict__ v, long long v_stride, const int32_t* __restrict__ slots, int group_log2,
+                 int page_log2, uint32_t* status) {
+  constexpr int U = kAppendUnroll;
   pdl_trigger();
   pdl_wait();
-  const int per_head = c.D / 8, per_tok = c.Hkv * per_head;
-  const long long total = 2LL * T * per_tok;     // of every token: its keys, then its values
-  const long long n_slots = (long long)c.pages * c.page_size;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const long long tk = i / per_tok;
-    const int e = (int)(i - tk * per_tok);
-    const long long t = tk >> 1;
-    const bool is_v = tk & 1;
-    const int slot = __ldg(slots + t);
-    const int h = e / per_head, d8 = e % per_head;
-    const uint4 a = *reinterpret_cast<const uint4*>((is_v ? v + t * v_stride : k + t * k_stride) + e * 8);
-    const bool in = slot >= 0 && slot < n_slots;
-    if (!in && slot != -1 && e == 0 && !is_v) atomicCAS(status, 0u, (uint32_t)DEV_BAD_INPUT);
-    const long long row = in ? ((long long)(slot / c.page_size) * c.Hkv + h) * c.page_size + slot % c.page_size : 0;
-    if (!MX) {
-      if (in) reinterpret_cast<uint4*>(is_v ? c.v : c.k)[row * per_head + d8] = a;
-    } else {
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-      float f[8], m = 0.f;
-      bool finite = true;
+  const int head_log2 = c.D == 128 ? 4 : 3, per_tok = c.Hkv << head_log2;     // 16-byte parts of a head, of a token's keys
+  const int tokens = kAppendThreads >> group_log2;                           // of a block at a time
+  const int t0 = blockIdx.x * (tokens * U) + (threadIdx.x >> group_log2);
+  const long long n_slots = (long long)c.pages << page_log2;
+  // groups of less than a token's parts go through them in turns; every lane goes along (the shuffles need it)
+  for (int e0 = 0; e0 < 2 * per_tok; e0 += 1 << group_log2) {
+    const int e = e0 + (threadIdx.x & ((1 << group_log2) - 1));
+    const bool part = e < 2 * per_tok, is_v = e >= per_tok;
+    const int x = is_v ? e - per_tok : e, h = x >> head_log2, d8 = x & ((1 << head_log2) - 1);
+    const uint16_t* src = (is_v ? v : k) + x * 8;
+    const long long stride = is_v ? v_stride : k_stride;
+    uint4 a[U];
+    int slot[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = bf16_lo(w[j]);
-        f[2 * j + 1] = bf16_hi(w[j]);
-        m = fmaxf(m, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
-        finite = finite && (w[j] & 0x7F80u) != 0x7F80u && (w[j] & 0x7F800000u) != 0x7F800000u;
-      }
-      // total is a multiple of 4 and so is the first index of a group: a group's lanes are all here
-      const unsigned group = 0xFu << (threadIdx.x & 28);
-      finite = __all_sync(group, finite);
-      m = fmaxf(m, __shfl_xor_sync(group, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(group, m, 2));
-      const int se = e4m3_scale_exp(m);
-      const float sc = finite ? pow2_neg(se) : 0.f;
-      if (in) {
-        uint2 codes = make_uint2(0, 0);
-        if (finite)
-          codes = make_uint2(e4m3x2(f[0] * sc, f[1] * sc) | (e4m3x2(f[2] * sc, f[3] * sc) << 16),
-                             e4m3x2(f[4] * sc, f[5] * sc) | (e4m3x2(f[6] * sc, f[7] * sc) << 16));
-        reinterpret_cast<uint2*>(is_v ? c.v : c.k)[row * per_head + d8] = codes;
-        if ((d8 & 3) == 0) (is_v ? c.v_s : c.k_s)[row * (c.D / 32) + d8 / 4] = finite ? (uint8_t)(se + 127) : 255;
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * tokens;
+      const bool there = part && t < T;
+      slot[u] = there ? __ldg(slots + t) : -1;
+      a[u] = there ? __ldcs(reinterpret_cast<const uint4*>(src + t * stride)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = slot[u] >= 0 && slot[u] < n_slots;
+      if (!in && slot[u] != -1 && e == 0) atomicCAS(status, 0u, (uint32_t)DEV_BAD_INPUT);
+      const long long page = in ? slot[u] >> page_log2 : 0;
+      const long long row = ((page * c.Hkv + h) << page_log2) + (in ? slot[u] & (c.page_size - 1) : 0);
+      if (!MX) {
+        if (in) reinterpret_cast<uint4*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = a[u];
+      } else {
+        // the largest magnitude by its bits: what is not finite lies above all else
+        const uint32_t w[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+        uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+        const unsigned four = 0xFu << (threadIdx.x & 28);
+        m2 = __vmaxu2(m2, __shfl_xor_sync(four, m2, 1));
+        m2 = __vmaxu2(m2, __shfl_xor_sync(four, m2, 2));
+        const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        const bool finite = m < 0x7F80u;
+        const int se = e4m3_scale_exp_bf16(m);
+        const float sc = pow2_neg(se);
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+        if (in) {
+          uint2 codes = make_uint2(0, 0);
+          if (finite)
+            codes = make_uint2(e4m3x2(f[0] * sc, f[1] * sc) | (e4m3x2(f[2] * sc, f[3] * sc) << 16),
+                               e4m3x2(f[4] * sc, f[5] * sc) | (e4m3x2(f[6] * sc, f[7] * sc) << 16));
+          reinterpret_cast<uint2*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = codes;
+          if ((d8 & 3) == 0) (is_v ? c.v_s : c.k_s)[row * (c.D / 32) + d8 / 4] = finite ? (uint8_t)(se + 127) : 255;
+        }
       }
     }
   }
@@ -79,9 +94,12 @@ extern "C" int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_
     return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) return MOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(slots) & 3) return MOE_ERR_INVALID_ARG;
-  const long long total = 2LL * T * row / 8;
-  const int blocks = (int)std::min<long long>((total + 255) / 256, (long long)num_sms() * 8);
+  int group_log2 = 4, page_log2 = 3;
+  while ((1 << group_log2) < 2 * row / 8 && (1 << group_log2) < kAppendThreads) ++group_log2;
+  while ((1 << page_log2) < cache->page_size) ++page_log2;
+  const int per_block = (kAppendThreads >> group_log2) * kAppendUnroll;
   auto kern = cache->format == MOE_KV_MXFP8 ? kv_append_kernel<true> : kv_append_kernel<false>;
-  return launch_pdl(kern, dim3(blocks), dim3(256), 0, static_cast<cudaStream_t>(stream), *cache, (int)T, k,
-                    (long long)k_stride, v, (long long)v_stride, slots, static_cast<uint32_t*>(ws));
+  return launch_pdl(kern, dim3((unsigned)((T + (long long)per_block - 1) / per_block)), dim3(kAppendThreads), 0,
+                    static_cast<cudaStream_t>(stream), *cache, (int)T, k, (long long)k_stride, v, (long long)v_stride, slots,
+                    group_log2, page_log2, static_cast<uint32_t*>(ws));
 }

@@ -21,6 +21,10 @@ __device__ __forceinline__ int mx_scale_exp(float amax, int qe, uint32_t qm) {
   return max(-127, min(126, s));      // 127 is unreachable for finite fp32 amax and both formats
 }
 __device__ __forceinline__ int e4m3_scale_exp(float amax) { return mx_scale_exp(amax, 8, 0x600000u); }  // 448
+// The same for an amax that is a bf16 value, from its bits: one whose exponent field is zero ends at -127 either way.
+__device__ __forceinline__ int e4m3_scale_exp_bf16(uint32_t bits) {
+  return max(-127, (int)(bits >> 7) - 127 - 8 + ((bits & 0x7Fu) > 0x60u ? 1 : 0));
+}
 __device__ __forceinline__ int e2m1_scale_exp(float amax) { return mx_scale_exp(amax, 2, 0x400000u); }  // 6
 
 // 2^-s for s in [-127, 126] (always a normal fp32)
