@@ -44,6 +44,9 @@ struct TcCfg {
   static constexpr int MORE = MX ? 168 : 208, LESS = MX ? 48 : 88;
   static constexpr int FEEDERS = MX ? 4 : 1;                       // warps that hand a tile to the products
   static constexpr int GROUPS = MX ? 2 : 1;                        // of them, which take tiles in turn
+  // Barriers of the entries that the products have read, by tile: a group waits for those of its own tiles alone, and a barrier
+  // cannot end its next phase before the group has seen this one.
+  static constexpr int ENT_BARS = ENTRIES % GROUPS ? ENTRIES * GROUPS : ENTRIES;
   static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;   // Tensor Memory columns
   static_assert(RAWS % GROUPS == 0, "a group of feeders sees every phase of its stages");
   static_assert(SMEM + 4096 <= 227 * 1024, "shared memory");
@@ -109,7 +112,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t w_full[2], w_empty[2], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
   __shared__ uint64_t sums_there, outs_read;
-  __shared__ uint64_t landed[C::MX ? C::RAWS : C::ENTRIES], raw_empty[C::RAWS], ready[C::ENTRIES], ent_empty[C::ENTRIES];
+  __shared__ uint64_t landed[C::MX ? C::RAWS : C::ENTRIES], raw_empty[C::RAWS], ready[C::ENTRIES], ent_empty[C::ENT_BARS];
   __shared__ PagedItem items[2];
   __shared__ int4 infos[kInfos];                // of a step: first token, pages there, whether some row does not see a key
   __shared__ int listed_n[2], listed[2][kListed];
@@ -138,10 +141,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     }
     for (int i = 0; i < (C::MX ? C::RAWS : C::ENTRIES); ++i) mbar_init(&landed[i], 1);
     for (int i = 0; i < C::RAWS; ++i) mbar_init(&raw_empty[i], C::FEEDERS);
-    for (int i = 0; i < C::ENTRIES; ++i) {
-      mbar_init(&ready[i], C::FEEDERS);
-      mbar_init(&ent_empty[i], 1);
-    }
+    for (int i = 0; i < C::ENTRIES; ++i) mbar_init(&ready[i], C::FEEDERS);
+    for (int i = 0; i < C::ENT_BARS; ++i) mbar_init(&ent_empty[i], 1);
     abort_flag = 0;
     mbar_fence_init();
   }
@@ -164,6 +165,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   auto item_done = [&](int n) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+  };
+  // the products have read what was in this tile's entry before
+  auto ent_free = [&](int tile) {
+    const int last = tile - C::ENTRIES;
+    return last < 0 || wait(&ent_empty[last % C::ENT_BARS], (last / C::ENT_BARS) & 1, DEV_TIMEOUT_EMPTY);
   };
   // An item's tiles pass in this order: K0 K1 V0 K2 V1 K3 V2 ..., one counter for all.
 
@@ -246,7 +252,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             constexpr int N = C::MX ? C::RAWS : C::ENTRIES;
             const int st = tile % N, use = tile / N;
             const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
-            if (use > 0 && !(ok = wait(C::MX ? &raw_empty[st] : &ent_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
+            if (!(ok = C::MX ? use == 0 || wait(&raw_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY) : ent_free(tile))) break;
             if (lane == 0) {
               if (!is_v) {
                 const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks) &&
@@ -304,7 +310,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             mma_bf16(tm + (x ? C::S1 : C::S0), qdesc + at, kx + at, idesc_qk, ks > 0);
           }
           tc_commit(&s_full[x]);
-          tc_commit(&ent_empty[tile % C::ENTRIES]);
+          tc_commit(&ent_empty[tile % C::ENT_BARS]);
         }
         __syncwarp();
         ++tile;
@@ -344,7 +350,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           tc_fence_after();
           pv(x, 1, true);
           if (leader) {
-            tc_commit(&ent_empty[tile % C::ENTRIES]);
+            tc_commit(&ent_empty[tile % C::ENT_BARS]);
             tc_commit(&o_full[x]);
           }
           __syncwarp();
@@ -418,8 +424,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         };
         auto feed = [&](int i, bool is_v) {
           const int e = tile % C::ENTRIES, st = C::MX ? tile % C::RAWS : e;
-          if (tile % C::GROUPS != group) {      // the other group's; its entry's phase passes here too
-            if (tile >= C::ENTRIES) ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY);
+          if (tile % C::GROUPS != group) {      // the other group's
             ++tile;
             return;
           }
@@ -428,7 +433,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           const bool edge = is_v && info.z != 0;
           uint8_t* dst = ring + e * C::TILE;
           if (C::MX) {
-            if (tile >= C::ENTRIES && !(ok = wait(&ent_empty[e], (tile / C::ENTRIES - 1) & 1, DEV_TIMEOUT_EMPTY))) return;
+            if (!(ok = ent_free(tile))) return;
             const uint8_t* src = raws + st * C::RAW;
             constexpr int CH = D / 16, RPT = 128 / CH;          // 16 codes at a time; rows of the tile a pass covers
             const int ch = tid % CH, row0 = tid / CH;
