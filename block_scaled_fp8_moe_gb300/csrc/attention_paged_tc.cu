@@ -437,9 +437,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             const uint8_t* src = raws + st * C::RAW;
             constexpr int CH = D / 16, RPT = 128 / CH;          // 16 codes at a time; rows of the tile a pass covers
             const int ch = tid % CH, row0 = tid / CH;
+            // half of the lanes take their second 8 codes first: the lanes of a load, and of a store, are then in different banks
+            const uint32_t flip = ((lane >> 3) ^ (D == 128 ? ch >> 2 : 0)) & 1;
             // a thread's rows are RPT apart, a multiple of 8: their chunks are turned alike
-            const uint32_t from = smem_u32(src) + row0 * D + ch * 16, sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
-            const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 + ((((2 * ch) & 7) ^ (row0 & 7)) << 4);
+            const uint32_t from = smem_u32(src) + row0 * D + ch * 16 + flip * 8, sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
+            const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 + ((((2 * ch + flip) & 7) ^ (row0 & 7)) << 4);
             static_assert(RPT % 8 == 0, "turned alike");
             uint32_t top = 0;
 #pragma unroll 1
@@ -447,8 +449,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
               uint32_t w[4][4], by[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[j][0]), "=r"(w[j][1]), "=r"(w[j][2]), "=r"(w[j][3]) : "r"(from + (r + j * RPT) * D));
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(from + (r + j * RPT) * D));
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[j][2]), "=r"(w[j][3]) : "r"((from ^ 8) + (r + j * RPT) * D));
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(by[j]) : "r"(sc + (r + j * RPT) * (D / 32)));
               }
 #pragma unroll
@@ -478,7 +480,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 bool bad = false;
 #pragma unroll 1
                 for (int b = 0; b < 8; ++b) {
-                  const uint32_t w = *reinterpret_cast<const uint32_t*>(src + row * D + ch * 16 + (b / 2) * 4);
+                  const uint32_t w = *reinterpret_cast<const uint32_t*>(src + row * D + ch * 16 + (b / 2 ^ flip * 2) * 4);
                   uint32_t o = mul_bf16x2(mul_bf16x2(e4m3_pair(w, w, b & 1 ? kCodes23 : kCodes01, k16), f), f2);
                   const uint32_t hit = ((o & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                   if (edge) {
