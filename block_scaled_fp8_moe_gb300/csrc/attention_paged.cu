@@ -132,95 +132,84 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   if (warp == C::WARPS) {
     // ---------------- items and loads ----------------
     const int rows_of = min(p.page_size, kTileTok);
-    const int units = p.a.B * p.a.Hkv, total = units * p.max_pieces;
     int n = 0, issued = 0;
     bool ok = true;
-    // 32 candidates at a time; pieces that a sequence does not have are passed over. The first pieces of all come first, so
-    // that the ones that are there spread evenly over the blocks.
-    for (long long c0 = blockIdx.x; ok && c0 < total; c0 += 32ll * gridDim.x) {
-      const long long idx = c0 + (long long)lane * gridDim.x;
-      FewItem mine{};
-      if (idx < total) {
-        const int u = (int)(idx % units);
-        mine.piece = (int)(idx / units);
-        mine.hk = u % p.a.Hkv;
-        mine.b = u / p.a.Hkv;
-        const int len = checked_len(p, mine.b, true);
-        const Pieces pc(p, len, 0);
-        mine.there = mine.piece < pc.count;
-        mine.pos0 = len - p.rows;
-        mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
-        mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
-        mine.i0 = mine.piece * pc.per;
-        mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
-        mine.pieces = pc.count;
+    ItemWalk walk;
+    for (long long idx = blockIdx.x; ok; idx += gridDim.x) {
+      const int who = walk.lane_of(p, idx);
+      if (n >= 2 && !(ok = __all_sync(0xffffffffu, bar_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kPagedWaitNs, &abort_flag,
+                                                            DEV_TIMEOUT_EMPTY))))
+        break;
+      if (lane == max(who, 0)) {
+        FewItem mine{};                          // no more items: that one is not there
+        if (who >= 0) {
+          const int u = walk.group + lane, j = (int)(idx - walk.before) - (walk.upto - walk.mine);
+          const Pieces& pc = walk.pc;
+          mine.there = 1;
+          mine.b = u;
+          mine.piece = j / p.a.Hkv;
+          mine.hk = j - mine.piece * p.a.Hkv;
+          mine.pos0 = pc.pos0;
+          mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
+          mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
+          mine.i0 = mine.piece * pc.per;
+          mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+          mine.pieces = pc.count;
+        }
+        items[n & 1] = mine;
       }
-      for (unsigned some = __ballot_sync(0xffffffffu, mine.there != 0); ok && some; some &= some - 1) {
-        const int who = __ffs(some) - 1;
-        if (n >= 2)
-          ok = __all_sync(0xffffffffu, bar_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kPagedWaitNs, &abort_flag,
-                                                DEV_TIMEOUT_EMPTY));
-        if (!ok) break;
-        if (lane == who) items[n & 1] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_full[n & 1]);
+      if (who < 0) break;
+      const FewItem it = items[n & 1];
+      ++n;
+      const int32_t* table = p.table + (long long)it.b * p.table_width;
+      const int last_page = it.pmax >> p.page_log2;
+      int base = -1000, ids = 0, next = 0;   // 32 table entries from `base` on, and the 32 behind them
+      for (int i = 0; i < it.cnt; ++i, ++issued) {
+        const int s = issued % C::STAGES;
+        const int tok0 = it.tok(i), page0 = tok0 >> p.page_log2;
+        if (page0 < base || page0 + in_tile > base + 32) {
+          // in_tile divides 32: a step's pages lie in one group of 32 entries
+          const int nb = page0 & ~31;
+          ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+          base = nb;
+          next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+        // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+        const int t0 = tok0 + lane * rows_of;
+        const bool want = lane < in_tile && t0 <= it.pmax &&
+                          (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, it.first_all));
+        const bool good = want && id >= 0 && id < p.pages;
+        if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        if (issued >= C::STAGES &&
+            !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
+                                                    DEV_TIMEOUT_EMPTY))))
+          break;
+        if (lane == 0) {
+          page_mask[s] = mask;
+          mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&w_full[n & 1]);
-        const FewItem it = items[n & 1];
-        ++n;
-        const int32_t* table = p.table + (long long)it.b * p.table_width;
-        const int last_page = it.pmax >> p.page_log2;
-        int base = -1000, ids = 0, next = 0;   // 32 table entries from `base` on, and the 32 behind them
-        for (int i = 0; i < it.cnt; ++i, ++issued) {
-          const int s = issued % C::STAGES;
-          const int tok0 = it.tok(i), page0 = tok0 >> p.page_log2;
-          if (page0 < base || page0 + in_tile > base + 32) {
-            // in_tile divides 32: a step's pages lie in one group of 32 entries
-            const int nb = page0 & ~31;
-            ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
-            base = nb;
-            next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
-          }
-          const int id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
-          // pages that no row sees are not loaded: past the end, or between the first tokens and the window
-          const int t0 = tok0 + lane * rows_of;
-          const bool want = lane < in_tile && t0 <= it.pmax &&
-                            (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, it.first_all));
-          const bool good = want && id >= 0 && id < p.pages;
-          if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-          const uint32_t mask = __ballot_sync(0xffffffffu, good);
-          if (issued >= C::STAGES &&
-              !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
-                                                      DEV_TIMEOUT_EMPTY))))
-            break;
-          if (lane == 0) {
-            page_mask[s] = mask;
-            mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
-          }
-          __syncwarp();
-          if (good) {
-            const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
-            uint8_t* st = smem + s * C::STAGE;
+        if (good) {
+          const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
+          uint8_t* st = smem + s * C::STAGE;
 #pragma unroll
-            for (int h = 0; h < C::HALVES; ++h) {
-              const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
-              tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
-              tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
-            }
-            if (C::MX) {
-              const uint32_t bytes = rows_of * (D / 32);
-              uint8_t* sc = st + 2 * C::KV + lane * bytes;
-              bulk_load(sc, p.k_s + (long long)row * (D / 32), bytes, &full[s]);
-              bulk_load(sc + C::SC, p.v_s + (long long)row * (D / 32), bytes, &full[s]);
-            }
+          for (int h = 0; h < C::HALVES; ++h) {
+            const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
+            tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
+            tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
+          }
+          if (C::MX) {
+            const uint32_t bytes = rows_of * (D / 32);
+            uint8_t* sc = st + 2 * C::KV + lane * bytes;
+            bulk_load(sc, p.k_s + (long long)row * (D / 32), bytes, &full[s]);
+            bulk_load(sc + C::SC, p.v_s + (long long)row * (D / 32), bytes, &full[s]);
           }
         }
       }
-    }
-    // no more items
-    if (ok && n >= 2)
-      ok = __all_sync(0xffffffffu, bar_wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_EMPTY));
-    if (ok && lane == 0) {
-      items[n & 1].there = 0;
-      mbar_arrive(&w_full[n & 1]);
     }
     // a block that gives up still waits for its copies in flight
     if (abort_flag && lane == 0) {

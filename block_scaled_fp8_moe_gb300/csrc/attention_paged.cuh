@@ -9,7 +9,6 @@
 
 namespace moe {
 
-constexpr int kMaxPieces = 64;
 constexpr uint64_t kPagedWaitNs = 1000000000ull;
 
 struct PagedArgs {
@@ -53,14 +52,16 @@ __host__ __device__ inline int piece_steps(int tile, int tiles) {
 // What the rows of block mb of a sequence see, as steps, and its pieces. The pieces follow from the sequence's own length
 // alone: a row's result is the same in every batch.
 struct Pieces {
-  int pmin, pmax;        // positions of the first and the last row
+  int pos0, pmin, pmax;  // positions of the sequence's first new row, of the block's first and last row
   int first_any, first_all;
   int sink_tiles, win_tile, tiles;
   int per, count;
+  Pieces() = default;
   __device__ __forceinline__ Pieces(const PagedArgs& p, int len, int mb) {
     const int G = p.a.Hq / p.a.Hkv, r_hi = (min(p.rows * G, (mb + 1) * p.block_rows) - 1) / G;
-    pmin = len - p.rows + mb * p.block_rows / G;
-    pmax = len == 0 ? -1 : len - p.rows + r_hi;
+    pos0 = len - p.rows;
+    pmin = pos0 + mb * p.block_rows / G;
+    pmax = len == 0 ? -1 : pos0 + r_hi;
     first_any = (p.a.window && pmin >= p.a.window) ? pmin + 1 - p.a.window : 0;
     first_all = (p.a.window && pmax >= p.a.window) ? pmax + 1 - p.a.window : 0;
     sink_tiles = (min(p.a.sinks, first_all) + p.tile - 1) / p.tile;
@@ -78,6 +79,40 @@ __device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool
   if (report) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
   return 0;
 }
+
+// The items (sequence, block of rows, piece, head) that there are, numbered without gaps, so that blocks that take every
+// grid-th of them differ by one at most. A warp goes along them, 32 blocks of rows at a time; numbers only go up.
+struct ItemWalk {
+  long long before = 0;  // items of the groups that have been passed
+  int group = -32, total = 0;
+  Pieces pc;                         // the lane's block of rows,
+  int mine = 0, upto = 0;            // its items, these and those before
+  // The lane that has item idx, or -1 if there are not as many.
+  __device__ __forceinline__ int lane_of(const PagedArgs& p, long long idx) {
+    const int lane = threadIdx.x % 32, units = p.a.B * p.mblocks;
+    while (idx >= before + total) {
+      before += total;
+      total = 0;
+      group += 32;
+      if (group >= units) return -1;
+      const int u = group + lane;
+      mine = 0;
+      if (u < units) {
+        const int b = p.mblocks == 1 ? u : u / p.mblocks;
+        pc = Pieces(p, checked_len(p, b, true), u - b * p.mblocks);
+        mine = pc.count * p.a.Hkv;
+      }
+      upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int t = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += t;
+      }
+      total = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return __ffs(__ballot_sync(0xffffffffu, idx - before < upto)) - 1;
+  }
+};
 
 // Two E4M3 codes as bf16 with their values times 2^-120: sign, exponent and fraction in bf16's places (subnormal codes
 // become subnormals). `sel` takes, from the lowest byte on, a code, its sign (replicated), another code, its sign; four bits

@@ -57,6 +57,7 @@ struct PagedItem {
   int there, b, hk, rho0, live;                 // first row of the block, rows there are
   int pos0;                                     // position of row 0 of the sequence's new rows
   int pmax, first_any, sink_tiles, win_tile;
+  int first_all, pmin;                          // tokens from first_all to pmin are in all rows' windows
   int i0, cnt, piece, pieces;                   // first step, steps; piece of how many
   __device__ __forceinline__ int tok(int i) const {
     const int t = i0 + i;
@@ -177,114 +178,99 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LESS));
     if (warp == 8) {
       // ---------------- items and loads ----------------
-      const int units = p.a.B * p.mblocks * p.a.Hkv;
-      const int total = units * p.max_pieces;
       const int in_tile = p.page_size >= kStepTok ? 1 : kStepTok >> p.page_log2;   // pages of a step
       const int rows_of = min(p.page_size, kStepTok);
       int n = 0, tile = 0, steps = 0;
       bool ok = true;
-      // 32 candidates at a time; pieces that a sequence does not have are passed over. The first pieces of all come first,
-      // so that the ones that are there spread evenly over the blocks.
-      for (long long c0 = blockIdx.x; ok && c0 < total; c0 += 32ll * gridDim.x) {
-        const long long idx = c0 + (long long)lane * gridDim.x;
-        PagedItem mine{};
-        int first_all = 0, pmin = 0;
-        if (idx < total) {
-          int u = (int)(idx % units);
-          mine.piece = (int)(idx / units);
-          mine.hk = u % p.a.Hkv;
-          u /= p.a.Hkv;
-          const int mb = u % p.mblocks;
-          mine.b = u / p.mblocks;
-          const int len = checked_len(p, mine.b, true);
-          const Pieces pc(p, len, mb);
-          mine.there = mine.piece < pc.count;
-          mine.rho0 = mb * kRowsM;
-          mine.live = min(p.rows * (p.a.Hq / p.a.Hkv) - mine.rho0, kRowsM);
-          mine.pos0 = len - p.rows;
-          mine.pmax = pc.pmax, mine.first_any = pc.first_any;
-          mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
-          mine.i0 = mine.piece * pc.per;
-          mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
-          mine.pieces = pc.count;
-          first_all = pc.first_all, pmin = pc.pmin;
+      ItemWalk walk;
+      for (long long idx = blockIdx.x; ok; idx += gridDim.x) {
+        const int who = walk.lane_of(p, idx);
+        if (n >= 2 && !(ok = wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
+        if (lane == max(who, 0)) {
+          PagedItem mine{};                     // no more items: that one is not there
+          if (who >= 0) {
+            const int u = walk.group + lane, b = p.mblocks == 1 ? u : u / p.mblocks, j = (int)(idx - walk.before) - (walk.upto - walk.mine);
+            const Pieces& pc = walk.pc;
+            mine.there = 1;
+            mine.b = b;
+            mine.piece = j / p.a.Hkv;
+            mine.hk = j - mine.piece * p.a.Hkv;
+            mine.rho0 = (u - b * p.mblocks) * kRowsM;
+            mine.live = min(p.rows * (p.a.Hq / p.a.Hkv) - mine.rho0, kRowsM);
+            mine.pos0 = pc.pos0;
+            mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
+            mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
+            mine.i0 = mine.piece * pc.per;
+            mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+            mine.pieces = pc.count;
+          }
+          items[n & 1] = mine;
+          listed_n[n & 1] = 0;                  // the last item but one, whose list this was, is done
         }
-        for (unsigned some = __ballot_sync(0xffffffffu, mine.there != 0); ok && some; some &= some - 1) {
-          const int who = __ffs(some) - 1;
-          if (n >= 2 && !(ok = wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
-          if (lane == who) {
-            items[n & 1] = mine;
-            listed_n[n & 1] = 0;                // the last item but one, whose list this was, is done
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_full[n & 1]);
+        if (who < 0) break;
+        const PagedItem it = items[n & 1];
+        const int all_from = it.first_all, all_to = it.pmin;
+        ++n;
+        const int cnt = it.cnt;
+        const int32_t* table = p.table + (long long)it.b * p.table_width;
+        const int last_page = it.pmax >> p.page_log2;
+        int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
+        int held[2] = {-1, -1};                    // page of this lane in the last two steps
+        for (int t = 0; t < 2 * cnt + 2; ++t) {    // the turns: K0 K1 V0 K2 V1 ...
+          const bool is_v = t >= 2 && !(t & 1);
+          const int i = t < 2 ? t : is_v ? (t - 2) / 2 : (t + 1) / 2;
+          if (i >= cnt) continue;
+          const int tok0 = it.tok(i), t0 = tok0 + lane * rows_of;
+          int id = i & 1 ? held[1] : held[0];
+          if (!is_v) {
+            const int page0 = tok0 >> p.page_log2;
+            if (page0 < base || page0 + in_tile > base + 32) {
+              const int nb = page0 & ~31;          // in_tile divides 32: a step's pages lie in one group of 32 entries
+              ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
+              base = nb;
+              next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
+            }
+            id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
+            // pages that no row sees are not loaded: past the end, or between the first tokens and the window
+            const bool want = lane < in_tile && t0 <= it.pmax &&
+                              (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, all_from));
+            const bool good = want && id >= 0 && id < p.pages;
+            if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
+            id = good ? id : -1;
+            if (i & 1) held[1] = id; else held[0] = id;
+          }
+          constexpr int N = C::MX ? C::RAWS : C::ENTRIES;
+          const int st = tile % N, use = tile / N;
+          const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
+          if (!(ok = C::MX ? use == 0 || wait(&raw_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY) : ent_free(tile))) break;
+          if (lane == 0) {
+            if (!is_v) {
+              const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks) &&
+                                 mask == (1u << in_tile) - 1u;
+              infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
+            }
+            mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&w_full[n & 1]);
-          const PagedItem it = items[n & 1];
-          const int all_from = __shfl_sync(0xffffffffu, first_all, who), all_to = __shfl_sync(0xffffffffu, pmin, who);
-          ++n;
-          const int cnt = it.cnt;
-          const int32_t* table = p.table + (long long)it.b * p.table_width;
-          const int last_page = it.pmax >> p.page_log2;
-          int base = -1000, ids = 0, next = 0;       // 32 table entries from `base` on, and the 32 behind them
-          int held[2] = {-1, -1};                    // page of this lane in the last two steps
-          for (int t = 0; t < 2 * cnt + 2; ++t) {    // the turns: K0 K1 V0 K2 V1 ...
-            const bool is_v = t >= 2 && !(t & 1);
-            const int i = t < 2 ? t : is_v ? (t - 2) / 2 : (t + 1) / 2;
-            if (i >= cnt) continue;
-            const int tok0 = it.tok(i), t0 = tok0 + lane * rows_of;
-            int id = i & 1 ? held[1] : held[0];
-            if (!is_v) {
-              const int page0 = tok0 >> p.page_log2;
-              if (page0 < base || page0 + in_tile > base + 32) {
-                const int nb = page0 & ~31;          // in_tile divides 32: a step's pages lie in one group of 32 entries
-                ids = nb == base + 32 ? next : (nb + lane <= last_page ? table[nb + lane] : -1);
-                base = nb;
-                next = nb + 32 + lane <= last_page ? table[nb + 32 + lane] : -1;
-              }
-              id = __shfl_sync(0xffffffffu, ids, (page0 - base + lane) & 31);
-              // pages that no row sees are not loaded: past the end, or between the first tokens and the window
-              const bool want = lane < in_tile && t0 <= it.pmax &&
-                                (t0 + rows_of > it.first_any || t0 < min(p.a.sinks, all_from));
-              const bool good = want && id >= 0 && id < p.pages;
-              if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
-              id = good ? id : -1;
-              if (i & 1) held[1] = id; else held[0] = id;
+          if (id >= 0) {
+            const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
+            const CUtensorMap* map = is_v ? &vmap : &kmap;
+            if (C::MX) {
+              uint8_t* dst = raws + st * C::RAW;
+              tma_load_2d(dst + lane * rows_of * D, map, 0, row, &landed[st]);
+              bulk_load(dst + kStepTok * D + lane * rows_of * (D / 32), (is_v ? p.v_s : p.k_s) + (long long)row * (D / 32),
+                        rows_of * (D / 32), &landed[st]);
+            } else {
+              uint8_t* dst = ring + st * C::TILE;
+              for (int h = 0; h < C::HALVES; ++h)
+                tma_load_2d(dst + h * kStepTok * 128 + lane * rows_of * 128, map, h * 64, row, &landed[st]);
             }
-            constexpr int N = C::MX ? C::RAWS : C::ENTRIES;
-            const int st = tile % N, use = tile / N;
-            const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
-            if (!(ok = C::MX ? use == 0 || wait(&raw_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY) : ent_free(tile))) break;
-            if (lane == 0) {
-              if (!is_v) {
-                const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks) &&
-                                   mask == (1u << in_tile) - 1u;
-                infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
-              }
-              mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D));
-            }
-            __syncwarp();
-            if (id >= 0) {
-              const int row = (int)(((long long)id * p.a.Hkv + it.hk) << p.page_log2) + (t0 & (p.page_size - 1));
-              const CUtensorMap* map = is_v ? &vmap : &kmap;
-              if (C::MX) {
-                uint8_t* dst = raws + st * C::RAW;
-                tma_load_2d(dst + lane * rows_of * D, map, 0, row, &landed[st]);
-                bulk_load(dst + kStepTok * D + lane * rows_of * (D / 32), (is_v ? p.v_s : p.k_s) + (long long)row * (D / 32),
-                          rows_of * (D / 32), &landed[st]);
-              } else {
-                uint8_t* dst = ring + st * C::TILE;
-                for (int h = 0; h < C::HALVES; ++h)
-                  tma_load_2d(dst + h * kStepTok * 128 + lane * rows_of * 128, map, h * 64, row, &landed[st]);
-              }
-            }
-            ++tile;
           }
-          steps += cnt;
+          ++tile;
         }
-      }
-      // no more items
-      if (ok && (n < 2 || wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) && lane == 0) {
-        items[n & 1].there = 0;
-        mbar_arrive(&w_full[n & 1]);
+        steps += cnt;
       }
       if (abort_flag)                           // copies in flight end before the block does
         for (int j = max(0, tile - (C::MX ? C::RAWS : C::ENTRIES)); j < tile; ++j)
@@ -552,12 +538,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     // scores in units of log2 e / scale; a scale of zero becomes one that tells none apart
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
     const uint64_t c2 = pack2(c, c);
+    const int G = p.a.Hq / p.a.Hkv;
     int done = 0, steps = 0;                    // steps of this chain, and of all, so far
     bool ok = true;
     for (int n = 0; ok && item_there(n); ++n) {
       const int cnt = items[n & 1].cnt;
       const bool live = row < items[n & 1].live, warp_live = __any_sync(0xffffffffu, live);
-      const int pos = live ? items[n & 1].pos0 + (items[n & 1].rho0 + row) / (p.a.Hq / p.a.Hkv) : -1;
+      const int pos = live ? items[n & 1].pos0 + (items[n & 1].rho0 + row) / G : -1;
       const int first = (p.a.window && pos >= p.a.window) ? pos + 1 - p.a.window : 0;
       float m = -INFINITY;                      // the maximum that the weights so far refer to
       uint64_t l2 = pack2(0.f, 0.f);
@@ -677,7 +664,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       ok = wait(&sums_there, n & 1, DEV_TIMEOUT_ACCUM) && ok;
       tc_fence_after();
       const PagedItem& it = items[n & 1];
-      const int G = p.a.Hq / p.a.Hkv, rho = it.rho0 + row, r = rho / G;
+      const int rho = it.rho0 + row, r = rho / G;
       const float2 s0 = sums[0][row], s1 = sums[1][row];
       const float both = fmaxf(s0.x, s1.x), base = both == -INFINITY ? 0.f : both;
       const float f0 = ex2(s0.x - base), f1 = ex2(s1.x - base), tl = f0 * s0.y + f1 * s1.y;
@@ -710,8 +697,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           for (int d = 0; d < D / 2; ++d) a[d] = 0;
         }
 #pragma unroll
-        for (int d = 0; d < D / 2; ++d)
-          a[d] = __float_as_uint(fmaf(__uint_as_float(b[d]), g1, __uint_as_float(a[d]) * g0));
+        for (int d = 0; d < D / 2; d += 2) {
+          const uint64_t sum = fma2(pack2(__uint_as_float(b[d]), __uint_as_float(b[d + 1])), pack2(g1, g1),
+                                    mul2(pack2(__uint_as_float(a[d]), __uint_as_float(a[d + 1])), pack2(g0, g0)));
+          float lo, hi;
+          unpack2(sum, lo, hi);
+          a[d] = __float_as_uint(lo), a[d + 1] = __float_as_uint(hi);
+        }
         if (one) {
           uint16_t* out = p.out + (((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho - r * G) * D + e0;
 #pragma unroll
