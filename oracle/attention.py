@@ -54,10 +54,12 @@ def attend_heads(q, k, v, p0, scale, window=0, sinks=0):
 def attention_tolerance(out, mag):
     """How far a kernel may be that rounds its softmax weights to bf16 and its result once more.
 
-    Each weight is off by at most 2^-9 of itself, in the weighted sum and again in the sum that it is divided by:
-    2^-8 of the weighted magnitudes. fp32 scores and sums add less than 2^-10 of them at the tested sizes (a score is a
-    sum of 128 products, off by less than 128 * 2^-24 of their magnitudes, which stay below 50). The result's own
-    rounding to bf16 is 2^-9 of it."""
+    A rounding to bf16 is off by at most 2^-8 of the value. If every weight were
+    off by the most, in the weighted sum one way and in the sum that it is divided by the other, that would make 2^-7 of
+    the weighted magnitudes, and 2^-8 of the result for its own rounding. Half of either is asked for, because weights
+    round both ways (a row with few of them has to do better than one rounding each). fp32 scores and sums add less than
+    2^-10 at the tested sizes (a score is a sum of 128 products, off by less than 128 * 2^-24 of their magnitudes, which
+    stay below 50)."""
     return (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -9 * np.abs(out) + 1e-30
 
 

@@ -2,7 +2,7 @@
 
 Tolerances, before any run: the sum is one fp32 addition of two bf16 values and one rounding, so it equals the
 rounding of the exact sum except where fp32 rounded first: within one bf16 step, 2^-8 of its magnitude. The norm is
-rounded to bf16 once (2^-9) after a handful of fp32 operations (each 2^-24, the sum of squares at most cols * 2^-24
+rounded to bf16 once (2^-8 / (1 + 2^-8) at most) after a handful of fp32 operations (each 2^-24, the sum of squares at most cols * 2^-24
 relative): within 2^-8. Codes and scales equal the quantiser's on the rounded norm, bit for bit.
 """
 import numpy as np
