@@ -12,9 +12,9 @@
 // stage each. Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
 // until an item's end.
 //
-// One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 202 us, 6.2 TB/s. 160 rows of 64
-// heads over 8 of 64, a window of 1024 and 4 first tokens: 72 us, 4.7 TB/s (17 steps a row leave an item little to run
-// ahead of). One sequence's rows are a matter of latency: 12 us for 1024 to 4096 tokens, the join among them.
+// One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 200 us, 6.3 TB/s. 160 rows of 64
+// heads over 8 of 64, a window of 1024 and 4 first tokens: 70 us, 4.8 TB/s (17 steps a row leave an item little to run
+// ahead of). One sequence's rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -114,9 +114,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
+  const int G = p.G, R = p.R;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -131,6 +130,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   }
   __syncthreads();
   pdl_wait();
+  pdl_trigger();
   const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;     // pages of a step
 
   if (warp == C::WARPS) {
@@ -156,8 +156,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
           mine.pos0 = pc.pos0;
           mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
           mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
-          mine.i0 = mine.piece * pc.per;
-          mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+          mine.i0 = pc.begin(mine.piece);
+          mine.cnt = pc.steps(mine.piece);
           mine.pieces = pc.count;
         }
         items[n & 1] = mine;
@@ -562,37 +562,50 @@ constexpr int kJoinCols = 16;           // ... and groups of four columns
 
 template <int D>
 __global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const PagedArgs p) {
-  const int G = p.a.Hq / p.a.Hkv, R = p.rows * G;
+  const int G = p.G, R = p.R;
   const int row_blocks = (R + kJoinRows - 1) / kJoinRows;
   const unsigned unit = blockIdx.x / row_blocks;
   const int rho = (int)(blockIdx.x % row_blocks) * kJoinRows + threadIdx.x % kJoinRows;
   const int d4 = blockIdx.y * kJoinCols + threadIdx.x / kJoinRows, hk = (int)(unit % p.a.Hkv);
   const long long b = unit / p.a.Hkv;
+  // The lengths are there: the kernel before this one lets it start only after its own wait for what was before.
+  const Pieces pc(p, checked_len(p, b, false), min(rho, R - 1) >> p.block_log2);
   pdl_wait();
-  if (rho >= R) return;
-  const Pieces pc(p, checked_len(p, b, false), rho / p.block_rows);
-  if (pc.count == 1) return;
+  if (rho >= R || pc.count == 1) return;
   const long long at = (b * p.a.Hkv + hk) * p.max_pieces;
+  // Eight pieces at a time, the next eight under way meanwhile. The last one stands in for those past the end, so that no load
+  // waits for a comparison; it is added once.
+  const int count = pc.count;
+  float2 s[2][8];
+  float4 v[2][8];
+  auto load = [&](float2 (&sums)[8], float4 (&sum)[8], int i) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int piece = min(i + k, count - 1);
+      sums[k] = *sums_of(p, at + piece, rho);
+      sum[k] = *reinterpret_cast<const float4*>(part_of(p, at + piece, D, rho, d4));
+    }
+  };
   float m = -INFINITY, tl = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < pc.count; i += 8) {
-    float2 s[8];
-    float4 v[8];
+  auto add = [&](const float2 (&sums)[8], const float4 (&sum)[8], int i) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      s[k] = i + k < pc.count ? *sums_of(p, at + i + k, rho) : make_float2(-INFINITY, 0.f);
-      v[k] = i + k < pc.count ? *reinterpret_cast<const float4*>(part_of(p, at + i + k, D, rho, d4))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float mn = fmaxf(m, s[k].x), base = mn == -INFINITY ? 0.f : mn;
-      const float keep = ex2(m - base), f = ex2(s[k].x - base);
+      if (i + k >= count) break;
+      const float mn = fmaxf(m, sums[k].x), base = mn == -INFINITY ? 0.f : mn;
+      const float keep = ex2(m - base), f = ex2(sums[k].x - base);
       m = mn;
-      tl = fmaf(f, s[k].y, tl * keep);
-      o.x = fmaf(f, v[k].x, o.x * keep), o.y = fmaf(f, v[k].y, o.y * keep);
-      o.z = fmaf(f, v[k].z, o.z * keep), o.w = fmaf(f, v[k].w, o.w * keep);
+      tl = fmaf(f, sums[k].y, tl * keep);
+      o.x = fmaf(f, sum[k].x, o.x * keep), o.y = fmaf(f, sum[k].y, o.y * keep);
+      o.z = fmaf(f, sum[k].z, o.z * keep), o.w = fmaf(f, sum[k].w, o.w * keep);
     }
+  };
+  load(s[0], v[0], 0);
+  for (int i = 0; i < count; i += 16) {
+    if (i + 8 < count) load(s[1], v[1], i + 8);
+    add(s[0], v[0], i);
+    if (i + 16 < count) load(s[0], v[0], i + 16);
+    add(s[1], v[1], i + 8);
   }
   const float inv = 1.f / tl;
   *reinterpret_cast<uint2*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d4 * 4) =
@@ -614,7 +627,7 @@ static int max_pieces_of(const moe_attention* a, int rows, int max_len) {
   }
   // a shorter sequence can have more, where a piece's steps change
   int most = 1;
-  for (long long t : {tiles, std::min(tiles, 63ll)}) most = std::max(most, piece_count(tile, (int)t));
+  for (long long t : {tiles, std::min(tiles, 63ll)}) most = std::max(most, piece_count(tile == kTileTok ? 6 : 7, (int)t));
   return most;
 }
 
@@ -640,11 +653,11 @@ static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_
 static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
   const bool mx = cache->format == MOE_KV_MXFP8, d64 = p.a.D == 64;
   int rc;
-  if (p.tile != kTileTok) rc = launch_paged_tc(p, cache, st);
+  if (p.tile_log2 != 6) rc = launch_paged_tc(p, cache, st);
   else if (d64) rc = mx ? launch_few<64, true>(p, cache, st) : launch_few<64, false>(p, cache, st);
   else rc = mx ? launch_few<128, true>(p, cache, st) : launch_few<128, false>(p, cache, st);
   if (rc || p.max_pieces == 1) return rc;
-  const int R = p.rows * (p.a.Hq / p.a.Hkv);
+  const int R = p.R;
   return launch_pdl(d64 ? paged_join_kernel<64> : paged_join_kernel<128>,
                     dim3((unsigned)(ceil_div(R, kJoinRows) * p.a.B * p.a.Hkv), (unsigned)(p.a.D / 4 / kJoinCols)),
                     dim3(kJoinRows * kJoinCols), 0, st, p);
@@ -687,13 +700,14 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.rows = rows;
   p.max_len = max_len;
   p.table_width = table_width;
-  p.tile = tile_of(a, rows);
-  p.block_rows = p.tile == kTileTok ? kFewRows : 128;
-  p.mblocks = ceil_div(rows * (a->Hq / a->Hkv), p.block_rows);
+  p.G = a->Hq / a->Hkv;
+  p.R = rows * p.G;
+  p.tile_log2 = tile_of(a, rows) == kTileTok ? 6 : 7;
+  p.block_log2 = p.tile_log2 == 6 ? 4 : 7;
+  p.mblocks = ceil_div(p.R, 1 << p.block_log2);
   p.max_pieces = max_pieces_of(a, rows, max_len);
   // grids and the numbers of pieces stay below 2^31
-  if ((int64_t)a->B * a->Hkv * std::max((int64_t)p.mblocks * p.max_pieces, (int64_t)ceil_div(rows * (a->Hq / a->Hkv), kJoinRows)) >=
-      (int64_t)1 << 31)
+  if ((int64_t)a->B * a->Hkv * std::max((int64_t)p.mblocks * p.max_pieces, (int64_t)ceil_div(p.R, kJoinRows)) >= (int64_t)1 << 31)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   p.q = q;
   p.q_stride = q_stride;

@@ -19,7 +19,8 @@ struct PagedArgs {
   const uint8_t* k_s;
   const uint8_t* v_s;
   int rows, max_len, table_width;
-  int tile, block_rows;      // tokens of a step; rows (row, head of the group) of a block
+  int G, R;                  // heads of a group; rows (row, head of the group) of a sequence and kv head
+  int tile_log2, block_log2; // tokens of a step; rows of a block
   int mblocks, max_pieces;
   const uint16_t* q;
   long long q_stride;
@@ -35,20 +36,20 @@ struct PagedArgs {
 
 // Four columns of row rho's sums, and its maximum and sum, in piece `at` (of all).
 __device__ __forceinline__ float* part_of(const PagedArgs& p, long long at, int D, int rho, int d4) {
-  return p.part_o + ((at * (D / 4) + d4) * (p.rows * (p.a.Hq / p.a.Hkv)) + rho) * 4;
+  return p.part_o + ((at * (D / 4) + d4) * p.R + rho) * 4;
 }
 __device__ __forceinline__ float2* sums_of(const PagedArgs& p, long long at, int rho) {
-  return reinterpret_cast<float2*>(p.part_ml) + at * (p.rows * (p.a.Hq / p.a.Hkv)) + rho;
+  return reinterpret_cast<float2*>(p.part_ml) + at * p.R + rho;
 }
 
-// Pieces of about equal length. Steps of 64 tokens (few rows, two blocks a multiprocessor): about 8 a piece, and at most 64
-// pieces. Steps of 128 (one block a multiprocessor): about 4, 8 from 8192 tokens on, and at most 32 pieces. Shorter pieces
+// Pieces of equal length, to a step. Steps of 64 tokens (few rows, two blocks a multiprocessor): about 8 a piece, and at most
+// 64 pieces. Steps of 128 (one block a multiprocessor): about 4, 8 from 8192 tokens on, and at most 32 pieces. Shorter pieces
 // help the smallest batch and cost a large one, whose cache is read apace anyway: 1400 tokens, 64 heads over 8 of 128 bf16
-// elements take 12 us for one sequence and 242 us for 256 in pieces of 8 steps, 19 us and 215 us in one piece; four rows of
-// 1024 tokens take 14 us and 263 us in pieces of 4 steps of 128, 17 us and 198 us in one of 8. The small call counts here.
-__host__ __device__ inline int piece_count(int tile, int tiles) {
-  const int steps = tile == 64 || tiles >= 64 ? 8 : 4;
-  return min(max((tiles + steps / 2) / steps, 1), tile == 64 ? 64 : 32);
+// elements take 11 us for one sequence and 240 us for 256 in pieces of 8 steps, 19 us and 215 us in one piece; four rows of
+// 1024 tokens take 13 us and 257 us in pieces of 4 steps of 128, 17 us and 198 us in one of 8. The small call counts here.
+__host__ __device__ inline int piece_count(int tile_log2, int tiles) {
+  const int log2 = tile_log2 == 6 || tiles >= 64 ? 3 : 2;      // of the steps
+  return min(max((tiles + (1 << log2 >> 1)) >> log2, 1), tile_log2 == 6 ? 64 : 32);
 }
 
 // What the rows of block mb of a sequence see, as steps, and its pieces. The pieces follow from the sequence's own length
@@ -57,23 +58,28 @@ struct Pieces {
   int pos0, pmin, pmax;  // positions of the sequence's first new row, of the block's first and last row
   int first_any, first_all;
   int sink_tiles, win_tile, tiles;
-  int per, count;
+  int count, per, longer;    // pieces; steps of each, and how many have one more (the first ones)
   Pieces() = default;
   __device__ __forceinline__ Pieces(const PagedArgs& p, int len, int mb) {
-    const int G = p.a.Hq / p.a.Hkv, r_hi = (min(p.rows * G, (mb + 1) * p.block_rows) - 1) / G;
     pos0 = len - p.rows;
-    pmin = pos0 + mb * p.block_rows / G;
-    pmax = len == 0 ? -1 : pos0 + r_hi;
+    pmin = pos0, pmax = len - 1;
+    if (p.mblocks > 1) {
+      pmin = pos0 + (mb << p.block_log2) / p.G;
+      pmax = pos0 + (min(p.R, (mb + 1) << p.block_log2) - 1) / p.G;
+    }
+    if (len == 0) pmax = -1;
     first_any = (p.a.window && pmin >= p.a.window) ? pmin + 1 - p.a.window : 0;
     first_all = (p.a.window && pmax >= p.a.window) ? pmax + 1 - p.a.window : 0;
-    sink_tiles = (min(p.a.sinks, first_all) + p.tile - 1) / p.tile;
-    win_tile = max(first_any / p.tile, sink_tiles);
-    tiles = pmax < 0 ? 0 : sink_tiles + (pmax + p.tile) / p.tile - win_tile;
-    count = piece_count(p.tile, tiles);
-    per = (tiles + count - 1) / count;
-    count = max(1, per ? (tiles + per - 1) / per : 1);
+    const int up = (1 << p.tile_log2) - 1;
+    sink_tiles = (min(p.a.sinks, first_all) + up) >> p.tile_log2;
+    win_tile = max(first_any >> p.tile_log2, sink_tiles);
+    tiles = pmax < 0 ? 0 : sink_tiles + ((pmax + up + 1) >> p.tile_log2) - win_tile;
+    count = piece_count(p.tile_log2, tiles);
+    per = count == 1 ? tiles : (int)((unsigned)tiles / (unsigned)count);
+    longer = tiles - per * count;
   }
-  __device__ __forceinline__ int tile(int i) const { return i < sink_tiles ? i : win_tile + (i - sink_tiles); }
+  __device__ __forceinline__ int begin(int piece) const { return piece * per + min(piece, longer); }
+  __device__ __forceinline__ int steps(int piece) const { return per + (piece < longer); }
 };
 
 __device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool report) {

@@ -6,7 +6,7 @@
 // So both products run on tcgen05 with the rows as M = 128 (the rows beyond R cost nothing but tensor time, of which
 // there is enough: 1024 cycles a step of 128 tokens, against 2800 that its bytes take in bf16 and 1440 in MXFP8). Both
 // sides of the limit measured: 24 rows over bf16 take 14 us here and 18 us there (4096 tokens, 8 kv heads), 48 rows over
-// MXFP8 80 us here and 248 us there (8 sequences of up to 16k tokens). 16 rows go there: M = 16 wastes nothing of them.
+// MXFP8 76 us here and 248 us there (8 sequences of up to 16k tokens). 16 rows go there: M = 16 wastes nothing of them.
 //
 // Resident blocks take item after item: one piece of one (sequence, kv head). Its steps go in turn to two chains, each with
 // scores, weights and output of its own in Tensor Memory and a warpgroup of its own (a thread per row), so that one
@@ -18,7 +18,7 @@
 // What an MXFP8 step takes, about 2,350 cycles, is shared memory's time for the most part: 270 for the codes to come in, 320
 // for them to be read, 512 to be stored converted, 770 for the operands of the products. An item's end takes about 5,000
 // more, in which the chains join and write and no product runs; the pieces are long enough for four fifths of the time to
-// go to steps. 8 sequences of up to 16k tokens, 48 rows, 8 kv heads of 128: 80 us, 2.5 TB/s.
+// go to steps. 8 sequences of up to 16k tokens, 48 rows, 8 kv heads of 128: 76 us, 2.6 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -77,7 +77,7 @@ struct PagedItem {
 template <int D, bool MX>
 __device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, int rho, int half) {
   constexpr int N = D / 32;
-  const int lane = threadIdx.x % 32, G = p.a.Hq / p.a.Hkv, r = rho / G;
+  const int lane = threadIdx.x % 32, G = p.G, r = rho / G;
   const Visible see(it.pos0 + r, p.a.window, p.a.sinks);
   const long long row = ((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho % G;
   LaneRow<D> q;
@@ -132,7 +132,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   uint8_t* raws = ring + C::ENTRIES * C::TILE;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  pdl_trigger();
   if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -163,6 +162,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
+  pdl_trigger();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
     return __all_sync(0xffffffffu, bar_wait(bar, parity, kPagedWaitNs, &abort_flag, code)) != 0;
@@ -204,12 +204,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             mine.piece = j / p.a.Hkv;
             mine.hk = j - mine.piece * p.a.Hkv;
             mine.rho0 = (u - b * p.mblocks) * kRowsM;
-            mine.live = min(p.rows * (p.a.Hq / p.a.Hkv) - mine.rho0, kRowsM);
+            mine.live = min(p.R - mine.rho0, kRowsM);
             mine.pos0 = pc.pos0;
             mine.pmin = pc.pmin, mine.pmax = pc.pmax, mine.first_any = pc.first_any, mine.first_all = pc.first_all;
             mine.sink_tiles = pc.sink_tiles, mine.win_tile = pc.win_tile;
-            mine.i0 = mine.piece * pc.per;
-            mine.cnt = max(0, min(pc.tiles - mine.i0, pc.per));
+            mine.i0 = pc.begin(mine.piece);
+            mine.cnt = pc.steps(mine.piece);
             mine.pieces = pc.count;
           }
           items[n & 1] = mine;
@@ -373,7 +373,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         if (it.cnt > 0) {
           if (qs > 0 && !(ok = wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
           ++qs;
-          const int G = p.a.Hq / p.a.Hkv;
+          const int G = p.G;
           // a scale below zero turns the queries' sign instead
           const uint32_t turn = p.a.scale < 0.f ? 0x80008000u : 0u;
           const uint16_t* q = p.q + (long long)it.b * p.rows * p.q_stride + (long long)it.hk * G * D;
@@ -546,7 +546,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     // scores in units of log2 e / scale; a scale of zero becomes one that tells none apart
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
     const uint64_t c2 = pack2(c, c);
-    const int G = p.a.Hq / p.a.Hkv;
+    const int G = p.G;
     int done = 0, steps = 0;                    // steps of this chain, and of all, so far
     bool ok = true;
     for (int n = 0; ok && item_there(n); ++n) {
