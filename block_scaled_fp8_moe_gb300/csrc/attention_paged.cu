@@ -18,6 +18,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attention.cuh"
 #include "attention_paged.cuh"
 #include "attention_tc.cuh"
@@ -295,30 +297,40 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
               mma_16816(sc[2 * jp + 1], qf[ks], r[2], r[3]);
             }
         } else {
+          // Tokens whose scales one factor does not hold have a copy of the code to themselves: a branch inside would keep
+          // loads, conversions and products of neighbouring blocks apart.
           const uint8_t* scales = st + 2 * C::KV;
+          uint32_t sw[ST / 8], most = 0;
 #pragma unroll
           for (int j = 0; j < ST / 8; ++j) {
             const int t = loc0 + j * 8 + g;
-            const uint32_t sw = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
-                                         : *reinterpret_cast<const uint16_t*>(scales + t * 2);
-            const bool large = __any_sync(0xffffffffu, __vcmpgtu4(sw, kScaleFits * 0x01010101u) != 0);
-#pragma unroll
-            for (int bl = 0; bl < D / 32; ++bl) {
-              uint32_t w0, w1;
-              const uint32_t at = kv_addr<C>(kb, t, 2 * bl + (c >> 1)) + 8 * (c & 1);
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
-              const uint32_t by = (sw >> (8 * bl)) & 255u, f = scale_bits(by) * 0x10001u;
-              uint32_t x[4] = {mul_bf16x2(e4m3_pair(w0, w0, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w0, w0, kCodes23, k16), f),
-                               mul_bf16x2(e4m3_pair(w1, w1, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w1, w1, kCodes23, k16), f)};
-              if (large) {
-                const uint32_t f2 = scale_rest(by) * 0x10001u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = mul_bf16x2(x[e], f2);
-              }
-              mma_16816(sc[j], qf[2 * bl], x[0], x[1]);
-              mma_16816(sc[j], qf[2 * bl + 1], x[2], x[3]);
-            }
+            sw[j] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
+                             : *reinterpret_cast<const uint16_t*>(scales + t * 2);
+            most |= __vcmpgtu4(sw[j], kScaleFits * 0x01010101u);
           }
+          auto scores = [&](auto large) {
+#pragma unroll
+            for (int bl = 0; bl < D / 32; ++bl)
+#pragma unroll
+              for (int j = 0; j < ST / 8; ++j) {
+                uint32_t w0, w1;
+                const uint32_t at = kv_addr<C>(kb, loc0 + j * 8 + g, 2 * bl + (c >> 1)) + 8 * (c & 1);
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+                const uint32_t by = (sw[j] >> (8 * bl)) & 255u;
+                const uint32_t f = (large.value ? scale_bits(by) : (by + 120u) << 7) * 0x10001u;
+                uint32_t x[4] = {mul_bf16x2(e4m3_pair(w0, w0, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w0, w0, kCodes23, k16), f),
+                                 mul_bf16x2(e4m3_pair(w1, w1, kCodes01, k16), f), mul_bf16x2(e4m3_pair(w1, w1, kCodes23, k16), f)};
+                if (large.value) {
+                  const uint32_t f2 = scale_rest(by) * 0x10001u;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[e] = mul_bf16x2(x[e], f2);
+                }
+                mma_16816(sc[j], qf[2 * bl], x[0], x[1]);
+                mma_16816(sc[j], qf[2 * bl + 1], x[2], x[3]);
+              }
+          };
+          if (__any_sync(0xffffffffu, most != 0)) scores(std::true_type{});
+          else scores(std::false_type{});
         }
 
         // ---- what the rows do not see ----
@@ -435,20 +447,23 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
               }
               by[e] = scales[tk * (D / 32) + g / (256 / D)];
             }
-            const uint32_t f0 = scale_bits(by[0]) | scale_bits(by[1]) << 16, f1 = scale_bits(by[2]) | scale_bits(by[3]) << 16;
-            const bool large = __any_sync(0xffffffffu, max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits);
+            const bool large = max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits;
+            auto values = [&](auto rare) {       // rare: some scale is large, or some token left out
+              auto fac = [&](uint32_t b) { return rare.value ? scale_bits(b) : (b + 120u) << 7; };
+              const uint32_t f0 = fac(by[0]) | fac(by[1]) << 16, f1 = fac(by[2]) | fac(by[3]) << 16;
+              uint32_t r0 = 0, r1 = 0;
+              if (rare.value) r0 = scale_rest(by[0]) | scale_rest(by[1]) << 16, r1 = scale_rest(by[2]) | scale_rest(by[3]) << 16;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              constexpr uint32_t kSel[4] = {0xC480, 0xD591, 0xE6A2, 0xF7B3};      // the j-th code of either word
-              uint32_t x0 = mul_bf16x2(e4m3_pair(w[0][j / 4], w[1][j / 4], kSel[j & 3], k16), f0);
-              uint32_t x1 = mul_bf16x2(e4m3_pair(w[2][j / 4], w[3][j / 4], kSel[j & 3], k16), f1);
-              if (large) {
-                x0 = mul_bf16x2(x0, scale_rest(by[0]) | scale_rest(by[1]) << 16);
-                x1 = mul_bf16x2(x1, scale_rest(by[2]) | scale_rest(by[3]) << 16);
+              for (int j = 0; j < NT; ++j) {
+                constexpr uint32_t kSel[4] = {0xC480, 0xD591, 0xE6A2, 0xF7B3};    // the j-th code of either word
+                uint32_t x0 = mul_bf16x2(e4m3_pair(w[0][j / 4], w[1][j / 4], kSel[j & 3], k16), f0);
+                uint32_t x1 = mul_bf16x2(e4m3_pair(w[2][j / 4], w[3][j / 4], kSel[j & 3], k16), f1);
+                if (rare.value) x0 = mul_bf16x2(x0, r0) & keep0, x1 = mul_bf16x2(x1, r1) & keep1;
+                mma_16816(o[j], pf[t], x0, x1);
               }
-              if (drop) x0 &= keep0, x1 &= keep1;
-              mma_16816(o[j], pf[t], x0, x1);
-            }
+            };
+            if (__any_sync(0xffffffffu, large || drop != 0)) values(std::true_type{});
+            else values(std::false_type{});
           }
         }
         for (; alone; alone &= alone - 1) {
