@@ -372,6 +372,24 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
           drop |= alone;
         }
 
+        // the values' codes, under way while the weights are worked out
+        uint32_t w[4][D / 32], by[4];
+        if constexpr (C::MX) {
+          const uint8_t* scales = st + 2 * C::KV + C::SC;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = loc0 + 2 * c + (e & 1) + 8 * (e >> 1);
+            if constexpr (D == 128) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                           : "r"(kv_addr<C>(vb, tk, g)) : "memory");
+            } else {
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
+                           : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
+            }
+            by[e] = scales[tk * (D / 32) + g / (256 / D)];
+          }
+        }
         // ---- softmax ----
         float mx[2] = {-INFINITY, -INFINITY}, base[2];
 #pragma unroll
@@ -432,21 +450,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
             }
           } else {
             // thread (g, c) holds the D/8 values from g D/8 on of its four tokens; product j takes the j-th of each
-            const uint8_t* scales = st + 2 * C::KV + C::SC;
-            uint32_t w[4][D / 32], by[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tk = loc0 + t * 16 + 2 * c + (e & 1) + 8 * (e >> 1);
-              if constexpr (D == 128) {
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
-                             : "r"(kv_addr<C>(vb, tk, g)) : "memory");
-              } else {
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
-                             : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
-              }
-              by[e] = scales[tk * (D / 32) + g / (256 / D)];
-            }
             const bool large = max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits;
             auto values = [&](auto rare) {       // rare: some scale is large, or some token left out
               auto fac = [&](uint32_t b) { return rare.value ? scale_bits(b) : (b + 120u) << 7; };
