@@ -46,17 +46,18 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-template <int D_, bool MX_>
+template <int D_, bool MX_, bool EIGHT_>
 struct PagedCfg {
   static constexpr int D = D_;
-  static constexpr bool MX = MX_;
+  static constexpr bool MX = MX_, EIGHT = EIGHT_;                  // EIGHT: up to 8 rows, as a product's columns
+  static constexpr int CTAS = EIGHT && MX ? 3 : 2;                 // blocks of a multiprocessor
   static constexpr int WARPS = 4, ST = kTileTok / WARPS;           // tokens of a stage that a warp takes
   static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
   static constexpr int ROWB = MX ? D : 128;                        // bytes of a row in a column block
   static constexpr int KV = kTileTok * D * (MX ? 1 : 2);           // bytes of a stage's keys, or values
   static constexpr int SC = MX ? kTileTok * D / 32 : 0;
   static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
-  static constexpr int STAGES = 98304 / STAGE;
+  static constexpr int STAGES = (CTAS == 3 ? 65536 : 98304) / STAGE;
   static constexpr int PITCH = D + 4;                              // floats of a row in the join buffer
   static constexpr int JOIN = 2 * 8 * PITCH * 4;                   // of two warps 8 rows at a time
   static constexpr int SMEM = STAGES * STAGE + JOIN + 1024;
@@ -101,8 +102,341 @@ struct FewItem {
   }
 };
 
+// One 8 x 8 matrix of 16-bit values over the warp's lanes (row lane / 4, columns 2 (lane % 4) and the next), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// The consuming warps' work for up to 8 rows: the rows are the columns of both products (scores: 16 tokens x 8 rows, output: 16
+// of the D columns x 8 rows), so that half as many products, exponentials and accumulators do as with the rows as M = 16.
+// Thread (g, c) = (lane / 4, lane % 4) has the scores of tokens g and g + 8 for rows 2c and 2c + 1.
 template <class C>
-__global__ void __launch_bounds__((C::WARPS + 1) * 32, 2)
+__device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem, float* join, uint64_t* full, uint64_t* empty,
+                                              uint64_t* w_full, uint64_t* w_empty, const uint32_t* page_mask,
+                                              const FewItem* items, float2 (*sums)[16], volatile uint32_t* abort, int warp,
+                                              int lane) {
+  constexpr int D = C::D, ST = C::ST, MT = D / 16;
+  static_assert(ST == 16, "a warp's tokens of a stage are a product's rows");
+  const int g = lane >> 2, c = lane & 3, G = p.G, R = p.R;
+  const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;
+  const float scale = p.a.scale * 1.4426950408889634f;
+  uint32_t qf[D / 16][2];
+  auto load_q = [&](int n) {
+    if (!__all_sync(0xffffffffu, bar_wait(&w_full[n & 1], (n >> 1) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) ||
+        !items[n & 1].there)
+      return false;
+    const bool live = g < R;
+    const int r = g / G;
+    const uint16_t* row = p.q + ((long long)items[n & 1].b * p.rows + r) * p.q_stride + (long long)(items[n & 1].hk * G + g - r * G) * D;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      // MX: the k of a step are the codes that one thread has at hand (8 in a row, 4 for each of two steps)
+      const int d0 = C::MX ? (ks / 2) * 32 + 8 * c + 4 * (ks & 1) : ks * 16 + 2 * c;
+      const int d1 = C::MX ? d0 + 2 : d0 + 8;
+      qf[ks][0] = live ? *reinterpret_cast<const uint32_t*>(row + d0) : 0;
+      qf[ks][1] = live ? *reinterpret_cast<const uint32_t*>(row + d1) : 0;
+    }
+    return true;
+  };
+  int tiles = 0;                                // steps so far
+  const uint32_t k16 = C::MX ? sixteen() : 0;
+  // the warps go on together or not at all, also when one of them has given up
+  bool stop = consumers_any<C::WARPS>(!load_q(0));
+  for (int n = 0; !stop; ++n) {
+    const FewItem& it = items[n & 1];
+    const int cnt = it.cnt;
+    int pos[2], first[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rho = 2 * c + e;
+      pos[e] = rho < R ? it.pos0 + rho / G : -1;
+      first[e] = (p.a.window && pos[e] >= p.a.window) ? pos[e] + 1 - p.a.window : 0;
+    }
+    float o[MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+    for (int i = 0; i < cnt; ++i, ++tiles) {
+      const int s = tiles % C::STAGES;
+      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) break;
+      __syncwarp();
+      const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
+      const uint8_t* st = smem + s * C::STAGE;
+      const uint32_t kb = smem_u32(st), vb = kb + C::KV;
+      const uint32_t mask = page_mask[s];
+      // every row of the block sees every token of this warp
+      const bool whole = tok0 + ST - 1 <= it.pmin && (tok0 >= it.first_all || tok0 + ST <= p.a.sinks) &&
+                         mask == (1u << in_tile) - 1u;
+      if (tok0 <= it.pmax) {
+        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};      // of every other product
+        if constexpr (!C::MX) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t r[4];
+            ldsm4(kv_addr<C>(kb, loc0 + (lane & 15), 2 * ks + (lane >> 4)), r);
+            mma_16816(ks & 1 ? sd : sc, r, qf[ks][0], qf[ks][1]);
+          }
+        } else {
+          // Tokens whose scales one factor does not hold have a copy of the code to themselves: a branch inside would keep
+          // loads, conversions and products of neighbouring blocks apart.
+          const uint8_t* scales = st + 2 * C::KV;
+          uint32_t sw[2], most = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = loc0 + g + 8 * h;
+            sw[h] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
+                             : *reinterpret_cast<const uint16_t*>(scales + t * 2);
+            most |= __vcmpgtu4(sw[h], kScaleFits * 0x01010101u);
+          }
+          auto scores = [&](auto large) {
+#pragma unroll
+            for (int bl = 0; bl < D / 32; ++bl) {
+              uint32_t x[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w0, w1;
+                const uint32_t at = kv_addr<C>(kb, loc0 + g + 8 * h, 2 * bl + (c >> 1)) + 8 * (c & 1);
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at) : "memory");
+                const uint32_t by = (sw[h] >> (8 * bl)) & 255u;
+                const uint32_t f = (large.value ? scale_bits(by) : (by + 120u) << 7) * 0x10001u;
+                x[0][h] = mul_bf16x2(e4m3_pair(w0, w0, kCodes01, k16), f);
+                x[0][2 + h] = mul_bf16x2(e4m3_pair(w0, w0, kCodes23, k16), f);
+                x[1][h] = mul_bf16x2(e4m3_pair(w1, w1, kCodes01, k16), f);
+                x[1][2 + h] = mul_bf16x2(e4m3_pair(w1, w1, kCodes23, k16), f);
+                if (large.value) {
+                  const uint32_t f2 = scale_rest(by) * 0x10001u;
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) x[e][h] = mul_bf16x2(x[e][h], f2), x[e][2 + h] = mul_bf16x2(x[e][2 + h], f2);
+                }
+              }
+              mma_16816(sc, x[0], qf[2 * bl][0], qf[2 * bl][1]);
+              mma_16816(sd, x[1], qf[2 * bl + 1][0], qf[2 * bl + 1][1]);
+            }
+          };
+          if (__any_sync(0xffffffffu, most != 0)) scores(std::true_type{});
+          else scores(std::false_type{});
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] = (sc[e] + sd[e]) * scale;
+
+        // ---- what the rows do not see ----
+        uint32_t drop = 0, alone = 0;            // of this warp's tokens: left out of the product; added one by one
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int loc = g + 8 * (e >> 1), t = tok0 + loc;
+            const bool there = (mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u;
+            const bool see = there && t <= pos[e & 1] && (t >= first[e & 1] || t < p.a.sinks);
+            sc[e] = see ? sc[e] : -INFINITY;
+          }
+          // A weight of zero does not hide a value that is not finite: the product leaves out what no row sees, and
+          // what only some rows see where it is not finite.
+          const int t = tok0 + lane;
+          const bool there = lane < ST && ((mask >> ((loc0 + lane) >> min(p.page_log2, 6))) & 1u);
+          const bool any = there && t <= it.pmax && (t >= it.first_any || t < p.a.sinks);
+          const bool all = any && t <= it.pmin && (t >= it.first_all || t < p.a.sinks);
+          drop = __ballot_sync(0xffffffffu, lane < ST && !any);
+          alone = __ballot_sync(0xffffffffu, any && !all);
+          for (uint32_t some = alone; some; some &= some - 1) {
+            const int loc = __ffs(some) - 1;
+            bool fine = true;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+              fine = fine && isfinite(value_at<C>(st + C::KV, st + 2 * C::KV + C::SC, loc0 + loc, lane + 32 * e));
+            if (__all_sync(0xffffffffu, fine)) alone &= ~(1u << loc);
+          }
+          drop |= alone;
+        }
+
+        // the values' codes, under way while the weights are worked out: thread (g, c) has the D/8 values from g D/8 on of its
+        // four tokens; product j takes the 2j-th of each as its row g, and the next as its row g + 8
+        uint32_t w[4][D / 32], by[4];
+        if constexpr (C::MX) {
+          const uint8_t* scales = st + 2 * C::KV + C::SC;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = loc0 + 2 * c + (e & 1) + 8 * (e >> 1);
+            if constexpr (D == 128) {
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                           : "r"(kv_addr<C>(vb, tk, g)) : "memory");
+            } else {
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
+                           : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
+            }
+            by[e] = scales[tk * (D / 32) + g / (256 / D)];
+          }
+        }
+        // ---- softmax ----
+        float mx[2], base[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(sc[e], sc[2 + e]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+          mx[e] = fmaxf(mx[e], m[e]);
+          base[e] = mx[e] == -INFINITY ? 0.f : mx[e];
+        }
+        if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+          const float k0 = ex2(m[0] - base[0]), k1 = ex2(m[1] - base[1]);
+          l[0] *= k0;
+          l[1] *= k1;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            o[j][0] *= k0;
+            o[j][1] *= k1;
+            o[j][2] *= k0;
+            o[j][3] *= k1;
+          }
+          m[0] = mx[0];
+          m[1] = mx[1];
+        }
+        // the weights are rounded to bf16 for the second product; the sum takes the rounded ones, so that a single large
+        // weight divides out exactly
+        const uint32_t w0 = bf16x2(ex2(sc[0] - base[0]), ex2(sc[1] - base[1]));
+        const uint32_t w1 = bf16x2(ex2(sc[2] - base[0]), ex2(sc[3] - base[1]));
+        l[0] += bf16_lo(w0) + bf16_lo(w1);
+        l[1] += bf16_hi(w0) + bf16_hi(w1);
+        const uint32_t p0 = transposed(w0), p1 = transposed(w1);
+
+        // ---- weighted values ----
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (drop) {
+          keep0 = ((drop >> (2 * c)) & 1u ? 0u : 0xffffu) | ((drop >> (2 * c + 1)) & 1u ? 0u : 0xffff0000u);
+          keep1 = ((drop >> (2 * c + 8)) & 1u ? 0u : 0xffffu) | ((drop >> (2 * c + 9)) & 1u ? 0u : 0xffff0000u);
+        }
+        if constexpr (!C::MX) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            uint32_t r[4];
+            ldsm4t(kv_addr<C>(vb, loc0 + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)), r);
+            if (drop) r[0] &= keep0, r[1] &= keep0, r[2] &= keep1, r[3] &= keep1;
+            mma_16816(o[j], r, p0, p1);
+          }
+        } else {
+          const bool large = max(max(by[0], by[1]), max(by[2], by[3])) > kScaleFits;
+          auto values = [&](auto rare) {         // rare: some scale is large, or some token left out
+            auto fac = [&](uint32_t b) { return rare.value ? scale_bits(b) : (b + 120u) << 7; };
+            const uint32_t f0 = fac(by[0]) | fac(by[1]) << 16, f1 = fac(by[2]) | fac(by[3]) << 16;
+            uint32_t r0 = 0, r1 = 0;
+            if (rare.value) r0 = scale_rest(by[0]) | scale_rest(by[1]) << 16, r1 = scale_rest(by[2]) | scale_rest(by[3]) << 16;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              uint32_t x[4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                constexpr uint32_t kSel[4] = {0xC480, 0xD591, 0xE6A2, 0xF7B3};    // the code of that number of either word
+                const int at = 2 * j + h;
+                x[h] = mul_bf16x2(e4m3_pair(w[0][at / 4], w[1][at / 4], kSel[at & 3], k16), f0);
+                x[2 + h] = mul_bf16x2(e4m3_pair(w[2][at / 4], w[3][at / 4], kSel[at & 3], k16), f1);
+                if (rare.value) x[h] = mul_bf16x2(x[h], r0) & keep0, x[2 + h] = mul_bf16x2(x[2 + h], r1) & keep1;
+              }
+              mma_16816(o[j], x, p0, p1);
+            }
+          };
+          if (__any_sync(0xffffffffu, large || drop != 0)) values(std::true_type{});
+          else values(std::false_type{});
+        }
+        for (; alone; alone &= alone - 1) {
+          const int loc = __ffs(alone) - 1, t = tok0 + loc;
+          const uint32_t both = __shfl_sync(0xffffffffu, loc & 8 ? w1 : w0, (loc & 7) * 4 + c);
+          const bool see0 = t <= pos[0] && (t >= first[0] || t < p.a.sinks);
+          const bool see1 = t <= pos[1] && (t >= first[1] || t < p.a.sinks);
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float v = value_at<C>(st + C::KV, st + 2 * C::KV + C::SC, loc0 + loc,
+                                          C::MX ? g * (D / 8) + 2 * j + h : j * 16 + g + 8 * h);
+              if (see0) o[j][2 * h] = fmaf(bf16_lo(both), v, o[j][2 * h]);
+              if (see1) o[j][2 * h + 1] = fmaf(bf16_hi(both), v, o[j][2 * h + 1]);
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---------------- the warps' parts joined, in the order of their tokens ----------------
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+      if (g == 0) sums[warp][2 * c + e] = make_float2(m[e], l[e]);
+    }
+    const int piece = it.piece, pieces = it.pieces, hk = it.hk;
+    const long long b = it.b;
+    const bool more = load_q(n + 1);              // on their way while this item ends
+    stop = consumers_any<C::WARPS>(!more || *abort);
+    float top[2], tl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      top[e] = -INFINITY, tl[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) top[e] = fmaxf(top[e], sums[w][2 * c + e].x);
+      const float base = top[e] == -INFINITY ? 0.f : top[e];
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) tl[e] += ex2(sums[w][2 * c + e].x - base) * sums[w][2 * c + e].y;
+      const float f = ex2(m[e] - base);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[j][e] *= f, o[j][2 + e] *= f;
+    }
+    // ((0 + 2) + (1 + 3)): the upper two warps hand theirs to the lower two, those one to the other
+#pragma unroll
+    for (int far = 2; far; far >>= 1) {
+      float4* mine = reinterpret_cast<float4*>(join) + (warp & (far - 1)) * MT * 32 + lane;
+      if (warp >= far && warp < 2 * far) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) mine[j * 32] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      }
+      named_bar_sync(1, C::WARPS * 32);
+      if (warp < far) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const float4 v = mine[j * 32];
+          o[j][0] += v.x, o[j][1] += v.y, o[j][2] += v.z, o[j][3] += v.w;
+        }
+      }
+      named_bar_sync(1, C::WARPS * 32);
+    }
+    if (warp == 0 && !*abort) {
+      const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rho = 2 * c + e;
+        if (rho >= R) continue;
+        const bool one = pieces == 1;
+        const float inv = !one ? 1.f : tl[e] == 0.f ? 0.f : 1.f / tl[e];
+        const int r = rho / G;
+        uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
+#pragma unroll
+        for (int j = 0; j < MT; j += 2) {
+          // of products j and j + 1: MX four columns in a row, else g, g + 8, g + 16 and g + 24 of 32
+          const float v[4] = {o[j][e] * inv, o[j][2 + e] * inv, o[j + 1][e] * inv, o[j + 1][2 + e] * inv};
+          if (C::MX) {
+            const int d = g * (D / 8) + 2 * j;
+            if (one) *reinterpret_cast<uint2*>(out + d) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+            else *reinterpret_cast<float4*>(part_of(p, at, D, rho, d / 4)) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int d = j * 16 + g + 8 * k;
+              if (one) out[d] = (uint16_t)bf16x2(v[k], 0.f);
+              else part_of(p, at, D, rho, d / 4)[d % 4] = v[k];
+            }
+          }
+        }
+        if (!one && g == 0) *sums_of(p, at, rho) = make_float2(top[e], tl[e]);
+      }
+    }
+    if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__((C::WARPS + 1) * 32, C::CTAS)
 paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const PagedArgs p) {
   constexpr int D = C::D, ST = C::ST, NT = D / 8;
@@ -227,6 +561,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   }
 
   // ---------------- consumers ----------------
+  if constexpr (C::EIGHT) {
+    consume_eight<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
+    return;
+  }
   const int g = lane >> 2, c = lane & 3;
   const float scale = p.a.scale * 1.4426950408889634f;
   uint32_t qf[D / 16][4];
@@ -654,9 +992,8 @@ static size_t part_rows(const moe_attention* a, int rows, int max_len) {
   return pieces == 1 ? 0 : (size_t)a->B * a->Hq * rows * pieces;
 }
 
-template <int D, bool MX>
-static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  using C = PagedCfg<D, MX>;
+template <class C>
+static int launch_cfg(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
   CUtensorMap km, vm;
   const int box = std::min(cache->page_size, kTileTok);
   const CUtensorMapSwizzle swizzle = C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
@@ -665,15 +1002,21 @@ static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_
   auto kern = paged_attention_kernel<C>;
   if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM))) return rc;
   const long long items = (long long)p.a.B * p.a.Hkv * p.max_pieces;
-  return launch_pdl(kern, dim3((unsigned)std::min(items, 2ll * num_sms())), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
+  return launch_pdl(kern, dim3((unsigned)std::min(items, (long long)C::CTAS * num_sms())), dim3((C::WARPS + 1) * 32), C::SMEM, st, km, vm, p);
+}
+
+template <int D, bool EIGHT>
+static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
+  return cache->format == MOE_KV_MXFP8 ? launch_cfg<PagedCfg<D, true, EIGHT>>(p, cache, st)
+                                       : launch_cfg<PagedCfg<D, false, EIGHT>>(p, cache, st);
 }
 
 static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  const bool mx = cache->format == MOE_KV_MXFP8, d64 = p.a.D == 64;
+  const bool d64 = p.a.D == 64;
   int rc;
   if (p.tile_log2 != 6) rc = launch_paged_tc(p, cache, st);
-  else if (d64) rc = mx ? launch_few<64, true>(p, cache, st) : launch_few<64, false>(p, cache, st);
-  else rc = mx ? launch_few<128, true>(p, cache, st) : launch_few<128, false>(p, cache, st);
+  else if (p.R <= 8) rc = d64 ? launch_few<64, true>(p, cache, st) : launch_few<128, true>(p, cache, st);
+  else rc = d64 ? launch_few<64, false>(p, cache, st) : launch_few<128, false>(p, cache, st);
   if (rc || p.max_pieces == 1) return rc;
   const int R = p.R;
   return launch_pdl(d64 ? paged_join_kernel<64> : paged_join_kernel<128>,
