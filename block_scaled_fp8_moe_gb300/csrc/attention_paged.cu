@@ -4,17 +4,18 @@
 // Bound: HBM. Every visible key and value is read once for all rows and all heads of a group; per key and kv head that
 // is 4 D bytes (bf16) or 2.06 D (MXFP8) against 4 D R flops, R = rows * Hq / Hkv: far above what CUDA cores do at full
 // bandwidth (R = 8 would need 54 of their ~75 TFLOP/s), so both products run on the tensor cores. This file's kernel takes
-// up to 16 rows, as m16n8k16 with the rows as M (a tcgen05 product has at least 64); more rows go to
-// attention_paged_tc.cu. Pieces of both are joined here.
+// up to 16 rows, with m16n8k16: up to 8 rows as its columns, more as its M (a tcgen05 product has at least 64 rows); above 16
+// they go to attention_paged_tc.cu. Pieces of both are joined here.
 //
-// Resident blocks (two a multiprocessor) take item after item, one piece of one (sequence, kv head): a producer warp streams
-// pages by TMA through a ring of 64-token stages and runs ahead into the next item, four warps consume it, 16 tokens of a
-// stage each. Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
+// Resident blocks (two to four a multiprocessor) take item after item, one piece of one (sequence, kv head): a producer warp
+// streams pages by TMA through a ring of 64-token stages and runs ahead into the next item, four warps consume it, 16 tokens
+// of a stage each. Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
 // until an item's end.
 //
-// One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 200 us, 6.3 TB/s. 160 rows of 64
-// heads over 8 of 64, a window of 1024 and 4 first tokens: 70 us, 4.8 TB/s (17 steps a row leave an item little to run
-// ahead of). One sequence's rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
+// One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 196 us, 6.4 TB/s. 160 rows of 64
+// heads over 8 of 64, a window of 1024 and 4 first tokens: 63 us, 5.4 TB/s (17 steps a row leave an item little to run
+// ahead of). 256 rows over 4096 MXFP8 tokens: 441 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
+// rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -50,14 +51,17 @@ template <int D_, bool MX_, bool EIGHT_>
 struct PagedCfg {
   static constexpr int D = D_;
   static constexpr bool MX = MX_, EIGHT = EIGHT_;                  // EIGHT: up to 8 rows, as a product's columns
-  static constexpr int CTAS = EIGHT && MX ? 3 : 2;                 // blocks of a multiprocessor
+  // Blocks of a multiprocessor. Up to 16 rows take 168 registers, up to 8 rows 128 or less. Measured with 2, 3 and 4 blocks:
+  // 256 sequences of 4096 tokens, 32 heads over 8 of 128, MXFP8 651 (16 rows' code), 441, 456 us; 64 over 8 of 64, MXFP8
+  // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us.
+  static constexpr int CTAS = !EIGHT ? 2 : MX && D == 64 ? 4 : 3;
   static constexpr int WARPS = 4, ST = kTileTok / WARPS;           // tokens of a stage that a warp takes
   static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
   static constexpr int ROWB = MX ? D : 128;                        // bytes of a row in a column block
   static constexpr int KV = kTileTok * D * (MX ? 1 : 2);           // bytes of a stage's keys, or values
   static constexpr int SC = MX ? kTileTok * D / 32 : 0;
   static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
-  static constexpr int STAGES = (CTAS == 3 ? 65536 : 98304) / STAGE;
+  static constexpr int STAGES = (CTAS == 4 ? 45056 : CTAS == 3 ? 65536 : 98304) / STAGE;
   static constexpr int PITCH = D + 4;                              // floats of a row in the join buffer
   static constexpr int JOIN = 2 * 8 * PITCH * 4;                   // of two warps 8 rows at a time
   static constexpr int SMEM = STAGES * STAGE + JOIN + 1024;
