@@ -5,11 +5,15 @@
 // softmax weights P as bf16 over S's own columns, O += P V with P read from Tensor Memory.
 //
 // A block has two tiles of 128 rows that share their keys: two heads of a group, or where a group has an odd number of
-// heads, 256 rows of one. While one tile's weights are computed (one warpgroup each, a thread per row), the tensor
+// heads, 256 rows of one. (Where there are few tiles, a block has one.) While one tile's weights are computed (one warpgroup each, a thread per row), the tensor
 // cores work on the other's products:  PV0(i) QK0(i+1) | PV1(i) QK1(i+1).
 // Blocks stay (one an SM) and take one item after the other, so that the next item's loads and first products run under
-// the last one's end. The output is rescaled only when a row's maximum has grown by more than 2^8 since the last time (weights of up to 256
-// are as exact in bf16 as those up to 1), so that the softmax warps seldom touch it.
+// the last one's end. The output is rescaled only when a row's maximum has grown by more than 2^8 since the last time
+// (weights of up to 256 are as exact in bf16 as those up to 1), so that the softmax warps seldom touch it.
+//
+// A step of 128 keys takes two tiles about 2650 cycles, of which the products run 2048; an item's end 4000 to 5000, in which
+// none runs. Three prompts of 12288 tokens together, 32 heads of 128, a window of 4096: 382 us, 1.24 PFLOP/s of visible pairs;
+// one of 8192 without a window 330 us, 1.67 PFLOP/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -144,7 +148,7 @@ struct Item {
   }
 };
 
-template <int D>
+template <int D, bool ONE>                // ONE: a block has one tile alone (p.pair is 1 too)
 __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const PrefillArgs p) {
@@ -208,7 +212,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     // ---------------- items and loads ----------------
     if (warp == 8) {
       const int per_item = p.pair ? kTileM : 2 * kTileM;
-      const int head_items = p.pair ? p.a.Hq / 2 : p.a.Hq;
+      const int head_items = p.pair && !ONE ? p.a.Hq / 2 : p.a.Hq;
       int kv = 0, qs = 0;                       // tiles of keys or values, and pairs of tiles of queries, loaded so far
       bool ok = true;
       for (int n = 0; ok; ++n) {
@@ -242,7 +246,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           }
         }
         if (n >= 2 && !wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
-        const int slot[8] = {sp.q0, sp.qn, sp.k0, sp.kn, want * per_item, (int)(idx % (unsigned)head_items) * (p.pair ? 2 : 1), found, 0};
+        const int slot[8] = {sp.q0, sp.qn, sp.k0, sp.kn, want * per_item, (int)(idx % (unsigned)head_items) * (p.pair && !ONE ? 2 : 1), found, 0};
         if (lane == 0) {
 #pragma unroll
           for (int i = 0; i < 7; ++i) slots[n & 1][i] = slot[i];
@@ -254,8 +258,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         if (it.tiles == 0) continue;
         if (qs > 0 && !wait(&q_empty, (qs - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full, 2 * C::TILE);
-          for (int x = 0; x < 2; ++x)
+          mbar_arrive_expect_tx(&q_full, (2 - ONE) * C::TILE);
+          for (int x = 0; x < 2 - ONE; ++x)
             for (int d = 0; d < C::HALVES; ++d)
               tma_load_3d(smem + x * C::TILE + d * kTileM * 128, &qmap, d * 64, p.pair ? it.h0 + x : it.h0,
                           it.s.q0 + it.row_of(p, x), &q_full);
@@ -344,7 +348,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         ++qs;
         // S lies over the last item's weights: products are executed in the order of their issue
         qk(0, kv % C::STAGES, it.short_sinks);
-        qk(1, kv % C::STAGES, it.short_sinks);
+        if (!ONE) qk(1, kv % C::STAGES, it.short_sinks);
         release(&kv_empty[kv % C::STAGES]);
         if (it.tiles == 1) release(&q_empty);
         const Edges e0 = it.edges(p, 0), e1 = it.edges(p, 1);
@@ -356,13 +360,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           ok = wait(&v_clean[vs], ((kv + 1) / C::STAGES) & 1, DEV_TIMEOUT_FULL);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            if (x == 1 && ONE) break;
             if (!ok || !(ok = wait(&p_full[x][0], step & 1, DEV_TIMEOUT_ACCUM))) break;
             tc_fence_after();
             pv(x, 0, vs, i > 0, edge[x] && split[x], brief);
             if (!(ok = wait(&p_full[x][1], step & 1, DEV_TIMEOUT_ACCUM))) break;
             tc_fence_after();
             if (!brief) pv(x, 1, vs, true, edge[x] && split[x], false);
-            if (x == 1) release(&kv_empty[vs]);
+            if (x == 1 || ONE) release(&kv_empty[vs]);
             release(&o_full[x]);
             if (i + 1 < it.tiles) {
               if (x == 0 && !(ok = have(kv + 2))) break;
@@ -459,6 +464,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     int step = 0;                               // steps so far
     bool ok = true;
     for (int n = 0; ok && item_there(n); ++n) {
+      if (x == 1 && ONE) {
+        item_done(n);
+        continue;
+      }
       int tiles, sink_tiles, win_shift, pos, first;
       bool split;
       Edges edges;
@@ -687,6 +696,12 @@ static int rows_map(CUtensorMap* m, const void* base, int D, int heads, int rows
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The most items that there can be: every sequence may end in a part of a tile.
+static long long items_of(const PrefillArgs& p, bool one) {
+  const int rows = one || p.pair ? kTileM : 2 * kTileM;
+  return ((long long)p.Tq / rows + p.a.B) * (!one && p.pair ? p.a.Hq / 2 : p.a.Hq);
+}
+
 template <int D>
 static int launch_prefill(const PrefillArgs& p, cudaStream_t st) {
   CUtensorMap qm, km, vm;
@@ -695,12 +710,17 @@ static int launch_prefill(const PrefillArgs& p, cudaStream_t st) {
   if (!rc) rc = p.Tk ? rows_map(&km, p.k, D, p.a.Hkv, p.Tk, p.k_stride) : rows_map(&km, p.q, D, p.a.Hq, p.Tq, p.q_stride);
   if (!rc) rc = p.Tk ? rows_map(&vm, p.v, D, p.a.Hkv, p.Tk, p.v_stride) : rows_map(&vm, p.q, D, p.a.Hq, p.Tq, p.q_stride);
   if (rc) return rc;
-  auto kern = prefill_attention_kernel<D>;
+  // Two tiles a block take 2650 cycles a step, one alone about 1900: one each where there are blocks enough for it (one
+  // head, 2048 tokens of 128: 24 us against 29; 32 heads, 128 tokens: 6.9 against 8.7).
+  PrefillArgs args = p;
+  const bool one = items_of(p, true) <= num_sms();
+  if (one) args.pair = 1;
+  auto kern = one ? prefill_attention_kernel<D, true> : prefill_attention_kernel<D, false>;
   if ((rc = ensure_smem_limit(reinterpret_cast<const void*>(kern), PrefillCfg<D>::SMEM))) return rc;
-  const int per_block = p.pair ? kTileM : 2 * kTileM;
-  const long long items = ((long long)p.Tq / per_block + p.a.B) * (p.pair ? p.a.Hq / 2 : p.a.Hq);     // at most
+  const long long items = items_of(p, one);
   if (items >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  return launch_pdl(kern, dim3((unsigned)std::min(items, (long long)num_sms())), dim3(PrefillCfg<D>::THREADS), PrefillCfg<D>::SMEM, st, qm, km, vm, p);
+  return launch_pdl(kern, dim3((unsigned)std::min(items, (long long)num_sms())), dim3(PrefillCfg<D>::THREADS),
+                    PrefillCfg<D>::SMEM, st, qm, km, vm, args);
 }
 
 }  // namespace moe

@@ -132,6 +132,22 @@ def test_a_value_that_is_not_finite_reaches_its_column_alone():
     assert np.isposinf(got[10:, :, 7]).all() and np.isfinite(got[:10]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 4), (20, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 1), (100, 5), (129, 200)])
+def test_blocks_of_two_tiles(window, sinks, Hq, Hkv, D):
+    """Enough tiles for blocks to take two at a time: two heads of a group, or 256 rows where a group's heads are odd."""
+    p = Prompts([1, 0, 130, 7, 128, 63, 0, 257, 2], Hq, Hkv, D, seed=Hq)
+    p.check(window, sinks)
+    p.v[400, :, 5] = float("inf")                 # prompt 7's key 71
+    got, (want, mag) = _np(p.run(window, sinks)), p.oracle(window, sinks)
+    rows = np.isfinite(want[:, 0, 5])
+    assert not rows.all() and np.array_equal(np.isfinite(got[:, :, 5]), np.isfinite(want[:, :, 5]))
+    keep = [d for d in range(D) if d != 5]
+    with np.errstate(invalid="ignore"):
+        assert np.all(np.abs(got - want)[:, :, keep] <= A.attention_tolerance(want, mag)[:, :, keep])
+
+
 @pytest.mark.parametrize("D,Hq,Hkv", [(64, 64, 8), (128, 32, 4), (128, 33, 11)])
 def test_more_work_than_the_gpu_has_room_for(D, Hq, Hkv):
     """Several times as many blocks of rows as multiprocessors, with values that are not finite here and there: sampled
