@@ -434,7 +434,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             // half of the lanes take their second 8 codes first: the lanes of a load, and of a store, are then in different banks
             const uint32_t flip = ((lane >> 3) ^ (D == 128 ? ch >> 2 : 0)) & 1;
             // a thread's rows are RPT apart, a multiple of 8: their chunks are turned alike
-            const uint32_t from = smem_u32(src) + row0 * D + ch * 16 + flip * 8, sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
+            const uint32_t from = smem_u32(src) + row0 * D + ch * 16 + flip * 8;
+            const uint32_t sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
             const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 + ((((2 * ch + flip) & 7) ^ (row0 & 7)) << 4);
             static_assert(RPT % 8 == 0, "turned alike");
             uint32_t top = 0;
@@ -470,6 +471,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                 const int row = row0 + r;
                 const uint32_t by = src[kStepTok * D + row * (D / 32) + ch / 2];
                 if (by <= kScaleFits) continue;
+                if (!((info.y >> (row >> min(p.page_log2, 7))) & 1)) {       // of a page that was not loaded: whatever was here
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + r * 128), "r"(0) : "memory");
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"((to + r * 128) ^ 16), "r"(0) : "memory");
+                  continue;
+                }
                 const uint32_t f = scale_bits(by) * 0x10001u, f2 = scale_rest(by) * 0x10001u;
                 bool bad = false;
 #pragma unroll 1
