@@ -140,7 +140,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     mbar_init(&outs_read, 256);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 10 + C::FEEDERS * C::GROUPS);  // the warps of the products, of the queries, of the feeding, of the softmax
+      // the warps of the products, of the queries, of the feeding, of the softmax
+      mbar_init(&w_empty[i], 10 + C::FEEDERS * C::GROUPS);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i][0], 128);
       mbar_init(&p_full[i][1], 128);
@@ -497,6 +498,18 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             if (lane == 0) mbar_arrive(&raw_empty[st]);
           } else if (edge) {
             uint4* v = reinterpret_cast<uint4*>(dst);
+            // places of pages that were not loaded hold whatever was here
+            const int rows_of = min(p.page_size, kStepTok);
+            uint32_t gone = ~(uint32_t)info.y & ((2u << (kStepTok / rows_of - 1)) - 1u);
+            if (gone) {
+              for (; gone; gone &= gone - 1) {
+                const int row = (__ffs(gone) - 1) * rows_of;
+                for (int h = 0; h < C::HALVES; ++h)
+                  for (int a = lane; a < rows_of * 8; a += 32) v[(h * kStepTok + row) * 8 + a] = make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
             // zero times a value that is not finite is NaN, and stays in the sum
             uint32_t sum = 0;
 #pragma unroll 8

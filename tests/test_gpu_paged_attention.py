@@ -107,6 +107,20 @@ def test_long_sequences_in_many_pieces(mx, D):
     Paged([9001, 4097], 1, 4, 2, D, 64, mx, seed=5).check(4100, 33)
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,Hq,Hkv", [(1, 8, 1), (2, 8, 1), (4, 8, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_short_sequences_where_a_kernel_has_left_nan(D, rows, Hq, Hkv, mx):
+    """Pages that a short sequence does not have leave their places in a block's shared memory as they were."""
+    p = Paged([5, 17, 40, 70, 100, 129], rows, Hq, Hkv, D, 16, mx, seed=D + rows)
+    nan = torch.full((20000, Hkv, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+    q, cu = torch.zeros((20000, Hq, D), device="cuda", dtype=torch.bfloat16), torch.tensor([0, 20000], dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        p.B.moe_prefill_attention(q, nan, nan, cu, window=300)
+        p.check()
+        p.check(30, 3)
+
+
 def test_one_large_score_takes_all():
     """Scores far apart, and growing along the sequence, so that the running maximum moves again and again."""
     for mx in (False, True):
