@@ -437,7 +437,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             // a thread's rows are RPT apart, a multiple of 8: their chunks are turned alike
             const uint32_t from = smem_u32(src) + row0 * D + ch * 16 + flip * 8;
             const uint32_t sc = smem_u32(src) + kStepTok * D + row0 * (D / 32) + ch / 2;
-            const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 + ((((2 * ch + flip) & 7) ^ (row0 & 7)) << 4);
+            const uint32_t to = smem_u32(dst) + (ch >> 2) * kStepTok * 128 + row0 * 128 +
+                                ((((2 * ch + flip) & 7) ^ (row0 & 7)) << 4);
             static_assert(RPT % 8 == 0, "turned alike");
             uint32_t top = 0;
 #pragma unroll 1
@@ -446,7 +447,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[j][0]), "=r"(w[j][1]) : "r"(from + (r + j * RPT) * D));
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[j][2]), "=r"(w[j][3]) : "r"((from ^ 8) + (r + j * RPT) * D));
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                             : "=r"(w[j][2]), "=r"(w[j][3]) : "r"((from ^ 8) + (r + j * RPT) * D));
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(by[j]) : "r"(sc + (r + j * RPT) * (D / 32)));
               }
 #pragma unroll
