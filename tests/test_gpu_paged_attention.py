@@ -108,6 +108,14 @@ def test_long_sequences_in_many_pieces(mx, D):
 
 
 @pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,Hq,Hkv", [(3, 8, 1), (9, 16, 1)])
+def test_many_rows_where_the_pieces_of_a_sequence_change(rows, Hq, Hkv, mx):
+    """8192 tokens and around: pieces of twice as many steps; 144 rows are two blocks of rows."""
+    Paged([8064, 8065, 8192, 8193, 8320, 700], rows, Hq, Hkv, 64, 64, mx, seed=rows).check()
+    Paged([8192, 8193, 9000], rows, Hq, Hkv, 64, 64, mx, seed=rows + 1).check(8100, 130)
+
+
+@pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("rows,Hq,Hkv", [(1, 8, 1), (2, 8, 1), (4, 8, 1)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_short_sequences_where_a_kernel_has_left_nan(D, rows, Hq, Hkv, mx):
