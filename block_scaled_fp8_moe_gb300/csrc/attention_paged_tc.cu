@@ -366,7 +366,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     } else if (warp == 10) {
       // ---------------- queries ----------------
       // Into the layout of a swizzled TMA tile. Rows beyond R keep what was there: a row of the products depends on its own
-      // query alone.
+      // query alone, and the softmax asks live rows alone.
       int qs = 0;
       bool ok = true;
       for (int n = 0; ok && item_there(n); ++n) {
@@ -623,7 +623,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           for (int f = 0; f < 4; ++f)
             m4[f] = max3(m4[f], __uint_as_float(s[e + 2 * f]), __uint_as_float(s[e + 2 * f + 1]));
         const float mn = max3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), m);
-        if (__any_sync(0xffffffffu, (mn - m) * c > kGrow)) {             // (-inf) - (-inf): no
+        // (-inf) - (-inf): no. Rows that nobody has hold an earlier kernel's leftovers and have no say: where the others' maximum
+        // moves decides how their weights round.
+        if (__any_sync(0xffffffffu, live && (mn - m) * c > kGrow)) {
           if (any) {
             if (!(ok = wait(&o_full[x], (done - 1) & 1, DEV_TIMEOUT_ACCUM))) break;
             tc_fence_after();

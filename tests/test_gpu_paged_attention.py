@@ -417,3 +417,22 @@ def test_refusals():
             call()
         assert e.value.code == code
     assert f(p.q[:0], p.cache, t[:0], n[:0], 0).shape == (0, 2, 4, 64)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,Hq", [(17, 1), (6, 4), (5, 8), (6, 8)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_whatever_a_kernel_has_left(D, rows, Hq, mx):
+    """A block's tile of 128 queries has rows that nobody owns: what an earlier kernel left there, large queries of a
+    prompt here, must not reach the others, nor how their weights are rounded."""
+    p = Paged([3000, 777, 1025], rows, Hq, 1, D, 16, mx, seed=rows)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cu = torch.tensor([0, 20000], dtype=torch.int32, device="cuda")
+    kv = torch.randn((20000, 8, D), generator=g, device="cuda").bfloat16()
+    want = []
+    for size in (0.0, 1.0, 30.0, 1000.0):
+        q = (size * torch.randn((20000, 8, D), generator=g, device="cuda")).bfloat16()
+        p.B.moe_prefill_attention(q, kv, kv, cu, window=64)
+        want.append([p.run(), p.run(300, 5)])
+    for got in want[1:]:
+        assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1])
