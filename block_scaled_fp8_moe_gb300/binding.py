@@ -31,6 +31,7 @@ EXPORTED = [
     "moe_shared_workspace_bytes", "moe_forward_shared", "moe_dead_from_survival", "moe_w2_grouped", "moe_combine",
     "moe_probe_mma_rate", "moe_quant_mxfp8_plan", "moe_experts_grouped", "moe_add_rmsnorm_mxfp8", "moe_kv_append",
     "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_prefill_attention",
+    "moe_selftest_attention_hold",
 ]
 
 MOE_FLAG_SWIGLU_DEBUG = 1
@@ -94,6 +95,7 @@ lib.moe_forward.argtypes = [_SHP] + [_P] * 9 + [ctypes.POINTER(MoeIntermediates)
 lib.moe_check_device_status.argtypes = [_P, _P]
 lib.moe_route_topk_noalloc.argtypes = [_SHP] + [_P] * 10 + [_P]
 lib.moe_selftest_timeout.argtypes = [_P, ctypes.c_uint64, _P]
+lib.moe_selftest_attention_hold.argtypes = [ctypes.c_int32]
 lib.moe_route_topk_anchored.argtypes = [_SHP] + [_P] * 11 + [_P, _SZ, _P]
 lib.moe_forward_anchored.argtypes = [_SHP] + [_P] * 10 + [ctypes.POINTER(MoeIntermediates), _P, _SZ, _P]
 lib.moe_packed_shared_w13_bytes.restype = _SZ
@@ -710,6 +712,11 @@ def moe_probe_mma_rate(iters: int, ws, mode: int = 0, stream=None) -> tuple[int,
 
 def moe_selftest_timeout(ws, limit_ns: int, stream=None) -> None:
     _check(lib.moe_selftest_timeout(_ptr(ws), int(limit_ns), _stream(stream)), "moe_selftest_timeout")
+
+
+def moe_selftest_attention_hold(load: int = -1) -> None:
+    """Test hook: which load of every block never completes in the calls that follow (-1: none)."""
+    _check(lib.moe_selftest_attention_hold(int(load)), "moe_selftest_attention_hold")
 
 
 def moe_check_device_status(ws, stream=None) -> None:

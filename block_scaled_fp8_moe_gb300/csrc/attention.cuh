@@ -34,6 +34,9 @@ inline bool status_ws_ok(void* ws, size_t ws_bytes) {
   return ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && ws_bytes >= 256;
 }
 
+// The load of each block that is told to wait for more bytes than come (none below zero), by moe_selftest_attention_hold.
+int held_load();
+
 // The keys that the row at position p sees are [0, low) and [first, p + 1), low <= first; none for p < 0.
 struct Visible {
   int low, first, end;

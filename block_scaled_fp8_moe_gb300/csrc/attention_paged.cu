@@ -19,6 +19,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "attention.cuh"
@@ -162,10 +163,16 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
+    // A wait that runs out ends the item for all lanes or none: the vote is cast where each of them is. (In one place, as `if
+    // (!__all_sync(mask, bar_wait(...)))`, the code of a step grows by 7 % of its instructions: 256 sequences of 4096 MXFP8
+    // tokens 470 us instead of 445.)
     for (int i = 0; i < cnt; ++i, ++tiles) {
       const int s = tiles % C::STAGES;
-      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) break;
-      __syncwarp();
+      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) {
+        __all_sync(0xffffffffu, false);         // told to those that go on below
+        break;
+      }
+      if (!__all_sync(0xffffffffu, true)) break;
       const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
       const uint8_t* st = smem + s * C::STAGE;
       const uint32_t kb = smem_u32(st), vb = kb + C::KV;
@@ -439,6 +446,14 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
   }
 }
 
+// Every warp comes here at its end. A wait that ran out, in whichever of them, is recorded once nobody can give up any more.
+template <class C>
+__device__ __forceinline__ void end_block(const PagedArgs& p, volatile uint32_t* abort) {
+  __syncwarp();
+  named_bar_sync(2, (C::WARPS + 1) * 32);
+  if (threadIdx.x == 0 && *abort) atomicCAS(p.status, 0u, *abort);
+}
+
 template <class C>
 __global__ void __launch_bounds__((C::WARPS + 1) * 32, C::CTAS)
 paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -528,13 +543,15 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         const bool good = want && id >= 0 && id < p.pages;
         if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        // a warp that has given up frees stages that may still be on their way
         if (issued >= C::STAGES &&
             !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
-                                                    DEV_TIMEOUT_EMPTY))))
+                                                    DEV_TIMEOUT_EMPTY) && !abort_flag)))
           break;
         if (lane == 0) {
           page_mask[s] = mask;
-          mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)));
+          mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)) +
+                                              (issued == p.hold ? 16 : 0));
         }
         __syncwarp();
         if (good) {
@@ -555,18 +572,18 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         }
       }
     }
-    // a block that gives up still waits for its copies in flight
-    if (abort_flag && lane == 0) {
-      atomicCAS(p.status, 0u, abort_flag);
+    // copies in flight end before the block does, whoever gives up and when
+    if (lane == 0)
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
         mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
-    }
+    end_block<C>(p, &abort_flag);
     return;
   }
 
   // ---------------- consumers ----------------
   if constexpr (C::EIGHT) {
     consume_eight<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
+    end_block<C>(p, &abort_flag);
     return;
   }
   const int g = lane >> 2, c = lane & 3;
@@ -615,8 +632,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
 
     for (int i = 0; i < cnt; ++i, ++tiles) {
       const int s = tiles % C::STAGES;
-      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_FULL)) break;
-      __syncwarp();
+      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, &abort_flag, DEV_TIMEOUT_FULL)) {
+        __all_sync(0xffffffffu, false);         // told to those that go on below
+        break;
+      }
+      if (!__all_sync(0xffffffffu, true)) break;
       const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
       const uint8_t* st = smem + s * C::STAGE;
       const uint32_t kb = smem_u32(st), vb = kb + C::KV;
@@ -913,6 +933,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
     }
     if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   }
+  end_block<C>(p, &abort_flag);
 }
 
 // The pieces' parts joined in order, a thread per four columns of a row, rows next to each other. Rows of one piece are
@@ -1028,9 +1049,18 @@ static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStrea
                     dim3(kJoinRows * kJoinCols), 0, st, p);
 }
 
+static std::atomic<int> hold_load{-1};
+
+int held_load() { return hold_load; }
+
 }  // namespace moe
 
 using namespace moe;
+
+extern "C" int moe_selftest_attention_hold(int32_t load) {
+  hold_load = load;
+  return MOE_OK;
+}
 
 extern "C" size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len) {
   if (!attention_ok(a) || rows < 1 || rows > 64 || max_len < 0) return 0;
@@ -1080,6 +1110,7 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.lens = seq_lens;
   p.out = out;
   p.status = static_cast<uint32_t*>(ws);
+  p.hold = held_load();
   const size_t n = part_rows(a, rows, max_len);
   p.part_o = ws_ptr<float>(ws, 256);
   p.part_ml = ws_ptr<float>(ws, 256 + align_up(n * a->D * 4, 256));

@@ -28,6 +28,7 @@ struct PagedArgs {
   const int32_t* lens;
   uint16_t* out;
   uint32_t* status;
+  int hold;                             // see held_load
   // Partial results of pieces. Rows are next to each other, because threads of a warp have rows of their own where they are
   // written and where they are joined.
   float* part_o;    // [B, Hkv, max_pieces, D / 4, R, 4]: sums of weighted values

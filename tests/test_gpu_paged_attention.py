@@ -436,3 +436,26 @@ def test_many_rows_whatever_a_kernel_has_left(D, rows, Hq, mx):
         want.append([p.run(), p.run(300, 5)])
     for got in want[1:]:
         assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1])
+
+
+def _gives_up(p, load):
+    """A call whose blocks wait for a load that does not complete: it ends, says so, and the next one is as ever."""
+    want = p.run()
+    p.B.attention_status()
+    p.B.moe_selftest_attention_hold(load)
+    try:
+        p.run()
+        with pytest.raises(p.B.MoeError) as e:
+            p.B.attention_status()
+        assert e.value.code == p.B.MOE_ERR_TIMEOUT
+    finally:
+        p.B.moe_selftest_attention_hold()
+    assert torch.equal(p.run(), want)
+    p.B.attention_status()
+
+
+@pytest.mark.parametrize("mx,D,rows", [(False, 128, 2), (False, 64, 4), (True, 64, 2), (True, 128, 4)])
+@pytest.mark.parametrize("load", [0, 3, 7])
+def test_a_wait_that_runs_out_is_reported(load, mx, D, rows):
+    """Pieces of 8 steps, one a block: the eighth is the last that a loading warp issues."""
+    _gives_up(Paged([4096] * 4, rows, 8, 2, D, 64, mx, seed=load), load)
