@@ -260,7 +260,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
                                  mask == (1u << in_tile) - 1u;
               infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
             }
-            mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D));
+            mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D) + (tile == p.hold ? 16 : 0));
           }
           __syncwarp();
           if (id >= 0) {
@@ -281,10 +281,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
         }
         steps += cnt;
       }
-      if (abort_flag)                           // copies in flight end before the block does
-        for (int j = max(0, tile - (C::MX ? C::RAWS : C::ENTRIES)); j < tile; ++j)
-          mbar_wait(&landed[j % (C::MX ? C::RAWS : C::ENTRIES)], (j / (C::MX ? C::RAWS : C::ENTRIES)) & 1, kPagedWaitNs,
-                    nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      // copies in flight end before the block does, whoever gives up and when
+      for (int j = max(0, tile - (C::MX ? C::RAWS : C::ENTRIES)); j < tile; ++j)
+        mbar_wait(&landed[j % (C::MX ? C::RAWS : C::ENTRIES)], (j / (C::MX ? C::RAWS : C::ENTRIES)) & 1, kPagedWaitNs,
+                  nullptr, nullptr, DEV_TIMEOUT_DRAIN);
     } else if (warp == 9) {
       // ---------------- products ----------------
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -359,7 +359,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           }
         }
       }
-      if (leader && abort_flag) {
+      if (leader) {                             // and so do the products
         tc_commit(&drain);
         mbar_wait(&drain, 0, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
       }

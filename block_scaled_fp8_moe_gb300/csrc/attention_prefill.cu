@@ -47,6 +47,7 @@ struct PrefillArgs {
   uint16_t* out;
   uint32_t* status;
   int pair;                             // 1: the two tiles are two heads, 0: two blocks of rows
+  int hold;                             // see held_load
 };
 
 struct Span {
@@ -270,7 +271,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           const int s = kv % C::STAGES;
           if (kv >= C::STAGES && !(ok = wait(&kv_empty[s], (kv / C::STAGES - 1) & 1, DEV_TIMEOUT_EMPTY))) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&kv_full[s], C::TILE);
+            mbar_arrive_expect_tx(&kv_full[s], C::TILE + (kv == p.hold ? 16 : 0));
             for (int d = 0; d < C::HALVES; ++d)
               tma_load_3d(ring + s * C::TILE + d * kTileN * 128, i & 1 ? &vmap : &kmap, d * 64, hk,
                           it.s.k0 + it.key_of(i / 2), &kv_full[s]);
@@ -278,11 +279,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           ++kv;
         }
       }
-      if (abort_flag) {                         // copies in flight end before the block does
-        if (qs) mbar_wait(&q_full, (qs - 1) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
-        for (int j = max(0, kv - C::STAGES); j < kv; ++j)
-          mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
-      }
+      // copies in flight end before the block does, whoever gives up and when
+      if (qs) mbar_wait(&q_full, (qs - 1) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      for (int j = max(0, kv - C::STAGES); j < kv; ++j)
+        mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
     }
     // ---------------- products ----------------
     // The whole warp goes along and one lane issues: addresses stay uniform, and so in uniform registers. (With one
@@ -374,14 +374,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
               qk(x, ks, false);
             }
           }
-          if (i + 1 < it.tiles) {
+          if (ok && i + 1 < it.tiles) {         // a stage that was not read is not given back
             release(&kv_empty[ks]);
             if (i + 2 == it.tiles) release(&q_empty);
           }
           kv += 2;
         }
       }
-      if (leader && abort_flag) {
+      if (leader) {                             // the products end before the block does, too
         tc_commit(&drain);
         mbar_wait(&drain, 0, kPrefillWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
       }
@@ -743,7 +743,7 @@ extern "C" int moe_prefill_attention(const moe_attention* a, int32_t Tq, int32_t
     return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3) return MOE_ERR_INVALID_ARG;
   const PrefillArgs p{*a, Tq, Tk, q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k ? cu_k : cu_q, out,
-                      static_cast<uint32_t*>(ws), (a->Hq / a->Hkv) % 2 == 0};
+                      static_cast<uint32_t*>(ws), (a->Hq / a->Hkv) % 2 == 0, held_load()};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a->D == 64 ? launch_prefill<64>(p, st) : launch_prefill<128>(p, st);
 }

@@ -310,8 +310,8 @@ MOE_API int moe_forward_shared(const moe_shape* shape, const uint16_t* x, const 
  * `ws` and the kernel returns; moe_check_device_status then reports MOE_ERR_TIMEOUT. No fault, no
  * hang, the context stays usable. Not part of the layer. */
 MOE_API int moe_selftest_timeout(void* ws, uint64_t limit_ns, void* stream);
-/* The same for the waits inside moe_paged_attention, which end after 1 s: in the calls that follow in this
- * process, the load-th load of every block waits for 16 bytes that never come. A block that meets it gives up: its
+/* The same for the waits inside moe_paged_attention and moe_prefill_attention, which end after 1 s: in the calls
+ * that follow in this process, the load-th load of every block waits for 16 bytes that never come. A block that meets it gives up: its
  * remaining rows are not written, the status word says MOE_ERR_TIMEOUT, the context stays usable. -1 ends this. */
 MOE_API int moe_selftest_attention_hold(int32_t load);
 

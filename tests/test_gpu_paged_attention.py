@@ -459,3 +459,11 @@ def _gives_up(p, load):
 def test_a_wait_that_runs_out_is_reported(load, mx, D, rows):
     """Pieces of 8 steps, one a block: the eighth is the last that a loading warp issues."""
     _gives_up(Paged([4096] * 4, rows, 8, 2, D, 64, mx, seed=load), load)
+
+
+@pytest.mark.parametrize("mx,D", [(False, 128), (False, 64), (True, 64), (True, 128)])
+@pytest.mark.parametrize("load", [0, 3, 7])
+def test_many_rows_a_wait_that_runs_out_is_reported(load, mx, D):
+    """Pieces of 4 steps, one a block: 8 tiles of keys and values, of which the loading warp has issued all but the held
+    one's successors when the others give up."""
+    _gives_up(Paged([4096] * 4, 6, 16, 2, D, 64, mx, seed=load), load)

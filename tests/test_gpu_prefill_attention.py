@@ -234,3 +234,23 @@ def test_refusals():
     with pytest.raises(B.MoeError):
         f(p.q, p.k, p.v, p.cu_q, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     assert f(p.q[:0], p.k[:0], p.v[:0], _cu([])).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 128), (32, 4, 64), (20, 4, 128)])
+@pytest.mark.parametrize("load", [0, 3, 10])
+def test_a_wait_that_runs_out_is_reported(load, Hq, Hkv, D):
+    """Blocks of one tile, of two heads and of 256 rows wait for a load that does not complete: the call ends, says so,
+    and the next one is as ever."""
+    p = Prompts([1100, 700], Hq, Hkv, D, seed=load)
+    want = p.run()
+    p.B.attention_status()
+    p.B.moe_selftest_attention_hold(load)
+    try:
+        p.run()
+        with pytest.raises(p.B.MoeError) as e:
+            p.B.attention_status()
+        assert e.value.code == p.B.MOE_ERR_TIMEOUT
+    finally:
+        p.B.moe_selftest_attention_hold()
+    assert torch.equal(p.run(), want)
+    p.B.attention_status()
