@@ -93,6 +93,68 @@ struct LaneRow {
   }
 };
 
+// The keys of an item that have a value that is not finite and that the product was kept from, because some row of the item
+// does not see them: 128 keys a step, a bit each. Only steps at an edge of the mask are looked over. An item of n <= 256
+// neighbouring rows has at most 7: steps that hold the end of some rows' keys (n + 126 places for its first key), the
+// beginning of their window (n + 126), the end of the first tokens (one).
+constexpr int kBadSteps = 8;
+struct BadKeys {
+  int some;
+  int j0[kBadSteps];                    // a step's first key, or -1; used from the first on
+  uint32_t keys[kBadSteps][4];
+  __device__ __forceinline__ void clear(int lane) {      // by a warp
+    if (lane < kBadSteps) j0[lane] = -1;
+    (&keys[0][0])[lane] = 0;
+    if (lane == 0) some = 0;
+  }
+  __device__ __forceinline__ void add(int j) {           // by any thread
+    for (int s = 0; s < kBadSteps; ++s) {
+      const int was = atomicCAS(&j0[s], -1, j & ~127);
+      if (was != -1 && was != (j & ~127)) continue;
+      atomicOr(&keys[s][(j & 127) / 32], 1u << (j & 31));
+      *const_cast<volatile int*>(&some) = 1;
+      return;
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(const F& f) const {
+    for (int s = 0; s < kBadSteps && j0[s] >= 0; ++s)
+      for (int w = 0; w < 4; ++w)
+        for (uint32_t m = keys[s][w]; m; m &= m - 1) f(j0[s] + 32 * w + __ffs(m) - 1);
+  }
+};
+static_assert(sizeof(BadKeys::keys) == 32 * 4, "a word a lane");
+
+// What those keys add to one row's result, by one warp, its lanes spread over D: weighted values that are not finite, whose
+// weights are above zero (however small; zero for a score of minus infinity alone). All else that the keys have is in the
+// result already. `top` is what the row's weights refer to (times log2 e), `load(j, k, v)` fetches a key, `add(i, x)` adds x
+// to the result's i-th column of the lane. The cost goes with the keys that are listed, not with the row's length.
+template <int D, class Load, class Add>
+__device__ __forceinline__ void add_not_finite(const BadKeys& bad, const LaneRow<D>& q, const Visible& see, float scale_log2,
+                                               float top, const Load& load, const Add& add) {
+  constexpr int N = D / 32;
+  float acc[N] = {};
+  uint32_t hit = 0;
+  bad.each([&](int j) {
+    if (!see.sees(j)) return;
+    LaneRow<D> k, v;
+    load(j, k, v);
+    float s = 0.f;
+#pragma unroll
+    for (int d = 0; d < N; ++d) s = fmaf(q.f[d], k.f[d], s);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    s *= scale_log2;
+    const float p = s == -INFINITY ? 0.f : fmaxf(exp2f(s - top), 1e-30f);
+#pragma unroll
+    for (int d = 0; d < N; ++d)
+      if (!isfinite(v.f[d])) acc[d] += p * v.f[d], hit |= 1u << d;
+  });
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+    if ((hit >> d) & 1u) add(d, acc[d]);
+}
+
 // One row's attention by one warp straight from the definition, its lanes spread over D, over the visible keys from j0 to
 // j1. `load(j, k, v)` fetches a key's and its value's parts and returns whether the key is there. m, l, o hold the running
 // maximum of the scores (times log2 e), the sum and the weighted values (of the lane).

@@ -31,7 +31,6 @@ constexpr uint64_t kPrefillWaitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kShort = 32;              // keys of a step that has few first tokens alone
 constexpr int kFewKeys = 512;           // rows that see fewer keep their weights in two parts
-constexpr int kBadKeys = 64;            // keys with values that are not finite that a block lists
 
 struct PrefillArgs {
   moe_attention a;
@@ -84,30 +83,24 @@ struct PrefillCfg {
   static constexpr int S0 = 0, S1 = 128, O0 = 256, O1 = 256 + D;
 };
 
-// One row's attention straight from its definition, by a warp: for rows that see a value that is not finite in a step
-// where others do not.
+// The columns of one row's result that a listed key decides, by a warp.
 template <int D>
-__device__ __noinline__ void redo_row(const PrefillArgs& p, const Span& s, int row, int h) {
+__device__ __noinline__ void finish_row(const PrefillArgs& p, const BadKeys& bad, const Span& s, int row, int h, float top) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, hk = h / (p.a.Hq / p.a.Hkv);
   const long long t = s.q0 + row;
-  const Visible see(s.kn - s.qn + row, p.a.window, p.a.sinks);
   LaneRow<D> q;
   q.load_bf16(p.q + t * p.q_stride + (long long)h * D, lane);
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  attend_keys<D>(q, see, 0, s.kn, p.a.scale * 1.4426950408889634f, m, l, o, [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
-    k.load_bf16(p.k + (long long)(s.k0 + j) * p.k_stride + (long long)hk * D, lane);
-    v.load_bf16(p.v + (long long)(s.k0 + j) * p.v_stride + (long long)hk * D, lane);
-    return true;
-  });
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (t * p.a.Hq + h) * D + lane * N);
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i)
-    out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
+  uint16_t* out = p.out + (t * p.a.Hq + h) * D + lane * N;
+  add_not_finite<D>(bad, q, Visible(s.kn - s.qn + row, p.a.window, p.a.sinks), p.a.scale * 1.4426950408889634f, top,
+                    [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
+                      k.load_bf16(p.k + (long long)(s.k0 + j) * p.k_stride + (long long)hk * D, lane);
+                      v.load_bf16(p.v + (long long)(s.k0 + j) * p.v_stride + (long long)hk * D, lane);
+                    },
+                    [&](int i, float x) { out[i] = (uint16_t)bf16x2(bf16_lo(out[i]) + x, 0.f); });
 }
 
-// Which steps of a tile are edges: some row of it does not see some key of the step that begins at j0. (Scales below
-// zero, which nobody uses, take the way of such steps throughout.)
+// Which steps of a tile are edges: some row of it does not see some key of the step that begins at j0.
 struct Edges {
   int hi, lo, low;
   __device__ __forceinline__ bool at(int j0) const { return j0 > hi || (j0 < lo && j0 > low); }
@@ -139,8 +132,8 @@ struct Item {
   __device__ __forceinline__ int row_of(const PrefillArgs& p, int x) const { return r0 + (p.pair ? 0 : x * kTileM); }
   __device__ __forceinline__ Edges edges(const PrefillArgs& p, int x) const {
     const int t0 = row_of(p, x);
-    if (t0 + kTileM > r_end || p.a.scale < 0.f) return Edges{-1, 0, 0};
-    return Edges{off + t0 + 1 - kTileN, first_of(p, off + t0 + kTileM - 1), p.a.sinks - kTileN};
+    if (t0 >= r_end) return Edges{0x7fffffff, 0, 0};      // nobody's rows
+    return Edges{off + t0 + 1 - kTileN, first_of(p, off + min(t0 + kTileM, r_end) - 1), p.a.sinks - kTileN};
   }
   // Tiles whose first row sees few keys give their weights to the product in two parts in edge steps, rounded and rest;
   // over many keys the roundings even out.
@@ -158,7 +151,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   __shared__ uint64_t w_full[2], w_empty[2], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain;
   __shared__ uint64_t kv_full[C::STAGES], kv_empty[C::STAGES], v_clean[C::STAGES];
   __shared__ int slots[2][8];                   // items: span, first row, first head, whether there is one
-  __shared__ int bad_count[2], bad_keys[2][kBadKeys];
+  __shared__ BadKeys bad[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -248,10 +241,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         }
         if (n >= 2 && !wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
         const int slot[8] = {sp.q0, sp.qn, sp.k0, sp.kn, want * per_item, (int)(idx % (unsigned)head_items) * (p.pair && !ONE ? 2 : 1), found, 0};
+        bad[n & 1].clear(lane);                 // the last item but one, whose list this was, is done
+        __syncwarp();
         if (lane == 0) {
 #pragma unroll
           for (int i = 0; i < 7; ++i) slots[n & 1][i] = slot[i];
-          bad_count[n & 1] = 0;                 // the last item but one, whose list this was, is done
           mbar_arrive(&w_full[n & 1]);
         }
         if (!found) break;                      // the later rounds have none either
@@ -388,7 +382,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     }
     // ---------------- values that are not finite ----------------
     // A weight of zero does not hide such a value in the product. Where a row of the block does not see every key of a
-    // step, they are set to zero, and the rows that do see them are listed to be computed again.
+    // step, they are set to zero and their keys listed, for the rows that do see them.
     if (warp >= 10) {
       const int tid = threadIdx.x - 320;
       int kv = 0;
@@ -439,10 +433,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
               }
               v[e] = make_uint4(z[0], z[1], z[2], z[3]);
               wrote = true;
-              if (__ffs(hits & (0xFFu << (tid & 24))) - 1 == (tid & 31)) {
-                const int at = atomicAdd(&bad_count[n & 1], 1);
-                if (at < kBadKeys) bad_keys[n & 1][at] = j0 + e / 8 % kTileN;
-              }
+              if (__ffs(hits & (0xFFu << (tid & 24))) - 1 == (tid & 31)) bad[n & 1].add(j0 + e / 8 % kTileN);
             }
           }
           if (wrote) fence_async_smem();
@@ -491,7 +482,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         // rescaled.
         auto move_base = [&]() {
           const float mn = fmaxf(m, mx);
-          if (!__any_sync(0xffffffffu, (mn - m) * c > kRescaleLog2)) return true;    // (-inf) - (-inf): no
+          // (-inf) - (-inf): no. Rows that nobody has, or that see nothing, have no say: where the others' maximum moves
+          // decides how their weights round.
+          if (!__any_sync(0xffffffffu, pos >= 0 && (mn - m) * c > kRescaleLog2)) return true;
           if (i > 0) {
             if (!wait(&o_full[x], (step - 1) & 1, DEV_TIMEOUT_ACCUM)) return false;
             tc_fence_after();
@@ -527,7 +520,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           mbar_arrive(&p_full[x][h]);
         };
         const bool edge = edges.at(j0);
-        if (edge) {
+        if (edge || turn) {
           // Hidden in Tensor Memory, 32 scores at a time: little code, and groups that all of the warp's rows see are left.
           // The row sees key j0 + e when e <= hi and (e >= lo or e < low). (Scores that a short step has not computed are
           // hidden with the rest behind the first tokens.)
@@ -615,14 +608,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       unpack2(l2, la, lb);
       const float l = la + lb;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      // Rows that see a listed key are computed again. (Every value that is not finite was listed before the last product
-      // that met it. A score that is NaN makes the sum NaN, and with it the row: that is its result.)
+      // Rows that see a listed key. (Every value that is not finite was listed before the last product that met it. A score
+      // that is NaN makes the sum NaN, and with it the row: that is its result.)
       bool again = false;
-      if (it.tiles > 0) {
-        const int listed = *reinterpret_cast<volatile int*>(&bad_count[n & 1]);
-        again = listed > kBadKeys;
+      if (it.tiles > 0 && *reinterpret_cast<volatile int*>(&bad[n & 1].some)) {
         const Visible see(live ? it.off + row : -1, p.a.window, p.a.sinks);
-        for (int i = 0; i < min(listed, kBadKeys); ++i) again = again || see.sees(bad_keys[n & 1][i]);
+        bad[n & 1].each([&](int j) { again = again || see.sees(j); });
         again = again && live && l == l;
       }
       // Through shared memory, so that a warp writes 128-byte pieces of rows: 64 columns of its 32 rows at a time, in
@@ -671,7 +662,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         __syncwarp();
       }
       for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-        redo_row<D>(p, it.s, row - ln + __ffs(rows) - 1, h);
+        finish_row<D>(p, bad[n & 1], it.s, row - ln + __ffs(rows) - 1, h,
+                      __shfl_sync(0xffffffffu, m * c, __ffs(rows) - 1));
       item_done(n);
     }
   }

@@ -254,3 +254,74 @@ def test_a_wait_that_runs_out_is_reported(load, Hq, Hkv, D):
         p.B.moe_selftest_attention_hold()
     assert torch.equal(p.run(), want)
     p.B.attention_status()
+
+
+def _inf_in_a_long_prompt(n, D, window, sinks, bad, clean):
+    """A prompt of n tokens with values that are not finite at keys `bad` (column 3) and a short one beside it: sampled rows
+    of either against the oracle, in a time far below the limit of the kernel's waits."""
+    p = Prompts([n, clean], 2, 1, D, seed=n % 97)
+    p.v[torch.tensor(bad, device="cuda"), 0, 3] = float("inf")
+    p.run(window, sinks)
+    times = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    times[0].record()
+    got = _np(p.run(window, sinks))
+    times[1].record()
+    torch.cuda.synchronize()
+    p.B.attention_status()
+    assert times[0].elapsed_time(times[1]) < 400
+    q, k, v = _np(p.q), _np(p.k), _np(p.v)
+    cols = [d for d in range(D) if d != 3]
+    for a, b, rows in ((0, n, sorted({bad[0] - 1, bad[0], bad[-1], bad[-1] + 1, n - 130, n - 2, n - 1} - {-1, n})),
+                       (n, n + clean, range(0, clean, 7))):
+        for r in rows:
+            with np.errstate(all="ignore"):
+                want, mag = A.attend_heads(q[a + r:a + r + 1], k[a:b], v[a:b], r, D ** -0.5, window, sinks)
+            mine = got[a + r:a + r + 1]
+            assert np.all(np.abs(mine - want)[..., cols] <= A.attention_tolerance(want, mag)[..., cols]), r
+            if a:
+                assert np.isfinite(mine).all()
+            else:
+                assert np.array_equal(np.isfinite(mine[..., 3]), np.isfinite(want[..., 3])), r
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20001, 5)])
+@pytest.mark.parametrize("at", [100, -3, -140])
+def test_one_infinite_value_in_a_long_prompt(at, window, sinks, D):
+    n = 100_037                                  # its last tile is a partial one
+    _inf_in_a_long_prompt(n, D, window, sinks, [at % n], 40)
+
+
+def test_a_whole_edge_of_infinite_values_in_a_long_prompt():
+    _inf_in_a_long_prompt(100_037, 128, 0, 0, list(range(99_700, 100_000)), 40)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (20, 4), (32, 4)])
+def test_infinities_of_either_sign_and_nan_together(Hq, Hkv):
+    """Columns with one infinity, both, NaN and an infinity; keys in several steps of an item, first tokens and window
+    ends among them; more of them than 64 at once."""
+    lens, inf, nan = [700, 300], float("inf"), float("nan")
+    for window, sinks in ((0, 0), (150, 20)):
+        p = Prompts(lens, Hq, Hkv, 64, seed=3)
+        for j, col, x in ((5, 1, inf), (6, 2, -inf), (130, 2, inf), (131, 3, nan), (132, 3, inf), (400, 4, -inf), (699, 5, inf)):
+            p.v[j, :, col] = x
+        p.v[700 + 100:700 + 200, :, 7] = inf
+        p.v[700 + 150, :, 7] = -inf
+        got = _np(p.run(window, sinks))
+        with np.errstate(all="ignore"):
+            want, mag = p.oracle(window, sinks)
+        fine = np.isfinite(want)
+        assert not fine.all() and np.array_equal(np.where(fine, 0, got), np.where(fine, 0, want), equal_nan=True)
+        with np.errstate(all="ignore"):
+            assert np.all((np.abs(got - want) <= A.attention_tolerance(want, mag))[fine])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 32, 4), (128, 20, 4)])
+def test_a_last_tile_does_not_depend_on_what_follows_it(D, Hq, Hkv):
+    """A partial tile's rows beyond its prompt are the next prompt's: they have no part in it, however large they are."""
+    p = Prompts([300, 1, 140, 700], Hq, Hkv, D, seed=4)
+    want = p.run()
+    p.q[441:] *= 100
+    p.q[300] *= 1000
+    got = p.run()
+    assert torch.equal(got[:300], want[:300]) and torch.equal(got[301:441], want[301:441])
