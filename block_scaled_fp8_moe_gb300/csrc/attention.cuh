@@ -1,5 +1,5 @@
-// What the attention kernels share: which keys a row sees, the cache's addresses, and the attention of
-// one row by one warp straight from its definition (fp32, no tensor cores).
+// What the attention kernels share: argument checks, which keys a row sees, and what values that are not finite add to a
+// row.
 #pragma once
 #include <cmath>
 #include <cstdint>
@@ -153,37 +153,6 @@ __device__ __forceinline__ void add_not_finite(const BadKeys& bad, const LaneRow
 #pragma unroll
   for (int d = 0; d < N; ++d)
     if ((hit >> d) & 1u) add(d, acc[d]);
-}
-
-// One row's attention by one warp straight from the definition, its lanes spread over D, over the visible keys from j0 to
-// j1. `load(j, k, v)` fetches a key's and its value's parts and returns whether the key is there. m, l, o hold the running
-// maximum of the scores (times log2 e), the sum and the weighted values (of the lane).
-template <int D, class Load>
-__device__ __forceinline__ void attend_keys(const LaneRow<D>& q, const Visible& see, int j0, int j1, float scale_log2,
-                                            float& m, float& l, float (&o)[D / 32], const Load& load) {
-  constexpr int N = D / 32;
-  j1 = min(j1, see.end);
-  for (int j = j0; j < j1; ++j) {
-    if (!see.sees(j)) {
-      if (j < see.first) j = min(see.first, j1) - 1;
-      continue;
-    }
-    LaneRow<D> k, v;
-    if (!load(j, k, v)) continue;
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < N; ++d) s = fmaf(q.f[d], k.f[d], s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= scale_log2;
-    const float mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float keep = exp2f(m - base), p = exp2f(s - base);
-    m = mn;
-    l = l * keep + p;
-#pragma unroll
-    for (int d = 0; d < N; ++d) o[d] = o[d] * keep + p * v.f[d];
-  }
 }
 
 }  // namespace moe

@@ -33,7 +33,8 @@ namespace moe {
 constexpr int kRowsM = 128;             // rows of a block
 constexpr int kStepTok = 128;           // tokens of a step
 constexpr int kInfos = 16;              // steps whose tokens are remembered
-constexpr int kListed = 64;             // keys with values that are not finite that an item lists
+// Kinds of steps: every row sees every key; does so but for pages out of range; some row does not see some key.
+enum : int { kSeen, kHoles, kEdge };
 constexpr float kGrow = 8.f;            // the maximum that weights refer to moves when outgrown by 2^8
 
 template <int D_, bool MX_>
@@ -72,45 +73,34 @@ struct PagedItem {
   }
 };
 
-// One row's part of an item straight from the definition, by a warp, which writes one half of its columns: for rows that see a
-// value that is not finite in a step where others do not.
+// The columns of one row's part of an item that a listed key decides, by a warp, which takes one half of them.
 template <int D, bool MX>
-__device__ __noinline__ void redo_part(const PagedArgs& p, const PagedItem& it, int rho, int half) {
+__device__ __noinline__ void finish_part(const PagedArgs& p, const BadKeys& bad, const PagedItem& it, int rho, int half,
+                                         float top) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, G = p.G, r = rho / G;
-  const Visible see(it.pos0 + r, p.a.window, p.a.sinks);
   const long long row = ((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho % G;
+  const long long at = ((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece;
   LaneRow<D> q;
   q.load_bf16(p.q + ((long long)it.b * p.rows + r) * p.q_stride + (long long)(it.hk * G + rho % G) * D, lane);
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  for (int i = 0; i < it.cnt; ++i)
-    attend_keys<D>(q, see, it.tok(i), it.tok(i) + kStepTok, p.a.scale * 1.4426950408889634f, m, l, o,
-                   [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
-                     const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
-                     if (page < 0 || page >= p.pages) return false;
-                     const long long at = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) + (j & (p.page_size - 1));
-                     if (MX) {
-                       k.load_mxfp8(p.k + at * D, p.k_s + at * N, lane);
-                       v.load_mxfp8(p.v + at * D, p.v_s + at * N, lane);
-                     } else {
-                       k.load_bf16(reinterpret_cast<const uint16_t*>(p.k) + at * D, lane);
-                       v.load_bf16(reinterpret_cast<const uint16_t*>(p.v) + at * D, lane);
-                     }
-                     return true;
-                   });
-  const bool mine = lane / 16 == half;
-  if (it.pieces == 1) {
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * N);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i)
-      if (mine) out[i] = l == 0.f ? 0u : bf16x2(o[2 * i] / l, o[2 * i + 1] / l);
-  } else {
-    const long long at = ((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (mine) part_of(p, at, D, rho, (lane * N + i) / 4)[(lane * N + i) % 4] = o[i];
-    if (half == 0 && lane == 0) *sums_of(p, at, rho) = make_float2(m, l);
-  }
+  add_not_finite<D>(bad, q, Visible(it.pos0 + r, p.a.window, p.a.sinks), p.a.scale * 1.4426950408889634f, top,
+                    [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
+                      const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
+                      const long long t = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) + (j & (p.page_size - 1));
+                      if (MX) {
+                        k.load_mxfp8(p.k + t * D, p.k_s + t * N, lane);
+                        v.load_mxfp8(p.v + t * D, p.v_s + t * N, lane);
+                      } else {
+                        k.load_bf16(reinterpret_cast<const uint16_t*>(p.k) + t * D, lane);
+                        v.load_bf16(reinterpret_cast<const uint16_t*>(p.v) + t * D, lane);
+                      }
+                    },
+                    [&](int i, float x) {
+                      if (lane / 16 != half) return;
+                      const int d = lane * N + i;
+                      if (it.pieces == 1) p.out[row * D + d] = (uint16_t)bf16x2(bf16_lo(p.out[row * D + d]) + x, 0.f);
+                      else part_of(p, at, D, rho, d / 4)[d % 4] += x;
+                    });
 }
 
 template <class C>
@@ -122,8 +112,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   __shared__ uint64_t sums_there, outs_read;
   __shared__ uint64_t landed[C::MX ? C::RAWS : C::ENTRIES], raw_empty[C::RAWS], ready[C::ENTRIES], ent_empty[C::ENT_BARS];
   __shared__ PagedItem items[2];
-  __shared__ int4 infos[kInfos];                // of a step: first token, pages there, whether some row does not see a key
-  __shared__ int listed_n[2], listed[2][kListed];
+  __shared__ int4 infos[kInfos];                // of a step: first token, pages there, its kind
+  __shared__ BadKeys bad[2];
   __shared__ float2 sums[2][kRowsM];            // the chains' maximum (times log2 e) and sum of a row
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -214,8 +204,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             mine.pieces = pc.count;
           }
           items[n & 1] = mine;
-          listed_n[n & 1] = 0;                  // the last item but one, whose list this was, is done
         }
+        bad[n & 1].clear(lane);                 // the last item but one, whose list this was, is done
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_full[n & 1]);
         if (who < 0) break;
@@ -256,9 +246,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           if (!(ok = C::MX ? use == 0 || wait(&raw_empty[st], (use - 1) & 1, DEV_TIMEOUT_EMPTY) : ent_free(tile))) break;
           if (lane == 0) {
             if (!is_v) {
-              const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks) &&
-                                 mask == (1u << in_tile) - 1u;
-              infos[(steps + i) % kInfos] = make_int4(tok0, (int)mask, whole ? 0 : 1, 0);
+              const bool whole = tok0 + kStepTok - 1 <= all_to && (tok0 >= all_from || tok0 + kStepTok <= p.a.sinks);
+              infos[(steps + i) % kInfos] =
+                  make_int4(tok0, (int)mask, whole ? (mask == (1u << in_tile) - 1u ? kSeen : kHoles) : kEdge, 0);
             }
             mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D) + (tile == p.hold ? 16 : 0));
           }
@@ -404,8 +394,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     } else if (C::MX ? warp >= 12 : warp == 11) {
       // ---------------- feeding ----------------
       // Hands every tile to the products, MXFP8 converted. In steps where some row does not see a key, values that are not
-      // finite become zero (a weight of zero would not hide them), and those that some row sees are listed: rows that see
-      // them are computed again.
+      // finite become zero (a weight of zero would not hide them), and the keys that some row sees are listed, for the rows
+      // that do see them.
       const int tid = C::MX ? threadIdx.x % 128 : lane, group = C::MX ? warp / 4 - 3 : 0;
       const uint32_t k16 = sixteen();
       int tile = 0, steps = 0;
@@ -413,9 +403,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       for (int n = 0; ok && item_there(n); ++n) {
         const int cnt = items[n & 1].cnt, pmax = items[n & 1].pmax, first_any = items[n & 1].first_any;
         auto list = [&](int tok) {
-          if (tok > pmax || (tok < first_any && tok >= p.a.sinks)) return;
-          const int at = atomicAdd(&listed_n[n & 1], 1);
-          if (at < kListed) listed[n & 1][at] = tok;
+          if (tok <= pmax && (tok >= first_any || tok < p.a.sinks)) bad[n & 1].add(tok);
         };
         auto feed = [&](int i, bool is_v) {
           const int e = tile % C::ENTRIES, st = C::MX ? tile % C::RAWS : e;
@@ -425,7 +413,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           }
           if (!(ok = wait(&landed[st], (tile / (C::MX ? C::RAWS : C::ENTRIES)) & 1, DEV_TIMEOUT_FULL))) return;
           const int4 info = infos[(steps + i) % kInfos];
-          const bool edge = is_v && info.z != 0;
+          const bool edge = is_v && info.z == kEdge;
           uint8_t* dst = ring + e * C::TILE;
           if (C::MX) {
             if (!(ok = ent_free(tile))) return;
@@ -498,7 +486,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&raw_empty[st]);
-          } else if (edge) {
+          } else if (is_v && info.z != kSeen) {
             uint4* v = reinterpret_cast<uint4*>(dst);
             // places of pages that were not loaded hold whatever was here
             const int rows_of = min(p.page_size, kStepTok);
@@ -515,7 +503,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             // zero times a value that is not finite is NaN, and stays in the sum
             uint32_t sum = 0;
 #pragma unroll 8
-            for (int a = lane; a < C::TILE / 16; a += 32) {
+            for (int a = edge ? lane : C::TILE / 16; a < C::TILE / 16; a += 32) {
               const uint4 w = v[a];
               sum = fma_bf16x2(w.x, 0, sum);
               sum = fma_bf16x2(w.y, 0, sum);
@@ -754,16 +742,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           if (x == 0) *sums_of(p, at, rho) = make_float2(both, tl);
         }
       }
-      // ---- rows that see a listed key, from the definition: each chain's warps their half of the columns ----
+      // ---- rows that see a listed key: each chain's warps their half of the columns ----
       if (ok && cnt > 0) {
-        const int some = *reinterpret_cast<volatile int*>(&listed_n[n & 1]);
-        if (some) {
-          bool again = some > kListed;
+        if (*reinterpret_cast<volatile int*>(&bad[n & 1].some)) {
+          bool again = false;
           const Visible see(live ? pos : -1, p.a.window, p.a.sinks);
-          for (int i = 0; i < min(some, kListed); ++i) again = again || see.sees(listed[n & 1][i]);
+          bad[n & 1].each([&](int j) { again = again || see.sees(j); });
           again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
+          __syncwarp();                         // what a lane has written another one adds to
           for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-            redo_part<D, C::MX>(p, it, rho - lane + __ffs(rows) - 1, x);
+            finish_part<D, C::MX>(p, bad[n & 1], it, rho - lane + __ffs(rows) - 1, x,
+                                  __shfl_sync(0xffffffffu, both, __ffs(rows) - 1));
         }
       }
       ok = wait(&outs_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;

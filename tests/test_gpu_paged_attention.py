@@ -467,3 +467,64 @@ def test_many_rows_a_wait_that_runs_out_is_reported(load, mx, D):
     """Pieces of 4 steps, one a block: 8 tiles of keys and values, of which the loading warp has issued all but the held
     one's successors when the others give up."""
     _gives_up(Paged([4096] * 4, 6, 16, 2, D, 64, mx, seed=load), load)
+
+
+def _put(p, b, j, col, x):
+    """Value `x` (MXFP8: NaN in the column's block of 32) at key j of sequence b."""
+    page, at = int(p.table[b, j // p.page]), j % p.page
+    if p.cache.v_s is not None:
+        p.cache.v_s[page, :, at, col // 32] = 255
+    else:
+        p.cache.v[page, :, at, col] = x
+    p.values[1][page, :, at, slice(col // 32 * 32, col // 32 * 32 + 32) if p.cache.v_s is not None else col] = (
+        np.nan if p.cache.v_s is not None else x)
+
+
+def _check_not_finite(p, window=0, sinks=0):
+    """Where the oracle's result is not finite, the same infinity or NaN; elsewhere as ever."""
+    got = p.run(window, sinks).float().cpu().numpy()
+    p.B.attention_status()
+    with np.errstate(all="ignore"):
+        want, mag = p.oracle(window, sinks)
+        near = np.abs(got - want) <= A.attention_tolerance(want, mag)
+    fine = np.isfinite(want)
+    assert near[fine].all() and not fine.all()
+    assert np.array_equal(np.where(fine, 0, got), np.where(fine, 0, want), equal_nan=True)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq,lens", [(6, 16, [700, 300, 5000]), (60, 3, [700, 300, 5000])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20), (700, 200)])
+def test_many_rows_infinities_and_nan_that_some_rows_see(window, sinks, rows, Hq, lens, D, mx):
+    """In the last keys, at the windows' beginnings, among the first tokens, a whole step of them; infinities of either sign
+    in one column, in steps at the mask's edge and in others."""
+    inf = float("inf")
+    p = Paged(lens, rows, Hq, 1, D, 16, mx, seed=rows + window)
+    for b, n in enumerate(lens):
+        _put(p, b, n - 1, 1, inf)
+        _put(p, b, n - rows // 2, 40, -inf)
+        _put(p, b, 10, 40, inf)
+        _put(p, b, 19, 2, float("nan"))
+        _put(p, b, max(n - rows + 3 - 150, 0), 41, inf)
+        _put(p, b, max(n - rows + 3 - 700, 0), 42, inf)
+    for j in range(200, 290):
+        _put(p, 1, j, 50, inf)
+    _check_not_finite(p, window, sinks)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_many_rows_infinities_beside_pages_out_of_range(mx):
+    """A page that is not there makes its step no edge: what every row sees stays in the product."""
+    p = Paged([500], 6, 8, 1, 64, 16, mx, seed=3)
+    clean = p.run()
+    _put(p, 0, 40, 3, float("inf"))
+    table = p.table.clone()
+    table[0, 3] = -1                               # keys 48 to 63
+    got = p.B.moe_paged_attention(p.q, p.cache, table, p.seq_lens(), 500)
+    with pytest.raises(p.B.MoeError):
+        p.B.attention_status()
+    cols = list(range(32)) if mx else [3]
+    keep = [d for d in range(64) if d not in cols]
+    assert not got[..., cols].isfinite().any() and got[..., keep].isfinite().all()
+    assert not torch.equal(got[..., keep], clean[..., keep])
