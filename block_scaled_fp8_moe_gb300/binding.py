@@ -493,31 +493,53 @@ def _sized(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> int:
 
 
 _scratch: dict[tuple[int, int], tuple[torch.Tensor, int, int]] = {}
-_outgrown: list[torch.Tensor] = []      # kept: a captured CUDA graph may still write to them
+# Buffers that a stream has outgrown. Kept: another thread may be about to launch with one.
+_outgrown: dict[tuple[int, int], list[torch.Tensor]] = {}
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _workspace(nbytes: int, like: torch.Tensor, stream, dev: int, raw: int) -> tuple[int, int]:
-    """Address and size of this stream's workspace of the attention and cache calls, grown as needed (at least
-    twofold); its status word starts at zero."""
+    """Address and size of this stream's workspace of the attention and cache calls. Not for a graph: all that are
+    captured share one stream, and would share their partial results when they are replayed on others."""
+    if stream is None:
+        captured = _capturing()
+    else:
+        with torch.cuda.stream(stream):
+            captured = _capturing()
+    if captured:
+        raise ValueError(f"a captured call needs a workspace of its own: pass ws, uint8 of at least {max(nbytes, 256)} "
+                         "zeros, which the graph's replays use and moe_check_device_status(ws) reads")
     have = _scratch.get((dev, raw))
     if have is None or have[2] < nbytes:
-        size = max(nbytes, 4096, 0 if have is None else 2 * have[2])
-        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
-            ws = torch.empty(size, dtype=torch.uint8, device=like.device)
-            ws[:256].zero_() if have is None else ws[:256].copy_(have[0][:256])
-        if have is not None:
-            _outgrown.append(have[0])
-        have = _scratch[dev, raw] = (ws, ws.data_ptr(), size)
+        have = _grown(have, nbytes, like, stream, (dev, raw))
     return have[1], have[2]
+
+
+def _grown(have, nbytes: int, like: torch.Tensor, stream, key):
+    """A larger workspace for that stream (at least twofold); its status word starts at zero."""
+    size = max(nbytes, 4096, 0 if have is None else 2 * have[2])
+    with _allocating(stream):
+        ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+        ws[:256].zero_()
+    if have is not None:
+        _outgrown.setdefault(key, []).append(have[0])
+    _scratch[key] = ws, ws.data_ptr(), size
+    return _scratch[key]
 
 
 def attention_status(device=None, stream=None) -> None:
     """Synchronises `stream` and raises what the attention and cache calls without a workspace of their own found
-    invalid on the device there (a page, slot or length out of range), then clears it."""
+    invalid on the device there (a page, slot or length out of range) or gave up, then clears it."""
     s = torch.cuda.current_stream(device) if stream is None else stream
-    have = _scratch.get((s.device_index, s.cuda_stream))
-    if have is not None:
-        moe_check_device_status(have[0], s)
+    found = None
+    key = s.device_index, s.cuda_stream
+    for ws in _outgrown.get(key, []) + [have[0] for have in (_scratch.get(key),) if have]:
+        try:
+            moe_check_device_status(ws, s)
+        except MoeError as e:
+            found = found or e
+    if found:
+        raise found
 
 
 @functools.lru_cache(maxsize=4096)
@@ -613,7 +635,8 @@ class KvCache:
 
 def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
     """Stores the bf16 rows k and v [T, Hkv, D] (rows may lie apart) at slots i32 [T] (page * page_size + place;
-    -1 = not stored)."""
+    -1 = not stored). ws: at least 256 bytes of uint8, zeros at first; one per stream is kept where it is not given (inside
+    a graph's capture it has to be)."""
     dev = _current(k, "k")
     pk, sk = _rows_on(k, "k", cache.Hkv, cache.D, dev)
     pv, sv = _rows_on(v, "v", cache.Hkv, cache.D, dev)
@@ -635,7 +658,9 @@ def moe_paged_attention_workspace_bytes(B: int, rows: int, Hq: int, Hkv: int, D:
 def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, scale: float | None = None,
                         window: int = 0, sinks: int = 0, out=None, ws=None, stream=None):
     """Attention of q bf16 [B, rows, Hq, D] (each sequence's newest rows) over the paged cache. block_table i32
-    [B, width], seq_lens i32 [B] (the new rows counted), max_len >= every seq_len. Returns bf16 [B, rows, Hq, D]."""
+    [B, width], seq_lens i32 [B] (the new rows counted), max_len >= every seq_len. Returns bf16 [B, rows, Hq, D]. ws:
+    moe_paged_attention_workspace_bytes of uint8, zeros at first; one per stream is kept where it is not given (inside a
+    graph's capture it has to be)."""
     dev = _current(q, "q")
     B, rows, Hq, D = q.shape
     width = block_table.shape[-1]
@@ -671,7 +696,7 @@ def moe_prefill_attention(q, k, v, cu_q, cu_k=None, scale: float | None = None, 
                           out=None, ws=None, stream=None):
     """Attention of packed prompts: q bf16 [Tq, Hq, D], k and v bf16 [Tk, Hkv, D] (rows may lie apart), cu_q and cu_k
     i32 [B + 1] the sequences' bounds (cu_k None: the same). Returns bf16 [Tq, Hq, D]; rows outside every sequence are
-    left as they are in `out`."""
+    left as they are in `out`. ws: as for moe_kv_append."""
     dev = _current(q, "q")
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape

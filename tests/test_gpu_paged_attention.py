@@ -528,3 +528,59 @@ def test_many_rows_infinities_beside_pages_out_of_range(mx):
     keep = [d for d in range(64) if d not in cols]
     assert not got[..., cols].isfinite().any() and got[..., keep].isfinite().all()
     assert not torch.equal(got[..., keep], clean[..., keep])
+
+
+def test_a_captured_call_needs_its_own_workspace():
+    """All captures share one stream, and with it they would share one buffer of partial results. Each with its own, two
+    graphs can be replayed side by side."""
+    a, b = Paged([9000, 700], 6, 8, 2, 64, 16, False, seed=1), Paged([4000, 30, 2500], 2, 8, 2, 64, 16, False, seed=2)
+    B = a.B
+    kv = torch.randn(3, 2, 64, device="cuda").bfloat16()
+    slots, cu = torch.full((3,), -1, dtype=torch.int32, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    lens = [p.seq_lens() for p in (a, b)]
+    outs = [torch.empty_like(p.q) for p in (a, b)]
+    for stream in (None, torch.cuda.Stream()):
+        graph, x = torch.cuda.CUDAGraph(), torch.zeros(4, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph) if stream is None else torch.cuda.graph(graph, stream=stream):
+            x += 1
+            for call in (lambda s: B.moe_paged_attention(a.q, a.cache, a.table, lens[0], 9000, out=outs[0], stream=s),
+                         lambda s: B.moe_kv_append(a.cache, kv, kv, slots, stream=s),
+                         lambda s: B.moe_prefill_attention(kv, kv, kv, cu, out=kv, stream=s)):
+                with pytest.raises(ValueError, match="workspace"):
+                    call(stream)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (x == 1).all()
+    want, graphs = [a.run(), b.run()], []
+    for p, n, out in zip((a, b), lens, outs):
+        ws = torch.zeros(B.moe_paged_attention_workspace_bytes(*p.q.shape[:3], 2, 64, max(p.lens)), dtype=torch.uint8,
+                         device="cuda")
+        graphs.append((torch.cuda.CUDAGraph(), torch.cuda.Stream(), ws))
+        with torch.cuda.graph(graphs[-1][0]):
+            for _ in range(20):
+                B.moe_paged_attention(p.q, p.cache, p.table, n, max(p.lens), out=out, ws=ws)
+    for _ in range(5):
+        for out in outs:
+            out.fill_(7)
+        torch.cuda.synchronize()
+        for graph, stream, _ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    for _, _, ws in graphs:
+        B.moe_check_device_status(ws)
+
+
+def test_errors_found_before_a_workspace_grew_are_reported_once():
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        p = Paged([90, 41], 1, 4, 2, 64, 16, False, seed=9)
+        p.B.moe_paged_attention(p.q, p.cache, p.table, torch.tensor([90, 91], dtype=torch.int32, device="cuda"), 90)
+        big = Paged([9000] * 40, 4, 8, 2, 64, 64, False, seed=1)
+        big.run()
+        with pytest.raises(p.B.MoeError) as e:
+            p.B.attention_status()
+        assert e.value.code == p.B.MOE_ERR_DEVICE_INPUT
+        p.B.attention_status()
