@@ -209,6 +209,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       const int head_items = p.pair && !ONE ? p.a.Hq / 2 : p.a.Hq;
       int kv = 0, qs = 0;                       // tiles of keys or values, and pairs of tiles of queries, loaded so far
       bool ok = true;
+      // The walk along the sequences, 32 at a time from the last ones on; a block's items only go up, so that it goes once.
+      int group = (p.a.B + 31) / 32 * 32;       // first sequence of the 32
+      int before = 0, total = 0, upto = 0;      // blocks of rows of those that were passed; of the 32; up to this lane's
+      Span mine{0, 0, 0, 0};                    // the lane's sequence: lane 0 has the last one
       for (int n = 0; ok; ++n) {
         // Items are numbered from the last rows of the last sequence on, so that long rows are begun first; the heads of
         // the same rows are neighbours and share their keys in L2. Every other round is dealt out backwards: who had the
@@ -216,28 +220,28 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         const unsigned idx = (unsigned)n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         int want = (int)(idx / (unsigned)head_items), found = 0;
         Span sp{0, 0, 0, 0};
-        for (int b0 = (p.a.B - 1) / 32 * 32; b0 >= 0 && !found; b0 -= 32) {
-          const int b = b0 + 31 - lane;         // lane 0 has the last sequence
-          const Span mine = b < p.a.B ? span_of(p, b) : Span{0, 0, 0, 0};
-          const int cnt = (mine.qn + per_item - 1) / per_item;
-          int upto = cnt;
+        while (want >= before + total && group > 0) {
+          before += total;
+          group -= 32;
+          const int b = group + 31 - lane;
+          mine = b < p.a.B ? span_of(p, b) : Span{0, 0, 0, 0};
+          upto = (mine.qn + per_item - 1) / per_item;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += x;
           }
-          const unsigned here = __ballot_sync(0xffffffffu, want < upto);
-          if (here) {
-            const int who = __ffs(here) - 1;
-            found = 1;
-            want = __shfl_sync(0xffffffffu, upto, who) - 1 - want;      // of the sequence's items, from its first on
-            sp.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
-            sp.qn = __shfl_sync(0xffffffffu, mine.qn, who);
-            sp.k0 = __shfl_sync(0xffffffffu, mine.k0, who);
-            sp.kn = __shfl_sync(0xffffffffu, mine.kn, who);
-          } else {
-            want -= __shfl_sync(0xffffffffu, upto, 31);
-          }
+          total = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        want -= before;
+        if (want < total) {
+          const int who = __ffs(__ballot_sync(0xffffffffu, want < upto)) - 1;
+          found = 1;
+          want = __shfl_sync(0xffffffffu, upto, who) - 1 - want;        // of the sequence's items, from its first on
+          sp.q0 = __shfl_sync(0xffffffffu, mine.q0, who);
+          sp.qn = __shfl_sync(0xffffffffu, mine.qn, who);
+          sp.k0 = __shfl_sync(0xffffffffu, mine.k0, who);
+          sp.kn = __shfl_sync(0xffffffffu, mine.kn, who);
         }
         if (n >= 2 && !wait(&w_empty[n & 1], ((n >> 1) - 1) & 1, DEV_TIMEOUT_EMPTY)) break;
         const int slot[8] = {sp.q0, sp.qn, sp.k0, sp.kn, want * per_item, (int)(idx % (unsigned)head_items) * (p.pair && !ONE ? 2 : 1), found, 0};

@@ -325,3 +325,23 @@ def test_a_last_tile_does_not_depend_on_what_follows_it(D, Hq, Hkv):
     p.q[300] *= 1000
     got = p.run()
     assert torch.equal(got[:300], want[:300]) and torch.equal(got[301:441], want[301:441])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (3, 3)])
+def test_thousands_of_short_prompts(Hq, Hkv):
+    """Most of them empty, bounds that break the rule among them: every block passes the bounds once."""
+    rng = np.random.default_rng(3)
+    lens = np.where(rng.random(5000) < 0.3, rng.integers(1, 6, 5000), 0)
+    lens[[0, 31, 32, 4999]] = [300, 0, 1, 140]
+    p = Prompts(lens.tolist(), Hq, Hkv, 64, seed=1)
+    p.check()
+    p.check(3, 1)
+    want = p.run()
+    cu = p.cu_q.clone()
+    b = int(np.flatnonzero(lens)[500])
+    p.cu_q[b + 1] += 10 ** 6                       # sequence b ends past the rows, and the next begins there
+    got = p.run(out=torch.full_like(want, 7))
+    with pytest.raises(p.B.MoeError):
+        p.B.attention_status()
+    a, z = int(cu[b]), int(cu[b + 2])
+    assert torch.equal(got[:a], want[:a]) and torch.equal(got[z:], want[z:]) and (got[a:z] == 7).all()
