@@ -125,13 +125,13 @@ struct BadKeys {
 };
 static_assert(sizeof(BadKeys::keys) == 32 * 4, "a word a lane");
 
-// What those keys add to one row's result, by one warp, its lanes spread over D: weighted values that are not finite, whose
-// weights are above zero (however small; zero for a score of minus infinity alone). All else that the keys have is in the
-// result already. `top` is what the row's weights refer to (times log2 e), `load(j, k, v)` fetches a key, `add(i, x)` adds x
-// to the result's i-th column of the lane. The cost goes with the keys that are listed, not with the row's length.
+// What those keys add to one row's result, by one warp, its lanes spread over D: values that are not finite, times a weight
+// that is above zero, however small, or zero for a score of minus infinity; which size it has does not matter to them. All
+// else that the keys have is in the result already. `load(j, k, v)` fetches a key, `add(i, x)` adds x to the result's i-th
+// column of the lane. The cost goes with the keys that are listed, not with the row's length.
 template <int D, class Load, class Add>
-__device__ __forceinline__ void add_not_finite(const BadKeys& bad, const LaneRow<D>& q, const Visible& see, float scale_log2,
-                                               float top, const Load& load, const Add& add) {
+__device__ __forceinline__ void add_not_finite(const BadKeys& bad, const LaneRow<D>& q, const Visible& see, float scale,
+                                               const Load& load, const Add& add) {
   constexpr int N = D / 32;
   float acc[N] = {};
   uint32_t hit = 0;
@@ -144,8 +144,7 @@ __device__ __forceinline__ void add_not_finite(const BadKeys& bad, const LaneRow
     for (int d = 0; d < N; ++d) s = fmaf(q.f[d], k.f[d], s);
 #pragma unroll
     for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= scale_log2;
-    const float p = s == -INFINITY ? 0.f : fmaxf(exp2f(s - top), 1e-30f);
+    const float p = s * scale == -INFINITY ? 0.f : 1.f;
 #pragma unroll
     for (int d = 0; d < N; ++d)
       if (!isfinite(v.f[d])) acc[d] += p * v.f[d], hit |= 1u << d;

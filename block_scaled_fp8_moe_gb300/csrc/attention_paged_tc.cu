@@ -75,15 +75,14 @@ struct PagedItem {
 
 // The columns of one row's part of an item that a listed key decides, by a warp, which takes one half of them.
 template <int D, bool MX>
-__device__ __noinline__ void finish_part(const PagedArgs& p, const BadKeys& bad, const PagedItem& it, int rho, int half,
-                                         float top) {
+__device__ __noinline__ void finish_part(const PagedArgs& p, const BadKeys& bad, const PagedItem& it, int rho, int half) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, G = p.G, r = rho / G;
   const long long row = ((long long)it.b * p.rows + r) * p.a.Hq + it.hk * G + rho % G;
   const long long at = ((long long)it.b * p.a.Hkv + it.hk) * p.max_pieces + it.piece;
   LaneRow<D> q;
   q.load_bf16(p.q + ((long long)it.b * p.rows + r) * p.q_stride + (long long)(it.hk * G + rho % G) * D, lane);
-  add_not_finite<D>(bad, q, Visible(it.pos0 + r, p.a.window, p.a.sinks), p.a.scale * 1.4426950408889634f, top,
+  add_not_finite<D>(bad, q, Visible(it.pos0 + r, p.a.window, p.a.sinks), p.a.scale,
                     [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
                       const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
                       const long long t = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) + (j & (p.page_size - 1));
@@ -751,8 +750,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
           __syncwarp();                         // what a lane has written another one adds to
           for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-            finish_part<D, C::MX>(p, bad[n & 1], it, rho - lane + __ffs(rows) - 1, x,
-                                  __shfl_sync(0xffffffffu, both, __ffs(rows) - 1));
+            finish_part<D, C::MX>(p, bad[n & 1], it, rho - lane + __ffs(rows) - 1, x);
         }
       }
       ok = wait(&outs_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;

@@ -85,14 +85,14 @@ struct PrefillCfg {
 
 // The columns of one row's result that a listed key decides, by a warp.
 template <int D>
-__device__ __noinline__ void finish_row(const PrefillArgs& p, const BadKeys& bad, const Span& s, int row, int h, float top) {
+__device__ __noinline__ void finish_row(const PrefillArgs& p, const BadKeys& bad, const Span& s, int row, int h) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, hk = h / (p.a.Hq / p.a.Hkv);
   const long long t = s.q0 + row;
   LaneRow<D> q;
   q.load_bf16(p.q + t * p.q_stride + (long long)h * D, lane);
   uint16_t* out = p.out + (t * p.a.Hq + h) * D + lane * N;
-  add_not_finite<D>(bad, q, Visible(s.kn - s.qn + row, p.a.window, p.a.sinks), p.a.scale * 1.4426950408889634f, top,
+  add_not_finite<D>(bad, q, Visible(s.kn - s.qn + row, p.a.window, p.a.sinks), p.a.scale,
                     [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
                       k.load_bf16(p.k + (long long)(s.k0 + j) * p.k_stride + (long long)hk * D, lane);
                       v.load_bf16(p.v + (long long)(s.k0 + j) * p.v_stride + (long long)hk * D, lane);
@@ -666,8 +666,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
         __syncwarp();
       }
       for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-        finish_row<D>(p, bad[n & 1], it.s, row - ln + __ffs(rows) - 1, h,
-                      __shfl_sync(0xffffffffu, m * c, __ffs(rows) - 1));
+        finish_row<D>(p, bad[n & 1], it.s, row - ln + __ffs(rows) - 1, h);
       item_done(n);
     }
   }
