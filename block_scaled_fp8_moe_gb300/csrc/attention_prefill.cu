@@ -159,7 +159,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   uint8_t* staging = ring + C::STAGES * C::TILE;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  pdl_trigger();
   if (threadIdx.x == 0) {
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -188,6 +187,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  // Only now: a successor that takes Tensor Memory as well must not come before this block has its own, which it would keep
+  // until this grid ends.
+  pdl_trigger();
   pdl_wait();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {       // a whole warp's
