@@ -557,7 +557,7 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight and y's MXFP8 codes and scales, for bf16 rows [..., cols].
 
     Returns (y, sum, q, s): bf16(y), bf16(h), u8 codes and u8 scales [..., cols / 32]. sum_out and y may be x or residual
-    themselves. With quant=False, q and s are None."""
+    themselves. With quant=False, q and s are None. residual has x's shape, or its rows in another number of dimensions."""
     dev = _current(x, "x")
     bf16, u8 = torch.bfloat16, torch.uint8
     shape_ = x.shape
@@ -570,8 +570,9 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
     pr = None
     if residual is not None:
         pr = _on(residual, "residual", bf16, dev)
-        if residual.numel() != n:
-            raise ValueError(f"residual needs {n} elements, has {residual.numel()}")
+        if residual.shape != shape_ and (residual.numel() != n or residual.dim() == x.dim() or
+                                         residual.dim() > 1 and residual.shape[-1] != cols):
+            raise ValueError(f"residual must be {tuple(shape_)}, is {tuple(residual.shape)}")
 
     with _allocating(stream):
         if sum_out is None:

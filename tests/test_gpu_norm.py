@@ -134,3 +134,16 @@ def test_refusals():
     with pytest.raises(B.MoeError):
         B.moe_add_rmsnorm_mxfp8(x[:, :40].contiguous(), w[:40].contiguous())
     assert B.moe_add_rmsnorm_mxfp8(x[:0], w)[0].shape == (0, 64)
+
+
+def test_residuals_of_other_shapes():
+    """The rows in another number of dimensions are the same rows; the same elements in another order are not."""
+    from block_scaled_fp8_moe_gb300 import binding as B
+    x, r, w = _inputs(6, 64, 2)
+    want = B.moe_add_rmsnorm_mxfp8(x, w, r)
+    for a, b in ((x.view(2, 3, 64), r), (x, r.view(3, 2, 64)), (x, r.view(-1)), (x.view(2, 3, 64), r.view(2, 3, 64))):
+        for p, q in zip(B.moe_add_rmsnorm_mxfp8(a, w, b), want):
+            assert torch.equal(p.flatten(), q.flatten())
+    for a, b in ((x, r.view(64, 6)), (x.view(2, 3, 64), r.view(3, 2, 64)), (x, r.view(3, 4, 32)), (x, r.view(12, 32))):
+        with pytest.raises(ValueError, match="residual"):
+            B.moe_add_rmsnorm_mxfp8(a, w, b)
