@@ -573,6 +573,8 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
         if residual.shape != shape_ and (residual.numel() != n or residual.dim() == x.dim() or
                                          residual.dim() > 1 and residual.shape[-1] != cols):
             raise ValueError(f"residual must be {tuple(shape_)}, is {tuple(residual.shape)}")
+    if not quant and (q is not None or s is not None):
+        raise ValueError("q and s are not written with quant=False")
 
     with _allocating(stream):
         if sum_out is None:

@@ -147,3 +147,13 @@ def test_residuals_of_other_shapes():
     for a, b in ((x, r.view(64, 6)), (x.view(2, 3, 64), r.view(3, 2, 64)), (x, r.view(3, 4, 32)), (x, r.view(12, 32))):
         with pytest.raises(ValueError, match="residual"):
             B.moe_add_rmsnorm_mxfp8(a, w, b)
+
+
+def test_outputs_that_would_not_be_written_are_refused():
+    from block_scaled_fp8_moe_gb300 import binding as B
+    x, r, w = _inputs(6, 64, 2)
+    q, s = torch.zeros(6, 64, dtype=torch.uint8, device="cuda"), torch.zeros(6, 2, dtype=torch.uint8, device="cuda")
+    for kw in (dict(q=q), dict(s=s), dict(q=q, s=s)):
+        with pytest.raises(ValueError):
+            B.moe_add_rmsnorm_mxfp8(x, w, r, quant=False, **kw)
+    assert B.moe_add_rmsnorm_mxfp8(x, w, r, q=q, s=s)[2] is q and q.any()
