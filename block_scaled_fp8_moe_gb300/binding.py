@@ -456,7 +456,7 @@ def _on(t: torch.Tensor, name: str, dtype, dev: int) -> int:
 
 
 def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[int, int]:
-    """The address and the row stride of bf16 rows [rows, heads, D] (rows may lie apart)."""
+    """The address and the row stride of bf16 rows [rows, heads, D] (rows may lie apart; one row has no stride)."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
     if t.dtype is not torch.bfloat16:
@@ -467,7 +467,7 @@ def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[
     row, head, one = t.stride()
     if (one != 1 and d > 1) or (head != D and h > 1):
         raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.data_ptr(), row if n > 1 else max(row, h * d)
+    return t.data_ptr(), row if n > 1 else h * d
 
 
 def _current(t: torch.Tensor, name: str) -> int:

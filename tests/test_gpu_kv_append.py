@@ -153,3 +153,25 @@ def test_refusals():
             B.moe_kv_append(odd, kk, kk, slots)
         assert e.value.code == B.MOE_ERR_UNSUPPORTED_SHAPE
     B.moe_kv_append(cache, k[:0], v[:0], slots[:0])
+
+
+@pytest.mark.parametrize("stride", [131, 1, 2 ** 40])
+def test_the_stride_of_a_single_row_does_not_matter(stride):
+    from block_scaled_fp8_moe_gb300 import binding as B
+    cache = _cache(3, 16, 2, 64, False)
+    k, v = _rows(1, 2, 64, 5)
+    odd = lambda t: t.contiguous().as_strided((1, 2, 64), (stride, 64, 1))  # noqa: E731
+    slots = np.array([17], dtype=np.int32)
+    want = _want(cache, k, v, slots)
+    B.moe_kv_append(cache, odd(k), odd(v), torch.from_numpy(slots).cuda())
+    for a, b in zip(_got(cache), want):
+        assert np.array_equal(a, b)
+    for t in (cache.k, cache.v):
+        t.zero_()
+    B.moe_kv_append(cache, odd(k), odd(v), torch.from_numpy(slots).cuda())
+    lens, table = torch.tensor([18], dtype=torch.int32, device="cuda"), torch.tensor([[2, 1]], dtype=torch.int32, device="cuda")
+    q = torch.cat([k, k], 1).view(1, 1, 4, 64)
+    one = q.contiguous().as_strided((1, 1, 4, 64), (stride, stride, 64, 1))
+    assert torch.equal(B.moe_paged_attention(one, cache, table, lens, 18), B.moe_paged_attention(q, cache, table, lens, 18))
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    assert torch.equal(B.moe_prefill_attention(odd(k), odd(k), odd(v), cu), B.moe_prefill_attention(k, k, v, cu))
