@@ -622,7 +622,7 @@ class KvCache:
                 if tuple(t.shape) != (pages, Hkv, page_size, D // 32):
                     raise ValueError(f"{name} must be [pages, Hkv, page_size, D/32], is {tuple(t.shape)}")
                 ptrs[2 + i] = _on(t, name, torch.uint8, dev)
-        self.k, self.v, self.k_s, self.v_s = k, v, k_s, v_s
+        self.k, self.v, self.k_s, self.v_s, self.dev = k, v, k_s, v_s, dev
         self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
         self.desc = MoeKvCache(pages, page_size, Hkv, D, MOE_KV_MXFP8 if mx else MOE_KV_BF16, *ptrs)
         self.ref = ctypes.byref(self.desc)
@@ -641,6 +641,8 @@ def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
     -1 = not stored). ws: at least 256 bytes of uint8, zeros at first; one per stream is kept where it is not given (inside
     a graph's capture it has to be)."""
     dev = _current(k, "k")
+    if cache.dev != dev:
+        raise ValueError("cache and k must be on the same CUDA device")
     pk, sk = _rows_on(k, "k", cache.Hkv, cache.D, dev)
     pv, sv = _rows_on(v, "v", cache.Hkv, cache.D, dev)
     T = slots.numel()
@@ -665,6 +667,8 @@ def moe_paged_attention(q, cache: KvCache, block_table, seq_lens, max_len: int, 
     moe_paged_attention_workspace_bytes of uint8, zeros at first; one per stream is kept where it is not given (inside a
     graph's capture it has to be)."""
     dev = _current(q, "q")
+    if cache.dev != dev:
+        raise ValueError("cache and q must be on the same CUDA device")
     B, rows, Hq, D = q.shape
     width = block_table.shape[-1]
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:

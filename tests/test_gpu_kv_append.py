@@ -175,3 +175,15 @@ def test_the_stride_of_a_single_row_does_not_matter(stride):
     assert torch.equal(B.moe_paged_attention(one, cache, table, lens, 18), B.moe_paged_attention(q, cache, table, lens, 18))
     cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     assert torch.equal(B.moe_prefill_attention(odd(k), odd(k), odd(v), cu), B.moe_prefill_attention(k, k, v, cu))
+
+
+def test_a_cache_on_another_device_is_refused():
+    from block_scaled_fp8_moe_gb300 import binding as B
+    cache = _cache(3, 16, 2, 64, False)
+    k, v = _rows(2, 2, 64, 5)
+    ids = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cache.dev += 1                                # as if it had been made there
+    with pytest.raises(ValueError, match="device"):
+        B.moe_kv_append(cache, k, v, ids)
+    with pytest.raises(ValueError, match="device"):
+        B.moe_paged_attention(k.contiguous().view(2, 1, 2, 64), cache, ids.view(2, 1), ids, 16)
