@@ -385,10 +385,11 @@ typedef struct moe_kv_cache {
 
 /* Stores T new tokens: k and v bf16, token t's heads at k + t * k_stride (elements; [Hkv, D] contiguous
  * there, strides multiples of 8 and at least Hkv * D), go to page slots[t] / page_size, place
- * slots[t] % page_size. slots i32 [T]; -1 = not stored (a dead row); two equal slots in one call leave
- * one of the two tokens' values, which one is not defined, head by head. Any other slot outside
- * [0, pages * page_size) is not stored and recorded in the status word (MOE_ERR_DEVICE_INPUT). ws: at least 256
- * bytes, 256-byte aligned, its first 4 bytes the status word. k, v 16-byte aligned. */
+ * slots[t] % page_size. slots i32 [T]; -1 = not stored (a dead row). The others of one call must differ: what a
+ * slot that two tokens have holds afterwards is not defined, and may be parts of both (codes of one, scales of
+ * the other). Any other slot outside [0, pages * page_size) is not stored and recorded in the status word
+ * (MOE_ERR_DEVICE_INPUT). ws: at least 256 bytes, 256-byte aligned, its first 4 bytes the status word. k, v
+ * 16-byte aligned. */
 MOE_API int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_t* k, int64_t k_stride,
                           const uint16_t* v, int64_t v_stride, const int32_t* slots, void* ws, size_t ws_bytes,
                           void* stream);
