@@ -419,8 +419,8 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
         const int rho = 2 * c + e;
         if (rho >= R) continue;
         const bool one = pieces == 1;
-        const float inv = !one ? 1.f : tl[e] == 0.f ? 0.f : 1.f / tl[e];
         const int r = rho / G;
+        const float inv = !one ? 1.f : tl[e] == 0.f ? no_weights(p, b, pos[e]) : 1.f / tl[e];
         uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
 #pragma unroll
         for (int j = 0; j < MT; j += 2) {
@@ -905,8 +905,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
       const int rho = g + 8 * h;
       if (warp == 0 && rho < R && !abort_flag) {
         const bool one = pieces == 1;
-        const float inv = !one ? 1.f : tl[h] == 0.f ? 0.f : 1.f / tl[h];
         const int r = rho / G;
+        const float inv = !one ? 1.f : tl[h] == 0.f ? no_weights(p, b, pos[h]) : 1.f / tl[h];
         const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
         uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
 #pragma unroll
@@ -988,9 +988,9 @@ __global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const
     if (i + 16 < count) load(s[0], v[0], i + 16);
     add(s[1], v[1], i + 8);
   }
-  const float inv = 1.f / tl;
+  const float inv = tl == 0.f ? no_weights(p, b, pc.pos0 + rho / G) : 1.f / tl;
   *reinterpret_cast<uint2*>(p.out + ((b * p.rows + rho / G) * p.a.Hq + hk * G + rho % G) * D + d4 * 4) =
-      tl == 0.f ? make_uint2(0, 0) : make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+      make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
 }
 
 // Blocks of up to 16 rows take steps of 64 tokens, more rows steps of 128.

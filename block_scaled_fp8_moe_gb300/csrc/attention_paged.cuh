@@ -90,6 +90,14 @@ __device__ __forceinline__ int checked_len(const PagedArgs& p, long long b, bool
   return 0;
 }
 
+// What a row without weights is: zero where it sees nothing. Where it does (its own key, in a page that there is), all scores
+// were minus infinity, and 0 / 0 is NaN.
+__device__ __forceinline__ float no_weights(const PagedArgs& p, long long b, int pos) {
+  if (pos < 0) return 0.f;
+  const int page = p.table[b * p.table_width + (pos >> p.page_log2)];
+  return page >= 0 && page < p.pages ? __uint_as_float(0x7FC00000u) : 0.f;
+}
+
 // The items (sequence, block of rows, piece, head) that there are, numbered without gaps, so that blocks that take every
 // grid-th of them differ by one at most. A warp goes along them, 32 blocks of rows at a time; numbers only go up.
 struct ItemWalk {

@@ -703,7 +703,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
       mbar_arrive(&outs_read);                  // the next item's products may write there
       if (ok && live) {
         const bool one = it.pieces == 1;
-        const float inv = !one ? 1.f : tl == 0.f ? 0.f : 1.f / tl;
+        const float inv = !one ? 1.f : tl == 0.f ? no_weights(p, it.b, pos) : 1.f / tl;
         const float g0 = f0 * inv, g1 = f1 * inv;
         // a chain without steps has no output: what is there is nobody's
         if (cnt < 2) {

@@ -613,7 +613,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
       float la, lb;
       unpack2(l2, la, lb);
       const float l = la + lb;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // without weights: zero where a row sees nothing; else all scores were minus infinity, and 0 / 0 is NaN
+      const float inv = l != 0.f ? 1.f / l : it.off + row < 0 ? 0.f : __uint_as_float(0x7FC00000u);
       // Rows that see a listed key. (Every value that is not finite was listed before the last product that met it. A score
       // that is NaN makes the sum NaN, and with it the row: that is its result.)
       bool again = false;

@@ -399,7 +399,7 @@ MOE_API int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_t* 
  * head h reads key head h / (Hq / Hkv). The row at position p of its sequence sees key j when
  *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks):
  * a sliding window and the sequence's first `sinks` tokens, which stay visible. A row that sees nothing
- * gets +0. Keys and values that a row does not see, and what lies in a page behind its sequence's last
+ * gets +0; one whose visible scores are all minus infinity is NaN, as the formula has it. Keys and values that a row does not see, and what lies in a page behind its sequence's last
  * token, do not reach its result whatever they hold, NaN and infinities included. */
 typedef struct moe_attention {
   int32_t B;             /* sequences                                       */

@@ -584,3 +584,26 @@ def test_errors_found_before_a_workspace_grew_are_reported_once():
             p.B.attention_status()
         assert e.value.code == p.B.MOE_ERR_DEVICE_INPUT
         p.B.attention_status()
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv", [(2, 4, 2), (3, 4, 1), (6, 16, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_of_minus_infinity(D, rows, Hq, Hkv):
+    """A row whose scores are all minus infinity is 0 / 0; one finite score takes all; rows that see nothing stay zero, those
+    whose pages are all out of range among them."""
+    p = Paged([40, 1, 3000, 3000], rows, Hq, Hkv, D, 16, False, seed=2)
+    p.q[..., 0] = 1
+    p.cache.k[..., 0] = float("-inf")
+    p.cache.k[int(p.table[3, 60]), :, 5, 0] = 1
+    p.values[0] = p.cache.k.float().cpu().numpy().astype(np.float64)
+    got = p.run().float().cpu().numpy()
+    with np.errstate(all="ignore"):
+        want, mag = p.oracle()
+        near = np.abs(got - want) <= A.attention_tolerance(want, mag)
+    assert np.isnan(want[0]).all() and np.isnan(want[2]).all() and np.isfinite(want[3]).all()
+    assert (want[1, :rows - 1] == 0).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and near[~np.isnan(want)].all()
+    none = p.B.moe_paged_attention(p.q, p.cache, torch.full_like(p.table, -1), p.seq_lens(), 3000)
+    assert not none.any()
+    with pytest.raises(p.B.MoeError):
+        p.B.attention_status()

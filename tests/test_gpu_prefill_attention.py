@@ -345,3 +345,18 @@ def test_thousands_of_short_prompts(Hq, Hkv):
         p.B.attention_status()
     a, z = int(cu[b]), int(cu[b + 2])
     assert torch.equal(got[:a], want[:a]) and torch.equal(got[z:], want[z:]) and (got[a:z] == 7).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 1), (128, 40, 4), (64, 64, 8)])
+def test_scores_of_minus_infinity(D, Hq, Hkv):
+    """A row whose scores are all minus infinity is 0 / 0; one finite score takes all; rows without keys stay zero."""
+    p = Prompts([200, 5, 30], Hq, Hkv, D, k_lens=[200, 2, 30], seed=2)
+    p.q[..., 0] = 1
+    p.k[..., 0] = float("-inf")
+    p.k[100, :, 0] = 1
+    got = _np(p.run())
+    with np.errstate(all="ignore"):
+        want, mag = p.oracle()
+        near = np.abs(got - want) <= A.attention_tolerance(want, mag)
+    assert np.isnan(want[:100]).all() and (want[200:203] == 0).all() and np.isfinite(want[100:200]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and near[~np.isnan(want)].all()
