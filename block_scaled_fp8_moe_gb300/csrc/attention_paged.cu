@@ -884,7 +884,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
     // ((0 + 2) + (1 + 3)): the upper two warps hand theirs to the lower two, those one to the other, 8 rows at a time
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (h == 1 && R <= 8) break;
 #pragma unroll
       for (int far = 2; far; far >>= 1) {
         float* mine = join + ((warp & (far - 1)) * 8 + g) * C::PITCH;
