@@ -638,8 +638,8 @@ class KvCache:
 
 def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
     """Stores the bf16 rows k and v [T, Hkv, D] (rows may lie apart) at slots i32 [T] (page * page_size + place;
-    -1 = not stored; the others must differ). ws: at least 256 bytes of uint8, zeros at first; one per stream is kept where it is not given (inside
-    a graph's capture it has to be)."""
+    -1 = not stored; the others must differ). ws: at least 256 bytes of uint8, zeros at first; one per stream is kept where
+    it is not given (inside a graph's capture it has to be)."""
     dev = _current(k, "k")
     if cache.dev != dev:
         raise ValueError("cache and k must be on the same CUDA device")

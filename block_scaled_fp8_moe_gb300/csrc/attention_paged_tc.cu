@@ -13,7 +13,8 @@
 // chain's products run under the other's softmax:  PV0(0) QK0(2) | PV1(1) QK1(3) | PV0(2) QK0(4) ...  The chains' outputs
 // are joined at the item's end.
 // Pages come by TMA, bf16 straight into the ring that the products read, MXFP8 into a ring of raw codes from where a
-// warpgroup converts them once for all rows (exactly: four significant bits and a power of two fit bf16).
+// warpgroup converts them once for all rows (four significant bits and a power of two fit bf16: exactly, but for scale bytes 0
+// to 2, whose blocks may have codes below bf16's last subnormal, 2^-133, and are rounded to it).
 //
 // What an MXFP8 step takes, about 2,350 cycles, is shared memory's time for the most part: 270 for the codes to come in, 320
 // for them to be read, 512 to be stored converted, 770 for the operands of the products. An item's end takes about 5,000
