@@ -607,3 +607,58 @@ def test_scores_of_minus_infinity(D, rows, Hq, Hkv):
     assert not none.any()
     with pytest.raises(p.B.MoeError):
         p.B.attention_status()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,Hq,Hkv,D,page", [(3, 4, 2, 64, 16), (1, 8, 1, 128, 64), (8, 1, 1, 64, 8), (5, 3, 1, 128, 32)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 4), (16, 0), (64, 4), (100, 70), (128, 300), (1000, 3),
+                                          (257, 129)])
+def test_few_rows_windows_and_first_tokens(window, sinks, rows, Hq, Hkv, D, page, mx):
+    """Up to 8 rows, and up to 16."""
+    Paged([700, 5, 64, 129, 1, 333, 1100], rows, Hq, Hkv, D, page, mx, seed=window).check(window, sinks)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq", [(4, 2), (6, 1), (5, 3), (16, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20), (700, 200)])
+def test_few_rows_infinities_and_nan_that_some_rows_see(window, sinks, rows, Hq, D, mx):
+    """Keys that some rows see and others do not, with values that are not finite: added one by one."""
+    inf = float("inf")
+    lens = [700, 300, 5000]
+    p = Paged(lens, rows, Hq, 1, D, 16, mx, seed=rows + window)
+    for b, n in enumerate(lens):
+        _put(p, b, n - 1, 1, inf)
+        _put(p, b, n - 2, 40, -inf)
+        _put(p, b, 10, 40, inf)
+        _put(p, b, 19, 2, float("nan"))
+        _put(p, b, max(n - rows + 2 - 150, 0), 41, inf)
+        _put(p, b, max(n - rows + 2 - 700, 0), 42, inf)
+    for j in range(200, 290):
+        _put(p, 1, j, 50, inf)
+    _check_not_finite(p, window, sinks)
+
+
+@pytest.mark.parametrize("rows,Hq", [(1, 2), (2, 4), (3, 5), (6, 4), (6, 8)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+def test_mxfp8_scales_over_their_range_for_every_kernel(window, sinks, D, rows, Hq):
+    """Values of up to 2^110 in some blocks, whose scales one factor of the conversion does not hold, beside small ones."""
+    p = Paged([300, 90, 1500], rows, Hq, 1, D, 16, True, seed=12, q_scale=2.0 ** -5)
+    rng = np.random.default_rng(rows)
+    for t, x, low, high in ((p.cache.k, p.cache.k_s, 0, 124), (p.cache.v, p.cache.v_s, 7, 237)):
+        s = rng.integers(low, high, tuple(x.shape), dtype=np.uint8)
+        x.copy_(torch.from_numpy(s).cuda())
+        t &= 0xBF                             # finite codes, of at most 15/8
+    p.values = [F.dequant_blocks(F.decode_e4m3(t.cpu().numpy()), s.cpu().numpy())
+                for t, s in ((p.cache.k, p.cache.k_s), (p.cache.v, p.cache.v_s))]
+    p.check(window, sinks)
+    # a few keys' scores far above the others', by a scale of more than 134
+    for b, j in ((0, 7), (0, 250), (2, 1200), (2, 1499)):
+        page, at = int(p.table[b, j // 16]), j % 16
+        p.cache.k[page, :, at] = 0x38         # ones
+        p.cache.k_s[page, :, at] = 137
+        p.cache.v_s[page, :, at] = 230
+    p.values = [F.dequant_blocks(F.decode_e4m3(t.cpu().numpy()), s.cpu().numpy())
+                for t, s in ((p.cache.k, p.cache.k_s), (p.cache.v, p.cache.v_s))]
+    p.check(window, sinks)
