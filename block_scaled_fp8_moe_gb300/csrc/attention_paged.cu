@@ -992,6 +992,9 @@ __global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const
       make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
 }
 
+// Positions are 32 bits wide, and steps are rounded up to 128 tokens behind the last one.
+constexpr int kMaxLen = 0x7fffffff - 255;
+
 // Blocks of up to 16 rows take steps of 64 tokens, more rows steps of 128.
 static int tile_of(const moe_attention* a, int rows) {
   return rows * (a->Hq / a->Hkv) <= kFewRows ? kTileTok : 2 * kTileTok;
@@ -1062,7 +1065,7 @@ extern "C" int moe_selftest_attention_hold(int32_t load) {
 }
 
 extern "C" size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len) {
-  if (!attention_ok(a) || rows < 1 || rows > 64 || max_len < 0) return 0;
+  if (!attention_ok(a) || rows < 1 || rows > 64 || max_len < 0 || max_len > kMaxLen) return 0;
   const size_t n = part_rows(a, rows, max_len);
   return 256 + align_up(n * a->D * 4, 256) + align_up(n * 8, 256);
 }
@@ -1072,7 +1075,8 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
                                    int32_t table_width, const int32_t* seq_lens, uint16_t* out, void* ws,
                                    size_t ws_bytes, void* stream) {
   if (!a || !cache) return MOE_ERR_INVALID_ARG;
-  if (!attention_ok(a) || !kv_cache_ok(cache) || rows < 1 || rows > 64) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!attention_ok(a) || !kv_cache_ok(cache) || rows < 1 || rows > 64 || max_len > kMaxLen)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (cache->Hkv != a->Hkv || cache->D != a->D) return MOE_ERR_INVALID_ARG;
   if (max_len < 0 || table_width < 0 || max_len > (int64_t)table_width * cache->page_size) return MOE_ERR_INVALID_ARG;
   if (!status_ws_ok(ws, ws_bytes) || ws_bytes < moe_paged_attention_workspace_bytes(a, rows, max_len))

@@ -417,7 +417,8 @@ typedef struct moe_attention {
  * the workspace, not the work. A sequence outside [0, max_len] gets zeros, keys in a page outside [0, pages)
  * are left out, and both are recorded in the status word (MOE_ERR_DEVICE_INPUT).
  * A sequence is cut into pieces by its own length alone and the pieces are joined in order, so a row's
- * result does not depend on its batch. 1 <= rows <= 64; q, out 16-byte aligned, q_stride % 8 == 0.
+ * result does not depend on its batch. 1 <= rows <= 64, max_len <= 2^31 - 256; q, out 16-byte aligned,
+ * q_stride % 8 == 0.
  * ws: moe_paged_attention_workspace_bytes (0 for unsupported sizes). */
 MOE_API size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len);
 MOE_API int moe_paged_attention(const moe_attention* a, const moe_kv_cache* cache, int32_t rows, int32_t max_len,

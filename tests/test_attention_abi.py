@@ -99,3 +99,11 @@ def test_prefill_attention_refusals(B):
     for kw in (dict(ws=N), dict(n=8)):
         assert call(**kw) == B.MOE_ERR_WORKSPACE, kw
     assert call(Tq=0, q=N, out=N) == B.MOE_OK and call(_att(B, B=0), q=N) == B.MOE_OK
+
+
+def test_lengths_whose_last_step_passes_32_bits_are_refused(B):
+    for n in (2 ** 31 - 255, 2 ** 31 - 1):
+        assert B.lib.moe_paged_attention_workspace_bytes(_att(B), 1, n) == 0
+        assert B.lib.moe_paged_attention(_att(B), _cache(B), 1, n, AT, 512, AT, 2 ** 28, AT, AT, AT, 2 ** 60, N) == \
+            B.MOE_ERR_UNSUPPORTED_SHAPE
+    assert B.lib.moe_paged_attention_workspace_bytes(_att(B), 1, 2 ** 31 - 256) > 0
