@@ -14,7 +14,7 @@
 //
 // One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 201 us, 6.2 TB/s. 160 rows of 64
 // heads over 8 of 64, a window of 1024 and 4 first tokens: 63 us, 5.4 TB/s (17 steps a row leave an item little to run
-// ahead of). 256 rows over 4096 MXFP8 tokens: 441 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
+// ahead of). 256 rows over 4096 MXFP8 tokens: 446 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
 // rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -12,8 +12,8 @@
 // (weights of up to 256 are as exact in bf16 as those up to 1), so that the softmax warps seldom touch it.
 //
 // A step of 128 keys takes two tiles about 2650 cycles, of which the products run 2048; an item's end 4000 to 5000, in which
-// none runs. Three prompts of 12288 tokens together, 32 heads of 128, a window of 4096: 382 us, 1.24 PFLOP/s of visible pairs;
-// one of 8192 without a window 330 us, 1.67 PFLOP/s.
+// none runs. Three prompts of 12288 tokens together, 32 heads of 128, a window of 4096: 366 us, 1.29 PFLOP/s of visible pairs;
+// one of 8192 without a window 338 us, 1.63 PFLOP/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -709,7 +709,7 @@ static int launch_prefill(const PrefillArgs& p, cudaStream_t st) {
   if (!rc) rc = p.Tk ? rows_map(&vm, p.v, D, p.a.Hkv, p.Tk, p.v_stride) : rows_map(&vm, p.q, D, p.a.Hq, p.Tq, p.q_stride);
   if (rc) return rc;
   // Two tiles a block take 2650 cycles a step, one alone about 1900: one each where there are blocks enough for it (one
-  // head, 2048 tokens of 128: 24 us against 29; 32 heads, 128 tokens: 6.9 against 8.7).
+  // head, 2048 tokens of 128: 24 us against 29; 32 heads, 128 tokens: 6.4 against 8.7).
   PrefillArgs args = p;
   const bool one = items_of(p, true) <= num_sms();
   if (one) args.pair = 1;
