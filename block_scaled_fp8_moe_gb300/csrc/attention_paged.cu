@@ -14,7 +14,7 @@
 //
 // One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 201 us, 6.2 TB/s. 160 rows of 64
 // heads over 8 of 64, a window of 1024 and 4 first tokens: 63 us, 5.4 TB/s (17 steps a row leave an item little to run
-// ahead of). 256 rows over 4096 MXFP8 tokens: 446 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
+// ahead of). 256 rows over 4096 MXFP8 tokens: 445 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
 // rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -446,12 +446,10 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
   }
 }
 
-// Every warp comes here at its end. A wait that ran out, in whichever of them, is recorded once nobody can give up any more.
-template <class C>
-__device__ __forceinline__ void end_block(const PagedArgs& p, volatile uint32_t* abort) {
+// At the end of every warp: who gave up, or saw that another one had, records it.
+__device__ __forceinline__ void record_end(const PagedArgs& p, volatile uint32_t* abort) {
   __syncwarp();
-  named_bar_sync(2, (C::WARPS + 1) * 32);
-  if (threadIdx.x == 0 && *abort) atomicCAS(p.status, 0u, *abort);
+  if (threadIdx.x % 32 == 0 && *abort) atomicCAS(p.status, 0u, *abort);
 }
 
 template <class C>
@@ -543,10 +541,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         const bool good = want && id >= 0 && id < p.pages;
         if (want && !good) atomicCAS(p.status, 0u, (uint32_t)DEV_BAD_INPUT);
         const uint32_t mask = __ballot_sync(0xffffffffu, good);
-        // a warp that has given up frees stages that may still be on their way
         if (issued >= C::STAGES &&
             !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
-                                                    DEV_TIMEOUT_EMPTY) && !abort_flag)))
+                                                    DEV_TIMEOUT_EMPTY))))
           break;
         if (lane == 0) {
           page_mask[s] = mask;
@@ -576,14 +573,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
     if (lane == 0)
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
         mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
-    end_block<C>(p, &abort_flag);
+    record_end(p, &abort_flag);
     return;
   }
 
   // ---------------- consumers ----------------
   if constexpr (C::EIGHT) {
     consume_eight<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
-    end_block<C>(p, &abort_flag);
+    record_end(p, &abort_flag);
     return;
   }
   const int g = lane >> 2, c = lane & 3;
@@ -932,7 +929,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
     }
     if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   }
-  end_block<C>(p, &abort_flag);
+  record_end(p, &abort_flag);
 }
 
 // The pieces' parts joined in order, a thread per four columns of a row, rows next to each other. Rows of one piece are
