@@ -662,3 +662,28 @@ def test_mxfp8_scales_over_their_range_for_every_kernel(window, sinks, D, rows, 
     p.values = [F.dequant_blocks(F.decode_e4m3(t.cpu().numpy()), s.cpu().numpy())
                 for t, s in ((p.cache.k, p.cache.k_s), (p.cache.v, p.cache.v_s))]
     p.check(window, sinks)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("rows,Hq,Hkv,D", [(2, 4, 2, 64), (8, 1, 1, 128), (4, 4, 1, 128), (3, 4, 1, 64), (6, 16, 2, 64), (60, 3, 1, 128)])
+def test_rows_that_see_nothing_are_plus_zero(rows, Hq, Hkv, D, mx):
+    """Bit for bit, beside values below zero: before their sequence begins, in a batch of one piece and of many, over pages
+    out of range, and for a length out of range."""
+    for longest in (70, 9000):
+        p = Paged([1, rows - 1, 0, longest], rows, Hq, Hkv, D, 16, mx, seed=2)
+        if mx:
+            p.cache.v |= 0x80
+        else:
+            p.cache.v.copy_(-p.cache.v.abs())
+        got = p.run().view(torch.int16)
+        assert not got[0, :rows - 1].any() and not got[1, :1].any() and not got[2].any() and got[3].any()
+        p.B.attention_status()
+        none = p.B.moe_paged_attention(p.q, p.cache, torch.full_like(p.table, -1), p.seq_lens(), longest).view(torch.int16)
+        assert not none.any()
+        with pytest.raises(p.B.MoeError):
+            p.B.attention_status()
+        lens = torch.tensor([1, -5, 0, longest + 1], dtype=torch.int32, device="cuda")
+        got = p.B.moe_paged_attention(p.q, p.cache, p.table, lens, longest).view(torch.int16)
+        assert not got[1:].any()
+        with pytest.raises(p.B.MoeError):
+            p.B.attention_status()

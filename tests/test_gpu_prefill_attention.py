@@ -360,3 +360,12 @@ def test_scores_of_minus_infinity(D, Hq, Hkv):
         near = np.abs(got - want) <= A.attention_tolerance(want, mag)
     assert np.isnan(want[:100]).all() and (want[200:203] == 0).all() and np.isfinite(want[100:200]).all()
     assert np.array_equal(np.isnan(got), np.isnan(want)) and near[~np.isnan(want)].all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 1), (128, 40, 4), (64, 64, 8), (128, 33, 11)])
+def test_rows_that_see_nothing_are_plus_zero(D, Hq, Hkv):
+    """Bit for bit, beside values below zero: rows before their first key, in prompts with fewer keys than rows or none."""
+    p = Prompts([300, 5, 30], Hq, Hkv, D, k_lens=[40, 0, 30], seed=2)
+    p.v.copy_(-p.v.abs())
+    got = p.run().view(torch.int16)
+    assert not got[:260].any() and not got[300:305].any() and got[260:300].any() and got[305:].any()
