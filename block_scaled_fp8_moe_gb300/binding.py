@@ -31,7 +31,7 @@ EXPORTED = [
     "moe_shared_workspace_bytes", "moe_forward_shared", "moe_dead_from_survival", "moe_w2_grouped", "moe_combine",
     "moe_probe_mma_rate", "moe_quant_mxfp8_plan", "moe_experts_grouped", "moe_add_rmsnorm_mxfp8", "moe_kv_append",
     "moe_paged_attention_workspace_bytes", "moe_paged_attention", "moe_prefill_attention",
-    "moe_selftest_attention_hold",
+    "moe_selftest_attention_hold", "moe_rotary_turns", "moe_rope", "moe_rope_kv_append",
 ]
 
 MOE_FLAG_SWIGLU_DEBUG = 1
@@ -63,6 +63,12 @@ class MoeKvCache(ctypes.Structure):
 class MoeAttention(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeRotary(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("factor", ctypes.c_float), ("turns", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -117,6 +123,11 @@ lib.moe_paged_attention_workspace_bytes.restype = _SZ
 lib.moe_paged_attention_workspace_bytes.argtypes = [_ATT, _I32, _I32]
 lib.moe_paged_attention.argtypes = [_ATT, _KVC, _I32, _I32, _P, _I64, _P, _I32, _P, _P, _P, _SZ, _P]
 lib.moe_prefill_attention.argtypes = [_ATT, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]
+_ROT = ctypes.POINTER(MoeRotary)
+lib.moe_rotary_turns.argtypes = [_I32, _P, _P]
+lib.moe_rope.argtypes = [_ROT, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]
+lib.moe_rope_kv_append.argtypes = [_ROT, _KVC, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64,
+                                   _P, _SZ, _P]
 for _n in EXPORTED:
     if _n not in ("moe_status_string", "moe_workspace_bytes", "moe_packed_w13_bytes", "moe_packed_w2_bytes",
                   "moe_packed_shared_w13_bytes", "moe_packed_shared_w2_bytes", "moe_shared_workspace_bytes",
@@ -432,10 +443,11 @@ def moe_forward(shp: MoeShape, x, w_router, bias, dead, w13p, w13sp, w2p, w2sp, 
 
 
 # --------------------------------------------------------------------------------------------------
-# Residual norm, key/value cache, attention
+# Residual norm, rotary positions, key/value cache, attention
 # --------------------------------------------------------------------------------------------------
 MOE_KV_BF16 = 0
 MOE_KV_MXFP8 = 1
+MOE_KV_MXFP4 = 4
 
 
 # These calls run once or more per layer and step, where the host's time counts as much as the kernel's: addresses
@@ -465,7 +477,7 @@ def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[
     if h != heads or d != D:
         raise ValueError(f"{name} must be [rows, {heads}, {D}], is {tuple(t.shape)}")
     row, head, one = t.stride()
-    if (one != 1 and d > 1) or (head != D and h > 1):
+    if n * h and ((one != 1 and d > 1) or (head != D and h > 1)):
         raise ValueError(f"{name}: a row's heads must be contiguous")
     return t.data_ptr(), row if n > 1 else h * d
 
@@ -606,8 +618,9 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
 
 
 class KvCache:
-    """A paged key/value cache: k and v [pages, Hkv, page_size, D] in bf16, or u8 E4M3 codes with u8 UE8M0 scales
-    k_s and v_s [pages, Hkv, page_size, D/32] (see include/moe.h). Holds the tensors it is given."""
+    """A paged key/value cache: k and v [pages, Hkv, page_size, D] in bf16, or u8 codes with u8 UE8M0 scales k_s and v_s
+    [pages, Hkv, page_size, D/32]: E4M3, or E2M1 two to a byte, [pages, Hkv, page_size, D/2] (see include/moe.h).
+    Holds the tensors it is given."""
 
     def __init__(self, k, v, k_s=None, v_s=None):
         dev = _current(k, "k")
@@ -615,6 +628,10 @@ class KvCache:
         if k.dim() != 4 or v.shape != k.shape or (mx != (v_s is not None)):
             raise ValueError("k and v must be [pages, Hkv, page_size, D], with both scale tensors or none")
         pages, Hkv, page_size, D = k.shape
+        # codes of 4 bits have a scale for 16 bytes, codes of 8 bits one for 32
+        four = mx and k_s.dim() == 4 and k_s.shape[3] > 0 and D == 16 * k_s.shape[3]
+        if four:
+            D *= 2
         dtype = torch.uint8 if mx else torch.bfloat16
         ptrs = [_on(k, "k", dtype, dev), _on(v, "v", dtype, dev), None, None]
         if mx:
@@ -624,13 +641,16 @@ class KvCache:
                 ptrs[2 + i] = _on(t, name, torch.uint8, dev)
         self.k, self.v, self.k_s, self.v_s, self.dev = k, v, k_s, v_s, dev
         self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
-        self.desc = MoeKvCache(pages, page_size, Hkv, D, MOE_KV_MXFP8 if mx else MOE_KV_BF16, *ptrs)
+        self.format = MOE_KV_MXFP4 if four else MOE_KV_MXFP8 if mx else MOE_KV_BF16
+        self.desc = MoeKvCache(pages, page_size, Hkv, D, self.format, *ptrs)
         self.ref = ctypes.byref(self.desc)
 
     @classmethod
-    def empty(cls, pages: int, page_size: int, Hkv: int, D: int, mxfp8: bool = False, device="cuda"):
-        shp = (pages, Hkv, page_size, D)
-        if not mxfp8:
+    def empty(cls, pages: int, page_size: int, Hkv: int, D: int, mxfp8: bool = False, device="cuda", mxfp4: bool = False):
+        if mxfp8 and mxfp4:
+            raise ValueError("a cache has one format: mxfp8 or mxfp4")
+        shp = (pages, Hkv, page_size, D // 2 if mxfp4 else D)
+        if not mxfp8 and not mxfp4:
             return cls(*(torch.zeros(shp, dtype=torch.bfloat16, device=device) for _ in range(2)))
         k, v = (torch.zeros(shp, dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, *(torch.zeros(*shp[:3], D // 32, dtype=torch.uint8, device=device) for _ in range(2)))
@@ -654,6 +674,116 @@ def moe_kv_append(cache: KvCache, k, v, slots, ws=None, stream=None) -> None:
     rc = lib.moe_kv_append(cache.ref, T, pk, sk, pv, sv, ps, pws, nws, raw)
     if rc:
         _check(rc, "moe_kv_append")
+
+
+class Rotary:
+    """Rotary positions: the frequencies of a head's pairs (a tensor or a sequence of numbers, taken in 64 bits), which axis each
+    turns by (`axis`, a sequence of indexes; all 0 where it is not given) of `axes` positions a token has, whether pairs are
+    neighbours (2i, 2i + 1) or (i, i + dim/2), and a factor on cosines and sines (see include/moe.h). Holds its tables on
+    `device`."""
+
+    def __init__(self, inv_freq, axis=None, axes: int | None = None, interleaved: bool = False, factor: float = 1.0,
+                 device="cuda"):
+        freq = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+        if freq.dim() != 1 or not len(freq):
+            raise ValueError("inv_freq must be one frequency for every pair")
+        n = len(freq)
+        turns = torch.empty(n, dtype=torch.int64)
+        _check(lib.moe_rotary_turns(n, freq.data_ptr(), turns.data_ptr()), "moe_rotary_turns")
+        self.axis = None
+        if axis is not None:
+            which = torch.as_tensor(axis).cpu()
+            if which.dim() != 1 or len(which) != n or which.is_floating_point():
+                raise ValueError(f"axis needs {n} indexes, one for every pair")
+            axes = int(which.max()) + 1 if axes is None else axes
+            if int(which.min()) < 0 or int(which.max()) >= axes:
+                raise ValueError(f"axis must hold indexes below {axes}")
+            self.axis = which.to(torch.uint8).to(device)
+        self.turns = turns.to(device)
+        self.dim, self.axes, self.dev = 2 * n, 1 if axes is None else axes, self.turns.get_device()
+        self.refs = [ctypes.byref(MoeRotary(2 * n, self.axes, bool(interleaved), back, factor, self.turns.data_ptr(),
+                                            None if self.axis is None else self.axis.data_ptr())) for back in (0, 1)]
+
+
+def _positions(rotary: Rotary, pos, T: int, dev: int) -> int:
+    if rotary.dev != dev:
+        raise ValueError(f"rotary must be on device {dev}")
+    if tuple(pos.shape) != (rotary.axes, T) and (rotary.axes > 1 or tuple(pos.shape) != (T,)):
+        raise ValueError(f"pos must be [{rotary.axes}, {T}], is {tuple(pos.shape)}")
+    return _on(pos, "pos", torch.int32, dev)
+
+
+def _out_rows(out, name: str, like, x: int, stride: int, dev: int) -> tuple[int, int]:
+    """The address and the row stride of where `like`'s rows (at x, apart by stride) go: themselves, or rows of their own."""
+    T, heads, D = like.shape
+    po, so = _rows_on(out, name, heads, D, dev)
+    if out.shape[0] != T:
+        raise ValueError(f"{name} needs {T} rows, has {out.shape[0]}")
+    if T * heads and po == x and so != stride:
+        raise ValueError(f"{name} must not overlap what is read, or be the same rows")
+    return po, so
+
+
+def moe_rope(rotary: Rotary, q, k, pos, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Turns q bf16 [T, Hq, D] and k bf16 [T, Hkv, D] (or None; rows may lie apart) by the positions pos i32 [T] or [axes, T].
+    Returns (q_out, k_out), which may be q and k themselves (turned where they are). inverse: turns back, which is also
+    the gradient: of q and k, from that of the results."""
+    dev = _current(q, "q")
+    T, Hq, D = q.shape
+    pq, sq = _rows_on(q, "q", Hq, D, dev)
+    Hkv, pk, sk, pko, sko = 0, None, 0, None, 0
+    if k is not None:
+        Hkv = k.shape[1]
+        pk, sk = _rows_on(k, "k", Hkv, D, dev)
+        if k.shape[0] != T:
+            raise ValueError(f"k needs {T} rows, has {k.shape[0]}")
+    elif k_out is not None:
+        raise ValueError("k_out is not written without k")
+    pp = _positions(rotary, pos, T, dev)
+    with _allocating(stream):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device)
+    pqo, sqo = _out_rows(q_out, "q_out", q, pq, sq, dev)
+    if k is not None:
+        pko, sko = _out_rows(k_out, "k_out", k, pk, sk, dev)
+    rc = lib.moe_rope(rotary.refs[bool(inverse)], T, Hq, Hkv, D, pq, sq, pk, sk, pp, T, pqo, sqo, pko, sko,
+                      _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_rope")
+    return q_out, k_out
+
+
+def moe_rope_kv_append(rotary: Rotary, cache: KvCache, q, k, v, pos, slots, q_out=None, k_out=None, ws=None, stream=None):
+    """moe_kv_append of k and v [T, Hkv, D] with the keys turned on the way, and q [T, Hq, D] turned into q_out (which may be q
+    itself); pos as for moe_rope, slots and ws as for moe_kv_append. Where k_out is given (k itself, or rows of its own), the
+    turned keys go there too, for a prompt's own attention. Returns q_out."""
+    dev = _current(q, "q")
+    if cache.dev != dev:
+        raise ValueError("cache and q must be on the same CUDA device")
+    T, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"q must be [rows, heads, {cache.D}], is {tuple(q.shape)}")
+    pq, sq = _rows_on(q, "q", Hq, D, dev)
+    pk, sk = _rows_on(k, "k", cache.Hkv, D, dev)
+    pv, sv = _rows_on(v, "v", cache.Hkv, D, dev)
+    if k.shape[0] != T or v.shape[0] != T or slots.numel() != T:
+        raise ValueError(f"k, v and slots need {T} rows, have {k.shape[0]}, {v.shape[0]} and {slots.numel()}")
+    pp = _positions(rotary, pos, T, dev)
+    ps = _on(slots, "slots", torch.int32, dev)
+    if q_out is None:
+        with _allocating(stream):
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    pqo, sqo = _out_rows(q_out, "q_out", q, pq, sq, dev)
+    pko, sko = (None, 0) if k_out is None else _out_rows(k_out, "k_out", k, pk, sk, dev)
+    raw = _raw_stream(stream, dev)
+    pws, nws = _workspace(256, q, stream, dev, raw) if ws is None else (_on(ws, "ws", torch.uint8, dev), ws.numel())
+    rc = lib.moe_rope_kv_append(rotary.refs[0], cache.ref, T, Hq, pq, sq, pk, sk, pv, sv, pp, T, ps, pqo, sqo, pko, sko,
+                                pws, nws, raw)
+    if rc:
+        _check(rc, "moe_rope_kv_append")
+    return q_out
 
 
 def moe_paged_attention_workspace_bytes(B: int, rows: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:

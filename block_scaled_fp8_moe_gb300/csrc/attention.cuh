@@ -18,12 +18,12 @@ inline bool attention_ok(const moe_attention* a) {
 
 inline bool kv_cache_ok(const moe_kv_cache* c) {
   return c && c->pages > 0 && c->Hkv > 0 && (c->D == 64 || c->D == 128) && c->page_size >= 8 && c->page_size <= 256 &&
-         (c->page_size & (c->page_size - 1)) == 0 && (c->format == MOE_KV_BF16 || c->format == MOE_KV_MXFP8) &&
+         (c->page_size & (c->page_size - 1)) == 0 && (c->format == MOE_KV_BF16 || c->format == MOE_KV_MXFP8 || c->format == MOE_KV_MXFP4) &&
          (int64_t)c->pages * c->Hkv < ((int64_t)1 << 31) / c->page_size;
 }
 
 inline bool kv_cache_pointers_ok(const moe_kv_cache* c) {
-  const bool mx = c->format == MOE_KV_MXFP8;
+  const bool mx = c->format != MOE_KV_BF16;
   if (!c->k || !c->v || (mx && (!c->k_s || !c->v_s))) return false;
   uintptr_t any = reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v);
   if (mx) any |= reinterpret_cast<uintptr_t>(c->k_s) | reinterpret_cast<uintptr_t>(c->v_s);
@@ -73,6 +73,12 @@ __device__ __forceinline__ float e4m3(uint32_t c) {
   return __uint_as_float(((c & 0x80u) << 24) | ((c & 0x7Fu) << 20)) * __uint_as_float((127u + 120u) << 23);
 }
 
+// One E2M1 code in fp32.
+__device__ __forceinline__ float e2m1(uint32_t c) {
+  // as above: exponent and fraction moved into fp32's places give the value times 2^(1 - 127)
+  return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float((127u + 126u) << 23);
+}
+
 // A lane's part of a row of D values: the values lane * D/32 ... in fp32.
 template <int D>
 struct LaneRow {
@@ -90,6 +96,11 @@ struct LaneRow {
     const float sc = ue8m0(scales[lane * N / 32]);
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = e4m3(row[lane * N + i]) * sc;
+  }
+  __device__ __forceinline__ void load_mxfp4(const uint8_t* row, const uint8_t* scales, int lane) {
+    const float sc = ue8m0(scales[lane * N / 32]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = e2m1((row[(lane * N + i) / 2] >> (4 * (i & 1))) & 15u) * sc;
   }
 };
 

@@ -48,18 +48,18 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-template <int D_, bool MX_, bool EIGHT_>
+template <int D_, int FMT_, bool EIGHT_>
 struct PagedCfg {
-  static constexpr int D = D_;
-  static constexpr bool MX = MX_, EIGHT = EIGHT_;                  // EIGHT: up to 8 rows, as a product's columns
+  static constexpr int D = D_, FMT = FMT_, BITS = format_bits(FMT_);
+  static constexpr bool MX = FMT_ != MOE_KV_BF16, EIGHT = EIGHT_;  // EIGHT: up to 8 rows, as a product's columns
   // Blocks of a multiprocessor. Up to 16 rows take 168 registers, up to 8 rows 128 or less. Measured with 2, 3 and 4 blocks:
   // 256 sequences of 4096 tokens, 32 heads over 8 of 128, MXFP8 651 (16 rows' code), 441, 456 us; 64 over 8 of 64, MXFP8
   // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us.
   static constexpr int CTAS = !EIGHT ? 2 : MX && D == 64 ? 4 : 3;
   static constexpr int WARPS = 4, ST = kTileTok / WARPS;           // tokens of a stage that a warp takes
   static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
-  static constexpr int ROWB = MX ? D : 128;                        // bytes of a row in a column block
-  static constexpr int KV = kTileTok * D * (MX ? 1 : 2);           // bytes of a stage's keys, or values
+  static constexpr int ROWB = MX ? D * BITS / 8 : 128;             // bytes of a row in a column block
+  static constexpr int KV = kTileTok * D * BITS / 8;               // bytes of a stage's keys, or values
   static constexpr int SC = MX ? kTileTok * D / 32 : 0;
   static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
   static constexpr int STAGES = (CTAS == 4 ? 45056 : CTAS == 3 ? 65536 : 98304) / STAGE;
@@ -82,7 +82,8 @@ __device__ __forceinline__ bool consumers_any(bool said) {
 template <class C>
 __device__ __forceinline__ uint32_t kv_addr(uint32_t base, int tok, int chunk) {
   if (C::ROWB == 128) return base + (chunk >> 3) * (kTileTok * 128) + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
-  return base + tok * 64 + ((chunk ^ ((tok >> 1) & 3)) << 4);
+  if (C::ROWB == 64) return base + tok * 64 + ((chunk ^ ((tok >> 1) & 3)) << 4);
+  return base + tok * 32 + ((chunk ^ ((tok >> 2) & 1)) << 4);
 }
 
 template <class C>
@@ -446,6 +447,475 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
   }
 }
 
+// ---- MXFP4 ----
+// The consuming warps' work over MXFP4, for up to 16 rows: the rows are the columns of both products, 8 at a time, and the codes
+// their other side, as f16, which holds an E2M1 code and has an instruction for two of them. What f16's range asks for:
+//  - a query is scaled to less than 2 by a power of two of its row: what is 2^-17 of the largest or more keeps all of bf16's
+//    digits, the rest is rounded to 2^-25 of it, as fp32 sums would; a block's scale is put on its 32 products' sum, in fp32;
+//  - weights are 2^kLift times themselves at most 2^kGrow (the maximum that they refer to moves when outgrown by that): weights
+//    below 2^-24 - kLift of the largest become zero, 2^17 tokens of them 2^-13 of the result;
+//  - a thread's values are all of one block's columns and are held in units of 2^E, E the largest scale of that block so far:
+//    scales down to 2^-12 of it keep codes exact. Keys further apart go through bf16, in units of their own (`wide`).
+// Conversion: an instruction for two keys' codes; of values' codes, which lie the other way round, half a one more to put two
+// keys' codes into one byte, and one for the scales.
+constexpr float kFewLift = 7.f, kFewGrow = 8.f;
+constexpr int kSpread = 12;
+
+// The token of a warp's 16 that is row i of the products. Neighbouring threads' values are then in different banks.
+template <int D>
+__device__ __forceinline__ int tok_of(int i) {
+  return D == 128 ? (i & 12) | (i & 1) << 1 | (i >> 1 & 1) : (i & 8) | (i & 1) << 2 | (i >> 1 & 3);
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float f16_lo(uint32_t w) {
+  float r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_lo(w >> 16); }
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^e, 0 below 2^-149 (e <= 127).
+__device__ __forceinline__ float pow2i(int e) {
+  return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : e >= -149 ? __uint_as_float(1u << (e + 149)) : 0.f;
+}
+
+template <class C>
+__device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, float* join, uint64_t* full, uint64_t* empty,
+                                             uint64_t* w_full, uint64_t* w_empty, const uint32_t* page_mask,
+                                             const FewItem* items, float2 (*sums)[16], volatile uint32_t* abort, int warp,
+                                             int lane) {
+  constexpr int D = C::D, ST = C::ST, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
+  static_assert(ST == 16, "a warp's tokens of a stage are a product's rows");
+  const int g = lane >> 2, c = lane & 3, G = p.G, R = p.R;
+  const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;
+  const float scale = p.a.scale * 1.4426950408889634f;
+  const int tg = tok_of<D>(g);
+  uint32_t qf[NB][D / 16][2];
+  float qs[NB][2];                              // of rows 2c and 2c + 1: what their queries were divided by
+  auto load_q = [&](int n) {
+    if (!__all_sync(0xffffffffu, bar_wait(&w_full[n & 1], (n >> 1) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) ||
+        !items[n & 1].there)
+      return false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int rho = 8 * nb + g, r = rho / G;
+      const uint16_t* row = p.q + ((long long)items[n & 1].b * p.rows + r) * p.q_stride + (long long)(items[n & 1].hk * G + rho - r * G) * D;
+      uint4 w[D / 32];                          // block by block the 8 values whose codes one thread has at hand
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int bl = 0; bl < D / 32; ++bl) {
+        w[bl] = rho < R ? *reinterpret_cast<const uint4*>(row + bl * 32 + 8 * c) : make_uint4(0, 0, 0, 0);
+        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[bl].x & 0x7FFF7FFFu, w[bl].y & 0x7FFF7FFFu),
+                                   __vmaxu2(w[bl].z & 0x7FFF7FFFu, w[bl].w & 0x7FFF7FFFu)));
+      }
+      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // a row with a value that is not finite: the others do not matter, and stay out of f16's way
+      const bool finite = m < 0x7F80u;
+      const int e = min(max((int)(m >> 7), 1), 253);
+      const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+      auto conv = [&](uint32_t x) {
+        float lo = bf16_lo(x), hi = bf16_hi(x);
+        if (finite) lo *= down, hi *= down;
+        else lo = isfinite(lo) ? 0.f : lo, hi = isfinite(hi) ? 0.f : hi;
+        return f16x2(lo, hi);
+      };
+#pragma unroll
+      for (int bl = 0; bl < D / 32; ++bl) {
+        qf[nb][2 * bl][0] = conv(w[bl].x), qf[nb][2 * bl][1] = conv(w[bl].y);
+        qf[nb][2 * bl + 1][0] = conv(w[bl].z), qf[nb][2 * bl + 1][1] = conv(w[bl].w);
+      }
+      const float up = finite ? __uint_as_float((uint32_t)e << 23) : 1.f;
+      qs[nb][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+      qs[nb][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+    }
+    return true;
+  };
+  int tiles = 0;                                // steps so far
+  // the warps go on together or not at all, also when one of them has given up
+  bool stop = consumers_any<C::WARPS>(!load_q(0));
+  for (int n = 0; !stop; ++n) {
+    const FewItem& it = items[n & 1];
+    const int cnt = it.cnt;
+    int pos[NB][2], first[NB][2];
+    float o[NB][MT][4], ol[NB][4], m[NB][2];    // ol: the weights' sums, by a product with ones
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rho = 8 * nb + 2 * c + e;
+        pos[nb][e] = rho < R ? it.pos0 + rho / G : -1;
+        first[nb][e] = (p.a.window && pos[nb][e] >= p.a.window) ? pos[nb][e] + 1 - p.a.window : 0;
+        m[nb][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.f;
+      ol[nb][0] = ol[nb][1] = ol[nb][2] = ol[nb][3] = 0.f;
+    }
+    int E = -1;                                 // scale byte of the outputs' unit; none yet
+    bool wide = false;                          // for all of the warp
+
+    for (int i = 0; i < cnt; ++i, ++tiles) {
+      const int s = tiles % C::STAGES;
+      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) {
+        __all_sync(0xffffffffu, false);         // told to those that go on below
+        break;
+      }
+      if (!__all_sync(0xffffffffu, true)) break;
+      const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
+      const uint8_t* st = smem + s * C::STAGE;
+      const uint32_t kb = smem_u32(st), vb = kb + C::KV;
+      const uint32_t mask = page_mask[s];
+      // every row of the block sees every token of this warp
+      const bool whole = tok0 + ST - 1 <= it.pmin && (tok0 >= it.first_all || tok0 + ST <= p.a.sinks) &&
+                         mask == (1u << in_tile) - 1u;
+      if (tok0 <= it.pmax) {
+        // ---- scores ----
+        float sc[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
+        {
+          const uint8_t* scales = st + 2 * C::KV;
+          uint32_t sw[2], w[2][D / 32];
+          bool bad[2];                          // a block's scale is NaN
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = loc0 + tg + 8 * h;
+            sw[h] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
+                             : *reinterpret_cast<const uint16_t*>(scales + t * 2);
+            bad[h] = ((~sw[h] - 0x01010101u) & sw[h] & 0x80808080u) != 0;
+#pragma unroll
+            for (int bl = 0; bl < D / 32; ++bl)
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(kv_addr<C>(kb, t, bl) + 4 * c) : "memory");
+          }
+#pragma unroll
+          for (int bl = 0; bl < D / 32; ++bl) {
+            const uint32_t x0[4] = {e2m1_pair<0>(w[0][bl]), e2m1_pair<0>(w[1][bl]), e2m1_pair<1>(w[0][bl]), e2m1_pair<1>(w[1][bl])};
+            const uint32_t x1[4] = {e2m1_pair<2>(w[0][bl]), e2m1_pair<2>(w[1][bl]), e2m1_pair<3>(w[0][bl]), e2m1_pair<3>(w[1][bl])};
+            float f[2];                         // 2^(byte - 127); 2^-127 is below fp32's normal numbers
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              f[h] = __uint_as_float(max((bl < 3 ? sw[h] << (23 - 8 * bl) : sw[h] >> 1) & 0x7F800000u, 0x00400000u));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float a[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16816_f16(a, x0, qf[nb][2 * bl][0], qf[nb][2 * bl][1]);
+              mma_16816_f16(a, x1, qf[nb][2 * bl + 1][0], qf[nb][2 * bl + 1][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[nb][e] = fmaf(a[e], f[e >> 1], sc[nb][e]);
+            }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sc[nb][e] = sc[nb][e] * qs[nb][e & 1] * scale;
+              if (bad[e >> 1]) sc[nb][e] = __uint_as_float(0x7FC00000u);
+            }
+        }
+        // the values' codes, under way while the weights are worked out: thread (g, c) has the D/8 values from g D/8 on of its
+        // four tokens; product j takes the 2j-th of each as its row g, and the next as its row g + 8
+        uint32_t w[4][VW], by[4];
+        {
+          const uint8_t* scales = st + 2 * C::KV + C::SC;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tk = loc0 + tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1);
+            if constexpr (D == 128)
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
+                           : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
+            else
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[e][0])
+                           : "r"(kv_addr<C>(vb, tk, g >> 2) + 4 * (g & 3)) : "memory");
+            by[e] = scales[tk * (D / 32) + g / (256 / D)];
+          }
+        }
+
+        // ---- what the rows do not see ----
+        uint32_t drop = 0, some = 0;             // of this warp's tokens: no row sees it; some row does, some does not
+        if (!whole) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int loc = tg + 8 * (e >> 1), t = tok0 + loc;
+              const bool there = (mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u;
+              const bool see = there && t <= pos[nb][e & 1] && (t >= first[nb][e & 1] || t < p.a.sinks);
+              sc[nb][e] = see ? sc[nb][e] : -INFINITY;
+            }
+          const int t = tok0 + lane;
+          const bool there = lane < ST && ((mask >> ((loc0 + lane) >> min(p.page_log2, 6))) & 1u);
+          const bool any = there && t <= it.pmax && (t >= it.first_any || t < p.a.sinks);
+          const bool all = any && t <= it.pmin && (t >= it.first_all || t < p.a.sinks);
+          drop = __ballot_sync(0xffffffffu, lane < ST && !any);
+          some = __ballot_sync(0xffffffffu, any && !all);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)           // whose codes and scales may be anything
+            if ((drop >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u) {
+#pragma unroll
+              for (int v = 0; v < VW; ++v) w[e][v] = 0;
+              by[e] = max(E, 0);
+            }
+        }
+
+        // ---- where weights and outputs refer to ----
+        uint32_t nan = 0;                       // tokens whose block here has the scale NaN and that not all rows see
+        bool move = wide, nans = false;
+        {
+          const uint32_t hi = max(max(by[0], by[1]), max(by[2], by[3])), lo = min(min(by[0], by[1]), min(by[2], by[3]));
+          move = move || (int)hi > E || (int)lo < E - kSpread;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) move = move || sc[nb][e] > m[nb][e & 1] + kFewGrow;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float mx[2], k[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[e] = fmaxf(sc[nb][e], sc[nb][2 + e]);
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+              if (!(mx[e] > m[nb][e] + kFewGrow)) mx[e] = m[nb][e];
+              k[e] = mx[e] == -INFINITY ? 1.f : ex2(m[nb][e] - mx[e]);
+              m[nb][e] = mx[e];
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j) o[nb][j][0] *= k[0], o[nb][j][1] *= k[1], o[nb][j][2] *= k[0], o[nb][j][3] *= k[1];
+            ol[nb][0] *= k[0], ol[nb][1] *= k[1];
+          }
+          // The unit: the largest scale of a block whose codes are not all zero. Blocks of zeros have any scale.
+          int hi = -1;
+          bool not_zero[4], far = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int v = 0; v < VW; ++v) any |= w[e][v] & 0x77777777u;
+            not_zero[e] = any != 0;
+            nans = nans || by[e] == 255u;
+            if (by[e] == 255u) {                // NaN, whatever the codes
+              const int loc = tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1);
+              if ((some >> loc) & 1u) nan |= 1u << loc;
+            } else if (any) {
+              hi = max(hi, (int)by[e]);
+            }
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d *= 2) {
+            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+            nan |= __shfl_xor_sync(0xffffffffu, nan, d);
+          }
+          const int was = E;
+          if (!wide) E = max(E, hi);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!not_zero[e] && by[e] != 255u) by[e] = max(E, 0);
+            far = far || (int)by[e] < E - kSpread;
+          }
+          wide = wide || __any_sync(0xffffffffu, far);
+          // units of 1, or of 2^35 where a value is too large for sums in those: what is below 2^-126 of them loses digits
+          if (wide) E = max(E, hi) > 212 || E == 162 ? 162 : 127;
+          if (was >= 0 && was != E) {
+            const float k = pow2i(min(was - E, 127));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < MT; ++j) o[nb][j][0] *= k, o[nb][j][1] *= k, o[nb][j][2] *= k, o[nb][j][3] *= k;
+          }
+        }
+
+        // ---- weights ----
+        // Rounded to 16 bits for the second product; the sum takes the rounded ones, so that a single large weight divides out
+        // exactly.
+        float wt[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            wt[nb][e] = ex2(sc[nb][e] - (m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1] - kFewLift));
+
+        // ---- weighted values ----
+        if (!wide) {
+          uint32_t pf[NB][2];
+          const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            pf[nb][0] = transposed(f16x2(wt[nb][0], wt[nb][1]));
+            pf[nb][1] = transposed(f16x2(wt[nb][2], wt[nb][3]));
+            mma_16816_f16(ol[nb], ones, pf[nb][0], pf[nb][1]);
+          }
+          uint32_t fac[2];                      // of two tokens each: 2^(byte - E) in f16
+#pragma unroll
+          for (int h = 0; h < 2; ++h) fac[h] = ((by[2 * h] | by[2 * h + 1] << 16) - (uint32_t)((E - 15) * 0x10001)) << 10;
+          if (nans) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (by[e] == 255u) {
+                const bool later = (some >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u;
+                const uint32_t sh = 16 * (e & 1);
+                fac[e >> 1] = (fac[e >> 1] & ~(0xFFFFu << sh)) | (later ? 0u : 0x7E00u) << sh;
+              }
+          }
+#pragma unroll
+          for (int v = 0; v < VW; ++v) {
+            // one byte of two neighbouring tokens' codes of the same column
+            uint32_t even[2], odd[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x = w[2 * h][v], y = w[2 * h + 1][v];
+              even[h] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+              odd[h] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+            }
+            auto product = [&](auto b) {
+              constexpr int I = decltype(b)::value;
+              const uint32_t x[4] = {mul_f16x2(e2m1_pair<I>(even[0]), fac[0]), mul_f16x2(e2m1_pair<I>(odd[0]), fac[0]),
+                                     mul_f16x2(e2m1_pair<I>(even[1]), fac[1]), mul_f16x2(e2m1_pair<I>(odd[1]), fac[1])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_16816_f16(o[nb][4 * v + I], x, pf[nb][0], pf[nb][1]);
+            };
+            product(std::integral_constant<int, 0>{});
+            product(std::integral_constant<int, 1>{});
+            product(std::integral_constant<int, 2>{});
+            product(std::integral_constant<int, 3>{});
+          }
+        } else {
+          uint32_t pf[NB][2];
+          const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            pf[nb][0] = transposed(bf16x2(wt[nb][0], wt[nb][1]));
+            pf[nb][1] = transposed(bf16x2(wt[nb][2], wt[nb][3]));
+            mma_16816(ol[nb], ones, pf[nb][0], pf[nb][1]);
+          }
+          float fac[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            fac[e] = by[e] != 255u ? pow2i(min((int)by[e] - E, 127))
+                     : (some >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u ? 0.f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+          for (int v = 0; v < VW; ++v)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              uint32_t x[4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                // columns 2b and 2b + 1 of either token
+                const uint32_t u = e2m1_pair<0>(w[2 * h][v] >> (8 * b)), y = e2m1_pair<0>(w[2 * h + 1][v] >> (8 * b));
+                x[2 * h] = bf16x2(f16_lo(u) * fac[2 * h], f16_lo(y) * fac[2 * h + 1]);
+                x[2 * h + 1] = bf16x2(f16_hi(u) * fac[2 * h], f16_hi(y) * fac[2 * h + 1]);
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_16816(o[nb][4 * v + b], x, pf[nb][0], pf[nb][1]);
+            }
+        }
+        for (; nan; nan &= nan - 1) {
+          const int t = tok0 + __ffs(nan) - 1;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (t <= pos[nb][e] && (t >= first[nb][e] || t < p.a.sinks)) {
+#pragma unroll
+                for (int j = 0; j < MT; ++j) o[nb][j][e] = o[nb][j][2 + e] = __uint_as_float(0x7FC00000u);
+              }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---------------- the warps' parts joined, in the order of their tokens ----------------
+    // sums are the same in all lanes of a column; kLift out of them and of the outputs
+    const float unlift = pow2i(-(int)kFewLift);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (g == 0) sums[warp][8 * nb + 2 * c + e] = make_float2(m[nb][e], ol[nb][e] * unlift);
+      }
+    const int piece = it.piece, pieces = it.pieces, hk = it.hk;
+    const long long b = it.b;
+    const bool more = load_q(n + 1);              // on their way while this item ends
+    stop = consumers_any<C::WARPS>(!more || *abort);
+    const float unit = E < 0 ? 1.f : pow2i(E - 127 - (int)kFewLift);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float top[2], tl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rho = 8 * nb + 2 * c + e;
+        top[e] = -INFINITY, tl[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) top[e] = fmaxf(top[e], sums[w][rho].x);
+        const float base = top[e] == -INFINITY ? 0.f : top[e];
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) tl[e] += ex2(sums[w][rho].x - base) * sums[w][rho].y;
+        const float f = ex2(m[nb][e] - base);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o[nb][j][e] = o[nb][j][e] * unit * f, o[nb][j][2 + e] = o[nb][j][2 + e] * unit * f;
+      }
+      // ((0 + 2) + (1 + 3)): the upper two warps hand theirs to the lower two, those one to the other
+#pragma unroll
+      for (int far = 2; far; far >>= 1) {
+        float4* mine = reinterpret_cast<float4*>(join) + (warp & (far - 1)) * MT * 32 + lane;
+        if (warp >= far && warp < 2 * far) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j) mine[j * 32] = make_float4(o[nb][j][0], o[nb][j][1], o[nb][j][2], o[nb][j][3]);
+        }
+        named_bar_sync(1, C::WARPS * 32);
+        if (warp < far) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            const float4 v = mine[j * 32];
+            o[nb][j][0] += v.x, o[nb][j][1] += v.y, o[nb][j][2] += v.z, o[nb][j][3] += v.w;
+          }
+        }
+        named_bar_sync(1, C::WARPS * 32);
+      }
+      if (warp == 0 && !*abort) {
+        const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rho = 8 * nb + 2 * c + e;
+          if (rho >= R) continue;
+          const bool one = pieces == 1;
+          const int r = rho / G;
+          const float inv = !one ? 1.f : tl[e] == 0.f ? no_weights(p, b, pos[nb][e]) : 1.f / tl[e];
+          uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
+#pragma unroll
+          for (int j = 0; j < MT; j += 2) {
+            // of products j and j + 1 four columns in a row
+            const int d = g * (D / 8) + 2 * j;
+            const float v[4] = {o[nb][j][e] * inv, o[nb][j][2 + e] * inv, o[nb][j + 1][e] * inv, o[nb][j + 1][2 + e] * inv};
+            if (one) *reinterpret_cast<uint2*>(out + d) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+            else *reinterpret_cast<float4*>(part_of(p, at, D, rho, d / 4)) = make_float4(v[0], v[1], v[2], v[3]);
+          }
+          if (!one && g == 0) *sums_of(p, at, rho) = make_float2(top[e], tl[e]);
+        }
+      }
+    }
+    if (lane == 0) mbar_arrive(&w_empty[n & 1]);
+  }
+}
+
 // At the end of every warp: who gave up, or saw that another one had, records it.
 __device__ __forceinline__ void record_end(const PagedArgs& p, volatile uint32_t* abort) {
   __syncwarp();
@@ -547,7 +1017,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
           break;
         if (lane == 0) {
           page_mask[s] = mask;
-          mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * (C::MX ? 1 : 2) + (C::MX ? 2 * D / 32 : 0)) +
+          mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * C::BITS / 8 + (C::MX ? 2 * D / 32 : 0)) +
                                               (issued == p.hold ? 16 : 0));
         }
         __syncwarp();
@@ -578,7 +1048,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   }
 
   // ---------------- consumers ----------------
-  if constexpr (C::EIGHT) {
+  if constexpr (C::FMT == MOE_KV_MXFP4) {
+    consume_four<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
+    record_end(p, &abort_flag);
+    return;
+  } else if constexpr (C::EIGHT) {
     consume_eight<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
     record_end(p, &abort_flag);
     return;
@@ -1020,7 +1494,9 @@ template <class C>
 static int launch_cfg(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
   CUtensorMap km, vm;
   const int box = std::min(cache->page_size, kTileTok);
-  const CUtensorMapSwizzle swizzle = C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle swizzle = C::ROWB == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                     : C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
   int rc = page_map(&km, cache->k, cache, box, swizzle);
   if (rc || (rc = page_map(&vm, cache->v, cache, box, swizzle))) return rc;
   auto kern = paged_attention_kernel<C>;
@@ -1031,8 +1507,11 @@ static int launch_cfg(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_
 
 template <int D, bool EIGHT>
 static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  return cache->format == MOE_KV_MXFP8 ? launch_cfg<PagedCfg<D, true, EIGHT>>(p, cache, st)
-                                       : launch_cfg<PagedCfg<D, false, EIGHT>>(p, cache, st);
+  switch (cache->format) {
+    case MOE_KV_MXFP8: return launch_cfg<PagedCfg<D, MOE_KV_MXFP8, EIGHT>>(p, cache, st);
+    case MOE_KV_MXFP4: return launch_cfg<PagedCfg<D, MOE_KV_MXFP4, EIGHT>>(p, cache, st);
+    default: return launch_cfg<PagedCfg<D, MOE_KV_BF16, EIGHT>>(p, cache, st);
+  }
 }
 
 static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {

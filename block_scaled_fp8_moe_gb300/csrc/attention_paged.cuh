@@ -1,4 +1,4 @@
-// What the two kernels of the paged attention share: their arguments, a sequence's pieces, and MXFP8 in bf16.
+// What the two kernels of the paged attention share: their arguments, a sequence's pieces, and MXFP8 and MXFP4 in 16 bits.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -160,14 +160,38 @@ __device__ __forceinline__ uint32_t scale_rest(uint32_t byte) {
   return byte == 255u ? 0x7FC0u : byte > kScaleFits ? (byte - kScaleFits + 127u) << 7 : 0x3F80u;
 }
 
+// ---- MXFP4 ----
+constexpr int format_bits(int format) { return format == MOE_KV_BF16 ? 16 : format == MOE_KV_MXFP8 ? 8 : 4; }
+
+// The codes of byte i of w as two f16, exactly; the low half's code in the low one.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w) {
+  uint32_t r;
+  if constexpr (I == 0) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (I == 1) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (I == 2) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
+  if constexpr (I == 3) asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// The same as bf16 times 2^-112: f16's exponent and fraction in bf16's places. And the largest scale byte whose factor,
+// 2^(112 + byte - 127), is a bf16.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1_bf16(uint32_t w) {
+  const uint32_t h = e2m1_pair<I>(w);
+  return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
+}
+constexpr uint32_t kScaleFits4 = 142;
+
 // Tensor map of the cache's rows [pages * Hkv * page_size, D], loaded `rows` at a time.
 inline int page_map(CUtensorMap* m, const void* base, const moe_kv_cache* c, int rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return MOE_ERR_CUDA;
-  const bool mx = c->format == MOE_KV_MXFP8;
-  const cuuint64_t dims[2] = {(cuuint64_t)c->D, (cuuint64_t)c->pages * c->Hkv * c->page_size};
-  const cuuint64_t stride[1] = {(cuuint64_t)c->D * (mx ? 1 : 2)};
-  const cuuint32_t box[2] = {(cuuint32_t)(mx ? c->D : 64), (cuuint32_t)rows};
+  const bool mx = c->format != MOE_KV_BF16;
+  const cuuint32_t wide = c->format == MOE_KV_MXFP4 ? c->D / 2 : c->D;       // elements of a row: values, or bytes of codes
+  const cuuint64_t dims[2] = {wide, (cuuint64_t)c->pages * c->Hkv * c->page_size};
+  const cuuint64_t stride[1] = {(cuuint64_t)wide * (mx ? 1 : 2)};
+  const cuuint32_t box[2] = {mx ? wide : 64, (cuuint32_t)rows};
   const cuuint32_t one[2] = {1, 1};
   const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                          const_cast<void*>(base), dims, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,

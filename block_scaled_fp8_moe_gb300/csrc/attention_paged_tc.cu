@@ -38,14 +38,15 @@ constexpr int kInfos = 16;              // steps whose tokens are remembered
 enum : int { kSeen, kHoles, kEdge };
 constexpr float kGrow = 8.f;            // the maximum that weights refer to moves when outgrown by 2^8
 
-template <int D_, bool MX_>
+template <int D_, int FMT_>
 struct TcCfg {
-  static constexpr int D = D_;
-  static constexpr bool MX = MX_;
+  static constexpr int D = D_, FMT = FMT_;
+  static constexpr bool MX = FMT_ != MOE_KV_BF16, FOUR = FMT_ == MOE_KV_MXFP4;
+  static constexpr int ROWB = D * format_bits(FMT_) / 8;           // bytes of a token's key, or value
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = kStepTok * D * 2;                    // a step's keys, or values, in bf16; the queries
-  static constexpr int RAW = MX ? (kStepTok * D + kStepTok * (D / 32) + 1023) / 1024 * 1024 : 0;
-  static constexpr int RAWS = !MX ? 1 : D == 128 ? 4 : 10;          // stages of raw codes
+  static constexpr int RAW = MX ? (kStepTok * ROWB + kStepTok * (D / 32) + 1023) / 1024 * 1024 : 0;
+  static constexpr int RAWS = !MX ? 1 : FOUR ? (D == 128 ? 8 : 14) : D == 128 ? 4 : 10;         // stages of raw codes
   static constexpr int ENTRIES = MX ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
   static constexpr int SMEM = TILE + ENTRIES * TILE + RAWS * RAW + 1024;
   static constexpr int THREADS = MX ? 640 : 384;
@@ -75,7 +76,7 @@ struct PagedItem {
 };
 
 // The columns of one row's part of an item that a listed key decides, by a warp, which takes one half of them.
-template <int D, bool MX>
+template <int D, int FMT>
 __device__ __noinline__ void finish_part(const PagedArgs& p, const BadKeys& bad, const PagedItem& it, int rho, int half) {
   constexpr int N = D / 32;
   const int lane = threadIdx.x % 32, G = p.G, r = rho / G;
@@ -87,7 +88,10 @@ __device__ __noinline__ void finish_part(const PagedArgs& p, const BadKeys& bad,
                     [&](int j, LaneRow<D>& k, LaneRow<D>& v) {
                       const int page = p.table[(long long)it.b * p.table_width + (j >> p.page_log2)];
                       const long long t = (((long long)page * p.a.Hkv + it.hk) << p.page_log2) + (j & (p.page_size - 1));
-                      if (MX) {
+                      if (FMT == MOE_KV_MXFP4) {
+                        k.load_mxfp4(p.k + t * (D / 2), p.k_s + t * N, lane);
+                        v.load_mxfp4(p.v + t * (D / 2), p.v_s + t * N, lane);
+                      } else if (FMT == MOE_KV_MXFP8) {
                         k.load_mxfp8(p.k + t * D, p.k_s + t * N, lane);
                         v.load_mxfp8(p.v + t * D, p.v_s + t * N, lane);
                       } else {
@@ -250,7 +254,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
               infos[(steps + i) % kInfos] =
                   make_int4(tok0, (int)mask, whole ? (mask == (1u << in_tile) - 1u ? kSeen : kHoles) : kEdge, 0);
             }
-            mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::MX ? D + D / 32 : 2 * D) + (tile == p.hold ? 16 : 0));
+            mbar_arrive_expect_tx(&landed[st], __popc(mask) * rows_of * (C::ROWB + (C::MX ? D / 32 : 0)) + (tile == p.hold ? 16 : 0));
           }
           __syncwarp();
           if (id >= 0) {
@@ -258,8 +262,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             const CUtensorMap* map = is_v ? &vmap : &kmap;
             if (C::MX) {
               uint8_t* dst = raws + st * C::RAW;
-              tma_load_2d(dst + lane * rows_of * D, map, 0, row, &landed[st]);
-              bulk_load(dst + kStepTok * D + lane * rows_of * (D / 32), (is_v ? p.v_s : p.k_s) + (long long)row * (D / 32),
+              tma_load_2d(dst + lane * rows_of * C::ROWB, map, 0, row, &landed[st]);
+              bulk_load(dst + kStepTok * C::ROWB + lane * rows_of * (D / 32), (is_v ? p.v_s : p.k_s) + (long long)row * (D / 32),
                         rows_of * (D / 32), &landed[st]);
             } else {
               uint8_t* dst = ring + st * C::TILE;
@@ -415,7 +419,52 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           const int4 info = infos[(steps + i) % kInfos];
           const bool edge = is_v && info.z == kEdge;
           uint8_t* dst = ring + e * C::TILE;
-          if (C::MX) {
+          if constexpr (C::FOUR) {
+            if (!(ok = ent_free(tile))) return;
+            // A thread takes one block of 32 codes of a row at a time, neighbouring lanes neighbouring rows: the lanes of a load
+            // and of a store are in different banks.
+            const uint8_t* src = raws + st * C::RAW;
+            const uint8_t* scales = src + kStepTok * C::ROWB;
+            constexpr int CH = D / 32, RPT = 128 / CH;
+            const int bl = tid / 32 % CH, row0 = tid / (32 * CH) * 32 + lane;
+#pragma unroll 1
+            for (int r = row0; r < kStepTok; r += RPT) {
+              uint32_t w[4], o[16];
+              const uint32_t at = D == 128 ? r * 64 + ((bl ^ ((r >> 1) & 3)) << 4) : r * 32 + ((bl ^ ((r >> 2) & 1)) << 4);
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(smem_u32(src) + at));
+              const uint32_t by = scales[r * (D / 32) + bl];
+              const uint32_t f = ((min(by, kScaleFits4) + 112u) << 7) * 0x10001u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[4 * i] = mul_bf16x2(e2m1_bf16<0>(w[i]), f), o[4 * i + 1] = mul_bf16x2(e2m1_bf16<1>(w[i]), f);
+                o[4 * i + 2] = mul_bf16x2(e2m1_bf16<2>(w[i]), f), o[4 * i + 3] = mul_bf16x2(e2m1_bf16<3>(w[i]), f);
+              }
+              // Scales past what one factor holds, and NaN, take a second one; what a page that was not loaded left becomes zero.
+              if (by > kScaleFits4) {
+                const bool there = (info.y >> (r >> min(p.page_log2, 7))) & 1;
+                const uint32_t f2 = (by == 255u ? 0x7FC0u : (by - kScaleFits4 + 127u) << 7) * 0x10001u;
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  o[i] = mul_bf16x2(o[i], f2);
+                  const uint32_t hit = ((o[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  bad = bad || hit;
+                  if (edge) o[i] &= ~((hit >> 15) * 0xFFFFu);
+                  if (!there) o[i] = 0;
+                }
+                if (bad && edge && there) list(info.x + r);
+              }
+              const uint32_t to = smem_u32(dst) + (bl >> 1) * kStepTok * 128 + r * 128;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((((bl & 1) * 4 + k) ^ (r & 7)) << 4)),
+                             "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3]) : "memory");
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[st]);
+          } else if constexpr (C::MX) {
             if (!(ok = ent_free(tile))) return;
             const uint8_t* src = raws + st * C::RAW;
             constexpr int CH = D / 16, RPT = 128 / CH;          // 16 codes at a time; rows of the tile a pass covers
@@ -751,7 +800,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           again = again && live && tl == tl;    // a score that is NaN makes the sum NaN, and with it the row
           __syncwarp();                         // what a lane has written another one adds to
           for (unsigned rows = __ballot_sync(0xffffffffu, again); rows; rows &= rows - 1)
-            finish_part<D, C::MX>(p, bad[n & 1], it, rho - lane + __ffs(rows) - 1, x);
+            finish_part<D, C::FMT>(p, bad[n & 1], it, rho - lane + __ffs(rows) - 1, x);
         }
       }
       ok = wait(&outs_read, n & 1, DEV_TIMEOUT_ACCUM) && ok;
@@ -767,12 +816,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
   if (threadIdx.x == 0 && abort_flag) atomicCAS(p.status, 0u, abort_flag);
 }
 
-template <int D, bool MX>
+template <int D, int FMT>
 static int launch_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  using C = TcCfg<D, MX>;
+  using C = TcCfg<D, FMT>;
   CUtensorMap km, vm;
   const int box = std::min(cache->page_size, kStepTok);
-  const CUtensorMapSwizzle swizzle = MX ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle swizzle = FMT == MOE_KV_MXFP8   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                     : FMT == MOE_KV_BF16 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : D == 128           ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                          : CU_TENSOR_MAP_SWIZZLE_32B;
   int rc = page_map(&km, cache->k, cache, box, swizzle);
   if (rc || (rc = page_map(&vm, cache->v, cache, box, swizzle))) return rc;
   auto kern = paged_tc_kernel<C>;
@@ -782,9 +834,12 @@ static int launch_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t
 }
 
 int launch_paged_tc(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
-  const bool mx = cache->format == MOE_KV_MXFP8;
-  if (p.a.D == 64) return mx ? launch_tc<64, true>(p, cache, st) : launch_tc<64, false>(p, cache, st);
-  return mx ? launch_tc<128, true>(p, cache, st) : launch_tc<128, false>(p, cache, st);
+  const bool d64 = p.a.D == 64;
+  switch (cache->format) {
+    case MOE_KV_MXFP8: return d64 ? launch_tc<64, MOE_KV_MXFP8>(p, cache, st) : launch_tc<128, MOE_KV_MXFP8>(p, cache, st);
+    case MOE_KV_MXFP4: return d64 ? launch_tc<64, MOE_KV_MXFP4>(p, cache, st) : launch_tc<128, MOE_KV_MXFP4>(p, cache, st);
+    default: return d64 ? launch_tc<64, MOE_KV_BF16>(p, cache, st) : launch_tc<128, MOE_KV_BF16>(p, cache, st);
+  }
 }
 
 }  // namespace moe

@@ -1,4 +1,4 @@
-// New tokens' keys and values into the paged cache, copied (bf16) or quantised (MXFP8).
+// New tokens' keys and values into the paged cache, copied (bf16) or quantised (MXFP8, MXFP4).
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
@@ -13,14 +13,15 @@ constexpr int kAppendUnroll = 2;
 
 // A thread has 8 values (16 bytes) of `kAppendUnroll` tokens at a time, all loaded before any is written; 4 neighbouring lanes
 // have one block of 32. `group` threads (a power of two, up to a block) share a token, its keys first, then its values.
-// Bound: HBM, 4 bytes a value in bf16 and 3.03 in MXFP8. Two tokens at a time: with four, 48 tokens took 2.5 us in MXFP8
+// Bound: HBM, 4 bytes a value in bf16, 3.03 in MXFP8 and 2.53 in MXFP4. Two tokens at a time: with four, 48 tokens took 2.5 us in MXFP8
 // instead of 1.6, with one, 20011 tokens 31.6 us instead of 28.
-template <bool MX>
+template <int FMT>
 __global__ void __launch_bounds__(kAppendThreads, 8)
 kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, long long k_stride,
                  const uint16_t* __restrict__ v, long long v_stride, const int32_t* __restrict__ slots, int group_log2,
                  int page_log2, uint32_t* status) {
   constexpr int U = kAppendUnroll;
+  constexpr bool MX4 = FMT == MOE_KV_MXFP4;
   pdl_trigger();
   pdl_wait();
   const int head_log2 = c.D == 128 ? 4 : 3, per_tok = c.Hkv << head_log2;     // 16-byte parts of a head, of a token's keys
@@ -49,7 +50,7 @@ kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, lo
       if (!in && slot[u] != -1 && e == 0) atomicCAS(status, 0u, (uint32_t)DEV_BAD_INPUT);
       const long long page = in ? slot[u] >> page_log2 : 0;
       const long long row = ((page * c.Hkv + h) << page_log2) + (in ? slot[u] & (c.page_size - 1) : 0);
-      if (!MX) {
+      if (FMT == MOE_KV_BF16) {
         if (in) reinterpret_cast<uint4*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = a[u];
       } else {
         // the largest magnitude by its bits: what is not finite lies above all else
@@ -60,7 +61,7 @@ kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, lo
         m2 = __vmaxu2(m2, __shfl_xor_sync(four, m2, 2));
         const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
         const bool finite = m < 0x7F80u;
-        const int se = e4m3_scale_exp_bf16(m);
+        const int se = MX4 ? e2m1_scale_exp(__uint_as_float(m << 16)) : e4m3_scale_exp_bf16(m);
         const float sc = pow2_neg(se);
         float f[8];
 #pragma unroll
@@ -70,11 +71,18 @@ kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, lo
         sb |= __shfl_down_sync(0xffffffffu, sb, 4) << 8;
         sb |= __shfl_down_sync(0xffffffffu, sb, 8) << 16;
         if (in) {
-          uint2 codes = make_uint2(0, 0);
-          if (finite)
-            codes = make_uint2(e4m3x2(f[0] * sc, f[1] * sc) | (e4m3x2(f[2] * sc, f[3] * sc) << 16),
-                               e4m3x2(f[4] * sc, f[5] * sc) | (e4m3x2(f[6] * sc, f[7] * sc) << 16));
-          reinterpret_cast<uint2*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = codes;
+          if constexpr (MX4) {
+            uint32_t codes = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) codes |= e2m1x2(f[2 * j] * sc, f[2 * j + 1] * sc) << (8 * j);
+            reinterpret_cast<uint32_t*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = finite ? codes : 0u;
+          } else {
+            uint2 codes = make_uint2(0, 0);
+            if (finite)
+              codes = make_uint2(e4m3x2(f[0] * sc, f[1] * sc) | (e4m3x2(f[2] * sc, f[3] * sc) << 16),
+                                 e4m3x2(f[4] * sc, f[5] * sc) | (e4m3x2(f[6] * sc, f[7] * sc) << 16));
+            reinterpret_cast<uint2*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = codes;
+          }
           uint8_t* scales = (is_v ? c.v_s : c.k_s) + (row << (head_log2 - 2));
           if (d8 == 0) {
             if (head_log2 == 4) *reinterpret_cast<uint32_t*>(scales) = sb;
@@ -107,7 +115,9 @@ extern "C" int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_
   while ((1 << group_log2) < 2 * row / 8 && (1 << group_log2) < kAppendThreads) ++group_log2;
   while ((1 << page_log2) < cache->page_size) ++page_log2;
   const int per_block = (kAppendThreads >> group_log2) * kAppendUnroll;
-  auto kern = cache->format == MOE_KV_MXFP8 ? kv_append_kernel<true> : kv_append_kernel<false>;
+  auto kern = cache->format == MOE_KV_MXFP8   ? kv_append_kernel<MOE_KV_MXFP8>
+              : cache->format == MOE_KV_MXFP4 ? kv_append_kernel<MOE_KV_MXFP4>
+                                              : kv_append_kernel<MOE_KV_BF16>;
   return launch_pdl(kern, dim3((unsigned)((T + (long long)per_block - 1) / per_block)), dim3(kAppendThreads), 0,
                     static_cast<cudaStream_t>(stream), *cache, (int)T, k, (long long)k_stride, v, (long long)v_stride, slots,
                     group_log2, page_log2, static_cast<uint32_t*>(ws));

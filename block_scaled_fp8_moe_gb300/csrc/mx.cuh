@@ -38,6 +38,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two E2M1 codes (round to nearest even, as e2m1_code below), `lo` in the low half of the byte.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // E2M1 round-to-nearest-even of v (|v| <= 6 under the scale rule), from the value grid
 // {0, .5, 1, 1.5, 2, 3, 4, 6}: each comparison counts one grid step passed; at an exact midpoint
 // the step is taken only when it lands on the even code.

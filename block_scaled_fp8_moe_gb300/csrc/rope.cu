@@ -1,0 +1,331 @@
+// Rotary positions: heads of queries and keys turned by their tokens' positions, alone (moe_rope) or on the way into the paged
+// cache (moe_rope_kv_append).
+//
+// Pair i of a head, (a, b), goes to (a cos t - b sin t, a sin t + b cos t) with t = position * w_i. An angle is needed modulo
+// one turn only, so w_i is held as the 64-bit integer 2^64 w_i / 2 pi: its product with the position, modulo 2^64, is the
+// fraction of the turn, off by less than 2^-33 of one for any 32-bit position (fp32 angles would be off by 0.06 rad at a
+// million).
+//
+// Bound: HBM, 4 bytes a value turned; what is stored adds 2, 1.03 or 0.53 a value and 2 read. A warp takes a part of one token:
+// it works out the token's cosines and sines once, a lane a pair, leaves them in shared memory, and every lane then has those of
+// its own 8 (4) neighbouring values for all heads, whose partners come from another lane of the same head. So a head is read
+// before any of it is written, and rows may be turned where they are.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "attention.cuh"
+#include "common.cuh"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kRopeWarps = 8;
+constexpr int kRopeMaxD = 256;
+constexpr int kNoCache = -1;
+
+struct RopeArgs {
+  int half, axes;                       // pairs; positions of a token
+  int back;                             // the other way round
+  float factor;
+  const uint64_t* turns;
+  const uint8_t* axis;
+  int T, D, lane_log2;                  // lanes of a head
+  int Hq, Hk, Hv;                       // heads turned into q_out, into k_out and the cache, stored as they are
+  int groups, per, parts;               // heads of a token in groups of a warp's width; groups of a warp; warps of a token
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* pos;
+  long long pos_stride;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  long long qo_stride, ko_stride;
+  moe_kv_cache c;
+  int page_log2;
+  const int32_t* slots;
+  uint32_t* status;
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint16_t* p) {
+  if constexpr (N == 4) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    w[0] = a.x, w[1] = a.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N]) {
+  if constexpr (N == 4) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (N == 2) *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else *static_cast<uint32_t*>(p) = w[0];
+}
+
+// A lane's VEC values of a row in the cache's MX format; all lanes of the warp call this. `mine`: this lane's are stored.
+template <int VEC, int FMT>
+__device__ __forceinline__ void store_mx(const float (&f)[VEC], bool mine, uint8_t* codes, uint8_t* scales, long long row,
+                                         int D, int ch) {
+  constexpr int BL = 32 / VEC;          // lanes of a block
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);    // what is not finite lies above all else
+#pragma unroll
+  for (int d = 1; d < BL; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool finite = m < 0x7F800000u;
+  const int se = FMT == MOE_KV_MXFP8 ? e4m3_scale_exp(__uint_as_float(m)) : e2m1_scale_exp(__uint_as_float(m));
+  const float sc = pow2_neg(se);
+  // a row's scale bytes in one word, in its first lane
+  const uint32_t b = finite ? (uint32_t)(se + 127) : 255u;
+  uint32_t all = b;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    const uint32_t other = __shfl_down_sync(0xffffffffu, b, i * BL);
+    if (i < D / 32) all |= other << (8 * i);
+  }
+  if (!mine) return;
+  if constexpr (FMT == MOE_KV_MXFP8) {
+    uint32_t w[VEC / 4];
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      w[i] = finite ? e4m3x2(f[4 * i] * sc, f[4 * i + 1] * sc) | e4m3x2(f[4 * i + 2] * sc, f[4 * i + 3] * sc) << 16 : 0u;
+    store_words(codes + row * D + ch * VEC, w);
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) w |= e2m1x2(f[2 * i] * sc, f[2 * i + 1] * sc) << (8 * i);
+    if (!finite) w = 0;
+    uint8_t* to = codes + row * (D / 2) + ch * (VEC / 2);
+    if constexpr (VEC == 8) *reinterpret_cast<uint32_t*>(to) = w;
+    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
+  }
+  if (ch == 0) {
+    if (D == 128) *reinterpret_cast<uint32_t*>(scales + row * 4) = all;
+    else *reinterpret_cast<uint16_t*>(scales + row * 2) = (uint16_t)all;
+  }
+}
+
+// PAIRS: neighbours (2i, 2i + 1), in one lane; else (i, i + half), `half / VEC` lanes apart.
+template <int VEC, bool PAIRS, int FMT>
+__global__ void __launch_bounds__(kRopeWarps * 32)
+rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int U = 4;                  // groups under way
+  __shared__ float2 turn[kRopeWarps][kRopeMaxD / 2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long wid = (long long)blockIdx.x * kRopeWarps + warp;
+  const int t = (int)(wid / a.parts), part = (int)(wid - (long long)t * a.parts);
+  pdl_trigger();
+  pdl_wait();
+  if (t >= a.T) return;
+  const int ch = lane & ((1 << a.lane_log2) - 1), d0 = ch * VEC, rot = 2 * a.half;
+  const int in_warp = lane >> a.lane_log2, heads = 32 >> a.lane_log2, units = a.Hq + a.Hk + a.Hv;
+  const int end = min(a.groups, (part + 1) * a.per);
+
+  uint32_t w[U][VEC / 2];
+  auto fetch = [&](int g0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int u = (g0 + j) * heads + in_warp;
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) w[j][e] = 0;
+      if (g0 + j < end && u < units && d0 < a.D) {
+        const uint16_t* row = u < a.Hq ? a.q + t * a.q_stride + u * a.D
+                            : u < a.Hq + a.Hk ? a.k + t * a.k_stride + (u - a.Hq) * a.D
+                                              : a.v + t * a.v_stride + (u - a.Hq - a.Hk) * a.D;
+        load_words(w[j], row + d0);
+      }
+    }
+  };
+  fetch(part * a.per);
+
+  for (int i = lane; i < a.half; i += 32) {
+    const int x = a.axis ? min((int)a.axis[i], a.axes - 1) : 0;
+    uint64_t n = (uint64_t)(long long)a.pos[x * a.pos_stride + t] * a.turns[i];
+    if (a.back) n = 0 - n;
+    float s, c;
+    sincospif((float)(int32_t)((n + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);    // the fraction in half turns, from -1 to 1
+    turn[warp][i] = make_float2(c * a.factor, s * a.factor);
+  }
+  int slot = -1;
+  long long row0 = 0;                   // the token's place in head 0 of its page
+  bool stored = false;
+  if constexpr (FMT != kNoCache) {
+    slot = a.slots[t];
+    stored = slot >= 0 && slot < (long long)a.c.pages << a.page_log2;
+    if (!stored && slot != -1 && lane == 0) atomicCAS(a.status, 0u, (uint32_t)DEV_BAD_INPUT);
+    if (stored) row0 = (((long long)(slot >> a.page_log2) * a.c.Hkv) << a.page_log2) + (slot & (a.c.page_size - 1));
+  }
+  __syncwarp();
+
+  const bool turned = d0 < rot, second = d0 >= a.half;
+  float c[VEC], s[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const int i = PAIRS ? d0 / 2 + e / 2 : second ? d0 - a.half + e : d0 + e;
+    const float2 cs = turned ? turn[warp][i] : make_float2(1.f, 0.f);
+    c[e] = cs.x;
+    s[e] = (PAIRS ? (e & 1) == 0 : !second) ? -cs.y : cs.y;
+  }
+  const int far = turned && !PAIRS ? (second ? lane - a.half / VEC : lane + a.half / VEC) : lane;
+
+  for (int g0 = part * a.per; g0 < end; g0 += U) {
+    if (g0 != part * a.per) fetch(g0);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (g0 + j >= end) break;
+      const int u = (g0 + j) * heads + in_warp;
+      const bool is_q = u < a.Hq, is_k = !is_q && u < a.Hq + a.Hk, is_v = !is_q && !is_k && u < units;
+      const bool turns = turned && !is_v;
+      uint32_t other[VEC / 2], o[VEC / 2];
+      float f[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) {
+        other[e] = PAIRS ? (w[j][e] >> 16) | (w[j][e] << 16) : __shfl_sync(0xffffffffu, w[j][e], far);
+        f[2 * e] = bf16_lo(w[j][e]);
+        f[2 * e + 1] = bf16_hi(w[j][e]);
+        if (turns) {
+          f[2 * e] = f[2 * e] * c[2 * e] + bf16_lo(other[e]) * s[2 * e];
+          f[2 * e + 1] = f[2 * e + 1] * c[2 * e + 1] + bf16_hi(other[e]) * s[2 * e + 1];
+        }
+        o[e] = turns ? bf16x2(f[2 * e], f[2 * e + 1]) : w[j][e];        // copies keep their bits
+      }
+      if (d0 < a.D) {
+        if (is_q) store_words(a.q_out + t * a.qo_stride + u * a.D + d0, o);
+        if (is_k && a.k_out) store_words(a.k_out + t * a.ko_stride + (u - a.Hq) * a.D + d0, o);
+      }
+      if constexpr (FMT != kNoCache) {
+        const bool in = stored && (is_k || is_v);
+        const int h = is_v ? u - a.Hq - a.Hk : u - a.Hq;
+        const long long row = row0 + ((long long)h << a.page_log2);
+        if constexpr (FMT == MOE_KV_BF16) {
+          if (in) store_words(static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + row * a.D + d0, o);
+        } else {
+          if (__any_sync(0xffffffffu, in))
+            store_mx<VEC, FMT>(f, in, static_cast<uint8_t*>(is_v ? a.c.v : a.c.k), is_v ? a.c.v_s : a.c.k_s, row, a.D, ch);
+        }
+      }
+    }
+  }
+}
+
+// The rotary description and the rows, checked and laid out; what has to do with the cache is the caller's.
+static int rope_args(RopeArgs& p, const moe_rotary* r, int T, int Hq, int Hk, int Hv, int D, const uint16_t* q,
+                     int64_t q_stride, const uint16_t* k, int64_t k_stride, const int32_t* pos, int64_t pos_stride,
+                     uint16_t* q_out, int64_t qo_stride, uint16_t* k_out, int64_t ko_stride) {
+  if (!r->turns || !pos || (reinterpret_cast<uintptr_t>(r->turns) & 7) || (reinterpret_cast<uintptr_t>(pos) & 3) ||
+      pos_stride < T)
+    return MOE_ERR_INVALID_ARG;
+  auto rows_ok = [&](const uint16_t* x, int64_t stride, int heads) {
+    return x && !(reinterpret_cast<uintptr_t>(x) & 15) && stride % 8 == 0 && stride >= (int64_t)heads * D;
+  };
+  if (Hq && (!rows_ok(q, q_stride, Hq) || !rows_ok(q_out, qo_stride, Hq))) return MOE_ERR_INVALID_ARG;
+  if (Hk && (!rows_ok(k, k_stride, Hk) || (k_out && !rows_ok(k_out, ko_stride, Hk)))) return MOE_ERR_INVALID_ARG;
+  p.half = r->dim / 2;
+  p.axes = r->axes;
+  p.back = r->inverse != 0;
+  p.factor = r->factor;
+  p.turns = r->turns;
+  p.axis = r->axis;
+  p.T = T, p.D = D, p.Hq = Hq, p.Hk = Hk, p.Hv = Hv;
+  p.q = q, p.k = k, p.q_stride = q_stride, p.k_stride = k_stride;
+  p.pos = pos, p.pos_stride = pos_stride;
+  p.q_out = q_out, p.k_out = k_out, p.qo_stride = qo_stride, p.ko_stride = ko_stride;
+  return MOE_OK;
+}
+
+static bool rotary_ok(const moe_rotary* r, int D) {
+  return r->dim >= 8 && r->dim <= D && r->dim % 8 == 0 && r->axes >= 1 && r->axes <= 4 && std::isfinite(r->factor) &&
+         D % 8 == 0 && D <= kRopeMaxD;
+}
+
+// Lanes take 8 values, or 4 where the second half of a turned head would begin inside 8: half the bytes a load, for which the
+// head has to fit 32 lanes.
+static int rope_vec(const moe_rotary* r) { return !r->interleaved && r->dim % 16 ? 4 : 8; }
+
+template <int VEC, bool PAIRS>
+static void (*rope_kernel_of(int format))(RopeArgs) {
+  switch (format) {
+    case MOE_KV_BF16: return rope_kernel<VEC, PAIRS, MOE_KV_BF16>;
+    case MOE_KV_MXFP8: return rope_kernel<VEC, PAIRS, MOE_KV_MXFP8>;
+    case MOE_KV_MXFP4: return rope_kernel<VEC, PAIRS, MOE_KV_MXFP4>;
+    default: return rope_kernel<VEC, PAIRS, kNoCache>;
+  }
+}
+
+static int launch_rope(RopeArgs& p, bool pairs, int vec, int format, cudaStream_t st) {
+  while ((vec << p.lane_log2) < p.D) ++p.lane_log2;
+  p.groups = ceil_div(p.Hq + p.Hk + p.Hv, 32 >> p.lane_log2);
+  // As many groups a warp as leave every multiprocessor 32 warps, at least 2: few tokens are a matter of latency, many of not
+  // working out their cosines again.
+  const long long all = (long long)p.T * p.groups, slots = (long long)num_sms() * 32;
+  p.per = all >= 8 * slots ? 8 : all >= 4 * slots ? 4 : 2;
+  p.parts = ceil_div(p.groups, p.per);
+  const long long warps = (long long)p.T * p.parts, blocks = (warps + kRopeWarps - 1) / kRopeWarps;
+  if (blocks >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  auto kern = vec == 4 ? rope_kernel_of<4, false>(format)
+              : pairs  ? rope_kernel_of<8, true>(format)
+                       : rope_kernel_of<8, false>(format);
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(kRopeWarps * 32), 0, st, p);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_rotary_turns(int32_t n, const double* inv_freq, uint64_t* turns) {
+  if (n < 0 || (n && (!inv_freq || !turns))) return MOE_ERR_INVALID_ARG;
+  // 1 / 2 pi in two doubles: the product's first part is exact with its remainder
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int i = 0; i < n; ++i)
+    if (!(std::fabs(inv_freq[i]) <= 1e6)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    const double w = std::fabs(inv_freq[i]), t = w * hi, rest = std::fma(w, hi, -t) + w * lo;
+    // t - floor(t) is exact and below one; in 64 bits whole but for what lies below 2^-64
+    const double f = std::ldexp(t - std::floor(t), 64), whole = std::floor(f);
+    const uint64_t n = static_cast<uint64_t>(whole) + static_cast<uint64_t>(std::llrint(f - whole + std::ldexp(rest, 64)));
+    turns[i] = inv_freq[i] < 0 ? 0 - n : n;
+  }
+  return MOE_OK;
+}
+
+extern "C" int moe_rope(const moe_rotary* r, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, const uint16_t* q,
+                        int64_t q_stride, const uint16_t* k, int64_t k_stride, const int32_t* pos, int64_t pos_stride,
+                        uint16_t* q_out, int64_t qo_stride, uint16_t* k_out, int64_t ko_stride, void* stream) {
+  if (!r || T < 0 || Hq < 0 || Hkv < 0 || D <= 0) return MOE_ERR_INVALID_ARG;
+  const int vec = rope_vec(r);
+  if (!rotary_ok(r, D) || D > 32 * vec || Hq > 65535 || Hkv > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || (Hq == 0 && Hkv == 0)) return MOE_OK;
+  if (Hkv && !k_out) return MOE_ERR_INVALID_ARG;
+  RopeArgs p{};
+  const int rc = rope_args(p, r, T, Hq, Hkv, 0, D, q, q_stride, k, k_stride, pos, pos_stride, q_out, qo_stride, k_out, ko_stride);
+  return rc ? rc : launch_rope(p, r->interleaved != 0, vec, kNoCache, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_rope_kv_append(const moe_rotary* r, const moe_kv_cache* cache, int32_t T, int32_t Hq,
+                                  const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                  const uint16_t* v, int64_t v_stride, const int32_t* pos, int64_t pos_stride,
+                                  const int32_t* slots, uint16_t* q_out, int64_t qo_stride, uint16_t* k_out,
+                                  int64_t ko_stride, void* ws, size_t ws_bytes, void* stream) {
+  if (!r || !cache || T < 0 || Hq < 0) return MOE_ERR_INVALID_ARG;
+  if (!kv_cache_ok(cache) || !rotary_ok(r, cache->D) || Hq > 65535 || cache->Hkv > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!status_ws_ok(ws, ws_bytes)) return MOE_ERR_WORKSPACE;
+  if (T == 0) return MOE_OK;
+  const int64_t row = (int64_t)cache->Hkv * cache->D;
+  if (!v || (reinterpret_cast<uintptr_t>(v) & 15) || v_stride % 8 || v_stride < row || !slots ||
+      (reinterpret_cast<uintptr_t>(slots) & 3) || !kv_cache_pointers_ok(cache))
+    return MOE_ERR_INVALID_ARG;
+  RopeArgs p{};
+  const int rc = rope_args(p, r, T, Hq, cache->Hkv, cache->Hkv, cache->D, q, q_stride, k, k_stride, pos, pos_stride,
+                           q_out, qo_stride, k_out, ko_stride);
+  if (rc) return rc;
+  p.v = v, p.v_stride = v_stride;
+  p.c = *cache;
+  while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
+  p.slots = slots;
+  p.status = static_cast<uint32_t*>(ws);
+  return launch_rope(p, r->interleaved != 0, rope_vec(r), cache->format, static_cast<cudaStream_t>(stream));
+}

@@ -370,10 +370,14 @@ MOE_API int moe_add_rmsnorm_mxfp8(int32_t rows, int32_t cols, const uint16_t* x,
  *                 of moe_quant_mxfp8 per 32 values of a row. A block with a value that is not finite is
  *                 stored with scale byte 255 (NaN) and reads back as NaN; the codes of the format's own
  *                 NaN (0x7F, 0xFF) are never written and must not be in the cache.
+ *   MOE_KV_MXFP4  k, v u8 [pages, Hkv, page_size, D/2] E2M1 codes, element 2m in the LOW nibble, k_s, v_s
+ *                 as for MXFP8, the rule of moe_quant_mxfp4 per 32 values of a row. A block with a value
+ *                 that is not finite has scale byte 255 and reads back as NaN.
  * D is 64 or 128, page_size a power of two from 8 to 256, pages * Hkv * page_size < 2^31. k, v, k_s,
  * v_s 128-byte aligned. */
 #define MOE_KV_BF16 0
 #define MOE_KV_MXFP8 1
+#define MOE_KV_MXFP4 4
 typedef struct moe_kv_cache {
   int32_t pages, page_size, Hkv, D;
   int32_t format; /* MOE_KV_* */
@@ -393,6 +397,49 @@ typedef struct moe_kv_cache {
 MOE_API int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_t* k, int64_t k_stride,
                           const uint16_t* v, int64_t v_stride, const int32_t* slots, void* ws, size_t ws_bytes,
                           void* stream);
+
+/* Rotary positions. Pair i of a head, (a, b), with frequency w_i and axis x_i becomes, for a token whose position
+ * along that axis is p,
+ *   factor * (a cos(p w_i) - b sin(p w_i)),  factor * (a sin(p w_i) + b cos(p w_i))
+ * (inverse: the angle's sign turned, which is also the gradient: of a row that was turned, from the gradient
+ * of the result). Of a head's D values the first `dim` are turned, in pairs (i, i + dim/2) or, interleaved,
+ * (2i, 2i + 1); the others are copied. Angles are exact to 2^-32 of a turn at every int32 position, below zero
+ * too; the arithmetic is fp32, with one rounding at the end. */
+typedef struct moe_rotary {
+  int32_t dim;           /* turned values of a head, a multiple of 8              */
+  int32_t axes;          /* positions of a token (time, height, width): 1 to 4    */
+  int32_t interleaved;   /* pairs are neighbours                                  */
+  int32_t inverse;       /* turn back                                             */
+  float factor;          /* finite; on cosines and sines, 1 if there is none      */
+  const uint64_t* turns; /* [dim/2] on the device, from moe_rotary_turns          */
+  const uint8_t* axis;   /* [dim/2] on the device, every pair's axis; NULL: axis 0 for all. Values past the last
+                            axis count as the last one */
+} moe_rotary;
+
+/* The frequencies in the form that the kernels take, 2^64 w / 2 pi modulo 2^64. Both arrays in HOST memory, n
+ * entries; |w| <= 10^6. Done once per model; the caller copies the result to the device. */
+MOE_API int moe_rotary_turns(int32_t n, const double* inv_freq, uint64_t* turns);
+
+/* Turns T tokens' queries and keys, bf16: token t's heads at q + t * q_stride ([Hq, D] contiguous there), k + t *
+ * k_stride ([Hkv, D]), to q_out and k_out, spaced by strides of their own. q_out may be q with the same stride,
+ * and k_out k (turned where they are); otherwise they do not overlap what is read. Hq or Hkv may be 0
+ * (its pointers are not looked at). pos i32: the position along axis x at pos[x * pos_stride + t], pos_stride >= T.
+ * D a multiple of 8, at most 256 (128 where dim is not a multiple of 16 and pairs are not neighbours). Pointers
+ * 16-byte aligned, strides multiples of 8 elements. T = 0 is a no-op. */
+MOE_API int moe_rope(const moe_rotary* r, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, const uint16_t* q,
+                     int64_t q_stride, const uint16_t* k, int64_t k_stride, const int32_t* pos, int64_t pos_stride,
+                     uint16_t* q_out, int64_t qo_stride, uint16_t* k_out, int64_t ko_stride, void* stream);
+
+/* moe_kv_append with the turn on the way: queries turned into q_out, keys turned into the cache, values stored as
+ * they are. Cache, slots and ws as for moe_kv_append; rows and positions as for moe_rope. A key is rounded once, from
+ * fp32 to the cache's format (in a bf16 cache it is what moe_rope gives). Tokens that are not stored are
+ * turned into q_out all the same. k_out (may be NULL): the turned keys in bf16 too, for a prompt's own
+ * attention. */
+MOE_API int moe_rope_kv_append(const moe_rotary* r, const moe_kv_cache* cache, int32_t T, int32_t Hq,
+                               const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, const int32_t* pos, int64_t pos_stride,
+                               const int32_t* slots, uint16_t* q_out, int64_t qo_stride, uint16_t* k_out,
+                               int64_t ko_stride, void* ws, size_t ws_bytes, void* stream);
 
 /* Attention: out = softmax(scale * q k^T) v over the keys that a row sees, in fp32, one rounding to bf16
  * at the end (the softmax weights are rounded to bf16 for the tensor cores' second product). Query

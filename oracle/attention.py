@@ -74,3 +74,31 @@ def quant_block_mxfp8(x):
     q, s = M.quant_mxfp8(safe)
     s = np.where(fine, s, 255).astype(np.uint8)
     return q.reshape(x.shape), s.reshape(*x.shape[:-1], -1)
+
+
+def quant_block_mxfp4(x):
+    """The cache's MXFP4 rule for rows [..., D]: (codes two to a byte [..., D/2], scales) as uint8; a block with a value that
+    is not finite has codes of zero and scale byte 255."""
+    from . import moe as M
+    x = np.asarray(x, dtype=np.float32)
+    rows = x.reshape(-1, x.shape[-1])
+    fine = np.isfinite(rows.reshape(rows.shape[0], -1, F.BLOCK)).all(-1)
+    q, s = M.quant_mxfp4(np.where(np.repeat(fine, F.BLOCK, axis=1), rows, 0))
+    s = np.where(fine, s, 255).astype(np.uint8)
+    return q.reshape(*x.shape[:-1], -1), s.reshape(*x.shape[:-1], -1)
+
+
+def rope(x, pos, inv_freq, axis=None, interleaved=False, factor=1.0, inverse=False):
+    """Rows x [T, heads, D] turned by their positions pos [axes, T], pair by pair. Returns (out, mag): the result, and
+    |a| + |b| of the pair times the factor, which bounds the rounding of its two products."""
+    x = np.asarray(x, dtype=np.float64)
+    out, mag = x.copy(), np.zeros_like(x)
+    half = len(inv_freq)
+    for i, w in enumerate(np.asarray(inv_freq, dtype=np.float64)):
+        t = np.asarray(pos[axis[i] if axis is not None else 0], dtype=np.float64) * w * (-1 if inverse else 1)
+        i0, i1 = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        a, b = x[..., i0], x[..., i1]
+        c, s = factor * np.cos(t)[:, None], factor * np.sin(t)[:, None]
+        out[..., i0], out[..., i1] = a * c - b * s, a * s + b * c
+        mag[..., i0] = mag[..., i1] = abs(factor) * (np.abs(a) + np.abs(b))
+    return out, mag
