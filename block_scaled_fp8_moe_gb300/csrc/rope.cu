@@ -6,12 +6,12 @@
 // fraction of the turn, off by less than 2^-33 of one for any 32-bit position (fp32 angles would be off by 0.06 rad at a
 // million).
 //
-// Bound: HBM, 4 bytes a value turned; what is stored adds 2, 1.03 or 0.53 a value and 2 read. A warp takes a part of one token:
-// it works out the token's cosines and sines once, a lane a pair, leaves them in shared memory, and every lane then has those of
-// its own 8 (4) neighbouring values for all heads, whose partners come from another lane of the same head. So a head is read
-// before any of it is written, and rows may be turned where they are.
+// Bound: HBM, 4 bytes a value turned; what is stored adds 2, 1.03 or 0.53 a value and 2 read. Cosines and sines are worked out
+// once for all heads of a token, left in shared memory, and held by every thread for its own places in a head. All of a head that
+// a warp writes it has read before, so rows may be turned where they are.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "attention.cuh"
@@ -31,9 +31,11 @@ struct RopeArgs {
   float factor;
   const uint64_t* turns;
   const uint8_t* axis;
-  int T, D, lane_log2;                  // lanes of a head
+  int T, D, lanes;                      // lanes of a head
   int Hq, Hk, Hv;                       // heads turned into q_out, into k_out and the cache, stored as they are
-  int groups, per, parts;               // heads of a token in groups of a warp's width; groups of a warp; warps of a token
+  int groups;                           // heads of a token in groups of a warp's width
+  int tokens;                           // tokens of a block
+  int per, parts;                       // the general kernel's: groups of a warp; warps of a token
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;
@@ -66,54 +68,182 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N]) {
   else *static_cast<uint32_t*>(p) = w[0];
 }
 
-// A lane's VEC values of a row in the cache's MX format; all lanes of the warp call this. `mine`: this lane's are stored.
-template <int VEC, int FMT>
-__device__ __forceinline__ void store_mx(const float (&f)[VEC], bool mine, uint8_t* codes, uint8_t* scales, long long row,
-                                         int D, int ch) {
-  constexpr int BL = 32 / VEC;          // lanes of a block
+// A lane's VEC values, which are 1/4 (1/8) of a block, in the cache's MX format: the block's scale byte, and the codes. All lanes of
+// the warp call this.
+template <int VEC, int FMT, int N>
+__device__ __forceinline__ uint32_t mx_codes(const float (&f)[VEC], uint32_t (&w)[N]) {
+  static_assert(N == (FMT == MOE_KV_MXFP8 ? VEC / 4 : 1), "words of codes");
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);    // what is not finite lies above all else
 #pragma unroll
-  for (int d = 1; d < BL; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int d = 1; d < 32 / VEC; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   const bool finite = m < 0x7F800000u;
   const int se = FMT == MOE_KV_MXFP8 ? e4m3_scale_exp(__uint_as_float(m)) : e2m1_scale_exp(__uint_as_float(m));
   const float sc = pow2_neg(se);
-  // a row's scale bytes in one word, in its first lane
-  const uint32_t b = finite ? (uint32_t)(se + 127) : 255u;
-  uint32_t all = b;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    const uint32_t other = __shfl_down_sync(0xffffffffu, b, i * BL);
-    if (i < D / 32) all |= other << (8 * i);
+  for (int i = 0; i < N; ++i) {
+    w[i] = 0;
+    if constexpr (FMT == MOE_KV_MXFP8) {
+      w[i] = e4m3x2(f[4 * i] * sc, f[4 * i + 1] * sc) | e4m3x2(f[4 * i + 2] * sc, f[4 * i + 3] * sc) << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) w[i] |= e2m1x2(f[2 * e] * sc, f[2 * e + 1] * sc) << (8 * e);
+    }
+    if (!finite) w[i] = 0;
   }
-  if (!mine) return;
-  if constexpr (FMT == MOE_KV_MXFP8) {
-    uint32_t w[VEC / 4];
-#pragma unroll
-    for (int i = 0; i < VEC / 4; ++i)
-      w[i] = finite ? e4m3x2(f[4 * i] * sc, f[4 * i + 1] * sc) | e4m3x2(f[4 * i + 2] * sc, f[4 * i + 3] * sc) << 16 : 0u;
-    store_words(codes + row * D + ch * VEC, w);
+  return finite ? (uint32_t)(se + 127) : 255u;
+}
+
+// VEC values of a row that go into the cache, from value d0 on; `row` counts the cache's rows of D values. All lanes of the warp
+// call this; `mine`: this lane's are stored.
+template <int VEC, int FMT>
+__device__ __forceinline__ void store_kv(const RopeArgs& a, const float (&f)[VEC], const uint32_t (&o)[VEC / 2], bool mine,
+                                         bool is_v, long long row, int d0) {
+  uint8_t* data = static_cast<uint8_t*>(is_v ? a.c.v : a.c.k);
+  if constexpr (FMT == MOE_KV_BF16) {
+    if (mine) store_words(reinterpret_cast<uint16_t*>(data) + row * a.D + d0, o);
   } else {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) w |= e2m1x2(f[2 * i] * sc, f[2 * i + 1] * sc) << (8 * i);
-    if (!finite) w = 0;
-    uint8_t* to = codes + row * (D / 2) + ch * (VEC / 2);
-    if constexpr (VEC == 8) *reinterpret_cast<uint32_t*>(to) = w;
-    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)w;
-  }
-  if (ch == 0) {
-    if (D == 128) *reinterpret_cast<uint32_t*>(scales + row * 4) = all;
-    else *reinterpret_cast<uint16_t*>(scales + row * 2) = (uint16_t)all;
+    uint32_t w[FMT == MOE_KV_MXFP8 ? VEC / 4 : 1];
+    const uint32_t byte = mx_codes<VEC, FMT>(f, w);
+    if (!mine) return;
+    if constexpr (FMT == MOE_KV_MXFP8) store_words(data + row * a.D + d0, w);
+    else if constexpr (VEC == 8) *reinterpret_cast<uint32_t*>(data + (row * a.D + d0) / 2) = w[0];
+    else *reinterpret_cast<uint16_t*>(data + (row * a.D + d0) / 2) = (uint16_t)w[0];
+    if (d0 % 32 == 0) (is_v ? a.c.v_s : a.c.k_s)[(row * a.D + d0) / 32] = (uint8_t)byte;
   }
 }
 
-// PAIRS: neighbours (2i, 2i + 1), in one lane; else (i, i + half), `half / VEC` lanes apart.
+// The cosine and sine of pair i of token t.
+__device__ __forceinline__ float2 turn_of(const RopeArgs& a, int t, int i) {
+  const int x = a.axis ? min((int)a.axis[i], a.axes - 1) : 0;
+  uint64_t n = (uint64_t)(long long)a.pos[x * a.pos_stride + t] * a.turns[i];
+  if (a.back) n = 0 - n;
+  float s, c;
+  sincospif((float)(int32_t)((n + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);    // the fraction in half turns, from -1 to 1
+  return make_float2(c * a.factor, s * a.factor);
+}
+
+// Where a token is stored: its row in head 0 of its page, or -1.
+__device__ __forceinline__ long long kv_row(const RopeArgs& a, int t, bool report) {
+  const int slot = a.slots[t];
+  const bool in = slot >= 0 && slot < (long long)a.c.pages << a.page_log2;
+  if (!in && slot != -1 && report) atomicCAS(a.status, 0u, (uint32_t)DEV_BAD_INPUT);
+  return in ? (((long long)(slot >> a.page_log2) * a.c.Hkv) << a.page_log2) + (slot & (a.c.page_size - 1)) : -1;
+}
+
+// Head u of a token's q, k and v, as they are read.
+__device__ __forceinline__ const uint16_t* row_of(const RopeArgs& a, int t, int u) {
+  return u < a.Hq        ? a.q + t * a.q_stride + u * a.D
+         : u < a.Hq + a.Hk ? a.k + t * a.k_stride + (u - a.Hq) * a.D
+                           : a.v + t * a.v_stride + (u - a.Hq - a.Hk) * a.D;
+}
+
+// A thread has two chunks of 8 values of a head, which are the halves of 8 pairs, or 4 pairs each (PAIRS: neighbours), or two that
+// are copied; D / 16 threads a head. So no value passes from lane to lane. A block takes `tokens` tokens (1, 2, 4 or 8): its threads
+// work out their cosines and sines together, while the first heads are on their way, and its warps share the tokens' heads.
+template <bool PAIRS, int FMT>
+__global__ void __launch_bounds__(kRopeWarps * 32, FMT == kNoCache || FMT == MOE_KV_BF16 ? 4 : 3)
+rope_paired_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int U = 2;                  // groups of heads under way
+  __shared__ float2 turn[kRopeWarps][kRopeMaxD / 2];    // by token of the block
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int share = kRopeWarps / a.tokens, mine = warp / share;          // warps of a token
+  const int t = min((int)blockIdx.x * a.tokens + mine, a.T - 1);
+  const bool there = blockIdx.x * (long long)a.tokens + mine < a.T;
+  const int heads = 32 / a.lanes, in_warp = lane / a.lanes, l = lane - in_warp * a.lanes;
+  const int n = a.half / 8, tail = a.lanes - n;         // lanes of what is turned, of what is not
+  const bool turned = l < n;
+  const int d0 = 8 * (turned ? l : n + l), d1 = d0 + 8 * (turned ? n : tail);
+  const int units = in_warp < heads && there ? a.Hq + a.Hk + a.Hv : 0;
+
+  uint32_t x[U][2][4];
+  auto fetch = [&](int g0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int u = (g0 + j * share) * heads + in_warp;
+      if (u < units) {
+        const uint16_t* row = row_of(a, t, u);
+        load_words(x[j][0], row + d0);
+        load_words(x[j][1], row + d1);
+      }
+    }
+  };
+  int g0 = warp - mine * share;
+  fetch(g0);
+  for (int i = threadIdx.x; i < a.tokens * a.half; i += kRopeWarps * 32) {
+    const int k = i / a.half, at = blockIdx.x * a.tokens + k;
+    if (at < a.T) turn[k][i - k * a.half] = turn_of(a, at, i - k * a.half);
+  }
+  long long row0 = -1;
+  if constexpr (FMT != kNoCache) {
+    if (there) row0 = kv_row(a, t, lane == 0 && warp == mine * share);
+  }
+  __syncthreads();
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // of neighbours, chunk d0 has pairs d0 / 2 to d0 / 2 + 3, and d1 the other four
+    const float2 cs = turned ? turn[mine][PAIRS ? (e < 4 ? d0 / 2 + e : d1 / 2 + e - 4) : d0 + e] : make_float2(1.f, 0.f);
+    c[e] = cs.x, s[e] = cs.y;
+  }
+
+  for (; g0 < a.groups; g0 += U * share) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (g0 + j * share >= a.groups) break;
+      const int u = (g0 + j * share) * heads + in_warp;
+      const bool is_q = u < min(a.Hq, units), is_k = !is_q && u < min(a.Hq + a.Hk, units), is_v = !is_q && !is_k && u < units;
+      float f[2][8];
+      uint32_t o[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[h][e] = x[j][h][e];         // copies keep their bits
+          f[h][2 * e] = bf16_lo(x[j][h][e]);
+          f[h][2 * e + 1] = bf16_hi(x[j][h][e]);
+        }
+      if (turned && !is_v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& p = PAIRS ? f[e / 4][2 * (e % 4)] : f[0][e];
+          float& q = PAIRS ? f[e / 4][2 * (e % 4) + 1] : f[1][e];
+          const float p0 = p, q0 = q;
+          p = p0 * c[e] - q0 * s[e];
+          q = p0 * s[e] + q0 * c[e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][e] = bf16x2(f[h][2 * e], f[h][2 * e + 1]);
+      }
+      if (is_q || (is_k && a.k_out)) {
+        uint16_t* to = is_q ? a.q_out + t * a.qo_stride + u * a.D : a.k_out + t * a.ko_stride + (u - a.Hq) * a.D;
+        store_words(to + d0, o[0]);
+        store_words(to + d1, o[1]);
+      }
+      if constexpr (FMT != kNoCache) {
+        const bool in = row0 >= 0 && (is_k || is_v);
+        if (__any_sync(0xffffffffu, in)) {
+          const long long row = row0 + ((long long)(is_v ? u - a.Hq - a.Hk : u - a.Hq) << a.page_log2);
+          store_kv<8, FMT>(a, f[0], o[0], in, is_v, row, d0);
+          store_kv<8, FMT>(a, f[1], o[1], in, is_v, row, d1);
+        }
+      }
+    }
+    fetch(g0 + U * share);
+  }
+}
+
+// Heads whose halves, or whose blocks of 32, do not lie so: a lane has one chunk of a head, of 8 values, or 4 where the turned
+// part's second half would begin inside 8, and the other half of its pairs comes from another lane. A warp takes a part of a token
+// and works out its cosines and sines.
 template <int VEC, bool PAIRS, int FMT>
 __global__ void __launch_bounds__(kRopeWarps * 32)
 rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int U = 4;                  // groups under way
   __shared__ float2 turn[kRopeWarps][kRopeMaxD / 2];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long wid = (long long)blockIdx.x * kRopeWarps + warp;
@@ -121,93 +251,48 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_trigger();
   pdl_wait();
   if (t >= a.T) return;
-  const int ch = lane & ((1 << a.lane_log2) - 1), d0 = ch * VEC, rot = 2 * a.half;
-  const int in_warp = lane >> a.lane_log2, heads = 32 >> a.lane_log2, units = a.Hq + a.Hk + a.Hv;
+  const int heads = 32 / a.lanes, in_warp = lane / a.lanes, ch = lane - in_warp * a.lanes;
+  const int d0 = ch * VEC, rot = 2 * a.half, units = in_warp < heads ? a.Hq + a.Hk + a.Hv : 0;
   const int end = min(a.groups, (part + 1) * a.per);
 
-  uint32_t w[U][VEC / 2];
-  auto fetch = [&](int g0) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int u = (g0 + j) * heads + in_warp;
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) w[j][e] = 0;
-      if (g0 + j < end && u < units && d0 < a.D) {
-        const uint16_t* row = u < a.Hq ? a.q + t * a.q_stride + u * a.D
-                            : u < a.Hq + a.Hk ? a.k + t * a.k_stride + (u - a.Hq) * a.D
-                                              : a.v + t * a.v_stride + (u - a.Hq - a.Hk) * a.D;
-        load_words(w[j], row + d0);
-      }
-    }
-  };
-  fetch(part * a.per);
-
-  for (int i = lane; i < a.half; i += 32) {
-    const int x = a.axis ? min((int)a.axis[i], a.axes - 1) : 0;
-    uint64_t n = (uint64_t)(long long)a.pos[x * a.pos_stride + t] * a.turns[i];
-    if (a.back) n = 0 - n;
-    float s, c;
-    sincospif((float)(int32_t)((n + 0x80000000u) >> 32) * 0x1p-31f, &s, &c);    // the fraction in half turns, from -1 to 1
-    turn[warp][i] = make_float2(c * a.factor, s * a.factor);
-  }
-  int slot = -1;
-  long long row0 = 0;                   // the token's place in head 0 of its page
-  bool stored = false;
-  if constexpr (FMT != kNoCache) {
-    slot = a.slots[t];
-    stored = slot >= 0 && slot < (long long)a.c.pages << a.page_log2;
-    if (!stored && slot != -1 && lane == 0) atomicCAS(a.status, 0u, (uint32_t)DEV_BAD_INPUT);
-    if (stored) row0 = (((long long)(slot >> a.page_log2) * a.c.Hkv) << a.page_log2) + (slot & (a.c.page_size - 1));
-  }
+  for (int i = lane; i < a.half; i += 32) turn[warp][i] = turn_of(a, t, i);
+  long long row0 = -1;
+  if constexpr (FMT != kNoCache) row0 = kv_row(a, t, lane == 0 && part == 0);
   __syncwarp();
-
   const bool turned = d0 < rot, second = d0 >= a.half;
   float c[VEC], s[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const int i = PAIRS ? d0 / 2 + e / 2 : second ? d0 - a.half + e : d0 + e;
-    const float2 cs = turned ? turn[warp][i] : make_float2(1.f, 0.f);
+    const float2 cs = turned ? turn[warp][PAIRS ? d0 / 2 + e / 2 : second ? d0 - a.half + e : d0 + e] : make_float2(1.f, 0.f);
     c[e] = cs.x;
     s[e] = (PAIRS ? (e & 1) == 0 : !second) ? -cs.y : cs.y;
   }
   const int far = turned && !PAIRS ? (second ? lane - a.half / VEC : lane + a.half / VEC) : lane;
 
-  for (int g0 = part * a.per; g0 < end; g0 += U) {
-    if (g0 != part * a.per) fetch(g0);
+  for (int g = part * a.per; g < end; ++g) {
+    const int u = g * heads + in_warp;
+    const bool is_q = u < min(a.Hq, units), is_k = !is_q && u < min(a.Hq + a.Hk, units), is_v = !is_q && !is_k && u < units;
+    uint32_t w[VEC / 2] = {}, o[VEC / 2];
+    if (u < units) load_words(w, row_of(a, t, u) + d0);
+    float f[VEC];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (g0 + j >= end) break;
-      const int u = (g0 + j) * heads + in_warp;
-      const bool is_q = u < a.Hq, is_k = !is_q && u < a.Hq + a.Hk, is_v = !is_q && !is_k && u < units;
-      const bool turns = turned && !is_v;
-      uint32_t other[VEC / 2], o[VEC / 2];
-      float f[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        other[e] = PAIRS ? (w[j][e] >> 16) | (w[j][e] << 16) : __shfl_sync(0xffffffffu, w[j][e], far);
-        f[2 * e] = bf16_lo(w[j][e]);
-        f[2 * e + 1] = bf16_hi(w[j][e]);
-        if (turns) {
-          f[2 * e] = f[2 * e] * c[2 * e] + bf16_lo(other[e]) * s[2 * e];
-          f[2 * e + 1] = f[2 * e + 1] * c[2 * e + 1] + bf16_hi(other[e]) * s[2 * e + 1];
-        }
-        o[e] = turns ? bf16x2(f[2 * e], f[2 * e + 1]) : w[j][e];        // copies keep their bits
+    for (int e = 0; e < VEC / 2; ++e) {
+      const uint32_t other = PAIRS ? (w[e] >> 16) | (w[e] << 16) : __shfl_sync(0xffffffffu, w[e], far & 31);
+      f[2 * e] = bf16_lo(w[e]);
+      f[2 * e + 1] = bf16_hi(w[e]);
+      o[e] = w[e];                      // copies keep their bits
+      if (turned && !is_v) {
+        f[2 * e] = f[2 * e] * c[2 * e] + bf16_lo(other) * s[2 * e];
+        f[2 * e + 1] = f[2 * e + 1] * c[2 * e + 1] + bf16_hi(other) * s[2 * e + 1];
+        o[e] = bf16x2(f[2 * e], f[2 * e + 1]);
       }
-      if (d0 < a.D) {
-        if (is_q) store_words(a.q_out + t * a.qo_stride + u * a.D + d0, o);
-        if (is_k && a.k_out) store_words(a.k_out + t * a.ko_stride + (u - a.Hq) * a.D + d0, o);
-      }
-      if constexpr (FMT != kNoCache) {
-        const bool in = stored && (is_k || is_v);
-        const int h = is_v ? u - a.Hq - a.Hk : u - a.Hq;
-        const long long row = row0 + ((long long)h << a.page_log2);
-        if constexpr (FMT == MOE_KV_BF16) {
-          if (in) store_words(static_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + row * a.D + d0, o);
-        } else {
-          if (__any_sync(0xffffffffu, in))
-            store_mx<VEC, FMT>(f, in, static_cast<uint8_t*>(is_v ? a.c.v : a.c.k), is_v ? a.c.v_s : a.c.k_s, row, a.D, ch);
-        }
-      }
+    }
+    if (is_q) store_words(a.q_out + t * a.qo_stride + u * a.D + d0, o);
+    if (is_k && a.k_out) store_words(a.k_out + t * a.ko_stride + (u - a.Hq) * a.D + d0, o);
+    if constexpr (FMT != kNoCache) {
+      const bool in = row0 >= 0 && (is_k || is_v);
+      if (__any_sync(0xffffffffu, in))
+        store_kv<VEC, FMT>(a, f, o, in, is_v, row0 + ((long long)(is_v ? u - a.Hq - a.Hk : u - a.Hq) << a.page_log2), d0);
     }
   }
 }
@@ -242,8 +327,8 @@ static bool rotary_ok(const moe_rotary* r, int D) {
          D % 8 == 0 && D <= kRopeMaxD;
 }
 
-// Lanes take 8 values, or 4 where the second half of a turned head would begin inside 8: half the bytes a load, for which the
-// head has to fit 32 lanes.
+// The general kernel's lanes take 8 values, or 4 where the second half of a turned head would begin inside 8: half the bytes a load,
+// for which the head has to fit 32 lanes.
 static int rope_vec(const moe_rotary* r) { return !r->interleaved && r->dim % 16 ? 4 : 8; }
 
 template <int VEC, bool PAIRS>
@@ -255,14 +340,33 @@ static void (*rope_kernel_of(int format))(RopeArgs) {
     default: return rope_kernel<VEC, PAIRS, kNoCache>;
   }
 }
+template <bool PAIRS>
+static void (*rope_paired_of(int format))(RopeArgs) {
+  switch (format) {
+    case MOE_KV_BF16: return rope_paired_kernel<PAIRS, MOE_KV_BF16>;
+    case MOE_KV_MXFP8: return rope_paired_kernel<PAIRS, MOE_KV_MXFP8>;
+    case MOE_KV_MXFP4: return rope_paired_kernel<PAIRS, MOE_KV_MXFP4>;
+    default: return rope_paired_kernel<PAIRS, kNoCache>;
+  }
+}
 
 static int launch_rope(RopeArgs& p, bool pairs, int vec, int format, cudaStream_t st) {
-  while ((vec << p.lane_log2) < p.D) ++p.lane_log2;
-  p.groups = ceil_div(p.Hq + p.Hk + p.Hv, 32 >> p.lane_log2);
-  // As many groups a warp as leave every multiprocessor 32 warps, at least 2: few tokens are a matter of latency, many of not
-  // working out their cosines again.
+  const int rot = 2 * p.half, heads = p.Hq + p.Hk + p.Hv;
+  const bool blocks_fit = format == kNoCache || format == MOE_KV_BF16 || (rot % 64 == 0 && p.D % 64 == 0);
+  if (rot % 16 == 0 && p.D % 16 == 0 && blocks_fit) {
+    p.lanes = p.D / 16;
+    p.groups = ceil_div(heads, 32 / p.lanes);
+    // Tokens of a block: as many as leave a warp no more than 8 groups of heads and the GPU 4 blocks a multiprocessor.
+    p.tokens = kRopeWarps;
+    while (p.tokens > 1 && (p.groups > 8 * (kRopeWarps / p.tokens) || p.T < 4ll * num_sms() * p.tokens)) p.tokens /= 2;
+    return launch_pdl(pairs ? rope_paired_of<true>(format) : rope_paired_of<false>(format),
+                      dim3((unsigned)ceil_div(p.T, p.tokens)), dim3(kRopeWarps * 32), 0, st, p);
+  }
+  p.lanes = ceil_div(p.D, vec);
+  p.groups = ceil_div(heads, 32 / p.lanes);
+  // As many groups a warp as leave every multiprocessor 32 warps, at least 2 and at most 16.
   const long long all = (long long)p.T * p.groups, slots = (long long)num_sms() * 32;
-  p.per = all >= 8 * slots ? 8 : all >= 4 * slots ? 4 : 2;
+  p.per = (int)std::max(2ll, std::min(16ll, all / slots));
   p.parts = ceil_div(p.groups, p.per);
   const long long warps = (long long)p.T * p.parts, blocks = (warps + kRopeWarps - 1) / kRopeWarps;
   if (blocks >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
