@@ -30,7 +30,7 @@
 
 namespace moe {
 
-constexpr int kTileTok = 64;          // tokens of a stage
+constexpr int kTileTok = 64;          // tokens of a stage; over MXFP4 twice as many
 constexpr int kFewRows = 16;          // rows that this kernel takes
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -56,17 +56,21 @@ struct PagedCfg {
   // 256 sequences of 4096 tokens, 32 heads over 8 of 128, MXFP8 651 (16 rows' code), 441, 456 us; 64 over 8 of 64, MXFP8
   // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us.
   static constexpr int CTAS = !EIGHT ? 2 : MX && D == 64 ? 4 : 3;
-  static constexpr int WARPS = 4, ST = kTileTok / WARPS;           // tokens of a stage that a warp takes
+  static constexpr int TILE = BITS == 4 ? 2 * kTileTok : kTileTok;
+  static constexpr int WARPS = 4, ST = TILE / WARPS;               // tokens of a stage that a warp takes
   static constexpr int HALVES = MX ? 1 : D / 64;                   // 128-byte (MX: D-byte) column blocks of a row
   static constexpr int ROWB = MX ? D * BITS / 8 : 128;             // bytes of a row in a column block
-  static constexpr int KV = kTileTok * D * BITS / 8;               // bytes of a stage's keys, or values
-  static constexpr int SC = MX ? kTileTok * D / 32 : 0;
+  static constexpr int KV = TILE * D * BITS / 8;                   // bytes of a stage's keys, or values
+  static constexpr int SC = MX ? TILE * D / 32 : 0;
   static constexpr int STAGE = 2 * KV + (MX ? 1024 : 0);
-  static constexpr int STAGES = (CTAS == 4 ? 45056 : CTAS == 3 ? 65536 : 98304) / STAGE;
+  static constexpr int STAGES = (CTAS == 4 ? 45056 : CTAS == 3 ? 65536 : BITS == 4 ? 73728 : 98304) / STAGE;
   static constexpr int PITCH = D + 4;                              // floats of a row in the join buffer
-  static constexpr int JOIN = 2 * 8 * PITCH * 4;                   // of two warps 8 rows at a time
-  static constexpr int SMEM = STAGES * STAGE + JOIN + 1024;
-  static_assert(2 * SC <= 1024, "scales");
+  // of two warps 8 rows at a time; over MXFP4 of all warps all rows
+  static constexpr int JOIN = (BITS == 4 ? WARPS * (EIGHT ? 8 : 16) : 2 * 8) * PITCH * 4;
+  static constexpr int QROWS = BITS == 4 ? (EIGHT ? 8 : 16) : 0;   // rows of queries that come with an item, twice
+  static constexpr int QBUF = QROWS * D * 2;
+  static constexpr int SMEM = STAGES * STAGE + JOIN + 2 * QBUF + 1024;
+  static_assert(2 * SC <= 1024 && JOIN % 16 == 0, "scales; queries at multiples of 16 bytes");
 };
 
 // A barrier of the consuming warps, and whether any thread says so.
@@ -81,7 +85,7 @@ __device__ __forceinline__ bool consumers_any(bool said) {
 // Shared address of 16-byte chunk `chunk` (of the row's D values) of token `tok`.
 template <class C>
 __device__ __forceinline__ uint32_t kv_addr(uint32_t base, int tok, int chunk) {
-  if (C::ROWB == 128) return base + (chunk >> 3) * (kTileTok * 128) + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
+  if (C::ROWB == 128) return base + (chunk >> 3) * (C::TILE * 128) + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4);
   if (C::ROWB == 64) return base + tok * 64 + ((chunk ^ ((tok >> 1) & 3)) << 4);
   return base + tok * 32 + ((chunk ^ ((tok >> 2) & 1)) << 4);
 }
@@ -102,9 +106,9 @@ struct FewItem {
   int pos0, pmin, pmax;                         // positions of the first of all rows, of the first and last that are there
   int first_any, first_all, sink_tiles, win_tile;
   int i0, cnt, piece, pieces;                   // first step, steps; piece of how many
-  __device__ __forceinline__ int tok(int i) const {
+  __device__ __forceinline__ int tok(int i, int tile = kTileTok) const {
     const int t = i0 + i;
-    return (t < sink_tiles ? t : win_tile + (t - sink_tiles)) * kTileTok;
+    return (t < sink_tiles ? t : win_tile + (t - sink_tiles)) * tile;
   }
 };
 
@@ -452,19 +456,28 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 // their other side, as f16, which holds an E2M1 code and has an instruction for two of them. What f16's range asks for:
 //  - a query is scaled to less than 2 by a power of two of its row: what is 2^-17 of the largest or more keeps all of bf16's
 //    digits, the rest is rounded to 2^-25 of it, as fp32 sums would; a block's scale is put on its 32 products' sum, in fp32;
-//  - weights are 2^kLift times themselves at most 2^kGrow (the maximum that they refer to moves when outgrown by that): weights
-//    below 2^-24 - kLift of the largest become zero, 2^17 tokens of them 2^-13 of the result;
-//  - a thread's values are all of one block's columns and are held in units of 2^E, E the largest scale of that block so far:
-//    scales down to 2^-12 of it keep codes exact. Keys further apart go through bf16, in units of their own (`wide`).
+//  - weights are 2^kFewLift times themselves, at most 2^kFewGrow more (the maximum that they refer to moves when outgrown by
+//    that): weights below 2^-25 - kFewLift of the largest become zero, 2^17 tokens of them 2^-15 of the result;
+//  - a thread's values are all of one block's columns and are held in units of 2^(E - kUp): scales from 2^-kSpread to 1 of 2^E
+//    keep codes exact. E grows with the scales that come; keys too far below it, and those whose scale is NaN, are left out of the
+//    product and added one by one in fp32 (`apart`).
+// Both references begin at values that most caches never leave, so that an item has no first step of its own: weights at 1,
+// for scores of 2^-kFewLow to 2^kFewGrow, and E at kFirstE, for values' scales of 2^-20 to 2^7.
 // Conversion: an instruction for two keys' codes; of values' codes, which lie the other way round, half a one more to put two
 // keys' codes into one byte, and one for the scales.
-constexpr float kFewLift = 7.f, kFewGrow = 8.f;
-constexpr int kSpread = 12;
+constexpr float kFewLift = 7.f, kFewGrow = 8.f, kFewLow = 7.f;
+constexpr int kUp = 13, kSpread = 27, kFirstE = 134;
 
 // The token of a warp's 16 that is row i of the products. Neighbouring threads' values are then in different banks.
 template <int D>
 __device__ __forceinline__ int tok_of(int i) {
   return D == 128 ? (i & 12) | (i & 1) << 1 | (i >> 1 & 1) : (i & 8) | (i & 1) << 2 | (i >> 1 & 3);
+}
+
+// And the row of the products (of 8) that has token i.
+template <int D>
+__device__ __forceinline__ int row_of_tok(int i) {
+  return D == 128 ? (i & 4) | (i & 1) << 1 | (i >> 1 & 1) : (i & 3) << 1 | i >> 2;
 }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -494,16 +507,25 @@ __device__ __forceinline__ float pow2i(int e) {
 }
 
 template <class C>
-__device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, float* join, uint64_t* full, uint64_t* empty,
-                                             uint64_t* w_full, uint64_t* w_empty, const uint32_t* page_mask,
+__device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, float* join, const uint8_t* queries, uint64_t* full, uint64_t* empty,
+                                             uint64_t* w_full, uint64_t* w_empty, const int4* infos,
                                              const FewItem* items, float2 (*sums)[16], volatile uint32_t* abort, int warp,
                                              int lane) {
-  constexpr int D = C::D, ST = C::ST, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
-  static_assert(ST == 16, "a warp's tokens of a stage are a product's rows");
+  constexpr int D = C::D, ST = C::ST, GR = ST / 16, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
   const int g = lane >> 2, c = lane & 3, G = p.G, R = p.R;
-  const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;
+  const int page_log2 = min(p.page_log2, 7);
   const float scale = p.a.scale * 1.4426950408889634f;
   const int tg = tok_of<D>(g);
+  // A stage's places of this lane: its key's word of block 0 (the block's number turns bits 4 and 5), its two values' codes, their
+  // scales. Keys 8 and 16 further lie at the same places of their 8, turned alike.
+  const uint32_t k_lane = kv_addr<C>(0, warp * ST + tg, 0) + 4 * c, ks_lane = 2 * C::KV + (warp * ST + tg) * (D / 32);
+  uint32_t v_lane[2], vs_lane[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int tk = warp * ST + tok_of<D>(2 * c + e);
+    v_lane[e] = C::KV + kv_addr<C>(0, tk, D == 128 ? g >> 1 : g >> 2) + (D == 128 ? 8 * (g & 1) : 4 * (g & 3));
+    vs_lane[e] = 2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D);
+  }
   uint32_t qf[NB][D / 16][2];
   float qs[NB][2];                              // of rows 2c and 2c + 1: what their queries were divided by
   auto load_q = [&](int n) {
@@ -512,13 +534,13 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
       return false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int rho = 8 * nb + g, r = rho / G;
-      const uint16_t* row = p.q + ((long long)items[n & 1].b * p.rows + r) * p.q_stride + (long long)(items[n & 1].hk * G + rho - r * G) * D;
+      const int rho = 8 * nb + g;
+      const uint8_t* row = queries + (n & 1) * C::QBUF + rho * D * 2;
       uint4 w[D / 32];                          // block by block the 8 values whose codes one thread has at hand
       uint32_t m2 = 0;
 #pragma unroll
       for (int bl = 0; bl < D / 32; ++bl) {
-        w[bl] = rho < R ? *reinterpret_cast<const uint4*>(row + bl * 32 + 8 * c) : make_uint4(0, 0, 0, 0);
+        w[bl] = rho < R ? *reinterpret_cast<const uint4*>(row + (bl * 32 + 8 * c) * 2) : make_uint4(0, 0, 0, 0);
         m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[bl].x & 0x7FFF7FFFu, w[bl].y & 0x7FFF7FFFu),
                                    __vmaxu2(w[bl].z & 0x7FFF7FFFu, w[bl].w & 0x7FFF7FFFu)));
       }
@@ -546,241 +568,302 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     }
     return true;
   };
-  int tiles = 0;                                // steps so far
+  int stage = 0;                                // of the next step, and its phase
+  uint32_t phase = 0;
   // the warps go on together or not at all, also when one of them has given up
   bool stop = consumers_any<C::WARPS>(!load_q(0));
   for (int n = 0; !stop; ++n) {
     const FewItem& it = items[n & 1];
     const int cnt = it.cnt;
-    int pos[NB][2], first[NB][2];
-    float o[NB][MT][4], ol[NB][4], m[NB][2];    // ol: the weights' sums, by a product with ones
+    float o[NB][MT][4], ol[NB][4];              // ol: the weights' sums, by a product with ones
+    float off[NB][2];                           // kFewLift less what weights refer to
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rho = 8 * nb + 2 * c + e;
-        pos[nb][e] = rho < R ? it.pos0 + rho / G : -1;
-        first[nb][e] = (p.a.window && pos[nb][e] >= p.a.window) ? pos[nb][e] + 1 - p.a.window : 0;
-        m[nb][e] = -INFINITY;
-      }
+      for (int e = 0; e < 2; ++e) off[nb][e] = kFewLift;
 #pragma unroll
       for (int j = 0; j < MT; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.f;
       ol[nb][0] = ol[nb][1] = ol[nb][2] = ol[nb][3] = 0.f;
     }
-    int E = -1;                                 // scale byte of the outputs' unit; none yet
-    bool wide = false;                          // for all of the warp
+    int E = kFirstE;                            // scale byte of the outputs' unit
+    uint32_t early = 0;                         // this thread's rows that have had no weight worth the name yet
+#pragma unroll
+    for (int r = 0; r < 2 * NB; ++r) early |= (uint32_t)(4 * (r & ~1) + 2 * c + (r & 1) < R) << r;
+    bool first = true;                          // no value so far
 
-    for (int i = 0; i < cnt; ++i, ++tiles) {
-      const int s = tiles % C::STAGES;
-      if (!bar_wait(&full[s], (tiles / C::STAGES) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) {
+    for (int i = 0; i < cnt; ++i) {
+      const int s = stage;
+      if (!bar_wait(&full[s], phase, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) {
         __all_sync(0xffffffffu, false);         // told to those that go on below
         break;
       }
       if (!__all_sync(0xffffffffu, true)) break;
-      const int loc0 = warp * ST, tok0 = it.tok(i) + loc0;
-      const uint8_t* st = smem + s * C::STAGE;
-      const uint32_t kb = smem_u32(st), vb = kb + C::KV;
-      const uint32_t mask = page_mask[s];
-      // every row of the block sees every token of this warp
-      const bool whole = tok0 + ST - 1 <= it.pmin && (tok0 >= it.first_all || tok0 + ST <= p.a.sinks) &&
-                         mask == (1u << in_tile) - 1u;
-      if (tok0 <= it.pmax) {
+      if (++stage == C::STAGES) stage = 0, phase ^= 1;
+      const int4 info = infos[s];
+      const uint32_t st = smem_u32(smem) + s * C::STAGE;
+      const bool whole = (info.z >> warp) & 1;  // every row of the block sees every token of this warp
+      if ((info.z >> (C::WARPS + warp)) & 1) {
         // ---- scores ----
-        float sc[NB][4];
+        float sc[GR][NB][4];
+        bool bad = false;                       // a block's scale is NaN
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
-        {
-          const uint8_t* scales = st + 2 * C::KV;
+        for (int gr = 0; gr < GR; ++gr) {
           uint32_t sw[2], w[2][D / 32];
-          bool bad[2];                          // a block's scale is NaN
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int t = loc0 + tg + 8 * h;
-            sw[h] = D == 128 ? *reinterpret_cast<const uint32_t*>(scales + t * 4)
-                             : *reinterpret_cast<const uint16_t*>(scales + t * 2);
-            bad[h] = ((~sw[h] - 0x01010101u) & sw[h] & 0x80808080u) != 0;
+            const uint32_t at = st + ks_lane + (8 * h + 16 * gr) * (D / 32);
+            if constexpr (D == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw[h]) : "r"(at) : "memory");
+            else asm volatile("{\n\t.reg .b16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(sw[h]) : "r"(at) : "memory");
+            bad = bad || ((~sw[h] - 0x01010101u) & sw[h] & 0x80808080u) != 0;
 #pragma unroll
             for (int bl = 0; bl < D / 32; ++bl)
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(kv_addr<C>(kb, t, bl) + 4 * c) : "memory");
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((st + k_lane) ^ (bl << 4)) + (8 * h + 16 * gr) * C::ROWB) : "memory");
           }
 #pragma unroll
           for (int bl = 0; bl < D / 32; ++bl) {
             const uint32_t x0[4] = {e2m1_pair<0>(w[0][bl]), e2m1_pair<0>(w[1][bl]), e2m1_pair<1>(w[0][bl]), e2m1_pair<1>(w[1][bl])};
             const uint32_t x1[4] = {e2m1_pair<2>(w[0][bl]), e2m1_pair<2>(w[1][bl]), e2m1_pair<3>(w[0][bl]), e2m1_pair<3>(w[1][bl])};
-            float f[2];                         // 2^(byte - 127); 2^-127 is below fp32's normal numbers
+            float f[2];                         // 2^(byte - 127); byte 0, 2^-127, counts as zero
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              f[h] = __uint_as_float(max((bl < 3 ? sw[h] << (23 - 8 * bl) : sw[h] >> 1) & 0x7F800000u, 0x00400000u));
+            for (int h = 0; h < 2; ++h) f[h] = __uint_as_float((bl < 3 ? sw[h] << (23 - 8 * bl) : sw[h] >> 1) & 0x7F800000u);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               float a[4] = {0.f, 0.f, 0.f, 0.f};
               mma_16816_f16(a, x0, qf[nb][2 * bl][0], qf[nb][2 * bl][1]);
               mma_16816_f16(a, x1, qf[nb][2 * bl + 1][0], qf[nb][2 * bl + 1][1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sc[nb][e] = fmaf(a[e], f[e >> 1], sc[nb][e]);
+              for (int e = 0; e < 4; ++e) sc[gr][nb][e] = bl == 0 ? a[e] * f[e >> 1] : fmaf(a[e], f[e >> 1], sc[gr][nb][e]);
             }
           }
+        }
+        // The values' codes, under way while the weights are worked out: thread (g, c) has the D/8 values from g D/8 on of its
+        // four tokens of 16; product j takes the 2j-th of each as its row g, and the next as its row g + 8.
+        uint32_t w[GR][4][VW], by[GR][2];       // by: the scales' bytes of two tokens, in halves
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t b[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t at = st + v_lane[e] + (8 * h + 16 * gr) * C::ROWB;
+              if constexpr (D == 128)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[gr][2 * h + e][0]), "=r"(w[gr][2 * h + e][1]) : "r"(at) : "memory");
+              else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[gr][2 * h + e][0]) : "r"(at) : "memory");
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[e]) : "r"(st + vs_lane[e] + (8 * h + 16 * gr) * (D / 32)) : "memory");
+            }
+            by[gr][h] = b[0] | b[1] << 16;
+          }
+        float t[GR][NB][4];                     // exponents of the weights
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              sc[nb][e] = sc[nb][e] * qs[nb][e & 1] * scale;
-              if (bad[e >> 1]) sc[nb][e] = __uint_as_float(0x7FC00000u);
+              sc[gr][nb][e] *= qs[nb][e & 1];
+              t[gr][nb][e] = fmaf(sc[gr][nb][e], scale, off[nb][e & 1]);
             }
-        }
-        // the values' codes, under way while the weights are worked out: thread (g, c) has the D/8 values from g D/8 on of its
-        // four tokens; product j takes the 2j-th of each as its row g, and the next as its row g + 8
-        uint32_t w[4][VW], by[4];
-        {
-          const uint8_t* scales = st + 2 * C::KV + C::SC;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tk = loc0 + tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1);
-            if constexpr (D == 128)
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1])
-                           : "r"(kv_addr<C>(vb, tk, g >> 1) + 8 * (g & 1)) : "memory");
-            else
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[e][0])
-                           : "r"(kv_addr<C>(vb, tk, g >> 2) + 4 * (g & 3)) : "memory");
-            by[e] = scales[tk * (D / 32) + g / (256 / D)];
-          }
-        }
 
         // ---- what the rows do not see ----
-        uint32_t drop = 0, some = 0;             // of this warp's tokens: no row sees it; some row does, some does not
+        uint32_t hidden = 0;                    // of t
+        const int tok0 = info.x + warp * ST;
         if (!whole) {
+          const uint32_t mask = (uint32_t)info.y;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int loc = tg + 8 * (e >> 1), t = tok0 + loc;
-              const bool there = (mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u;
-              const bool see = there && t <= pos[nb][e & 1] && (t >= first[nb][e & 1] || t < p.a.sinks);
-              sc[nb][e] = see ? sc[nb][e] : -INFINITY;
-            }
-          const int t = tok0 + lane;
-          const bool there = lane < ST && ((mask >> ((loc0 + lane) >> min(p.page_log2, 6))) & 1u);
-          const bool any = there && t <= it.pmax && (t >= it.first_any || t < p.a.sinks);
-          const bool all = any && t <= it.pmin && (t >= it.first_all || t < p.a.sinks);
-          drop = __ballot_sync(0xffffffffu, lane < ST && !any);
-          some = __ballot_sync(0xffffffffu, any && !all);
+            for (int e = 0; e < 2; ++e) {
+              const int rho = 8 * nb + 2 * c + e;
+              const Visible see(rho < R ? it.pos0 + rho / G : -1, p.a.window, p.a.sinks);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)           // whose codes and scales may be anything
-            if ((drop >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u) {
+              for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-              for (int v = 0; v < VW; ++v) w[e][v] = 0;
-              by[e] = max(E, 0);
+                for (int h = 0; h < 2; ++h) {
+                  const int loc = tg + 8 * h + 16 * gr;
+                  const bool there = (mask >> ((warp * ST + loc) >> page_log2)) & 1u;
+                  if (!there || !see.sees(tok0 + loc)) {
+                    t[gr][nb][2 * h + e] = -INFINITY;
+                    hidden |= 1u << (4 * (gr * NB + nb) + 2 * h + e);
+                  }
+                }
             }
+          const int tt = tok0 + lane;
+          const bool any = ((mask >> ((warp * ST + lane) >> page_log2)) & 1u) && tt <= it.pmax && (tt >= it.first_any || tt < p.a.sinks);
+          const uint32_t drop = __ballot_sync(0xffffffffu, !any);
+#pragma unroll
+          for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)         // whose codes and scales may be anything
+              if ((drop >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1) + 16 * gr)) & 1u) {
+#pragma unroll
+                for (int v = 0; v < VW; ++v) w[gr][e][v] = 0;
+                by[gr][e >> 1] = (by[gr][e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
+              }
         }
 
         // ---- where weights and outputs refer to ----
-        uint32_t nan = 0;                       // tokens whose block here has the scale NaN and that not all rows see
-        bool move = wide, nans = false;
-        {
-          const uint32_t hi = max(max(by[0], by[1]), max(by[2], by[3])), lo = min(min(by[0], by[1]), min(by[2], by[3]));
-          move = move || (int)hi > E || (int)lo < E - kSpread;
+        uint32_t u[GR][2], top = 0;             // kSpread less how far a scale is below E
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            u[gr][h] = by[gr][h] - (uint32_t)((E - kSpread) * 0x10001);
+            top = __vmaxu2(top, u[gr][h]);
+          }
+        const bool scales_move = max(top & 0xFFFFu, top >> 16) > kSpread;
+        bool weights_move = bad;
+#pragma unroll
+        for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) move = move || sc[nb][e] > m[nb][e & 1] + kFewGrow;
-        }
-        if (__any_sync(0xffffffffu, move)) {
+            for (int e = 0; e < 4; ++e) weights_move = weights_move || t[gr][nb][e] > kFewLift + kFewGrow;
+        if (__any_sync(0xffffffffu, early != 0)) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float mx[2], k[2];
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              mx[e] = fmaxf(sc[nb][e], sc[nb][2 + e]);
+              float mx = -INFINITY;
 #pragma unroll
-              for (int d = 4; d < 32; d *= 2) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-              if (!(mx[e] > m[nb][e] + kFewGrow)) mx[e] = m[nb][e];
-              k[e] = mx[e] == -INFINITY ? 1.f : ex2(m[nb][e] - mx[e]);
-              m[nb][e] = mx[e];
+              for (int gr = 0; gr < GR; ++gr) mx = fmaxf(mx, fmaxf(t[gr][nb][e], t[gr][nb][2 + e]));
+              const uint32_t bit = 1u << (2 * nb + e), seen = __ballot_sync(0xffffffffu, mx > kFewLift - kFewLow);
+              if (seen & (0x11111111u << c)) early &= ~bit;
+              else weights_move = weights_move || ((early & bit) && mx > -INFINITY);
             }
+        }
+        uint32_t apart = 0;                     // tokens that are added one by one
+        if (__any_sync(0xffffffffu, weights_move || scales_move)) {
+          if (__any_sync(0xffffffffu, bad)) {   // keys' scores that are NaN
+#pragma unroll
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t at = st + ks_lane + (8 * h + 16 * gr) * (D / 32);
+                bool is = false;
+                for (int b = 0; b < D / 32; ++b) {
+                  uint32_t x;
+                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at + b) : "memory");
+                  is = is || x == 255u;
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int e = 2 * h; e < 2 * h + 2; ++e)
+                    if (is) sc[gr][nb][e] = __uint_as_float(0x7FC00000u);
+              }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float k[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u)) mx = fmaxf(mx, sc[gr][nb][2 * h + e] * scale);
+#pragma unroll
+              for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              k[e] = 1.f;
+              const uint32_t bit = 1u << (2 * nb + e);
+              const float to = kFewLift - mx;
+              if (mx > -INFINITY && (to < off[nb][e] - kFewGrow || (early & bit))) {
+                k[e] = ex2(to - off[nb][e]);
+                off[nb][e] = to;
+                early &= ~bit;
+              }
+#pragma unroll
+              for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u))
+                    t[gr][nb][2 * h + e] = fmaf(sc[gr][nb][2 * h + e], scale, off[nb][e]);
+            }
+            ol[nb][0] *= k[0], ol[nb][1] *= k[1];
 #pragma unroll
             for (int j = 0; j < MT; ++j) o[nb][j][0] *= k[0], o[nb][j][1] *= k[1], o[nb][j][2] *= k[0], o[nb][j][3] *= k[1];
-            ol[nb][0] *= k[0], ol[nb][1] *= k[1];
           }
-          // The unit: the largest scale of a block whose codes are not all zero. Blocks of zeros have any scale.
-          int hi = -1;
-          bool not_zero[4], far = false;
+          if (__any_sync(0xffffffffu, scales_move)) {
+            // The unit follows the largest scale of a block whose codes are not all zero (blocks of zeros have any scale), down
+            // too while there is no value yet.
+            int hi = -1;
+            uint32_t zeros = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t any = 0;
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-            for (int v = 0; v < VW; ++v) any |= w[e][v] & 0x77777777u;
-            not_zero[e] = any != 0;
-            nans = nans || by[e] == 255u;
-            if (by[e] == 255u) {                // NaN, whatever the codes
-              const int loc = tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1);
-              if ((some >> loc) & 1u) nan |= 1u << loc;
-            } else if (any) {
-              hi = max(hi, (int)by[e]);
+              for (int e = 0; e < 4; ++e) {
+                const int b = (by[gr][e >> 1] >> (16 * (e & 1))) & 0xFFFF;
+                uint32_t any = 0;
+#pragma unroll
+                for (int v = 0; v < VW; ++v) any |= w[gr][e][v] & 0x77777777u;
+                if (b != 255 && any) hi = max(hi, b);
+                if (b != 255 && !any) zeros |= 1u << (4 * gr + e);
+              }
+#pragma unroll
+            for (int d = 1; d < 4; d *= 2) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+            const int was = E;
+            if (hi >= 0) E = first ? hi : max(E, hi);
+            const float k = pow2i(max(was - E, -149));       // 2^0 where nothing changes; with no value yet, of zeros
+            if (!first) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < MT; ++j) o[nb][j][0] *= k, o[nb][j][1] *= k, o[nb][j][2] *= k, o[nb][j][3] *= k;
             }
-          }
 #pragma unroll
-          for (int d = 1; d < 4; d *= 2) {
-            hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-            nan |= __shfl_xor_sync(0xffffffffu, nan, d);
-          }
-          const int was = E;
-          if (!wide) E = max(E, hi);
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!not_zero[e] && by[e] != 255u) by[e] = max(E, 0);
-            far = far || (int)by[e] < E - kSpread;
-          }
-          wide = wide || __any_sync(0xffffffffu, far);
-          // units of 1, or of 2^35 where a value is too large for sums in those: what is below 2^-126 of them loses digits
-          if (wide) E = max(E, hi) > 212 || E == 162 ? 162 : 127;
-          if (was >= 0 && was != E) {
-            const float k = pow2i(min(was - E, 127));
+              for (int e = 0; e < 4; ++e) {
+                const int b = (by[gr][e >> 1] >> (16 * (e & 1))) & 0xFFFF;
+                const bool zero = (zeros >> (4 * gr + e)) & 1u, away = !zero && (b == 255 || b < E - kSpread);
+                if (away) {
+                  apart |= 1u << (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1) + 16 * gr);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                  for (int v = 0; v < VW; ++v) w[gr][e][v] = 0;
+                }
+                if (zero || away) by[gr][e >> 1] = (by[gr][e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
+              }
+            apart = __reduce_or_sync(0xffffffffu, apart);
 #pragma unroll
-              for (int j = 0; j < MT; ++j) o[nb][j][0] *= k, o[nb][j][1] *= k, o[nb][j][2] *= k, o[nb][j][3] *= k;
+            for (int gr = 0; gr < GR; ++gr)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) u[gr][h] = by[gr][h] - (uint32_t)((E - kSpread) * 0x10001);
           }
         }
+        first = false;
 
-        // ---- weights ----
-        // Rounded to 16 bits for the second product; the sum takes the rounded ones, so that a single large weight divides out
-        // exactly.
-        float wt[NB][4];
+        uint32_t wt[GR][NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            wt[nb][e] = ex2(sc[nb][e] - (m[nb][e & 1] == -INFINITY ? 0.f : m[nb][e & 1] - kFewLift));
-
-        // ---- weighted values ----
-        if (!wide) {
+        for (int gr = 0; gr < GR; ++gr) {
+          // ---- weights ----
+          // Rounded to 16 bits for the second product; the sum takes the rounded ones, so that a single large weight divides
+          // out exactly.
           uint32_t pf[NB][2];
           const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            pf[nb][0] = transposed(f16x2(wt[nb][0], wt[nb][1]));
-            pf[nb][1] = transposed(f16x2(wt[nb][2], wt[nb][3]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              wt[gr][nb][h] = f16x2(ex2(t[gr][nb][2 * h]), ex2(t[gr][nb][2 * h + 1]));
+              pf[nb][h] = transposed(wt[gr][nb][h]);
+            }
             mma_16816_f16(ol[nb], ones, pf[nb][0], pf[nb][1]);
           }
-          uint32_t fac[2];                      // of two tokens each: 2^(byte - E) in f16
+          // ---- weighted values ----
+          uint32_t fac[2];                      // of two tokens each: 2^(byte - E + kUp) in f16
+          static_assert(kUp + 15 == kSpread + 1, "the smallest factor is the smallest normal number");
 #pragma unroll
-          for (int h = 0; h < 2; ++h) fac[h] = ((by[2 * h] | by[2 * h + 1] << 16) - (uint32_t)((E - 15) * 0x10001)) << 10;
-          if (nans) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (by[e] == 255u) {
-                const bool later = (some >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u;
-                const uint32_t sh = 16 * (e & 1);
-                fac[e >> 1] = (fac[e >> 1] & ~(0xFFFFu << sh)) | (later ? 0u : 0x7E00u) << sh;
-              }
-          }
+          for (int h = 0; h < 2; ++h) fac[h] = (u[gr][h] << 10) + 0x04000400u;
 #pragma unroll
           for (int v = 0; v < VW; ++v) {
             // one byte of two neighbouring tokens' codes of the same column
             uint32_t even[2], odd[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t x = w[2 * h][v], y = w[2 * h + 1][v];
+              const uint32_t x = w[gr][2 * h][v], y = w[gr][2 * h + 1][v];
               even[h] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
               odd[h] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
             }
@@ -796,46 +879,46 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             product(std::integral_constant<int, 2>{});
             product(std::integral_constant<int, 3>{});
           }
-        } else {
-          uint32_t pf[NB][2];
-          const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        }
+        for (; apart; apart &= apart - 1) {
+          const int loc = __ffs(apart) - 1, tk = warp * ST + loc, src = 4 * row_of_tok<D>(loc & 7) + c;
+          const uint8_t* at = smem + s * C::STAGE;
+          const int b = at[2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D)];
+          if (b != 255 && b >= E - kSpread) at = nullptr;     // of this thread's block it is in the product, or zero
+          const float unit = b == 255 ? __uint_as_float(0x7FC00000u) : pow2i(min(b - E + kUp, 127));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            pf[nb][0] = transposed(bf16x2(wt[nb][0], wt[nb][1]));
-            pf[nb][1] = transposed(bf16x2(wt[nb][2], wt[nb][3]));
-            mma_16816(ol[nb], ones, pf[nb][0], pf[nb][1]);
-          }
-          float fac[4];
+            uint32_t x = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            fac[e] = by[e] != 255u ? pow2i(min((int)by[e] - E, 127))
-                     : (some >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u ? 0.f : __uint_as_float(0x7FC00000u);
+            for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
-          for (int v = 0; v < VW; ++v)
+              for (int h = 0; h < 2; ++h)
+                if (loc >> 3 == 2 * gr + h) x = wt[gr][nb][h];
+            x = __shfl_sync(0xffffffffu, x, src);
+            if (!at) continue;
+            bool see[2];
+            float p2[2] = {f16_lo(x) * unit, f16_hi(x) * unit};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              uint32_t x[4];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                // columns 2b and 2b + 1 of either token
-                const uint32_t u = e2m1_pair<0>(w[2 * h][v] >> (8 * b)), y = e2m1_pair<0>(w[2 * h + 1][v] >> (8 * b));
-                x[2 * h] = bf16x2(f16_lo(u) * fac[2 * h], f16_lo(y) * fac[2 * h + 1]);
-                x[2 * h + 1] = bf16x2(f16_hi(u) * fac[2 * h], f16_hi(y) * fac[2 * h + 1]);
-              }
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma_16816(o[nb][4 * v + b], x, pf[nb][0], pf[nb][1]);
+            for (int e = 0; e < 2; ++e) {
+              const int rho = 8 * nb + 2 * c + e;
+              see[e] = Visible(rho < R ? it.pos0 + rho / G : -1, p.a.window, p.a.sinks).sees(tok0 + loc);
             }
-        }
-        for (; nan; nan &= nan - 1) {
-          const int t = tok0 + __ffs(nan) - 1;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+            for (int v = 0; v < VW; ++v) {
+              const uint32_t codes = *reinterpret_cast<const uint32_t*>(
+                  at + C::KV + kv_addr<C>(0, tk, D == 128 ? g >> 1 : g >> 2) + (D == 128 ? 8 * (g & 1) + 4 * v : 4 * (g & 3)));
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (t <= pos[nb][e] && (t >= first[nb][e] || t < p.a.sinks)) {
+              for (int j = 0; j < 4; ++j) {
+                const float lo = e2m1((codes >> (8 * j)) & 15u), hi = e2m1((codes >> (8 * j + 4)) & 15u);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) o[nb][j][e] = o[nb][j][2 + e] = __uint_as_float(0x7FC00000u);
+                for (int e = 0; e < 2; ++e)
+                  if (see[e]) {
+                    o[nb][4 * v + j][e] = fmaf(p2[e], lo, o[nb][4 * v + j][e]);
+                    o[nb][4 * v + j][2 + e] = fmaf(p2[e], hi, o[nb][4 * v + j][2 + e]);
+                  }
               }
+            }
+          }
         }
       }
       __syncwarp();
@@ -843,75 +926,69 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     }
 
     // ---------------- the warps' parts joined, in the order of their tokens ----------------
-    // sums are the same in all lanes of a column; kLift out of them and of the outputs
+    // sums are the same in all lanes of a column; kFewLift out of them and of the outputs
     const float unlift = pow2i(-(int)kFewLift);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (g == 0) sums[warp][8 * nb + 2 * c + e] = make_float2(m[nb][e], ol[nb][e] * unlift);
-      }
+      for (int e = 0; e < 2; ++e)
+        if (g == 0)
+          sums[(n & 1) * C::WARPS + warp][8 * nb + 2 * c + e] = make_float2(ol[nb][e] == 0.f ? -INFINITY : kFewLift - off[nb][e], ol[nb][e] * unlift);
     const int piece = it.piece, pieces = it.pieces, hk = it.hk;
     const long long b = it.b;
     const bool more = load_q(n + 1);              // on their way while this item ends
     stop = consumers_any<C::WARPS>(!more || *abort);
-    const float unit = E < 0 ? 1.f : pow2i(E - 127 - (int)kFewLift);
+    const float unit = pow2i(E - 127 - kUp - (int)kFewLift);
+    auto total = [&](int rho, float& top) {
+      top = -INFINITY;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float top[2], tl[2];
+      for (int w = 0; w < C::WARPS; ++w) top = fmaxf(top, sums[(n & 1) * C::WARPS + w][rho].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      float tl = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::WARPS; ++w) tl += ex2(sums[(n & 1) * C::WARPS + w][rho].x - base) * sums[(n & 1) * C::WARPS + w][rho].y;
+      return tl;
+    };
+    float* mine = join + warp * (8 * NB * C::PITCH);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rho = 8 * nb + 2 * c + e;
-        top[e] = -INFINITY, tl[e] = 0.f;
+        float top;
+        total(rho, top);
+        // a warp without weights has zeros here, or what values that are not numbers made of them
+        const float f = ex2((ol[nb][e] == 0.f ? 0.f : kFewLift - off[nb][e] - (top == -INFINITY ? 0.f : top)));
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) top[e] = fmaxf(top[e], sums[w][rho].x);
-        const float base = top[e] == -INFINITY ? 0.f : top[e];
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) tl[e] += ex2(sums[w][rho].x - base) * sums[w][rho].y;
-        const float f = ex2(m[nb][e] - base);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) o[nb][j][e] = o[nb][j][e] * unit * f, o[nb][j][2 + e] = o[nb][j][2 + e] * unit * f;
+        for (int j = 0; j < MT; j += 2)           // of products j and j + 1 four columns in a row
+          *reinterpret_cast<float4*>(mine + rho * C::PITCH + g * (D / 8) + 2 * j) =
+              make_float4(o[nb][j][e] * unit * f, o[nb][j][2 + e] * unit * f, o[nb][j + 1][e] * unit * f, o[nb][j + 1][2 + e] * unit * f);
       }
-      // ((0 + 2) + (1 + 3)): the upper two warps hand theirs to the lower two, those one to the other
+    named_bar_sync(1, C::WARPS * 32);
+    if (!*abort) {
+      const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
+      const bool one = pieces == 1;
+      const int tid = warp * 32 + lane, rho = tid % (8 * NB);
+      if (rho < R) {
+        float top;
+        const float tl = total(rho, top);
+        const int r = rho / G;
+        const float inv = !one ? 1.f : tl == 0.f ? no_weights(p, b, it.pos0 + r) : 1.f / tl;
+        uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
+        for (int d4 = tid / (8 * NB); d4 < D / 4; d4 += C::WARPS * 32 / (8 * NB)) {
+          const float* x = join + rho * C::PITCH + 4 * d4;
+          float4 v[C::WARPS];
 #pragma unroll
-      for (int far = 2; far; far >>= 1) {
-        float4* mine = reinterpret_cast<float4*>(join) + (warp & (far - 1)) * MT * 32 + lane;
-        if (warp >= far && warp < 2 * far) {
-#pragma unroll
-          for (int j = 0; j < MT; ++j) mine[j * 32] = make_float4(o[nb][j][0], o[nb][j][1], o[nb][j][2], o[nb][j][3]);
+          for (int w = 0; w < C::WARPS; ++w) v[w] = *reinterpret_cast<const float4*>(x + w * (8 * NB * C::PITCH));
+          float y[4] = {(v[0].x + v[2].x) + (v[1].x + v[3].x), (v[0].y + v[2].y) + (v[1].y + v[3].y),
+                        (v[0].z + v[2].z) + (v[1].z + v[3].z), (v[0].w + v[2].w) + (v[1].w + v[3].w)};
+          if (one) *reinterpret_cast<uint2*>(out + 4 * d4) = make_uint2(bf16x2(y[0] * inv, y[1] * inv), bf16x2(y[2] * inv, y[3] * inv));
+          else *reinterpret_cast<float4*>(part_of(p, at, D, rho, d4)) = make_float4(y[0], y[1], y[2], y[3]);
         }
-        named_bar_sync(1, C::WARPS * 32);
-        if (warp < far) {
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            const float4 v = mine[j * 32];
-            o[nb][j][0] += v.x, o[nb][j][1] += v.y, o[nb][j][2] += v.z, o[nb][j][3] += v.w;
-          }
-        }
-        named_bar_sync(1, C::WARPS * 32);
-      }
-      if (warp == 0 && !*abort) {
-        const long long at = (b * p.a.Hkv + hk) * p.max_pieces + piece;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rho = 8 * nb + 2 * c + e;
-          if (rho >= R) continue;
-          const bool one = pieces == 1;
-          const int r = rho / G;
-          const float inv = !one ? 1.f : tl[e] == 0.f ? no_weights(p, b, pos[nb][e]) : 1.f / tl[e];
-          uint16_t* out = p.out + ((b * p.rows + r) * p.a.Hq + hk * G + rho - r * G) * D;
-#pragma unroll
-          for (int j = 0; j < MT; j += 2) {
-            // of products j and j + 1 four columns in a row
-            const int d = g * (D / 8) + 2 * j;
-            const float v[4] = {o[nb][j][e] * inv, o[nb][j][2 + e] * inv, o[nb][j + 1][e] * inv, o[nb][j + 1][2 + e] * inv};
-            if (one) *reinterpret_cast<uint2*>(out + d) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-            else *reinterpret_cast<float4*>(part_of(p, at, D, rho, d / 4)) = make_float4(v[0], v[1], v[2], v[3]);
-          }
-          if (!one && g == 0) *sums_of(p, at, rho) = make_float2(top[e], tl[e]);
-        }
+        if (!one && tid < 8 * NB) *sums_of(p, at, rho) = make_float2(top, tl);
       }
     }
+    __syncwarp();
     if (lane == 0) mbar_arrive(&w_empty[n & 1]);
   }
 }
@@ -930,11 +1007,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], w_full[2], w_empty[2];
   __shared__ uint32_t page_mask[C::STAGES];
+  __shared__ int4 infos[C::BITS == 4 ? C::STAGES : 1];   // of a stage: first token, pages there, kinds
   __shared__ FewItem items[2];
-  __shared__ float2 sums[C::WARPS][16];         // the warps' maximum (times log2 e) and sum of a row
+  __shared__ float2 sums[C::WARPS * (C::BITS == 4 ? 2 : 1)][16];   // the warps' maximum (times log2 e) and sum of a row
   __shared__ volatile uint32_t abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* join = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+  uint8_t* queries = smem + C::STAGES * C::STAGE + C::JOIN;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int G = p.G, R = p.R;
@@ -954,13 +1033,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int in_tile = p.page_size >= kTileTok ? 1 : kTileTok >> p.page_log2;     // pages of a step
+  const int in_tile = p.page_size >= C::TILE ? 1 : C::TILE >> p.page_log2;     // pages of a step
 
   if (warp == C::WARPS) {
     // ---------------- items and loads ----------------
-    const int rows_of = min(p.page_size, kTileTok);
+    const int rows_of = min(p.page_size, C::TILE);
     int n = 0, issued = 0;
-    bool ok = true;
+    bool ok = true, told = false;
     ItemWalk walk;
     for (long long idx = blockIdx.x; ok; idx += gridDim.x) {
       const int who = walk.lane_of(p, idx);
@@ -986,16 +1065,27 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         items[n & 1] = mine;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&w_full[n & 1]);
-      if (who < 0) break;
       const FewItem it = items[n & 1];
+      if constexpr (C::BITS == 4) {
+        if (lane == 0) {
+          if (who < 0) mbar_arrive(&w_full[n & 1]);
+          else mbar_arrive_expect_tx(&w_full[n & 1], R * D * 2);
+        }
+        __syncwarp();
+        if (who >= 0 && lane < p.rows)
+          bulk_load(queries + (n & 1) * C::QBUF + lane * G * D * 2,
+                    p.q + ((long long)it.b * p.rows + lane) * p.q_stride + (long long)it.hk * G * D, G * D * 2, &w_full[n & 1]);
+      } else {
+        if (lane == 0) mbar_arrive(&w_full[n & 1]);
+      }
+      if ((told = who < 0)) break;
       ++n;
       const int32_t* table = p.table + (long long)it.b * p.table_width;
       const int last_page = it.pmax >> p.page_log2;
       int base = -1000, ids = 0, next = 0;   // 32 table entries from `base` on, and the 32 behind them
       for (int i = 0; i < it.cnt; ++i, ++issued) {
         const int s = issued % C::STAGES;
-        const int tok0 = it.tok(i), page0 = tok0 >> p.page_log2;
+        const int tok0 = it.tok(i, C::TILE), page0 = tok0 >> p.page_log2;
         if (page0 < base || page0 + in_tile > base + 32) {
           // in_tile divides 32: a step's pages lie in one group of 32 entries
           const int nb = page0 & ~31;
@@ -1015,7 +1105,14 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
             !(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], (issued / C::STAGES - 1) & 1, kPagedWaitNs, &abort_flag,
                                                     DEV_TIMEOUT_EMPTY))))
           break;
+        uint32_t kinds = 0;                      // of MXFP4's warps: every row sees every token; some row may see one
+        if constexpr (C::BITS == 4) {
+          const int t = tok0 + (lane % C::WARPS) * C::ST;
+          const bool whole = t + C::ST - 1 <= it.pmin && (t >= it.first_all || t + C::ST <= p.a.sinks) && mask == (1u << in_tile) - 1u;
+          kinds = __ballot_sync(0xffffffffu, lane < C::WARPS ? whole : t <= it.pmax);
+        }
         if (lane == 0) {
+          if constexpr (C::BITS == 4) infos[s] = make_int4(tok0, (int)mask, (int)kinds, 0);
           page_mask[s] = mask;
           mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * C::BITS / 8 + (C::MX ? 2 * D / 32 : 0)) +
                                               (issued == p.hold ? 16 : 0));
@@ -1026,7 +1123,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
           uint8_t* st = smem + s * C::STAGE;
 #pragma unroll
           for (int h = 0; h < C::HALVES; ++h) {
-            const uint32_t at = h * kTileTok * C::ROWB + lane * rows_of * C::ROWB;
+            const uint32_t at = h * C::TILE * C::ROWB + lane * rows_of * C::ROWB;
             tma_load_2d(st + at, &kmap, h * 64, row, &full[s]);
             tma_load_2d(st + C::KV + at, &vmap, h * 64, row, &full[s]);
           }
@@ -1040,16 +1137,20 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
       }
     }
     // copies in flight end before the block does, whoever gives up and when
-    if (lane == 0)
+    if (lane == 0) {
       for (int j = max(0, issued - C::STAGES); j < issued; ++j)
         mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+      // queries of the last two items, or of the last one where the end has been told in the other one's place
+      for (int j = C::BITS == 4 ? max(0, n - (told ? 1 : 2)) : n; j < n; ++j)
+        mbar_wait(&w_full[j & 1], (j >> 1) & 1, kPagedWaitNs, nullptr, nullptr, DEV_TIMEOUT_DRAIN);
+    }
     record_end(p, &abort_flag);
     return;
   }
 
   // ---------------- consumers ----------------
   if constexpr (C::FMT == MOE_KV_MXFP4) {
-    consume_four<C>(p, smem, join, full, empty, w_full, w_empty, page_mask, items, sums, &abort_flag, warp, lane);
+    consume_four<C>(p, smem, join, queries, full, empty, w_full, w_empty, infos, items, sums, &abort_flag, warp, lane);
     record_end(p, &abort_flag);
     return;
   } else if constexpr (C::EIGHT) {
@@ -1466,14 +1567,14 @@ __global__ void __launch_bounds__(kJoinRows * kJoinCols) paged_join_kernel(const
 // Positions are 32 bits wide, and steps are rounded up to 128 tokens behind the last one.
 constexpr int kMaxLen = 0x7fffffff - 255;
 
-// Blocks of up to 16 rows take steps of 64 tokens, more rows steps of 128.
-static int tile_of(const moe_attention* a, int rows) {
-  return rows * (a->Hq / a->Hkv) <= kFewRows ? kTileTok : 2 * kTileTok;
+// Blocks of up to 16 rows take steps of 64 tokens, more rows, and MXFP4, steps of 128.
+static int tile_of(const moe_attention* a, int rows, bool four) {
+  return !four && rows * (a->Hq / a->Hkv) <= kFewRows ? kTileTok : 2 * kTileTok;
 }
 
 // The most pieces a sequence of up to max_len tokens can have.
-static int max_pieces_of(const moe_attention* a, int rows, int max_len) {
-  const int tile = tile_of(a, rows);
+static int max_pieces_of(const moe_attention* a, int rows, int max_len, bool four) {
+  const int tile = tile_of(a, rows, four);
   long long tiles = ((long long)max_len + tile - 1) / tile;
   if (a->window) {
     const long long sinks = ((long long)a->sinks + tile - 1) / tile;
@@ -1485,15 +1586,16 @@ static int max_pieces_of(const moe_attention* a, int rows, int max_len) {
   return most;
 }
 
+// A workspace serves every format.
 static size_t part_rows(const moe_attention* a, int rows, int max_len) {
-  const int pieces = max_pieces_of(a, rows, max_len);
+  const int pieces = std::max(max_pieces_of(a, rows, max_len, false), max_pieces_of(a, rows, max_len, true));
   return pieces == 1 ? 0 : (size_t)a->B * a->Hq * rows * pieces;
 }
 
 template <class C>
 static int launch_cfg(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
   CUtensorMap km, vm;
-  const int box = std::min(cache->page_size, kTileTok);
+  const int box = std::min(cache->page_size, C::TILE);
   const CUtensorMapSwizzle swizzle = C::ROWB == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                                      : C::ROWB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                      : CU_TENSOR_MAP_SWIZZLE_128B;
@@ -1517,7 +1619,7 @@ static int launch_few(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_
 static int launch_paged(const PagedArgs& p, const moe_kv_cache* cache, cudaStream_t st) {
   const bool d64 = p.a.D == 64;
   int rc;
-  if (p.tile_log2 != 6) rc = launch_paged_tc(p, cache, st);
+  if (p.R > kFewRows) rc = launch_paged_tc(p, cache, st);
   else if (p.R <= 8) rc = d64 ? launch_few<64, true>(p, cache, st) : launch_few<128, true>(p, cache, st);
   else rc = d64 ? launch_few<64, false>(p, cache, st) : launch_few<128, false>(p, cache, st);
   if (rc || p.max_pieces == 1) return rc;
@@ -1576,10 +1678,11 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.table_width = table_width;
   p.G = a->Hq / a->Hkv;
   p.R = rows * p.G;
-  p.tile_log2 = tile_of(a, rows) == kTileTok ? 6 : 7;
-  p.block_log2 = p.tile_log2 == 6 ? 4 : 7;
+  const bool four = cache->format == MOE_KV_MXFP4;
+  p.tile_log2 = tile_of(a, rows, four) == kTileTok ? 6 : 7;
+  p.block_log2 = p.R <= kFewRows ? 4 : 7;
   p.mblocks = ceil_div(p.R, 1 << p.block_log2);
-  p.max_pieces = max_pieces_of(a, rows, max_len);
+  p.max_pieces = max_pieces_of(a, rows, max_len, four);
   // grids and the numbers of pieces stay below 2^31
   if ((int64_t)a->B * a->Hkv * std::max((int64_t)p.mblocks * p.max_pieces, (int64_t)ceil_div(p.R, kJoinRows)) >= (int64_t)1 << 31)
     return MOE_ERR_UNSUPPORTED_SHAPE;
