@@ -511,7 +511,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
                                              uint64_t* w_full, uint64_t* w_empty, const int4* infos,
                                              const FewItem* items, float2 (*sums)[16], volatile uint32_t* abort, int warp,
                                              int lane) {
-  constexpr int D = C::D, ST = C::ST, GR = ST / 16, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
+  constexpr int D = C::D, ST = C::ST, GR = 1, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
   const int g = lane >> 2, c = lane & 3, G = p.G, R = p.R;
   const int page_log2 = min(p.page_log2, 7);
   const float scale = p.a.scale * 1.4426950408889634f;
@@ -602,7 +602,10 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
       const int4 info = infos[s];
       const uint32_t st = smem_u32(smem) + s * C::STAGE;
       const bool whole = (info.z >> warp) & 1;  // every row of the block sees every token of this warp
-      if ((info.z >> (C::WARPS + warp)) & 1) {
+      // 16 tokens at a time, in little code: the instruction cache is what more in a turn is short of
+#pragma unroll 1
+      for (int part = 0; part < ST / 16 && ((info.z >> (C::WARPS + warp)) & 1); ++part) {
+        const uint32_t codes_at = st + part * 16 * C::ROWB, scales_at = st + part * 16 * (D / 32);
         // ---- scores ----
         float sc[GR][NB][4];
         bool bad = false;                       // a block's scale is NaN
@@ -611,13 +614,13 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           uint32_t sw[2], w[2][D / 32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t at = st + ks_lane + (8 * h + 16 * gr) * (D / 32);
+            const uint32_t at = scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32);
             if constexpr (D == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw[h]) : "r"(at) : "memory");
             else asm volatile("{\n\t.reg .b16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(sw[h]) : "r"(at) : "memory");
             bad = bad || ((~sw[h] - 0x01010101u) & sw[h] & 0x80808080u) != 0;
 #pragma unroll
             for (int bl = 0; bl < D / 32; ++bl)
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((st + k_lane) ^ (bl << 4)) + (8 * h + 16 * gr) * C::ROWB) : "memory");
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((codes_at + k_lane) ^ (bl << 4)) + (8 * h + 16 * gr) * C::ROWB) : "memory");
           }
 #pragma unroll
           for (int bl = 0; bl < D / 32; ++bl) {
@@ -646,12 +649,12 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             uint32_t b[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t at = st + v_lane[e] + (8 * h + 16 * gr) * C::ROWB;
+              const uint32_t at = codes_at + v_lane[e] + (8 * h + 16 * gr) * C::ROWB;
               if constexpr (D == 128)
                 asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[gr][2 * h + e][0]), "=r"(w[gr][2 * h + e][1]) : "r"(at) : "memory");
               else
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[gr][2 * h + e][0]) : "r"(at) : "memory");
-              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[e]) : "r"(st + vs_lane[e] + (8 * h + 16 * gr) * (D / 32)) : "memory");
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[e]) : "r"(scales_at + vs_lane[e] + (8 * h + 16 * gr) * (D / 32)) : "memory");
             }
             by[gr][h] = b[0] | b[1] << 16;
           }
@@ -668,7 +671,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 
         // ---- what the rows do not see ----
         uint32_t hidden = 0;                    // of t
-        const int tok0 = info.x + warp * ST;
+        const int loc0 = warp * ST + part * 16, tok0 = info.x + loc0;
         if (!whole) {
           const uint32_t mask = (uint32_t)info.y;
 #pragma unroll
@@ -682,7 +685,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const int loc = tg + 8 * h + 16 * gr;
-                  const bool there = (mask >> ((warp * ST + loc) >> page_log2)) & 1u;
+                  const bool there = (mask >> ((loc0 + loc) >> page_log2)) & 1u;
                   if (!there || !see.sees(tok0 + loc)) {
                     t[gr][nb][2 * h + e] = -INFINITY;
                     hidden |= 1u << (4 * (gr * NB + nb) + 2 * h + e);
@@ -690,7 +693,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
                 }
             }
           const int tt = tok0 + lane;
-          const bool any = ((mask >> ((warp * ST + lane) >> page_log2)) & 1u) && tt <= it.pmax && (tt >= it.first_any || tt < p.a.sinks);
+          const bool any = lane < 16 && ((mask >> ((loc0 + lane) >> page_log2)) & 1u) && tt <= it.pmax && (tt >= it.first_any || tt < p.a.sinks);
           const uint32_t drop = __ballot_sync(0xffffffffu, !any);
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr)
@@ -740,7 +743,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t at = st + ks_lane + (8 * h + 16 * gr) * (D / 32);
+                const uint32_t at = scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32);
                 bool is = false;
                 for (int b = 0; b < D / 32; ++b) {
                   uint32_t x;
@@ -881,7 +884,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           }
         }
         for (; apart; apart &= apart - 1) {
-          const int loc = __ffs(apart) - 1, tk = warp * ST + loc, src = 4 * row_of_tok<D>(loc & 7) + c;
+          const int loc = __ffs(apart) - 1, tk = loc0 + loc, src = 4 * row_of_tok<D>(loc & 7) + c;
           const uint8_t* at = smem + s * C::STAGE;
           const int b = at[2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D)];
           if (b != 255 && b >= E - kSpread) at = nullptr;     // of this thread's block it is in the product, or zero
