@@ -485,7 +485,7 @@ def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[
 def _current(t: torch.Tensor, name: str) -> int:
     """t's device, which has to be the current one (launches go there)."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device")
     return dev
 
@@ -740,11 +740,12 @@ def moe_rope(rotary: Rotary, q, k, pos, inverse: bool = False, q_out=None, k_out
     elif k_out is not None:
         raise ValueError("k_out is not written without k")
     pp = _positions(rotary, pos, T, dev)
-    with _allocating(stream):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device)
+    if q_out is None or (k_out is None and k is not None):
+        with _allocating(stream):
+            if q_out is None:
+                q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            if k_out is None and k is not None:
+                k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device)
     pqo, sqo = _out_rows(q_out, "q_out", q, pq, sq, dev)
     if k is not None:
         pko, sko = _out_rows(k_out, "k_out", k, pk, sk, dev)

@@ -49,10 +49,7 @@ __device__ __forceinline__ float2* sums_of(const PagedArgs& p, long long at, int
 // elements take 11 us for one sequence and 240 us for 256 in pieces of 8 steps, 19 us and 215 us in one piece; four rows of
 // 1024 tokens take 13 us and 257 us in pieces of 4 steps of 128, 17 us and 198 us in one of 8. The small call counts here.
 __host__ __device__ inline int piece_count(int tile_log2, int tiles) {
-#ifndef PLOG
-#define PLOG 2
-#endif
-  const int log2 = tile_log2 == 6 || tiles >= 64 ? PLOG + 1 : PLOG;      // of the steps
+  const int log2 = tile_log2 == 6 || tiles >= 64 ? 3 : 2;      // of the steps
   return min(max((tiles + (1 << log2 >> 1)) >> log2, 1), tile_log2 == 6 ? 64 : 32);
 }
 
