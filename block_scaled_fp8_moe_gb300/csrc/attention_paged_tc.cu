@@ -427,7 +427,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
             const uint8_t* scales = src + kStepTok * C::ROWB;
             constexpr int CH = D / 32, RPT = 128 / CH;
             const int bl = tid / 32 % CH, row0 = tid / (32 * CH) * 32 + lane;
-#pragma unroll 1
+#pragma unroll 4
             for (int r = row0; r < kStepTok; r += RPT) {
               uint32_t w[4], o[16];
               const uint32_t at = D == 128 ? r * 64 + ((bl ^ ((r >> 1) & 3)) << 4) : r * 32 + ((bl ^ ((r >> 2) & 1)) << 4);
