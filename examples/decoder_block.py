@@ -1,12 +1,12 @@
 """One decoder block of a serving step around the routed-expert layer, prompt and decode:
 
-  norm (residual added)  ->  q, k, v projections  ->  cache append  ->  attention  ->  output projection
+  norm (residual added)  ->  q, k, v projections  ->  positions, cache append  ->  attention  ->  output projection
   norm (residual added, MXFP8 rows)  ->  router  ->  experts  ->  combine
 
 Projections are plain matrix products; everything else is this package's. Run it for a prompt of ragged sequences and a few
 decode steps of verification rows each:
 
-    python examples/decoder_block.py [--mxfp8-cache] [--window 128 --sinks 4]
+    python examples/decoder_block.py [--mxfp8-cache | --mxfp4-cache] [--rope] [--window 128 --sinks 4]
 """
 from __future__ import annotations
 
@@ -40,7 +40,8 @@ class PageTable:
 
 
 class DecoderBlock:
-    def __init__(self, hidden, heads, heads_kv, dim, experts, top_k, inter, window=0, sinks=0, seed=0):
+    def __init__(self, hidden, heads, heads_kv, dim, experts, top_k, inter, window=0, sinks=0, seed=0, rotary=None):
+        self.rotary = rotary                    # a B.Rotary; None: a block without positions
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, std=0.02):
@@ -53,12 +54,16 @@ class DecoderBlock:
         self.moe = B.MoeLayer.from_fp32(normal(experts, hidden).bfloat16(), normal(experts, std=0.1),
                                         normal(experts, 2 * inter, hidden), normal(experts, hidden, inter), top_k)
 
-    def _attention(self, x, residual, cache, slots, attend):
-        """Norm, projections, cache and attention of rows x [T, hidden]; `attend(q, k, v)` is the attention itself."""
+    def _attention(self, x, residual, cache, slots, attend, pos=None, keys=False):
+        """Norm, projections, cache and attention of rows x [T, hidden] at positions pos (where the block has positions);
+        `attend(q, k, v)` is the attention itself, and `keys` says whether it reads k."""
         y, residual, _, _ = B.moe_add_rmsnorm_mxfp8(x, self.norm1, residual, quant=False)
         qkv = (y @ self.w_qkv).view(x.shape[0], -1, self.dim)
         q, k, v = qkv.split((self.heads, self.heads_kv, self.heads_kv), dim=1)
-        B.moe_kv_append(cache, k, v, slots)
+        if self.rotary is None:
+            B.moe_kv_append(cache, k, v, slots)
+        else:                                   # turned where they are
+            B.moe_rope_kv_append(self.rotary, cache, q, k, v, pos, slots, q_out=q, k_out=k if keys else None)
         return attend(q, k, v).view(x.shape[0], -1) @ self.w_out, residual
 
     def _experts(self, x, residual, dead=None):
@@ -70,12 +75,12 @@ class DecoderBlock:
         _, _, rows = B.moe_experts_grouped(shp, q, s, self.moe.w13p, self.moe.w13sp, self.moe.w2p, self.moe.w2sp, plan, ws)
         return B.moe_combine(shp, rows, plan, ws, dead=dead), residual
 
-    def prompt(self, x, residual, cache, slots, cu):
+    def prompt(self, x, residual, cache, slots, cu, pos=None):
         """Whole prompts, packed one behind the other (bounds cu). Returns the block's output and the residual."""
         attend = lambda q, k, v: B.moe_prefill_attention(q, k, v, cu, window=self.window, sinks=self.sinks)  # noqa: E731
-        return self._experts(*self._attention(x, residual, cache, slots, attend))
+        return self._experts(*self._attention(x, residual, cache, slots, attend, pos, keys=True))
 
-    def decode(self, x, residual, cache, slots, pages: PageTable, dead=None):
+    def decode(self, x, residual, cache, slots, pages: PageTable, dead=None, pos=None):
         """The newest rows of every sequence: x [sequences * rows, hidden]; pages.lens counts them already. Dead rows have
         slot -1 and take no expert."""
         seqs = pages.lens.numel()
@@ -83,7 +88,7 @@ class DecoderBlock:
         def attend(q, k, v):
             return B.moe_paged_attention(q.view(seqs, -1, self.heads, self.dim), cache, pages.table, pages.lens,
                                          pages.max_len, window=self.window, sinks=self.sinks)
-        return self._experts(*self._attention(x, residual, cache, slots, attend), dead=dead)
+        return self._experts(*self._attention(x, residual, cache, slots, attend, pos), dead=dead)
 
 
 def run(prompt_lens, rows, steps, block, cache, hidden, seed=0, on_step=None):
@@ -95,7 +100,7 @@ def run(prompt_lens, rows, steps, block, cache, hidden, seed=0, on_step=None):
     seq = torch.repeat_interleave(torch.arange(n, device="cuda"), torch.tensor(prompt_lens, device="cuda"))
     pos = torch.cat([torch.arange(m, device="cuda") for m in prompt_lens])
     x = torch.randn(sum(prompt_lens), hidden, generator=g, device="cuda").bfloat16()
-    out, _ = block.prompt(x, None, cache, pages.slots(seq, pos), cu)
+    out, _ = block.prompt(x, None, cache, pages.slots(seq, pos), cu, pos=pos.int())
     pages.lens += torch.tensor(prompt_lens, dtype=torch.int32, device="cuda")
     outs = [out]
     seq = torch.repeat_interleave(torch.arange(n, device="cuda"), rows)
@@ -103,7 +108,7 @@ def run(prompt_lens, rows, steps, block, cache, hidden, seed=0, on_step=None):
         pages.lens += rows
         pos = (pages.lens[:, None] - rows + torch.arange(rows, device="cuda")).flatten()
         x = torch.randn(n * rows, hidden, generator=g, device="cuda").bfloat16()
-        out, _ = block.decode(x, None, cache, pages.slots(seq, pos), pages)
+        out, _ = block.decode(x, None, cache, pages.slots(seq, pos), pages, pos=pos.int())
         outs.append(out)
         if on_step:
             on_step(step, pages)
@@ -115,14 +120,17 @@ def run(prompt_lens, rows, steps, block, cache, hidden, seed=0, on_step=None):
 def main():
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--mxfp8-cache", action="store_true")
+    p.add_argument("--mxfp4-cache", action="store_true")
+    p.add_argument("--rope", action="store_true", help="rotary positions")
     p.add_argument("--window", type=int, default=0)
     p.add_argument("--sinks", type=int, default=0)
     p.add_argument("--rows", type=int, default=6)
     p.add_argument("--steps", type=int, default=8)
     a = p.parse_args()
     hidden, heads, heads_kv, dim = 4096, 32, 8, 128
-    block = DecoderBlock(hidden, heads, heads_kv, dim, 64, 8, 576, a.window, a.sinks)
-    cache = B.KvCache.empty(512, 16, heads_kv, dim, mxfp8=a.mxfp8_cache)
+    rotary = B.Rotary([10000.0 ** (-i / (dim // 2)) for i in range(dim // 2)]) if a.rope else None
+    block = DecoderBlock(hidden, heads, heads_kv, dim, 64, 8, 576, a.window, a.sinks, rotary=rotary)
+    cache = B.KvCache.empty(512, 16, heads_kv, dim, mxfp8=a.mxfp8_cache, mxfp4=a.mxfp4_cache)
     lens = [700, 31, 1, 1200]
     stamps = []
     run(lens, a.rows, 2, block, cache, hidden)          # once for allocations
