@@ -2,20 +2,27 @@
 // speculative decoding), cut into pieces along the cache and joined.
 //
 // Bound: HBM. Every visible key and value is read once for all rows and all heads of a group; per key and kv head that
-// is 4 D bytes (bf16) or 2.06 D (MXFP8) against 4 D R flops, R = rows * Hq / Hkv: far above what CUDA cores do at full
+// is 4 D bytes (bf16), 2.06 D (MXFP8) or 1.06 D (MXFP4) against 4 D R flops, R = rows * Hq / Hkv: far above what CUDA cores do at full
 // bandwidth (R = 8 would need 54 of their ~75 TFLOP/s), so both products run on the tensor cores. This file's kernel takes
-// up to 16 rows, with m16n8k16: up to 8 rows as its columns, more as its M (a tcgen05 product has at least 64 rows); above 16
-// they go to attention_paged_tc.cu. Pieces of both are joined here.
+// up to 16 rows, with m16n8k16: up to 8 rows as its columns, more as its M (a tcgen05 product has at least 64 rows), or over
+// MXFP4 as more columns; above 16 they go to attention_paged_tc.cu. Pieces of both are joined here.
 //
 // Resident blocks (two to four a multiprocessor) take item after item, one piece of one (sequence, kv head): a producer warp
-// streams pages by TMA through a ring of 64-token stages and runs ahead into the next item, four warps consume it, 16 tokens
-// of a stage each. Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
+// streams pages by TMA through a ring of 64-token stages (128 over MXFP4) and runs ahead into the next item, four warps consume
+// it, 16 tokens of a stage each (32). Every warp keeps its own running maximum, sum and output, so that nothing but the ring's barriers is shared
 // until an item's end.
 //
 // One row of 32 heads over 8 kv heads of 128, four sequences of up to 128k bf16 tokens: 201 us, 6.2 TB/s. 160 rows of 64
 // heads over 8 of 64, a window of 1024 and 4 first tokens: 63 us, 5.4 TB/s (17 steps a row leave an item little to run
 // ahead of). 256 rows over 4096 MXFP8 tokens: 445 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
 // rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
+//
+// Over MXFP4 a key brings so few bytes that its instructions count: about 530 a warp for 32 keys and 8 rows, 260 of them conversion
+// and products. One row of 32 heads over 8 of 128: four sequences of up to 128k tokens 96 us (3.6 TB/s), 256 of up to 4096 220 us
+// (3.2 TB/s; 1,024 to 4,096 tokens are 2 to 8 pieces of 4 steps, of 10,000 cycles each, and 4,500 from one to the next: the
+// next queries 950, waiting for the slowest warp 1,300, the join and its output 2,100). 31 sequences of 16 rows to a head 53 us,
+// 160 rows under a window of 1024 57 us. tcgen05 with the codes as they are (keys as M, values converted to E4M3 in shared memory,
+// weights and queries as two E4M3 values each) takes 278, 127, 72 and 130 us for these.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -54,7 +61,9 @@ struct PagedCfg {
   static constexpr bool MX = FMT_ != MOE_KV_BF16, EIGHT = EIGHT_;  // EIGHT: up to 8 rows, as a product's columns
   // Blocks of a multiprocessor. Up to 16 rows take 168 registers, up to 8 rows 128 or less. Measured with 2, 3 and 4 blocks:
   // 256 sequences of 4096 tokens, 32 heads over 8 of 128, MXFP8 651 (16 rows' code), 441, 456 us; 64 over 8 of 64, MXFP8
-  // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us.
+  // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us, MXFP4 with 3, 4 and
+  // 5 blocks 63, 55, 61 us; 256 sequences, 32 over 8 of 128, MXFP4 with 2, 3 and 4 blocks 221, 231, 280 us, but four of 128k tokens
+  // 99, 96, 101 us; 16 rows over MXFP4 with 1 and 2 blocks 64, 55 us.
   static constexpr int CTAS = !EIGHT ? 2 : MX && D == 64 ? 4 : 3;
   static constexpr int TILE = BITS == 4 ? 2 * kTileTok : kTileTok;
   static constexpr int WARPS = 4, ST = TILE / WARPS;               // tokens of a stage that a warp takes
@@ -457,7 +466,7 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 //  - a query is scaled to less than 2 by a power of two of its row: what is 2^-17 of the largest or more keeps all of bf16's
 //    digits, the rest is rounded to 2^-25 of it, as fp32 sums would; a block's scale is put on its 32 products' sum, in fp32;
 //  - weights are 2^kFewLift times themselves, at most 2^kFewGrow more (the maximum that they refer to moves when outgrown by
-//    that): weights below 2^-25 - kFewLift of the largest become zero, 2^17 tokens of them 2^-15 of the result;
+//    that), so that weights below 2^-30 of the largest become zero, 2^17 tokens of them 2^-13 of the result;
 //  - a thread's values are all of one block's columns and are held in units of 2^(E - kUp): scales from 2^-kSpread to 1 of 2^E
 //    keep codes exact. E grows with the scales that come; keys too far below it, and those whose scale is NaN, are left out of the
 //    product and added one by one in fp32 (`apart`).
@@ -465,7 +474,7 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 // for scores of 2^-kFewLow to 2^kFewGrow, and E at kFirstE, for values' scales of 2^-20 to 2^7.
 // Conversion: an instruction for two keys' codes; of values' codes, which lie the other way round, half a one more to put two
 // keys' codes into one byte, and one for the scales.
-constexpr float kFewLift = 7.f, kFewGrow = 8.f, kFewLow = 7.f;
+constexpr float kFewLift = 7.f, kFewGrow = 8.f, kFewLow = 2.f;
 constexpr int kUp = 13, kSpread = 27, kFirstE = 134;
 
 // The token of a warp's 16 that is row i of the products. Neighbouring threads' values are then in different banks.

@@ -13,8 +13,8 @@ constexpr int kAppendUnroll = 2;
 
 // A thread has 8 values (16 bytes) of `kAppendUnroll` tokens at a time, all loaded before any is written; 4 neighbouring lanes
 // have one block of 32. `group` threads (a power of two, up to a block) share a token, its keys first, then its values.
-// Bound: HBM, 4 bytes a value in bf16, 3.03 in MXFP8 and 2.53 in MXFP4. Two tokens at a time: with four, 48 tokens took 2.5 us in MXFP8
-// instead of 1.6, with one, 20011 tokens 31.6 us instead of 28.
+// Bound: HBM, 4 bytes a value in bf16, 3.03 in MXFP8 and 2.53 in MXFP4. Two tokens at a time: with four, 48 tokens took 2.5 us in
+// MXFP8 instead of 1.6, with one, 20011 tokens 31.6 us instead of 28.
 template <int FMT>
 __global__ void __launch_bounds__(kAppendThreads, 8)
 kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, long long k_stride,

@@ -9,6 +9,10 @@
 // Bound: HBM, 4 bytes a value turned; what is stored adds 2, 1.03 or 0.53 a value and 2 read. Cosines and sines are worked out
 // once for all heads of a token, left in shared memory, and held by every thread for its own places in a head. All of a head that
 // a warp writes it has read before, so rows may be turned where they are.
+//
+// 20011 tokens of 32 heads over 8 of 128 into a bf16 cache: 85 us, 5.8 TB/s. 16384 tokens of 16 and 16 heads of 80, turned back: 36 us,
+// 4.7 TB/s. 3061 tokens into an MXFP4 cache: 20 us, 3.3 TB/s, the quantisation's arithmetic. With a chunk a lane and the other half
+// from another lane, cosines by every warp, these take 147, 55 and 29 us. 6 tokens: 2.4 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -145,7 +149,7 @@ __device__ __forceinline__ const uint16_t* row_of(const RopeArgs& a, int t, int 
 template <bool PAIRS, int FMT>
 __global__ void __launch_bounds__(kRopeWarps * 32, FMT == kNoCache || FMT == MOE_KV_BF16 ? 4 : 3)
 rope_paired_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int U = 2;                  // groups of heads under way
+  constexpr int U = 2;                  // groups of heads under way; 1 and 3 are slower or the same, and so are other numbers of blocks
   __shared__ float2 turn[kRopeWarps][kRopeMaxD / 2];    // by token of the block
   pdl_trigger();
   pdl_wait();

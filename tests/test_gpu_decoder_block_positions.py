@@ -92,7 +92,7 @@ def test_prompt_and_decode_steps(dim, rot, axes, window, sinks, rows, fmt, monke
         assert n == lens[b] + 2 * (steps - 1) + rows
         k, v = (t[table[b]].transpose(0, 2, 1, 3).reshape(-1, heads_kv, dim)[:n] for t in vals)
         out, mag = A.attend_heads(_np(a[0])[b], k, v, n - rows, dim ** -0.5, window, sinks)
-        tol = A.attention_tolerance(out, mag) + 2.0 ** -32 * np.repeat(np.abs(v).sum(0), heads // heads_kv, 0)   # f16 weights
+        tol = A.attention_tolerance(out, mag) + 2.0 ** -30 * np.repeat(np.abs(v).sum(0), heads // heads_kv, 0)   # f16 weights
         assert np.all(np.abs(_np(r)[b] - out) <= tol)
 
 

@@ -2,10 +2,11 @@
 the values that the cache holds.
 
 Tolerance: the oracle's own, which allows for weights rounded to bf16 (more than 16 rows a block) by 2^-8; f16's 2^-11 (up to 16
-rows) are within it down to f16's smallest normal number. Below, f16's steps are 2^-24, so that a rounding is off by 2^-25 whatever
-the weight; weights are held 2^7 times themselves relative to a key whose own weight is 1, so by 2^-32 each, and the sum that
-they are divided by is at least 1: at most 2^-32 of the values' magnitudes, summed without weights, come on top. That
-shows where the keys that count have the code 0 in a column."""
+rows) are within it down to f16's smallest normal number. Below, f16's steps are 2^-24, so that a rounding is off by 2^-25
+whatever the weight; weights are held 2^7 times themselves, so they are off by 2^-32 each, and the sum that they are divided by is
+at least 2^-2, the least that the largest of them may be before their reference moves: at most 2^-30 of the values' magnitudes,
+summed without weights, come on top. That shows where the keys that count have the code 0 in a column.
+"""
 import numpy as np
 import pytest
 import torch
@@ -43,7 +44,7 @@ class Paged4(Paged):
         for b in range(len(self.lens)):
             mine = self.table[b, :self.used[b]].cpu().numpy()
             whole = np.nansum(np.abs(self.values[1][mine]), axis=(0, 2))            # [Hkv, D]; more than any row sees
-            tol[b] += 2.0 ** -32 * np.repeat(whole, tol.shape[2] // whole.shape[0], 0)
+            tol[b] += 2.0 ** -30 * np.repeat(whole, tol.shape[2] // whole.shape[0], 0)
         return tol
 
     def check(self, window=0, sinks=0, **kw):
