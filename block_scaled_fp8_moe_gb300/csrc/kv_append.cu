@@ -72,10 +72,9 @@ kv_append_kernel(const moe_kv_cache c, int T, const uint16_t* __restrict__ k, lo
         sb |= __shfl_down_sync(0xffffffffu, sb, 8) << 16;
         if (in) {
           if constexpr (MX4) {
-            uint32_t codes = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) codes |= e2m1x2(f[2 * j] * sc, f[2 * j + 1] * sc) << (8 * j);
-            reinterpret_cast<uint32_t*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = finite ? codes : 0u;
+            for (int j = 0; j < 8; ++j) f[j] *= sc;
+            reinterpret_cast<uint32_t*>(is_v ? c.v : c.k)[(row << head_log2) + d8] = finite ? e2m1x8(f) : 0u;
           } else {
             uint2 codes = make_uint2(0, 0);
             if (finite)

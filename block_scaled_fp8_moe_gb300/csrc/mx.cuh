@@ -38,10 +38,19 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Two E2M1 codes (round to nearest even, as e2m1_code below), `lo` in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// The scale byte s + 127 of the same rule from a finite amax's bits, in three instructions: the sum carries into the exponent
+// where the fraction is above qm; an amax below the normal numbers ends at byte 0 either way, and none at 254.
+template <int QE, uint32_t QM>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  return (uint32_t)max((int)((amax_bits + (0x7FFFFFu - QM)) >> 23) - QE, 0);
+}
+
+// Eight E2M1 codes (round to nearest even, as e2m1_code below), the first in the lowest half byte.
+__device__ __forceinline__ uint32_t e2m1x8(const float* f) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r) : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
 

@@ -83,20 +83,18 @@ __device__ __forceinline__ uint32_t mx_codes(const float (&f)[VEC], uint32_t (&w
 #pragma unroll
   for (int d = 1; d < 32 / VEC; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
   const bool finite = m < 0x7F800000u;
-  const int se = FMT == MOE_KV_MXFP8 ? e4m3_scale_exp(__uint_as_float(m)) : e2m1_scale_exp(__uint_as_float(m));
-  const float sc = pow2_neg(se);
+  const uint32_t byte = FMT == MOE_KV_MXFP8 ? mx_scale_byte<8, 0x600000u>(m) : mx_scale_byte<2, 0x400000u>(m);
+  const float sc = __uint_as_float((254u - byte) << 23);
+  float x[8] = {};
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = f[e] * sc;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    w[i] = 0;
-    if constexpr (FMT == MOE_KV_MXFP8) {
-      w[i] = e4m3x2(f[4 * i] * sc, f[4 * i + 1] * sc) | e4m3x2(f[4 * i + 2] * sc, f[4 * i + 3] * sc) << 16;
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) w[i] |= e2m1x2(f[2 * e] * sc, f[2 * e + 1] * sc) << (8 * e);
-    }
+    if constexpr (FMT == MOE_KV_MXFP8) w[i] = e4m3x2(x[4 * i], x[4 * i + 1]) | e4m3x2(x[4 * i + 2], x[4 * i + 3]) << 16;
+    else w[i] = e2m1x8(x);
     if (!finite) w[i] = 0;
   }
-  return finite ? (uint32_t)(se + 127) : 255u;
+  return finite ? byte : 255u;
 }
 
 // VEC values of a row that go into the cache, from value d0 on; `row` counts the cache's rows of D values. All lanes of the warp
