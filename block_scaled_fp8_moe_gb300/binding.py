@@ -708,20 +708,23 @@ class Rotary:
 def _positions(rotary: Rotary, pos, T: int, dev: int) -> int:
     if rotary.dev != dev:
         raise ValueError(f"rotary must be on device {dev}")
-    if tuple(pos.shape) != (rotary.axes, T) and (rotary.axes > 1 or tuple(pos.shape) != (T,)):
+    if pos.shape != (rotary.axes, T) and (rotary.axes > 1 or pos.shape != (T,)):
         raise ValueError(f"pos must be [{rotary.axes}, {T}], is {tuple(pos.shape)}")
     return _on(pos, "pos", torch.int32, dev)
 
 
-def _out_rows(out, name: str, like, x: int, stride: int, dev: int) -> tuple[int, int]:
-    """The address and the row stride of where `like`'s rows (at x, apart by stride) go: themselves, or rows of their own."""
-    T, heads, D = like.shape
-    po, so = _rows_on(out, name, heads, D, dev)
-    if out.shape[0] != T:
-        raise ValueError(f"{name} needs {T} rows, has {out.shape[0]}")
-    if T * heads and po == x and so != stride:
+def _tokens_on(t: torch.Tensor, name: str, T: int, heads: int, D: int, dev: int) -> tuple[int, int]:
+    """As _rows_on, of so many rows."""
+    at, stride = _rows_on(t, name, heads, D, dev)
+    if t.shape[0] != T:
+        raise ValueError(f"{name} needs {T} rows, has {t.shape[0]}")
+    return at, stride
+
+
+def _not_across(out: int, so: int, x: int, sx: int, n: int, name: str) -> None:
+    """Rows are turned to rows of their own or where they are, not to the same place at another spacing."""
+    if out == x and so != sx and n:
         raise ValueError(f"{name} must not overlap what is read, or be the same rows")
-    return po, so
 
 
 def moe_rope(rotary: Rotary, q, k, pos, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -734,9 +737,7 @@ def moe_rope(rotary: Rotary, q, k, pos, inverse: bool = False, q_out=None, k_out
     Hkv, pk, sk, pko, sko = 0, None, 0, None, 0
     if k is not None:
         Hkv = k.shape[1]
-        pk, sk = _rows_on(k, "k", Hkv, D, dev)
-        if k.shape[0] != T:
-            raise ValueError(f"k needs {T} rows, has {k.shape[0]}")
+        pk, sk = _tokens_on(k, "k", T, Hkv, D, dev)
     elif k_out is not None:
         raise ValueError("k_out is not written without k")
     pp = _positions(rotary, pos, T, dev)
@@ -746,9 +747,11 @@ def moe_rope(rotary: Rotary, q, k, pos, inverse: bool = False, q_out=None, k_out
                 q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
             if k_out is None and k is not None:
                 k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=q.device)
-    pqo, sqo = _out_rows(q_out, "q_out", q, pq, sq, dev)
+    pqo, sqo = _tokens_on(q_out, "q_out", T, Hq, D, dev)
+    _not_across(pqo, sqo, pq, sq, T * Hq, "q_out")
     if k is not None:
-        pko, sko = _out_rows(k_out, "k_out", k, pk, sk, dev)
+        pko, sko = _tokens_on(k_out, "k_out", T, Hkv, D, dev)
+        _not_across(pko, sko, pk, sk, T * Hkv, "k_out")
     rc = lib.moe_rope(rotary.refs[bool(inverse)], T, Hq, Hkv, D, pq, sq, pk, sk, pp, T, pqo, sqo, pko, sko,
                       _raw_stream(stream, dev))
     if rc:
@@ -763,21 +766,24 @@ def moe_rope_kv_append(rotary: Rotary, cache: KvCache, q, k, v, pos, slots, q_ou
     dev = _current(q, "q")
     if cache.dev != dev:
         raise ValueError("cache and q must be on the same CUDA device")
-    T, Hq, D = q.shape
-    if D != cache.D:
-        raise ValueError(f"q must be [rows, heads, {cache.D}], is {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    Hkv, D = cache.Hkv, cache.D
     pq, sq = _rows_on(q, "q", Hq, D, dev)
-    pk, sk = _rows_on(k, "k", cache.Hkv, D, dev)
-    pv, sv = _rows_on(v, "v", cache.Hkv, D, dev)
-    if k.shape[0] != T or v.shape[0] != T or slots.numel() != T:
-        raise ValueError(f"k, v and slots need {T} rows, have {k.shape[0]}, {v.shape[0]} and {slots.numel()}")
+    pk, sk = _tokens_on(k, "k", T, Hkv, D, dev)
+    pv, sv = _tokens_on(v, "v", T, Hkv, D, dev)
+    if slots.numel() != T:
+        raise ValueError(f"slots needs {T} entries, has {slots.numel()}")
     pp = _positions(rotary, pos, T, dev)
     ps = _on(slots, "slots", torch.int32, dev)
     if q_out is None:
         with _allocating(stream):
             q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    pqo, sqo = _out_rows(q_out, "q_out", q, pq, sq, dev)
-    pko, sko = (None, 0) if k_out is None else _out_rows(k_out, "k_out", k, pk, sk, dev)
+    pqo, sqo = _tokens_on(q_out, "q_out", T, Hq, D, dev)
+    _not_across(pqo, sqo, pq, sq, T * Hq, "q_out")
+    pko, sko = None, 0
+    if k_out is not None:
+        pko, sko = _tokens_on(k_out, "k_out", T, Hkv, D, dev)
+        _not_across(pko, sko, pk, sk, T * Hkv, "k_out")
     raw = _raw_stream(stream, dev)
     pws, nws = _workspace(256, q, stream, dev, raw) if ws is None else (_on(ws, "ws", torch.uint8, dev), ws.numel())
     rc = lib.moe_rope_kv_append(rotary.refs[0], cache.ref, T, Hq, pq, sq, pk, sk, pv, sv, pp, T, ps, pqo, sqo, pko, sko,
