@@ -598,7 +598,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     uint32_t early = 0;                         // this thread's rows that have had no weight worth the name yet
 #pragma unroll
     for (int r = 0; r < 2 * NB; ++r) early |= (uint32_t)(4 * (r & ~1) + 2 * c + (r & 1) < R) << r;
-    bool first = true;                          // no value so far
+    bool first = true;                          // no value of this thread's block so far
 
     for (int i = 0; i < cnt; ++i) {
       const int s = stage;
@@ -679,7 +679,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             }
 
         // ---- what the rows do not see ----
-        uint32_t hidden = 0;                    // of t
+        uint32_t hidden = 0, drop = 0;          // of t; tokens that no row sees
         const int loc0 = warp * ST + part * 16, tok0 = info.x + loc0;
         if (!whole) {
           const uint32_t mask = (uint32_t)info.y;
@@ -703,7 +703,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             }
           const int tt = tok0 + lane;
           const bool any = lane < 16 && ((mask >> ((loc0 + lane) >> page_log2)) & 1u) && tt <= it.pmax && (tt >= it.first_any || tt < p.a.sinks);
-          const uint32_t drop = __ballot_sync(0xffffffffu, !any);
+          drop = __ballot_sync(0xffffffffu, !any);
 #pragma unroll
           for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
@@ -746,6 +746,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             }
         }
         uint32_t apart = 0;                     // tokens that are added one by one
+        bool unit_looked_at = false;
         if (__any_sync(0xffffffffu, weights_move || scales_move)) {
           if (__any_sync(0xffffffffu, bad)) {   // keys' scores that are NaN
 #pragma unroll
@@ -783,7 +784,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               const uint32_t bit = 1u << (2 * nb + e);
               const float to = kFewLift - mx;
               if (mx > -INFINITY && (to < off[nb][e] - kFewGrow || (early & bit))) {
-                k[e] = ex2(to - off[nb][e]);
+                if (!(early & bit)) k[e] = ex2(to - off[nb][e]);       // else there are no weights, and it may be infinite
                 off[nb][e] = to;
                 early &= ~bit;
               }
@@ -803,6 +804,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             // too while there is no value yet.
             int hi = -1;
             uint32_t zeros = 0;
+            unit_looked_at = true;
 #pragma unroll
             for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
@@ -818,8 +820,9 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             for (int d = 1; d < 4; d *= 2) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             const int was = E;
             if (hi >= 0) E = first ? hi : max(E, hi);
-            const float k = pow2i(max(was - E, -149));       // 2^0 where nothing changes; with no value yet, of zeros
-            if (!first) {
+            const float k = first ? 1.f : pow2i(was - E);
+            first = first && hi < 0;
+            if (__any_sync(0xffffffffu, k != 1.f)) {
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -845,7 +848,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               for (int h = 0; h < 2; ++h) u[gr][h] = by[gr][h] - (uint32_t)((E - kSpread) * 0x10001);
           }
         }
-        first = false;
+        if (!unit_looked_at) first = first && (uint16_t)drop == 0xFFFFu;
 
         uint32_t wt[GR][NB][2];
 #pragma unroll

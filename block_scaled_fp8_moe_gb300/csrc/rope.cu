@@ -27,6 +27,7 @@ namespace moe {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeMaxD = 256;
+constexpr int kRopeMaxT = 1 << 30;
 constexpr int kNoCache = -1;
 
 struct RopeArgs {
@@ -403,7 +404,7 @@ extern "C" int moe_rope(const moe_rotary* r, int32_t T, int32_t Hq, int32_t Hkv,
                         uint16_t* q_out, int64_t qo_stride, uint16_t* k_out, int64_t ko_stride, void* stream) {
   if (!r || T < 0 || Hq < 0 || Hkv < 0 || D <= 0) return MOE_ERR_INVALID_ARG;
   const int vec = rope_vec(r);
-  if (!rotary_ok(r, D) || D > 32 * vec || Hq > 65535 || Hkv > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!rotary_ok(r, D) || D > 32 * vec || Hq > 65535 || Hkv > 65535 || T > kRopeMaxT) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || (Hq == 0 && Hkv == 0)) return MOE_OK;
   if (Hkv && !k_out) return MOE_ERR_INVALID_ARG;
   RopeArgs p{};
@@ -417,7 +418,8 @@ extern "C" int moe_rope_kv_append(const moe_rotary* r, const moe_kv_cache* cache
                                   const int32_t* slots, uint16_t* q_out, int64_t qo_stride, uint16_t* k_out,
                                   int64_t ko_stride, void* ws, size_t ws_bytes, void* stream) {
   if (!r || !cache || T < 0 || Hq < 0) return MOE_ERR_INVALID_ARG;
-  if (!kv_cache_ok(cache) || !rotary_ok(r, cache->D) || Hq > 65535 || cache->Hkv > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!kv_cache_ok(cache) || !rotary_ok(r, cache->D) || Hq > 65535 || cache->Hkv > 65535 || T > kRopeMaxT)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!status_ws_ok(ws, ws_bytes)) return MOE_ERR_WORKSPACE;
   if (T == 0) return MOE_OK;
   const int64_t row = (int64_t)cache->Hkv * cache->D;

@@ -424,8 +424,8 @@ MOE_API int moe_rotary_turns(int32_t n, const double* inv_freq, uint64_t* turns)
  * k_stride ([Hkv, D]), to q_out and k_out, spaced by strides of their own. q_out may be q with the same stride,
  * and k_out k (turned where they are); otherwise they do not overlap what is read. Hq or Hkv may be 0
  * (its pointers are not looked at). pos i32: the position along axis x at pos[x * pos_stride + t], pos_stride >= T.
- * D a multiple of 8, at most 256 (128 where dim is not a multiple of 16 and pairs are not neighbours). Pointers
- * 16-byte aligned, strides multiples of 8 elements. T = 0 is a no-op. */
+ * D a multiple of 8, at most 256 (128 where dim is not a multiple of 16 and pairs are not neighbours), at most 2^30
+ * tokens, 65535 heads. Pointers 16-byte aligned, strides multiples of 8 elements. T = 0 is a no-op. */
 MOE_API int moe_rope(const moe_rotary* r, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, const uint16_t* q,
                      int64_t q_stride, const uint16_t* k, int64_t k_stride, const int32_t* pos, int64_t pos_stride,
                      uint16_t* q_out, int64_t qo_stride, uint16_t* k_out, int64_t ko_stride, void* stream);
@@ -446,7 +446,10 @@ MOE_API int moe_rope_kv_append(const moe_rotary* r, const moe_kv_cache* cache, i
  * head h reads key head h / (Hq / Hkv). The row at position p of its sequence sees key j when
  *   j <= p  and  (window == 0  or  p - j < window  or  j < sinks):
  * a sliding window and the sequence's first `sinks` tokens, which stay visible. A row that sees nothing
- * gets +0; one whose visible scores are all minus infinity is NaN, as the formula has it. Keys and values that a row does not see, and what lies in a page behind its sequence's last
+ * gets +0; one whose visible scores are all minus infinity is NaN, as the formula has it. Over an MXFP4 cache, up to
+ * 16 rows (row, head of the group) have their weights rounded to f16: those below 2^-30 of the largest count as
+ * zero there, so does a key's block of scale byte 0 (2^-127), and keys past 2^117 may make a score infinite.
+ * Keys and values that a row does not see, and what lies in a page behind its sequence's last
  * token, do not reach its result whatever they hold, NaN and infinities included. */
 typedef struct moe_attention {
   int32_t B;             /* sequences                                       */

@@ -198,6 +198,30 @@ def test_one_block_far_above_and_zeros_below(D, rows, Hq):
 
 
 @pytest.mark.parametrize("rows,Hq", SHAPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shift", [-60, -25, 20, 100])
+def test_all_values_far_from_one(shift, D, rows, Hq):
+    """Caches whose values are all small or all large, some sequences beginning with tokens of zeros, or with a window behind
+    which the first steps' tokens are nobody's; and scores that are all far below or above zero."""
+    p = Paged4([400, 1300, 90], rows, Hq, 1, D, 16, seed=6)
+    p.cache.v_s += shift if shift > 0 else 256 + shift
+    for j in range(150):
+        p.cache.v[p.at(1, j)], p.cache.v_s[p.at(1, j)] = 0, 0
+    p.reread()
+    p.check()
+    p.check(333, 0)
+    p.check(70, 3)
+    p.q[..., 1:] = 0
+    for x in (-300.0, 30.0, -20.0):              # every score near x * (6 to 8) / sqrt(D), whose spread it keeps small
+        p.q[..., 0] = x
+        p.cache.k[..., 0] = (p.cache.k[..., 0] & 0xF0) | 7
+        p.cache.k_s[..., 0] = 127
+        p.reread()
+        p.check()
+        p.check(70, 3)
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES)
 def test_small_and_large_queries(rows, Hq):
     """Rows whose queries are 2^-100 and 2^100 times the others', and scales of keys that make up for it."""
     for power in (-100, 100, -120):

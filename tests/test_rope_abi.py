@@ -61,7 +61,7 @@ def test_rope_refusals(B):
     for kw in (dict(dim=0), dict(dim=4), dict(dim=72), dict(dim=63), dict(axes=0), dict(axes=5), dict(factor=float("nan")),
                dict(dim=-8)):
         assert call(_rotary(B, **kw)) == B.MOE_ERR_UNSUPPORTED_SHAPE, kw
-    for kw in (dict(D=68), dict(D=264), dict(Hq=65536), dict(Hkv=65536)):
+    for kw in (dict(D=68), dict(D=264), dict(Hq=65536), dict(Hkv=65536), dict(T=2 ** 30 + 1, ps=2 ** 31)):
         assert call(**kw) == B.MOE_ERR_UNSUPPORTED_SHAPE, kw
     assert call(_rotary(B, dim=56), D=136) == B.MOE_ERR_UNSUPPORTED_SHAPE       # 4 values a lane: at most 128
     odd = ctypes.c_void_p(0x10008)
