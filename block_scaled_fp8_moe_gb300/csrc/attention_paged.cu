@@ -536,7 +536,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     vs_lane[e] = 2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D);
   }
   uint32_t qf[NB][D / 16][2];
-  float qs[NB][2];                              // of rows 2c and 2c + 1: what their queries were divided by
+  float qs[NB][2];                              // of rows 2c and 2c + 1: the scores' factor, and what their queries were divided by
   auto load_q = [&](int n) {
     if (!__all_sync(0xffffffffu, bar_wait(&w_full[n & 1], (n >> 1) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) ||
         !items[n & 1].there)
@@ -571,7 +571,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
         qf[nb][2 * bl][0] = conv(w[bl].x), qf[nb][2 * bl][1] = conv(w[bl].y);
         qf[nb][2 * bl + 1][0] = conv(w[bl].z), qf[nb][2 * bl + 1][1] = conv(w[bl].w);
       }
-      const float up = finite ? __uint_as_float((uint32_t)e << 23) : 1.f;
+      const float up = (finite ? __uint_as_float((uint32_t)e << 23) : 1.f) * scale;
       qs[nb][0] = __shfl_sync(0xffffffffu, up, 8 * c);
       qs[nb][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
     }
@@ -585,7 +585,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     const FewItem& it = items[n & 1];
     const int cnt = it.cnt;
     float o[NB][MT][4], ol[NB][4];              // ol: the weights' sums, by a product with ones
-    float off[NB][2];                           // kFewLift less what weights refer to
+    float off[NB][2];                           // kFewLift less what weights refer to, a score as it is rounded for its weight
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -674,8 +674,10 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              sc[gr][nb][e] *= qs[nb][e & 1];
-              t[gr][nb][e] = fmaf(sc[gr][nb][e], scale, off[nb][e & 1]);
+              // rounded before anything is added: from scores of 2^29 on, what one fused operation would keep of the product
+              // outgrows every weight
+              sc[gr][nb][e] = __fmul_rn(sc[gr][nb][e], qs[nb][e & 1]);
+              t[gr][nb][e] = __fadd_rn(sc[gr][nb][e], off[nb][e & 1]);
             }
 
         // ---- what the rows do not see ----
@@ -777,7 +779,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u)) mx = fmaxf(mx, sc[gr][nb][2 * h + e] * scale);
+                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u)) mx = fmaxf(mx, sc[gr][nb][2 * h + e]);
 #pragma unroll
               for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               k[e] = 1.f;
@@ -793,7 +795,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                   if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u))
-                    t[gr][nb][2 * h + e] = fmaf(sc[gr][nb][2 * h + e], scale, off[nb][e]);
+                    t[gr][nb][2 * h + e] = __fadd_rn(sc[gr][nb][2 * h + e], off[nb][e]);
             }
             ol[nb][0] *= k[0], ol[nb][1] *= k[1];
 #pragma unroll
@@ -941,14 +943,15 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     }
 
     // ---------------- the warps' parts joined, in the order of their tokens ----------------
-    // sums are the same in all lanes of a column; kFewLift out of them and of the outputs
+    // Sums are the same in all lanes of a column. 2^kFewLift is taken out of them and of the outputs alike, and what they refer to
+    // is -off itself, without it: any other number next to a large one would be rounded.
     const float unlift = pow2i(-(int)kFewLift);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (g == 0)
-          sums[(n & 1) * C::WARPS + warp][8 * nb + 2 * c + e] = make_float2(ol[nb][e] == 0.f ? -INFINITY : kFewLift - off[nb][e], ol[nb][e] * unlift);
+          sums[(n & 1) * C::WARPS + warp][8 * nb + 2 * c + e] = make_float2(ol[nb][e] == 0.f ? -INFINITY : -off[nb][e], ol[nb][e] * unlift);
     const int piece = it.piece, pieces = it.pieces, hk = it.hk;
     const long long b = it.b;
     const bool more = load_q(n + 1);              // on their way while this item ends
@@ -973,7 +976,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
         float top;
         total(rho, top);
         // a warp without weights has zeros here, or what values that are not numbers made of them
-        const float f = ex2((ol[nb][e] == 0.f ? 0.f : kFewLift - off[nb][e] - (top == -INFINITY ? 0.f : top)));
+        const float f = ex2(ol[nb][e] == 0.f ? 0.f : -off[nb][e] - top);
 #pragma unroll
         for (int j = 0; j < MT; j += 2)           // of products j and j + 1 four columns in a row
           *reinterpret_cast<float4*>(mine + rho * C::PITCH + g * (D / 8) + 2 * j) =
