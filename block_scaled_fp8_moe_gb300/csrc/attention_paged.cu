@@ -463,8 +463,12 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 // ---- MXFP4 ----
 // The consuming warps' work over MXFP4, for up to 16 rows: the rows are the columns of both products, 8 at a time, and the codes
 // their other side, as f16, which holds an E2M1 code and has an instruction for two of them. What f16's range asks for:
-//  - a query is scaled to less than 2 by a power of two of its row: what is 2^-17 of the largest or more keeps all of bf16's
-//    digits, the rest is rounded to 2^-25 of it, as fp32 sums would; a block's scale is put on its 32 products' sum, in fp32;
+//  - a query's row is scaled by a power of two so that its largest element lies from 2^15 to 2^16: elements down to 2^-32 of that
+//    keep all of bf16's digits. A block's scale is put on its 32 products' sum, in fp32. Rows with elements further apart
+//    or not finite, rows and scores' factors far from one (kFarRow, kFarScale), and keys whose scales are 2^65 or more or NaN,
+//    which fp32 would not hold the sums of, are multiplied again as bf16, keys and queries as they are, like more rows are
+//    (`again`): no element's digits depend on another's size. Below, a block of scale byte 0, 2^-127, adds nothing to a score
+//    (less than 2^-30) and counts as zero;
 //  - weights are 2^kFewLift times themselves, at most 2^kFewGrow more (the maximum that they refer to moves when outgrown by
 //    that), so that weights below 2^-30 of the largest become zero, 2^17 tokens of them 2^-13 of the result;
 //  - a thread's values are all of one block's columns and are held in units of 2^(E - kUp): scales from 2^-kSpread to 1 of 2^E
@@ -476,6 +480,8 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 // keys' codes into one byte, and one for the scales.
 constexpr float kFewLift = 7.f, kFewGrow = 8.f, kFewLow = 2.f;
 constexpr int kUp = 13, kSpread = 27, kFirstE = 134;
+constexpr int kFarRow = 64;                                // rows whose largest element is 2^64 or more, or below 2^-64
+constexpr float kFarLow = 0x1p-40f, kFarHigh = 0x1p20f;    // scores' factors that are kept
 
 // The token of a warp's 16 that is row i of the products. Neighbouring threads' values are then in different banks.
 template <int D>
@@ -515,6 +521,34 @@ __device__ __forceinline__ float pow2i(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : e >= -149 ? __uint_as_float(1u << (e + 149)) : 0.f;
 }
 
+// The scores of 16 keys and 8 rows, without their factor, from bf16: keys whose scale is large or NaN, and rows that f16 does not hold.
+// A thread's places of its first key's codes (whose blocks' numbers turn bits 4 and 5) and scales, and of its row's queries
+// (0: no row). Not inlined: the step that calls it would take 1 to 2 % longer.
+template <class C>
+__device__ __noinline__ float4 scores_again(uint32_t codes, uint32_t scales, uint32_t query) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int bl = 0; bl < C::D / 32; ++bl) {
+    uint32_t x[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w, by;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"((codes ^ (bl << 4)) + 8 * h * C::ROWB) : "memory");
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(by) : "r"(scales + 8 * h * (C::D / 32) + bl) : "memory");
+      const uint32_t f = ((min(by, kScaleFits4) + 112u) << 7) * 0x10001u;
+      const uint32_t f2 = (by == 255u ? 0x7FC0u : by > kScaleFits4 ? (by - kScaleFits4 + 127u) << 7 : 0x3F80u) * 0x10001u;
+      auto key = [&](uint32_t pair) { return mul_bf16x2(mul_bf16x2(pair, f), f2); };
+      x[0][h] = key(e2m1_bf16<0>(w)), x[0][2 + h] = key(e2m1_bf16<1>(w));
+      x[1][h] = key(e2m1_bf16<2>(w)), x[1][2 + h] = key(e2m1_bf16<3>(w));
+    }
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (query) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(query + bl * 64) : "memory");
+    mma_16816(s, x[0], q.x, q.y);
+    mma_16816(s, x[1], q.z, q.w);
+  }
+  return make_float4(s[0], s[1], s[2], s[3]);
+}
+
 template <class C>
 __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, float* join, const uint8_t* queries, uint64_t* full, uint64_t* empty,
                                              uint64_t* w_full, uint64_t* w_empty, const int4* infos,
@@ -535,8 +569,17 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     v_lane[e] = C::KV + kv_addr<C>(0, tk, D == 128 ? g >> 1 : g >> 2) + (D == 128 ? 8 * (g & 1) : 4 * (g & 3));
     vs_lane[e] = 2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D);
   }
+  // a token's scale bytes
+  auto scales_of = [](uint32_t at) {
+    uint32_t x;
+    if constexpr (D == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    else asm volatile("{\n\t.reg .b16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(x) : "r"(at) : "memory");
+    return x;
+  };
   uint32_t qf[NB][D / 16][2];
   float qs[NB][2];                              // of rows 2c and 2c + 1: the scores' factor, and what their queries were divided by
+  uint32_t again[NB];                           // rows whose f16 does not do, four lanes' bits each
+  const bool far_scale = scale != 0.f && !(fabsf(scale) >= kFarLow && fabsf(scale) < kFarHigh);
   auto load_q = [&](int n) {
     if (!__all_sync(0xffffffffu, bar_wait(&w_full[n & 1], (n >> 1) & 1, kPagedWaitNs, abort, DEV_TIMEOUT_FULL)) ||
         !items[n & 1].there)
@@ -546,32 +589,34 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
       const int rho = 8 * nb + g;
       const uint8_t* row = queries + (n & 1) * C::QBUF + rho * D * 2;
       uint4 w[D / 32];                          // block by block the 8 values whose codes one thread has at hand
-      uint32_t m2 = 0;
+      uint32_t most = 0, least = 0x7FFF7FFFu;   // magnitudes' bits; those of what is not zero, less one, with the sign's bit
+      auto seen = [&](uint32_t x) {
+        x &= 0x7FFF7FFFu;
+        most = __vmaxu2(most, x);
+        least = __vmins2(least, x + 0x7FFF7FFFu);
+      };
 #pragma unroll
       for (int bl = 0; bl < D / 32; ++bl) {
         w[bl] = rho < R ? *reinterpret_cast<const uint4*>(row + (bl * 32 + 8 * c) * 2) : make_uint4(0, 0, 0, 0);
-        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[bl].x & 0x7FFF7FFFu, w[bl].y & 0x7FFF7FFFu),
-                                   __vmaxu2(w[bl].z & 0x7FFF7FFFu, w[bl].w & 0x7FFF7FFFu)));
+        seen(w[bl].x), seen(w[bl].y), seen(w[bl].z), seen(w[bl].w);
       }
-      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      // a row with a value that is not finite: the others do not matter, and stay out of f16's way
-      const bool finite = m < 0x7F80u;
-      const int e = min(max((int)(m >> 7), 1), 253);
-      const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-      auto conv = [&](uint32_t x) {
-        float lo = bf16_lo(x), hi = bf16_hi(x);
-        if (finite) lo *= down, hi *= down;
-        else lo = isfinite(lo) ? 0.f : lo, hi = isfinite(hi) ? 0.f : hi;
-        return f16x2(lo, hi);
-      };
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, d));
+        least = __vmins2(least, __shfl_xor_sync(0xffffffffu, least, d));
+      }
+      const int m = max(most & 0xFFFFu, most >> 16), e = m >> 7;
+      const int l = min((int)(int16_t)least, (int)(int16_t)(least >> 16)) + 0x8001;     // past all magnitudes if all are zero
+      again[nb] = __ballot_sync(0xffffffffu, far_scale || (m && (e < 127 - kFarRow || e >= 127 + kFarRow || l < (e - 32) << 7)));
+      const int to = min(max(e, 127 - kFarRow), 126 + kFarRow);
+      const float down = __uint_as_float((uint32_t)(127 + 15 + 127 - to) << 23);
+      auto conv = [&](uint32_t x) { return f16x2(bf16_lo(x) * down, bf16_hi(x) * down); };
 #pragma unroll
       for (int bl = 0; bl < D / 32; ++bl) {
         qf[nb][2 * bl][0] = conv(w[bl].x), qf[nb][2 * bl][1] = conv(w[bl].y);
         qf[nb][2 * bl + 1][0] = conv(w[bl].z), qf[nb][2 * bl + 1][1] = conv(w[bl].w);
       }
-      const float up = (finite ? __uint_as_float((uint32_t)e << 23) : 1.f) * scale;
+      const float up = __uint_as_float((uint32_t)(to - 15) << 23) * scale;
       qs[nb][0] = __shfl_sync(0xffffffffu, up, 8 * c);
       qs[nb][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
     }
@@ -611,22 +656,25 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
       const int4 info = infos[s];
       const uint32_t st = smem_u32(smem) + s * C::STAGE;
       const bool whole = (info.z >> warp) & 1;  // every row of the block sees every token of this warp
+      // whether there are rows, or keys of this warp (a lane has a key's scales), whose products are done again
+      static_assert(ST == 32, "a lane for a token");
+      uint32_t far = scales_of(st + 2 * C::KV + (warp * ST + lane) * (D / 32));
+      far = far & (far << 1) & 0x80808080u;     // a block's scale is 2^65 or more, or NaN
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) far |= again[nb];
+      const bool redo = __any_sync(0xffffffffu, far != 0);
       // 16 tokens at a time, in little code: the instruction cache is what more in a turn is short of
 #pragma unroll 1
       for (int part = 0; part < ST / 16 && ((info.z >> (C::WARPS + warp)) & 1); ++part) {
         const uint32_t codes_at = st + part * 16 * C::ROWB, scales_at = st + part * 16 * (D / 32);
         // ---- scores ----
         float sc[GR][NB][4];
-        bool bad = false;                       // a block's scale is NaN
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr) {
           uint32_t sw[2], w[2][D / 32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t at = scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32);
-            if constexpr (D == 128) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sw[h]) : "r"(at) : "memory");
-            else asm volatile("{\n\t.reg .b16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(sw[h]) : "r"(at) : "memory");
-            bad = bad || ((~sw[h] - 0x01010101u) & sw[h] & 0x80808080u) != 0;
+            sw[h] = scales_of(scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32));
 #pragma unroll
             for (int bl = 0; bl < D / 32; ++bl)
               asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((codes_at + k_lane) ^ (bl << 4)) + (8 * h + 16 * gr) * C::ROWB) : "memory");
@@ -635,7 +683,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           for (int bl = 0; bl < D / 32; ++bl) {
             const uint32_t x0[4] = {e2m1_pair<0>(w[0][bl]), e2m1_pair<0>(w[1][bl]), e2m1_pair<1>(w[0][bl]), e2m1_pair<1>(w[1][bl])};
             const uint32_t x1[4] = {e2m1_pair<2>(w[0][bl]), e2m1_pair<2>(w[1][bl]), e2m1_pair<3>(w[0][bl]), e2m1_pair<3>(w[1][bl])};
-            float f[2];                         // 2^(byte - 127); byte 0, 2^-127, counts as zero
+            float f[2];                         // 2^(byte - 127), or 0
 #pragma unroll
             for (int h = 0; h < 2; ++h) f[h] = __uint_as_float((bl < 3 ? sw[h] << (23 - 8 * bl) : sw[h] >> 1) & 0x7F800000u);
 #pragma unroll
@@ -645,6 +693,29 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               mma_16816_f16(a, x1, qf[nb][2 * bl + 1][0], qf[nb][2 * bl + 1][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) sc[gr][nb][e] = bl == 0 ? a[e] * f[e >> 1] : fmaf(a[e], f[e >> 1], sc[gr][nb][e]);
+            }
+          }
+        }
+        // Rounded before anything is added: from scores of 2^29 on, what one fused operation would keep of the product outgrows
+        // every weight.
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[0][nb][e] = __fmul_rn(sc[0][nb][e], qs[nb][e & 1]);
+        if (redo) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const int rho = 8 * nb + g;
+            const float4 x = scores_again<C>(codes_at + k_lane, scales_at + ks_lane,
+                                             rho < R ? smem_u32(queries) + (n & 1) * C::QBUF + (rho * D + 8 * c) * 2 : 0);
+            const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t mine = scales_of(scales_at + ks_lane + 8 * h * (D / 32));
+              mine = mine & (mine << 1) & 0x80808080u;
+#pragma unroll
+              for (int e = 2 * h; e < 2 * h + 2; ++e)
+                if (mine || ((again[nb] >> (8 * c + 4 * (e & 1))) & 1u)) sc[0][nb][e] = __fmul_rn(y[e], scale);
             }
           }
         }
@@ -673,12 +744,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // rounded before anything is added: from scores of 2^29 on, what one fused operation would keep of the product
-              // outgrows every weight
-              sc[gr][nb][e] = __fmul_rn(sc[gr][nb][e], qs[nb][e & 1]);
-              t[gr][nb][e] = __fadd_rn(sc[gr][nb][e], off[nb][e & 1]);
-            }
+            for (int e = 0; e < 4; ++e) t[gr][nb][e] = __fadd_rn(sc[gr][nb][e], off[nb][e & 1]);
 
         // ---- what the rows do not see ----
         uint32_t hidden = 0, drop = 0;          // of t; tokens that no row sees
@@ -727,7 +793,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             top = __vmaxu2(top, u[gr][h]);
           }
         const bool scales_move = max(top & 0xFFFFu, top >> 16) > kSpread;
-        bool weights_move = bad;
+        bool weights_move = false;
 #pragma unroll
         for (int gr = 0; gr < GR; ++gr)
 #pragma unroll
@@ -750,25 +816,6 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
         uint32_t apart = 0;                     // tokens that are added one by one
         bool unit_looked_at = false;
         if (__any_sync(0xffffffffu, weights_move || scales_move)) {
-          if (__any_sync(0xffffffffu, bad)) {   // keys' scores that are NaN
-#pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t at = scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32);
-                bool is = false;
-                for (int b = 0; b < D / 32; ++b) {
-                  uint32_t x;
-                  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at + b) : "memory");
-                  is = is || x == 255u;
-                }
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                  for (int e = 2 * h; e < 2 * h + 2; ++e)
-                    if (is) sc[gr][nb][e] = __uint_as_float(0x7FC00000u);
-              }
-          }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             float k[2];

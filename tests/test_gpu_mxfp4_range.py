@@ -62,3 +62,58 @@ def test_equal_keys_share_at_any_score(power, rows, Hq):
     p.reread()
     p.check()
     p.check(scale=-0.3)
+
+
+def _spread(p, r, block):
+    """Every other row's largest query elements 2^r times the others, where they meet keys of nothing: one element and codes of
+    zero, or a block of queries and keys whose scale makes up for it."""
+    if block:
+        p.q[:, ::2, :, 32:64] *= 2.0 ** r
+        p.cache.k_s[..., 1] -= r
+    else:
+        p.q[:, ::2, :, 3] = 2.0 ** r
+        p.cache.k[..., 1] &= 0x0F                               # element 3 is the high half of byte 1
+    p.reread()
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("block", [False, True])
+@pytest.mark.parametrize("r", [10, 17, 20, 24, 26, 31, 34, 60, 100])
+def test_queries_with_elements_far_apart(r, block, D, rows, Hq):
+    p = Paged4([700, 90], rows, Hq, 1, D, 16, seed=r)
+    _spread(p, r, block)
+    p.check()
+    p.check(200, 3)
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES)
+@pytest.mark.parametrize("r", [20, 26, 60, 100])
+def test_small_query_blocks_that_large_keys_make_up_for(r, rows, Hq):
+    """A row's first block is of ordinary size and meets codes of zero, its second is 2^-r of that and meets scales of 2^r."""
+    p = Paged4([700, 90], rows, Hq, 1, 64, 16, seed=r)
+    p.q[..., 32:] *= 2.0 ** -r
+    p.cache.k[..., :16] = 0
+    p.cache.k_s[..., 1] += r
+    p.reread()
+    p.check()
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES)
+def test_scales_at_their_ends(rows, Hq):
+    """Keys of scale byte 0 and of the largest, some among ordinary ones, with queries that make up for them; factors of the scores
+    far from one."""
+    for q, k, scale in ((2.0 ** 124, -126, None), (2.0 ** -120, 120, None), (2.0 ** 30, 30, 2.0 ** -63),
+                        (2.0 ** -25, -25, 2.0 ** 47), (2.0 ** 60, 40, 2.0 ** -103), (2.0 ** -70, -40, 2.0 ** 107)):
+        p = Paged4([300, 90], rows, Hq, 1, 64, 16, seed=4)
+        p.cache.k_s.copy_(torch.clamp(p.cache.k_s.int() + k, 0, 255).byte())
+        p.q *= q
+        p.reread()
+        p.check(scale=scale)
+    p = Paged4([300, 90], rows, Hq, 1, 64, 16, seed=5, q_scale=2.0 ** -63)
+    for j in (3, 40, 250):                       # keys of 2^66 among others whose scores are next to nothing
+        p.cache.k_s[p.at(0, j)] += 66
+    p.cache.k_s[p.at(0, 77)] = 0
+    p.reread()
+    p.check()
+    p.check(100, 4)
