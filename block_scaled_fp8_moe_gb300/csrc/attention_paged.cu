@@ -990,20 +990,23 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
     }
 
     // ---------------- the warps' parts joined, in the order of their tokens ----------------
-    // Sums are the same in all lanes of a column. 2^kFewLift is taken out of them and of the outputs alike, and what they refer to
-    // is -off itself, without it: any other number next to a large one would be rounded.
-    const float unlift = pow2i(-(int)kFewLift);
+    // Sums are the same in all lanes of a column. What a warp's sum and outputs refer to moves up by its exponent and 8 more: no
+    // sum of 4 warps' values, or of 32 pieces', is above the largest of them. (Next to a score of 2^24 or more the move is rounded;
+    // the sum takes what was moved.)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (g == 0)
-          sums[(n & 1) * C::WARPS + warp][8 * nb + 2 * c + e] = make_float2(ol[nb][e] == 0.f ? -INFINITY : -off[nb][e], ol[nb][e] * unlift);
+        if (g == 0) {
+          const float x = -off[nb][e] + (float)((int)(__float_as_uint(ol[nb][e]) >> 23) - 127 + 8);
+          sums[(n & 1) * C::WARPS + warp][8 * nb + 2 * c + e] =
+              make_float2(ol[nb][e] == 0.f ? -INFINITY : x, ol[nb][e] * ex2(-off[nb][e] - x));
+        }
     const int piece = it.piece, pieces = it.pieces, hk = it.hk;
     const long long b = it.b;
     const bool more = load_q(n + 1);              // on their way while this item ends
     stop = consumers_any<C::WARPS>(!more || *abort);
-    const float unit = pow2i(E - 127 - kUp - (int)kFewLift);
+    const float unit = pow2i(E - 127 - kUp);
     auto total = [&](int rho, float& top) {
       top = -INFINITY;
 #pragma unroll
@@ -1027,7 +1030,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
         for (int j = 0; j < MT; j += 2)           // of products j and j + 1 four columns in a row
           *reinterpret_cast<float4*>(mine + rho * C::PITCH + g * (D / 8) + 2 * j) =
-              make_float4(o[nb][j][e] * unit * f, o[nb][j][2 + e] * unit * f, o[nb][j + 1][e] * unit * f, o[nb][j + 1][2 + e] * unit * f);
+              make_float4(o[nb][j][e] * f * unit, o[nb][j][2 + e] * f * unit, o[nb][j + 1][e] * f * unit, o[nb][j + 1][2 + e] * f * unit);
       }
     named_bar_sync(1, C::WARPS * 32);
     if (!*abort) {

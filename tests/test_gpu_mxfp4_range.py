@@ -117,3 +117,17 @@ def test_scales_at_their_ends(rows, Hq):
     p.reread()
     p.check()
     p.check(100, 4)
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES[:2])
+@pytest.mark.parametrize("power", [0, 120, 124])
+def test_sums_of_large_values(power, rows, Hq):
+    """The mean of thousands of values of 2^power and more, with weights that refer to one far below them (5.5, of equal keys)."""
+    p = Paged4([1300, 9001, 90], rows, Hq, 1, 64, 16, seed=11)
+    p.cache.k[:], p.cache.k_s[:] = 0x22, 127
+    p.q[:] = 0.6875
+    p.cache.v &= 0x33                            # 0 to 1.5
+    p.cache.v_s += power
+    p.reread()
+    p.check()
+    p.check(700, 50)
