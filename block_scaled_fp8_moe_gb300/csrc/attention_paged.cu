@@ -472,14 +472,16 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
 //  - weights are 2^kFewLift times themselves, at most 2^kFewGrow more (the maximum that they refer to moves when outgrown by
 //    that), so that weights below 2^-30 of the largest become zero, 2^17 tokens of them 2^-13 of the result;
 //  - a thread's values are all of one block's columns and are held in units of 2^(E - kUp): scales from 2^-kSpread to 1 of 2^E
-//    keep codes exact. E grows with the scales that come; keys too far below it, and those whose scale is NaN, are left out of the
-//    product and added one by one in fp32 (`apart`).
+//    keep codes exact. E grows with the scales that come, up to kTopE; keys too far below it, or above, and those whose scale is NaN,
+//    are left out of the product and added one by one in fp32 (`apart`). All rows of an item share E, and with a unit of
+//    2^(kTopE - 127 - kUp) at most, the largest value of the format, which some row sees or has no weight for, leaves the others'
+//    values down to 2^-96.
 // Both references begin at values that most caches never leave, so that an item has no first step of its own: weights at 1,
 // for scores of 2^-kFewLow to 2^kFewGrow, and E at kFirstE, for values' scales of 2^-20 to 2^7.
 // Conversion: an instruction for two keys' codes; of values' codes, which lie the other way round, half a one more to put two
 // keys' codes into one byte, and one for the scales.
 constexpr float kFewLift = 7.f, kFewGrow = 8.f, kFewLow = 2.f;
-constexpr int kUp = 13, kSpread = 27, kFirstE = 134;
+constexpr int kUp = 13, kSpread = 27, kFirstE = 134, kTopE = 177;
 constexpr int kFarRow = 64;                                // rows whose largest element is 2^64 or more, or below 2^-64
 constexpr float kFarLow = 0x1p-40f, kFarHigh = 0x1p20f;    // scores' factors that are kept
 
@@ -868,7 +870,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
             for (int d = 1; d < 4; d *= 2) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             const int was = E;
-            if (hi >= 0) E = first ? hi : max(E, hi);
+            if (hi >= 0) E = min(first ? hi : max(E, hi), kTopE);
             const float k = first ? 1.f : pow2i(was - E);
             first = first && hi < 0;
             if (__any_sync(0xffffffffu, k != 1.f)) {
@@ -882,7 +884,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int b = (by[gr][e >> 1] >> (16 * (e & 1))) & 0xFFFF;
-                const bool zero = (zeros >> (4 * gr + e)) & 1u, away = !zero && (b == 255 || b < E - kSpread);
+                const bool zero = (zeros >> (4 * gr + e)) & 1u, away = !zero && (b < E - kSpread || b > E);
                 if (away) {
                   apart |= 1u << (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1) + 16 * gr);
 #pragma unroll
@@ -948,7 +950,8 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           const int loc = __ffs(apart) - 1, tk = loc0 + loc, src = 4 * row_of_tok<D>(loc & 7) + c;
           const uint8_t* at = smem + s * C::STAGE;
           const int b = at[2 * C::KV + C::SC + tk * (D / 32) + g / (256 / D)];
-          if (b != 255 && b >= E - kSpread) at = nullptr;     // of this thread's block it is in the product, or zero
+          // of this thread's block it is in the product, or zero
+          if (b != 255 && b >= E - kSpread && (b <= E || E < kTopE)) at = nullptr;
           const float unit = b == 255 ? __uint_as_float(0x7FC00000u) : pow2i(min(b - E + kUp, 127));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {

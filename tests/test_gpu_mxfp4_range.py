@@ -119,6 +119,51 @@ def test_scales_at_their_ends(rows, Hq):
     p.check(100, 4)
 
 
+@pytest.mark.parametrize("rows,Hq", SHAPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_beside_ones_of_2_to_the_127(D, rows, Hq):
+    """Values of 2^-40, and a token whose values are the largest of the format: in the last row's own place, which the others do not
+    see; and where every row's weight of it is zero."""
+    def small(seed):
+        p = Paged4([200, 1300], rows, Hq, 1, D, 16, seed=seed)
+        p.cache.v_s -= 40
+        return p
+    p = small(6)
+    for b, n in enumerate(p.lens):
+        p.cache.v[p.at(b, n - 1)], p.cache.v_s[p.at(b, n - 1)] = 0x22, 254          # 2^127
+    p.reread()
+    got = p.run().double().cpu().numpy()
+    p.B.attention_status()
+    want, mag = p.oracle()
+    near = np.abs(got - want) <= p.tolerance(want, mag)
+    # what the rest of the values' sum may be off is not what the largest one may
+    for b in range(2):
+        rest = np.abs(got - want)[b, :-1]
+        assert (rest <= A.attention_tolerance(want, mag)[b, :-1] + 2.0 ** -30 * 2.0 ** -38 * p.lens[b]).all()
+    assert near.all()
+    p = small(7)
+    p.q[..., 0] = 100.0
+    p.cache.k[..., 0] = (p.cache.k[..., 0] & 0xF0) | 7
+    large = [(0, 100), (1, 3), (1, 777)]
+    for b, j in large:
+        p.cache.k[p.at(b, j) + (0,)] = (p.cache.k[p.at(b, j) + (0,)] & 0xF0) | 15     # -6 instead of 6
+        p.cache.v[p.at(b, j)], p.cache.v_s[p.at(b, j)] = 0x22, 254
+        p.cache.k_s[p.at(b, j)] += 3
+    p.reread()
+    got = p.run().double().cpu().numpy()
+    p.B.attention_status()
+    # Such a key's score is so far below the row's best that its weight, below e^-88 < 2^-126, is none that fp32 has.
+    q = p.q.double().cpu().numpy()
+    for b, j in large:
+        mine = p.table[b, :p.used[b]].cpu().numpy()
+        k = p.values[0][mine].transpose(0, 2, 1, 3).reshape(-1, D)[:p.lens[b] - rows + 1]       # what all rows see
+        s = np.einsum("rhd,nd->rhn", q[b], k) * D ** -0.5
+        assert (s.max(-1) - s[..., j] > 88).all()
+        p.values[1][p.at(b, j)] = 0
+    want, mag = p.oracle()
+    assert (np.abs(got - want) <= A.attention_tolerance(want, mag) + 2.0 ** -30 * 2.0 ** -38 * 1300).all()
+
+
 @pytest.mark.parametrize("rows,Hq", SHAPES[:2])
 @pytest.mark.parametrize("power", [0, 120, 124])
 def test_sums_of_large_values(power, rows, Hq):
