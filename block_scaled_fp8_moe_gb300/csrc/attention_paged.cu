@@ -244,7 +244,7 @@ __device__ __forceinline__ void consume_eight(const PagedArgs& p, uint8_t* smem,
           else scores(std::false_type{});
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[e] = (sc[e] + sd[e]) * scale;
+        for (int e = 0; e < 4; ++e) sc[e] = __fmul_rn(sc[e] + sd[e], scale);      // rounded before a reference is taken from it
 
         // ---- what the rows do not see ----
         uint32_t drop = 0, alone = 0;            // of this warp's tokens: left out of the product; added one by one
@@ -1344,7 +1344,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
 #pragma unroll
           for (int j = 0; j < ST / 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[j][e] *= scale;
+            for (int e = 0; e < 4; ++e) sc[j][e] = __fmul_rn(sc[j][e], scale);    // rounded before a reference is taken from it
         } else {
 #pragma unroll
           for (int j = 0; j < ST / 8; ++j)
@@ -1353,7 +1353,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
               const int loc = j * 8 + 2 * c + (e & 1), t = tok0 + loc;
               const bool there = (mask >> ((loc0 + loc) >> min(p.page_log2, 6))) & 1u;
               const bool see = there && t <= pos[e >> 1] && (t >= first[e >> 1] || t < p.a.sinks);
-              sc[j][e] = see ? sc[j][e] * scale : -INFINITY;
+              sc[j][e] = see ? __fmul_rn(sc[j][e], scale) : -INFINITY;
             }
           // A weight of zero does not hide a value that is not finite: the product leaves out what no row sees, and
           // what only some rows see where it is not finite.

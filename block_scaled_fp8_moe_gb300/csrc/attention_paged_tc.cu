@@ -606,7 +606,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     const uint32_t ts = tmem + (x ? C::S1 : C::S0) + lanes, to = tmem + (x ? C::O1 : C::O0) + lanes;
     // scores in units of log2 e / scale; a scale of zero becomes one that tells none apart
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
-    const uint64_t c2 = pack2(c, c);
     const int G = p.G;
     int done = 0, steps = 0;                    // steps of this chain, and of all, so far
     bool ok = true;
@@ -685,7 +684,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
           m = mn;
         }
         any = true;
-        const float base = m == -INFINITY ? 0.f : -m * c;
+        const float cw = weight_factor(m, c), base = m == -INFINITY ? 0.f : -m * cw;
+        const uint64_t c2 = pack2(cw, cw);
         const uint64_t b2 = pack2(base, base);
         uint64_t la = pack2(0.f, 0.f), lb = la;
 #pragma unroll

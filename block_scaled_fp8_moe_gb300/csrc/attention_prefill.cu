@@ -457,7 +457,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
     // scores in units of log2 e / scale; a scale below zero turns their sign, zero becomes a scale that tells none apart
     const uint32_t turn = p.a.scale < 0.f ? 0x80000000u : 0u;
     const float c = fmaxf(fabsf(p.a.scale) * 1.4426950408889634f, 1e-37f);
-    const uint64_t c2 = pack2(c, c);
     int step = 0;                               // steps so far
     bool ok = true;
     for (int n = 0; ok && item_there(n); ++n) {
@@ -510,7 +509,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
           m = mn;
           return true;
         };
-        uint64_t la = pack2(0.f, 0.f), lb = la, b2 = la;
+        uint64_t la = pack2(0.f, 0.f), lb = la, b2 = la, c2 = la;
         auto weights = [&](const uint32_t* s, float (&w)[4]) {
           unpack2(fma2(pack2(__uint_as_float(s[0]), __uint_as_float(s[1])), c2, b2), w[0], w[1]);
           unpack2(fma2(pack2(__uint_as_float(s[2]), __uint_as_float(s[3])), c2, b2), w[2], w[3]);
@@ -560,8 +559,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_
             m4[f] = max3(m4[f], __uint_as_float(s[e + 2 * f]), __uint_as_float(s[e + 2 * f + 1]));
         mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
         if (!(ok = move_base())) break;
-        const float base = m == -INFINITY ? 0.f : -m * c;
+        const float cw = weight_factor(m, c), base = m == -INFINITY ? 0.f : -m * cw;
         b2 = pack2(base, base);
+        c2 = pack2(cw, cw);
         if (!edge || !split) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

@@ -79,6 +79,14 @@ __device__ __forceinline__ void reg_fence32(uint32_t (&r)[N], int i) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The factor of a score s in its weight's exponent, s c - m c in one fused operation, which keeps what rounding m c has left out: up
+// to 16 below 2^29, which fp32 and bf16 weights can bear, but more than either at 2^32. From 2^29 on two scores that differ at all
+// differ by 32 or more, so the power of two below c takes c's place: its products are exact, m's own exponent is 0, and the
+// others' are below -16 still.
+__device__ __forceinline__ float weight_factor(float m, float c) {
+  return fabsf(m * c) < 0x1p29f ? c : __uint_as_float(__float_as_uint(c) & 0x7F800000u);
+}
+
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
