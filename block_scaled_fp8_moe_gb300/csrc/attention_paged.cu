@@ -1657,10 +1657,15 @@ static int max_pieces_of(const moe_attention* a, int rows, int max_len, bool fou
   return most;
 }
 
-// A workspace serves every format.
-static size_t part_rows(const moe_attention* a, int rows, int max_len) {
-  const int pieces = std::max(max_pieces_of(a, rows, max_len, false), max_pieces_of(a, rows, max_len, true));
+static size_t part_rows(const moe_attention* a, int rows, int max_len, bool four) {
+  const int pieces = max_pieces_of(a, rows, max_len, four);
   return pieces == 1 ? 0 : (size_t)a->B * a->Hq * rows * pieces;
+}
+
+// What a call needs of its workspace.
+static size_t paged_bytes(const moe_attention* a, int rows, int max_len, bool four) {
+  const size_t n = part_rows(a, rows, max_len, four);
+  return 256 + align_up(n * a->D * 4, 256) + align_up(n * 8, 256);
 }
 
 template <class C>
@@ -1715,8 +1720,8 @@ extern "C" int moe_selftest_attention_hold(int32_t load) {
 
 extern "C" size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len) {
   if (!attention_ok(a) || rows < 1 || rows > 64 || max_len < 0 || max_len > kMaxLen) return 0;
-  const size_t n = part_rows(a, rows, max_len);
-  return 256 + align_up(n * a->D * 4, 256) + align_up(n * 8, 256);
+  // serves every format
+  return std::max(paged_bytes(a, rows, max_len, false), paged_bytes(a, rows, max_len, true));
 }
 
 extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* cache, int32_t rows, int32_t max_len,
@@ -1728,8 +1733,8 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (cache->Hkv != a->Hkv || cache->D != a->D) return MOE_ERR_INVALID_ARG;
   if (max_len < 0 || table_width < 0 || max_len > (int64_t)table_width * cache->page_size) return MOE_ERR_INVALID_ARG;
-  if (!status_ws_ok(ws, ws_bytes) || ws_bytes < moe_paged_attention_workspace_bytes(a, rows, max_len))
-    return MOE_ERR_WORKSPACE;
+  const bool four = cache->format == MOE_KV_MXFP4;
+  if (!status_ws_ok(ws, ws_bytes) || ws_bytes < paged_bytes(a, rows, max_len, four)) return MOE_ERR_WORKSPACE;
   if (a->B == 0) return MOE_OK;
   if (!q || !block_table || !seq_lens || !out || !kv_cache_pointers_ok(cache)) return MOE_ERR_INVALID_ARG;
   if (q_stride < (int64_t)a->Hq * a->D || q_stride % 8) return MOE_ERR_INVALID_ARG;
@@ -1749,7 +1754,6 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.table_width = table_width;
   p.G = a->Hq / a->Hkv;
   p.R = rows * p.G;
-  const bool four = cache->format == MOE_KV_MXFP4;
   p.tile_log2 = tile_of(a, rows, four) == kTileTok ? 6 : 7;
   p.block_log2 = p.R <= kFewRows ? 4 : 7;
   p.mblocks = ceil_div(p.R, 1 << p.block_log2);
@@ -1764,7 +1768,7 @@ extern "C" int moe_paged_attention(const moe_attention* a, const moe_kv_cache* c
   p.out = out;
   p.status = static_cast<uint32_t*>(ws);
   p.hold = held_load();
-  const size_t n = part_rows(a, rows, max_len);
+  const size_t n = part_rows(a, rows, max_len, four);
   p.part_o = ws_ptr<float>(ws, 256);
   p.part_ml = ws_ptr<float>(ws, 256 + align_up(n * a->D * 4, 256));
   return launch_paged(p, cache, static_cast<cudaStream_t>(stream));

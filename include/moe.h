@@ -470,7 +470,7 @@ typedef struct moe_attention {
  * A sequence is cut into pieces by its own length alone and the pieces are joined in order, so a row's
  * result does not depend on its batch. 1 <= rows <= 64, max_len <= 2^31 - 256; q, out 16-byte aligned,
  * q_stride % 8 == 0.
- * ws: moe_paged_attention_workspace_bytes (0 for unsupported sizes). */
+ * ws: moe_paged_attention_workspace_bytes (0 for unsupported sizes), which serves every format of the cache. */
 MOE_API size_t moe_paged_attention_workspace_bytes(const moe_attention* a, int32_t rows, int32_t max_len);
 MOE_API int moe_paged_attention(const moe_attention* a, const moe_kv_cache* cache, int32_t rows, int32_t max_len,
                                 const uint16_t* q, int64_t q_stride, const int32_t* block_table,
