@@ -620,9 +620,10 @@ def moe_add_rmsnorm_mxfp8(x, weight, residual=None, eps: float = 1e-6, sum_out=N
 class KvCache:
     """A paged key/value cache: k and v [pages, Hkv, page_size, D] in bf16, or u8 codes with u8 UE8M0 scales k_s and v_s
     [pages, Hkv, page_size, D/32]: E4M3, or E2M1 two to a byte, [pages, Hkv, page_size, D/2] (see include/moe.h).
-    Holds the tensors it is given."""
+    The scales tell which it is, one for 32 bytes or for 16; format, MOE_KV_*, refuses tensors of another one. Holds the
+    tensors it is given."""
 
-    def __init__(self, k, v, k_s=None, v_s=None):
+    def __init__(self, k, v, k_s=None, v_s=None, format: int | None = None):
         dev = _current(k, "k")
         mx = k_s is not None
         if k.dim() != 4 or v.shape != k.shape or (mx != (v_s is not None)):
@@ -632,6 +633,9 @@ class KvCache:
         four = mx and k_s.dim() == 4 and k_s.shape[3] > 0 and D == 16 * k_s.shape[3]
         if four:
             D *= 2
+        self.format = MOE_KV_MXFP4 if four else MOE_KV_MXFP8 if mx else MOE_KV_BF16
+        if format is not None and format != self.format:
+            raise ValueError(f"k, v and their scales are a cache of format {self.format}, not {format}")
         dtype = torch.uint8 if mx else torch.bfloat16
         ptrs = [_on(k, "k", dtype, dev), _on(v, "v", dtype, dev), None, None]
         if mx:
@@ -641,7 +645,6 @@ class KvCache:
                 ptrs[2 + i] = _on(t, name, torch.uint8, dev)
         self.k, self.v, self.k_s, self.v_s, self.dev = k, v, k_s, v_s, dev
         self.pages, self.page_size, self.Hkv, self.D = pages, page_size, Hkv, D
-        self.format = MOE_KV_MXFP4 if four else MOE_KV_MXFP8 if mx else MOE_KV_BF16
         self.desc = MoeKvCache(pages, page_size, Hkv, D, self.format, *ptrs)
         self.ref = ctypes.byref(self.desc)
 
