@@ -485,7 +485,7 @@ def _rows_on(t: torch.Tensor, name: str, heads: int, D: int, dev: int) -> tuple[
 def _current(t: torch.Tensor, name: str) -> int:
     """t's device, which has to be the current one (launches go there)."""
     dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current CUDA device")
     return dev
 
