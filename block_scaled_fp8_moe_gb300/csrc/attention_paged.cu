@@ -556,7 +556,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
                                              uint64_t* w_full, uint64_t* w_empty, const int4* infos,
                                              const FewItem* items, float2 (*sums)[16], volatile uint32_t* abort, int warp,
                                              int lane) {
-  constexpr int D = C::D, ST = C::ST, GR = 1, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
+  constexpr int D = C::D, ST = C::ST, MT = D / 16, NB = C::EIGHT ? 1 : 2, VW = D / 64;   // VW: words of a thread's part of a value
   const int g = lane >> 2, c = lane & 3, G = p.G, R = p.R;
   const int page_log2 = min(p.page_log2, 7);
   const float scale = p.a.scale * 1.4426950408889634f;
@@ -670,16 +670,15 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
       for (int part = 0; part < ST / 16 && ((info.z >> (C::WARPS + warp)) & 1); ++part) {
         const uint32_t codes_at = st + part * 16 * C::ROWB, scales_at = st + part * 16 * (D / 32);
         // ---- scores ----
-        float sc[GR][NB][4];
-#pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
+        float sc[NB][4];
+        {
           uint32_t sw[2], w[2][D / 32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            sw[h] = scales_of(scales_at + ks_lane + (8 * h + 16 * gr) * (D / 32));
+            sw[h] = scales_of(scales_at + ks_lane + 8 * h * (D / 32));
 #pragma unroll
             for (int bl = 0; bl < D / 32; ++bl)
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((codes_at + k_lane) ^ (bl << 4)) + (8 * h + 16 * gr) * C::ROWB) : "memory");
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[h][bl]) : "r"(((codes_at + k_lane) ^ (bl << 4)) + 8 * h * C::ROWB) : "memory");
           }
 #pragma unroll
           for (int bl = 0; bl < D / 32; ++bl) {
@@ -694,7 +693,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               mma_16816_f16(a, x0, qf[nb][2 * bl][0], qf[nb][2 * bl][1]);
               mma_16816_f16(a, x1, qf[nb][2 * bl + 1][0], qf[nb][2 * bl + 1][1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sc[gr][nb][e] = bl == 0 ? a[e] * f[e >> 1] : fmaf(a[e], f[e >> 1], sc[gr][nb][e]);
+              for (int e = 0; e < 4; ++e) sc[nb][e] = bl == 0 ? a[e] * f[e >> 1] : fmaf(a[e], f[e >> 1], sc[nb][e]);
             }
           }
         }
@@ -703,7 +702,7 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[0][nb][e] = __fmul_rn(sc[0][nb][e], qs[nb][e & 1]);
+          for (int e = 0; e < 4; ++e) sc[nb][e] = __fmul_rn(sc[nb][e], qs[nb][e & 1]);
         if (redo) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -717,36 +716,32 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               mine = mine & (mine << 1) & 0x80808080u;
 #pragma unroll
               for (int e = 2 * h; e < 2 * h + 2; ++e)
-                if (mine || ((again[nb] >> (8 * c + 4 * (e & 1))) & 1u)) sc[0][nb][e] = __fmul_rn(y[e], scale);
+                if (mine || ((again[nb] >> (8 * c + 4 * (e & 1))) & 1u)) sc[nb][e] = __fmul_rn(y[e], scale);
             }
           }
         }
         // The values' codes, under way while the weights are worked out: thread (g, c) has the D/8 values from g D/8 on of its
         // four tokens of 16; product j takes the 2j-th of each as its row g, and the next as its row g + 8.
-        uint32_t w[GR][4][VW], by[GR][2];       // by: the scales' bytes of two tokens, in halves
+        uint32_t w[4][VW], by[2];               // by: the scales' bytes of two tokens, in halves
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t b[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t b[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t at = codes_at + v_lane[e] + (8 * h + 16 * gr) * C::ROWB;
-              if constexpr (D == 128)
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[gr][2 * h + e][0]), "=r"(w[gr][2 * h + e][1]) : "r"(at) : "memory");
-              else
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[gr][2 * h + e][0]) : "r"(at) : "memory");
-              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[e]) : "r"(scales_at + vs_lane[e] + (8 * h + 16 * gr) * (D / 32)) : "memory");
-            }
-            by[gr][h] = b[0] | b[1] << 16;
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t at = codes_at + v_lane[e] + 8 * h * C::ROWB;
+            if constexpr (D == 128)
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[2 * h + e][0]), "=r"(w[2 * h + e][1]) : "r"(at) : "memory");
+            else
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[2 * h + e][0]) : "r"(at) : "memory");
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[e]) : "r"(scales_at + vs_lane[e] + 8 * h * (D / 32)) : "memory");
           }
-        float t[GR][NB][4];                     // exponents of the weights
+          by[h] = b[0] | b[1] << 16;
+        }
+        float t[NB][4];                         // exponents of the weights
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[gr][nb][e] = __fadd_rn(sc[gr][nb][e], off[nb][e & 1]);
+          for (int e = 0; e < 4; ++e) t[nb][e] = __fadd_rn(sc[nb][e], off[nb][e & 1]);
 
         // ---- what the rows do not see ----
         uint32_t hidden = 0, drop = 0;          // of t; tokens that no row sees
@@ -760,56 +755,46 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
               const int rho = 8 * nb + 2 * c + e;
               const Visible see(rho < R ? it.pos0 + rho / G : -1, p.a.window, p.a.sinks);
 #pragma unroll
-              for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int loc = tg + 8 * h + 16 * gr;
-                  const bool there = (mask >> ((loc0 + loc) >> page_log2)) & 1u;
-                  if (!there || !see.sees(tok0 + loc)) {
-                    t[gr][nb][2 * h + e] = -INFINITY;
-                    hidden |= 1u << (4 * (gr * NB + nb) + 2 * h + e);
-                  }
+              for (int h = 0; h < 2; ++h) {
+                const int loc = tg + 8 * h;
+                const bool there = (mask >> ((loc0 + loc) >> page_log2)) & 1u;
+                if (!there || !see.sees(tok0 + loc)) {
+                  t[nb][2 * h + e] = -INFINITY;
+                  hidden |= 1u << (4 * nb + 2 * h + e);
                 }
+              }
             }
           const int tt = tok0 + lane;
           const bool any = lane < 16 && ((mask >> ((loc0 + lane) >> page_log2)) & 1u) && tt <= it.pmax && (tt >= it.first_any || tt < p.a.sinks);
           drop = __ballot_sync(0xffffffffu, !any);
 #pragma unroll
-          for (int gr = 0; gr < GR; ++gr)
+          for (int e = 0; e < 4; ++e)           // whose codes and scales may be anything
+            if ((drop >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1))) & 1u) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)         // whose codes and scales may be anything
-              if ((drop >> (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1) + 16 * gr)) & 1u) {
-#pragma unroll
-                for (int v = 0; v < VW; ++v) w[gr][e][v] = 0;
-                by[gr][e >> 1] = (by[gr][e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
-              }
+              for (int v = 0; v < VW; ++v) w[e][v] = 0;
+              by[e >> 1] = (by[e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
+            }
         }
 
         // ---- where weights and outputs refer to ----
-        uint32_t u[GR][2], top = 0;             // kSpread less how far a scale is below E
+        uint32_t u[2], top = 0;                 // kSpread less how far a scale is below E
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            u[gr][h] = by[gr][h] - (uint32_t)((E - kSpread) * 0x10001);
-            top = __vmaxu2(top, u[gr][h]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          u[h] = by[h] - (uint32_t)((E - kSpread) * 0x10001);
+          top = __vmaxu2(top, u[h]);
+        }
         const bool scales_move = max(top & 0xFFFFu, top >> 16) > kSpread;
         bool weights_move = false;
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) weights_move = weights_move || t[gr][nb][e] > kFewLift + kFewGrow;
+          for (int e = 0; e < 4; ++e) weights_move = weights_move || t[nb][e] > kFewLift + kFewGrow;
         if (__any_sync(0xffffffffu, early != 0)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = -INFINITY;
-#pragma unroll
-              for (int gr = 0; gr < GR; ++gr) mx = fmaxf(mx, fmaxf(t[gr][nb][e], t[gr][nb][2 + e]));
+              const float mx = fmaxf(t[nb][e], t[nb][2 + e]);
               const uint32_t bit = 1u << (2 * nb + e), seen = __ballot_sync(0xffffffffu, mx > kFewLift - kFewLow);
               if (seen & (0x11111111u << c)) early &= ~bit;
               else weights_move = weights_move || ((early & bit) && mx > -INFINITY);
@@ -825,10 +810,8 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             for (int e = 0; e < 2; ++e) {
               float mx = -INFINITY;
 #pragma unroll
-              for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u)) mx = fmaxf(mx, sc[gr][nb][2 * h + e]);
+              for (int h = 0; h < 2; ++h)
+                if (!((hidden >> (4 * nb + 2 * h + e)) & 1u)) mx = fmaxf(mx, sc[nb][2 * h + e]);
 #pragma unroll
               for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               k[e] = 1.f;
@@ -840,11 +823,8 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
                 early &= ~bit;
               }
 #pragma unroll
-              for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (!((hidden >> (4 * (gr * NB + nb) + 2 * h + e)) & 1u))
-                    t[gr][nb][2 * h + e] = __fadd_rn(sc[gr][nb][2 * h + e], off[nb][e]);
+              for (int h = 0; h < 2; ++h)
+                if (!((hidden >> (4 * nb + 2 * h + e)) & 1u)) t[nb][2 * h + e] = __fadd_rn(sc[nb][2 * h + e], off[nb][e]);
             }
             ol[nb][0] *= k[0], ol[nb][1] *= k[1];
 #pragma unroll
@@ -857,16 +837,14 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
             uint32_t zeros = 0;
             unit_looked_at = true;
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
+            for (int e = 0; e < 4; ++e) {
+              const int b = (by[e >> 1] >> (16 * (e & 1))) & 0xFFFF;
+              uint32_t any = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int b = (by[gr][e >> 1] >> (16 * (e & 1))) & 0xFFFF;
-                uint32_t any = 0;
-#pragma unroll
-                for (int v = 0; v < VW; ++v) any |= w[gr][e][v] & 0x77777777u;
-                if (b != 255 && any) hi = max(hi, b);
-                if (b != 255 && !any) zeros |= 1u << (4 * gr + e);
-              }
+              for (int v = 0; v < VW; ++v) any |= w[e][v] & 0x77777777u;
+              if (b != 255 && any) hi = max(hi, b);
+              if (b != 255 && !any) zeros |= 1u << e;
+            }
 #pragma unroll
             for (int d = 1; d < 4; d *= 2) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, d));
             const int was = E;
@@ -880,71 +858,63 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
                 for (int j = 0; j < MT; ++j) o[nb][j][0] *= k, o[nb][j][1] *= k, o[nb][j][2] *= k, o[nb][j][3] *= k;
             }
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
+            for (int e = 0; e < 4; ++e) {
+              const int b = (by[e >> 1] >> (16 * (e & 1))) & 0xFFFF;
+              const bool zero = (zeros >> e) & 1u, away = !zero && (b < E - kSpread || b > E);
+              if (away) {
+                apart |= 1u << (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int b = (by[gr][e >> 1] >> (16 * (e & 1))) & 0xFFFF;
-                const bool zero = (zeros >> (4 * gr + e)) & 1u, away = !zero && (b < E - kSpread || b > E);
-                if (away) {
-                  apart |= 1u << (tok_of<D>(2 * c + (e & 1)) + 8 * (e >> 1) + 16 * gr);
-#pragma unroll
-                  for (int v = 0; v < VW; ++v) w[gr][e][v] = 0;
-                }
-                if (zero || away) by[gr][e >> 1] = (by[gr][e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
+                for (int v = 0; v < VW; ++v) w[e][v] = 0;
               }
+              if (zero || away) by[e >> 1] = (by[e >> 1] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)E << (16 * (e & 1));
+            }
             apart = __reduce_or_sync(0xffffffffu, apart);
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) u[gr][h] = by[gr][h] - (uint32_t)((E - kSpread) * 0x10001);
+            for (int h = 0; h < 2; ++h) u[h] = by[h] - (uint32_t)((E - kSpread) * 0x10001);
           }
         }
         if (!unit_looked_at) first = first && (uint16_t)drop == 0xFFFFu;
 
-        uint32_t wt[GR][NB][2];
+        // ---- weights ----
+        // Rounded to 16 bits for the second product; the sum takes the rounded ones, so that a single large weight divides
+        // out exactly.
+        uint32_t wt[NB][2], pf[NB][2];
+        const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
-        for (int gr = 0; gr < GR; ++gr) {
-          // ---- weights ----
-          // Rounded to 16 bits for the second product; the sum takes the rounded ones, so that a single large weight divides
-          // out exactly.
-          uint32_t pf[NB][2];
-          const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              wt[gr][nb][h] = f16x2(ex2(t[gr][nb][2 * h]), ex2(t[gr][nb][2 * h + 1]));
-              pf[nb][h] = transposed(wt[gr][nb][h]);
-            }
-            mma_16816_f16(ol[nb], ones, pf[nb][0], pf[nb][1]);
+          for (int h = 0; h < 2; ++h) {
+            wt[nb][h] = f16x2(ex2(t[nb][2 * h]), ex2(t[nb][2 * h + 1]));
+            pf[nb][h] = transposed(wt[nb][h]);
           }
-          // ---- weighted values ----
-          uint32_t fac[2];                      // of two tokens each: 2^(byte - E + kUp) in f16
-          static_assert(kUp + 15 == kSpread + 1, "the smallest factor is the smallest normal number");
+          mma_16816_f16(ol[nb], ones, pf[nb][0], pf[nb][1]);
+        }
+        // ---- weighted values ----
+        uint32_t fac[2];                        // of two tokens each: 2^(byte - E + kUp) in f16
+        static_assert(kUp + 15 == kSpread + 1, "the smallest factor is the smallest normal number");
 #pragma unroll
-          for (int h = 0; h < 2; ++h) fac[h] = (u[gr][h] << 10) + 0x04000400u;
+        for (int h = 0; h < 2; ++h) fac[h] = (u[h] << 10) + 0x04000400u;
 #pragma unroll
-          for (int v = 0; v < VW; ++v) {
-            // one byte of two neighbouring tokens' codes of the same column
-            uint32_t even[2], odd[2];
+        for (int v = 0; v < VW; ++v) {
+          // one byte of two neighbouring tokens' codes of the same column
+          uint32_t even[2], odd[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t x = w[gr][2 * h][v], y = w[gr][2 * h + 1][v];
-              even[h] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
-              odd[h] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
-            }
-            auto product = [&](auto b) {
-              constexpr int I = decltype(b)::value;
-              const uint32_t x[4] = {mul_f16x2(e2m1_pair<I>(even[0]), fac[0]), mul_f16x2(e2m1_pair<I>(odd[0]), fac[0]),
-                                     mul_f16x2(e2m1_pair<I>(even[1]), fac[1]), mul_f16x2(e2m1_pair<I>(odd[1]), fac[1])};
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma_16816_f16(o[nb][4 * v + I], x, pf[nb][0], pf[nb][1]);
-            };
-            product(std::integral_constant<int, 0>{});
-            product(std::integral_constant<int, 1>{});
-            product(std::integral_constant<int, 2>{});
-            product(std::integral_constant<int, 3>{});
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = w[2 * h][v], y = w[2 * h + 1][v];
+            even[h] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+            odd[h] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
           }
+          auto product = [&](auto b) {
+            constexpr int I = decltype(b)::value;
+            const uint32_t x[4] = {mul_f16x2(e2m1_pair<I>(even[0]), fac[0]), mul_f16x2(e2m1_pair<I>(odd[0]), fac[0]),
+                                   mul_f16x2(e2m1_pair<I>(even[1]), fac[1]), mul_f16x2(e2m1_pair<I>(odd[1]), fac[1])};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma_16816_f16(o[nb][4 * v + I], x, pf[nb][0], pf[nb][1]);
+          };
+          product(std::integral_constant<int, 0>{});
+          product(std::integral_constant<int, 1>{});
+          product(std::integral_constant<int, 2>{});
+          product(std::integral_constant<int, 3>{});
         }
         for (; apart; apart &= apart - 1) {
           const int loc = __ffs(apart) - 1, tk = loc0 + loc, src = 4 * row_of_tok<D>(loc & 7) + c;
@@ -957,10 +927,8 @@ __device__ __forceinline__ void consume_four(const PagedArgs& p, uint8_t* smem, 
           for (int nb = 0; nb < NB; ++nb) {
             uint32_t x = 0;
 #pragma unroll
-            for (int gr = 0; gr < GR; ++gr)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (loc >> 3 == 2 * gr + h) x = wt[gr][nb][h];
+            for (int h = 0; h < 2; ++h)
+              if (loc >> 3 == h) x = wt[nb][h];
             x = __shfl_sync(0xffffffffu, x, src);
             if (!at) continue;
             bool see[2];
@@ -1077,7 +1045,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
   constexpr int D = C::D, ST = C::ST, NT = D / 8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], w_full[2], w_empty[2];
-  __shared__ uint32_t page_mask[C::STAGES];
+  __shared__ uint32_t page_mask[C::BITS == 4 ? 1 : C::STAGES];
   __shared__ int4 infos[C::BITS == 4 ? C::STAGES : 1];   // of a stage: first token, pages there, kinds
   __shared__ FewItem items[2];
   __shared__ float2 sums[C::WARPS * (C::BITS == 4 ? 2 : 1)][16];   // the warps' maximum (times log2 e) and sum of a row
@@ -1184,7 +1152,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_co
         }
         if (lane == 0) {
           if constexpr (C::BITS == 4) infos[s] = make_int4(tok0, (int)mask, (int)kinds, 0);
-          page_mask[s] = mask;
+          else page_mask[s] = mask;
           mbar_arrive_expect_tx(&full[s], __popc(mask) * rows_of * (2 * D * C::BITS / 8 + (C::MX ? 2 * D / 32 : 0)) +
                                               (issued == p.hold ? 16 : 0));
         }
