@@ -524,29 +524,36 @@ __device__ __forceinline__ float pow2i(int e) {
 }
 
 // The scores of 16 keys and 8 rows, without their factor, from bf16: keys whose scale is large or NaN, and rows that f16 does not hold.
-// A thread's places of its first key's codes (whose blocks' numbers turn bits 4 and 5) and scales, and of its row's queries
-// (0: no row). Not inlined: the step that calls it would take 1 to 2 % longer.
+// (Codes up to 6 times scales up to 2^123 are bf16 values; what is above in a scale goes on its block's products.) A thread's places
+// of its first key's codes (whose blocks' numbers turn bits 4 and 5) and scales, and of its row's queries (0: no row). Not inlined:
+// the step that calls it would take 1 to 2 % longer.
 template <class C>
 __device__ __noinline__ float4 scores_again(uint32_t codes, uint32_t scales, uint32_t query) {
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int bl = 0; bl < C::D / 32; ++bl) {
     uint32_t x[2][4];
+    float rest[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w, by;
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"((codes ^ (bl << 4)) + 8 * h * C::ROWB) : "memory");
       asm volatile("ld.shared.u8 %0, [%1];" : "=r"(by) : "r"(scales + 8 * h * (C::D / 32) + bl) : "memory");
-      const uint32_t f = ((min(by, kScaleFits4) + 112u) << 7) * 0x10001u;
-      const uint32_t f2 = (by == 255u ? 0x7FC0u : by > kScaleFits4 ? (by - kScaleFits4 + 127u) << 7 : 0x3F80u) * 0x10001u;
+      const uint32_t in = min(by, 250u);
+      rest[h] = by == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((by - in + 127u) << 23);
+      const uint32_t f = ((min(in, kScaleFits4) + 112u) << 7) * 0x10001u;
+      const uint32_t f2 = ((max(in, kScaleFits4) - kScaleFits4 + 127u) << 7) * 0x10001u;
       auto key = [&](uint32_t pair) { return mul_bf16x2(mul_bf16x2(pair, f), f2); };
       x[0][h] = key(e2m1_bf16<0>(w)), x[0][2 + h] = key(e2m1_bf16<1>(w));
       x[1][h] = key(e2m1_bf16<2>(w)), x[1][2 + h] = key(e2m1_bf16<3>(w));
     }
     uint4 q = make_uint4(0, 0, 0, 0);
     if (query) asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(query + bl * 64) : "memory");
-    mma_16816(s, x[0], q.x, q.y);
-    mma_16816(s, x[1], q.z, q.w);
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_16816(a, x[0], q.x, q.y);
+    mma_16816(a, x[1], q.z, q.w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = fmaf(a[e], rest[e >> 1], s[e]);
   }
   return make_float4(s[0], s[1], s[2], s[3]);
 }

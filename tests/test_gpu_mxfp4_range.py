@@ -176,3 +176,17 @@ def test_sums_of_large_values(power, rows, Hq):
     p.reread()
     p.check()
     p.check(700, 50)
+
+
+@pytest.mark.parametrize("rows,Hq", SHAPES[:2])
+def test_keys_past_the_largest_number_of_fp32(rows, Hq):
+    """Scales of 2^126 and 2^127 and codes up to 6, which an append of the largest bf16 values stores (4 * 2^126), with queries that
+    are zero or make up for them."""
+    p = Paged4([300, 90], rows, Hq, 1, 64, 16, seed=8)
+    p.q *= 2.0 ** -100
+    p.q[..., 32:] *= 2.0 ** -26
+    p.q[..., 40:50] = 0
+    p.cache.k_s[..., 0] += 100
+    p.cache.k_s[..., 1] = 253 + (torch.arange(16, device="cuda") & 1)
+    p.reread()
+    p.check()
