@@ -17,11 +17,11 @@
 // ahead of). 256 rows over 4096 MXFP8 tokens: 445 us, 5.0 TB/s, the conversion's and the products' latencies. One sequence's
 // rows are a matter of latency: 11 us for 1024 to 4096 tokens, the join among them.
 //
-// Over MXFP4 a key brings so few bytes that its instructions count: about 530 a warp for 32 keys and 8 rows, 260 of them conversion
-// and products. One row of 32 heads over 8 of 128: four sequences of up to 128k tokens 96 us (3.6 TB/s), 256 of up to 4096 220 us
-// (3.2 TB/s; 1,024 to 4,096 tokens are 2 to 8 pieces of 4 steps, of 10,000 cycles each, and 4,500 from one to the next: the
-// next queries 950, waiting for the slowest warp 1,300, the join and its output 2,100). 31 sequences of 16 rows to a head 53 us,
-// 160 rows under a window of 1024 57 us. tcgen05 with the codes as they are (keys as M, values converted to E4M3 in shared memory,
+// Over MXFP4 a key brings so few bytes that its instructions count: 720 a warp for 32 keys and 8 rows where pieces are long, 260 of
+// them conversion and products. One row of 32 heads over 8 of 128: four sequences of up to 128k tokens 99 us (3.5 TB/s), 256 of up to
+// 4096 217 us (3.2 TB/s; 1,024 to 4,096 tokens are 2 to 8 pieces of 4 steps, of about 10,000 cycles each, and 4,500 from one to the
+// next: the next queries 950, waiting for the slowest warp 1,300, the join and its output 2,100). 31 sequences of 16 rows to a
+// head 54 us, 160 rows under a window of 1024 58 us. tcgen05 with the codes as they are (keys as M, values converted to E4M3 in shared memory,
 // weights and queries as two E4M3 values each) takes 278, 127, 72 and 130 us for these.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -62,8 +62,8 @@ struct PagedCfg {
   // Blocks of a multiprocessor. Up to 16 rows take 168 registers, up to 8 rows 128 or less. Measured with 2, 3 and 4 blocks:
   // 256 sequences of 4096 tokens, 32 heads over 8 of 128, MXFP8 651 (16 rows' code), 441, 456 us; 64 over 8 of 64, MXFP8
   // 459 (16 rows' code), 338, 296 us; 160 sequences, a window of 1024, 64 over 8 of 64, bf16 68, 63, 67 us, MXFP4 with 3, 4 and
-  // 5 blocks 63, 55, 61 us; 256 sequences, 32 over 8 of 128, MXFP4 with 2, 3 and 4 blocks 221, 231, 280 us, but four of 128k tokens
-  // 99, 96, 101 us; 16 rows over MXFP4 with 1 and 2 blocks 64, 55 us.
+  // 5 blocks 66, 58, 67 us; 256 sequences, 32 over 8 of 128, MXFP4 with 2, 3 and 4 blocks 242, 218, 299 us, four of 128k tokens
+  // 103, 99, 111 us; 16 rows over MXFP4 with 1 and 2 blocks 71, 54 us.
   static constexpr int CTAS = !EIGHT ? 2 : MX && D == 64 ? 4 : 3;
   static constexpr int TILE = BITS == 4 ? 2 * kTileTok : kTileTok;
   static constexpr int WARPS = 4, ST = TILE / WARPS;               // tokens of a stage that a warp takes

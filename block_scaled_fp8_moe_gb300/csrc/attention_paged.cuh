@@ -48,8 +48,8 @@ __device__ __forceinline__ float2* sums_of(const PagedArgs& p, long long at, int
 // help the smallest batch and cost a large one, whose cache is read apace anyway: 1400 tokens, 64 heads over 8 of 128 bf16
 // elements take 11 us for one sequence and 240 us for 256 in pieces of 8 steps, 19 us and 215 us in one piece; four rows of
 // 1024 tokens take 13 us and 257 us in pieces of 4 steps of 128, 17 us and 198 us in one of 8. The small call counts here.
-// Few rows over MXFP4 (steps of 128): 4096 tokens, one row of 32 heads over 8 of 128, take 10.8 us for one sequence and 231 us for
-// 256 ragged ones in pieces of 4 steps, 16.2 us and 193 us in pieces of 8.
+// Few rows over MXFP4 (steps of 128): 4096 tokens, one row of 32 heads over 8 of 128, take 11.0 us for one sequence and 217 us for
+// 256 ragged ones in pieces of 4 steps, 16.3 us and 194 us in pieces of 8.
 __host__ __device__ inline int piece_count(int tile_log2, int tiles) {
   const int log2 = tile_log2 == 6 || tiles >= 64 ? 3 : 2;      // of the steps
   return min(max((tiles + (1 << log2 >> 1)) >> log2, 1), tile_log2 == 6 ? 64 : 32);

@@ -4,14 +4,14 @@
 // Pair i of a head, (a, b), goes to (a cos t - b sin t, a sin t + b cos t) with t = position * w_i. An angle is needed modulo
 // one turn only, so w_i is held as the 64-bit integer 2^64 w_i / 2 pi: its product with the position, modulo 2^64, is the
 // fraction of the turn, off by less than 2^-33 of one for any 32-bit position (fp32 angles would be off by 0.06 rad at a
-// million).
+// million); in fp32, from where the cosine takes it, by 2^-26.
 //
 // Bound: HBM, 4 bytes a value turned; what is stored adds 2, 1.03 or 0.53 a value and 2 read. Cosines and sines are worked out
 // once for all heads of a token, left in shared memory, and held by every thread for its own places in a head. All of a head that
 // a warp writes it has read before, so rows may be turned where they are.
 //
-// 20011 tokens of 32 heads over 8 of 128 into a bf16 cache: 85 us, 5.8 TB/s. 16384 tokens of 16 and 16 heads of 80, turned back: 36 us,
-// 4.7 TB/s. 3061 tokens into an MXFP4 cache: 20 us, 3.3 TB/s, the quantisation's arithmetic. With a chunk a lane and the other half
+// 20011 tokens of 32 heads over 8 of 128 into a bf16 cache: 84 us, 5.8 TB/s. 16384 tokens of 16 and 16 heads of 80, turned back: 36 us,
+// 4.7 TB/s. 3061 tokens into an MXFP4 cache: 19 us, 3.5 TB/s, the quantisation's arithmetic. With a chunk a lane and the other half
 // from another lane, cosines by every warp, these take 147, 55 and 29 us. 6 tokens: 2.4 us.
 #include <cuda_runtime.h>
 

@@ -403,8 +403,9 @@ MOE_API int moe_kv_append(const moe_kv_cache* cache, int32_t T, const uint16_t* 
  *   factor * (a cos(p w_i) - b sin(p w_i)),  factor * (a sin(p w_i) + b cos(p w_i))
  * (inverse: the angle's sign turned, which is also the gradient: of a row that was turned, from the gradient
  * of the result). Of a head's D values the first `dim` are turned, in pairs (i, i + dim/2) or, interleaved,
- * (2i, 2i + 1); the others are copied. Angles are exact to 2^-32 of a turn at every int32 position, below zero
- * too; the arithmetic is fp32, with one rounding at the end. */
+ * (2i, 2i + 1); the others are copied. The fraction of a turn that is left of p w_i is held to 2^-32 at every int32
+ * position, below zero too, and rounded to fp32, so that angles are within 2^-26 of a turn; the arithmetic is fp32,
+ * with one rounding at the end. */
 typedef struct moe_rotary {
   int32_t dim;           /* turned values of a head, a multiple of 8              */
   int32_t axes;          /* positions of a token (time, height, width): 1 to 4    */
