@@ -449,8 +449,8 @@ MOE_API int moe_rope_kv_append(const moe_rotary* r, const moe_kv_cache* cache, i
  * a sliding window and the sequence's first `sinks` tokens, which stay visible. A row that sees nothing
  * gets +0; one whose visible scores are all minus infinity is NaN, as the formula has it. Over an MXFP4 cache, up to
  * 16 rows (row, head of the group) have their weights rounded to f16: those below 2^-30 of the largest count as
- * zero there, and beside values of 2^50 or more that some row of the same sequence and key head sees, values below
- * 2^-96 count as zero in all of them. Sums are fp32: many values past 2^100 may make one infinite.
+ * zero there, and beside values of 2^80 or more that some row of the same sequence and key head sees, values below
+ * 2^-66 count as zero in all of them. Sums are fp32: many values past 2^100 may make one infinite.
  * Keys and values that a row does not see, and what lies in a page behind its sequence's last
  * token, do not reach its result whatever they hold, NaN and infinities included. */
 typedef struct moe_attention {
